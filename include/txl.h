@@ -397,6 +397,110 @@ txl_status txl_rel_attn_fwd_noalloc(const void *q, const void *k, const void *v,
                                     txl_dtype dtype, void *out, void *stream);
 
 /*
+ * txl_softmax_xent_fwd -- the output layer's cross entropy (Transformer-XL's
+ * training objective, Section 4: the negative log-likelihood of the next
+ * token), taken over the vocabulary in pieces: the rows x vocab logits are
+ * never in memory.  For every row i < rows, with j < vocab:
+ *     z_ij   = h_i . w_j + bias_j
+ *     lse_i  = log sum_j exp(z_ij)
+ *     loss_i = lse_i - z_{i,target_i}
+ * A row whose target lies outside [0, vocab) (a negative padding label, say)
+ * is empty: its loss is 0, whatever h_i holds, and its lse is still
+ * computed.  A row whose every logit is -infinity has lse -infinity and
+ * loss 0.  A bias entry of -infinity takes its token out of the vocabulary.
+ *
+ * h         : device, dtype [rows][d_model] (any leading shape: a T-major
+ *             [positions][batch][d_model] buffer has rows = positions*batch).
+ * w         : device, dtype [vocab][d_model] (torch.nn.Linear's and
+ *             torch.nn.Embedding's weight layout: a tied embedding fits).
+ * bias      : device, float32 [vocab], or NULL (no bias).
+ * target    : device, int64 [rows].
+ * loss, lse : device outputs, float32 [rows].
+ * workspace : device scratch of at least the bytes that
+ *             txl_softmax_xent_workspace reports for backward = 0, 256-byte
+ *             aligned, owned by the caller: calls that may overlap on the GPU
+ *             need workspaces of their own.  Nothing is kept in it between
+ *             calls.
+ * Pointers are element-aligned (h, w: 2 or 4 bytes; float32: 4; int64: 8);
+ * rows of w and h that the TMA unit can address (d_model a multiple of 8,
+ * 16-byte aligned bases) are read in place with TXL_BF16, others are copied
+ * piece by piece into the workspace first.
+ * rows == 0: nothing to do.  d_model >= 1, vocab >= 1, else TXL_ERR_INVALID;
+ * vocab <= 2^30 and rows <= 2^30, else TXL_ERR_UNSUPPORTED.  Asynchronous on
+ * stream; no allocation; results do not depend on what else runs (no
+ * atomics: the same call gives the same bits).  bf16: products of bf16
+ * operands, accumulated and normalised in fp32.
+ */
+txl_status txl_softmax_xent_workspace(int rows, int d_model, int vocab, txl_dtype dtype, int backward, size_t *bytes);
+txl_status txl_softmax_xent_fwd(const void *h, const void *w, const float *bias, const int64_t *target, int rows,
+                                int d_model, int vocab, txl_dtype dtype, float *loss, float *lse, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/*
+ * txl_softmax_xent_bwd -- gradients of sum_i dloss_i loss_i of one
+ * txl_softmax_xent_fwd call, from its lse:
+ *     dz_ij = dloss_i (exp(z_ij - lse_i) - [j = target_i])
+ *     dh_i  = sum_j dz_ij w_j,  dw_j = sum_i dz_ij h_i,  dbias_j = sum_i dz_ij
+ * The logits are computed again, piece by piece.  Empty rows, rows of lse
+ * -infinity and rows of dloss 0 have dh exactly 0 and add nothing to dw and
+ * dbias, whatever h_i holds.
+ *
+ * lse       : device, float32 [rows], as the forward wrote it.
+ * dloss     : device, float32 [rows].
+ * dh, dw    : device outputs, dtype, shaped like h and w; either may be NULL
+ *             (not computed: a frozen layer).
+ * dbias     : device output, float32 [vocab], or NULL; it may be asked for
+ *             with bias NULL as well.
+ * workspace : as above, for backward = 1 (which also suffices for the
+ *             forward).
+ * rows == 0: dw and dbias are set to 0.  Outputs must not overlap each other,
+ * any input or the workspace.  bf16: dz is rounded once to bf16 for the two
+ * products (fp32 accumulation over the whole vocabulary and all rows, one
+ * rounding of the results); dbias sums the unrounded dz.
+ */
+txl_status txl_softmax_xent_bwd(const void *h, const void *w, const float *bias, const int64_t *target,
+                                const float *lse, const float *dloss, int rows, int d_model, int vocab,
+                                txl_dtype dtype, void *dh, void *dw, float *dbias, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/*
+ * txl_distill_fwd -- the output layer as a student of a teacher of which the
+ * top_k largest logits per row were kept.  With temperature t,
+ *     p_ik   = softmax over row i's valid entries of teacher_logits_ik / t
+ *     lse_i  = log sum_j exp(z_ij / t)      (the whole vocabulary)
+ *     loss_i = t^2 sum_k p_ik (log p_ik - (z_{i,idx_ik} / t - lse_i))
+ * i.e. t^2 KL(teacher's kept entries, renormalised || student), the factor
+ * t^2 keeping gradients of different temperatures alike.  An entry is valid
+ * when 0 <= teacher_idx < vocab and its logit is not -infinity; a row
+ * without a valid entry is empty (loss 0, as a padding row above).  An index
+ * listed twice counts twice.  z, h, w, bias, loss, lse, workspace and
+ * everything unsaid as txl_softmax_xent_fwd.
+ *
+ * teacher_idx    : device, int64 [rows][top_k], in any order.
+ * teacher_logits : device, teacher_dtype [rows][top_k].
+ * 1 <= top_k (else TXL_ERR_INVALID), top_k <= 256 (else
+ * TXL_ERR_UNSUPPORTED); temperature finite and > 0.
+ */
+txl_status txl_distill_workspace(int rows, int d_model, int vocab, int top_k, txl_dtype dtype, int backward,
+                                 size_t *bytes);
+txl_status txl_distill_fwd(const void *h, const void *w, const float *bias, const int64_t *teacher_idx,
+                           const void *teacher_logits, txl_dtype teacher_dtype, float temperature, int rows,
+                           int d_model, int vocab, int top_k, txl_dtype dtype, float *loss, float *lse,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * txl_distill_bwd -- gradients of sum_i dloss_i loss_i of one
+ * txl_distill_fwd call, from its lse (taken at the same temperature t):
+ *     dz_ij = dloss_i t (exp(z_ij / t - lse_i) - sum_{k: idx_ik = j} p_ik)
+ * and dh, dw, dbias as txl_softmax_xent_bwd, with its rules for empty rows,
+ * absent outputs, rows == 0, the workspace and rounding.
+ */
+txl_status txl_distill_bwd(const void *h, const void *w, const float *bias, const int64_t *teacher_idx,
+                           const void *teacher_logits, txl_dtype teacher_dtype, float temperature, const float *lse,
+                           const float *dloss, int rows, int d_model, int vocab, int top_k, txl_dtype dtype,
+                           void *dh, void *dw, float *dbias, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * txl_check -- synchronise `stream`, then report and clear the library's
  * device error word: TXL_ERR_TIMEOUT if an in-kernel bounded wait gave up
  * since the last check, TXL_ERR_CUDA if the stream reports an error, else

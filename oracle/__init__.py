@@ -19,6 +19,9 @@ Contents
   * ``sinusoid`` / ``rel_table`` -- the relative encoding R (the sinusoid of
     Vaswani et al. that Section 3.3 re-uses) and Appendix B's reversed
     projected table Q_t = W_kR R_{T-1-t}, in float64.
+  * ``softmax_xent`` / ``distill`` -- the output layer's losses and their
+    gradients, row by row from their definitions (the training objective of
+    Section 4; distillation from a teacher's kept logits).
 
 All functions take numpy arrays in the T-major layouts of the library:
 ``q, out: [L, B, H, D]``, ``k, v: [T, B, H, D]`` with ``T = M + L``,
@@ -245,3 +248,60 @@ def rel_table(w_r, klen: int, heads: int, d_head: int, d_pad: Optional[int] = No
     R = sinusoid(klen, w_r.shape[1])
     by_distance = project_heads(R, w_r, heads, d_head, d_pad)      # row p: distance p
     return np.ascontiguousarray(by_distance[::-1])
+
+
+def _sparse_loss(h, w, bias, entries, temperature, dloss):
+    """Losses t^2 sum_k p_k (log p_k - log softmax(z / t)_{c_k}) of rows whose
+    kept entries are ``entries[i]`` = (columns, log weights), and, with
+    ``dloss``, the gradients of sum_i dloss_i loss_i."""
+    h, w = np.asarray(h, dtype=np.float64), np.asarray(w, dtype=np.float64)
+    n, v, t = h.shape[0], w.shape[0], float(temperature)
+    b = np.zeros(v) if bias is None else np.asarray(bias, dtype=np.float64)
+    loss, lse = np.zeros(n), np.zeros(n)
+    dh, dw, db = np.zeros_like(h), np.zeros_like(w), np.zeros(v)
+    for i in range(n):
+        z = (w @ h[i] + b) / t
+        top = z.max()
+        lse[i] = top + np.log(np.exp(z - top).sum()) if top != -np.inf else -np.inf
+        cols, logp = entries[i]
+        if len(cols) == 0 or lse[i] == -np.inf:
+            continue
+        p = np.exp(logp)
+        for c, lp, pk in zip(cols, logp, p):
+            if pk > 0.0:
+                loss[i] += t * t * pk * (lp - (z[c] - lse[i]))
+        if dloss is None or dloss[i] == 0.0:
+            continue
+        dz = np.exp(z - lse[i])
+        for c, pk in zip(cols, p):
+            dz[c] -= pk
+        dz *= float(dloss[i]) * t
+        dh[i] = dz @ w
+        dw += np.outer(dz, h[i])
+        db += dz
+    return (loss, lse) if dloss is None else (loss, lse, dict(dh=dh, dw=dw, db=db))
+
+
+def softmax_xent(h, w, target, bias=None, dloss=None):
+    """Cross entropy of z = h W^T + bias per row: loss_i = lse_i - z_{i,y_i}; a
+    target outside [0, vocab) leaves its row empty (loss 0, no gradient).
+    h [n, d], w [vocab, d], target [n].  Returns (loss, lse), with ``dloss``
+    [n] also the gradients dh, dw, db."""
+    v = len(w)
+    entries = [([int(y)], np.zeros(1)) if 0 <= y < v else ([], np.zeros(0)) for y in np.asarray(target)]
+    return _sparse_loss(h, w, bias, entries, 1.0, dloss)
+
+
+def distill(h, w, teacher_idx, teacher_logits, temperature=1.0, bias=None, dloss=None):
+    """t^2 KL(teacher || student) per row, the teacher's softmax over its kept
+    entries ([n, k] indices and logits; indices outside [0, vocab) and logits
+    of -inf left out) at temperature t.  Returns as ``softmax_xent``."""
+    v, entries = len(w), []
+    for e, y in zip(np.asarray(teacher_idx), np.asarray(teacher_logits, dtype=np.float64)):
+        keep = (e >= 0) & (e < v) & (y != -np.inf)
+        u = y[keep] / float(temperature)
+        if len(u):
+            u = u - u.max()
+            u = u - np.log(np.exp(u).sum())
+        entries.append(([int(c) for c in e[keep]], u))
+    return _sparse_loss(h, w, bias, entries, temperature, dloss)

@@ -26,7 +26,9 @@ _lib: Optional[ctypes.CDLL] = None
 EXPORTS = ("txl_rel_attn_fwd", "txl_mem_update", "txl_check", "txl_status_string",
            "txl_last_cuda_error", "txl_version", "txl_shutdown", "txl_rel_attn_fwd_noalloc",
            "txl_rel_attn_fwd_ring", "txl_ring_append", "txl_rel_attn_fwd_padded", "txl_project_heads",
-           "txl_project_qkv", "txl_project_qkv_cells", "txl_rel_table", "txl_rel_attn_bwd", "txl_rel_attn_bwd_workspace", "txl_rel_attn_fwd_lse", "txl_rel_attn_fwd_mem", "txl_rel_attn_fwd_mem_cells", "txl_rel_attn_fwd_plan", "txl_selftest_wait")
+           "txl_project_qkv", "txl_project_qkv_cells", "txl_rel_table", "txl_rel_attn_bwd", "txl_rel_attn_bwd_workspace", "txl_rel_attn_fwd_lse", "txl_rel_attn_fwd_mem", "txl_rel_attn_fwd_mem_cells", "txl_rel_attn_fwd_plan", "txl_selftest_wait",
+           "txl_softmax_xent_workspace", "txl_softmax_xent_fwd", "txl_softmax_xent_bwd",
+           "txl_distill_workspace", "txl_distill_fwd", "txl_distill_bwd")
 
 
 class TxlError(RuntimeError):
@@ -83,6 +85,19 @@ def load_library() -> ctypes.CDLL:
     lib.txl_rel_attn_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i,
                                      vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
     lib.txl_rel_attn_bwd.restype = i
+    sz, f = ctypes.c_size_t, ctypes.c_float
+    lib.txl_softmax_xent_workspace.argtypes = [i, i, i, i, i, ctypes.POINTER(sz)]
+    lib.txl_softmax_xent_workspace.restype = i
+    lib.txl_softmax_xent_fwd.argtypes = [vp, vp, vp, vp, i, i, i, i, vp, vp, vp, sz, vp]
+    lib.txl_softmax_xent_fwd.restype = i
+    lib.txl_softmax_xent_bwd.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, vp, vp, vp, vp, sz, vp]
+    lib.txl_softmax_xent_bwd.restype = i
+    lib.txl_distill_workspace.argtypes = [i, i, i, i, i, i, ctypes.POINTER(sz)]
+    lib.txl_distill_workspace.restype = i
+    lib.txl_distill_fwd.argtypes = [vp, vp, vp, vp, vp, i, f, i, i, i, i, i, vp, vp, vp, sz, vp]
+    lib.txl_distill_fwd.restype = i
+    lib.txl_distill_bwd.argtypes = [vp, vp, vp, vp, vp, i, f, vp, vp, i, i, i, i, i, vp, vp, vp, vp, sz, vp]
+    lib.txl_distill_bwd.restype = i
     lib.txl_mem_update.argtypes = [vp, vp, i, i, i, i, i, vp]
     lib.txl_mem_update.restype = i
     lib.txl_selftest_wait.argtypes = [ctypes.c_uint, vp]
@@ -541,6 +556,212 @@ def mem_update_raw(dst_ptr, src_ptr, batch, mem_len, seg_len, d_model, dtype_cod
                    stream_ptr) -> int:
     return load_library().txl_mem_update(dst_ptr, src_ptr, batch, mem_len, seg_len, d_model,
                                          dtype_code, stream_ptr)
+
+
+def softmax_xent_workspace_bytes(rows: int, d_model: int, vocab: int, dtype_code: int,
+                                 backward: bool = False) -> int:
+    """Workspace bytes of ``softmax_xent_fwd`` (or, with ``backward``, of
+    ``softmax_xent_bwd``, which then suffices for both)."""
+    n = ctypes.c_size_t(0)
+    st = load_library().txl_softmax_xent_workspace(rows, d_model, vocab, dtype_code, int(bool(backward)),
+                                                   ctypes.byref(n))
+    _raise(st, "txl_softmax_xent_workspace")
+    return int(n.value)
+
+
+def distill_workspace_bytes(rows: int, d_model: int, vocab: int, top_k: int, dtype_code: int,
+                            backward: bool = False) -> int:
+    """Workspace bytes of ``distill_fwd`` (or, with ``backward``, of
+    ``distill_bwd``, which then suffices for both)."""
+    n = ctypes.c_size_t(0)
+    st = load_library().txl_distill_workspace(rows, d_model, vocab, top_k, dtype_code, int(bool(backward)),
+                                              ctypes.byref(n))
+    _raise(st, "txl_distill_workspace")
+    return int(n.value)
+
+
+class _LossCall:
+    """The argument checks the output-layer losses share, and where the call's
+    own tensors are made: on h's device and, with ``stream`` given, in that
+    stream's order (so that a workspace freed at return is reused only behind
+    the call)."""
+
+    def __init__(self, h, w, bias, per_row, stream):
+        import torch
+        self.lead = tuple(h.shape[:-1])
+        if h.dim() < 1 or w.dim() != 2 or w.shape[1] != h.shape[-1] or w.dtype != h.dtype:
+            raise ValueError("w must be [vocab, d_model] with h's last dimension and dtype")
+        self.rows = 1
+        for n in self.lead:
+            self.rows *= n
+        self.vocab, self.d = w.shape
+        self.h, self.stream = h, stream
+        self.code = _dtype_code(h)
+        self.tensors = [h, w]
+        if bias is not None:
+            self.typed("bias", bias, (self.vocab,), torch.float32)
+        for name, t, shape, dtype in per_row:
+            self.typed(name, t, shape, dtype)
+        self.placed()
+
+    def typed(self, name, t, shape, dtype):
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        self.tensors.append(t)
+
+    def placed(self):
+        for t in self.tensors:
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError("all tensors must be contiguous CUDA tensors")
+            if t.device != self.h.device:
+                raise ValueError("all tensors must be on h's device")
+        if self.stream is not None and self.stream.device != self.h.device:
+            raise ValueError("stream must belong to h's device")
+
+    def output(self, name, t, shape, dtype):
+        import torch
+        if t is not None:
+            self.typed(name, t, shape, dtype)
+            self.placed()
+            return t
+        with self.context():
+            return torch.empty(*shape, dtype=dtype, device=self.h.device)
+
+    def workspace(self, t, nbytes):
+        import torch
+        if t is None:
+            with self.context():
+                return torch.empty(nbytes, dtype=torch.uint8, device=self.h.device)
+        self.tensors.append(t)
+        self.placed()
+        if t.numel() * t.element_size() < nbytes:
+            raise ValueError(f"workspace must hold {nbytes} bytes")
+        return t
+
+    def context(self):
+        import torch
+        return torch.cuda.stream(self.stream) if self.stream is not None else torch.cuda.device(self.h.device)
+
+    def run(self, fn, what, *args):
+        import torch
+        with torch.cuda.device(self.h.device):
+            stream = self.stream if self.stream is not None else torch.cuda.current_stream(self.h.device)
+            st = fn(*args, int(stream.cuda_stream))
+        _raise(st, what)
+
+
+def _loss_grads(call, grads, w, bias, weight_grads):
+    """The gradients' dict of a backward: given tensors are used, absent ones made."""
+    import torch
+    grads = {} if grads is None else grads
+    grads["dh"] = call.output("dh", grads.get("dh"), tuple(call.h.shape), call.h.dtype)
+    if weight_grads:
+        grads["dw"] = call.output("dw", grads.get("dw"), tuple(w.shape), w.dtype)
+        if bias is not None or grads.get("db") is not None:
+            grads["db"] = call.output("db", grads.get("db"), (call.vocab,), torch.float32)
+    else:
+        grads["dw"] = grads["db"] = None
+    grads.setdefault("db", None)
+    return grads
+
+
+def softmax_xent_fwd(h, w, target, bias=None, loss=None, lse=None, workspace=None, stream=None):
+    """Cross entropy of the output layer z = h @ w.T + bias without its logits
+    (txl_softmax_xent_fwd).
+
+    h: [*lead, d_model] hidden states; w: [vocab, d_model] (torch.nn.Linear's
+    and Embedding's layout), h's dtype (float32 or bfloat16); target: [*lead]
+    int64 (a label outside [0, vocab), such as -100, is a padding row: loss
+    0); bias: [vocab] float32 or None; all CUDA, contiguous.  Returns
+    (loss, lse), float32 [*lead]: the rows' losses (no reduction) and
+    log-sum-exps, the latter for ``softmax_xent_bwd``.  ``workspace``: a CUDA
+    tensor of at least ``softmax_xent_workspace_bytes`` bytes, not shared with
+    a call that may run at the same time (allocated when None)."""
+    import torch
+    lead = tuple(h.shape[:-1])
+    c = _LossCall(h, w, bias, [("target", target, lead, torch.int64)], stream)
+    loss = c.output("loss", loss, lead, torch.float32)
+    lse = c.output("lse", lse, lead, torch.float32)
+    ws = c.workspace(workspace, softmax_xent_workspace_bytes(c.rows, c.d, c.vocab, c.code))
+    c.run(load_library().txl_softmax_xent_fwd, "txl_softmax_xent_fwd", _ptr(h), _ptr(w), _ptr(bias), _ptr(target),
+          c.rows, c.d, c.vocab, c.code, _ptr(loss), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size())
+    return loss, lse
+
+
+def softmax_xent_bwd(h, w, target, lse, dloss, bias=None, grads=None, weight_grads: bool = True, workspace=None,
+                     stream=None):
+    """Gradients of ``(dloss * loss).sum()`` of one ``softmax_xent_fwd`` call
+    (txl_softmax_xent_bwd): a dict ``dh`` (like h), ``dw`` (like w) and ``db``
+    (float32 [vocab]; None without a bias).  ``lse``: the forward's; ``dloss``:
+    float32 [*lead] (1 / tokens for a mean).  ``weight_grads=False`` skips dw
+    and db (a frozen output layer).  ``grads``: preallocated outputs with the
+    same keys; ``workspace`` as the forward's, of
+    ``softmax_xent_workspace_bytes(..., backward=True)`` bytes."""
+    import torch
+    lead = tuple(h.shape[:-1])
+    c = _LossCall(h, w, bias, [("target", target, lead, torch.int64), ("lse", lse, lead, torch.float32),
+                               ("dloss", dloss, lead, torch.float32)], stream)
+    g = _loss_grads(c, grads, w, bias, weight_grads)
+    ws = c.workspace(workspace, softmax_xent_workspace_bytes(c.rows, c.d, c.vocab, c.code, backward=True))
+    c.run(load_library().txl_softmax_xent_bwd, "txl_softmax_xent_bwd", _ptr(h), _ptr(w), _ptr(bias), _ptr(target),
+          _ptr(lse), _ptr(dloss), c.rows, c.d, c.vocab, c.code, _ptr(g["dh"]), _ptr(g["dw"]), _ptr(g["db"]), _ptr(ws),
+          ws.numel() * ws.element_size())
+    return g
+
+
+def _teacher(teacher_idx, teacher_logits, lead):
+    import torch
+    if teacher_idx.dim() != len(lead) + 1 or tuple(teacher_idx.shape[:-1]) != lead:
+        raise ValueError(f"teacher_idx must be {list(lead)} + [top_k]")
+    if teacher_logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"teacher_logits must be float32 or bfloat16, got {teacher_logits.dtype}")
+    shape = tuple(teacher_idx.shape)
+    return shape[-1], [("teacher_idx", teacher_idx, shape, torch.int64),
+                       ("teacher_logits", teacher_logits, shape, teacher_logits.dtype)]
+
+
+def distill_fwd(h, w, teacher_idx, teacher_logits, temperature: float = 1.0, bias=None, loss=None, lse=None,
+                workspace=None, stream=None):
+    """Distillation loss of the output layer against a teacher's kept logits
+    (txl_distill_fwd): per row temperature^2 times the KL divergence from the
+    teacher's softmax over its kept entries to the student's softmax over the
+    vocabulary, both at ``temperature``.
+
+    teacher_idx: [*lead, top_k] int64, teacher_logits: [*lead, top_k] float32
+    or bfloat16 (``torch.topk``'s outputs; entries with an index outside
+    [0, vocab) or a logit of -inf are left out, a row without entries is a
+    padding row: loss 0).  Everything else as ``softmax_xent_fwd``.  Returns
+    (loss, lse); lse is the student's at ``temperature``."""
+    import torch
+    lead = tuple(h.shape[:-1])
+    k, rows = _teacher(teacher_idx, teacher_logits, lead)
+    c = _LossCall(h, w, bias, rows, stream)
+    loss = c.output("loss", loss, lead, torch.float32)
+    lse = c.output("lse", lse, lead, torch.float32)
+    ws = c.workspace(workspace, distill_workspace_bytes(c.rows, c.d, c.vocab, k, c.code))
+    c.run(load_library().txl_distill_fwd, "txl_distill_fwd", _ptr(h), _ptr(w), _ptr(bias), _ptr(teacher_idx),
+          _ptr(teacher_logits), _dtype_code(teacher_logits), float(temperature), c.rows, c.d, c.vocab, k, c.code,
+          _ptr(loss), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size())
+    return loss, lse
+
+
+def distill_bwd(h, w, teacher_idx, teacher_logits, lse, dloss, temperature: float = 1.0, bias=None, grads=None,
+                weight_grads: bool = True, workspace=None, stream=None):
+    """Gradients of ``(dloss * loss).sum()`` of one ``distill_fwd`` call
+    (txl_distill_bwd), as ``softmax_xent_bwd`` returns them."""
+    import torch
+    lead = tuple(h.shape[:-1])
+    k, rows = _teacher(teacher_idx, teacher_logits, lead)
+    c = _LossCall(h, w, bias, rows + [("lse", lse, lead, torch.float32), ("dloss", dloss, lead, torch.float32)],
+                  stream)
+    g = _loss_grads(c, grads, w, bias, weight_grads)
+    ws = c.workspace(workspace, distill_workspace_bytes(c.rows, c.d, c.vocab, k, c.code, backward=True))
+    c.run(load_library().txl_distill_bwd, "txl_distill_bwd", _ptr(h), _ptr(w), _ptr(bias), _ptr(teacher_idx),
+          _ptr(teacher_logits), _dtype_code(teacher_logits), float(temperature), _ptr(lse), _ptr(dloss), c.rows, c.d,
+          c.vocab, k, c.code, _ptr(g["dh"]), _ptr(g["dw"]), _ptr(g["db"]), _ptr(ws), ws.numel() * ws.element_size())
+    return g
 
 
 def selftest_wait(limit_us: int, stream=None) -> None:
