@@ -11,6 +11,7 @@
 #include <new>
 
 #include "internal.h"
+#include "loss_products.h"
 #include "txl.h"
 
 namespace txl {
@@ -529,12 +530,13 @@ txl_status txl_check(void *stream)
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return cuda_fail(e);
-    unsigned int word = 0, gword = 0, bword = 0;
+    unsigned int word = 0, gword = 0, bword = 0, lword = 0;
     e = read_and_clear_device_error(&word, s);
     if (e == cudaSuccess) e = read_and_clear_gemm_error(&gword, s);
     if (e == cudaSuccess) e = read_and_clear_bwd_error(&bword, s);
+    if (e == cudaSuccess) e = read_and_clear_loss_error(&lword, s);
     if (e != cudaSuccess) return cuda_fail(e);
-    return (word | gword | bword) ? TXL_ERR_TIMEOUT : TXL_OK;
+    return (word | gword | bword | lword) ? TXL_ERR_TIMEOUT : TXL_OK;
 }
 
 const char *txl_status_string(txl_status st)

@@ -1,0 +1,73 @@
+// loss_products.h -- the matrix products of the output-layer losses
+// (loss_products.cu), as output_loss.cu launches them.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace txl {
+
+// One call's rows, as the kernels see them.
+struct LossRows {
+    int *col;        // [rows][K] listed columns, ascending; kNoColumn behind them
+    float *p;        // [rows][K] their weights
+    float *ent;      // [rows] sum_k p log p
+    float *coef;     // [rows] t * dloss, 0 for an empty row (backward)
+    float *l2;       // [rows] lse * log2(e) (backward)
+    int K;
+};
+constexpr int kNoColumn = INT32_MAX;   // an invalid list entry: sorts behind every column
+
+// A bf16 matrix in device memory, [pieces][rows][cols] with `pitch` elements
+// between rows (a multiple of 8, 16-byte aligned base).  One piece holds
+// bf16 values; three hold fp32 values as the exact sum of their pieces.
+struct LossMatrix {
+    const void *base;
+    long pitch, piece_stride;
+    int rows, cols, pieces;
+};
+
+// How a launch divides its work (the split itself depends on sizes only).
+struct LossTiling {
+    int cg;             // CTAs per tile: 2 for outputs of more than 128 rows, else 1
+    int bn;             // output columns per tile
+    int tiles_m, tiles_n;
+    int strip;          // vocabulary passes: tiles of one row block that a CTA (pair) does in a row
+    int splits;         // contractions: parts of the long axis, each into a slot of its own
+};
+
+// Vocabulary pass over rows x cols logits.
+LossTiling vocab_tiling(int rows, int cols, int d, int pieces);
+// Contraction to m x n over k.
+LossTiling contract_tiling(int m, int n, int k, int pieces, bool always_slots);
+inline int vocab_strips(const LossTiling &t) { return (t.tiles_n + t.strip - 1) / t.strip; }
+constexpr int kSlotsPerStrip = 2;      // the halves of a tile's columns are kept apart
+
+// part[2 * strip + half][row] = (maximum, sum of 2^(y - maximum)) over the
+// columns, y = alpha (h . w) + bz; ysel[row][k] = y at the listed columns
+// (vocabulary column = v0 + column of w).
+cudaError_t launch_loss_lse(const LossMatrix &h, const LossMatrix &w, const float *bz, int v0, float alpha,
+                            const LossRows &r, float *ysel, float2 *part, const LossTiling &t, cudaStream_t s);
+
+// dz = coef (2^(y - l2) - listed weights), in dz's pieces; dbpart[row / 32][column]
+// (pitch dz.pitch) the columns' sums over 32 rows each, when given.
+cudaError_t launch_loss_dz(const LossMatrix &h, const LossMatrix &w, const float *bz, int v0, float alpha,
+                           const LossRows &r, const LossMatrix &dz, float *dbpart, const LossTiling &t,
+                           cudaStream_t s);
+
+// out[m][n] = sum_k a(m, k) b(k, n).  a is stored [m][k], or [k][m] with
+// a_t; b is stored [k][n].  out_f32 selects fp32 output; it then has
+// `splits` slots of slot_stride elements (the sum of which is the product),
+// added to what they hold with `add`.
+struct LossOutput {
+    void *base;
+    long pitch, slot_stride;
+    bool f32, add;
+};
+cudaError_t launch_loss_contract(const LossMatrix &a, bool a_t, const LossMatrix &b, int m, int n, int k,
+                                 const LossOutput &out, const LossTiling &t, cudaStream_t s);
+
+cudaError_t read_and_clear_loss_error(unsigned int *word, cudaStream_t s);
+
+}  // namespace txl

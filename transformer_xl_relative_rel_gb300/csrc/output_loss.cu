@@ -8,12 +8,12 @@
 // same with one entry of weight 1 and t = 1.  Both reduce to a sparse list
 // of (column, weight) per row, so one set of kernels serves both:
 //
-//   loss_rows_kernel   the row lists (for the backward also the row's factor
+//   *_rows_kernel      the row lists (for the backward also the row's factor
 //                      t * dloss and lse in base-2 units);
-//   lse pass           per 64-row block and strip of vocabulary tiles, the
-//                      running maximum and sum of the softmax; the logits of
-//                      the listed columns are kept on the way;
-//   loss_merge_kernel  joins the strips, loss and lse;
+//   forward            one pass over the vocabulary (loss_products.cu) leaves
+//                      a maximum and a sum per row and strip of vocabulary
+//                      tiles and the logits of the listed columns;
+//                      loss_merge_kernel joins them;
 //   backward           for each piece of the vocabulary: dz (one piece of it
 //                      in the workspace), dh += dz W, dW = dz^T h, and the
 //                      column sums of dz.
@@ -26,13 +26,13 @@
 #include <stdint.h>
 
 #include "internal.h"
+#include "loss_products.h"
 #include "txl.h"
 
 namespace txl {
 namespace {
 
 constexpr int kMaxTopK = 256;
-constexpr int kNoColumn = INT32_MAX;   // an invalid list entry: sorts behind every column
 constexpr float kLn2 = 0.693147180559945309f;
 
 template <typename T>
@@ -48,16 +48,6 @@ template <>
 __device__ __forceinline__ float from_f<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16(x); }
-
-// One call's rows, as the kernels see them.
-struct LossRows {
-    int *col;        // [rows][K] listed columns, ascending; kNoColumn behind them
-    float *p;        // [rows][K] their weights
-    float *ent;      // [rows] sum_k p log p
-    float *coef;     // [rows] t * dloss, 0 for an empty row (backward)
-    float *l2;       // [rows] lse * log2(e) (backward)
-    int K;
-};
 
 // cross entropy: one entry of weight 1
 __global__ void __launch_bounds__(256)
@@ -169,231 +159,161 @@ distill_rows_kernel(const int64_t *__restrict__ idx, const TT *__restrict__ logi
     }
 }
 
-// bz[j] = bias_j log2(e) / t (0 without a bias)
+// bz[j] = bias_j log2(e) / t
 __global__ void __launch_bounds__(256) bias_scale_kernel(const float *__restrict__ bias, float alpha,
                                                          float *__restrict__ bz, int vocab)
 {
     const int j = blockIdx.x * 256 + threadIdx.x;
-    if (j < vocab) bz[j] = bias ? bias[j] * alpha : 0.f;
+    if (j < vocab) bz[j] = bias[j] * alpha;
 }
 
-// ------------------------------------------------------------------ products
-// 64 x 64 tiles of sum_k A[m][k] B[k][n], 256 threads, 4 x 4 elements each.
-constexpr int TM = 64, TN = 64, TK = 16;
-struct TileSmem {
-    float a[TK][TM + 1], b[TK][TN + 1];
-};
-
-template <typename FA, typename FB>
-__device__ __forceinline__ void tile_product(TileSmem &s, int K, FA fa, FB fb, float (&acc)[4][4])
-{
-    const int tid = threadIdx.x, tr = tid / 16, tc = tid % 16;
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-#pragma unroll
-        for (int y = 0; y < 4; ++y) acc[x][y] = 0.f;
-    for (int k0 = 0; k0 < K; k0 += TK) {
-        for (int x = tid; x < TK * TM; x += 256) {
-            s.a[x % TK][x / TK] = k0 + x % TK < K ? fa(x / TK, k0 + x % TK) : 0.f;
-            s.b[x % TK][x / TK] = k0 + x % TK < K ? fb(x / TK, k0 + x % TK) : 0.f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < TK; ++k) {
-            float av[4], bv[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                av[x] = s.a[k][tr + 16 * x];
-                bv[x] = s.b[k][tc + 16 * x];
-            }
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-#pragma unroll
-                for (int y = 0; y < 4; ++y) acc[x][y] = fmaf(av[x], bv[y], acc[x][y]);
-        }
-        __syncthreads();
-    }
-}
-
-struct LossShape {
-    int rows, d, vocab, strips;
-    float alpha;    // log2(e) / t
-};
-
-// the tile's y_ij in shared memory, -infinity past the vocabulary
-template <typename T>
-__device__ __forceinline__ void logits_tile(TileSmem &s, float (*y)[TN + 1], const T *h, const T *w, const float *bz,
-                                            const LossShape &q, int m0, int n0)
-{
-    float acc[4][4];
-    tile_product(s, q.d,
-                 [&](int m, int k) { return m0 + m < q.rows ? to_f(h[(long)(m0 + m) * q.d + k]) : 0.f; },
-                 [&](int n, int k) { return n0 + n < q.vocab ? to_f(w[(long)(n0 + n) * q.d + k]) : 0.f; }, acc);
-    const int tr = threadIdx.x / 16, tc = threadIdx.x % 16;
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int n = n0 + tc + 16 * c;
-            y[tr + 16 * x][tc + 16 * c] = n < q.vocab ? fmaf(acc[x][c], q.alpha, bz[n]) : -INFINITY;
-        }
-    __syncthreads();
-}
-
-// part[strip][row] = (maximum, sum of 2^(y - maximum)) over the strip's
-// columns; ysel[row][k] = y at the row's listed columns
+// An operand of the products that the TMA unit cannot read as it lies (fp32,
+// row pitch or base not a multiple of 16 bytes), or h of the backward, whose
+// rows of factor 0 come out as zeros whatever they hold: dst[part][row][dp]
+// with zeros past d.  One part holds bf16 values, three the fp32 values
+// (each the bf16 nearest to what the parts before it leave; finite values
+// that would round to infinity round down instead).  One thread per 8
+// elements; HBM-bound.
 template <typename T>
 __global__ void __launch_bounds__(256)
-lse_kernel(const T *__restrict__ h, const T *__restrict__ w, const float *__restrict__ bz, LossRows r,
-           float *__restrict__ ysel, float2 *__restrict__ part, LossShape q)
+operand_kernel(const T *__restrict__ src, __nv_bfloat16 *__restrict__ dst, int rows, int d, int dp, long part_stride,
+               const float *__restrict__ coef, int vec)
 {
-    __shared__ TileSmem s;
-    __shared__ float y[TM][TN + 1];
-    const int m0 = blockIdx.x * TM, strip = blockIdx.y;
-    const int tiles = (q.vocab + TN - 1) / TN;
-    const int t0 = (int)((long)strip * tiles / q.strips), t1 = (int)((long)(strip + 1) * tiles / q.strips);
-    const int row = threadIdx.x >> 2, sub = threadIdx.x & 3, i = m0 + row;
-    float m = -INFINITY, l = 0.f;
-    for (int t = t0; t < t1; ++t) {
-        const int n0 = t * TN;
-        logits_tile(s, y, h, w, bz, q, m0, n0);
-        float cm = m;
-        for (int c = sub; c < TN; c += 4) cm = fmaxf(cm, y[row][c]);
-        if (cm != -INFINITY) {
-            l *= exp2f(m - cm);
-            for (int c = sub; c < TN; c += 4) l += exp2f(y[row][c] - cm);
-            m = cm;
+    const int per = dp / 8;
+    const long n = (long)rows * per;
+    for (long x = (long)blockIdx.x * 256 + threadIdx.x; x < n; x += (long)gridDim.x * 256) {
+        const long i = x / per;
+        const int c = (int)(x - i * per) * 8;
+        float v[8];
+        if (coef && coef[i] == 0.f) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = 0.f;
+        } else if (vec) {   // 16-byte aligned rows
+            __align__(16) T t[8];
+#pragma unroll
+            for (int j = 0; j < (int)sizeof(T) / 2; ++j)
+                reinterpret_cast<uint4 *>(t)[j] = reinterpret_cast<const uint4 *>(src + i * d + c)[j];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = to_f(t[j]);
         } else {
-            for (int c = sub; c < TN; c += 4) l += exp2f(y[row][c]);   // all -infinity, or NaN
-        }
-        if (i < q.rows)
-            for (int k = sub; k < r.K; k += 4) {
-                const int c = r.col[(long)i * r.K + k];
-                if (c >= n0 && c < n0 + TN) ysel[(long)i * r.K + k] = y[row][c - n0];
-            }
-        __syncthreads();
-    }
 #pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
-        const float mm = fmaxf(m, m2), ref = mm == -INFINITY ? 0.f : mm;
-        l = l * exp2f(m - ref) + l2 * exp2f(m2 - ref);
-        m = mm;
+            for (int j = 0; j < 8; ++j) v[j] = c + j < d ? to_f(src[i * d + c + j]) : 0.f;
+        }
+        const long at = i * dp + c;
+#pragma unroll
+        for (int part = 0; part < (sizeof(T) == 4 ? 3 : 1); ++part) {
+            __align__(16) __nv_bfloat16 b[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                __nv_bfloat16 r = __float2bfloat16(v[j]);
+                if (sizeof(T) == 4) {
+                    float f = __bfloat162float(r);
+                    if (isinf(f) && !isinf(v[j])) {
+                        f = __uint_as_float(__float_as_uint(v[j]) & 0xffff0000u);
+                        r = __float2bfloat16(f);
+                    }
+                    v[j] = isfinite(v[j]) ? v[j] - f : 0.f;
+                }
+                b[j] = r;
+            }
+            *reinterpret_cast<uint4 *>(dst + part * part_stride + at) = *reinterpret_cast<const uint4 *>(b);
+        }
     }
-    if (sub == 0 && i < q.rows) part[(long)strip * q.rows + i] = make_float2(m, l);
 }
 
+// out[row][c] = the sum of the slots' [row][dp] partial products, in order
+template <typename T>
 __global__ void __launch_bounds__(256)
+slots_kernel(const float *__restrict__ slot, int slots, long slot_stride, T *__restrict__ out, int rows, int d, int dp)
+{
+    const int per = (d + 3) / 4;
+    const long n = (long)rows * per;
+    for (long x = (long)blockIdx.x * 256 + threadIdx.x; x < n; x += (long)gridDim.x * 256) {
+        const long i = x / per;
+        const int c = (int)(x - i * per) * 4;
+        float4 sum = *reinterpret_cast<const float4 *>(slot + i * dp + c);
+        for (int k = 1; k < slots; ++k) {
+            const float4 e = *reinterpret_cast<const float4 *>(slot + k * slot_stride + i * dp + c);
+            sum.x += e.x, sum.y += e.y, sum.z += e.z, sum.w += e.w;
+        }
+        const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (c + j < d) out[i * d + c + j] = from_f<T>(v[j]);
+    }
+}
+
+// Joins the strips of a row's softmax and its listed logits: 32 rows per
+// block (coalesced over rows), 32 threads of a column of the block share a
+// row's slots and entries.
+__global__ void __launch_bounds__(1024)
 loss_merge_kernel(const float2 *__restrict__ part, int slots, const float *__restrict__ ysel, LossRows r, float t2,
                   float *__restrict__ loss, float *__restrict__ lse, int rows)
 {
-    const int i = blockIdx.x * 256 + threadIdx.x;
-    if (i >= rows) return;
-    float m = -INFINITY;
-    for (int x = 0; x < slots; ++x) m = fmaxf(m, part[(long)x * rows + i].x);
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    for (int x = 0; x < slots; ++x) {
-        const float2 e = part[(long)x * rows + i];
-        l += e.y * exp2f(e.x - ref);
-    }
-    const float y_lse = ref + log2f(l);
-    lse[i] = y_lse * kLn2;
-    float dot = 0.f;
-    bool any = false;
-    for (int k = 0; k < r.K; ++k) {
-        if (r.col[(long)i * r.K + k] == kNoColumn) continue;
-        any = true;
-        const float p = r.p[(long)i * r.K + k];
-        if (p != 0.f) dot += p * (y_lse - ysel[(long)i * r.K + k]);
-    }
-    loss[i] = any && y_lse != -INFINITY ? t2 * (r.ent[i] + kLn2 * dot) : 0.f;
-}
-
-// one piece of dz (columns v0 .. v0+cols) and its column sums per row block
-template <typename T>
-__global__ void __launch_bounds__(256)
-dz_kernel(const T *__restrict__ h, const T *__restrict__ w, const float *__restrict__ bz, LossRows r,
-          T *__restrict__ dz, float *__restrict__ dbpart, LossShape q, int v0, int cols)
-{
-    __shared__ TileSmem s;
-    __shared__ float y[TM][TN + 1];
-    const int m0 = blockIdx.x * TM, c0 = blockIdx.y * TN, n0 = v0 + c0;
-    LossShape qq = q;
-    qq.vocab = v0 + cols;
-    logits_tile(s, y, h, w, bz, qq, m0, n0);
-    const int row = threadIdx.x >> 2, sub = threadIdx.x & 3, i = m0 + row;
-    const float coef = i < q.rows ? r.coef[i] : 0.f, l2 = i < q.rows ? r.l2[i] : 0.f;
-    for (int c = sub; c < TN; c += 4) y[row][c] = coef != 0.f ? coef * exp2f(y[row][c] - l2) : 0.f;
-    __syncwarp();
-    if (coef != 0.f)   // entries of one column: the same thread, in order
-        for (int k = 0; k < r.K; ++k) {
-            const int c = r.col[(long)i * r.K + k] - n0;
-            if (c >= 0 && c < TN && (c & 3) == sub) y[row][c] -= coef * r.p[(long)i * r.K + k];
+    __shared__ float sm[32][33], sl[32][33];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const long i = (long)blockIdx.x * 32 + tx;
+    float m = -INFINITY, l = 0.f;
+    if (i < rows)
+        for (int x = ty; x < slots; x += 32) {
+            const float2 e = part[(long)x * rows + i];
+            const float mm = fmaxf(m, e.x), ref = mm == -INFINITY ? 0.f : mm;
+            l = l * exp2f(m - ref) + e.y * exp2f(e.x - ref);
+            m = mm;
         }
+    sm[ty][tx] = m;
+    sl[ty][tx] = l;
     __syncthreads();
-    for (int x = threadIdx.x; x < TM * TN; x += 256)
-        if (m0 + x / TN < q.rows && c0 + x % TN < cols)
-            dz[(long)(m0 + x / TN) * cols + c0 + x % TN] = from_f<T>(y[x / TN][x % TN]);
-    if (dbpart && threadIdx.x < TN && c0 + threadIdx.x < cols) {
-        float sum = 0.f;
-        for (int m = 0; m < TM; ++m) sum += y[m][threadIdx.x];
-        dbpart[(long)blockIdx.x * cols + c0 + threadIdx.x] = sum;
+    // warp ty takes row ty of the block: lane tx one thread's part of it
+    const long row = (long)blockIdx.x * 32 + ty;
+    if (row >= rows) return;
+    m = sm[tx][ty];
+    l = sl[tx][ty];
+    float mm = m;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+    const float ref = mm == -INFINITY ? 0.f : mm;
+    l *= exp2f(m - ref);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const float y_lse = ref + log2f(l);
+    float dot = 0.f;
+    int any = 0;
+    for (int k = tx; k < r.K; k += 32) {
+        if (r.col[row * r.K + k] == kNoColumn) continue;
+        any = 1;
+        const float p = r.p[row * r.K + k];
+        if (p != 0.f) dot += p * (y_lse - ysel[row * r.K + k]);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        any |= __shfl_xor_sync(0xffffffffu, any, o);
+    }
+    if (tx == 0) {
+        lse[row] = y_lse * kLn2;
+        loss[row] = any && y_lse != -INFINITY ? t2 * (r.ent[row] + kLn2 * dot) : 0.f;
     }
 }
 
-__global__ void __launch_bounds__(256)
-dbias_kernel(const float *__restrict__ dbpart, int parts, int cols, float *__restrict__ db)
+// db[j] = the sum of the row groups' sums: 32 columns per block, 32 threads
+// per column
+__global__ void __launch_bounds__(1024)
+dbias_kernel(const float *__restrict__ dbpart, int parts, long pitch, int cols, float *__restrict__ db)
 {
-    const int j = blockIdx.x * 256 + threadIdx.x;
-    if (j >= cols) return;
+    __shared__ float s[32][33];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const long j = (long)blockIdx.x * 32 + tx;
     float sum = 0.f;
-    for (int x = 0; x < parts; ++x) sum += dbpart[(long)x * cols + j];
-    db[j] = sum;
-}
-
-// dh += dz W over one piece, in fp32; the last piece rounds
-template <typename T>
-__global__ void __launch_bounds__(256)
-dh_kernel(const T *__restrict__ dz, const T *__restrict__ w, float *__restrict__ acc, T *__restrict__ dh, int rows,
-          int d, int cols, int first, int last)
-{
-    __shared__ TileSmem s;
-    const int m0 = blockIdx.x * TM, n0 = blockIdx.y * TN;
-    float a[4][4];
-    tile_product(s, cols, [&](int m, int k) { return m0 + m < rows ? to_f(dz[(long)(m0 + m) * cols + k]) : 0.f; },
-                 [&](int n, int k) { return n0 + n < d ? to_f(w[(long)k * d + n0 + n]) : 0.f; }, a);
-    const int tr = threadIdx.x / 16, tc = threadIdx.x % 16;
-    for (int x = 0; x < 4; ++x)
-        for (int c = 0; c < 4; ++c) {
-            const int m = m0 + tr + 16 * x, n = n0 + tc + 16 * c;
-            if (m >= rows || n >= d) continue;
-            float v = a[x][c];
-            if (!first) v += acc[(long)m * d + n];
-            if (last)
-                dh[(long)m * d + n] = from_f<T>(v);
-            else
-                acc[(long)m * d + n] = v;
-        }
-}
-
-// dW of one piece; rows whose factor is 0 are left out whatever h holds there
-template <typename T>
-__global__ void __launch_bounds__(256)
-dw_kernel(const T *__restrict__ dz, const T *__restrict__ h, const float *__restrict__ coef, T *__restrict__ dw,
-          int rows, int d, int cols)
-{
-    __shared__ TileSmem s;
-    const int m0 = blockIdx.x * TM, n0 = blockIdx.y * TN;
-    float a[4][4];
-    tile_product(s, rows, [&](int m, int k) { return m0 + m < cols ? to_f(dz[(long)k * cols + m0 + m]) : 0.f; },
-                 [&](int n, int k) { return n0 + n < d && coef[k] != 0.f ? to_f(h[(long)k * d + n0 + n]) : 0.f; }, a);
-    const int tr = threadIdx.x / 16, tc = threadIdx.x % 16;
-    for (int x = 0; x < 4; ++x)
-        for (int c = 0; c < 4; ++c) {
-            const int m = m0 + tr + 16 * x, n = n0 + tc + 16 * c;
-            if (m < cols && n < d) dw[(long)m * d + n] = from_f<T>(a[x][c]);
-        }
+    if (j < cols)
+        for (int x = ty; x < parts; x += 32) sum += dbpart[x * pitch + j];
+    s[ty][tx] = sum;
+    __syncthreads();
+    if (ty == 0 && j < cols) {
+        float all = 0.f;
+        for (int x = 0; x < 32; ++x) all += s[x][tx];
+        db[j] = all;
+    }
 }
 
 // ---------------------------------------------------------------- host side
@@ -406,16 +326,25 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb)
     return x < y + nb && y < x + na;
 }
 
-constexpr size_t kPieceBytes = (size_t)64 << 20;   // one piece of dz
+constexpr size_t kPieceBytes = (size_t)64 << 20;   // one piece of dz and of copied weights
 constexpr int kMaxSize = 1 << 30;                  // rows and vocabulary
+constexpr int kPieceUnit = 256;                    // vocabulary pieces start at multiples of the widest tile
 
-// Where things lie in the workspace, from the shape alone.
+long up(long a, long b) { return (a + b - 1) / b * b; }
+
+// How a call is divided and where things lie in the workspace; from sizes,
+// alignment and the number of SMs alone.
 struct LossPlan {
-    int strips, piece;     // vocabulary strips of the forward, columns of a backward piece
-    size_t col, p, ent, coef, l2, bz, ysel, part, dz, acc, dbpart, bytes;
+    int parts, dp;          // bf16 parts of an element; operand row pitch (d rounded up to 8)
+    bool copy_h, copy_w;
+    int piece;              // vocabulary columns per piece
+    int slots;              // forward: partial softmaxes per row over all pieces
+    LossTiling dh;          // of a whole piece
+    bool dh_slots;
+    size_t col, p, ent, coef, l2, bz, ysel, part, h, w, dz, dh_acc, dw_acc, dbpart, bytes;
 };
 
-LossPlan loss_plan(int rows, int d, int vocab, int K, size_t esz, bool backward)
+LossPlan loss_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool backward, bool h_ok, bool w_ok)
 {
     LossPlan q;
     size_t at = 0;
@@ -424,33 +353,61 @@ LossPlan loss_plan(int rows, int d, int vocab, int K, size_t esz, bool backward)
         at += (n + 255) / 256 * 256;
         return o;
     };
-    const int tiles = (vocab + TN - 1) / TN;
-    q.strips = tiles < 64 ? tiles : 64;
     const size_t n = (size_t)rows;
+    q.parts = dtype == TXL_F32 ? 3 : 1;
+    q.dp = (int)up(d, 8);
+    const bool tma = dtype == TXL_BF16 && d % 8 == 0;
+    q.copy_h = backward || !tma || !h_ok;
+    q.copy_w = !tma || !w_ok;
+    // what a vocabulary column of a piece takes
+    const size_t per = ((backward ? n : 0) + (q.copy_w ? (size_t)q.dp : 0)) * q.parts * 2;
+    size_t piece = per ? kPieceBytes / per / kPieceUnit * kPieceUnit : (size_t)vocab;
+    if (piece < (size_t)kPieceUnit) piece = kPieceUnit;
+    q.piece = piece < (size_t)vocab ? (int)piece : vocab;
     q.col = take(n * K * 4);
     q.p = take(n * K * 4);
     q.ent = take(n * 4);
     q.bz = take((size_t)vocab * 4);
-    const size_t common = at;
-    q.ysel = take(n * K * 4);
-    q.part = take(n * q.strips * 8);
-    const size_t fwd = at;
-    size_t piece = kPieceBytes / (n * esz > 0 ? n * esz : 1) / TN * TN;
-    if (piece < (size_t)TN) piece = TN;
-    if (piece > (size_t)TN * 65535) piece = (size_t)TN * 65535;
-    q.piece = piece < (size_t)vocab ? (int)piece : vocab;
-    q.coef = q.l2 = q.dz = q.acc = q.dbpart = 0;
-    if (backward) {
-        at = common;
+    q.h = take(q.copy_h ? n * q.dp * q.parts * 2 : 0);
+    q.w = take(q.copy_w ? (size_t)q.piece * q.dp * q.parts * 2 : 0);
+    q.coef = q.l2 = q.dz = q.dh_acc = q.dw_acc = q.dbpart = q.ysel = q.part = 0;
+    q.slots = 0;
+    q.dh_slots = false;
+    if (!backward) {
+        for (long v0 = 0; v0 < vocab; v0 += q.piece)
+            q.slots += kSlotsPerStrip *
+                       vocab_strips(vocab_tiling(rows, (int)(vocab - v0 < q.piece ? vocab - v0 : q.piece), d, q.parts));
+        q.ysel = take(n * K * 4);
+        q.part = take(n * q.slots * 8);
+    } else {
         q.coef = take(n * 4);
         q.l2 = take(n * 4);
-        q.dz = take(n * q.piece * esz);
-        q.acc = take(q.piece < vocab ? n * d * 4 : 0);
-        q.dbpart = take((n + TM - 1) / TM * q.piece * 4);
+        q.dz = take(n * up(q.piece, 64) * q.parts * 2);
+        q.dh_slots = q.piece < vocab;
+        q.dh = contract_tiling(rows, d, q.piece, q.parts, q.dh_slots);
+        // the last, narrower piece may split further
+        const int last = vocab % q.piece ? vocab % q.piece : q.piece;
+        const size_t dw_whole = (size_t)contract_tiling(q.piece, d, rows, q.parts, false).splits * q.piece;
+        const size_t dw_last = (size_t)contract_tiling(last, d, rows, q.parts, false).splits * last;
+        // whatever the output's alignment: the products go to the slots where TMA cannot write it
+        q.dh_acc = take((size_t)q.dh.splits * n * q.dp * 4);
+        q.dw_acc = take((dw_whole > dw_last ? dw_whole : dw_last) * q.dp * 4);
+        q.dbpart = take((size_t)up(rows, 32) / 32 * up(q.piece, 64) * 4);
     }
-    q.bytes = at > fwd ? at : fwd;
-    if (q.bytes == 0) q.bytes = 256;
+    q.bytes = at ? at : 256;
     return q;
+}
+
+// The bytes either direction may need whatever the buffers' alignment.
+size_t loss_bytes(int rows, int d, int vocab, int K, txl_dtype dtype, bool backward)
+{
+    size_t most = 0;
+    for (int b = 0; b <= (backward ? 1 : 0); ++b)
+        for (int ok = 0; ok < 4; ++ok) {
+            const size_t n = loss_plan(rows, d, vocab, K, dtype, b, ok & 1, ok & 2).bytes;
+            most = n > most ? n : most;
+        }
+    return most;
 }
 
 struct LossArgs {
@@ -484,7 +441,7 @@ txl_status loss_workspace(int rows, int d, int vocab, int K, txl_dtype dtype, in
     if (!bytes) return TXL_ERR_INVALID;
     const txl_status st = loss_sizes(rows, d, vocab, K, dtype);
     if (st != TXL_OK) return st;
-    *bytes = loss_plan(rows, d, vocab, K, dtype == TXL_F32 ? 4 : 2, backward != 0).bytes;
+    *bytes = loss_bytes(rows, d, vocab, K, dtype, backward != 0);
     return TXL_OK;
 }
 
@@ -527,9 +484,12 @@ txl_status loss_checks(const LossArgs &a, bool backward)
         for (const Buf &p : outs)
             if (&p != &o && overlap(o.p, o.bytes, p.p, p.bytes)) return TXL_ERR_INVALID;
     }
-    if (a.rows > 0 && a.ws_bytes < loss_plan(a.rows, a.d, a.vocab, a.K, esz, backward).bytes) return TXL_ERR_INVALID;
+    if (a.rows > 0 && a.ws_bytes < loss_plan(a.rows, a.d, a.vocab, a.K, a.dtype, backward, al(a.h, 16), al(a.w, 16)).bytes)
+        return TXL_ERR_INVALID;
     return TXL_OK;
 }
+
+float alpha_of(const LossArgs &a) { return 1.f / (kLn2 * (a.temp != 0.f ? a.temp : 1.f)); }
 
 LossRows rows_at(const LossArgs &a, const LossPlan &q)
 {
@@ -562,59 +522,138 @@ cudaError_t launch_rows(const LossArgs &a, const LossRows &r, const LossPlan &q,
                                                                        1.f / a.temp, a.temp, lse, dloss, r, a.rows,
                                                                        a.vocab, K2);
     }
-    const float alpha = 1.f / (kLn2 * (a.temp != 0.f ? a.temp : 1.f));
-    bias_scale_kernel<<<(a.vocab + 255) / 256, 256, 0, a.s>>>(a.bias, alpha, (float *)((unsigned char *)a.ws + q.bz),
-                                                              a.vocab);
+    if (a.bias)
+        bias_scale_kernel<<<(a.vocab + 255) / 256, 256, 0, a.s>>>(a.bias, alpha_of(a),
+                                                                  (float *)((unsigned char *)a.ws + q.bz), a.vocab);
     return cudaGetLastError();
 }
 
-LossShape shape_of(const LossArgs &a, const LossPlan &q)
+// a copied operand: h with the backward's row factors, or a piece of W
+cudaError_t copy_operand(const LossArgs &a, const LossPlan &q, const void *src, size_t at, int rows, long part_stride,
+                         const float *coef)
 {
-    return {a.rows, a.d, a.vocab, q.strips, 1.f / (kLn2 * (a.temp != 0.f ? a.temp : 1.f))};
+    __nv_bfloat16 *dst = (__nv_bfloat16 *)((unsigned char *)a.ws + at);
+    const long n = (long)rows * (q.dp / 8), want = (n + 255) / 256, most = 16L * device_sm_count();
+    const int grid = (int)(want < most ? want : most);
+    if (a.dtype == TXL_F32)
+        operand_kernel<float><<<grid, 256, 0, a.s>>>((const float *)src, dst, rows, a.d, q.dp, part_stride, coef,
+                                                     a.d % 8 == 0 && al(src, 16));
+    else
+        operand_kernel<__nv_bfloat16><<<grid, 256, 0, a.s>>>((const __nv_bfloat16 *)src, dst, rows, a.d, q.dp,
+                                                             part_stride, coef, a.d % 8 == 0 && al(src, 16));
+    return cudaGetLastError();
 }
 
-template <typename T>
+cudaError_t h_operand(const LossArgs &a, const LossPlan &q, const float *coef, LossMatrix *m)
+{
+    if (!q.copy_h) {
+        *m = {a.h, a.d, 0, a.rows, a.d, 1};
+        return cudaSuccess;
+    }
+    const long stride = (long)a.rows * q.dp;
+    *m = {(unsigned char *)a.ws + q.h, q.dp, stride, a.rows, q.dp, q.parts};
+    return copy_operand(a, q, a.h, q.h, a.rows, stride, coef);
+}
+
+// columns v0 .. v0+cols of the vocabulary
+cudaError_t w_operand(const LossArgs &a, const LossPlan &q, long v0, int cols, LossMatrix *m)
+{
+    const size_t esz = a.dtype == TXL_F32 ? 4 : 2;
+    const void *src = (const unsigned char *)a.w + (size_t)v0 * a.d * esz;
+    if (!q.copy_w) {
+        *m = {src, a.d, 0, cols, a.d, 1};
+        return cudaSuccess;
+    }
+    const long stride = (long)q.piece * q.dp;
+    *m = {(unsigned char *)a.ws + q.w, q.dp, stride, cols, q.dp, q.parts};
+    return copy_operand(a, q, src, q.w, cols, stride, nullptr);
+}
+
+cudaError_t sum_slots(const LossArgs &a, const LossPlan &q, const float *slot, int slots, long stride, void *out,
+                      int rows)
+{
+    const long n = (long)rows * ((a.d + 3) / 4), want = (n + 255) / 256, most = 16L * device_sm_count();
+    const int grid = (int)(want < most ? want : most);
+    if (a.dtype == TXL_F32)
+        slots_kernel<float><<<grid, 256, 0, a.s>>>(slot, slots, stride, (float *)out, rows, a.d, q.dp);
+    else
+        slots_kernel<__nv_bfloat16><<<grid, 256, 0, a.s>>>(slot, slots, stride, (__nv_bfloat16 *)out, rows, a.d, q.dp);
+    return cudaGetLastError();
+}
+
 cudaError_t run_fwd(const LossArgs &a)
 {
-    const LossPlan q = loss_plan(a.rows, a.d, a.vocab, a.K, sizeof(T), false);
+    const LossPlan q = loss_plan(a.rows, a.d, a.vocab, a.K, a.dtype, false, al(a.h, 16), al(a.w, 16));
     unsigned char *ws = (unsigned char *)a.ws;
     const LossRows r = rows_at(a, q);
+    const float *bz = (const float *)(ws + q.bz);
+    float2 *part = (float2 *)(ws + q.part);
+    LossMatrix h, w;
     cudaError_t e = launch_rows(a, r, q, false);
+    if (e == cudaSuccess) e = h_operand(a, q, nullptr, &h);
+    long slot = 0;
+    for (long v0 = 0; e == cudaSuccess && v0 < a.vocab; v0 += q.piece) {
+        const int cols = (int)(a.vocab - v0 < q.piece ? a.vocab - v0 : q.piece);
+        const LossTiling t = vocab_tiling(a.rows, cols, a.d, q.parts);
+        e = w_operand(a, q, v0, cols, &w);
+        if (e == cudaSuccess)
+            e = launch_loss_lse(h, w, a.bias ? bz + v0 : nullptr, (int)v0, alpha_of(a), r, (float *)(ws + q.ysel),
+                                part + slot * a.rows, t, a.s);
+        slot += kSlotsPerStrip * vocab_strips(t);
+    }
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)((a.rows + TM - 1) / TM), (unsigned)q.strips);
-    lse_kernel<T><<<grid, 256, 0, a.s>>>((const T *)a.h, (const T *)a.w, (const float *)(ws + q.bz), r,
-                                         (float *)(ws + q.ysel), (float2 *)(ws + q.part), shape_of(a, q));
     const float t2 = a.temp != 0.f ? a.temp * a.temp : 1.f;
-    loss_merge_kernel<<<(a.rows + 255) / 256, 256, 0, a.s>>>((const float2 *)(ws + q.part), q.strips,
-                                                             (const float *)(ws + q.ysel), r, t2, a.loss, a.lse_out,
-                                                             a.rows);
+    loss_merge_kernel<<<(a.rows + 31) / 32, 1024, 0, a.s>>>(part, q.slots, (const float *)(ws + q.ysel), r, t2, a.loss,
+                                                            a.lse_out, a.rows);
     return cudaGetLastError();
 }
 
-template <typename T>
 cudaError_t run_bwd(const LossArgs &a)
 {
-    const LossPlan q = loss_plan(a.rows, a.d, a.vocab, a.K, sizeof(T), true);
+    const LossPlan q = loss_plan(a.rows, a.d, a.vocab, a.K, a.dtype, true, al(a.h, 16), al(a.w, 16));
     unsigned char *ws = (unsigned char *)a.ws;
     const LossRows r = rows_at(a, q);
+    const float *bz = (const float *)(ws + q.bz);
+    const size_t esz = a.dtype == TXL_F32 ? 4 : 2;
+    const bool tma_out = ((size_t)a.d * esz) % 16 == 0;   // rows that a TMA store can address
+    LossMatrix h, w;
     cudaError_t e = launch_rows(a, r, q, true);
-    const T *w = (const T *)a.w;
-    T *dz = (T *)(ws + q.dz);
-    const unsigned rb = (unsigned)((a.rows + TM - 1) / TM), db = (unsigned)((a.d + TN - 1) / TN);
+    if (e == cudaSuccess) e = h_operand(a, q, r.coef, &h);
     for (long v0 = 0; e == cudaSuccess && v0 < a.vocab; v0 += q.piece) {
         const int cols = (int)(a.vocab - v0 < q.piece ? a.vocab - v0 : q.piece);
-        const unsigned cb = (unsigned)((cols + TN - 1) / TN);
+        const long pitch = up(cols, 64);
+        const LossMatrix dz = {ws + q.dz, pitch, (long)a.rows * pitch, a.rows, cols, q.parts};
         float *dbp = a.db ? (float *)(ws + q.dbpart) : nullptr;
-        dz_kernel<T><<<dim3(rb, cb), 256, 0, a.s>>>((const T *)a.h, w, (const float *)(ws + q.bz), r, dz, dbp,
-                                                    shape_of(a, q), (int)v0, cols);
-        if (a.db) dbias_kernel<<<(cols + 255) / 256, 256, 0, a.s>>>(dbp, (int)rb, cols, a.db + v0);
-        if (a.dh)
-            dh_kernel<T><<<dim3(rb, db), 256, 0, a.s>>>(dz, w + v0 * a.d, (float *)(ws + q.acc), (T *)a.dh, a.rows,
-                                                        a.d, cols, v0 == 0, v0 + cols == a.vocab);
-        if (a.dw)
-            dw_kernel<T><<<dim3(cb, db), 256, 0, a.s>>>(dz, (const T *)a.h, r.coef, (T *)a.dw + v0 * a.d, a.rows, a.d,
-                                                        cols);
-        e = cudaGetLastError();
+        e = w_operand(a, q, v0, cols, &w);
+        if (e == cudaSuccess)
+            e = launch_loss_dz(h, w, a.bias ? bz + v0 : nullptr, (int)v0, alpha_of(a), r, dz, dbp,
+                               vocab_tiling(a.rows, cols, a.d, q.parts), a.s);
+        if (e == cudaSuccess && a.db) {
+            dbias_kernel<<<(cols + 31) / 32, 1024, 0, a.s>>>(dbp, (a.rows + 31) / 32, pitch, cols, a.db + v0);
+            e = cudaGetLastError();
+        }
+        if (e == cudaSuccess && a.dh) {
+            // every piece splits the same way, so that each adds to the same slots
+            const bool direct = !q.dh_slots && q.dh.splits == 1 && tma_out && al(a.dh, 16);
+            const long stride = (long)a.rows * q.dp;
+            float *acc = (float *)(ws + q.dh_acc);
+            const LossOutput out = direct ? LossOutput{a.dh, a.d, 0, a.dtype == TXL_F32, false}
+                                          : LossOutput{acc, q.dp, stride, true, v0 > 0};
+            e = launch_loss_contract(dz, false, w, a.rows, a.d, cols, out, q.dh, a.s);
+            if (e == cudaSuccess && !direct && v0 + cols == a.vocab)
+                e = sum_slots(a, q, acc, q.dh.splits, stride, a.dh, a.rows);
+        }
+        if (e == cudaSuccess && a.dw) {
+            const LossTiling t = contract_tiling(cols, a.d, a.rows, q.parts, false);
+            void *dst = (unsigned char *)a.dw + (size_t)v0 * a.d * esz;
+            const bool direct = t.splits == 1 && tma_out && al(dst, 16);
+            const long stride = (long)cols * q.dp;
+            float *acc = (float *)(ws + q.dw_acc);
+            const LossOutput out = direct ? LossOutput{dst, a.d, 0, a.dtype == TXL_F32, false}
+                                          : LossOutput{acc, q.dp, stride, true, false};
+            e = launch_loss_contract(dz, true, h, cols, a.d, a.rows, out, t, a.s);
+            if (e == cudaSuccess && !direct) e = sum_slots(a, q, acc, t.splits, stride, dst, cols);
+        }
     }
     return e;
 }
@@ -623,7 +662,7 @@ txl_status loss_fwd(const LossArgs &a)
 {
     const txl_status st = loss_checks(a, false);
     if (st != TXL_OK || a.rows == 0) return st;
-    const cudaError_t e = a.dtype == TXL_F32 ? run_fwd<float>(a) : run_fwd<__nv_bfloat16>(a);
+    const cudaError_t e = run_fwd(a);
     if (e == cudaSuccess) return TXL_OK;
     note_cuda_error(e);
     return TXL_ERR_CUDA;
@@ -638,7 +677,7 @@ txl_status loss_bwd(const LossArgs &a)
         if (a.dw) e = cudaMemsetAsync(a.dw, 0, (size_t)a.vocab * a.d * (a.dtype == TXL_F32 ? 4 : 2), a.s);
         if (e == cudaSuccess && a.db) e = cudaMemsetAsync(a.db, 0, (size_t)a.vocab * 4, a.s);
     } else if (a.dh || a.dw || a.db) {
-        e = a.dtype == TXL_F32 ? run_bwd<float>(a) : run_bwd<__nv_bfloat16>(a);
+        e = run_bwd(a);
     }
     if (e == cudaSuccess) return TXL_OK;
     note_cuda_error(e);
