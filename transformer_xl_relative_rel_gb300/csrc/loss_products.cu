@@ -11,8 +11,11 @@
 //             (MN-major tiles), nothing is transposed in memory.
 // fp32 operands are held as three bf16 parts whose sum is exact (8 + 8 + 8
 // bits of the 24-bit significand); the product keeps the six part products
-// down to 2^-16 of the largest, dropping three of at most 2^-24, and runs
-// them as one contraction six times as long, smallest first.
+// down to 2^-16 of the largest, dropping three of at most 2^-24, smallest
+// first.  The tensor core truncates where it accumulates (measured: a chain
+// of n additions comes out about n 2^-25 too small), so with fp32 operands an
+// accumulator takes one 64-deep step and the epilogue warps add the steps in
+// registers, rounding to nearest.
 //
 // Roles (12 warps): warp 0 issues the TMA loads, warp 1 the MMAs, warps 4-11
 // are two epilogue groups of four (a warp per 32 TMEM lanes), which share a
@@ -48,25 +51,30 @@ constexpr int LNT = 384;
 constexpr int LEPI = 8;                        // epilogue warps
 constexpr uint64_t LWAIT_NS = 2000000000ull;   // 2 s per wait, then give up
 
-template <int CG>
+// kParts: fp32 operands in three bf16 parts (128-wide tiles, one stage per
+// part); else bf16 operands (256-wide tiles).
+template <int CG, bool kParts>
 struct LSmem {
-    static constexpr int ST = CG == 2 ? 6 : 4;
+    static constexpr int BN = kParts ? 128 : 256;           // widest tile
+    static constexpr int ST = kParts ? (CG == 2 ? 8 : 6) : (CG == 2 ? 6 : 4);
     static constexpr uint32_t ASZ = 128 * 128;              // 128 rows of 64 elements
-    static constexpr uint32_t BSZ = 256 / CG * 128;
+    static constexpr uint32_t BSZ = BN / CG * 128;
     static constexpr uint32_t A = 0, B = A + ST * ASZ, OST = B + ST * BSZ, BARS = OST + LEPI * 4096;
     static constexpr int FULL = 0, EMPTY = ST, AFULL = 2 * ST, AEMPTY = 2 * ST + 2, DONE = 2 * ST + 4,
                          NBAR = 2 * ST + 5;
     static constexpr uint32_t MISC = BARS + NBAR * 8 + 8;
     static constexpr uint32_t TOTAL = MISC + 16 + 1024;
 };
-static_assert(LSmem<1>::TOTAL <= 232448 && LSmem<2>::TOTAL <= 232448, "shared memory");
+static_assert(LSmem<1, false>::TOTAL <= 232448 && LSmem<2, false>::TOTAL <= 232448 &&
+                  LSmem<1, true>::TOTAL <= 232448 && LSmem<2, true>::TOTAL <= 232448,
+              "shared memory");
 
 enum { MODE_LSE = 0, MODE_DZ = 1, MODE_CT = 2 };
 
 struct LParams {
     int M, N;                 // output extent
     int bn, tiles_m, tiles_n, strip, strips, items;
-    int ksteps, nprod, splits;
+    int ksteps, splits;
     int a_mn, b_mn;           // operands stored with the output index innermost
     // vocabulary passes
     const float *bz;          // [columns], biases in base-2 units; -infinity takes a column out
@@ -262,12 +270,12 @@ struct Cursor {
     }
 };
 
-template <int CG, int MODE>
+template <int CG, int MODE, bool kParts>
 __global__ void __launch_bounds__(LNT, 1)
 loss_product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                     const __grid_constant__ CUtensorMap mo, const LParams p)
 {
-    using S = LSmem<CG>;
+    using S = LSmem<CG, kParts>;
     constexpr int ST = S::ST;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(
@@ -332,11 +340,8 @@ loss_product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constan
                 const int m0 = t.m0 + rank * 128;
                 for (int nt = t.nt0; ok && nt < t.nt1; ++nt) {
                     const int n0 = nt * p.bn + rank * bcols;
-                    for (int q = 0; ok && q < p.nprod; ++q) {
-                        // part products (2,0) (1,1) (0,2) (1,0) (0,1) (0,0)
-                        const int pa = p.nprod == 1 ? 0 : (0x001012 >> (4 * q)) & 3;
-                        const int pb = p.nprod == 1 ? 0 : (0x010210 >> (4 * q)) & 3;
-                        for (int ks = t.ks0; ks < t.ks1; ++ks, ++it) {
+                    for (int ks = t.ks0; ok && ks < t.ks1; ++ks) {
+                        for (int part = 0; part < (kParts ? 3 : 1); ++part, ++it) {
                             const int s = it % ST;
                             if (it >= ST && !wait(S::EMPTY + s, ((it / ST) - 1) & 1)) {
                                 ok = false;
@@ -346,16 +351,16 @@ loss_product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constan
                             const uint32_t full = l_leader<CG>(bar(S::FULL + s));
                             if (rank == 0) mbar_arrive_expect_tx(bar(S::FULL + s), bytes);
                             if (p.a_mn) {
-                                l_load<CG>(da, &ma, full, m0, ks * LK, pa);
-                                l_load<CG>(da + 8192u, &ma, full, m0 + 64, ks * LK, pa);
+                                l_load<CG>(da, &ma, full, m0, ks * LK, part);
+                                l_load<CG>(da + 8192u, &ma, full, m0 + 64, ks * LK, part);
                             } else {
-                                l_load<CG>(da, &ma, full, ks * LK, m0, pa);
+                                l_load<CG>(da, &ma, full, ks * LK, m0, part);
                             }
                             if (p.b_mn) {
                                 for (int b = 0; b < nb; ++b)
-                                    l_load<CG>(db + 8192u * b, &mb, full, n0 + 64 * b, ks * LK, pb);
+                                    l_load<CG>(db + 8192u * b, &mb, full, n0 + 64 * b, ks * LK, part);
                             } else {
-                                l_load<CG>(db, &mb, full, ks * LK, n0, pb);
+                                l_load<CG>(db, &mb, full, ks * LK, n0, part);
                             }
                         }
                     }
@@ -386,30 +391,43 @@ loss_product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constan
             bool ok = true;
             for (int item = c0; ok && item < p.items; item += G) {
                 const LItem t = l_item<CG, MODE>(p, item);
-                for (int nt = t.nt0; ok && nt < t.nt1; ++nt, ++lt) {
-                    const int buf = lt & 1;
-                    if (lt >= 2 && !wait(S::AEMPTY + buf, ((lt >> 1) - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t acc = tmem + (uint32_t)(buf * 256);
-                    const int steps = p.nprod * (t.ks1 - t.ks0);
-                    for (int x = 0; x < steps; ++x, ++it) {
-                        const int s = it % ST;
-                        if (!wait(S::FULL + s, (it / ST) & 1)) {
+                for (int nt = t.nt0; ok && nt < t.nt1; ++nt) {
+                    for (int ks = t.ks0; ok && ks < t.ks1; ++lt) {
+                        // one accumulation: the whole K range, or one step of three parts
+                        const int buf = lt & 1, k1 = kParts ? ks + 1 : t.ks1;
+                        if (lt >= 2 && !wait(S::AEMPTY + buf, ((lt >> 1) - 1) & 1)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        const uint64_t da = da0 + ((uint64_t)(s * S::ASZ) >> 4);
-                        const uint64_t db = db0 + ((uint64_t)(s * S::BSZ) >> 4);
+                        const uint32_t acc = tmem + (uint32_t)(buf * 256);
+                        uint32_t more = 0u;
+                        for (; ok && ks < k1; ++ks) {
+                            constexpr int kStages = kParts ? 3 : 1;
+                            uint64_t da[kStages], db[kStages];
 #pragma unroll
-                        for (int k = 0; k < LK / 16; ++k)
-                            l_mma<CG>(acc, da + sa * k, db + sb * k, idesc, (x > 0 || k > 0) ? 1u : 0u);
-                        l_commit<CG>(bar(S::EMPTY + s));
+                            for (int part = 0; part < kStages; ++part) {
+                                const int s = (it + part) % ST;
+                                if (ok && !wait(S::FULL + s, ((it + part) / ST) & 1)) ok = false;
+                                da[part] = da0 + ((uint64_t)(s * S::ASZ) >> 4);
+                                db[part] = db0 + ((uint64_t)(s * S::BSZ) >> 4);
+                            }
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int x = kParts ? 0 : 5; x < 6; ++x) {
+                                constexpr int pa[6] = {2, 1, 0, 1, 0, 0}, pb[6] = {0, 1, 2, 0, 1, 0};
+#pragma unroll
+                                for (int k = 0; k < LK / 16; ++k) {
+                                    l_mma<CG>(acc, da[pa[x]] + sa * k, db[pb[x]] + sb * k, idesc, more);
+                                    more = 1u;
+                                }
+                            }
+#pragma unroll
+                            for (int part = 0; part < kStages; ++part, ++it) l_commit<CG>(bar(S::EMPTY + it % ST));
+                        }
+                        if (ok) l_commit<CG>(bar(S::AFULL + buf));
                     }
-                    if (ok) l_commit<CG>(bar(S::AFULL + buf));
                 }
             }
             // every MMA issued here has completed before the pair winds down
@@ -446,20 +464,53 @@ loss_product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constan
                     l2 = p.r.l2[row];
                 }
             }
-            for (int nt = t.nt0; nt < t.nt1; ++nt, ++lt) {
-                const int buf = lt & 1;
-                if (!wait(S::AFULL + buf, (lt >> 1) & 1)) {
-                    ok = false;
-                    break;
+            for (int nt = t.nt0; ok && nt < t.nt1; ++nt) {
+                const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16);
+                float acc[kParts ? 64 : 1];
+                if (kParts) {
+                    // this half's 64 columns, summed over the steps
+#pragma unroll
+                    for (int j = 0; j < (kParts ? 64 : 1); ++j) acc[j] = 0.f;
+                    for (int ks = t.ks0; ks < t.ks1; ++ks, ++lt) {
+                        if (!wait(S::AFULL + (lt & 1), (lt >> 1) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (half < nch) {
+#pragma unroll
+                            for (int sub = 0; sub < 2; ++sub) {
+                                float v[32];
+                                tmem_ld32(tq + (uint32_t)((lt & 1) * 256 + 64 * half + 32 * sub), v);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) acc[kParts ? 32 * sub + j : 0] += v[j];
+                            }
+                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) l_arrive_leader<CG>(bar(S::AEMPTY + (lt & 1)));
+                    }
+                    if (!ok) break;
+                } else {
+                    if (!wait(S::AFULL + (lt & 1), (lt >> 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
                 }
-                tc_fence_after();
-                const uint32_t tacc = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * 256);
+                const int buf = lt & 1;
+                const uint32_t tacc = tq + (uint32_t)(buf * 256);
                 for (int c = half; c < nch; c += 2) {
 #pragma unroll
                     for (int sub = 0; sub < 2; ++sub) {
                         const int n0 = nt * p.bn + 64 * c + 32 * sub;   // first output column of these 32
                         float v[32];
-                        tmem_ld32(tacc + (uint32_t)(64 * c + 32 * sub), v);
+                        if (kParts) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = acc[kParts ? 32 * sub + j : 0];
+                        } else {
+                            tmem_ld32(tacc + (uint32_t)(64 * c + 32 * sub), v);
+                        }
                         if (MODE == MODE_CT) {
                             if (p.f32) {
                                 if (row0 >= p.M || n0 >= p.N) continue;
@@ -566,7 +617,7 @@ loss_product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constan
 #pragma unroll
                                 for (int j = 0; j < 32; ++j) v[j] = 0.f;
                             }
-                            if (p.nprod == 1) {
+                            if (!kParts) {
                                 if (sub == 0) stage_wait();
 #pragma unroll
                                 for (int j = 0; j < 4; ++j) {
@@ -635,10 +686,13 @@ loss_product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constan
                         }
                     }
                 }
-                // this warp's part of the accumulator is in registers
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) l_arrive_leader<CG>(bar(S::AEMPTY + buf));
+                if (!kParts) {
+                    // this warp's part of the accumulator is in registers
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) l_arrive_leader<CG>(bar(S::AEMPTY + buf));
+                    ++lt;
+                }
             }
             if (MODE == MODE_LSE && ok && live)
                 p.part[(long)(kSlotsPerStrip * t.strip + half) * p.M + row] = make_float2(m, l);
@@ -689,11 +743,11 @@ cudaError_t l_in_map(CUtensorMap *m, const LossMatrix &x, int box_y)
                  box_y, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int CG, int MODE>
+template <int CG, int MODE, bool kParts>
 cudaError_t l_launch(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo, const LParams &p,
                      cudaStream_t s)
 {
-    auto kern = loss_product_kernel<CG, MODE>;
+    auto kern = loss_product_kernel<CG, MODE, kParts>;
     static std::atomic<int> most[64];      // tiles that run at once, per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -702,7 +756,7 @@ cudaError_t l_launch(const CUtensorMap &ma, const CUtensorMap &mb, const CUtenso
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
     cfg.blockDim = dim3(LNT);
-    cfg.dynamicSmemBytes = LSmem<CG>::TOTAL;
+    cfg.dynamicSmemBytes = LSmem<CG, kParts>::TOTAL;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -712,7 +766,7 @@ cudaError_t l_launch(const CUtensorMap &ma, const CUtensorMap &mb, const CUtenso
     cfg.numAttrs = 1;
     int n = most[dev].load(std::memory_order_relaxed);
     if (n == 0) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LSmem<CG>::TOTAL);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LSmem<CG, kParts>::TOTAL);
         if (e != cudaSuccess) return e;
         n = device_sm_count() / CG;
         if (CG == 2) {
@@ -730,10 +784,11 @@ cudaError_t l_launch(const CUtensorMap &ma, const CUtensorMap &mb, const CUtenso
 }
 
 template <int MODE>
-cudaError_t l_launch_cg(int cg, const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo, const LParams &p,
+cudaError_t l_launch_cg(int cg, int parts, const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo, const LParams &p,
                         cudaStream_t s)
 {
-    return cg == 2 ? l_launch<2, MODE>(ma, mb, mo, p, s) : l_launch<1, MODE>(ma, mb, mo, p, s);
+    if (parts == 3) return cg == 2 ? l_launch<2, MODE, true>(ma, mb, mo, p, s) : l_launch<1, MODE, true>(ma, mb, mo, p, s);
+    return cg == 2 ? l_launch<2, MODE, false>(ma, mb, mo, p, s) : l_launch<1, MODE, false>(ma, mb, mo, p, s);
 }
 
 // the fields the two vocabulary passes share
@@ -752,7 +807,6 @@ cudaError_t vocab_params(LParams &p, CUtensorMap &ma, CUtensorMap &mb, const Los
     if (items > INT32_MAX) return cudaErrorNotSupported;
     p.items = (int)items;
     p.ksteps = (h.cols + LK - 1) / LK;
-    p.nprod = h.pieces == 3 ? 6 : 1;
     p.splits = 1;
     p.bz = bz;
     p.has_bz = bz != nullptr;
@@ -772,7 +826,8 @@ LossTiling vocab_tiling(int rows, int cols, int d, int pieces)
 {
     LossTiling t;
     t.cg = rows > 128 ? 2 : 1;
-    t.bn = cols > 192 ? 256 : (cols + 63) / 64 * 64;
+    const int widest = pieces == 3 ? 128 : 256;
+    t.bn = cols > widest - 64 ? widest : (cols + 63) / 64 * 64;
     t.tiles_m = (int)cdiv(rows, 128 * t.cg);
     t.tiles_n = (int)cdiv(cols, t.bn);
     t.splits = 1;
@@ -788,7 +843,6 @@ LossTiling vocab_tiling(int rows, int cols, int d, int pieces)
         }
     }
     (void)d;
-    (void)pieces;
     return t;
 }
 
@@ -797,19 +851,20 @@ LossTiling contract_tiling(int m, int n, int k, int pieces, bool always_slots)
     LossTiling t;
     t.cg = m > 128 ? 2 : 1;
     t.tiles_m = (int)cdiv(m, 128 * t.cg);
-    t.tiles_n = (int)cdiv(n, 256);
+    t.tiles_n = (int)cdiv(n, pieces == 3 ? 128 : 256);
     t.bn = (int)(cdiv(cdiv(n, t.tiles_n), 64) * 64);
     t.strip = 1;
     const long slots = device_sm_count() / t.cg;
     const long ksteps = cdiv(k, LK) * (pieces == 3 ? 6 : 1);
+    const double step_us = 0.27 * t.bn / 256;
     // splits of the long axis fill the SMs; each costs a pass over its slot
-    // (about 0.27 us per 64-deep step of a tile, 5 TB/s for the slots)
+    // (0.27 us per 64-deep step of a 256-wide tile, 5 TB/s for the slots)
     double best = 1e300;
     t.splits = 1;
     for (int s = 1; s <= 64 && s <= cdiv(k, LK); ++s) {
         const double rounds = (double)cdiv((long)t.tiles_m * t.tiles_n * s, slots);
         const double passes = s > 1 || always_slots ? 2.0 * s * m * n * 4 / 5e6 : 0.0;
-        const double cost = rounds * ((double)cdiv(ksteps, s) + 6) * 0.27 + passes + (s > 1 ? 3.0 : 0.0);
+        const double cost = rounds * ((double)cdiv(ksteps, s) + 6) * step_us + passes + (s > 1 ? 3.0 : 0.0);
         if (cost < best) {
             best = cost;
             t.splits = s;
@@ -827,7 +882,7 @@ cudaError_t launch_loss_lse(const LossMatrix &h, const LossMatrix &w, const floa
     if (e != cudaSuccess) return e;
     p.ysel = ysel;
     p.part = part;
-    return l_launch_cg<MODE_LSE>(t.cg, ma, mb, ma, p, s);
+    return l_launch_cg<MODE_LSE>(t.cg, h.pieces, ma, mb, ma, p, s);
 }
 
 cudaError_t launch_loss_dz(const LossMatrix &h, const LossMatrix &w, const float *bz, int v0, float alpha,
@@ -844,7 +899,7 @@ cudaError_t launch_loss_dz(const LossMatrix &h, const LossMatrix &w, const float
     e = l_map(&mo, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dz.base, dz.cols, dz.rows, dz.pieces, dz.pitch,
               dz.piece_stride, three ? 32 : 64, 32, three ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
-    return l_launch_cg<MODE_DZ>(t.cg, ma, mb, mo, p, s);
+    return l_launch_cg<MODE_DZ>(t.cg, h.pieces, ma, mb, mo, p, s);
 }
 
 cudaError_t launch_loss_contract(const LossMatrix &a, bool a_t, const LossMatrix &b, int m, int n, int k,
@@ -863,7 +918,6 @@ cudaError_t launch_loss_contract(const LossMatrix &a, bool a_t, const LossMatrix
     if (items > INT32_MAX) return cudaErrorNotSupported;
     p.items = (int)items;
     p.ksteps = (k + LK - 1) / LK;
-    p.nprod = a.pieces == 3 ? 6 : 1;
     p.a_mn = a_t;
     p.b_mn = 1;
     p.f32 = out.f32;
@@ -876,7 +930,7 @@ cudaError_t launch_loss_contract(const LossMatrix &a, bool a_t, const LossMatrix
                   out.base, n, m, t.splits, out.pitch, out.slot_stride, out.f32 ? 32 : 64, 32,
                   CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
-    return l_launch_cg<MODE_CT>(t.cg, ma, mb, mo, p, s);
+    return l_launch_cg<MODE_CT>(t.cg, a.pieces, ma, mb, mo, p, s);
 }
 
 cudaError_t read_and_clear_loss_error(unsigned int *word, cudaStream_t s)
