@@ -168,7 +168,7 @@ template <int CG>
 __device__ __forceinline__ void l_arrive_leader(uint32_t bar)
 {
     if (CG == 2)
-        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(l_leader<CG>(bar)) : "memory");
+        asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(l_leader<CG>(bar)) : "memory");
     else
         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -201,6 +201,78 @@ __device__ __forceinline__ float ex2(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// pairs of fp32 in one instruction
+__device__ __forceinline__ uint64_t pair(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max32(const float (&v)[32], float m)
+{
+    float a[11];
+#pragma unroll
+    for (int j = 0; j < 10; ++j) a[j] = max3(v[3 * j], v[3 * j + 1], v[3 * j + 2]);
+    a[10] = max3(v[30], v[31], m);
+    const float x = max3(a[0], a[1], a[2]), y = max3(a[3], a[4], a[5]), z = max3(a[6], a[7], a[8]);
+    return max3(max3(x, y, z), a[9], a[10]);
+}
+
+// 32 columns of a warp's 32 TMEM lanes; nothing reads v before l_tmem_wait(v)
+__device__ __forceinline__ void l_tmem_issue(uint32_t taddr, float (&v)[32])
+{
+    uint32_t *r = reinterpret_cast<uint32_t *>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void l_tmem_wait(float (&v)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]),
+                   "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]),
+                   "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27])
+                 :
+                 : "memory");
+    asm volatile("" : "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])::"memory");
 }
 
 // ------------------------------------------------------------------- items
@@ -443,34 +515,204 @@ loss_product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constan
         const int nch = p.bn / 64;                                // 64-column chunks, alternately per half
         int lt = 0;
         bool ok = true;
-        // 32 rows x 128 bytes from the staging buffer; the previous store has read it first
+        // the staging buffer (32 rows x 128 bytes) is free once the previous store has read it
         auto stage_wait = [&]() {
             if (lane == 0) bulk_wait_read();
             __syncwarp();
         };
+        auto stage_bf16 = [&](const float (&v)[32], int at) {      // columns 32 at .. 32 at + 31 of the row
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint4 pk;
+                pk.x = pack2(v[8 * j + 0], v[8 * j + 1]);
+                pk.y = pack2(v[8 * j + 2], v[8 * j + 3]);
+                pk.z = pack2(v[8 * j + 4], v[8 * j + 5]);
+                pk.w = pack2(v[8 * j + 6], v[8 * j + 7]);
+                *reinterpret_cast<uint4 *>(stg + lane * 128 + (((4 * at + j) ^ (lane & 7)) << 4)) = pk;
+            }
+        };
+        auto store = [&](int x, int y, int z, bool add) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (add)
+                    l_reduce_3d(&mo, stg_a, x, y, z);
+                else
+                    tma_store_3d(&mo, stg_a, x, y, z);
+                bulk_commit();
+            }
+        };
+        auto release = [&](int buf) {      // this warp's part of the accumulator is in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) l_arrive_leader<CG>(bar(S::AEMPTY + buf));
+        };
+        const uint64_t alpha2 = pair(p.alpha, p.alpha);
+        // without biases the running maximum is kept of the unscaled logits
+        const float mscale = p.has_bz ? 1.f : p.alpha;
+
         for (int item = c0; ok && item < p.items; item += G) {
             const LItem t = l_item<CG, MODE>(p, item);
             const int row0 = t.m0 + rank * 128 + 32 * q, row = row0 + lane;
             const bool live = row < p.M;
             float m = -INFINITY, l = 0.f, coef = 0.f, l2 = 0.f;
             Cursor cur;
+            bool dead = false;
             if (MODE != MODE_CT) {
                 cur.K = live ? p.r.K : 0;
                 cur.col = p.r.col + (long)(live ? row : 0) * p.r.K;
                 cur.p = MODE == MODE_DZ ? p.r.p + (long)(live ? row : 0) * p.r.K : nullptr;
                 cur.seek(p.v0 + t.nt0 * p.bn);
-                if (MODE == MODE_DZ && live) {
-                    coef = p.r.coef[row];
-                    l2 = p.r.l2[row];
+                if (MODE == MODE_DZ) {
+                    if (live) {
+                        coef = p.r.coef[row];
+                        l2 = p.r.l2[row];
+                    }
+                    dead = __any_sync(0xffffffffu, coef == 0.f);
                 }
             }
+            // 32 columns from n0 on (the second half of their 64-column chunk with sub = 1)
+            auto process = [&](float (&v)[32], int n0, int sub) {
+                if (MODE == MODE_CT) {
+                    if (row0 >= p.M || n0 - 32 * sub >= p.N) return;
+                    if (p.f32) {
+                        if (n0 >= p.N) return;
+                        stage_wait();
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<float4 *>(stg + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                                make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                        store(n0, row0, t.split, p.add);
+                    } else {
+                        if (sub == 0) stage_wait();
+                        stage_bf16(v, sub);
+                        if (sub == 1) store(n0 - 32, row0, 0, false);
+                    }
+                    return;
+                }
+                if (n0 >= p.N) return;
+                const int col0 = p.v0 + n0;
+                // y = alpha z + bz in base-2 units (dz: less the row's lse)
+                if (p.has_bz) {
+                    const uint64_t off = pair(-l2, -l2);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 b4 = __ldg(reinterpret_cast<const float4 *>(p.bz + n0 + j));
+                        uint64_t b01 = pair(b4.x, b4.y), b23 = pair(b4.z, b4.w);
+                        if (MODE == MODE_DZ) {
+                            b01 = add2(b01, off);
+                            b23 = add2(b23, off);
+                        }
+                        unpair(fma2(pair(v[j], v[j + 1]), alpha2, b01), v[j], v[j + 1]);
+                        unpair(fma2(pair(v[j + 2], v[j + 3]), alpha2, b23), v[j + 2], v[j + 3]);
+                    }
+                }
+                if (n0 + 32 > p.N) {   // columns past the vocabulary
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (n0 + j >= p.N) v[j] = -INFINITY;
+                }
+                if (MODE == MODE_LSE) {
+                    while (cur.c0 < col0 + 32) {
+                        if (cur.c0 >= col0) {
+                            float y = 0.f;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) y = cur.c0 == col0 + j ? v[j] : y;
+                            p.ysel[(long)row * p.r.K + cur.pos] = y * mscale;
+                        }
+                        cur.next();
+                    }
+                    __syncwarp();
+                    const float cm = max32(v, m), ref = cm == -INFINITY ? 0.f : cm;
+                    const uint64_t off = pair(-ref * mscale, -ref * mscale), one = pair(mscale, mscale);
+                    uint64_t s[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float a, b;
+                        const uint64_t x = pair(v[2 * j], v[2 * j + 1]);
+                        unpair(p.has_bz ? add2(x, off) : fma2(x, one, off), a, b);
+                        s[j & 3] = add2(s[j & 3], pair(ex2(a), ex2(b)));
+                    }
+                    float a, b;
+                    unpair(add2(add2(s[0], s[1]), add2(s[2], s[3])), a, b);
+                    l = fmaf(l, ex2((m - ref) * mscale), a + b);
+                    m = cm;
+                } else {
+                    const uint64_t off = pair(-l2, -l2), c2 = pair(coef, coef);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        float a = v[j], b = v[j + 1];
+                        if (!p.has_bz) unpair(fma2(pair(a, b), alpha2, off), a, b);
+                        unpair(mul2(pair(ex2(a), ex2(b)), c2), v[j], v[j + 1]);
+                    }
+                    while (cur.c0 < col0 + 32) {
+                        if (cur.c0 >= col0) {
+                            const float g = coef * cur.p0;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (cur.c0 == col0 + j) v[j] -= g;
+                        }
+                        cur.next();
+                    }
+                    __syncwarp();
+                    if (dead) {   // whatever an empty row holds
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = coef == 0.f ? 0.f : v[j];
+                    }
+                    if (!kParts) {
+                        if (sub == 0) stage_wait();
+                        stage_bf16(v, sub);
+                        // the second half of the chunk may lie past the last column
+                        if ((sub == 1 || n0 + 32 >= p.N) && row0 < p.M) store(n0 - 32 * sub, row0, 0, false);
+                    } else {
+                        float rest[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) rest[j] = v[j];
+#pragma unroll
+                        for (int part = 0; part < 3; ++part) {
+                            stage_wait();
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                uint32_t w4[4];
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) {
+                                    const float a = rest[8 * j + 2 * x], b = rest[8 * j + 2 * x + 1];
+                                    const float ta = top_part(a), tb = top_part(b);
+                                    w4[x] = pack2(ta, tb);
+                                    rest[8 * j + 2 * x] = a - ta;
+                                    rest[8 * j + 2 * x + 1] = b - tb;
+                                }
+                                // 64-byte rows, their swizzle: chunk c of row r at c ^ (r / 2 % 4)
+                                *reinterpret_cast<uint4 *>(stg + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+                                    make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                            }
+                            if (row0 < p.M) store(n0, row0, part, false);
+                        }
+                    }
+                    if (p.dbpart) {
+                        // sums over the warp's 32 rows: halving exchanges leave column j in lane j
+#pragma unroll
+                        for (int o = 16; o; o >>= 1) {
+                            const bool up = lane & o;
+#pragma unroll
+                            for (int j = 0; j < o; ++j) {
+                                const float send = up ? v[j] : v[j + o];
+                                const float keep = up ? v[j + o] : v[j];
+                                v[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                            }
+                        }
+                        if (row0 < p.M && n0 + lane < p.N)
+                            p.dbpart[(long)(row0 >> 5) * p.dbpitch + n0 + lane] = v[0];
+                    }
+                }
+            };
+            const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16);
             for (int nt = t.nt0; ok && nt < t.nt1; ++nt) {
-                const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16);
-                float acc[kParts ? 64 : 1];
+                float v0[32], v1[32];
                 if (kParts) {
                     // this half's 64 columns, summed over the steps
 #pragma unroll
-                    for (int j = 0; j < (kParts ? 64 : 1); ++j) acc[j] = 0.f;
+                    for (int j = 0; j < 32; ++j) v0[j] = v1[j] = 0.f;
                     for (int ks = t.ks0; ks < t.ks1; ++ks, ++lt) {
                         if (!wait(S::AFULL + (lt & 1), (lt >> 1) & 1)) {
                             ok = false;
@@ -478,224 +720,54 @@ loss_product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constan
                         }
                         tc_fence_after();
                         if (half < nch) {
+                            const uint32_t at = tq + (uint32_t)((lt & 1) * 256 + 64 * half);
+                            float x[32];
+                            tmem_ld32(at, x);
 #pragma unroll
-                            for (int sub = 0; sub < 2; ++sub) {
-                                float v[32];
-                                tmem_ld32(tq + (uint32_t)((lt & 1) * 256 + 64 * half + 32 * sub), v);
+                            for (int j = 0; j < 32; ++j) v0[j] += x[j];
+                            tmem_ld32(at + 32u, x);
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) acc[kParts ? 32 * sub + j : 0] += v[j];
-                            }
+                            for (int j = 0; j < 32; ++j) v1[j] += x[j];
                         }
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) l_arrive_leader<CG>(bar(S::AEMPTY + (lt & 1)));
+                        release(lt & 1);
                     }
                     if (!ok) break;
-                } else {
-                    if (!wait(S::AFULL + (lt & 1), (lt >> 1) & 1)) {
-                        ok = false;
-                        break;
+                    if (half < nch) {
+                        process(v0, nt * p.bn + 64 * half, 0);
+                        process(v1, nt * p.bn + 64 * half + 32, 1);
                     }
-                    tc_fence_after();
+                    continue;
                 }
                 const int buf = lt & 1;
-                const uint32_t tacc = tq + (uint32_t)(buf * 256);
-                for (int c = half; c < nch; c += 2) {
-#pragma unroll
-                    for (int sub = 0; sub < 2; ++sub) {
-                        const int n0 = nt * p.bn + 64 * c + 32 * sub;   // first output column of these 32
-                        float v[32];
-                        if (kParts) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) v[j] = acc[kParts ? 32 * sub + j : 0];
-                        } else {
-                            tmem_ld32(tacc + (uint32_t)(64 * c + 32 * sub), v);
-                        }
-                        if (MODE == MODE_CT) {
-                            if (p.f32) {
-                                if (row0 >= p.M || n0 >= p.N) continue;
-                                stage_wait();
-#pragma unroll
-                                for (int j = 0; j < 8; ++j)
-                                    *reinterpret_cast<float4 *>(stg + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-                                        make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                                fence_proxy_async_smem();
-                                __syncwarp();
-                                if (lane == 0) {
-                                    if (p.add)
-                                        l_reduce_3d(&mo, stg_a, n0, row0, t.split);
-                                    else
-                                        tma_store_3d(&mo, stg_a, n0, row0, t.split);
-                                    bulk_commit();
-                                }
-                            } else {
-                                if (row0 >= p.M || n0 - 32 * sub >= p.N) continue;
-                                if (sub == 0) stage_wait();
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    uint4 pk;
-                                    pk.x = pack2(v[8 * j + 0], v[8 * j + 1]);
-                                    pk.y = pack2(v[8 * j + 2], v[8 * j + 3]);
-                                    pk.z = pack2(v[8 * j + 4], v[8 * j + 5]);
-                                    pk.w = pack2(v[8 * j + 6], v[8 * j + 7]);
-                                    *reinterpret_cast<uint4 *>(stg + lane * 128 + (((4 * sub + j) ^ (lane & 7)) << 4)) = pk;
-                                }
-                                if (sub == 1) {
-                                    fence_proxy_async_smem();
-                                    __syncwarp();
-                                    if (lane == 0) {
-                                        tma_store_3d(&mo, stg_a, n0 - 32, row0, 0);
-                                        bulk_commit();
-                                    }
-                                }
-                            }
-                            continue;
-                        }
-                        if (n0 >= p.N) continue;
-                        // y in base-2 units; columns past the vocabulary are -infinity
-                        const bool tail = n0 + 32 > p.N;
-                        if (p.has_bz) {
-                            if (!tail) {
-#pragma unroll
-                                for (int j = 0; j < 32; j += 4) {
-                                    const float4 b4 = __ldg(reinterpret_cast<const float4 *>(p.bz + n0 + j));
-                                    v[j] = fmaf(v[j], p.alpha, b4.x);
-                                    v[j + 1] = fmaf(v[j + 1], p.alpha, b4.y);
-                                    v[j + 2] = fmaf(v[j + 2], p.alpha, b4.z);
-                                    v[j + 3] = fmaf(v[j + 3], p.alpha, b4.w);
-                                }
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 32; ++j)
-                                    v[j] = n0 + j < p.N ? fmaf(v[j], p.alpha, __ldg(p.bz + n0 + j)) : -INFINITY;
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                v[j] = !tail || n0 + j < p.N ? v[j] * p.alpha : -INFINITY;
-                        }
-                        const int col0 = p.v0 + n0;
-                        if (MODE == MODE_LSE) {
-                            float cm = m;
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) cm = fmaxf(cm, v[j]);
-                            const float ref = cm == -INFINITY ? 0.f : cm;
-                            float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-                            while (cur.c0 < col0 + 32) {
-                                if (cur.c0 >= col0) {
-                                    float y = 0.f;
-#pragma unroll
-                                    for (int j = 0; j < 32; ++j) y = cur.c0 == col0 + j ? v[j] : y;
-                                    p.ysel[(long)row * p.r.K + cur.pos] = y;
-                                }
-                                cur.next();
-                            }
-                            __syncwarp();
-#pragma unroll
-                            for (int j = 0; j < 32; j += 4) {
-                                s0 += ex2(v[j] - ref);
-                                s1 += ex2(v[j + 1] - ref);
-                                s2 += ex2(v[j + 2] - ref);
-                                s3 += ex2(v[j + 3] - ref);
-                            }
-                            l = l * ex2(m - ref) + ((s0 + s1) + (s2 + s3));
-                            m = cm;
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) v[j] = coef * ex2(v[j] - l2);
-                            while (cur.c0 < col0 + 32) {
-                                if (cur.c0 >= col0) {
-                                    const float g = coef * cur.p0;
-#pragma unroll
-                                    for (int j = 0; j < 32; ++j)
-                                        if (cur.c0 == col0 + j) v[j] -= g;
-                                }
-                                cur.next();
-                            }
-                            __syncwarp();
-                            if (coef == 0.f) {   // whatever the row holds
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) v[j] = 0.f;
-                            }
-                            if (!kParts) {
-                                if (sub == 0) stage_wait();
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    uint4 pk;
-                                    pk.x = pack2(v[8 * j + 0], v[8 * j + 1]);
-                                    pk.y = pack2(v[8 * j + 2], v[8 * j + 3]);
-                                    pk.z = pack2(v[8 * j + 4], v[8 * j + 5]);
-                                    pk.w = pack2(v[8 * j + 6], v[8 * j + 7]);
-                                    *reinterpret_cast<uint4 *>(stg + lane * 128 + (((4 * sub + j) ^ (lane & 7)) << 4)) = pk;
-                                }
-                                // the second half of the chunk may lie past the last column
-                                if (sub == 1 || n0 + 32 >= p.N) {
-                                    fence_proxy_async_smem();
-                                    __syncwarp();
-                                    if (lane == 0 && row0 < p.M) {
-                                        tma_store_3d(&mo, stg_a, n0 - 32 * sub, row0, 0);
-                                        bulk_commit();
-                                    }
-                                }
-                            } else {
-                                // three parts, each 32 columns wide in its own half of the row
-                                float rest[32];
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) rest[j] = v[j];
-#pragma unroll
-                                for (int part = 0; part < 3; ++part) {
-                                    stage_wait();
-#pragma unroll
-                                    for (int j = 0; j < 4; ++j) {
-                                        uint32_t w4[4];
-#pragma unroll
-                                        for (int x = 0; x < 4; ++x) {
-                                            const float a = rest[8 * j + 2 * x], b = rest[8 * j + 2 * x + 1];
-                                            const float ta = top_part(a), tb = top_part(b);
-                                            w4[x] = pack2(ta, tb);
-                                            rest[8 * j + 2 * x] = a - ta;
-                                            rest[8 * j + 2 * x + 1] = b - tb;
-                                        }
-                                        // 64-byte rows, their swizzle: chunk c of row r at c ^ (r / 2 % 4)
-                                        *reinterpret_cast<uint4 *>(stg + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
-                                            make_uint4(w4[0], w4[1], w4[2], w4[3]);
-                                    }
-                                    fence_proxy_async_smem();
-                                    __syncwarp();
-                                    if (lane == 0 && row0 < p.M) {
-                                        tma_store_3d(&mo, stg_a, n0, row0, part);
-                                        bulk_commit();
-                                    }
-                                }
-                            }
-                            if (p.dbpart) {
-                                // sums over the warp's 32 rows: halving exchanges leave column j in lane j
-#pragma unroll
-                                for (int o = 16; o; o >>= 1) {
-                                    const bool up = lane & o;
-#pragma unroll
-                                    for (int j = 0; j < o; ++j) {
-                                        const float send = up ? v[j] : v[j + o];
-                                        const float keep = up ? v[j + o] : v[j];
-                                        v[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-                                    }
-                                }
-                                if (row0 < p.M && n0 + lane < p.N)
-                                    p.dbpart[(long)(row0 >> 5) * p.dbpitch + n0 + lane] = v[0];
-                            }
-                        }
-                    }
+                if (!wait(S::AFULL + buf, (lt >> 1) & 1)) {
+                    ok = false;
+                    break;
                 }
-                if (!kParts) {
-                    // this warp's part of the accumulator is in registers
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) l_arrive_leader<CG>(bar(S::AEMPTY + buf));
-                    ++lt;
+                ++lt;
+                tc_fence_after();
+                if (half >= nch) {
+                    release(buf);
+                    continue;
+                }
+                // each load is in flight while the columns before it are worked on
+                const uint32_t tacc = tq + (uint32_t)(buf * 256);
+                l_tmem_issue(tacc + 64u * half, v0);
+                l_tmem_wait(v0);
+                for (int c = half; c < nch; c += 2) {
+                    const int n0 = nt * p.bn + 64 * c;
+                    l_tmem_issue(tacc + 64u * c + 32u, v1);
+                    process(v0, n0, 0);
+                    l_tmem_wait(v1);
+                    if (c + 2 < nch)
+                        l_tmem_issue(tacc + 64u * (c + 2), v0);
+                    else
+                        release(buf);
+                    process(v1, n0 + 32, 1);
+                    if (c + 2 < nch) l_tmem_wait(v0);
                 }
             }
             if (MODE == MODE_LSE && ok && live)
-                p.part[(long)(kSlotsPerStrip * t.strip + half) * p.M + row] = make_float2(m, l);
+                p.part[(long)(kSlotsPerStrip * t.strip + half) * p.M + row] = make_float2(m * mscale, l);
         }
         if (lane == 0) bulk_wait_all();
         __syncwarp();

@@ -367,7 +367,7 @@ LossPlan loss_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool back
     q.col = take(n * K * 4);
     q.p = take(n * K * 4);
     q.ent = take(n * 4);
-    q.bz = take((size_t)vocab * 4);
+    q.bz = take((size_t)vocab * 4 + 256);   // read in fours past the last column
     q.h = take(q.copy_h ? n * q.dp * q.parts * 2 : 0);
     q.w = take(q.copy_w ? (size_t)q.piece * q.dp * q.parts * 2 : 0);
     q.coef = q.l2 = q.dz = q.dh_acc = q.dw_acc = q.dbpart = q.ysel = q.part = 0;
