@@ -51,32 +51,40 @@ constexpr int LNT = 384;
 constexpr int LEPI = 8;                        // epilogue warps
 constexpr uint64_t LWAIT_NS = 2000000000ull;   // 2 s per wait, then give up
 
-// kParts: fp32 operands in three bf16 parts (128-wide tiles, one stage per
-// part); else bf16 operands (256-wide tiles).
-template <int CG, bool kParts>
-struct LSmem {
-    static constexpr int BN = kParts ? 128 : 256;           // widest tile
-    static constexpr int ST = kParts ? (CG == 2 ? 8 : 6) : (CG == 2 ? 6 : 4);
-    static constexpr uint32_t ASZ = 128 * 128;              // 128 rows of 64 elements
-    static constexpr uint32_t BSZ = BN / CG * 128;
-    static constexpr uint32_t A = 0, B = A + ST * ASZ, OST = B + ST * BSZ, BARS = OST + LEPI * 4096;
-    static constexpr int FULL = 0, EMPTY = ST, AFULL = 2 * ST, AEMPTY = 2 * ST + 2, DONE = 2 * ST + 4,
-                         NBAR = 2 * ST + 5;
-    static constexpr uint32_t MISC = BARS + NBAR * 8 + 8;
-    static constexpr uint32_t TOTAL = MISC + 16 + 1024;
-};
-static_assert(LSmem<1, false>::TOTAL <= 232448 && LSmem<2, false>::TOTAL <= 232448 &&
-                  LSmem<1, true>::TOTAL <= 232448 && LSmem<2, true>::TOTAL <= 232448,
-              "shared memory");
-
 enum { MODE_LSE = 0, MODE_DZ = 1, MODE_CT = 2 };
 
+// kParts: fp32 operands in three bf16 parts (128-wide tiles, one stage per
+// part); else bf16 operands (256-wide tiles).  dz stores a whole tile from
+// every accumulation, so its staging buffers are two per epilogue warp.
+template <int CG, int MODE, bool kParts>
+struct LSmem {
+    static constexpr int BN = kParts ? 128 : 256;           // widest tile
+    static constexpr int STG = MODE == MODE_LSE ? 0 : MODE == MODE_DZ ? 2 : 1;
+    static constexpr uint32_t ASZ = 128 * 128;              // 128 rows of 64 elements
+    static constexpr uint32_t BSZ = BN / CG * 128;
+    static constexpr int ST = (int)((224u * 1024u - LEPI * 4096u * STG) / (ASZ + BSZ));
+    static constexpr uint32_t A = 0, B = A + ST * ASZ, OST = B + ST * BSZ, BARS = OST + LEPI * 4096 * STG;
+    static constexpr int FULL = 0, EMPTY = ST, AFULL = 2 * ST, AEMPTY = 2 * ST + 2, DONE = 2 * ST + 4,
+                         NBAR = 2 * ST + 5;
+    static constexpr uint32_t MISC = BARS + (NBAR + (NBAR & 1)) * 8;
+    static constexpr uint32_t TOTAL = MISC + 16 + 1024;
+    static_assert(TOTAL <= 232448 && ST >= 3, "shared memory");
+};
+
+// one output of a contraction launch
+struct LJob {
+    int M, N, bn, tiles_m, tiles_n, ksteps, splits, items;
+    int a_mn;                 // A stored with the output row innermost
+    int f32, add;
+};
+struct LMaps {
+    CUtensorMap a[2], b[2], o[2];
+};
+
 struct LParams {
-    int M, N;                 // output extent
-    int bn, tiles_m, tiles_n, strip, strips, items;
-    int ksteps, splits;
-    int a_mn, b_mn;           // operands stored with the output index innermost
+    int items;
     // vocabulary passes
+    int M, N, bn, tiles_m, tiles_n, strip, ksteps;
     const float *bz;          // [columns], biases in base-2 units; -infinity takes a column out
     int has_bz, v0;
     float alpha;
@@ -85,7 +93,7 @@ struct LParams {
     float2 *part;
     long dbpitch;
     // contraction
-    int f32, add;
+    LJob job[2];
 };
 
 // ------------------------------------------------------------ cta_group forms
@@ -278,21 +286,32 @@ __device__ __forceinline__ void l_tmem_wait(float (&v)[32])
 // ------------------------------------------------------------------- items
 struct LItem {
     int m0, nt0, nt1, ks0, ks1, split, strip;
+    int job, M, N, bn, a_mn, b_mn, f32, add;
 };
 template <int CG, int MODE>
 __device__ __forceinline__ LItem l_item(const LParams &p, int item)
 {
     LItem t;
     if (MODE == MODE_CT) {
-        const int n = item % p.tiles_n, x = item / p.tiles_n;
-        t.m0 = (x % p.tiles_m) * 128 * CG;
-        t.split = x / p.tiles_m;
+        t.job = item >= p.job[0].items;
+        const LJob &j = t.job ? p.job[1] : p.job[0];
+        if (t.job) item -= p.job[0].items;
+        const int n = item % j.tiles_n, x = item / j.tiles_n;
+        t.m0 = (x % j.tiles_m) * 128 * CG;
+        t.split = x / j.tiles_m;
         t.nt0 = n;
         t.nt1 = n + 1;
-        t.ks0 = (int)((long)t.split * p.ksteps / p.splits);
-        t.ks1 = (int)((long)(t.split + 1) * p.ksteps / p.splits);
+        t.ks0 = (int)((long)t.split * j.ksteps / j.splits);
+        t.ks1 = (int)((long)(t.split + 1) * j.ksteps / j.splits);
         if (t.ks0 == t.ks1) t.nt1 = t.nt0;   // nothing to add
         t.strip = 0;
+        t.M = j.M;
+        t.N = j.N;
+        t.bn = j.bn;
+        t.a_mn = j.a_mn;
+        t.b_mn = 1;
+        t.f32 = j.f32;
+        t.add = j.add;
     } else {
         // row blocks fastest: neighbours read the same vocabulary tiles at the same time
         t.m0 = (item % p.tiles_m) * 128 * CG;
@@ -301,7 +320,10 @@ __device__ __forceinline__ LItem l_item(const LParams &p, int item)
         t.nt1 = t.nt0 + p.strip < p.tiles_n ? t.nt0 + p.strip : p.tiles_n;
         t.ks0 = 0;
         t.ks1 = p.ksteps;
-        t.split = 0;
+        t.split = t.job = t.a_mn = t.b_mn = t.f32 = t.add = 0;
+        t.M = p.M;
+        t.N = p.N;
+        t.bn = p.bn;
     }
     return t;
 }
@@ -344,10 +366,9 @@ struct Cursor {
 
 template <int CG, int MODE, bool kParts>
 __global__ void __launch_bounds__(LNT, 1)
-loss_product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
-                    const __grid_constant__ CUtensorMap mo, const LParams p)
+loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ LParams p)
 {
-    using S = LSmem<CG, kParts>;
+    using S = LSmem<CG, MODE, kParts>;
     constexpr int ST = S::ST;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(
@@ -387,9 +408,11 @@ loss_product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constan
         }
         mbar_init(bar(S::DONE), 1);
         fence_mbar_init();
-        prefetch_tmap(&ma);
-        prefetch_tmap(&mb);
-        if (MODE != MODE_LSE) prefetch_tmap(&mo);
+        for (int j = 0; j < (MODE == MODE_CT && p.job[1].items ? 2 : 1); ++j) {
+            prefetch_tmap(&maps.a[j]);
+            prefetch_tmap(&maps.b[j]);
+            if (MODE != MODE_LSE) prefetch_tmap(&maps.o[j]);
+        }
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -398,20 +421,21 @@ loss_product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constan
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     const int G = (int)gridDim.x / CG, c0 = (int)blockIdx.x / CG;
-    const int bcols = p.bn / CG;                                  // this CTA's columns of B
 
     if (warp == 0) {
         // =================================================================== TMA producer
         if (lane == 0) {
-            const int nb = (bcols + 63) / 64;                     // MN-major B: blocks of 64 columns
-            const uint32_t bytes = (S::ASZ + (p.b_mn ? (uint32_t)nb * 8192u : (uint32_t)bcols * 128u)) * CG;
             int it = 0;
             bool ok = true;
             for (int item = c0; ok && item < p.items; item += G) {
                 const LItem t = l_item<CG, MODE>(p, item);
+                const CUtensorMap *ma = &maps.a[t.job], *mb = &maps.b[t.job];
+                const int bcols = t.bn / CG;                          // this CTA's columns of B
+                const int nb = (bcols + 63) / 64;                     // MN-major B: blocks of 64 columns
+                const uint32_t bytes = (S::ASZ + (t.b_mn ? (uint32_t)nb * 8192u : (uint32_t)bcols * 128u)) * CG;
                 const int m0 = t.m0 + rank * 128;
                 for (int nt = t.nt0; ok && nt < t.nt1; ++nt) {
-                    const int n0 = nt * p.bn + rank * bcols;
+                    const int n0 = nt * t.bn + rank * bcols;
                     for (int ks = t.ks0; ok && ks < t.ks1; ++ks) {
                         for (int part = 0; part < (kParts ? 3 : 1); ++part, ++it) {
                             const int s = it % ST;
@@ -422,17 +446,17 @@ loss_product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constan
                             const uint32_t da = sbase + S::A + s * S::ASZ, db = sbase + S::B + s * S::BSZ;
                             const uint32_t full = l_leader<CG>(bar(S::FULL + s));
                             if (rank == 0) mbar_arrive_expect_tx(bar(S::FULL + s), bytes);
-                            if (p.a_mn) {
-                                l_load<CG>(da, &ma, full, m0, ks * LK, part);
-                                l_load<CG>(da + 8192u, &ma, full, m0 + 64, ks * LK, part);
+                            if (t.a_mn) {
+                                l_load<CG>(da, ma, full, m0, ks * LK, part);
+                                l_load<CG>(da + 8192u, ma, full, m0 + 64, ks * LK, part);
                             } else {
-                                l_load<CG>(da, &ma, full, ks * LK, m0, part);
+                                l_load<CG>(da, ma, full, ks * LK, m0, part);
                             }
-                            if (p.b_mn) {
+                            if (t.b_mn) {
                                 for (int b = 0; b < nb; ++b)
-                                    l_load<CG>(db + 8192u * b, &mb, full, n0 + 64 * b, ks * LK, part);
+                                    l_load<CG>(db + 8192u * b, mb, full, n0 + 64 * b, ks * LK, part);
                             } else {
-                                l_load<CG>(db, &mb, full, ks * LK, n0, part);
+                                l_load<CG>(db, mb, full, ks * LK, n0, part);
                             }
                         }
                     }
@@ -453,16 +477,16 @@ loss_product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constan
     } else if (warp == 1) {
         // =================================================================== MMA issuer
         if (lane == 0 && rank == 0) {
-            const uint32_t idesc = idesc_bf16(128 * CG, p.bn, p.a_mn, p.b_mn);
-            // K-major: K steps of 32 bytes along the swizzled row; MN-major:
-            // K steps of 16 rows (2 KB), blocks of 64 outputs 8 KB apart
-            const uint64_t da0 = smem_desc_sw128(sbase + S::A, p.a_mn ? 8192 : 16, 1024);
-            const uint64_t db0 = smem_desc_sw128(sbase + S::B, p.b_mn ? 8192 : 16, 1024);
-            const uint64_t sa = p.a_mn ? 128 : 2, sb = p.b_mn ? 128 : 2;
             int it = 0, lt = 0;
             bool ok = true;
             for (int item = c0; ok && item < p.items; item += G) {
                 const LItem t = l_item<CG, MODE>(p, item);
+                const uint32_t idesc = idesc_bf16(128 * CG, t.bn, t.a_mn, t.b_mn);
+                // K-major: K steps of 32 bytes along the swizzled row; MN-major:
+                // K steps of 16 rows (2 KB), blocks of 64 outputs 8 KB apart
+                const uint64_t da0 = smem_desc_sw128(sbase + S::A, t.a_mn ? 8192 : 16, 1024);
+                const uint64_t db0 = smem_desc_sw128(sbase + S::B, t.b_mn ? 8192 : 16, 1024);
+                const uint64_t sa = t.a_mn ? 128 : 2, sb = t.b_mn ? 128 : 2;
                 for (int nt = t.nt0; ok && nt < t.nt1; ++nt) {
                     for (int ks = t.ks0; ok && ks < t.ks1; ++lt) {
                         // one accumulation: the whole K range, or one step of three parts
@@ -510,14 +534,22 @@ loss_product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constan
     } else if (warp >= 4) {
         // =================================================================== epilogue
         const int q = warp & 3, half = (warp - 4) >> 2;
+        // staging: STG buffers of 32 rows x 128 bytes per warp, used in turn
         unsigned char *stg = smem + S::OST + (uint32_t)(warp - 4) * 4096u;
-        const uint32_t stg_a = sbase + S::OST + (uint32_t)(warp - 4) * 4096u;
-        const int nch = p.bn / 64;                                // 64-column chunks, alternately per half
+        uint32_t stg_a = sbase + S::OST + (uint32_t)(warp - 4) * 4096u;
+        int nst = 0;
         int lt = 0;
         bool ok = true;
-        // the staging buffer (32 rows x 128 bytes) is free once the previous store has read it
+        // the next staging buffer, once the store that last used it has read it
         auto stage_wait = [&]() {
-            if (lane == 0) bulk_wait_read();
+            if (S::STG == 2) {
+                const uint32_t flip = (nst++ & 1) ? LEPI * 4096u : 0u;
+                stg = smem + S::OST + (uint32_t)(warp - 4) * 4096u + flip;
+                stg_a = sbase + S::OST + (uint32_t)(warp - 4) * 4096u + flip;
+                if (lane == 0) bulk_wait_read_1();
+            } else if (lane == 0) {
+                bulk_wait_read();
+            }
             __syncwarp();
         };
         auto stage_bf16 = [&](const float (&v)[32], int at) {      // columns 32 at .. 32 at + 31 of the row
@@ -531,14 +563,14 @@ loss_product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constan
                 *reinterpret_cast<uint4 *>(stg + lane * 128 + (((4 * at + j) ^ (lane & 7)) << 4)) = pk;
             }
         };
-        auto store = [&](int x, int y, int z, bool add) {
+        auto store = [&](int job, int x, int y, int z, bool add) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
                 if (add)
-                    l_reduce_3d(&mo, stg_a, x, y, z);
+                    l_reduce_3d(&maps.o[job], stg_a, x, y, z);
                 else
-                    tma_store_3d(&mo, stg_a, x, y, z);
+                    tma_store_3d(&maps.o[job], stg_a, x, y, z);
                 bulk_commit();
             }
         };
@@ -554,7 +586,8 @@ loss_product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constan
         for (int item = c0; ok && item < p.items; item += G) {
             const LItem t = l_item<CG, MODE>(p, item);
             const int row0 = t.m0 + rank * 128 + 32 * q, row = row0 + lane;
-            const bool live = row < p.M;
+            const bool live = row < t.M;
+            const int nch = t.bn / 64;                                // 64-column chunks, alternately per half
             float m = -INFINITY, l = 0.f, coef = 0.f, l2 = 0.f;
             Cursor cur;
             bool dead = false;
@@ -562,7 +595,7 @@ loss_product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constan
                 cur.K = live ? p.r.K : 0;
                 cur.col = p.r.col + (long)(live ? row : 0) * p.r.K;
                 cur.p = MODE == MODE_DZ ? p.r.p + (long)(live ? row : 0) * p.r.K : nullptr;
-                cur.seek(p.v0 + t.nt0 * p.bn);
+                cur.seek(p.v0 + t.nt0 * t.bn);
                 if (MODE == MODE_DZ) {
                     if (live) {
                         coef = p.r.coef[row];
@@ -574,19 +607,19 @@ loss_product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constan
             // 32 columns from n0 on (the second half of their 64-column chunk with sub = 1)
             auto process = [&](float (&v)[32], int n0, int sub) {
                 if (MODE == MODE_CT) {
-                    if (row0 >= p.M || n0 - 32 * sub >= p.N) return;
-                    if (p.f32) {
-                        if (n0 >= p.N) return;
+                    if (row0 >= t.M || n0 - 32 * sub >= t.N) return;
+                    if (t.f32) {
+                        if (n0 >= t.N) return;
                         stage_wait();
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
                             *reinterpret_cast<float4 *>(stg + lane * 128 + ((j ^ (lane & 7)) << 4)) =
                                 make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                        store(n0, row0, t.split, p.add);
+                        store(t.job, n0, row0, t.split, t.add);
                     } else {
                         if (sub == 0) stage_wait();
                         stage_bf16(v, sub);
-                        if (sub == 1) store(n0 - 32, row0, 0, false);
+                        if (sub == 1) store(t.job, n0 - 32, row0, 0, false);
                     }
                     return;
                 }
@@ -663,7 +696,7 @@ loss_product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constan
                         if (sub == 0) stage_wait();
                         stage_bf16(v, sub);
                         // the second half of the chunk may lie past the last column
-                        if ((sub == 1 || n0 + 32 >= p.N) && row0 < p.M) store(n0 - 32 * sub, row0, 0, false);
+                        if ((sub == 1 || n0 + 32 >= p.N) && row0 < p.M) store(0, n0 - 32 * sub, row0, 0, false);
                     } else {
                         float rest[32];
 #pragma unroll
@@ -686,7 +719,7 @@ loss_product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constan
                                 *reinterpret_cast<uint4 *>(stg + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
                                     make_uint4(w4[0], w4[1], w4[2], w4[3]);
                             }
-                            if (row0 < p.M) store(n0, row0, part, false);
+                            if (row0 < p.M) store(0, n0, row0, part, false);
                         }
                     }
                     if (p.dbpart) {
@@ -733,8 +766,8 @@ loss_product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constan
                     }
                     if (!ok) break;
                     if (half < nch) {
-                        process(v0, nt * p.bn + 64 * half, 0);
-                        process(v1, nt * p.bn + 64 * half + 32, 1);
+                        process(v0, nt * t.bn + 64 * half, 0);
+                        process(v1, nt * t.bn + 64 * half + 32, 1);
                     }
                     continue;
                 }
@@ -754,7 +787,7 @@ loss_product_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constan
                 l_tmem_issue(tacc + 64u * half, v0);
                 l_tmem_wait(v0);
                 for (int c = half; c < nch; c += 2) {
-                    const int n0 = nt * p.bn + 64 * c;
+                    const int n0 = nt * t.bn + 64 * c;
                     l_tmem_issue(tacc + 64u * c + 32u, v1);
                     process(v0, n0, 0);
                     l_tmem_wait(v1);
@@ -816,8 +849,7 @@ cudaError_t l_in_map(CUtensorMap *m, const LossMatrix &x, int box_y)
 }
 
 template <int CG, int MODE, bool kParts>
-cudaError_t l_launch(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo, const LParams &p,
-                     cudaStream_t s)
+cudaError_t l_launch(const LMaps &maps, const LParams &p, cudaStream_t s)
 {
     auto kern = loss_product_kernel<CG, MODE, kParts>;
     static std::atomic<int> most[64];      // tiles that run at once, per device
@@ -828,7 +860,7 @@ cudaError_t l_launch(const CUtensorMap &ma, const CUtensorMap &mb, const CUtenso
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
     cfg.blockDim = dim3(LNT);
-    cfg.dynamicSmemBytes = LSmem<CG, kParts>::TOTAL;
+    cfg.dynamicSmemBytes = LSmem<CG, MODE, kParts>::TOTAL;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -838,7 +870,7 @@ cudaError_t l_launch(const CUtensorMap &ma, const CUtensorMap &mb, const CUtenso
     cfg.numAttrs = 1;
     int n = most[dev].load(std::memory_order_relaxed);
     if (n == 0) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LSmem<CG, kParts>::TOTAL);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LSmem<CG, MODE, kParts>::TOTAL);
         if (e != cudaSuccess) return e;
         n = device_sm_count() / CG;
         if (CG == 2) {
@@ -852,20 +884,21 @@ cudaError_t l_launch(const CUtensorMap &ma, const CUtensorMap &mb, const CUtenso
         most[dev].store(n, std::memory_order_relaxed);
     }
     cfg.gridDim = dim3((unsigned)(CG * (p.items < n ? p.items : n)));
-    return cudaLaunchKernelEx(&cfg, kern, ma, mb, mo, p);
+    return cudaLaunchKernelEx(&cfg, kern, maps, p);
 }
 
 template <int MODE>
-cudaError_t l_launch_cg(int cg, int parts, const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mo, const LParams &p,
-                        cudaStream_t s)
+cudaError_t l_launch_cg(int cg, int parts, const LMaps &maps, const LParams &p, cudaStream_t s)
 {
-    if (parts == 3) return cg == 2 ? l_launch<2, MODE, true>(ma, mb, mo, p, s) : l_launch<1, MODE, true>(ma, mb, mo, p, s);
-    return cg == 2 ? l_launch<2, MODE, false>(ma, mb, mo, p, s) : l_launch<1, MODE, false>(ma, mb, mo, p, s);
+    if (parts == 3) return cg == 2 ? l_launch<2, MODE, true>(maps, p, s) : l_launch<1, MODE, true>(maps, p, s);
+    return cg == 2 ? l_launch<2, MODE, false>(maps, p, s) : l_launch<1, MODE, false>(maps, p, s);
 }
 
+long cdiv(long a, long b) { return (a + b - 1) / b; }
+
 // the fields the two vocabulary passes share
-cudaError_t vocab_params(LParams &p, CUtensorMap &ma, CUtensorMap &mb, const LossMatrix &h, const LossMatrix &w,
-                         const float *bz, int v0, float alpha, const LossRows &r, const LossTiling &t)
+cudaError_t vocab_params(LParams &p, LMaps &maps, const LossMatrix &h, const LossMatrix &w, const float *bz, int v0,
+                         float alpha, const LossRows &r, const LossTiling &t)
 {
     memset(&p, 0, sizeof(p));
     p.M = h.rows;
@@ -874,31 +907,61 @@ cudaError_t vocab_params(LParams &p, CUtensorMap &ma, CUtensorMap &mb, const Los
     p.tiles_m = t.tiles_m;
     p.tiles_n = t.tiles_n;
     p.strip = t.strip;
-    p.strips = vocab_strips(t);
-    const long items = (long)t.tiles_m * p.strips;
+    const long items = (long)t.tiles_m * vocab_strips(t);
     if (items > INT32_MAX) return cudaErrorNotSupported;
     p.items = (int)items;
-    p.ksteps = (h.cols + LK - 1) / LK;
-    p.splits = 1;
+    p.ksteps = (int)cdiv(h.cols, LK);
     p.bz = bz;
     p.has_bz = bz != nullptr;
     p.v0 = v0;
     p.alpha = alpha;
     p.r = r;
-    cudaError_t e = l_in_map(&ma, h, 128);
-    if (e == cudaSuccess) e = l_in_map(&mb, w, t.bn / t.cg);
+    cudaError_t e = l_in_map(&maps.a[0], h, 128);
+    if (e == cudaSuccess) e = l_in_map(&maps.b[0], w, t.bn / t.cg);
     return e;
 }
 
-long cdiv(long a, long b) { return (a + b - 1) / b; }
+// What the division rules below count with, measured on GB300 at 2 GHz: a
+// 64-deep step of a 256-column tile (per SM 128 rows of it), what an item
+// costs beside its steps, a vocabulary tile's epilogue, a launch with the
+// drain before it, and HBM bytes per microsecond.
+constexpr double kStepUs = 0.26, kItemUs = 1.0, kEpilogueUs = 2.4, kLaunchUs = 5.0, kHbmPerUs = 6.0e6;
+constexpr double kL2Bytes = 80e6;      // dz pieces up to this are read back from L2
+
+double step_us(int bn, int parts) { return kStepUs * bn / 256 * (parts == 3 ? 6 : 1); }
+
+// the longest of the tile slots when n0 items of a and then n1 items of b go round them in turn
+double makespan(long slots, long n0, double a, long n1, double b)
+{
+    const long r = n0 % slots;
+    double most = 0;
+    const long at[4] = {0, r, (r + slots - 1) % slots, (r + n1 % slots + slots - 1) % slots};
+    for (long j : at) {
+        const long c0 = cdiv(n0 > j ? n0 - j : 0, slots), off = (j - r + slots) % slots;
+        const long c1 = cdiv(n1 > off ? n1 - off : 0, slots);
+        const double t = c0 * a + c1 * b;
+        most = t > most ? t : most;
+    }
+    return most;
+}
+
+void job_tiles(LossTiling &t, int m, int n, int cg, int parts)
+{
+    t.cg = cg;
+    t.tiles_m = (int)cdiv(m, 128 * cg);
+    t.tiles_n = (int)cdiv(n, parts == 3 ? 128 : 256);
+    t.bn = (int)(cdiv(cdiv(n, t.tiles_n), 64) * 64);
+    t.strip = 1;
+    t.splits = 1;
+}
 
 }  // namespace
 
-LossTiling vocab_tiling(int rows, int cols, int d, int pieces)
+LossTiling vocab_tiling(int rows, int cols, int d, int parts, double *us)
 {
     LossTiling t;
     t.cg = rows > 128 ? 2 : 1;
-    const int widest = pieces == 3 ? 128 : 256;
+    const int widest = parts == 3 ? 128 : 256;
     t.bn = cols > widest - 64 ? widest : (cols + 63) / 64 * 64;
     t.tiles_m = (int)cdiv(rows, 128 * t.cg);
     t.tiles_n = (int)cdiv(cols, t.bn);
@@ -914,47 +977,79 @@ LossTiling vocab_tiling(int rows, int cols, int d, int pieces)
             t.strip = s;
         }
     }
-    (void)d;
+    if (us) {
+        const double main = cdiv(d, LK) * step_us(t.bn, parts), epi = kEpilogueUs * t.bn / 256;
+        *us = best * (main > epi ? main : epi) + kLaunchUs;
+    }
     return t;
 }
 
-LossTiling contract_tiling(int m, int n, int k, int pieces, bool always_slots)
+double gradient_tiling(int rows, int d, int cols, int whole, int parts, bool dh_slots, LossTiling *dh, LossTiling *dw)
 {
-    LossTiling t;
-    t.cg = m > 128 ? 2 : 1;
-    t.tiles_m = (int)cdiv(m, 128 * t.cg);
-    t.tiles_n = (int)cdiv(n, pieces == 3 ? 128 : 256);
-    t.bn = (int)(cdiv(cdiv(n, t.tiles_n), 64) * 64);
-    t.strip = 1;
-    const long slots = device_sm_count() / t.cg;
-    const long ksteps = cdiv(k, LK) * (pieces == 3 ? 6 : 1);
-    const double step_us = 0.27 * t.bn / 256;
-    // splits of the long axis fill the SMs; each costs a pass over its slot
-    // (0.27 us per 64-deep step of a 256-wide tile, 5 TB/s for the slots)
+    const int cg = rows > 128 ? 2 : 1;
+    job_tiles(*dh, rows, d, cg, parts);
+    job_tiles(*dw, cols, d, cg, parts);
+    const long slots = device_sm_count() / cg;
+    const long n0 = (long)dh->tiles_m * dh->tiles_n, n1 = (long)dw->tiles_m * dw->tiles_n;
+    const double s0 = step_us(dh->bn, parts), s1 = step_us(dw->bn, parts);
+    const long k0 = cdiv(cols, LK), k1 = cdiv(rows, LK), kw = cdiv(whole, LK);
     double best = 1e300;
-    t.splits = 1;
-    for (int s = 1; s <= 64 && s <= cdiv(k, LK); ++s) {
-        const double rounds = (double)cdiv((long)t.tiles_m * t.tiles_n * s, slots);
-        const double passes = s > 1 || always_slots ? 2.0 * s * m * n * 4 / 5e6 : 0.0;
-        const double cost = rounds * ((double)cdiv(ksteps, s) + 6) * step_us + passes + (s > 1 ? 3.0 : 0.0);
-        if (cost < best) {
-            best = cost;
-            t.splits = s;
+    static const int cand[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32, 48, 64};
+    for (int a : cand) {
+        if (a > kw) break;
+        for (int b : cand) {
+            if (b > k1) break;
+            // a split costs a pass over its slot, written (added to) and read back
+            double us = makespan(slots, n0 * a, cdiv(k0, a) * s0 + kItemUs, n1 * b, cdiv(k1, b) * s1 + kItemUs);
+            const double pass = (a > 1 || dh_slots ? 2.0 * a * rows * d * 4 : 0.0) + (b > 1 ? 2.0 * b * cols * d * 4 : 0.0);
+            us += pass / kHbmPerUs + (b > 1 ? kLaunchUs : 0.0);
+            if (us < best) {
+                best = us;
+                dh->splits = a;
+                dw->splits = b;
+            }
         }
     }
-    return t;
+    return best + kLaunchUs;
+}
+
+int gradient_piece(int rows, int d, int vocab, int parts, int most)
+{
+    if (vocab <= kLossPieceUnit) return vocab;
+    int best_piece = 0;
+    double best = 1e300;
+    const long units = cdiv(vocab, kLossPieceUnit), least = cdiv(units, most / kLossPieceUnit);
+    for (long n = least; n <= units && n < least + 24; ++n) {
+        const long piece = cdiv(units, n) * kLossPieceUnit;
+        const int cols = (int)(piece < vocab ? piece : vocab), last = vocab % cols;
+        LossTiling a, b;
+        auto cost = [&](int c) {
+            double vus;
+            vocab_tiling(rows, c, d, parts, &vus);
+            const double dz = (double)rows * c * 2 * parts, hbm = dz > kL2Bytes ? dz / kHbmPerUs : 0.0;
+            const double g = gradient_tiling(rows, d, c, cols, parts, cols < vocab, &a, &b);
+            return (vus > hbm ? vus : hbm) + (g > 2 * hbm ? g : 2 * hbm);
+        };
+        const double us = vocab / cols * cost(cols) + (last ? cost(last) : 0.0);
+        if (us < best) {
+            best = us;
+            best_piece = cols;
+        }
+    }
+    return best_piece;
 }
 
 cudaError_t launch_loss_lse(const LossMatrix &h, const LossMatrix &w, const float *bz, int v0, float alpha,
                             const LossRows &r, float *ysel, float2 *part, const LossTiling &t, cudaStream_t s)
 {
     LParams p;
-    CUtensorMap ma, mb;
-    cudaError_t e = vocab_params(p, ma, mb, h, w, bz, v0, alpha, r, t);
+    LMaps maps;
+    memset(&maps, 0, sizeof(maps));
+    cudaError_t e = vocab_params(p, maps, h, w, bz, v0, alpha, r, t);
     if (e != cudaSuccess) return e;
     p.ysel = ysel;
     p.part = part;
-    return l_launch_cg<MODE_LSE>(t.cg, h.pieces, ma, mb, ma, p, s);
+    return l_launch_cg<MODE_LSE>(t.cg, h.pieces, maps, p, s);
 }
 
 cudaError_t launch_loss_dz(const LossMatrix &h, const LossMatrix &w, const float *bz, int v0, float alpha,
@@ -962,47 +1057,53 @@ cudaError_t launch_loss_dz(const LossMatrix &h, const LossMatrix &w, const float
                            cudaStream_t s)
 {
     LParams p;
-    CUtensorMap ma, mb, mo;
-    cudaError_t e = vocab_params(p, ma, mb, h, w, bz, v0, alpha, r, t);
+    LMaps maps;
+    memset(&maps, 0, sizeof(maps));
+    cudaError_t e = vocab_params(p, maps, h, w, bz, v0, alpha, r, t);
     if (e != cudaSuccess) return e;
     p.dbpart = dbpart;
     p.dbpitch = dz.pitch;
     const bool three = dz.pieces == 3;
-    e = l_map(&mo, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dz.base, dz.cols, dz.rows, dz.pieces, dz.pitch,
+    e = l_map(&maps.o[0], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dz.base, dz.cols, dz.rows, dz.pieces, dz.pitch,
               dz.piece_stride, three ? 32 : 64, 32, three ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
-    return l_launch_cg<MODE_DZ>(t.cg, h.pieces, ma, mb, mo, p, s);
+    return l_launch_cg<MODE_DZ>(t.cg, h.pieces, maps, p, s);
 }
 
-cudaError_t launch_loss_contract(const LossMatrix &a, bool a_t, const LossMatrix &b, int m, int n, int k,
-                                 const LossOutput &out, const LossTiling &t, cudaStream_t s)
+cudaError_t launch_loss_gradients(const LossContraction *jobs, int n, int parts, cudaStream_t s)
 {
     LParams p;
+    LMaps maps;
     memset(&p, 0, sizeof(p));
-    p.M = m;
-    p.N = n;
-    p.bn = t.bn;
-    p.tiles_m = t.tiles_m;
-    p.tiles_n = t.tiles_n;
-    p.strip = 1;
-    p.splits = t.splits;
-    const long items = (long)t.tiles_m * t.tiles_n * t.splits;
-    if (items > INT32_MAX) return cudaErrorNotSupported;
+    memset(&maps, 0, sizeof(maps));
+    long items = 0;
+    for (int x = 0; x < n; ++x) {
+        const LossContraction &c = jobs[x];
+        LJob &j = p.job[x];
+        j.M = c.m;
+        j.N = c.n;
+        j.bn = c.t.bn;
+        j.tiles_m = c.t.tiles_m;
+        j.tiles_n = c.t.tiles_n;
+        j.ksteps = (int)cdiv(c.k, LK);
+        j.splits = c.t.splits;
+        j.a_mn = c.a_t;
+        j.f32 = c.out.f32;
+        j.add = c.out.add;
+        const long mine = (long)j.tiles_m * j.tiles_n * j.splits;
+        items += mine;
+        if (items > INT32_MAX) return cudaErrorNotSupported;
+        j.items = (int)mine;
+        cudaError_t e = l_in_map(&maps.a[x], c.a, c.a_t ? 64 : 128);
+        if (e == cudaSuccess) e = l_in_map(&maps.b[x], c.b, 64);
+        if (e == cudaSuccess)
+            e = l_map(&maps.o[x], c.out.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                      c.out.f32 ? 4 : 2, c.out.base, c.n, c.m, j.splits, c.out.pitch, c.out.slot_stride,
+                      c.out.f32 ? 32 : 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
+        if (e != cudaSuccess) return e;
+    }
     p.items = (int)items;
-    p.ksteps = (k + LK - 1) / LK;
-    p.a_mn = a_t;
-    p.b_mn = 1;
-    p.f32 = out.f32;
-    p.add = out.add;
-    CUtensorMap ma, mb, mo;
-    cudaError_t e = l_in_map(&ma, a, a_t ? 64 : 128);
-    if (e == cudaSuccess) e = l_in_map(&mb, b, 64);
-    if (e == cudaSuccess)
-        e = l_map(&mo, out.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out.f32 ? 4 : 2,
-                  out.base, n, m, t.splits, out.pitch, out.slot_stride, out.f32 ? 32 : 64, 32,
-                  CU_TENSOR_MAP_SWIZZLE_128B);
-    if (e != cudaSuccess) return e;
-    return l_launch_cg<MODE_CT>(t.cg, a.pieces, ma, mb, mo, p, s);
+    return l_launch_cg<MODE_CT>(jobs[0].t.cg, parts, maps, p, s);
 }
 
 cudaError_t read_and_clear_loss_error(unsigned int *word, cudaStream_t s)

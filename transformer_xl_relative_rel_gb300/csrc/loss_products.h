@@ -28,21 +28,28 @@ struct LossMatrix {
     int rows, cols, pieces;
 };
 
-// How a launch divides its work (the split itself depends on sizes only).
+// How a launch divides its work (from sizes and the number of SMs alone).
 struct LossTiling {
-    int cg;             // CTAs per tile: 2 for outputs of more than 128 rows, else 1
+    int cg;             // CTAs per tile: 2 for more than 128 rows, else 1
     int bn;             // output columns per tile
     int tiles_m, tiles_n;
     int strip;          // vocabulary passes: tiles of one row block that a CTA (pair) does in a row
-    int splits;         // contractions: parts of the long axis, each into a slot of its own
+    int splits;         // gradients: parts of the long axis, each into a slot of its own
 };
 
-// Vocabulary pass over rows x cols logits.
-LossTiling vocab_tiling(int rows, int cols, int d, int pieces);
-// Contraction to m x n over k.
-LossTiling contract_tiling(int m, int n, int k, int pieces, bool always_slots);
+// Vocabulary pass over rows x cols logits; *us its estimated time.
+LossTiling vocab_tiling(int rows, int cols, int d, int parts, double *us = nullptr);
 inline int vocab_strips(const LossTiling &t) { return (t.tiles_n + t.strip - 1) / t.strip; }
 constexpr int kSlotsPerStrip = 2;      // the halves of a tile's columns are kept apart
+
+// The launch that makes dh += dz W and dW = dz^T h of one vocabulary piece of
+// `cols` columns (`whole`: the columns of the call's other pieces, whose dh
+// slots it adds to with dh_slots); returns its estimated time in us.
+double gradient_tiling(int rows, int d, int cols, int whole, int parts, bool dh_slots, LossTiling *dh, LossTiling *dw);
+// Columns of the backward's vocabulary pieces: at most `most`, a multiple of
+// kLossPieceUnit unless it is the whole vocabulary.
+constexpr int kLossPieceUnit = 256;
+int gradient_piece(int rows, int d, int vocab, int parts, int most);
 
 // part[2 * strip + half][row] = (maximum, sum of 2^(y - maximum)) over the
 // columns, y = alpha (h . w) + bz; ysel[row][k] = y at the listed columns
@@ -57,16 +64,22 @@ cudaError_t launch_loss_dz(const LossMatrix &h, const LossMatrix &w, const float
                            cudaStream_t s);
 
 // out[m][n] = sum_k a(m, k) b(k, n).  a is stored [m][k], or [k][m] with
-// a_t; b is stored [k][n].  out_f32 selects fp32 output; it then has
-// `splits` slots of slot_stride elements (the sum of which is the product),
-// added to what they hold with `add`.
+// a_t; b is stored [k][n].  f32 selects fp32 output; it then has `splits`
+// slots of slot_stride elements (the sum of which is the product), added to
+// what they hold with `add`.  One or two of them per launch, with one cg.
 struct LossOutput {
     void *base;
     long pitch, slot_stride;
     bool f32, add;
 };
-cudaError_t launch_loss_contract(const LossMatrix &a, bool a_t, const LossMatrix &b, int m, int n, int k,
-                                 const LossOutput &out, const LossTiling &t, cudaStream_t s);
+struct LossContraction {
+    LossMatrix a, b;
+    bool a_t;
+    int m, n, k;
+    LossOutput out;
+    LossTiling t;
+};
+cudaError_t launch_loss_gradients(const LossContraction *jobs, int n, int parts, cudaStream_t s);
 
 cudaError_t read_and_clear_loss_error(unsigned int *word, cudaStream_t s);
 

@@ -24,6 +24,9 @@
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+#include <string.h>
+
+#include <mutex>
 
 #include "internal.h"
 #include "loss_products.h"
@@ -326,9 +329,9 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb)
     return x < y + nb && y < x + na;
 }
 
-constexpr size_t kPieceBytes = (size_t)64 << 20;   // one piece of dz and of copied weights
+constexpr size_t kPieceBytes = (size_t)256 << 20;  // at most this for one piece of dz and of copied weights
+constexpr size_t kWeightBytes = (size_t)64 << 20;  // ... for the forward's copied weights
 constexpr int kMaxSize = 1 << 30;                  // rows and vocabulary
-constexpr int kPieceUnit = 256;                    // vocabulary pieces start at multiples of the widest tile
 
 long up(long a, long b) { return (a + b - 1) / b * b; }
 
@@ -344,7 +347,7 @@ struct LossPlan {
     size_t col, p, ent, coef, l2, bz, ysel, part, h, w, dz, dh_acc, dw_acc, dbpart, bytes;
 };
 
-LossPlan loss_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool backward, bool h_ok, bool w_ok)
+LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool backward, bool h_ok, bool w_ok)
 {
     LossPlan q;
     size_t at = 0;
@@ -359,11 +362,14 @@ LossPlan loss_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool back
     const bool tma = dtype == TXL_BF16 && d % 8 == 0;
     q.copy_h = backward || !tma || !h_ok;
     q.copy_w = !tma || !w_ok;
-    // what a vocabulary column of a piece takes
+    // what a vocabulary column of a piece takes; pieces start at multiples of the widest tile
     const size_t per = ((backward ? n : 0) + (q.copy_w ? (size_t)q.dp : 0)) * q.parts * 2;
-    size_t piece = per ? kPieceBytes / per / kPieceUnit * kPieceUnit : (size_t)vocab;
-    if (piece < (size_t)kPieceUnit) piece = kPieceUnit;
-    q.piece = piece < (size_t)vocab ? (int)piece : vocab;
+    size_t most = per ? (backward ? kPieceBytes : kWeightBytes) / per / kLossPieceUnit * kLossPieceUnit : (size_t)vocab;
+    if (most < (size_t)kLossPieceUnit) most = kLossPieceUnit;
+    if (backward)
+        q.piece = gradient_piece(rows, d, vocab, q.parts, most < (size_t)kMaxSize ? (int)most : kMaxSize);
+    else
+        q.piece = most < (size_t)vocab ? (int)most : vocab;
     q.col = take(n * K * 4);
     q.p = take(n * K * 4);
     q.ent = take(n * 4);
@@ -384,18 +390,49 @@ LossPlan loss_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool back
         q.l2 = take(n * 4);
         q.dz = take(n * up(q.piece, 64) * q.parts * 2);
         q.dh_slots = q.piece < vocab;
-        q.dh = contract_tiling(rows, d, q.piece, q.parts, q.dh_slots);
-        // the last, narrower piece may split further
+        // the last, narrower piece may split dW further
+        LossTiling dw, dh_last, dw_last;
         const int last = vocab % q.piece ? vocab % q.piece : q.piece;
-        const size_t dw_whole = (size_t)contract_tiling(q.piece, d, rows, q.parts, false).splits * q.piece;
-        const size_t dw_last = (size_t)contract_tiling(last, d, rows, q.parts, false).splits * last;
+        gradient_tiling(rows, d, q.piece, q.piece, q.parts, q.dh_slots, &q.dh, &dw);
+        gradient_tiling(rows, d, last, q.piece, q.parts, q.dh_slots, &dh_last, &dw_last);
+        const size_t dw_whole = (size_t)dw.splits * q.piece, dw_rest = (size_t)dw_last.splits * last;
         // whatever the output's alignment: the products go to the slots where TMA cannot write it
         q.dh_acc = take((size_t)q.dh.splits * n * q.dp * 4);
-        q.dw_acc = take((dw_whole > dw_last ? dw_whole : dw_last) * q.dp * 4);
+        q.dw_acc = take((dw_whole > dw_rest ? dw_whole : dw_rest) * q.dp * 4);
         q.dbpart = take((size_t)up(rows, 32) / 32 * up(q.piece, 64) * 4);
     }
     q.bytes = at ? at : 256;
     return q;
+}
+
+// The plans of the shapes used last (a plan's search takes up to a
+// millisecond of host time).
+struct PlanKey {
+    int rows, d, vocab, K, dtype, flags, sms;
+};
+std::mutex g_plan_mu;
+struct PlanEntry {
+    PlanKey key;
+    LossPlan plan;
+};
+PlanEntry g_plans[64];
+int g_plan_n = 0, g_plan_next = 0;
+
+LossPlan loss_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool backward, bool h_ok, bool w_ok)
+{
+    const PlanKey key = {rows, d, vocab, K, (int)dtype, backward * 4 + h_ok * 2 + w_ok, device_sm_count()};
+    {
+        std::lock_guard<std::mutex> lock(g_plan_mu);
+        for (int x = 0; x < g_plan_n; ++x)
+            if (!memcmp(&g_plans[x].key, &key, sizeof(key))) return g_plans[x].plan;
+    }
+    const LossPlan plan = make_plan(rows, d, vocab, K, dtype, backward, h_ok, w_ok);
+    std::lock_guard<std::mutex> lock(g_plan_mu);
+    g_plans[g_plan_next].key = key;
+    g_plans[g_plan_next].plan = plan;
+    g_plan_next = (g_plan_next + 1) % 64;
+    if (g_plan_n < 64) ++g_plan_n;
+    return plan;
 }
 
 // The bytes either direction may need whatever the buffers' alignment.
@@ -608,6 +645,28 @@ cudaError_t run_fwd(const LossArgs &a)
     return cudaGetLastError();
 }
 
+LossOutput direct_out(const LossArgs &a, void *p)
+{
+    LossOutput o;
+    o.base = p;
+    o.pitch = a.d;
+    o.slot_stride = 0;
+    o.f32 = a.dtype == TXL_F32;
+    o.add = false;
+    return o;
+}
+
+LossOutput slot_out(float *p, long pitch, long stride, bool add)
+{
+    LossOutput o;
+    o.base = p;
+    o.pitch = pitch;
+    o.slot_stride = stride;
+    o.f32 = true;
+    o.add = add;
+    return o;
+}
+
 cudaError_t run_bwd(const LossArgs &a)
 {
     const LossPlan q = loss_plan(a.rows, a.d, a.vocab, a.K, a.dtype, true, al(a.h, 16), al(a.w, 16));
@@ -632,28 +691,43 @@ cudaError_t run_bwd(const LossArgs &a)
             dbias_kernel<<<(cols + 31) / 32, 1024, 0, a.s>>>(dbp, (a.rows + 31) / 32, pitch, cols, a.db + v0);
             e = cudaGetLastError();
         }
-        if (e == cudaSuccess && a.dh) {
-            // every piece splits the same way, so that each adds to the same slots
-            const bool direct = !q.dh_slots && q.dh.splits == 1 && tma_out && al(a.dh, 16);
-            const long stride = (long)a.rows * q.dp;
-            float *acc = (float *)(ws + q.dh_acc);
-            const LossOutput out = direct ? LossOutput{a.dh, a.d, 0, a.dtype == TXL_F32, false}
-                                          : LossOutput{acc, q.dp, stride, true, v0 > 0};
-            e = launch_loss_contract(dz, false, w, a.rows, a.d, cols, out, q.dh, a.s);
-            if (e == cudaSuccess && !direct && v0 + cols == a.vocab)
-                e = sum_slots(a, q, acc, q.dh.splits, stride, a.dh, a.rows);
+        // both gradients of the piece in one launch
+        LossContraction job[2];
+        int n = 0;
+        LossTiling dh, dw;
+        gradient_tiling(a.rows, a.d, cols, q.piece, q.parts, q.dh_slots, &dh, &dw);
+        const long hs = (long)a.rows * q.dp, ws_stride = (long)cols * q.dp;
+        float *acc_h = (float *)(ws + q.dh_acc), *acc_w = (float *)(ws + q.dw_acc);
+        // every piece splits dh the same way, so that each adds to the same slots
+        const bool h_direct = !q.dh_slots && q.dh.splits == 1 && tma_out && al(a.dh, 16);
+        void *dw_out = a.dw ? (unsigned char *)a.dw + (size_t)v0 * a.d * esz : nullptr;
+        const bool w_direct = dw.splits == 1 && tma_out && al(dw_out, 16);
+        if (a.dh) {
+            LossContraction &j = job[n++];
+            j.a = dz;
+            j.b = w;
+            j.a_t = false;
+            j.m = a.rows;
+            j.n = a.d;
+            j.k = cols;
+            j.out = h_direct ? direct_out(a, a.dh) : slot_out(acc_h, q.dp, hs, v0 > 0);
+            j.t = q.dh;
         }
-        if (e == cudaSuccess && a.dw) {
-            const LossTiling t = contract_tiling(cols, a.d, a.rows, q.parts, false);
-            void *dst = (unsigned char *)a.dw + (size_t)v0 * a.d * esz;
-            const bool direct = t.splits == 1 && tma_out && al(dst, 16);
-            const long stride = (long)cols * q.dp;
-            float *acc = (float *)(ws + q.dw_acc);
-            const LossOutput out = direct ? LossOutput{dst, a.d, 0, a.dtype == TXL_F32, false}
-                                          : LossOutput{acc, q.dp, stride, true, false};
-            e = launch_loss_contract(dz, true, h, cols, a.d, a.rows, out, t, a.s);
-            if (e == cudaSuccess && !direct) e = sum_slots(a, q, acc, t.splits, stride, dst, cols);
+        if (a.dw) {
+            LossContraction &j = job[n++];
+            j.a = dz;
+            j.b = h;
+            j.a_t = true;
+            j.m = cols;
+            j.n = a.d;
+            j.k = a.rows;
+            j.out = w_direct ? direct_out(a, dw_out) : slot_out(acc_w, q.dp, ws_stride, false);
+            j.t = dw;
         }
+        if (e == cudaSuccess && n) e = launch_loss_gradients(job, n, q.parts, a.s);
+        if (e == cudaSuccess && a.dh && !h_direct && v0 + cols == a.vocab)
+            e = sum_slots(a, q, acc_h, q.dh.splits, hs, a.dh, a.rows);
+        if (e == cudaSuccess && a.dw && !w_direct) e = sum_slots(a, q, acc_w, dw.splits, ws_stride, dw_out, cols);
     }
     return e;
 }
