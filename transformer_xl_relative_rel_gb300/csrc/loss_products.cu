@@ -6,9 +6,13 @@
 //             strip of vocabulary tiles, the logits themselves never stored;
 //   dz        A = h, B = W: dz = coef (softmax - listed weights) of one
 //             vocabulary piece, rounded to bf16 and stored;
-//   contract  dh = dz W (A = dz, B = W^T) and dW = dz^T h (A = dz^T, B = h^T):
-//             the transposed operands are read as they are stored
-//             (MN-major tiles), nothing is transposed in memory.
+//   contract  dW = dz^T h (A = dz^T read as it is stored, MN-major tiles; B =
+//             h^T from a transposed copy of h) and dh = dz W, as its transpose
+//             W^T dz^T (A = W^T as W is stored, B = dz), turned back on the
+//             way out.  An MN-major A costs nothing, an MN-major B a quarter
+//             of the rate (9728 x 1024 over 9728: 1803 against 1323
+//             TFLOP/s), so B is MN-major only where d_model fills the rows of
+//             the transposed tiles badly (dh = dz W directly).
 // fp32 operands are held as three bf16 parts whose sum is exact (8 + 8 + 8
 // bits of the 24-bit significand); the product keeps the six part products
 // down to 2^-16 of the largest, dropping three of at most 2^-24, smallest
@@ -74,8 +78,8 @@ struct LSmem {
 // one output of a contraction launch
 struct LJob {
     int M, N, bn, tiles_m, tiles_n, ksteps, splits, items;
-    int a_mn;                 // A stored with the output row innermost
-    int f32, add;
+    int a_mn, b_mn;           // operands stored with the output index innermost
+    int f32, add, out_t;      // out_t: element (m, n) goes to row n, column m
 };
 struct LMaps {
     CUtensorMap a[2], b[2], o[2];
@@ -86,14 +90,16 @@ struct LParams {
     // vocabulary passes
     int M, N, bn, tiles_m, tiles_n, strip, ksteps;
     const float *bz;          // [columns], biases in base-2 units; -infinity takes a column out
-    int has_bz, v0;
+    int v0;
     float alpha;
     LossRows r;
     float *ysel, *dbpart;
     float2 *part;
     long dbpitch;
-    // contraction
+    // contraction: the pairs without a last item of job 0 do `ahead` items of
+    // job 1 in the meantime
     LJob job[2];
+    int ahead;
 };
 
 // ------------------------------------------------------------ cta_group forms
@@ -211,6 +217,24 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+__device__ __forceinline__ void st_shared(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void st_shared32(uint32_t at, float x)
+{
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(x) : "memory");
+}
+__device__ __forceinline__ void st_shared16(uint32_t at, float x)
+{
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(__bfloat16_as_ushort(__float2bfloat16(x))) : "memory");
+}
+__device__ __forceinline__ float4 ld_shared(uint32_t at)
+{
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    return v;
+}
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float r;
@@ -286,8 +310,28 @@ __device__ __forceinline__ void l_tmem_wait(float (&v)[32])
 // ------------------------------------------------------------------- items
 struct LItem {
     int m0, nt0, nt1, ks0, ks1, split, strip;
-    int job, M, N, bn, a_mn, b_mn, f32, add;
+    int job, M, N, bn, a_mn, b_mn, f32, add, out_t;
 };
+// The i-th item of tile slot c0 of G, or -1.  Items go round the slots; where
+// job 0's do not come out even, the slots left without one (r .. G-1) take
+// job 1's first items until the others are done.
+template <int MODE>
+__device__ __forceinline__ int l_next(const LParams &p, int c0, int G, int i)
+{
+    if (MODE != MODE_CT) {
+        const long item = c0 + (long)i * G;
+        return item < p.items ? (int)item : -1;
+    }
+    const int n0 = p.job[0].items, r = n0 % G, mine = n0 / G + (c0 < r);
+    if (i < mine) return c0 + i * G;
+    i -= mine;
+    long x;
+    if (c0 >= r)
+        x = i < p.ahead ? (long)i * (G - r) + (c0 - r) : (long)p.ahead * (G - r) + (long)(i - p.ahead) * G + (c0 - r);
+    else
+        x = (long)p.ahead * (G - r) + (long)i * G + (G - r) + c0;
+    return x < p.job[1].items ? (int)(n0 + x) : -1;
+}
 template <int CG, int MODE>
 __device__ __forceinline__ LItem l_item(const LParams &p, int item)
 {
@@ -309,7 +353,8 @@ __device__ __forceinline__ LItem l_item(const LParams &p, int item)
         t.N = j.N;
         t.bn = j.bn;
         t.a_mn = j.a_mn;
-        t.b_mn = 1;
+        t.b_mn = j.b_mn;
+        t.out_t = j.out_t;
         t.f32 = j.f32;
         t.add = j.add;
     } else {
@@ -320,7 +365,7 @@ __device__ __forceinline__ LItem l_item(const LParams &p, int item)
         t.nt1 = t.nt0 + p.strip < p.tiles_n ? t.nt0 + p.strip : p.tiles_n;
         t.ks0 = 0;
         t.ks1 = p.ksteps;
-        t.split = t.job = t.a_mn = t.b_mn = t.f32 = t.add = 0;
+        t.split = t.job = t.a_mn = t.b_mn = t.f32 = t.add = t.out_t = 0;
         t.M = p.M;
         t.N = p.N;
         t.bn = p.bn;
@@ -364,7 +409,7 @@ struct Cursor {
     }
 };
 
-template <int CG, int MODE, bool kParts>
+template <int CG, int MODE, bool kParts, bool kBias>
 __global__ void __launch_bounds__(LNT, 1)
 loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ LParams p)
 {
@@ -427,7 +472,7 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
         if (lane == 0) {
             int it = 0;
             bool ok = true;
-            for (int item = c0; ok && item < p.items; item += G) {
+            for (int i = 0, item; ok && (item = l_next<MODE>(p, c0, G, i)) >= 0; ++i) {
                 const LItem t = l_item<CG, MODE>(p, item);
                 const CUtensorMap *ma = &maps.a[t.job], *mb = &maps.b[t.job];
                 const int bcols = t.bn / CG;                          // this CTA's columns of B
@@ -479,7 +524,7 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
         if (lane == 0 && rank == 0) {
             int it = 0, lt = 0;
             bool ok = true;
-            for (int item = c0; ok && item < p.items; item += G) {
+            for (int i = 0, item; ok && (item = l_next<MODE>(p, c0, G, i)) >= 0; ++i) {
                 const LItem t = l_item<CG, MODE>(p, item);
                 const uint32_t idesc = idesc_bf16(128 * CG, t.bn, t.a_mn, t.b_mn);
                 // K-major: K steps of 32 bytes along the swizzled row; MN-major:
@@ -535,17 +580,17 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
         // =================================================================== epilogue
         const int q = warp & 3, half = (warp - 4) >> 2;
         // staging: STG buffers of 32 rows x 128 bytes per warp, used in turn
-        unsigned char *stg = smem + S::OST + (uint32_t)(warp - 4) * 4096u;
-        uint32_t stg_a = sbase + S::OST + (uint32_t)(warp - 4) * 4096u;
+        // (with column sums of dz the second one is their scratch)
+        const uint32_t stg0 = sbase + S::OST + (uint32_t)(warp - 4) * 4096u;
+        const bool sums = MODE == MODE_DZ && p.dbpart != nullptr;
+        uint32_t stg_a = stg0;
         int nst = 0;
         int lt = 0;
         bool ok = true;
         // the next staging buffer, once the store that last used it has read it
         auto stage_wait = [&]() {
-            if (S::STG == 2) {
-                const uint32_t flip = (nst++ & 1) ? LEPI * 4096u : 0u;
-                stg = smem + S::OST + (uint32_t)(warp - 4) * 4096u + flip;
-                stg_a = sbase + S::OST + (uint32_t)(warp - 4) * 4096u + flip;
+            if (S::STG == 2 && !sums) {
+                stg_a = stg0 + ((nst++ & 1) ? LEPI * 4096u : 0u);
                 if (lane == 0) bulk_wait_read_1();
             } else if (lane == 0) {
                 bulk_wait_read();
@@ -555,12 +600,9 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
         auto stage_bf16 = [&](const float (&v)[32], int at) {      // columns 32 at .. 32 at + 31 of the row
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                uint4 pk;
-                pk.x = pack2(v[8 * j + 0], v[8 * j + 1]);
-                pk.y = pack2(v[8 * j + 2], v[8 * j + 3]);
-                pk.z = pack2(v[8 * j + 4], v[8 * j + 5]);
-                pk.w = pack2(v[8 * j + 6], v[8 * j + 7]);
-                *reinterpret_cast<uint4 *>(stg + lane * 128 + (((4 * at + j) ^ (lane & 7)) << 4)) = pk;
+                st_shared(stg_a + lane * 128 + (((4 * at + j) ^ (lane & 7)) << 4), pack2(v[8 * j + 0], v[8 * j + 1]),
+                          pack2(v[8 * j + 2], v[8 * j + 3]), pack2(v[8 * j + 4], v[8 * j + 5]),
+                          pack2(v[8 * j + 6], v[8 * j + 7]));
             }
         };
         auto store = [&](int job, int x, int y, int z, bool add) {
@@ -581,9 +623,9 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
         };
         const uint64_t alpha2 = pair(p.alpha, p.alpha);
         // without biases the running maximum is kept of the unscaled logits
-        const float mscale = p.has_bz ? 1.f : p.alpha;
+        const float mscale = kBias ? 1.f : p.alpha;
 
-        for (int item = c0; ok && item < p.items; item += G) {
+        for (int i = 0, item; ok && (item = l_next<MODE>(p, c0, G, i)) >= 0; ++i) {
             const LItem t = l_item<CG, MODE>(p, item);
             const int row0 = t.m0 + rank * 128 + 32 * q, row = row0 + lane;
             const bool live = row < t.M;
@@ -608,13 +650,30 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
             auto process = [&](float (&v)[32], int n0, int sub) {
                 if (MODE == MODE_CT) {
                     if (row0 >= t.M || n0 - 32 * sub >= t.N) return;
+                    if (t.out_t) {
+                        // lanes are columns of the output, v its rows
+                        if (t.f32) {
+                            if (n0 >= t.N) return;
+                            stage_wait();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) st_shared32(stg_a + 128 * j + 4 * lane, v[j]);
+                            store(t.job, row0, n0, t.split, t.add);
+                        } else {
+                            if (sub == 0) stage_wait();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) st_shared16(stg_a + 64 * (32 * sub + j) + 2 * lane, v[j]);
+                            if (sub == 1) store(t.job, row0, n0 - 32, 0, false);
+                        }
+                        return;
+                    }
                     if (t.f32) {
                         if (n0 >= t.N) return;
                         stage_wait();
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            *reinterpret_cast<float4 *>(stg + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-                                make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                            st_shared(stg_a + lane * 128 + ((j ^ (lane & 7)) << 4), __float_as_uint(v[4 * j]),
+                                      __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
+                                      __float_as_uint(v[4 * j + 3]));
                         store(t.job, n0, row0, t.split, t.add);
                     } else {
                         if (sub == 0) stage_wait();
@@ -626,7 +685,7 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                 if (n0 >= p.N) return;
                 const int col0 = p.v0 + n0;
                 // y = alpha z + bz in base-2 units (dz: less the row's lse)
-                if (p.has_bz) {
+                if (kBias) {
                     const uint64_t off = pair(-l2, -l2);
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
@@ -663,7 +722,7 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                     for (int j = 0; j < 16; ++j) {
                         float a, b;
                         const uint64_t x = pair(v[2 * j], v[2 * j + 1]);
-                        unpair(p.has_bz ? add2(x, off) : fma2(x, one, off), a, b);
+                        unpair(kBias ? add2(x, off) : fma2(x, one, off), a, b);
                         s[j & 3] = add2(s[j & 3], pair(ex2(a), ex2(b)));
                     }
                     float a, b;
@@ -675,7 +734,7 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
                         float a = v[j], b = v[j + 1];
-                        if (!p.has_bz) unpair(fma2(pair(a, b), alpha2, off), a, b);
+                        if (!kBias) unpair(fma2(pair(a, b), alpha2, off), a, b);
                         unpair(mul2(pair(ex2(a), ex2(b)), c2), v[j], v[j + 1]);
                     }
                     while (cur.c0 < col0 + 32) {
@@ -691,6 +750,40 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                     if (dead) {   // whatever an empty row holds
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = coef == 0.f ? 0.f : v[j];
+                    }
+                    if (sums) {
+                        // column sums over the warp's 32 rows through the scratch
+                        // buffer: each thread adds 8 rows of 4 columns, two
+                        // exchanges join the four groups of rows
+                        const uint32_t scr = stg0 + LEPI * 4096u;
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            st_shared(scr + lane * 128 + ((j ^ (lane & 7)) << 4), __float_as_uint(v[4 * j]),
+                                      __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
+                                      __float_as_uint(v[4 * j + 3]));
+                        __syncwarp();
+                        const int c4 = lane & 7, r0 = (lane >> 3) * 8;
+                        float4 x = ld_shared(scr + r0 * 128 + (c4 << 4));
+                        uint64_t lo = pair(x.x, x.y), hi = pair(x.z, x.w);
+#pragma unroll
+                        for (int r = 1; r < 8; ++r) {
+                            x = ld_shared(scr + (r0 + r) * 128 + ((c4 ^ r) << 4));
+                            lo = add2(lo, pair(x.x, x.y));
+                            hi = add2(hi, pair(x.z, x.w));
+                        }
+                        unpair(lo, x.x, x.y);
+                        unpair(hi, x.z, x.w);
+#pragma unroll
+                        for (int o = 8; o < 32; o <<= 1) {
+                            x.x += __shfl_xor_sync(0xffffffffu, x.x, o);
+                            x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
+                            x.z += __shfl_xor_sync(0xffffffffu, x.z, o);
+                            x.w += __shfl_xor_sync(0xffffffffu, x.w, o);
+                        }
+                        // (columns past the last one lie in the row's padding)
+                        if (lane < 8 && row0 < p.M)
+                            *reinterpret_cast<float4 *>(p.dbpart + (long)(row0 >> 5) * p.dbpitch + n0 + 4 * c4) = x;
                     }
                     if (!kParts) {
                         if (sub == 0) stage_wait();
@@ -716,26 +809,10 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                                     rest[8 * j + 2 * x + 1] = b - tb;
                                 }
                                 // 64-byte rows, their swizzle: chunk c of row r at c ^ (r / 2 % 4)
-                                *reinterpret_cast<uint4 *>(stg + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
-                                    make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                                st_shared(stg_a + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), w4[0], w4[1], w4[2], w4[3]);
                             }
                             if (row0 < p.M) store(0, n0, row0, part, false);
                         }
-                    }
-                    if (p.dbpart) {
-                        // sums over the warp's 32 rows: halving exchanges leave column j in lane j
-#pragma unroll
-                        for (int o = 16; o; o >>= 1) {
-                            const bool up = lane & o;
-#pragma unroll
-                            for (int j = 0; j < o; ++j) {
-                                const float send = up ? v[j] : v[j + o];
-                                const float keep = up ? v[j + o] : v[j];
-                                v[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-                            }
-                        }
-                        if (row0 < p.M && n0 + lane < p.N)
-                            p.dbpart[(long)(row0 >> 5) * p.dbpitch + n0 + lane] = v[0];
                     }
                 }
             };
@@ -778,6 +855,8 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                 }
                 ++lt;
                 tc_fence_after();
+                if (kBias && nt + 1 < t.nt1 && 32 * lane < t.bn && (nt + 1) * t.bn + 32 * lane < t.N)   // the next tile's biases
+                    asm volatile("prefetch.global.L1 [%0];" ::"l"(p.bz + (nt + 1) * t.bn + 32 * lane));
                 if (half >= nch) {
                     release(buf);
                     continue;
@@ -848,10 +927,10 @@ cudaError_t l_in_map(CUtensorMap *m, const LossMatrix &x, int box_y)
                  box_y, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int CG, int MODE, bool kParts>
+template <int CG, int MODE, bool kParts, bool kBias>
 cudaError_t l_launch(const LMaps &maps, const LParams &p, cudaStream_t s)
 {
-    auto kern = loss_product_kernel<CG, MODE, kParts>;
+    auto kern = loss_product_kernel<CG, MODE, kParts, kBias>;
     static std::atomic<int> most[64];      // tiles that run at once, per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -887,11 +966,12 @@ cudaError_t l_launch(const LMaps &maps, const LParams &p, cudaStream_t s)
     return cudaLaunchKernelEx(&cfg, kern, maps, p);
 }
 
-template <int MODE>
+template <int MODE, bool kBias>
 cudaError_t l_launch_cg(int cg, int parts, const LMaps &maps, const LParams &p, cudaStream_t s)
 {
-    if (parts == 3) return cg == 2 ? l_launch<2, MODE, true>(maps, p, s) : l_launch<1, MODE, true>(maps, p, s);
-    return cg == 2 ? l_launch<2, MODE, false>(maps, p, s) : l_launch<1, MODE, false>(maps, p, s);
+    if (parts == 3)
+        return cg == 2 ? l_launch<2, MODE, true, kBias>(maps, p, s) : l_launch<1, MODE, true, kBias>(maps, p, s);
+    return cg == 2 ? l_launch<2, MODE, false, kBias>(maps, p, s) : l_launch<1, MODE, false, kBias>(maps, p, s);
 }
 
 long cdiv(long a, long b) { return (a + b - 1) / b; }
@@ -912,7 +992,6 @@ cudaError_t vocab_params(LParams &p, LMaps &maps, const LossMatrix &h, const Los
     p.items = (int)items;
     p.ksteps = (int)cdiv(h.cols, LK);
     p.bz = bz;
-    p.has_bz = bz != nullptr;
     p.v0 = v0;
     p.alpha = alpha;
     p.r = r;
@@ -925,24 +1004,32 @@ cudaError_t vocab_params(LParams &p, LMaps &maps, const LossMatrix &h, const Los
 // 64-deep step of a 256-column tile (per SM 128 rows of it), what an item
 // costs beside its steps, a vocabulary tile's epilogue, a launch with the
 // drain before it, and HBM bytes per microsecond.
-constexpr double kStepUs = 0.26, kItemUs = 1.0, kEpilogueUs = 2.4, kLaunchUs = 5.0, kHbmPerUs = 6.0e6;
+constexpr double kStepUs = 0.32, kItemUs = 1.0, kEpilogueUs = 2.4, kLaunchUs = 5.0, kHbmPerUs = 6.0e6;
+constexpr double kMnB = 1.36;          // what an MN-major B takes longer
 constexpr double kL2Bytes = 80e6;      // dz pieces up to this are read back from L2
 
 double step_us(int bn, int parts) { return kStepUs * bn / 256 * (parts == 3 ? 6 : 1); }
 
-// the longest of the tile slots when n0 items of a and then n1 items of b go round them in turn
-double makespan(long slots, long n0, double a, long n1, double b)
+// The longest of the tile slots when n0 items of a and n1 items of b go round
+// them as l_next deals them out, with the best `ahead`.
+double makespan(long slots, long n0, double a, long n1, double b, int *ahead)
 {
-    const long r = n0 % slots;
-    double most = 0;
-    const long at[4] = {0, r, (r + slots - 1) % slots, (r + n1 % slots + slots - 1) % slots};
-    for (long j : at) {
-        const long c0 = cdiv(n0 > j ? n0 - j : 0, slots), off = (j - r + slots) % slots;
-        const long c1 = cdiv(n1 > off ? n1 - off : 0, slots);
-        const double t = c0 * a + c1 * b;
-        most = t > most ? t : most;
+    const long r = n0 % slots, q = n0 / slots;
+    double best = 1e300;
+    const long k0 = r ? (long)(a / b) : 0;
+    for (long k = k0; k <= k0 + (r ? 1 : 0); ++k) {
+        const long rest = n1 - k * (slots - r);                     // items dealt out to all
+        const long late = rest > 0 ? cdiv(rest, slots) : 0;         // ... of them to the slots from r on
+        const long early = rest > slots - r ? cdiv(rest - (slots - r), slots) : 0;
+        const long kk = rest > 0 ? k : cdiv(n1, slots - r > 0 ? slots - r : 1);
+        const double x = q * a + (kk + late) * b, y = r ? (q + 1) * a + early * b : 0.0;
+        const double t = x > y ? x : y;
+        if (t < best) {
+            best = t;
+            *ahead = (int)k;
+        }
     }
-    return most;
+    return best;
 }
 
 void job_tiles(LossTiling &t, int m, int n, int cg, int parts)
@@ -953,6 +1040,8 @@ void job_tiles(LossTiling &t, int m, int n, int cg, int parts)
     t.bn = (int)(cdiv(cdiv(n, t.tiles_n), 64) * 64);
     t.strip = 1;
     t.splits = 1;
+    t.turned = t.first = false;
+    t.ahead = 0;
 }
 
 }  // namespace
@@ -966,6 +1055,8 @@ LossTiling vocab_tiling(int rows, int cols, int d, int parts, double *us)
     t.tiles_m = (int)cdiv(rows, 128 * t.cg);
     t.tiles_n = (int)cdiv(cols, t.bn);
     t.splits = 1;
+    t.turned = t.first = false;
+    t.ahead = 0;
     // strips: few enough partial results, and the last round of CTAs full
     const long slots = device_sm_count() / t.cg;
     double best = 1e300;
@@ -984,29 +1075,44 @@ LossTiling vocab_tiling(int rows, int cols, int d, int parts, double *us)
     return t;
 }
 
-double gradient_tiling(int rows, int d, int cols, int whole, int parts, bool dh_slots, LossTiling *dh, LossTiling *dw)
+double gradient_tiling(int rows, int d, int cols, int whole, int parts, bool dh_slots, int dh_splits, LossTiling *dh,
+                       LossTiling *dw)
 {
     const int cg = rows > 128 ? 2 : 1;
+    // dh as the transpose of W^T dz^T unless that wastes more rows of its tiles
+    // than an MN-major B costs
+    LossTiling turned;
+    job_tiles(turned, d, rows, cg, parts);
     job_tiles(*dh, rows, d, cg, parts);
+    turned.turned = true;
+    if ((double)turned.tiles_m * turned.tiles_n * turned.bn <= kMnB * dh->tiles_m * dh->tiles_n * dh->bn) *dh = turned;
     job_tiles(*dw, cols, d, cg, parts);
     const long slots = device_sm_count() / cg;
     const long n0 = (long)dh->tiles_m * dh->tiles_n, n1 = (long)dw->tiles_m * dw->tiles_n;
-    const double s0 = step_us(dh->bn, parts), s1 = step_us(dw->bn, parts);
+    const double s0 = step_us(dh->bn, parts) * (dh->turned ? 1.0 : kMnB), s1 = step_us(dw->bn, parts);
     const long k0 = cdiv(cols, LK), k1 = cdiv(rows, LK), kw = cdiv(whole, LK);
     double best = 1e300;
     static const int cand[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32, 48, 64};
     for (int a : cand) {
         if (a > kw) break;
+        if (dh_splits && a != dh_splits) continue;
         for (int b : cand) {
             if (b > k1) break;
             // a split costs a pass over its slot, written (added to) and read back
-            double us = makespan(slots, n0 * a, cdiv(k0, a) * s0 + kItemUs, n1 * b, cdiv(k1, b) * s1 + kItemUs);
+            int ahead;
+            const double l0 = cdiv(k0, a) * s0 + kItemUs, l1 = cdiv(k1, b) * s1 + kItemUs;
+            const bool w_first = l1 > l0;
+            double us = w_first ? makespan(slots, n1 * b, l1, n0 * a, l0, &ahead)
+                                : makespan(slots, n0 * a, l0, n1 * b, l1, &ahead);
             const double pass = (a > 1 || dh_slots ? 2.0 * a * rows * d * 4 : 0.0) + (b > 1 ? 2.0 * b * cols * d * 4 : 0.0);
             us += pass / kHbmPerUs + (b > 1 ? kLaunchUs : 0.0);
             if (us < best) {
                 best = us;
                 dh->splits = a;
                 dw->splits = b;
+                dh->first = !w_first;
+                dw->first = w_first;
+                dh->ahead = dw->ahead = ahead;
             }
         }
     }
@@ -1027,7 +1133,7 @@ int gradient_piece(int rows, int d, int vocab, int parts, int most)
             double vus;
             vocab_tiling(rows, c, d, parts, &vus);
             const double dz = (double)rows * c * 2 * parts, hbm = dz > kL2Bytes ? dz / kHbmPerUs : 0.0;
-            const double g = gradient_tiling(rows, d, c, cols, parts, cols < vocab, &a, &b);
+            const double g = gradient_tiling(rows, d, c, cols, parts, cols < vocab, 0, &a, &b);
             return (vus > hbm ? vus : hbm) + (g > 2 * hbm ? g : 2 * hbm);
         };
         const double us = vocab / cols * cost(cols) + (last ? cost(last) : 0.0);
@@ -1049,7 +1155,8 @@ cudaError_t launch_loss_lse(const LossMatrix &h, const LossMatrix &w, const floa
     if (e != cudaSuccess) return e;
     p.ysel = ysel;
     p.part = part;
-    return l_launch_cg<MODE_LSE>(t.cg, h.pieces, maps, p, s);
+    return bz ? l_launch_cg<MODE_LSE, true>(t.cg, h.pieces, maps, p, s)
+              : l_launch_cg<MODE_LSE, false>(t.cg, h.pieces, maps, p, s);
 }
 
 cudaError_t launch_loss_dz(const LossMatrix &h, const LossMatrix &w, const float *bz, int v0, float alpha,
@@ -1067,7 +1174,8 @@ cudaError_t launch_loss_dz(const LossMatrix &h, const LossMatrix &w, const float
     e = l_map(&maps.o[0], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dz.base, dz.cols, dz.rows, dz.pieces, dz.pitch,
               dz.piece_stride, three ? 32 : 64, 32, three ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
-    return l_launch_cg<MODE_DZ>(t.cg, h.pieces, maps, p, s);
+    return bz ? l_launch_cg<MODE_DZ, true>(t.cg, h.pieces, maps, p, s)
+              : l_launch_cg<MODE_DZ, false>(t.cg, h.pieces, maps, p, s);
 }
 
 cudaError_t launch_loss_gradients(const LossContraction *jobs, int n, int parts, cudaStream_t s)
@@ -1088,6 +1196,8 @@ cudaError_t launch_loss_gradients(const LossContraction *jobs, int n, int parts,
         j.ksteps = (int)cdiv(c.k, LK);
         j.splits = c.t.splits;
         j.a_mn = c.a_t;
+        j.b_mn = !c.b_t;
+        j.out_t = c.out_t;
         j.f32 = c.out.f32;
         j.add = c.out.add;
         const long mine = (long)j.tiles_m * j.tiles_n * j.splits;
@@ -1095,15 +1205,17 @@ cudaError_t launch_loss_gradients(const LossContraction *jobs, int n, int parts,
         if (items > INT32_MAX) return cudaErrorNotSupported;
         j.items = (int)mine;
         cudaError_t e = l_in_map(&maps.a[x], c.a, c.a_t ? 64 : 128);
-        if (e == cudaSuccess) e = l_in_map(&maps.b[x], c.b, 64);
+        if (e == cudaSuccess) e = l_in_map(&maps.b[x], c.b, c.b_t ? j.bn / c.t.cg : 64);
         if (e == cudaSuccess)
             e = l_map(&maps.o[x], c.out.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                      c.out.f32 ? 4 : 2, c.out.base, c.n, c.m, j.splits, c.out.pitch, c.out.slot_stride,
-                      c.out.f32 ? 32 : 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
+                      c.out.f32 ? 4 : 2, c.out.base, c.out_t ? c.m : c.n, c.out_t ? c.n : c.m, j.splits, c.out.pitch,
+                      c.out.slot_stride, c.out.f32 || c.out_t ? 32 : 64, c.out_t && !c.out.f32 ? 64 : 32,
+                      c.out_t ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B);
         if (e != cudaSuccess) return e;
     }
     p.items = (int)items;
-    return l_launch_cg<MODE_CT>(jobs[0].t.cg, parts, maps, p, s);
+    p.ahead = n == 2 ? jobs[0].t.ahead : 0;
+    return l_launch_cg<MODE_CT, false>(jobs[0].t.cg, parts, maps, p, s);
 }
 
 cudaError_t read_and_clear_loss_error(unsigned int *word, cudaStream_t s)

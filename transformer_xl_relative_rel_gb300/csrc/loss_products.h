@@ -35,6 +35,9 @@ struct LossTiling {
     int tiles_m, tiles_n;
     int strip;          // vocabulary passes: tiles of one row block that a CTA (pair) does in a row
     int splits;         // gradients: parts of the long axis, each into a slot of its own
+    bool turned;        // dh: computed as W^T dz^T
+    bool first;         // gradients: dealt out before the other (the longer items)
+    int ahead;          // ... items of the other that go to the CTAs without a last item of this one
 };
 
 // Vocabulary pass over rows x cols logits; *us its estimated time.
@@ -45,7 +48,9 @@ constexpr int kSlotsPerStrip = 2;      // the halves of a tile's columns are kep
 // The launch that makes dh += dz W and dW = dz^T h of one vocabulary piece of
 // `cols` columns (`whole`: the columns of the call's other pieces, whose dh
 // slots it adds to with dh_slots); returns its estimated time in us.
-double gradient_tiling(int rows, int d, int cols, int whole, int parts, bool dh_slots, LossTiling *dh, LossTiling *dw);
+// dh_splits fixes dh's splits (0: free).
+double gradient_tiling(int rows, int d, int cols, int whole, int parts, bool dh_slots, int dh_splits, LossTiling *dh,
+                       LossTiling *dw);
 // Columns of the backward's vocabulary pieces: at most `most`, a multiple of
 // kLossPieceUnit unless it is the whole vocabulary.
 constexpr int kLossPieceUnit = 256;
@@ -63,10 +68,11 @@ cudaError_t launch_loss_dz(const LossMatrix &h, const LossMatrix &w, const float
                            const LossRows &r, const LossMatrix &dz, float *dbpart, const LossTiling &t,
                            cudaStream_t s);
 
-// out[m][n] = sum_k a(m, k) b(k, n).  a is stored [m][k], or [k][m] with
-// a_t; b is stored [k][n].  f32 selects fp32 output; it then has `splits`
-// slots of slot_stride elements (the sum of which is the product), added to
-// what they hold with `add`.  One or two of them per launch, with one cg.
+// out(m, n) = sum_k a(m, k) b(k, n).  a is stored [m][k], or [k][m] with
+// a_t; b is stored [k][n], or [n][k] with b_t; out [m][n], or [n][m] with
+// out_t.  f32 selects fp32 output; it then has `splits` slots of slot_stride
+// elements (the sum of which is the product), added to what they hold with
+// `add`.  One or two of them per launch, with one cg.
 struct LossOutput {
     void *base;
     long pitch, slot_stride;
@@ -74,7 +80,7 @@ struct LossOutput {
 };
 struct LossContraction {
     LossMatrix a, b;
-    bool a_t;
+    bool a_t, b_t, out_t;
     int m, n, k;
     LossOutput out;
     LossTiling t;

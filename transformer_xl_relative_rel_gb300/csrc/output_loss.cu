@@ -170,17 +170,31 @@ __global__ void __launch_bounds__(256) bias_scale_kernel(const float *__restrict
     if (j < vocab) bz[j] = bias[j] * alpha;
 }
 
+// The bf16 parts of an element: itself, or the three parts of an fp32 value,
+// each the bf16 nearest to what the parts before it leave (a finite value
+// that would round to infinity rounds down instead); v keeps what is left.
+template <typename T>
+__device__ __forceinline__ __nv_bfloat16 next_part(float &v)
+{
+    __nv_bfloat16 r = __float2bfloat16(v);
+    if (sizeof(T) == 4) {
+        float f = __bfloat162float(r);
+        if (isinf(f) && !isinf(v)) {
+            f = __uint_as_float(__float_as_uint(v) & 0xffff0000u);
+            r = __float2bfloat16(f);
+        }
+        v = isfinite(v) ? v - f : 0.f;
+    }
+    return r;
+}
+
 // An operand of the products that the TMA unit cannot read as it lies (fp32,
-// row pitch or base not a multiple of 16 bytes), or h of the backward, whose
-// rows of factor 0 come out as zeros whatever they hold: dst[part][row][dp]
-// with zeros past d.  One part holds bf16 values, three the fp32 values
-// (each the bf16 nearest to what the parts before it leave; finite values
-// that would round to infinity round down instead).  One thread per 8
-// elements; HBM-bound.
+// row pitch or base not a multiple of 16 bytes): dst[part][row][dp] with
+// zeros past d.  One thread per 8 elements; HBM-bound.
 template <typename T>
 __global__ void __launch_bounds__(256)
 operand_kernel(const T *__restrict__ src, __nv_bfloat16 *__restrict__ dst, int rows, int d, int dp, long part_stride,
-               const float *__restrict__ coef, int vec)
+               int vec)
 {
     const int per = dp / 8;
     const long n = (long)rows * per;
@@ -188,10 +202,7 @@ operand_kernel(const T *__restrict__ src, __nv_bfloat16 *__restrict__ dst, int r
         const long i = x / per;
         const int c = (int)(x - i * per) * 8;
         float v[8];
-        if (coef && coef[i] == 0.f) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = 0.f;
-        } else if (vec) {   // 16-byte aligned rows
+        if (vec) {   // 16-byte aligned rows
             __align__(16) T t[8];
 #pragma unroll
             for (int j = 0; j < (int)sizeof(T) / 2; ++j)
@@ -207,19 +218,59 @@ operand_kernel(const T *__restrict__ src, __nv_bfloat16 *__restrict__ dst, int r
         for (int part = 0; part < (sizeof(T) == 4 ? 3 : 1); ++part) {
             __align__(16) __nv_bfloat16 b[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                __nv_bfloat16 r = __float2bfloat16(v[j]);
-                if (sizeof(T) == 4) {
-                    float f = __bfloat162float(r);
-                    if (isinf(f) && !isinf(v[j])) {
-                        f = __uint_as_float(__float_as_uint(v[j]) & 0xffff0000u);
-                        r = __float2bfloat16(f);
-                    }
-                    v[j] = isfinite(v[j]) ? v[j] - f : 0.f;
-                }
-                b[j] = r;
-            }
+            for (int j = 0; j < 8; ++j) b[j] = next_part<T>(v[j]);
             *reinterpret_cast<uint4 *>(dst + part * part_stride + at) = *reinterpret_cast<const uint4 *>(b);
+        }
+    }
+}
+
+// h transposed for dW: dst[part][column][rp], rows of factor 0 as zeros
+// whatever they hold, zeros from `rows` to rp (a multiple of 8).  64 x 64
+// elements per block through shared memory, 16 bytes per access of memory
+// (element loads where rows are not aligned); HBM-bound.
+template <typename T>
+__global__ void __launch_bounds__(256)
+transpose_kernel(const T *__restrict__ src, __nv_bfloat16 *__restrict__ dst, int rows, int d, long rp,
+                 long part_stride, const float *__restrict__ coef, int vec)
+{
+    constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
+    __shared__ __nv_bfloat16 s[kParts][64][65];   // [column][row]
+    const long i0 = (long)blockIdx.x * 64;
+    const int c0 = blockIdx.y * 64;
+#pragma unroll
+    for (int x = threadIdx.x; x < 512; x += 256) {
+        const int y = x >> 3, c = (x & 7) * 8;
+        const long i = i0 + y;
+        float v[8];
+        const bool live = i < rows && coef[i] != 0.f;
+        if (live && vec && c0 + c < d) {
+            __align__(16) T t[8];
+#pragma unroll
+            for (int j = 0; j < (int)sizeof(T) / 2; ++j)
+                reinterpret_cast<uint4 *>(t)[j] = reinterpret_cast<const uint4 *>(src + i * d + c0 + c)[j];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = to_f(t[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = live && c0 + c + j < d ? to_f(src[i * d + c0 + c + j]) : 0.f;
+        }
+#pragma unroll
+        for (int part = 0; part < kParts; ++part)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[part][c + j][y] = next_part<T>(v[j]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int x = threadIdx.x; x < 512; x += 256) {
+        const int c = x >> 3, y = (x & 7) * 8;
+        if (c0 + c >= d || i0 + y >= rp) continue;
+#pragma unroll
+        for (int part = 0; part < kParts; ++part) {
+            __align__(16) __nv_bfloat16 b[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) b[j] = s[part][c][y + j];
+            *reinterpret_cast<uint4 *>(dst + part * part_stride + (c0 + c) * rp + i0 + y) =
+                *reinterpret_cast<const uint4 *>(b);
         }
     }
 }
@@ -344,7 +395,7 @@ struct LossPlan {
     int slots;              // forward: partial softmaxes per row over all pieces
     LossTiling dh;          // of a whole piece
     bool dh_slots;
-    size_t col, p, ent, coef, l2, bz, ysel, part, h, w, dz, dh_acc, dw_acc, dbpart, bytes;
+    size_t col, p, ent, coef, l2, bz, ysel, part, h, ht, w, dz, dh_acc, dw_acc, dbpart, bytes;
 };
 
 LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool backward, bool h_ok, bool w_ok)
@@ -360,7 +411,7 @@ LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool back
     q.parts = dtype == TXL_F32 ? 3 : 1;
     q.dp = (int)up(d, 8);
     const bool tma = dtype == TXL_BF16 && d % 8 == 0;
-    q.copy_h = backward || !tma || !h_ok;
+    q.copy_h = !tma || !h_ok;
     q.copy_w = !tma || !w_ok;
     // what a vocabulary column of a piece takes; pieces start at multiples of the widest tile
     const size_t per = ((backward ? n : 0) + (q.copy_w ? (size_t)q.dp : 0)) * q.parts * 2;
@@ -376,7 +427,7 @@ LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool back
     q.bz = take((size_t)vocab * 4 + 256);   // read in fours past the last column
     q.h = take(q.copy_h ? n * q.dp * q.parts * 2 : 0);
     q.w = take(q.copy_w ? (size_t)q.piece * q.dp * q.parts * 2 : 0);
-    q.coef = q.l2 = q.dz = q.dh_acc = q.dw_acc = q.dbpart = q.ysel = q.part = 0;
+    q.coef = q.l2 = q.ht = q.dz = q.dh_acc = q.dw_acc = q.dbpart = q.ysel = q.part = 0;
     q.slots = 0;
     q.dh_slots = false;
     if (!backward) {
@@ -388,13 +439,14 @@ LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool back
     } else {
         q.coef = take(n * 4);
         q.l2 = take(n * 4);
+        q.ht = take((size_t)d * up(rows, 8) * q.parts * 2);
         q.dz = take(n * up(q.piece, 64) * q.parts * 2);
         q.dh_slots = q.piece < vocab;
         // the last, narrower piece may split dW further
         LossTiling dw, dh_last, dw_last;
         const int last = vocab % q.piece ? vocab % q.piece : q.piece;
-        gradient_tiling(rows, d, q.piece, q.piece, q.parts, q.dh_slots, &q.dh, &dw);
-        gradient_tiling(rows, d, last, q.piece, q.parts, q.dh_slots, &dh_last, &dw_last);
+        gradient_tiling(rows, d, q.piece, q.piece, q.parts, q.dh_slots, 0, &q.dh, &dw);
+        gradient_tiling(rows, d, last, q.piece, q.parts, q.dh_slots, q.dh.splits, &dh_last, &dw_last);
         const size_t dw_whole = (size_t)dw.splits * q.piece, dw_rest = (size_t)dw_last.splits * last;
         // whatever the output's alignment: the products go to the slots where TMA cannot write it
         q.dh_acc = take((size_t)q.dh.splits * n * q.dp * 4);
@@ -565,23 +617,22 @@ cudaError_t launch_rows(const LossArgs &a, const LossRows &r, const LossPlan &q,
     return cudaGetLastError();
 }
 
-// a copied operand: h with the backward's row factors, or a piece of W
-cudaError_t copy_operand(const LossArgs &a, const LossPlan &q, const void *src, size_t at, int rows, long part_stride,
-                         const float *coef)
+// a copied operand: h, or a piece of W
+cudaError_t copy_operand(const LossArgs &a, const LossPlan &q, const void *src, size_t at, int rows, long part_stride)
 {
     __nv_bfloat16 *dst = (__nv_bfloat16 *)((unsigned char *)a.ws + at);
     const long n = (long)rows * (q.dp / 8), want = (n + 255) / 256, most = 16L * device_sm_count();
     const int grid = (int)(want < most ? want : most);
     if (a.dtype == TXL_F32)
-        operand_kernel<float><<<grid, 256, 0, a.s>>>((const float *)src, dst, rows, a.d, q.dp, part_stride, coef,
+        operand_kernel<float><<<grid, 256, 0, a.s>>>((const float *)src, dst, rows, a.d, q.dp, part_stride,
                                                      a.d % 8 == 0 && al(src, 16));
     else
         operand_kernel<__nv_bfloat16><<<grid, 256, 0, a.s>>>((const __nv_bfloat16 *)src, dst, rows, a.d, q.dp,
-                                                             part_stride, coef, a.d % 8 == 0 && al(src, 16));
+                                                             part_stride, a.d % 8 == 0 && al(src, 16));
     return cudaGetLastError();
 }
 
-cudaError_t h_operand(const LossArgs &a, const LossPlan &q, const float *coef, LossMatrix *m)
+cudaError_t h_operand(const LossArgs &a, const LossPlan &q, LossMatrix *m)
 {
     if (!q.copy_h) {
         *m = {a.h, a.d, 0, a.rows, a.d, 1};
@@ -589,7 +640,24 @@ cudaError_t h_operand(const LossArgs &a, const LossPlan &q, const float *coef, L
     }
     const long stride = (long)a.rows * q.dp;
     *m = {(unsigned char *)a.ws + q.h, q.dp, stride, a.rows, q.dp, q.parts};
-    return copy_operand(a, q, a.h, q.h, a.rows, stride, coef);
+    return copy_operand(a, q, a.h, q.h, a.rows, stride);
+}
+
+// h^T for dW
+cudaError_t ht_operand(const LossArgs &a, const LossPlan &q, const float *coef, LossMatrix *m)
+{
+    const long rp = up(a.rows, 8), stride = a.d * rp;
+    __nv_bfloat16 *dst = (__nv_bfloat16 *)((unsigned char *)a.ws + q.ht);
+    *m = {dst, rp, stride, a.d, (int)rp, q.parts};
+    const dim3 grid((unsigned)((a.rows + 63) / 64), (unsigned)((a.d + 63) / 64));
+    const int vec = a.d % 8 == 0 && al(a.h, 16);
+    if (grid.y > 65535) return cudaErrorNotSupported;
+    if (a.dtype == TXL_F32)
+        transpose_kernel<float><<<grid, 256, 0, a.s>>>((const float *)a.h, dst, a.rows, a.d, rp, stride, coef, vec);
+    else
+        transpose_kernel<__nv_bfloat16><<<grid, 256, 0, a.s>>>((const __nv_bfloat16 *)a.h, dst, a.rows, a.d, rp, stride,
+                                                               coef, vec);
+    return cudaGetLastError();
 }
 
 // columns v0 .. v0+cols of the vocabulary
@@ -603,7 +671,7 @@ cudaError_t w_operand(const LossArgs &a, const LossPlan &q, long v0, int cols, L
     }
     const long stride = (long)q.piece * q.dp;
     *m = {(unsigned char *)a.ws + q.w, q.dp, stride, cols, q.dp, q.parts};
-    return copy_operand(a, q, src, q.w, cols, stride, nullptr);
+    return copy_operand(a, q, src, q.w, cols, stride);
 }
 
 cudaError_t sum_slots(const LossArgs &a, const LossPlan &q, const float *slot, int slots, long stride, void *out,
@@ -627,7 +695,7 @@ cudaError_t run_fwd(const LossArgs &a)
     float2 *part = (float2 *)(ws + q.part);
     LossMatrix h, w;
     cudaError_t e = launch_rows(a, r, q, false);
-    if (e == cudaSuccess) e = h_operand(a, q, nullptr, &h);
+    if (e == cudaSuccess) e = h_operand(a, q, &h);
     long slot = 0;
     for (long v0 = 0; e == cudaSuccess && v0 < a.vocab; v0 += q.piece) {
         const int cols = (int)(a.vocab - v0 < q.piece ? a.vocab - v0 : q.piece);
@@ -675,9 +743,10 @@ cudaError_t run_bwd(const LossArgs &a)
     const float *bz = (const float *)(ws + q.bz);
     const size_t esz = a.dtype == TXL_F32 ? 4 : 2;
     const bool tma_out = ((size_t)a.d * esz) % 16 == 0;   // rows that a TMA store can address
-    LossMatrix h, w;
+    LossMatrix h, ht, w;
     cudaError_t e = launch_rows(a, r, q, true);
-    if (e == cudaSuccess) e = h_operand(a, q, r.coef, &h);
+    if (e == cudaSuccess) e = h_operand(a, q, &h);
+    if (e == cudaSuccess && a.dw) e = ht_operand(a, q, r.coef, &ht);
     for (long v0 = 0; e == cudaSuccess && v0 < a.vocab; v0 += q.piece) {
         const int cols = (int)(a.vocab - v0 < q.piece ? a.vocab - v0 : q.piece);
         const long pitch = up(cols, 64);
@@ -695,29 +764,32 @@ cudaError_t run_bwd(const LossArgs &a)
         LossContraction job[2];
         int n = 0;
         LossTiling dh, dw;
-        gradient_tiling(a.rows, a.d, cols, q.piece, q.parts, q.dh_slots, &dh, &dw);
+        gradient_tiling(a.rows, a.d, cols, q.piece, q.parts, q.dh_slots, q.dh.splits, &dh, &dw);
         const long hs = (long)a.rows * q.dp, ws_stride = (long)cols * q.dp;
         float *acc_h = (float *)(ws + q.dh_acc), *acc_w = (float *)(ws + q.dw_acc);
         // every piece splits dh the same way, so that each adds to the same slots
-        const bool h_direct = !q.dh_slots && q.dh.splits == 1 && tma_out && al(a.dh, 16);
+        const bool h_direct = !q.dh_slots && dh.splits == 1 && tma_out && al(a.dh, 16);
         void *dw_out = a.dw ? (unsigned char *)a.dw + (size_t)v0 * a.d * esz : nullptr;
         const bool w_direct = dw.splits == 1 && tma_out && al(dw_out, 16);
         if (a.dh) {
-            LossContraction &j = job[n++];
-            j.a = dz;
-            j.b = w;
-            j.a_t = false;
-            j.m = a.rows;
-            j.n = a.d;
+            LossContraction &j = job[a.dw && dw.first ? 1 : 0];
+            ++n;
+            j.a = dh.turned ? w : dz;
+            j.b = dh.turned ? dz : w;
+            j.a_t = j.b_t = j.out_t = dh.turned;
+            j.m = dh.turned ? a.d : a.rows;
+            j.n = dh.turned ? a.rows : a.d;
             j.k = cols;
             j.out = h_direct ? direct_out(a, a.dh) : slot_out(acc_h, q.dp, hs, v0 > 0);
-            j.t = q.dh;
+            j.t = dh;
         }
         if (a.dw) {
-            LossContraction &j = job[n++];
+            LossContraction &j = job[a.dh && !dw.first ? 1 : 0];
+            ++n;
             j.a = dz;
-            j.b = h;
-            j.a_t = true;
+            j.b = ht;
+            j.a_t = j.b_t = true;
+            j.out_t = false;
             j.m = cols;
             j.n = a.d;
             j.k = a.rows;
@@ -726,7 +798,7 @@ cudaError_t run_bwd(const LossArgs &a)
         }
         if (e == cudaSuccess && n) e = launch_loss_gradients(job, n, q.parts, a.s);
         if (e == cudaSuccess && a.dh && !h_direct && v0 + cols == a.vocab)
-            e = sum_slots(a, q, acc_h, q.dh.splits, hs, a.dh, a.rows);
+            e = sum_slots(a, q, acc_h, dh.splits, hs, a.dh, a.rows);
         if (e == cudaSuccess && a.dw && !w_direct) e = sum_slots(a, q, acc_w, dw.splits, ws_stride, dw_out, cols);
     }
     return e;
