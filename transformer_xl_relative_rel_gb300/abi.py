@@ -581,90 +581,86 @@ def distill_workspace_bytes(rows: int, d_model: int, vocab: int, top_k: int, dty
 
 
 class _LossCall:
-    """The argument checks the output-layer losses share, and where the call's
-    own tensors are made: on h's device and, with ``stream`` given, in that
-    stream's order (so that a workspace freed at return is reused only behind
-    the call)."""
+    """The checks the output-layer losses share, and where their own tensors
+    are made: on h's device and, with ``stream`` given, in that stream's order
+    (so that a workspace freed at return is reused only behind the call)."""
 
-    def __init__(self, h, w, bias, per_row, stream):
-        import torch
-        self.lead = tuple(h.shape[:-1])
-        if h.dim() < 1 or w.dim() != 2 or w.shape[1] != h.shape[-1] or w.dtype != h.dtype:
+    def __init__(self, h, w, stream):
+        d = h.shape[-1] if h.dim() else -1
+        if w.dim() != 2 or w.shape[1] != d or w.dtype != h.dtype:
             raise ValueError("w must be [vocab, d_model] with h's last dimension and dtype")
-        self.rows = 1
-        for n in self.lead:
-            self.rows *= n
+        self.lead = h.shape[:-1]
+        self.rows = self.lead.numel()
         self.vocab, self.d = w.shape
-        self.h, self.stream = h, stream
         self.code = _dtype_code(h)
-        self.tensors = [h, w]
-        if bias is not None:
-            self.typed("bias", bias, (self.vocab,), torch.float32)
-        for name, t, shape, dtype in per_row:
-            self.typed(name, t, shape, dtype)
-        self.placed()
+        self.dev = h.get_device()
+        self.h, self.stream = h, stream
+        self.placed = h.is_contiguous() and w.is_contiguous() and w.get_device() == self.dev
 
-    def typed(self, name, t, shape, dtype):
-        if tuple(t.shape) != tuple(shape):
+    def arg(self, name, t, shape, dtype):
+        """A tensor argument's pointer (None stays None)."""
+        if t is None:
+            return None
+        if t.shape != shape:
             raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
         if t.dtype != dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        self.tensors.append(t)
+        if t.get_device() != self.dev or not t.is_contiguous():
+            self.placed = False
+        return t.data_ptr()
 
-    def placed(self):
-        for t in self.tensors:
-            if not t.is_cuda or not t.is_contiguous():
-                raise ValueError("all tensors must be contiguous CUDA tensors")
-            if t.device != self.h.device:
-                raise ValueError("all tensors must be on h's device")
-        if self.stream is not None and self.stream.device != self.h.device:
-            raise ValueError("stream must belong to h's device")
+    def on_device(self):
+        """After every argument given: all of them contiguous, on one CUDA device."""
+        if self.dev < 0 or not self.placed:
+            raise ValueError("all tensors must be contiguous CUDA tensors on one device")
+        if self.stream is not None and self.stream.device_index != self.dev:
+            raise ValueError("stream must belong to the tensors' device")
 
-    def output(self, name, t, shape, dtype):
+    def make(self, shape, dtype):
         import torch
-        if t is not None:
-            self.typed(name, t, shape, dtype)
-            self.placed()
-            return t
-        with self.context():
-            return torch.empty(*shape, dtype=dtype, device=self.h.device)
+        if self.stream is not None:
+            with torch.cuda.stream(self.stream):
+                return torch.empty(shape, dtype=dtype, device=self.h.device)
+        return torch.empty(shape, dtype=dtype, device=self.h.device)
 
-    def workspace(self, t, nbytes):
+    def run(self, fn, what, need, workspace, *args):
+        """Calls fn(*args, workspace, its bytes, stream); need() is the workspace's size."""
         import torch
-        if t is None:
-            with self.context():
-                return torch.empty(nbytes, dtype=torch.uint8, device=self.h.device)
-        self.tensors.append(t)
-        self.placed()
-        if t.numel() * t.element_size() < nbytes:
-            raise ValueError(f"workspace must hold {nbytes} bytes")
-        return t
-
-    def context(self):
-        import torch
-        return torch.cuda.stream(self.stream) if self.stream is not None else torch.cuda.device(self.h.device)
-
-    def run(self, fn, what, *args):
-        import torch
-        with torch.cuda.device(self.h.device):
-            stream = self.stream if self.stream is not None else torch.cuda.current_stream(self.h.device)
-            st = fn(*args, int(stream.cuda_stream))
+        if workspace is None:
+            workspace = self.make((need(),), torch.uint8)
+        elif workspace.get_device() != self.dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor on the other tensors' device")
+        nbytes = workspace.numel() * workspace.element_size()
+        stream = self.stream.cuda_stream if self.stream is not None else torch._C._cuda_getCurrentRawStream(self.dev)
+        if torch.cuda.current_device() == self.dev:
+            st = fn(*args, workspace.data_ptr(), nbytes, stream)
+        else:
+            with torch.cuda.device(self.dev):
+                st = fn(*args, workspace.data_ptr(), nbytes, stream)
+        if st == 1 and nbytes < need():
+            raise ValueError(f"workspace must hold {need()} bytes")
         _raise(st, what)
 
-
-def _loss_grads(call, grads, w, bias, weight_grads):
-    """The gradients' dict of a backward: given tensors are used, absent ones made."""
-    import torch
-    grads = {} if grads is None else grads
-    grads["dh"] = call.output("dh", grads.get("dh"), tuple(call.h.shape), call.h.dtype)
-    if weight_grads:
-        grads["dw"] = call.output("dw", grads.get("dw"), tuple(w.shape), w.dtype)
-        if bias is not None or grads.get("db") is not None:
-            grads["db"] = call.output("db", grads.get("db"), (call.vocab,), torch.float32)
-    else:
-        grads["dw"] = grads["db"] = None
-    grads.setdefault("db", None)
-    return grads
+    def gradients(self, grads, w, bias, weight_grads):
+        """The dict of a backward's outputs (given tensors used, absent ones made) and their pointers."""
+        import torch
+        grads = {} if grads is None else grads
+        given = [self.arg("dh", grads.get("dh"), self.h.shape, self.h.dtype)]
+        if weight_grads:
+            given.append(self.arg("dw", grads.get("dw"), w.shape, w.dtype))
+            given.append(self.arg("db", grads.get("db"), (self.vocab,), torch.float32))
+        self.on_device()
+        if given[0] is None:
+            grads["dh"] = self.make(self.h.shape, self.h.dtype)
+        if not weight_grads:
+            grads["dw"] = grads["db"] = None
+            return grads, (grads["dh"].data_ptr(), None, None)
+        if given[1] is None:
+            grads["dw"] = self.make(w.shape, w.dtype)
+        if given[2] is None:
+            grads["db"] = self.make((self.vocab,), torch.float32) if bias is not None else None
+        return grads, (grads["dh"].data_ptr(), grads["dw"].data_ptr(),
+                       grads["db"].data_ptr() if grads["db"] is not None else None)
 
 
 def softmax_xent_fwd(h, w, target, bias=None, loss=None, lse=None, workspace=None, stream=None):
@@ -680,13 +676,17 @@ def softmax_xent_fwd(h, w, target, bias=None, loss=None, lse=None, workspace=Non
     tensor of at least ``softmax_xent_workspace_bytes`` bytes, not shared with
     a call that may run at the same time (allocated when None)."""
     import torch
-    lead = tuple(h.shape[:-1])
-    c = _LossCall(h, w, bias, [("target", target, lead, torch.int64)], stream)
-    loss = c.output("loss", loss, lead, torch.float32)
-    lse = c.output("lse", lse, lead, torch.float32)
-    ws = c.workspace(workspace, softmax_xent_workspace_bytes(c.rows, c.d, c.vocab, c.code))
-    c.run(load_library().txl_softmax_xent_fwd, "txl_softmax_xent_fwd", _ptr(h), _ptr(w), _ptr(bias), _ptr(target),
-          c.rows, c.d, c.vocab, c.code, _ptr(loss), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size())
+    c = _LossCall(h, w, stream)
+    y = c.arg("target", target, c.lead, torch.int64)
+    b = c.arg("bias", bias, (c.vocab,), torch.float32)
+    c.arg("loss", loss, c.lead, torch.float32)
+    c.arg("lse", lse, c.lead, torch.float32)
+    c.on_device()
+    loss = c.make(c.lead, torch.float32) if loss is None else loss
+    lse = c.make(c.lead, torch.float32) if lse is None else lse
+    c.run(load_library().txl_softmax_xent_fwd, "txl_softmax_xent_fwd",
+          lambda: softmax_xent_workspace_bytes(c.rows, c.d, c.vocab, c.code), workspace, h.data_ptr(), w.data_ptr(), b,
+          y, c.rows, c.d, c.vocab, c.code, loss.data_ptr(), lse.data_ptr())
     return loss, lse
 
 
@@ -700,26 +700,29 @@ def softmax_xent_bwd(h, w, target, lse, dloss, bias=None, grads=None, weight_gra
     same keys; ``workspace`` as the forward's, of
     ``softmax_xent_workspace_bytes(..., backward=True)`` bytes."""
     import torch
-    lead = tuple(h.shape[:-1])
-    c = _LossCall(h, w, bias, [("target", target, lead, torch.int64), ("lse", lse, lead, torch.float32),
-                               ("dloss", dloss, lead, torch.float32)], stream)
-    g = _loss_grads(c, grads, w, bias, weight_grads)
-    ws = c.workspace(workspace, softmax_xent_workspace_bytes(c.rows, c.d, c.vocab, c.code, backward=True))
-    c.run(load_library().txl_softmax_xent_bwd, "txl_softmax_xent_bwd", _ptr(h), _ptr(w), _ptr(bias), _ptr(target),
-          _ptr(lse), _ptr(dloss), c.rows, c.d, c.vocab, c.code, _ptr(g["dh"]), _ptr(g["dw"]), _ptr(g["db"]), _ptr(ws),
-          ws.numel() * ws.element_size())
-    return g
+    c = _LossCall(h, w, stream)
+    y = c.arg("target", target, c.lead, torch.int64)
+    b = c.arg("bias", bias, (c.vocab,), torch.float32)
+    s = c.arg("lse", lse, c.lead, torch.float32)
+    g = c.arg("dloss", dloss, c.lead, torch.float32)
+    grads, out = c.gradients(grads, w, bias, weight_grads)
+    c.run(load_library().txl_softmax_xent_bwd, "txl_softmax_xent_bwd",
+          lambda: softmax_xent_workspace_bytes(c.rows, c.d, c.vocab, c.code, backward=True), workspace, h.data_ptr(),
+          w.data_ptr(), b, y, s, g, c.rows, c.d, c.vocab, c.code, *out)
+    return grads
 
 
-def _teacher(teacher_idx, teacher_logits, lead):
+def _teacher(c, teacher_idx, teacher_logits):
+    """(top_k, pointers of the indices and logits, the logits' type code)"""
     import torch
-    if teacher_idx.dim() != len(lead) + 1 or tuple(teacher_idx.shape[:-1]) != lead:
-        raise ValueError(f"teacher_idx must be {list(lead)} + [top_k]")
+    shape = teacher_idx.shape
+    if shape[:-1] != c.lead or len(shape) != len(c.lead) + 1:
+        raise ValueError(f"teacher_idx must be {list(c.lead)} + [top_k]")
     if teacher_logits.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"teacher_logits must be float32 or bfloat16, got {teacher_logits.dtype}")
-    shape = tuple(teacher_idx.shape)
-    return shape[-1], [("teacher_idx", teacher_idx, shape, torch.int64),
-                       ("teacher_logits", teacher_logits, shape, teacher_logits.dtype)]
+    e = c.arg("teacher_idx", teacher_idx, shape, torch.int64)
+    y = c.arg("teacher_logits", teacher_logits, shape, teacher_logits.dtype)
+    return shape[-1], e, y, _dtype_code(teacher_logits)
 
 
 def distill_fwd(h, w, teacher_idx, teacher_logits, temperature: float = 1.0, bias=None, loss=None, lse=None,
@@ -735,15 +738,17 @@ def distill_fwd(h, w, teacher_idx, teacher_logits, temperature: float = 1.0, bia
     padding row: loss 0).  Everything else as ``softmax_xent_fwd``.  Returns
     (loss, lse); lse is the student's at ``temperature``."""
     import torch
-    lead = tuple(h.shape[:-1])
-    k, rows = _teacher(teacher_idx, teacher_logits, lead)
-    c = _LossCall(h, w, bias, rows, stream)
-    loss = c.output("loss", loss, lead, torch.float32)
-    lse = c.output("lse", lse, lead, torch.float32)
-    ws = c.workspace(workspace, distill_workspace_bytes(c.rows, c.d, c.vocab, k, c.code))
-    c.run(load_library().txl_distill_fwd, "txl_distill_fwd", _ptr(h), _ptr(w), _ptr(bias), _ptr(teacher_idx),
-          _ptr(teacher_logits), _dtype_code(teacher_logits), float(temperature), c.rows, c.d, c.vocab, k, c.code,
-          _ptr(loss), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size())
+    c = _LossCall(h, w, stream)
+    k, e, y, t_code = _teacher(c, teacher_idx, teacher_logits)
+    b = c.arg("bias", bias, (c.vocab,), torch.float32)
+    c.arg("loss", loss, c.lead, torch.float32)
+    c.arg("lse", lse, c.lead, torch.float32)
+    c.on_device()
+    loss = c.make(c.lead, torch.float32) if loss is None else loss
+    lse = c.make(c.lead, torch.float32) if lse is None else lse
+    c.run(load_library().txl_distill_fwd, "txl_distill_fwd",
+          lambda: distill_workspace_bytes(c.rows, c.d, c.vocab, k, c.code), workspace, h.data_ptr(), w.data_ptr(), b, e,
+          y, t_code, temperature, c.rows, c.d, c.vocab, k, c.code, loss.data_ptr(), lse.data_ptr())
     return loss, lse
 
 
@@ -752,16 +757,16 @@ def distill_bwd(h, w, teacher_idx, teacher_logits, lse, dloss, temperature: floa
     """Gradients of ``(dloss * loss).sum()`` of one ``distill_fwd`` call
     (txl_distill_bwd), as ``softmax_xent_bwd`` returns them."""
     import torch
-    lead = tuple(h.shape[:-1])
-    k, rows = _teacher(teacher_idx, teacher_logits, lead)
-    c = _LossCall(h, w, bias, rows + [("lse", lse, lead, torch.float32), ("dloss", dloss, lead, torch.float32)],
-                  stream)
-    g = _loss_grads(c, grads, w, bias, weight_grads)
-    ws = c.workspace(workspace, distill_workspace_bytes(c.rows, c.d, c.vocab, k, c.code, backward=True))
-    c.run(load_library().txl_distill_bwd, "txl_distill_bwd", _ptr(h), _ptr(w), _ptr(bias), _ptr(teacher_idx),
-          _ptr(teacher_logits), _dtype_code(teacher_logits), float(temperature), _ptr(lse), _ptr(dloss), c.rows, c.d,
-          c.vocab, k, c.code, _ptr(g["dh"]), _ptr(g["dw"]), _ptr(g["db"]), _ptr(ws), ws.numel() * ws.element_size())
-    return g
+    c = _LossCall(h, w, stream)
+    k, e, y, t_code = _teacher(c, teacher_idx, teacher_logits)
+    b = c.arg("bias", bias, (c.vocab,), torch.float32)
+    s = c.arg("lse", lse, c.lead, torch.float32)
+    g = c.arg("dloss", dloss, c.lead, torch.float32)
+    grads, out = c.gradients(grads, w, bias, weight_grads)
+    c.run(load_library().txl_distill_bwd, "txl_distill_bwd",
+          lambda: distill_workspace_bytes(c.rows, c.d, c.vocab, k, c.code, backward=True), workspace, h.data_ptr(),
+          w.data_ptr(), b, e, y, t_code, temperature, s, g, c.rows, c.d, c.vocab, k, c.code, *out)
+    return grads
 
 
 def selftest_wait(limit_us: int, stream=None) -> None:

@@ -1125,7 +1125,7 @@ int gradient_piece(int rows, int d, int vocab, int parts, int most)
     int best_piece = 0;
     double best = 1e300;
     const long units = cdiv(vocab, kLossPieceUnit), least = cdiv(units, most / kLossPieceUnit);
-    for (long n = least; n <= units && n < least + 24; ++n) {
+    for (long n = least; n <= units && n < least + 12; ++n) {
         const long piece = cdiv(units, n) * kLossPieceUnit;
         const int cols = (int)(piece < vocab ? piece : vocab), last = vocab % cols;
         LossTiling a, b;

@@ -8,15 +8,17 @@
 // same with one entry of weight 1 and t = 1.  Both reduce to a sparse list
 // of (column, weight) per row, so one set of kernels serves both:
 //
-//   *_rows_kernel      the row lists (for the backward also the row's factor
-//                      t * dloss and lse in base-2 units);
+//   loss_prep_kernel   the row lists (for the backward also the row's factor
+//                      t * dloss and lse in base-2 units), scaled biases,
+//                      operands laid out for the products;
 //   forward            one pass over the vocabulary (loss_products.cu) leaves
 //                      a maximum and a sum per row and strip of vocabulary
 //                      tiles and the logits of the listed columns;
 //                      loss_merge_kernel joins them;
 //   backward           for each piece of the vocabulary: dz (one piece of it
-//                      in the workspace), dh += dz W, dW = dz^T h, and the
-//                      column sums of dz.
+//                      in the workspace), then dh += dz W and dW = dz^T h in
+//                      one launch; loss_finish_kernel adds up what lies in
+//                      parts (the column sums of dz, split products).
 //
 // Everything is scaled so that exponentials are powers of two:
 // y_ij = z_ij * log2(e) / t.
@@ -52,57 +54,86 @@ __device__ __forceinline__ float from_f<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16(x); }
 
-// cross entropy: one entry of weight 1
-__global__ void __launch_bounds__(256)
-xent_rows_kernel(const int64_t *__restrict__ target, const float *__restrict__ lse,
-                 const float *__restrict__ dloss, LossRows r, int rows, int vocab)
+// ------------------------------------------------------------ preparation
+// What has to be ready before the products, in one launch whose blocks take
+// different parts: the row lists, the scaled biases, operands that the TMA
+// unit cannot read as they lie, and (backward) h transposed.
+struct CopyJob {
+    const void *src;
+    __nv_bfloat16 *dst;
+    int rows, blocks;
+    long part_stride;
+    int vec;              // 16-byte aligned rows
+};
+struct PrepArgs {
+    const int64_t *idx;
+    const void *logits;   // NULL: cross entropy
+    int logits_f32;
+    float t, inv_t;
+    const float *lse, *dloss;   // backward, else NULL
+    LossRows r;
+    int rows, vocab, K2;
+    const float *bias;
+    float alpha;
+    float *bz;
+    int d, dp;
+    CopyJob copy[2];
+    // h^T
+    const void *h;
+    __nv_bfloat16 *ht;
+    long rp, ht_stride;
+    int h_vec, t_cols;    // column blocks of the transpose
+    int row_blocks, bias_blocks, t_blocks;
+};
+
+__device__ __forceinline__ float teacher_logit(const PrepArgs &p, long at)
 {
-    const int i = blockIdx.x * 256 + threadIdx.x;
-    if (i >= rows) return;
-    const int64_t y = target[i];
-    const bool valid = y >= 0 && y < vocab;
-    r.col[i] = valid ? (int)y : kNoColumn;
-    r.p[i] = valid ? 1.f : 0.f;
-    r.ent[i] = 0.f;
-    if (dloss) {
-        const float l = lse[i];
-        r.coef[i] = valid && l != -INFINITY ? dloss[i] : 0.f;
-        r.l2[i] = l * (1.f / kLn2);
+    return p.logits_f32 ? static_cast<const float *>(p.logits)[at]
+                        : to_f(static_cast<const __nv_bfloat16 *>(p.logits)[at]);
+}
+__device__ __forceinline__ bool teacher_valid(const PrepArgs &p, long at)
+{
+    const int64_t e = p.idx[at];
+    return e >= 0 && e < p.vocab && teacher_logit(p, at) != -INFINITY;
+}
+
+// t * dloss, 0 for a row without a valid entry or a finite logit
+__device__ __forceinline__ float row_factor(const PrepArgs &p, long i, bool valid)
+{
+    return valid && p.lse[i] != -INFINITY ? p.t * p.dloss[i] : 0.f;
+}
+
+// cross entropy: one entry of weight 1; a thread per row
+__device__ __forceinline__ void xent_rows(const PrepArgs &p)
+{
+    const long i = (long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= p.rows) return;
+    const int64_t y = p.idx[i];
+    const bool valid = y >= 0 && y < p.vocab;
+    p.r.col[i] = valid ? (int)y : kNoColumn;
+    p.r.p[i] = valid ? 1.f : 0.f;
+    p.r.ent[i] = 0.f;
+    if (p.dloss) {
+        p.r.coef[i] = row_factor(p, i, valid);
+        p.r.l2[i] = p.lse[i] * (1.f / kLn2);
     }
 }
 
 // distillation: the softmax of a row's valid entries at temperature t, then
 // the entries sorted by column (a bitonic network over the next power of
 // two).  One warp per row; K2 entries of shared memory per warp.
-template <typename TT>
-__global__ void __launch_bounds__(128)
-distill_rows_kernel(const int64_t *__restrict__ idx, const TT *__restrict__ logits, float inv_t, float t,
-                    const float *__restrict__ lse, const float *__restrict__ dloss, LossRows r, int rows, int vocab,
-                    int K2)
+__device__ __forceinline__ void distill_rows(const PrepArgs &p, int *sc, float *sp)
 {
-    extern __shared__ unsigned char sm[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int *sc = reinterpret_cast<int *>(sm) + warp * K2;
-    float *sp = reinterpret_cast<float *>(sm) + (4 + warp) * K2;
-    const int i = blockIdx.x * 4 + warp;
-    if (i >= rows) return;
-    const int K = r.K;
-    const long base = (long)i * K;
+    const int lane = threadIdx.x & 31, K = p.r.K, K2 = p.K2;
+    const long i = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (i >= p.rows) return;
+    const long base = i * K;
     float top = -INFINITY;
     for (int k = lane; k < K2; k += 32) {
-        int c = kNoColumn;
-        float y = -INFINITY;
-        if (k < K) {
-            const int64_t e = idx[base + k];
-            const float v = to_f(logits[base + k]);
-            if (e >= 0 && e < vocab && v != -INFINITY) {
-                c = (int)e;
-                y = v * inv_t;
-            }
-        }
-        sc[k] = c;
-        sp[k] = y;
-        top = fmaxf(top, y);
+        const bool valid = k < K && teacher_valid(p, base + k);
+        sc[k] = valid ? (int)p.idx[base + k] : kNoColumn;
+        sp[k] = valid ? teacher_logit(p, base + k) * p.inv_t : -INFINITY;
+        top = fmaxf(top, sp[k]);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -121,13 +152,13 @@ distill_rows_kernel(const int64_t *__restrict__ idx, const TT *__restrict__ logi
     const float lt = logf(sum);
     float ent = 0.f;
     for (int k = lane; k < K2; k += 32) {
-        float p = 0.f;
+        float w = 0.f;
         if (sc[k] != kNoColumn) {
             const float lp = sp[k] - top - lt;
-            p = expf(lp);
-            if (p != 0.f) ent += p * lp;   // (a NaN teacher logit stays NaN)
+            w = expf(lp);
+            if (w != 0.f) ent += w * lp;   // (a NaN teacher logit stays NaN)
         }
-        sp[k] = p;
+        sp[k] = w;
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) ent += __shfl_xor_sync(0xffffffffu, ent, o);
@@ -149,25 +180,16 @@ distill_rows_kernel(const int64_t *__restrict__ idx, const TT *__restrict__ logi
             __syncwarp();
         }
     for (int k = lane; k < K; k += 32) {
-        r.col[base + k] = sc[k];
-        r.p[base + k] = sp[k];
+        p.r.col[base + k] = sc[k];
+        p.r.p[base + k] = sp[k];
     }
     if (lane == 0) {
-        r.ent[i] = ent;
-        if (dloss) {
-            const float l = lse[i];
-            r.coef[i] = any && l != -INFINITY ? t * dloss[i] : 0.f;
-            r.l2[i] = l * (1.f / kLn2);
+        p.r.ent[i] = ent;
+        if (p.dloss) {
+            p.r.coef[i] = row_factor(p, i, any);
+            p.r.l2[i] = p.lse[i] * (1.f / kLn2);
         }
     }
-}
-
-// bz[j] = bias_j log2(e) / t
-__global__ void __launch_bounds__(256) bias_scale_kernel(const float *__restrict__ bias, float alpha,
-                                                         float *__restrict__ bz, int vocab)
-{
-    const int j = blockIdx.x * 256 + threadIdx.x;
-    if (j < vocab) bz[j] = bias[j] * alpha;
 }
 
 // The bf16 parts of an element: itself, or the three parts of an fp32 value,
@@ -188,113 +210,190 @@ __device__ __forceinline__ __nv_bfloat16 next_part(float &v)
     return r;
 }
 
-// An operand of the products that the TMA unit cannot read as it lies (fp32,
-// row pitch or base not a multiple of 16 bytes): dst[part][row][dp] with
-// zeros past d.  One thread per 8 elements; HBM-bound.
+// 8 elements of a row from column c on, zeros past d
 template <typename T>
-__global__ void __launch_bounds__(256)
-operand_kernel(const T *__restrict__ src, __nv_bfloat16 *__restrict__ dst, int rows, int d, int dp, long part_stride,
-               int vec)
+__device__ __forceinline__ void load8(const T *row, int c, int d, bool vec, float (&v)[8])
+{
+    if (vec && c < d) {
+        __align__(16) T t[8];
+#pragma unroll
+        for (int j = 0; j < (int)sizeof(T) / 2; ++j)
+            reinterpret_cast<uint4 *>(t)[j] = reinterpret_cast<const uint4 *>(row + c)[j];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = to_f(t[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = c + j < d ? to_f(row[c + j]) : 0.f;
+    }
+}
+
+// dst[part][row][dp], zeros past d; one thread per 8 elements
+template <typename T>
+__device__ __forceinline__ void copy_rows(const CopyJob &c, int d, int dp, int block)
 {
     const int per = dp / 8;
-    const long n = (long)rows * per;
-    for (long x = (long)blockIdx.x * 256 + threadIdx.x; x < n; x += (long)gridDim.x * 256) {
+    const long n = (long)c.rows * per;
+    for (long x = (long)block * 256 + threadIdx.x; x < n; x += (long)c.blocks * 256) {
         const long i = x / per;
-        const int c = (int)(x - i * per) * 8;
+        const int at = (int)(x - i * per) * 8;
         float v[8];
-        if (vec) {   // 16-byte aligned rows
-            __align__(16) T t[8];
-#pragma unroll
-            for (int j = 0; j < (int)sizeof(T) / 2; ++j)
-                reinterpret_cast<uint4 *>(t)[j] = reinterpret_cast<const uint4 *>(src + i * d + c)[j];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = to_f(t[j]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = c + j < d ? to_f(src[i * d + c + j]) : 0.f;
-        }
-        const long at = i * dp + c;
+        load8(static_cast<const T *>(c.src) + i * d, at, d, c.vec, v);
 #pragma unroll
         for (int part = 0; part < (sizeof(T) == 4 ? 3 : 1); ++part) {
             __align__(16) __nv_bfloat16 b[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) b[j] = next_part<T>(v[j]);
-            *reinterpret_cast<uint4 *>(dst + part * part_stride + at) = *reinterpret_cast<const uint4 *>(b);
+            *reinterpret_cast<uint4 *>(c.dst + part * c.part_stride + i * dp + at) = *reinterpret_cast<const uint4 *>(b);
         }
     }
 }
 
-// h transposed for dW: dst[part][column][rp], rows of factor 0 as zeros
+// h transposed for dW: ht[part][column][rp], rows of factor 0 as zeros
 // whatever they hold, zeros from `rows` to rp (a multiple of 8).  64 x 64
-// elements per block through shared memory, 16 bytes per access of memory
-// (element loads where rows are not aligned); HBM-bound.
+// elements per block through shared memory (s: [part][column][65]), 16 bytes
+// per access of memory.
 template <typename T>
-__global__ void __launch_bounds__(256)
-transpose_kernel(const T *__restrict__ src, __nv_bfloat16 *__restrict__ dst, int rows, int d, long rp,
-                 long part_stride, const float *__restrict__ coef, int vec)
+__device__ __forceinline__ void transpose_rows(const PrepArgs &p, int block, __nv_bfloat16 *s, int *live)
 {
     constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
-    __shared__ __nv_bfloat16 s[kParts][64][65];   // [column][row]
-    const long i0 = (long)blockIdx.x * 64;
-    const int c0 = blockIdx.y * 64;
-#pragma unroll
+    const long i0 = (long)(block / p.t_cols) * 64;
+    const int c0 = (block % p.t_cols) * 64;
+    if (threadIdx.x < 64) {
+        const long i = i0 + threadIdx.x;
+        bool valid = false;
+        if (i < p.rows) {
+            for (int k = 0; k < p.r.K && !valid; ++k) {
+                const int64_t e = p.idx[i * p.r.K + k];
+                valid = p.logits ? teacher_valid(p, i * p.r.K + k) : e >= 0 && e < p.vocab;
+            }
+            valid = row_factor(p, i, valid) != 0.f;
+        }
+        live[threadIdx.x] = valid;
+    }
+    __syncthreads();
     for (int x = threadIdx.x; x < 512; x += 256) {
         const int y = x >> 3, c = (x & 7) * 8;
-        const long i = i0 + y;
-        float v[8];
-        const bool live = i < rows && coef[i] != 0.f;
-        if (live && vec && c0 + c < d) {
-            __align__(16) T t[8];
-#pragma unroll
-            for (int j = 0; j < (int)sizeof(T) / 2; ++j)
-                reinterpret_cast<uint4 *>(t)[j] = reinterpret_cast<const uint4 *>(src + i * d + c0 + c)[j];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = to_f(t[j]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = live && c0 + c + j < d ? to_f(src[i * d + c0 + c + j]) : 0.f;
-        }
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (live[y]) load8(static_cast<const T *>(p.h) + (i0 + y) * p.d, c0 + c, p.d, p.h_vec, v);
 #pragma unroll
         for (int part = 0; part < kParts; ++part)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s[part][c + j][y] = next_part<T>(v[j]);
+            for (int j = 0; j < 8; ++j) s[(part * 64 + c + j) * 65 + y] = next_part<T>(v[j]);
     }
     __syncthreads();
-#pragma unroll
     for (int x = threadIdx.x; x < 512; x += 256) {
         const int c = x >> 3, y = (x & 7) * 8;
-        if (c0 + c >= d || i0 + y >= rp) continue;
+        if (c0 + c >= p.d || i0 + y >= p.rp) continue;
 #pragma unroll
         for (int part = 0; part < kParts; ++part) {
             __align__(16) __nv_bfloat16 b[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) b[j] = s[part][c][y + j];
-            *reinterpret_cast<uint4 *>(dst + part * part_stride + (c0 + c) * rp + i0 + y) =
+            for (int j = 0; j < 8; ++j) b[j] = s[(part * 64 + c) * 65 + y + j];
+            *reinterpret_cast<uint4 *>(p.ht + part * p.ht_stride + (c0 + c) * p.rp + i0 + y) =
                 *reinterpret_cast<const uint4 *>(b);
         }
     }
 }
 
+template <typename T>
+__global__ void __launch_bounds__(256) loss_prep_kernel(const __grid_constant__ PrepArgs p)
+{
+    // the lists of 8 rows, or a transposed block
+    constexpr int kBlock = (sizeof(T) == 4 ? 3 : 1) * 64 * 65 * 2, kLists = 8 * kMaxTopK * 8;
+    __shared__ __align__(16) unsigned char s[kBlock > kLists ? kBlock : kLists];
+    __shared__ int live[64];
+    int b = (int)blockIdx.x;
+    if (b < p.row_blocks) {
+        if (p.logits)
+            distill_rows(p, reinterpret_cast<int *>(s) + (threadIdx.x >> 5) * p.K2,
+                         reinterpret_cast<float *>(s) + (8 + (threadIdx.x >> 5)) * p.K2);
+        else
+            xent_rows(p);
+        return;
+    }
+    b -= p.row_blocks;
+    if (b < p.bias_blocks) {   // bz[j] = bias_j log2(e) / t
+        const long j = (long)b * 256 + threadIdx.x;
+        if (j < p.vocab) p.bz[j] = p.bias[j] * p.alpha;
+        return;
+    }
+    b -= p.bias_blocks;
+    if (b < p.t_blocks) {
+        transpose_rows<T>(p, b, reinterpret_cast<__nv_bfloat16 *>(s), live);
+        return;
+    }
+    b -= p.t_blocks;
+    if (b < p.copy[0].blocks)
+        copy_rows<T>(p.copy[0], p.d, p.dp, b);
+    else
+        copy_rows<T>(p.copy[1], p.d, p.dp, b - p.copy[0].blocks);
+}
+
+// ------------------------------------------------------------ finishing
+// What follows the products of a vocabulary piece, in one launch: the column
+// sums of dz from those of its row groups, and gradients that lie in slots.
+struct SumJob {
+    const float *slot;
+    void *out;
+    int slots, rows, blocks;
+    long stride;
+};
+struct FinishArgs {
+    const float *dbpart;
+    float *db;
+    int parts, cols, db_blocks;
+    long pitch;
+    int d, dp;
+    SumJob sum[2];
+};
+
 // out[row][c] = the sum of the slots' [row][dp] partial products, in order
 template <typename T>
-__global__ void __launch_bounds__(256)
-slots_kernel(const float *__restrict__ slot, int slots, long slot_stride, T *__restrict__ out, int rows, int d, int dp)
+__device__ __forceinline__ void sum_slots(const SumJob &j, int d, int dp, int block)
 {
     const int per = (d + 3) / 4;
-    const long n = (long)rows * per;
-    for (long x = (long)blockIdx.x * 256 + threadIdx.x; x < n; x += (long)gridDim.x * 256) {
+    const long n = (long)j.rows * per;
+    for (long x = (long)block * 1024 + threadIdx.x; x < n; x += (long)j.blocks * 1024) {
         const long i = x / per;
         const int c = (int)(x - i * per) * 4;
-        float4 sum = *reinterpret_cast<const float4 *>(slot + i * dp + c);
-        for (int k = 1; k < slots; ++k) {
-            const float4 e = *reinterpret_cast<const float4 *>(slot + k * slot_stride + i * dp + c);
+        float4 sum = *reinterpret_cast<const float4 *>(j.slot + i * dp + c);
+        for (int k = 1; k < j.slots; ++k) {
+            const float4 e = *reinterpret_cast<const float4 *>(j.slot + k * j.stride + i * dp + c);
             sum.x += e.x, sum.y += e.y, sum.z += e.z, sum.w += e.w;
         }
         const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+        T *out = static_cast<T *>(j.out) + i * d + c;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (c + j < d) out[i * d + c + j] = from_f<T>(v[j]);
+        for (int y = 0; y < 4; ++y)
+            if (c + y < d) out[y] = from_f<T>(v[y]);
     }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(1024) loss_finish_kernel(const __grid_constant__ FinishArgs p)
+{
+    __shared__ float s[32][33];
+    int b = (int)blockIdx.x;
+    if (b < p.db_blocks) {   // 32 columns, 32 threads per column
+        const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+        const long j = (long)b * 32 + tx;
+        float sum = 0.f;
+        if (j < p.cols)
+            for (int x = ty; x < p.parts; x += 32) sum += p.dbpart[x * p.pitch + j];
+        s[ty][tx] = sum;
+        __syncthreads();
+        if (ty == 0 && j < p.cols) {
+            float all = 0.f;
+            for (int x = 0; x < 32; ++x) all += s[x][tx];
+            p.db[j] = all;
+        }
+        return;
+    }
+    b -= p.db_blocks;
+    if (b < p.sum[0].blocks)
+        sum_slots<T>(p.sum[0], p.d, p.dp, b);
+    else
+        sum_slots<T>(p.sum[1], p.d, p.dp, b - p.sum[0].blocks);
 }
 
 // Joins the strips of a row's softmax and its listed logits: 32 rows per
@@ -350,26 +449,6 @@ loss_merge_kernel(const float2 *__restrict__ part, int slots, const float *__res
     }
 }
 
-// db[j] = the sum of the row groups' sums: 32 columns per block, 32 threads
-// per column
-__global__ void __launch_bounds__(1024)
-dbias_kernel(const float *__restrict__ dbpart, int parts, long pitch, int cols, float *__restrict__ db)
-{
-    __shared__ float s[32][33];
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const long j = (long)blockIdx.x * 32 + tx;
-    float sum = 0.f;
-    if (j < cols)
-        for (int x = ty; x < parts; x += 32) sum += dbpart[x * pitch + j];
-    s[ty][tx] = sum;
-    __syncthreads();
-    if (ty == 0 && j < cols) {
-        float all = 0.f;
-        for (int x = 0; x < 32; ++x) all += s[x][tx];
-        db[j] = all;
-    }
-}
-
 // ---------------------------------------------------------------- host side
 bool al(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
@@ -391,16 +470,21 @@ long up(long a, long b) { return (a + b - 1) / b * b; }
 struct LossPlan {
     int parts, dp;          // bf16 parts of an element; operand row pitch (d rounded up to 8)
     bool copy_h, copy_w;
+    bool tma_out;           // TMA stores can address dh and dw
     int piece;              // vocabulary columns per piece
     int slots;              // forward: partial softmaxes per row over all pieces
-    LossTiling dh;          // of a whole piece
-    bool dh_slots;
+    bool dh_slots;          // dh of several pieces adds up in slots
+    // backward, for a whole piece and for the last one
+    struct Piece {
+        LossTiling vocab, dh, dw;
+    } whole, last;
     size_t col, p, ent, coef, l2, bz, ysel, part, h, ht, w, dz, dh_acc, dw_acc, dbpart, bytes;
 };
 
-LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool backward, bool h_ok, bool w_ok)
+// h_ok, w_ok, out_ok: 16-byte aligned bases of h, w and both of dh and dw
+LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool backward, bool h_ok, bool w_ok, bool out_ok)
 {
-    LossPlan q;
+    LossPlan q = {};
     size_t at = 0;
     auto take = [&](size_t n) {
         const size_t o = at;
@@ -414,7 +498,9 @@ LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool back
     q.copy_h = !tma || !h_ok;
     q.copy_w = !tma || !w_ok;
     // what a vocabulary column of a piece takes; pieces start at multiples of the widest tile
-    const size_t per = ((backward ? n : 0) + (q.copy_w ? (size_t)q.dp : 0)) * q.parts * 2;
+    q.tma_out = out_ok && (size_t)d * (dtype == TXL_F32 ? 4 : 2) % 16 == 0;
+    const size_t per = ((backward ? n : 0) + (q.copy_w ? (size_t)q.dp : 0)) * q.parts * 2 +
+                       (backward && !q.tma_out ? (size_t)q.dp * 4 : 0);
     size_t most = per ? (backward ? kPieceBytes : kWeightBytes) / per / kLossPieceUnit * kLossPieceUnit : (size_t)vocab;
     if (most < (size_t)kLossPieceUnit) most = kLossPieceUnit;
     if (backward)
@@ -427,13 +513,12 @@ LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool back
     q.bz = take((size_t)vocab * 4 + 256);   // read in fours past the last column
     q.h = take(q.copy_h ? n * q.dp * q.parts * 2 : 0);
     q.w = take(q.copy_w ? (size_t)q.piece * q.dp * q.parts * 2 : 0);
-    q.coef = q.l2 = q.ht = q.dz = q.dh_acc = q.dw_acc = q.dbpart = q.ysel = q.part = 0;
-    q.slots = 0;
-    q.dh_slots = false;
     if (!backward) {
-        for (long v0 = 0; v0 < vocab; v0 += q.piece)
-            q.slots += kSlotsPerStrip *
-                       vocab_strips(vocab_tiling(rows, (int)(vocab - v0 < q.piece ? vocab - v0 : q.piece), d, q.parts));
+        const int last = vocab % q.piece ? vocab % q.piece : q.piece;
+        q.whole.vocab = vocab_tiling(rows, q.piece, d, q.parts);
+        q.last.vocab = vocab_tiling(rows, last, d, q.parts);
+        const long more = (vocab - last) / q.piece;   // whole pieces before the last one
+        q.slots = kSlotsPerStrip * (int)(more * vocab_strips(q.whole.vocab) + vocab_strips(q.last.vocab));
         q.ysel = take(n * K * 4);
         q.part = take(n * q.slots * 8);
     } else {
@@ -442,15 +527,19 @@ LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool back
         q.ht = take((size_t)d * up(rows, 8) * q.parts * 2);
         q.dz = take(n * up(q.piece, 64) * q.parts * 2);
         q.dh_slots = q.piece < vocab;
-        // the last, narrower piece may split dW further
-        LossTiling dw, dh_last, dw_last;
+        // every piece splits dh alike, so that each adds to the same slots; the last, narrower one may split dW further
         const int last = vocab % q.piece ? vocab % q.piece : q.piece;
-        gradient_tiling(rows, d, q.piece, q.piece, q.parts, q.dh_slots, 0, &q.dh, &dw);
-        gradient_tiling(rows, d, last, q.piece, q.parts, q.dh_slots, q.dh.splits, &dh_last, &dw_last);
-        const size_t dw_whole = (size_t)dw.splits * q.piece, dw_rest = (size_t)dw_last.splits * last;
-        // whatever the output's alignment: the products go to the slots where TMA cannot write it
-        q.dh_acc = take((size_t)q.dh.splits * n * q.dp * 4);
-        q.dw_acc = take((dw_whole > dw_rest ? dw_whole : dw_rest) * q.dp * 4);
+        gradient_tiling(rows, d, q.piece, q.piece, q.parts, q.dh_slots, 0, &q.whole.dh, &q.whole.dw);
+        gradient_tiling(rows, d, last, q.piece, q.parts, q.dh_slots, q.whole.dh.splits, &q.last.dh, &q.last.dw);
+        q.whole.vocab = vocab_tiling(rows, q.piece, d, q.parts);
+        q.last.vocab = vocab_tiling(rows, last, d, q.parts);
+        auto dw_slots = [&](const LossTiling &t, int cols) {
+            return t.splits > 1 || !q.tma_out ? (size_t)t.splits * cols * q.dp * 4 : 0;
+        };
+        const size_t dw_whole = dw_slots(q.whole.dw, q.piece), dw_last = dw_slots(q.last.dw, last);
+        const bool dh_acc = q.dh_slots || q.whole.dh.splits > 1 || !q.tma_out;
+        q.dh_acc = take(dh_acc ? (size_t)q.whole.dh.splits * n * q.dp * 4 : 0);
+        q.dw_acc = take(dw_whole > dw_last ? dw_whole : dw_last);
         q.dbpart = take((size_t)up(rows, 32) / 32 * up(q.piece, 64) * 4);
     }
     q.bytes = at ? at : 256;
@@ -470,15 +559,16 @@ struct PlanEntry {
 PlanEntry g_plans[64];
 int g_plan_n = 0, g_plan_next = 0;
 
-LossPlan loss_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool backward, bool h_ok, bool w_ok)
+LossPlan loss_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool backward, bool h_ok, bool w_ok, bool out_ok)
 {
-    const PlanKey key = {rows, d, vocab, K, (int)dtype, backward * 4 + h_ok * 2 + w_ok, device_sm_count()};
+    const PlanKey key = {rows, d, vocab, K, (int)dtype, backward * 8 + h_ok * 4 + w_ok * 2 + out_ok,
+                         device_sm_count()};
     {
         std::lock_guard<std::mutex> lock(g_plan_mu);
         for (int x = 0; x < g_plan_n; ++x)
             if (!memcmp(&g_plans[x].key, &key, sizeof(key))) return g_plans[x].plan;
     }
-    const LossPlan plan = make_plan(rows, d, vocab, K, dtype, backward, h_ok, w_ok);
+    const LossPlan plan = make_plan(rows, d, vocab, K, dtype, backward, h_ok, w_ok, out_ok);
     std::lock_guard<std::mutex> lock(g_plan_mu);
     g_plans[g_plan_next].key = key;
     g_plans[g_plan_next].plan = plan;
@@ -492,8 +582,8 @@ size_t loss_bytes(int rows, int d, int vocab, int K, txl_dtype dtype, bool backw
 {
     size_t most = 0;
     for (int b = 0; b <= (backward ? 1 : 0); ++b)
-        for (int ok = 0; ok < 4; ++ok) {
-            const size_t n = loss_plan(rows, d, vocab, K, dtype, b, ok & 1, ok & 2).bytes;
+        for (int ok = 0; ok < (b ? 8 : 4); ++ok) {
+            const size_t n = loss_plan(rows, d, vocab, K, dtype, b, ok & 1, ok & 2, ok & 4).bytes;
             most = n > most ? n : most;
         }
     return most;
@@ -534,7 +624,8 @@ txl_status loss_workspace(int rows, int d, int vocab, int K, txl_dtype dtype, in
     return TXL_OK;
 }
 
-txl_status loss_checks(const LossArgs &a, bool backward)
+// (fills *plan when there are rows)
+txl_status loss_checks(const LossArgs &a, bool backward, LossPlan *plan)
 {
     const txl_status st = loss_sizes(a.rows, a.d, a.vocab, a.K, a.dtype);
     if (st != TXL_OK) return st;
@@ -573,9 +664,10 @@ txl_status loss_checks(const LossArgs &a, bool backward)
         for (const Buf &p : outs)
             if (&p != &o && overlap(o.p, o.bytes, p.p, p.bytes)) return TXL_ERR_INVALID;
     }
-    if (a.rows > 0 && a.ws_bytes < loss_plan(a.rows, a.d, a.vocab, a.K, a.dtype, backward, al(a.h, 16), al(a.w, 16)).bytes)
-        return TXL_ERR_INVALID;
-    return TXL_OK;
+    if (a.rows == 0) return TXL_OK;
+    *plan = loss_plan(a.rows, a.d, a.vocab, a.K, a.dtype, backward, al(a.h, 16), al(a.w, 16),
+                      backward && al(a.dh, 16) && al(a.dw, 16));
+    return a.ws_bytes < plan->bytes ? TXL_ERR_INVALID : TXL_OK;
 }
 
 float alpha_of(const LossArgs &a) { return 1.f / (kLn2 * (a.temp != 0.f ? a.temp : 1.f)); }
@@ -593,114 +685,119 @@ LossRows rows_at(const LossArgs &a, const LossPlan &q)
     return r;
 }
 
-cudaError_t launch_rows(const LossArgs &a, const LossRows &r, const LossPlan &q, bool backward)
+// blocks of a pass over n threads' work that strides over its grid
+int grid_of(long n, int threads)
 {
-    const float *lse = backward ? a.lse : nullptr, *dloss = backward ? a.dloss : nullptr;
-    if (a.temp == 0.f) {
-        xent_rows_kernel<<<(a.rows + 255) / 256, 256, 0, a.s>>>(a.idx, lse, dloss, r, a.rows, a.vocab);
-    } else {
-        int K2 = 2;
-        while (K2 < a.K) K2 <<= 1;
-        const int grid = (a.rows + 3) / 4;
-        const size_t sm = (size_t)K2 * 8 * 4;
-        if (a.t_dtype == TXL_F32)
-            distill_rows_kernel<float><<<grid, 128, sm, a.s>>>(a.idx, (const float *)a.t_logits, 1.f / a.temp, a.temp,
-                                                               lse, dloss, r, a.rows, a.vocab, K2);
-        else
-            distill_rows_kernel<__nv_bfloat16><<<grid, 128, sm, a.s>>>(a.idx, (const __nv_bfloat16 *)a.t_logits,
-                                                                       1.f / a.temp, a.temp, lse, dloss, r, a.rows,
-                                                                       a.vocab, K2);
-    }
-    if (a.bias)
-        bias_scale_kernel<<<(a.vocab + 255) / 256, 256, 0, a.s>>>(a.bias, alpha_of(a),
-                                                                  (float *)((unsigned char *)a.ws + q.bz), a.vocab);
-    return cudaGetLastError();
+    const long want = (n + threads - 1) / threads, most = 16L * device_sm_count() * 256 / threads;
+    return (int)(want < most ? want : most);
 }
 
-// a copied operand: h, or a piece of W
-cudaError_t copy_operand(const LossArgs &a, const LossPlan &q, const void *src, size_t at, int rows, long part_stride)
+CopyJob copy_job(const LossArgs &a, const LossPlan &q, const void *src, size_t at, int rows, long part_stride)
 {
-    __nv_bfloat16 *dst = (__nv_bfloat16 *)((unsigned char *)a.ws + at);
-    const long n = (long)rows * (q.dp / 8), want = (n + 255) / 256, most = 16L * device_sm_count();
-    const int grid = (int)(want < most ? want : most);
+    CopyJob c;
+    c.src = src;
+    c.dst = (__nv_bfloat16 *)((unsigned char *)a.ws + at);
+    c.rows = rows;
+    c.blocks = grid_of((long)rows * (q.dp / 8), 256);
+    c.part_stride = part_stride;
+    c.vec = a.d % 8 == 0 && al(src, 16);
+    return c;
+}
+
+cudaError_t launch_prep(const LossArgs &a, const PrepArgs &p)
+{
+    const long blocks = (long)p.row_blocks + p.bias_blocks + p.t_blocks + p.copy[0].blocks + p.copy[1].blocks;
+    if (blocks > INT32_MAX) return cudaErrorNotSupported;
     if (a.dtype == TXL_F32)
-        operand_kernel<float><<<grid, 256, 0, a.s>>>((const float *)src, dst, rows, a.d, q.dp, part_stride,
-                                                     a.d % 8 == 0 && al(src, 16));
+        loss_prep_kernel<float><<<(unsigned)blocks, 256, 0, a.s>>>(p);
     else
-        operand_kernel<__nv_bfloat16><<<grid, 256, 0, a.s>>>((const __nv_bfloat16 *)src, dst, rows, a.d, q.dp,
-                                                             part_stride, a.d % 8 == 0 && al(src, 16));
+        loss_prep_kernel<__nv_bfloat16><<<(unsigned)blocks, 256, 0, a.s>>>(p);
     return cudaGetLastError();
 }
 
-cudaError_t h_operand(const LossArgs &a, const LossPlan &q, LossMatrix *m)
-{
-    if (!q.copy_h) {
-        *m = {a.h, a.d, 0, a.rows, a.d, 1};
-        return cudaSuccess;
-    }
-    const long stride = (long)a.rows * q.dp;
-    *m = {(unsigned char *)a.ws + q.h, q.dp, stride, a.rows, q.dp, q.parts};
-    return copy_operand(a, q, a.h, q.h, a.rows, stride);
-}
-
-// h^T for dW
-cudaError_t ht_operand(const LossArgs &a, const LossPlan &q, const float *coef, LossMatrix *m)
-{
-    const long rp = up(a.rows, 8), stride = a.d * rp;
-    __nv_bfloat16 *dst = (__nv_bfloat16 *)((unsigned char *)a.ws + q.ht);
-    *m = {dst, rp, stride, a.d, (int)rp, q.parts};
-    const dim3 grid((unsigned)((a.rows + 63) / 64), (unsigned)((a.d + 63) / 64));
-    const int vec = a.d % 8 == 0 && al(a.h, 16);
-    if (grid.y > 65535) return cudaErrorNotSupported;
-    if (a.dtype == TXL_F32)
-        transpose_kernel<float><<<grid, 256, 0, a.s>>>((const float *)a.h, dst, a.rows, a.d, rp, stride, coef, vec);
-    else
-        transpose_kernel<__nv_bfloat16><<<grid, 256, 0, a.s>>>((const __nv_bfloat16 *)a.h, dst, a.rows, a.d, rp, stride,
-                                                               coef, vec);
-    return cudaGetLastError();
-}
-
-// columns v0 .. v0+cols of the vocabulary
-cudaError_t w_operand(const LossArgs &a, const LossPlan &q, long v0, int cols, LossMatrix *m)
+// columns v0 .. v0+cols of the vocabulary: where they lie, or where *copy puts them
+LossMatrix w_operand(const LossArgs &a, const LossPlan &q, long v0, int cols, CopyJob *copy)
 {
     const size_t esz = a.dtype == TXL_F32 ? 4 : 2;
     const void *src = (const unsigned char *)a.w + (size_t)v0 * a.d * esz;
-    if (!q.copy_w) {
-        *m = {src, a.d, 0, cols, a.d, 1};
-        return cudaSuccess;
-    }
+    if (!q.copy_w) return {src, a.d, 0, cols, a.d, 1};
     const long stride = (long)q.piece * q.dp;
-    *m = {(unsigned char *)a.ws + q.w, q.dp, stride, cols, q.dp, q.parts};
-    return copy_operand(a, q, src, q.w, cols, stride);
+    *copy = copy_job(a, q, src, q.w, cols, stride);
+    return {(unsigned char *)a.ws + q.w, q.dp, stride, cols, q.dp, q.parts};
 }
 
-cudaError_t sum_slots(const LossArgs &a, const LossPlan &q, const float *slot, int slots, long stride, void *out,
-                      int rows)
+// The first preparation: rows, biases, h, the vocabulary's first piece and,
+// for dW, h^T.
+cudaError_t prepare(const LossArgs &a, const LossPlan &q, const LossRows &r, bool backward, LossMatrix *h, LossMatrix *w,
+                    LossMatrix *ht)
 {
-    const long n = (long)rows * ((a.d + 3) / 4), want = (n + 255) / 256, most = 16L * device_sm_count();
-    const int grid = (int)(want < most ? want : most);
-    if (a.dtype == TXL_F32)
-        slots_kernel<float><<<grid, 256, 0, a.s>>>(slot, slots, stride, (float *)out, rows, a.d, q.dp);
-    else
-        slots_kernel<__nv_bfloat16><<<grid, 256, 0, a.s>>>(slot, slots, stride, (__nv_bfloat16 *)out, rows, a.d, q.dp);
-    return cudaGetLastError();
+    PrepArgs p;
+    memset(&p, 0, sizeof(p));
+    p.idx = a.idx;
+    p.logits = a.t_logits;
+    p.logits_f32 = a.t_dtype == TXL_F32;
+    p.t = a.temp != 0.f ? a.temp : 1.f;
+    p.inv_t = 1.f / p.t;
+    p.lse = backward ? a.lse : nullptr;
+    p.dloss = backward ? a.dloss : nullptr;
+    p.r = r;
+    p.rows = a.rows;
+    p.vocab = a.vocab;
+    for (p.K2 = 2; p.K2 < a.K;) p.K2 <<= 1;
+    p.row_blocks = a.t_logits ? (a.rows + 7) / 8 : (a.rows + 255) / 256;
+    p.bias = a.bias;
+    p.alpha = alpha_of(a);
+    p.bz = (float *)((unsigned char *)a.ws + q.bz);
+    p.bias_blocks = a.bias ? (a.vocab + 255) / 256 : 0;
+    p.d = a.d;
+    p.dp = q.dp;
+    if (q.copy_h) {
+        const long stride = (long)a.rows * q.dp;
+        p.copy[0] = copy_job(a, q, a.h, q.h, a.rows, stride);
+        *h = {p.copy[0].dst, q.dp, stride, a.rows, q.dp, q.parts};
+    } else {
+        *h = {a.h, a.d, 0, a.rows, a.d, 1};
+    }
+    *w = w_operand(a, q, 0, a.vocab < q.piece ? a.vocab : q.piece, &p.copy[1]);
+    if (ht) {
+        p.h = a.h;
+        p.h_vec = a.d % 8 == 0 && al(a.h, 16);
+        p.ht = (__nv_bfloat16 *)((unsigned char *)a.ws + q.ht);
+        p.rp = up(a.rows, 8);
+        p.ht_stride = a.d * p.rp;
+        p.t_cols = (a.d + 63) / 64;
+        const long blocks = (long)((a.rows + 63) / 64) * p.t_cols;
+        if (blocks > INT32_MAX) return cudaErrorNotSupported;
+        p.t_blocks = (int)blocks;
+        *ht = {p.ht, p.rp, p.ht_stride, a.d, (int)p.rp, q.parts};
+    }
+    return launch_prep(a, p);
 }
 
-cudaError_t run_fwd(const LossArgs &a)
+// a later piece of the vocabulary
+cudaError_t next_weights(const LossArgs &a, const LossPlan &q, long v0, int cols, LossMatrix *w)
 {
-    const LossPlan q = loss_plan(a.rows, a.d, a.vocab, a.K, a.dtype, false, al(a.h, 16), al(a.w, 16));
+    PrepArgs p;
+    memset(&p, 0, sizeof(p));
+    p.d = a.d;
+    p.dp = q.dp;
+    *w = w_operand(a, q, v0, cols, &p.copy[0]);
+    return q.copy_w ? launch_prep(a, p) : cudaSuccess;
+}
+
+cudaError_t run_fwd(const LossArgs &a, const LossPlan &q)
+{
     unsigned char *ws = (unsigned char *)a.ws;
     const LossRows r = rows_at(a, q);
     const float *bz = (const float *)(ws + q.bz);
     float2 *part = (float2 *)(ws + q.part);
     LossMatrix h, w;
-    cudaError_t e = launch_rows(a, r, q, false);
-    if (e == cudaSuccess) e = h_operand(a, q, &h);
+    cudaError_t e = prepare(a, q, r, false, &h, &w, nullptr);
     long slot = 0;
     for (long v0 = 0; e == cudaSuccess && v0 < a.vocab; v0 += q.piece) {
         const int cols = (int)(a.vocab - v0 < q.piece ? a.vocab - v0 : q.piece);
-        const LossTiling t = vocab_tiling(a.rows, cols, a.d, q.parts);
-        e = w_operand(a, q, v0, cols, &w);
+        const LossTiling t = cols == q.piece ? q.whole.vocab : q.last.vocab;
+        if (v0 > 0) e = next_weights(a, q, v0, cols, &w);
         if (e == cudaSuccess)
             e = launch_loss_lse(h, w, a.bias ? bz + v0 : nullptr, (int)v0, alpha_of(a), r, (float *)(ws + q.ysel),
                                 part + slot * a.rows, t, a.s);
@@ -724,6 +821,18 @@ LossOutput direct_out(const LossArgs &a, void *p)
     return o;
 }
 
+SumJob sum_job(const LossArgs &a, const float *slot, int slots, long stride, void *out, int rows)
+{
+    SumJob j;
+    j.slot = slot;
+    j.out = out;
+    j.slots = slots;
+    j.rows = rows;
+    j.blocks = grid_of((long)rows * ((a.d + 3) / 4), 1024);
+    j.stride = stride;
+    return j;
+}
+
 LossOutput slot_out(float *p, long pitch, long stride, bool add)
 {
     LossOutput o;
@@ -735,56 +844,47 @@ LossOutput slot_out(float *p, long pitch, long stride, bool add)
     return o;
 }
 
-cudaError_t run_bwd(const LossArgs &a)
+cudaError_t run_bwd(const LossArgs &a, const LossPlan &q)
 {
-    const LossPlan q = loss_plan(a.rows, a.d, a.vocab, a.K, a.dtype, true, al(a.h, 16), al(a.w, 16));
     unsigned char *ws = (unsigned char *)a.ws;
     const LossRows r = rows_at(a, q);
     const float *bz = (const float *)(ws + q.bz);
     const size_t esz = a.dtype == TXL_F32 ? 4 : 2;
-    const bool tma_out = ((size_t)a.d * esz) % 16 == 0;   // rows that a TMA store can address
+    const long h_stride = (long)a.rows * q.dp;
+    float *acc_h = (float *)(ws + q.dh_acc), *acc_w = (float *)(ws + q.dw_acc);
     LossMatrix h, ht, w;
-    cudaError_t e = launch_rows(a, r, q, true);
-    if (e == cudaSuccess) e = h_operand(a, q, &h);
-    if (e == cudaSuccess && a.dw) e = ht_operand(a, q, r.coef, &ht);
+    cudaError_t e = prepare(a, q, r, true, &h, &w, a.dw ? &ht : nullptr);
     for (long v0 = 0; e == cudaSuccess && v0 < a.vocab; v0 += q.piece) {
         const int cols = (int)(a.vocab - v0 < q.piece ? a.vocab - v0 : q.piece);
-        const long pitch = up(cols, 64);
+        const bool last = v0 + cols == a.vocab;
+        const LossPlan::Piece &t = cols == q.piece ? q.whole : q.last;
+        const long pitch = up(cols, 64), w_stride = (long)cols * q.dp;
         const LossMatrix dz = {ws + q.dz, pitch, (long)a.rows * pitch, a.rows, cols, q.parts};
         float *dbp = a.db ? (float *)(ws + q.dbpart) : nullptr;
-        e = w_operand(a, q, v0, cols, &w);
+        if (v0 > 0) e = next_weights(a, q, v0, cols, &w);
         if (e == cudaSuccess)
-            e = launch_loss_dz(h, w, a.bias ? bz + v0 : nullptr, (int)v0, alpha_of(a), r, dz, dbp,
-                               vocab_tiling(a.rows, cols, a.d, q.parts), a.s);
-        if (e == cudaSuccess && a.db) {
-            dbias_kernel<<<(cols + 31) / 32, 1024, 0, a.s>>>(dbp, (a.rows + 31) / 32, pitch, cols, a.db + v0);
-            e = cudaGetLastError();
-        }
-        // both gradients of the piece in one launch
+            e = launch_loss_dz(h, w, a.bias ? bz + v0 : nullptr, (int)v0, alpha_of(a), r, dz, dbp, t.vocab, a.s);
+        if (e != cudaSuccess) return e;
+        // both gradients of the piece in one launch, the longer items first
         LossContraction job[2];
         int n = 0;
-        LossTiling dh, dw;
-        gradient_tiling(a.rows, a.d, cols, q.piece, q.parts, q.dh_slots, q.dh.splits, &dh, &dw);
-        const long hs = (long)a.rows * q.dp, ws_stride = (long)cols * q.dp;
-        float *acc_h = (float *)(ws + q.dh_acc), *acc_w = (float *)(ws + q.dw_acc);
-        // every piece splits dh the same way, so that each adds to the same slots
-        const bool h_direct = !q.dh_slots && dh.splits == 1 && tma_out && al(a.dh, 16);
+        const bool h_direct = !q.dh_slots && t.dh.splits == 1 && q.tma_out;
         void *dw_out = a.dw ? (unsigned char *)a.dw + (size_t)v0 * a.d * esz : nullptr;
-        const bool w_direct = dw.splits == 1 && tma_out && al(dw_out, 16);
+        const bool w_direct = t.dw.splits == 1 && q.tma_out;
         if (a.dh) {
-            LossContraction &j = job[a.dw && dw.first ? 1 : 0];
+            LossContraction &j = job[a.dw && t.dw.first ? 1 : 0];
             ++n;
-            j.a = dh.turned ? w : dz;
-            j.b = dh.turned ? dz : w;
-            j.a_t = j.b_t = j.out_t = dh.turned;
-            j.m = dh.turned ? a.d : a.rows;
-            j.n = dh.turned ? a.rows : a.d;
+            j.a = t.dh.turned ? w : dz;
+            j.b = t.dh.turned ? dz : w;
+            j.a_t = j.b_t = j.out_t = t.dh.turned;
+            j.m = t.dh.turned ? a.d : a.rows;
+            j.n = t.dh.turned ? a.rows : a.d;
             j.k = cols;
-            j.out = h_direct ? direct_out(a, a.dh) : slot_out(acc_h, q.dp, hs, v0 > 0);
-            j.t = dh;
+            j.out = h_direct ? direct_out(a, a.dh) : slot_out(acc_h, q.dp, h_stride, v0 > 0);
+            j.t = t.dh;
         }
         if (a.dw) {
-            LossContraction &j = job[a.dh && !dw.first ? 1 : 0];
+            LossContraction &j = job[a.dh && !t.dw.first ? 1 : 0];
             ++n;
             j.a = dz;
             j.b = ht;
@@ -793,22 +893,43 @@ cudaError_t run_bwd(const LossArgs &a)
             j.m = cols;
             j.n = a.d;
             j.k = a.rows;
-            j.out = w_direct ? direct_out(a, dw_out) : slot_out(acc_w, q.dp, ws_stride, false);
-            j.t = dw;
+            j.out = w_direct ? direct_out(a, dw_out) : slot_out(acc_w, q.dp, w_stride, false);
+            j.t = t.dw;
         }
-        if (e == cudaSuccess && n) e = launch_loss_gradients(job, n, q.parts, a.s);
-        if (e == cudaSuccess && a.dh && !h_direct && v0 + cols == a.vocab)
-            e = sum_slots(a, q, acc_h, dh.splits, hs, a.dh, a.rows);
-        if (e == cudaSuccess && a.dw && !w_direct) e = sum_slots(a, q, acc_w, dw.splits, ws_stride, dw_out, cols);
+        if (n) e = launch_loss_gradients(job, n, q.parts, a.s);
+        if (e != cudaSuccess) return e;
+        FinishArgs f;
+        memset(&f, 0, sizeof(f));
+        f.d = a.d;
+        f.dp = q.dp;
+        if (a.db) {
+            f.dbpart = dbp;
+            f.db = a.db + v0;
+            f.parts = (int)(up(a.rows, 32) / 32);
+            f.cols = cols;
+            f.pitch = pitch;
+            f.db_blocks = (cols + 31) / 32;
+        }
+        if (a.dw && !w_direct) f.sum[0] = sum_job(a, acc_w, t.dw.splits, w_stride, dw_out, cols);
+        if (a.dh && !h_direct && last) f.sum[1] = sum_job(a, acc_h, t.dh.splits, h_stride, a.dh, a.rows);
+        const int blocks = f.db_blocks + f.sum[0].blocks + f.sum[1].blocks;
+        if (blocks) {
+            if (a.dtype == TXL_F32)
+                loss_finish_kernel<float><<<blocks, 1024, 0, a.s>>>(f);
+            else
+                loss_finish_kernel<__nv_bfloat16><<<blocks, 1024, 0, a.s>>>(f);
+            e = cudaGetLastError();
+        }
     }
     return e;
 }
 
 txl_status loss_fwd(const LossArgs &a)
 {
-    const txl_status st = loss_checks(a, false);
+    LossPlan q;
+    const txl_status st = loss_checks(a, false, &q);
     if (st != TXL_OK || a.rows == 0) return st;
-    const cudaError_t e = run_fwd(a);
+    const cudaError_t e = run_fwd(a, q);
     if (e == cudaSuccess) return TXL_OK;
     note_cuda_error(e);
     return TXL_ERR_CUDA;
@@ -816,14 +937,15 @@ txl_status loss_fwd(const LossArgs &a)
 
 txl_status loss_bwd(const LossArgs &a)
 {
-    const txl_status st = loss_checks(a, true);
+    LossPlan q;
+    const txl_status st = loss_checks(a, true, &q);
     if (st != TXL_OK) return st;
     cudaError_t e = cudaSuccess;
     if (a.rows == 0) {   // sums over no rows
         if (a.dw) e = cudaMemsetAsync(a.dw, 0, (size_t)a.vocab * a.d * (a.dtype == TXL_F32 ? 4 : 2), a.s);
         if (e == cudaSuccess && a.db) e = cudaMemsetAsync(a.db, 0, (size_t)a.vocab * 4, a.s);
     } else if (a.dh || a.dw || a.db) {
-        e = run_bwd(a);
+        e = run_bwd(a, q);
     }
     if (e == cudaSuccess) return TXL_OK;
     note_cuda_error(e);
