@@ -229,12 +229,6 @@ __device__ __forceinline__ void st_shared16(uint32_t at, float x)
 {
     asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(__bfloat16_as_ushort(__float2bfloat16(x))) : "memory");
 }
-__device__ __forceinline__ float4 ld_shared(uint32_t at)
-{
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
-    return v;
-}
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float r;
@@ -294,6 +288,31 @@ __device__ __forceinline__ void l_tmem_issue(uint32_t taddr, float (&v)[32])
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr)
         : "memory");
+}
+// The same 32 lanes x 32 columns as 8 x 8 blocks spread over the warp (the
+// 16x256b shape): thread l holds rows l / 4 + 8 r and columns 8 i + 2 (l % 4)
+// + e in v[16 (r / 2) + 4 i + 2 (r % 2) + e], r, i < 4.
+__device__ __forceinline__ void l_tmem_issue_blocks(uint32_t taddr, float (&v)[32])
+{
+    uint32_t *r = reinterpret_cast<uint32_t *>(v);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(r[16 * h + 0]), "=r"(r[16 * h + 1]), "=r"(r[16 * h + 2]), "=r"(r[16 * h + 3]), "=r"(r[16 * h + 4]),
+              "=r"(r[16 * h + 5]), "=r"(r[16 * h + 6]), "=r"(r[16 * h + 7]), "=r"(r[16 * h + 8]), "=r"(r[16 * h + 9]),
+              "=r"(r[16 * h + 10]), "=r"(r[16 * h + 11]), "=r"(r[16 * h + 12]), "=r"(r[16 * h + 13]),
+              "=r"(r[16 * h + 14]), "=r"(r[16 * h + 15])
+            : "r"(taddr + ((uint32_t)(16 * h) << 16))
+            : "memory");
+}
+// four 8 x 8 blocks of bf16 to shared memory; thread l addresses row l % 8 of block l / 8
+__device__ __forceinline__ void st_blocks(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
 }
 __device__ __forceinline__ void l_tmem_wait(float (&v)[32])
 {
@@ -580,16 +599,14 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
         // =================================================================== epilogue
         const int q = warp & 3, half = (warp - 4) >> 2;
         // staging: STG buffers of 32 rows x 128 bytes per warp, used in turn
-        // (with column sums of dz the second one is their scratch)
         const uint32_t stg0 = sbase + S::OST + (uint32_t)(warp - 4) * 4096u;
-        const bool sums = MODE == MODE_DZ && p.dbpart != nullptr;
         uint32_t stg_a = stg0;
         int nst = 0;
         int lt = 0;
         bool ok = true;
         // the next staging buffer, once the store that last used it has read it
         auto stage_wait = [&]() {
-            if (S::STG == 2 && !sums) {
+            if (S::STG == 2) {
                 stg_a = stg0 + ((nst++ & 1) ? LEPI * 4096u : 0u);
                 if (lane == 0) bulk_wait_read_1();
             } else if (lane == 0) {
@@ -646,6 +663,116 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                     dead = __any_sync(0xffffffffu, coef == 0.f);
                 }
             }
+            // dz: a thread's four rows of the 8 x 8 blocks
+            float bc[4], bl[4];
+            if (MODE == MODE_DZ) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    bc[r] = __shfl_sync(0xffffffffu, coef, (lane >> 2) + 8 * r);
+                    bl[r] = __shfl_sync(0xffffffffu, l2, (lane >> 2) + 8 * r);
+                }
+            }
+            auto process_dz = [&](float (&v)[32], const float2 (&bz)[4], int n0, int sub) {
+                if (n0 >= p.N) return;
+                const int col0 = p.v0 + n0, c2 = 2 * (lane & 3);   // columns n0 + 8 i + c2 + {0, 1}
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint64_t b2 = pair(bz[i].x, bz[i].y);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        float &x = v[16 * (r >> 1) + 4 * i + 2 * (r & 1)], &y = v[16 * (r >> 1) + 4 * i + 2 * (r & 1) + 1];
+                        const uint64_t off = pair(-bl[r], -bl[r]);
+                        float a, b;
+                        unpair(fma2(pair(x, y), alpha2, kBias ? add2(b2, off) : off), a, b);
+                        unpair(mul2(pair(ex2(a), ex2(b)), pair(bc[r], bc[r])), x, y);
+                    }
+                }
+                if (dead) {   // whatever an empty row holds
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (bc[r] == 0.f) {
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) v[16 * (r >> 1) + 4 * (x >> 1) + 2 * (r & 1) + (x & 1)] = 0.f;
+                        }
+                }
+                if (n0 + 32 > p.N) {   // columns past the vocabulary
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        if (n0 + 8 * ((x >> 2) & 3) + c2 + (x & 1) >= p.N) v[x] = 0.f;
+                }
+                // listed columns: every row's next one at a time, applied one by
+                // one by the threads that hold them
+                while (cur.c0 < col0) cur.next();
+                __syncwarp();
+                while (unsigned hit = __ballot_sync(0xffffffffu, cur.c0 < col0 + 32)) {
+                    const float mine = coef == 0.f ? 0.f : coef * cur.p0;
+                    const int mc = cur.c0 - col0;
+                    if ((hit >> lane) & 1) cur.next();
+                    __syncwarp();
+                    for (; hit; hit &= hit - 1) {
+                        const int src = __ffs(hit) - 1, c = __shfl_sync(0xffffffffu, mc, src);
+                        const float g = __shfl_sync(0xffffffffu, mine, src);
+                        const bool holds = g != 0.f && (lane >> 2) == (src & 7) && (lane & 3) == ((c >> 1) & 3);
+                        const uint64_t g2 = pair(holds && !(c & 1) ? -g : 0.f, holds && (c & 1) ? -g : 0.f);
+                        const int at = 4 * (src >> 3) + (c >> 3);
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) {
+                            const int e = 16 * (x >> 3) + 4 * (x & 3) + 2 * ((x >> 2) & 1);
+                            if (x == at) unpair(add2(pair(v[e], v[e + 1]), g2), v[e], v[e + 1]);
+                        }
+                    }
+                }
+                if (p.dbpart) {
+                    // column sums over the warp's 32 rows: 4 in the thread, 8 by halving exchanges
+                    // over the threads of a column, which leave one column in each thread
+                    float s[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        const int at = 4 * (x >> 1) + (x & 1);
+                        s[x] = (v[at] + v[at + 2]) + (v[at + 16] + v[at + 18]);
+                    }
+#pragma unroll
+                    for (int o = 4; o; o >>= 1) {
+                        const bool up = lane & (4 * o);
+#pragma unroll
+                        for (int x = 0; x < o; ++x) {
+                            const float send = up ? s[x] : s[x + o], keep = up ? s[x + o] : s[x];
+                            s[x] = keep + __shfl_xor_sync(0xffffffffu, send, 4 * o);
+                        }
+                    }
+                    // (columns past the last one lie in the row's padding)
+                    if (row0 < p.M)
+                        p.dbpart[(long)(row0 >> 5) * p.dbpitch + n0 + 8 * (lane >> 3) + c2 + ((lane >> 2) & 1)] = s[0];
+                }
+#pragma unroll
+                for (int part = 0; part < (kParts ? 3 : 1); ++part) {
+                    if (kParts || sub == 0) stage_wait();
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        uint32_t w4[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float &a = v[16 * (r >> 1) + 4 * i + 2 * (r & 1)], &b = v[16 * (r >> 1) + 4 * i + 2 * (r & 1) + 1];
+                            w4[i] = pack2(a, b);
+                            if (kParts) {
+                                a -= top_part(a);
+                                b -= top_part(b);
+                            }
+                        }
+                        // rows of 128 bytes (64 per part of fp32) and their swizzles
+                        const int y = 8 * r + (lane & 7), i = lane >> 3;
+                        st_blocks(kParts ? stg_a + y * 64 + ((i ^ ((y >> 1) & 3)) << 4)
+                                         : stg_a + y * 128 + (((4 * sub + i) ^ (y & 7)) << 4),
+                                  w4[0], w4[1], w4[2], w4[3]);
+                    }
+                    if (kParts) {
+                        if (row0 < p.M) store(0, n0, row0, part, false);
+                    } else if ((sub == 1 || n0 + 32 >= p.N) && row0 < p.M) {
+                        // the second half of the chunk may lie past the last column
+                        store(0, n0 - 32 * sub, row0, 0, false);
+                    }
+                }
+            };
             // 32 columns from n0 on (the second half of their 64-column chunk with sub = 1)
             auto process = [&](float (&v)[32], int n0, int sub) {
                 if (MODE == MODE_CT) {
@@ -684,19 +811,13 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                 }
                 if (n0 >= p.N) return;
                 const int col0 = p.v0 + n0;
-                // y = alpha z + bz in base-2 units (dz: less the row's lse)
+                // y = alpha z + bz in base-2 units
                 if (kBias) {
-                    const uint64_t off = pair(-l2, -l2);
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
                         const float4 b4 = __ldg(reinterpret_cast<const float4 *>(p.bz + n0 + j));
-                        uint64_t b01 = pair(b4.x, b4.y), b23 = pair(b4.z, b4.w);
-                        if (MODE == MODE_DZ) {
-                            b01 = add2(b01, off);
-                            b23 = add2(b23, off);
-                        }
-                        unpair(fma2(pair(v[j], v[j + 1]), alpha2, b01), v[j], v[j + 1]);
-                        unpair(fma2(pair(v[j + 2], v[j + 3]), alpha2, b23), v[j + 2], v[j + 3]);
+                        unpair(fma2(pair(v[j], v[j + 1]), alpha2, pair(b4.x, b4.y)), v[j], v[j + 1]);
+                        unpair(fma2(pair(v[j + 2], v[j + 3]), alpha2, pair(b4.z, b4.w)), v[j + 2], v[j + 3]);
                     }
                 }
                 if (n0 + 32 > p.N) {   // columns past the vocabulary
@@ -704,121 +825,56 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                     for (int j = 0; j < 32; ++j)
                         if (n0 + j >= p.N) v[j] = -INFINITY;
                 }
-                if (MODE == MODE_LSE) {
-                    while (cur.c0 < col0 + 32) {
-                        if (cur.c0 >= col0) {
-                            float y = 0.f;
+                while (cur.c0 < col0 + 32) {
+                    if (cur.c0 >= col0) {
+                        float y = 0.f;
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) y = cur.c0 == col0 + j ? v[j] : y;
-                            p.ysel[(long)row * p.r.K + cur.pos] = y * mscale;
-                        }
-                        cur.next();
+                        for (int j = 0; j < 32; ++j) y = cur.c0 == col0 + j ? v[j] : y;
+                        p.ysel[(long)row * p.r.K + cur.pos] = y * mscale;
                     }
-                    __syncwarp();
-                    const float cm = max32(v, m), ref = cm == -INFINITY ? 0.f : cm;
-                    const uint64_t off = pair(-ref * mscale, -ref * mscale), one = pair(mscale, mscale);
-                    uint64_t s[4] = {0, 0, 0, 0};
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float a, b;
-                        const uint64_t x = pair(v[2 * j], v[2 * j + 1]);
-                        unpair(kBias ? add2(x, off) : fma2(x, one, off), a, b);
-                        s[j & 3] = add2(s[j & 3], pair(ex2(a), ex2(b)));
-                    }
-                    float a, b;
-                    unpair(add2(add2(s[0], s[1]), add2(s[2], s[3])), a, b);
-                    l = fmaf(l, ex2((m - ref) * mscale), a + b);
-                    m = cm;
-                } else {
-                    const uint64_t off = pair(-l2, -l2), c2 = pair(coef, coef);
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        float a = v[j], b = v[j + 1];
-                        if (!kBias) unpair(fma2(pair(a, b), alpha2, off), a, b);
-                        unpair(mul2(pair(ex2(a), ex2(b)), c2), v[j], v[j + 1]);
-                    }
-                    while (cur.c0 < col0 + 32) {
-                        if (cur.c0 >= col0) {
-                            const float g = coef * cur.p0;
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (cur.c0 == col0 + j) v[j] -= g;
-                        }
-                        cur.next();
-                    }
-                    __syncwarp();
-                    if (dead) {   // whatever an empty row holds
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = coef == 0.f ? 0.f : v[j];
-                    }
-                    if (sums) {
-                        // column sums over the warp's 32 rows through the scratch
-                        // buffer: each thread adds 8 rows of 4 columns, two
-                        // exchanges join the four groups of rows
-                        const uint32_t scr = stg0 + LEPI * 4096u;
-                        __syncwarp();
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            st_shared(scr + lane * 128 + ((j ^ (lane & 7)) << 4), __float_as_uint(v[4 * j]),
-                                      __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
-                                      __float_as_uint(v[4 * j + 3]));
-                        __syncwarp();
-                        const int c4 = lane & 7, r0 = (lane >> 3) * 8;
-                        float4 x = ld_shared(scr + r0 * 128 + (c4 << 4));
-                        uint64_t lo = pair(x.x, x.y), hi = pair(x.z, x.w);
-#pragma unroll
-                        for (int r = 1; r < 8; ++r) {
-                            x = ld_shared(scr + (r0 + r) * 128 + ((c4 ^ r) << 4));
-                            lo = add2(lo, pair(x.x, x.y));
-                            hi = add2(hi, pair(x.z, x.w));
-                        }
-                        unpair(lo, x.x, x.y);
-                        unpair(hi, x.z, x.w);
-#pragma unroll
-                        for (int o = 8; o < 32; o <<= 1) {
-                            x.x += __shfl_xor_sync(0xffffffffu, x.x, o);
-                            x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
-                            x.z += __shfl_xor_sync(0xffffffffu, x.z, o);
-                            x.w += __shfl_xor_sync(0xffffffffu, x.w, o);
-                        }
-                        // (columns past the last one lie in the row's padding)
-                        if (lane < 8 && row0 < p.M)
-                            *reinterpret_cast<float4 *>(p.dbpart + (long)(row0 >> 5) * p.dbpitch + n0 + 4 * c4) = x;
-                    }
-                    if (!kParts) {
-                        if (sub == 0) stage_wait();
-                        stage_bf16(v, sub);
-                        // the second half of the chunk may lie past the last column
-                        if ((sub == 1 || n0 + 32 >= p.N) && row0 < p.M) store(0, n0 - 32 * sub, row0, 0, false);
-                    } else {
-                        float rest[32];
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) rest[j] = v[j];
-#pragma unroll
-                        for (int part = 0; part < 3; ++part) {
-                            stage_wait();
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                uint32_t w4[4];
-#pragma unroll
-                                for (int x = 0; x < 4; ++x) {
-                                    const float a = rest[8 * j + 2 * x], b = rest[8 * j + 2 * x + 1];
-                                    const float ta = top_part(a), tb = top_part(b);
-                                    w4[x] = pack2(ta, tb);
-                                    rest[8 * j + 2 * x] = a - ta;
-                                    rest[8 * j + 2 * x + 1] = b - tb;
-                                }
-                                // 64-byte rows, their swizzle: chunk c of row r at c ^ (r / 2 % 4)
-                                st_shared(stg_a + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), w4[0], w4[1], w4[2], w4[3]);
-                            }
-                            if (row0 < p.M) store(0, n0, row0, part, false);
-                        }
-                    }
+                    cur.next();
                 }
+                __syncwarp();
+                const float cm = max32(v, m), ref = cm == -INFINITY ? 0.f : cm;
+                const uint64_t off = pair(-ref * mscale, -ref * mscale), one = pair(mscale, mscale);
+                uint64_t s[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    float a, b;
+                    const uint64_t x = pair(v[2 * j], v[2 * j + 1]);
+                    unpair(kBias ? add2(x, off) : fma2(x, one, off), a, b);
+                    s[j & 3] = add2(s[j & 3], pair(ex2(a), ex2(b)));
+                }
+                float a, b;
+                unpair(add2(add2(s[0], s[1]), add2(s[2], s[3])), a, b);
+                l = fmaf(l, ex2((m - ref) * mscale), a + b);
+                m = cm;
+            };
+            auto issue = [&](uint32_t taddr, float (&v)[32]) {
+                if (MODE == MODE_DZ)
+                    l_tmem_issue_blocks(taddr, v);
+                else
+                    l_tmem_issue(taddr, v);
+            };
+            // dz: the biases of a thread's columns, asked for ahead of their use
+            auto biases = [&](float2 (&bz)[4], int n0) {
+                if (MODE != MODE_DZ || !kBias) return;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    bz[i] = n0 < p.N ? __ldg(reinterpret_cast<const float2 *>(p.bz + n0 + 8 * i + 2 * (lane & 3)))
+                                     : make_float2(0.f, 0.f);
+            };
+            auto work = [&](float (&v)[32], const float2 (&bz)[4], int n0, int sub) {
+                if (MODE == MODE_DZ)
+                    process_dz(v, bz, n0, sub);
+                else
+                    process(v, n0, sub);
             };
             const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16);
             for (int nt = t.nt0; ok && nt < t.nt1; ++nt) {
                 float v0[32], v1[32];
+                float2 b0[4], b1[4];
+                biases(b0, nt * t.bn + 64 * half);
                 if (kParts) {
                     // this half's 64 columns, summed over the steps
 #pragma unroll
@@ -832,10 +888,12 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                         if (half < nch) {
                             const uint32_t at = tq + (uint32_t)((lt & 1) * 256 + 64 * half);
                             float x[32];
-                            tmem_ld32(at, x);
+                            issue(at, x);
+                            l_tmem_wait(x);
 #pragma unroll
                             for (int j = 0; j < 32; ++j) v0[j] += x[j];
-                            tmem_ld32(at + 32u, x);
+                            issue(at + 32u, x);
+                            l_tmem_wait(x);
 #pragma unroll
                             for (int j = 0; j < 32; ++j) v1[j] += x[j];
                         }
@@ -843,8 +901,9 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                     }
                     if (!ok) break;
                     if (half < nch) {
-                        process(v0, nt * t.bn + 64 * half, 0);
-                        process(v1, nt * t.bn + 64 * half + 32, 1);
+                        biases(b1, nt * t.bn + 64 * half + 32);
+                        work(v0, b0, nt * t.bn + 64 * half, 0);
+                        work(v1, b1, nt * t.bn + 64 * half + 32, 1);
                     }
                     continue;
                 }
@@ -855,7 +914,7 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                 }
                 ++lt;
                 tc_fence_after();
-                if (kBias && nt + 1 < t.nt1 && 32 * lane < t.bn && (nt + 1) * t.bn + 32 * lane < t.N)   // the next tile's biases
+                if (MODE == MODE_LSE && kBias && nt + 1 < t.nt1 && 32 * lane < t.bn && (nt + 1) * t.bn + 32 * lane < t.N)   // the next tile's biases
                     asm volatile("prefetch.global.L1 [%0];" ::"l"(p.bz + (nt + 1) * t.bn + 32 * lane));
                 if (half >= nch) {
                     release(buf);
@@ -863,18 +922,20 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                 }
                 // each load is in flight while the columns before it are worked on
                 const uint32_t tacc = tq + (uint32_t)(buf * 256);
-                l_tmem_issue(tacc + 64u * half, v0);
+                issue(tacc + 64u * half, v0);
                 l_tmem_wait(v0);
                 for (int c = half; c < nch; c += 2) {
                     const int n0 = nt * t.bn + 64 * c;
-                    l_tmem_issue(tacc + 64u * c + 32u, v1);
-                    process(v0, n0, 0);
+                    issue(tacc + 64u * c + 32u, v1);
+                    biases(b1, n0 + 32);
+                    work(v0, b0, n0, 0);
                     l_tmem_wait(v1);
                     if (c + 2 < nch)
-                        l_tmem_issue(tacc + 64u * (c + 2), v0);
+                        issue(tacc + 64u * (c + 2), v0);
                     else
                         release(buf);
-                    process(v1, n0 + 32, 1);
+                    if (c + 2 < nch) biases(b0, n0 + 128);
+                    work(v1, b1, n0 + 32, 1);
                     if (c + 2 < nch) l_tmem_wait(v0);
                 }
             }
