@@ -434,6 +434,7 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
 {
     using S = LSmem<CG, MODE, kParts>;
     constexpr int ST = S::ST;
+    loss_kernel_begin();
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -484,6 +485,7 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
     l_cluster_sync<CG>();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
+    loss_kernel_wait();
     const int G = (int)gridDim.x / CG, c0 = (int)blockIdx.x / CG;
 
     if (warp == 0) {
@@ -875,7 +877,7 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                 float v0[32], v1[32];
                 float2 b0[4], b1[4];
                 biases(b0, nt * t.bn + 64 * half);
-                if (kParts) {
+                if constexpr (kParts) {
                     // this half's 64 columns, summed over the steps
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v0[j] = v1[j] = 0.f;
@@ -905,38 +907,38 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                         work(v0, b0, nt * t.bn + 64 * half, 0);
                         work(v1, b1, nt * t.bn + 64 * half + 32, 1);
                     }
-                    continue;
-                }
-                const int buf = lt & 1;
-                if (!wait(S::AFULL + buf, (lt >> 1) & 1)) {
-                    ok = false;
-                    break;
-                }
-                ++lt;
-                tc_fence_after();
-                if (MODE == MODE_LSE && kBias && nt + 1 < t.nt1 && 32 * lane < t.bn && (nt + 1) * t.bn + 32 * lane < t.N)   // the next tile's biases
-                    asm volatile("prefetch.global.L1 [%0];" ::"l"(p.bz + (nt + 1) * t.bn + 32 * lane));
-                if (half >= nch) {
-                    release(buf);
-                    continue;
-                }
-                // each load is in flight while the columns before it are worked on
-                const uint32_t tacc = tq + (uint32_t)(buf * 256);
-                issue(tacc + 64u * half, v0);
-                l_tmem_wait(v0);
-                for (int c = half; c < nch; c += 2) {
-                    const int n0 = nt * t.bn + 64 * c;
-                    issue(tacc + 64u * c + 32u, v1);
-                    biases(b1, n0 + 32);
-                    work(v0, b0, n0, 0);
-                    l_tmem_wait(v1);
-                    if (c + 2 < nch)
-                        issue(tacc + 64u * (c + 2), v0);
-                    else
+                } else {
+                    const int buf = lt & 1;
+                    if (!wait(S::AFULL + buf, (lt >> 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    ++lt;
+                    tc_fence_after();
+                    if (MODE == MODE_LSE && kBias && nt + 1 < t.nt1 && 32 * lane < t.bn && (nt + 1) * t.bn + 32 * lane < t.N)   // the next tile's biases
+                        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.bz + (nt + 1) * t.bn + 32 * lane));
+                    if (half >= nch) {
                         release(buf);
-                    if (c + 2 < nch) biases(b0, n0 + 128);
-                    work(v1, b1, n0 + 32, 1);
-                    if (c + 2 < nch) l_tmem_wait(v0);
+                        continue;
+                    }
+                    // each load is in flight while the columns before it are worked on
+                    const uint32_t tacc = tq + (uint32_t)(buf * 256);
+                    issue(tacc + 64u * half, v0);
+                    l_tmem_wait(v0);
+                    for (int c = half; c < nch; c += 2) {
+                        const int n0 = nt * t.bn + 64 * c;
+                        issue(tacc + 64u * c + 32u, v1);
+                        biases(b1, n0 + 32);
+                        work(v0, b0, n0, 0);
+                        l_tmem_wait(v1);
+                        if (c + 2 < nch)
+                            issue(tacc + 64u * (c + 2), v0);
+                        else
+                            release(buf);
+                        if (c + 2 < nch) biases(b0, n0 + 128);
+                        work(v1, b1, n0 + 32, 1);
+                        if (c + 2 < nch) l_tmem_wait(v0);
+                    }
                 }
             }
             if (MODE == MODE_LSE && ok && live)
@@ -997,25 +999,24 @@ cudaError_t l_launch(const LMaps &maps, const LParams &p, cudaStream_t s)
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorNotSupported;
-    cudaLaunchConfig_t cfg;
-    memset(&cfg, 0, sizeof(cfg));
-    cfg.blockDim = dim3(LNT);
-    cfg.dynamicSmemBytes = LSmem<CG, MODE, kParts>::TOTAL;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = CG;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
+    const size_t smem = LSmem<CG, MODE, kParts>::TOTAL;
     int n = most[dev].load(std::memory_order_relaxed);
     if (n == 0) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LSmem<CG, MODE, kParts>::TOTAL);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
         n = device_sm_count() / CG;
         if (CG == 2) {
             // an odd SM of a GPC takes no pair
+            cudaLaunchAttribute at[1];
+            at[0].id = cudaLaunchAttributeClusterDimension;
+            at[0].val.clusterDim.x = CG;
+            at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3((unsigned)(CG * n));
+            cfg.blockDim = dim3(LNT);
+            cfg.dynamicSmemBytes = smem;
+            cfg.attrs = at;
+            cfg.numAttrs = 1;
             int fit = 0;
             e = cudaOccupancyMaxActiveClusters(&fit, kern, &cfg);
             if (e != cudaSuccess) return e;
@@ -1023,8 +1024,7 @@ cudaError_t l_launch(const LMaps &maps, const LParams &p, cudaStream_t s)
         }
         most[dev].store(n, std::memory_order_relaxed);
     }
-    cfg.gridDim = dim3((unsigned)(CG * (p.items < n ? p.items : n)));
-    return cudaLaunchKernelEx(&cfg, kern, maps, p);
+    return loss_launch(kern, (unsigned)(CG * (p.items < n ? p.items : n)), LNT, smem, CG, s, maps, p);
 }
 
 template <int MODE, bool kBias>

@@ -302,6 +302,8 @@ __global__ void __launch_bounds__(256) loss_prep_kernel(const __grid_constant__ 
     constexpr int kBlock = (sizeof(T) == 4 ? 3 : 1) * 64 * 65 * 2, kLists = 8 * kMaxTopK * 8;
     __shared__ __align__(16) unsigned char s[kBlock > kLists ? kBlock : kLists];
     __shared__ int live[64];
+    loss_kernel_begin();
+    loss_kernel_wait();
     int b = (int)blockIdx.x;
     if (b < p.row_blocks) {
         if (p.logits)
@@ -373,6 +375,8 @@ template <typename T>
 __global__ void __launch_bounds__(1024) loss_finish_kernel(const __grid_constant__ FinishArgs p)
 {
     __shared__ float s[32][33];
+    loss_kernel_begin();
+    loss_kernel_wait();
     int b = (int)blockIdx.x;
     if (b < p.db_blocks) {   // 32 columns, 32 threads per column
         const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
@@ -404,6 +408,8 @@ loss_merge_kernel(const float2 *__restrict__ part, int slots, const float *__res
                   float *__restrict__ loss, float *__restrict__ lse, int rows)
 {
     __shared__ float sm[32][33], sl[32][33];
+    loss_kernel_begin();
+    loss_kernel_wait();
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const long i = (long)blockIdx.x * 32 + tx;
     float m = -INFINITY, l = 0.f;
@@ -708,11 +714,8 @@ cudaError_t launch_prep(const LossArgs &a, const PrepArgs &p)
 {
     const long blocks = (long)p.row_blocks + p.bias_blocks + p.t_blocks + p.copy[0].blocks + p.copy[1].blocks;
     if (blocks > INT32_MAX) return cudaErrorNotSupported;
-    if (a.dtype == TXL_F32)
-        loss_prep_kernel<float><<<(unsigned)blocks, 256, 0, a.s>>>(p);
-    else
-        loss_prep_kernel<__nv_bfloat16><<<(unsigned)blocks, 256, 0, a.s>>>(p);
-    return cudaGetLastError();
+    return loss_launch(a.dtype == TXL_F32 ? loss_prep_kernel<float> : loss_prep_kernel<__nv_bfloat16>, (unsigned)blocks,
+                       256, 0, 1, a.s, p);
 }
 
 // columns v0 .. v0+cols of the vocabulary: where they lie, or where *copy puts them
@@ -805,9 +808,8 @@ cudaError_t run_fwd(const LossArgs &a, const LossPlan &q)
     }
     if (e != cudaSuccess) return e;
     const float t2 = a.temp != 0.f ? a.temp * a.temp : 1.f;
-    loss_merge_kernel<<<(a.rows + 31) / 32, 1024, 0, a.s>>>(part, q.slots, (const float *)(ws + q.ysel), r, t2, a.loss,
-                                                            a.lse_out, a.rows);
-    return cudaGetLastError();
+    return loss_launch(loss_merge_kernel, (unsigned)((a.rows + 31) / 32), 1024, 0, 1, a.s, (const float2 *)part, q.slots,
+                       (const float *)(ws + q.ysel), r, t2, a.loss, a.lse_out, a.rows);
 }
 
 LossOutput direct_out(const LossArgs &a, void *p)
@@ -913,13 +915,9 @@ cudaError_t run_bwd(const LossArgs &a, const LossPlan &q)
         if (a.dw && !w_direct) f.sum[0] = sum_job(a, acc_w, t.dw.splits, w_stride, dw_out, cols);
         if (a.dh && !h_direct && last) f.sum[1] = sum_job(a, acc_h, t.dh.splits, h_stride, a.dh, a.rows);
         const int blocks = f.db_blocks + f.sum[0].blocks + f.sum[1].blocks;
-        if (blocks) {
-            if (a.dtype == TXL_F32)
-                loss_finish_kernel<float><<<blocks, 1024, 0, a.s>>>(f);
-            else
-                loss_finish_kernel<__nv_bfloat16><<<blocks, 1024, 0, a.s>>>(f);
-            e = cudaGetLastError();
-        }
+        if (blocks)
+            e = loss_launch(a.dtype == TXL_F32 ? loss_finish_kernel<float> : loss_finish_kernel<__nv_bfloat16>,
+                            (unsigned)blocks, 1024, 0, 1, a.s, f);
     }
     return e;
 }
