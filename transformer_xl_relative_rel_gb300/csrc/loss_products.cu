@@ -79,7 +79,10 @@ struct LSmem {
 struct LJob {
     int M, N, bn, tiles_m, tiles_n, ksteps, splits, items;
     int a_mn, b_mn;           // operands stored with the output index innermost
+    int bn_last;              // the last column tile's width
     int f32, add, out_t;      // out_t: element (m, n) goes to row n, column m
+    void *out;                // where TMA stores cannot write (else NULL)
+    long pitch;
 };
 struct LMaps {
     CUtensorMap a[2], b[2], o[2];
@@ -329,7 +332,7 @@ __device__ __forceinline__ void l_tmem_wait(float (&v)[32])
 // ------------------------------------------------------------------- items
 struct LItem {
     int m0, nt0, nt1, ks0, ks1, split, strip;
-    int job, M, N, bn, a_mn, b_mn, f32, add, out_t;
+    int job, M, N, n0, bn, a_mn, b_mn, f32, add, out_t;
 };
 // The i-th item of tile slot c0 of G, or -1.  Items go round the slots; where
 // job 0's do not come out even, the slots left without one (r .. G-1) take
@@ -370,7 +373,8 @@ __device__ __forceinline__ LItem l_item(const LParams &p, int item)
         t.strip = 0;
         t.M = j.M;
         t.N = j.N;
-        t.bn = j.bn;
+        t.n0 = n * j.bn;
+        t.bn = n + 1 < j.tiles_n ? j.bn : j.bn_last;
         t.a_mn = j.a_mn;
         t.b_mn = j.b_mn;
         t.out_t = j.out_t;
@@ -387,6 +391,7 @@ __device__ __forceinline__ LItem l_item(const LParams &p, int item)
         t.split = t.job = t.a_mn = t.b_mn = t.f32 = t.add = t.out_t = 0;
         t.M = p.M;
         t.N = p.N;
+        t.n0 = t.nt0 * p.bn;
         t.bn = p.bn;
     }
     return t;
@@ -498,10 +503,12 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                 const CUtensorMap *ma = &maps.a[t.job], *mb = &maps.b[t.job];
                 const int bcols = t.bn / CG;                          // this CTA's columns of B
                 const int nb = (bcols + 63) / 64;                     // MN-major B: blocks of 64 columns
-                const uint32_t bytes = (S::ASZ + (t.b_mn ? (uint32_t)nb * 8192u : (uint32_t)bcols * 128u)) * CG;
+                // K-major B: a box as high as the widest tile's share, whatever this tile uses of it
+                const int box = (MODE == MODE_CT ? (t.job ? p.job[1].bn : p.job[0].bn) : p.bn) / CG;
+                const uint32_t bytes = (S::ASZ + (t.b_mn ? (uint32_t)nb * 8192u : (uint32_t)box * 128u)) * CG;
                 const int m0 = t.m0 + rank * 128;
                 for (int nt = t.nt0; ok && nt < t.nt1; ++nt) {
-                    const int n0 = nt * t.bn + rank * bcols;
+                    const int n0 = t.n0 + (nt - t.nt0) * t.bn + rank * bcols;
                     for (int ks = t.ks0; ok && ks < t.ks1; ++ks) {
                         for (int part = 0; part < (kParts ? 3 : 1); ++part, ++it) {
                             const int s = it % ST;
@@ -775,6 +782,32 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                     }
                 }
             };
+            // the staging buffer to rows that TMA stores cannot address: `high` rows of `wide` bytes
+            // (128 swizzled, else as they are), to row y and column x on, within `cols` columns
+            auto store_rows = [&](int x, int y, int high, int wide, int rows, int cols) {
+                const LJob &j = t.job ? p.job[1] : p.job[0];
+                const int esz = t.f32 ? 4 : 2, words = wide / 4, per = 32 / words;
+                __syncwarp();
+                for (int r0 = 0; r0 < high; r0 += per) {
+                    const int r = r0 + lane / words, w = lane % words;
+                    const bool sw = !t.out_t && wide == 128;
+                    const uint32_t at = stg_a + r * wide + (sw ? (((w >> 2) ^ (r & 7)) << 4) + (w & 3) * 4 : w * 4);
+                    uint32_t v;
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+                    if (y + r >= rows) continue;
+                    unsigned char *row = static_cast<unsigned char *>(j.out) + ((long)(y + r) * j.pitch + x) * esz;
+                    if (t.f32) {
+                        if (x + w < cols) reinterpret_cast<uint32_t *>(row)[w] = v;
+                    } else if (((j.pitch | (long)reinterpret_cast<uintptr_t>(j.out) / 2) & 1) == 0 && x + 2 * w + 1 < cols) {
+                        reinterpret_cast<uint32_t *>(row)[w] = v;
+                    } else {
+                        if (x + 2 * w < cols) reinterpret_cast<uint16_t *>(row)[2 * w] = (uint16_t)v;
+                        if (x + 2 * w + 1 < cols) reinterpret_cast<uint16_t *>(row)[2 * w + 1] = (uint16_t)(v >> 16);
+                    }
+                }
+                __syncwarp();
+            };
+            const bool by_tma = MODE != MODE_CT || (t.job ? p.job[1].out : p.job[0].out) == nullptr;
             // 32 columns from n0 on (the second half of their 64-column chunk with sub = 1)
             auto process = [&](float (&v)[32], int n0, int sub) {
                 if (MODE == MODE_CT) {
@@ -786,12 +819,20 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                             stage_wait();
 #pragma unroll
                             for (int j = 0; j < 32; ++j) st_shared32(stg_a + 128 * j + 4 * lane, v[j]);
-                            store(t.job, row0, n0, t.split, t.add);
+                            if (by_tma)
+                                store(t.job, row0, n0, t.split, t.add);
+                            else
+                                store_rows(row0, n0, 32, 128, t.N, t.M);
                         } else {
                             if (sub == 0) stage_wait();
 #pragma unroll
                             for (int j = 0; j < 32; ++j) st_shared16(stg_a + 64 * (32 * sub + j) + 2 * lane, v[j]);
-                            if (sub == 1) store(t.job, row0, n0 - 32, 0, false);
+                            if (sub == 1) {
+                                if (by_tma)
+                                    store(t.job, row0, n0 - 32, 0, false);
+                                else
+                                    store_rows(row0, n0 - 32, 64, 64, t.N, t.M);
+                            }
                         }
                         return;
                     }
@@ -803,11 +844,19 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                             st_shared(stg_a + lane * 128 + ((j ^ (lane & 7)) << 4), __float_as_uint(v[4 * j]),
                                       __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
                                       __float_as_uint(v[4 * j + 3]));
-                        store(t.job, n0, row0, t.split, t.add);
+                        if (by_tma)
+                            store(t.job, n0, row0, t.split, t.add);
+                        else
+                            store_rows(n0, row0, 32, 128, t.M, t.N);
                     } else {
                         if (sub == 0) stage_wait();
                         stage_bf16(v, sub);
-                        if (sub == 1) store(t.job, n0 - 32, row0, 0, false);
+                        if (sub == 1) {
+                            if (by_tma)
+                                store(t.job, n0 - 32, row0, 0, false);
+                            else
+                                store_rows(n0 - 32, row0, 32, 128, t.M, t.N);
+                        }
                     }
                     return;
                 }
@@ -860,11 +909,12 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
             };
             // dz: the biases of a thread's columns, asked for ahead of their use
             auto biases = [&](float2 (&bz)[4], int n0) {
-                if (MODE != MODE_DZ || !kBias) return;
+                if constexpr (MODE == MODE_DZ && kBias) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    bz[i] = n0 < p.N ? __ldg(reinterpret_cast<const float2 *>(p.bz + n0 + 8 * i + 2 * (lane & 3)))
-                                     : make_float2(0.f, 0.f);
+                    for (int i = 0; i < 4; ++i)
+                        bz[i] = n0 < p.N ? __ldg(reinterpret_cast<const float2 *>(p.bz + n0 + 8 * i + 2 * (lane & 3)))
+                                         : make_float2(0.f, 0.f);
+                }
             };
             auto work = [&](float (&v)[32], const float2 (&bz)[4], int n0, int sub) {
                 if (MODE == MODE_DZ)
@@ -876,7 +926,7 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
             for (int nt = t.nt0; ok && nt < t.nt1; ++nt) {
                 float v0[32], v1[32];
                 float2 b0[4], b1[4];
-                biases(b0, nt * t.bn + 64 * half);
+                biases(b0, t.n0 + (nt - t.nt0) * t.bn + 64 * half);
                 if constexpr (kParts) {
                     // this half's 64 columns, summed over the steps
 #pragma unroll
@@ -903,9 +953,9 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                     }
                     if (!ok) break;
                     if (half < nch) {
-                        biases(b1, nt * t.bn + 64 * half + 32);
-                        work(v0, b0, nt * t.bn + 64 * half, 0);
-                        work(v1, b1, nt * t.bn + 64 * half + 32, 1);
+                        biases(b1, t.n0 + (nt - t.nt0) * t.bn + 64 * half + 32);
+                        work(v0, b0, t.n0 + (nt - t.nt0) * t.bn + 64 * half, 0);
+                        work(v1, b1, t.n0 + (nt - t.nt0) * t.bn + 64 * half + 32, 1);
                     }
                 } else {
                     const int buf = lt & 1;
@@ -926,7 +976,7 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                     issue(tacc + 64u * half, v0);
                     l_tmem_wait(v0);
                     for (int c = half; c < nch; c += 2) {
-                        const int n0 = nt * t.bn + 64 * c;
+                        const int n0 = t.n0 + (nt - t.nt0) * t.bn + 64 * c;
                         issue(tacc + 64u * c + 32u, v1);
                         biases(b1, n0 + 32);
                         work(v0, b0, n0, 0);
@@ -1098,7 +1148,8 @@ void job_tiles(LossTiling &t, int m, int n, int cg, int parts)
     t.cg = cg;
     t.tiles_m = (int)cdiv(m, 128 * cg);
     t.tiles_n = (int)cdiv(n, parts == 3 ? 128 : 256);
-    t.bn = (int)(cdiv(cdiv(n, t.tiles_n), 64) * 64);
+    const int widest = parts == 3 ? 128 : 256;
+    t.bn = n >= widest ? widest : (int)(cdiv(n, 64) * 64);   // the last column tile may be narrower
     t.strip = 1;
     t.splits = 1;
     t.turned = t.first = false;
@@ -1146,11 +1197,14 @@ double gradient_tiling(int rows, int d, int cols, int whole, int parts, bool dh_
     job_tiles(turned, d, rows, cg, parts);
     job_tiles(*dh, rows, d, cg, parts);
     turned.turned = true;
-    if ((double)turned.tiles_m * turned.tiles_n * turned.bn <= kMnB * dh->tiles_m * dh->tiles_n * dh->bn) *dh = turned;
+    if ((double)turned.tiles_m * cdiv(rows, 64) <= kMnB * dh->tiles_m * cdiv(d, 64)) *dh = turned;
     job_tiles(*dw, cols, d, cg, parts);
     const long slots = device_sm_count() / cg;
     const long n0 = (long)dh->tiles_m * dh->tiles_n, n1 = (long)dw->tiles_m * dw->tiles_n;
-    const double s0 = step_us(dh->bn, parts) * (dh->turned ? 1.0 : kMnB), s1 = step_us(dw->bn, parts);
+    // a step of an average column tile
+    auto wide = [](int n, const LossTiling &t) { return (int)(cdiv(n, 64) * 64 / t.tiles_n); };
+    const double s0 = step_us(wide(dh->turned ? rows : d, *dh), parts) * (dh->turned ? 1.0 : kMnB);
+    const double s1 = step_us(wide(d, *dw), parts);
     const long k0 = cdiv(cols, LK), k1 = cdiv(rows, LK), kw = cdiv(whole, LK);
     double best = 1e300;
     static const int cand[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32, 48, 64};
@@ -1252,6 +1306,7 @@ cudaError_t launch_loss_gradients(const LossContraction *jobs, int n, int parts,
         j.M = c.m;
         j.N = c.n;
         j.bn = c.t.bn;
+        j.bn_last = (int)(cdiv(c.n - (long)(c.t.tiles_n - 1) * c.t.bn, 64) * 64);
         j.tiles_m = c.t.tiles_m;
         j.tiles_n = c.t.tiles_n;
         j.ksteps = (int)cdiv(c.k, LK);
@@ -1267,7 +1322,10 @@ cudaError_t launch_loss_gradients(const LossContraction *jobs, int n, int parts,
         j.items = (int)mine;
         cudaError_t e = l_in_map(&maps.a[x], c.a, c.a_t ? 64 : 128);
         if (e == cudaSuccess) e = l_in_map(&maps.b[x], c.b, c.b_t ? j.bn / c.t.cg : 64);
-        if (e == cudaSuccess)
+        if (!c.out.tma) {
+            j.out = c.out.base;
+            j.pitch = c.out.pitch;
+        } else if (e == cudaSuccess)
             e = l_map(&maps.o[x], c.out.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                       c.out.f32 ? 4 : 2, c.out.base, c.out_t ? c.m : c.n, c.out_t ? c.n : c.m, j.splits, c.out.pitch,
                       c.out.slot_stride, c.out.f32 || c.out_t ? 32 : 64, c.out_t && !c.out.f32 ? 64 : 32,

@@ -103,6 +103,7 @@ struct LossOutput {
     void *base;
     long pitch, slot_stride;
     bool f32, add;
+    bool tma;           // rows that TMA stores can address (slots are); else elements are stored one or two at a time
 };
 struct LossContraction {
     LossMatrix a, b;

@@ -63,7 +63,7 @@ struct CopyJob {
     __nv_bfloat16 *dst;
     int rows, blocks;
     long part_stride;
-    int vec;              // 16-byte aligned rows
+    int vec;
 };
 struct PrepArgs {
     const int64_t *idx;
@@ -210,11 +210,19 @@ __device__ __forceinline__ __nv_bfloat16 next_part(float &v)
     return r;
 }
 
-// 8 elements of a row from column c on, zeros past d
+// 8 elements of a row from column c on, zeros past d; vec: bytes at a time
+// that the rows' alignment and length allow (16, 4 or an element)
 template <typename T>
-__device__ __forceinline__ void load8(const T *row, int c, int d, bool vec, float (&v)[8])
+__device__ __forceinline__ void load8(const T *row, int c, int d, int vec, float (&v)[8])
 {
-    if (vec && c < d) {
+    if (sizeof(T) == 2 && vec == 4) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            const uint32_t w = c + j < d ? *reinterpret_cast<const uint32_t *>(row + c + j) : 0u;
+            v[j] = __uint_as_float(w << 16);
+            v[j + 1] = __uint_as_float(w & 0xffff0000u);
+        }
+    } else if (vec == 16 && c < d) {
         __align__(16) T t[8];
 #pragma unroll
         for (int j = 0; j < (int)sizeof(T) / 2; ++j)
@@ -400,39 +408,45 @@ __global__ void __launch_bounds__(1024) loss_finish_kernel(const __grid_constant
         sum_slots<T>(p.sum[1], p.d, p.dp, b - p.sum[0].blocks);
 }
 
-// Joins the strips of a row's softmax and its listed logits: 32 rows per
-// block (coalesced over rows), 32 threads of a column of the block share a
-// row's slots and entries.
+// Joins the strips of a row's softmax and its listed logits: kRows rows per
+// block (coalesced over rows), 1024 / kRows threads share a row's slots, then
+// a warp its entries.  8 rows where there are few, so that more SMs read.
+template <int kRows>
 __global__ void __launch_bounds__(1024)
 loss_merge_kernel(const float2 *__restrict__ part, int slots, const float *__restrict__ ysel, LossRows r, float t2,
                   float *__restrict__ loss, float *__restrict__ lse, int rows)
 {
-    __shared__ float sm[32][33], sl[32][33];
+    constexpr int kLanes = 1024 / kRows;
+    __shared__ float sm[kRows][kLanes + 1], sl[kRows][kLanes + 1];
     loss_kernel_begin();
     loss_kernel_wait();
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const long i = (long)blockIdx.x * 32 + tx;
-    float m = -INFINITY, l = 0.f;
-    if (i < rows)
-        for (int x = ty; x < slots; x += 32) {
-            const float2 e = part[(long)x * rows + i];
-            const float mm = fmaxf(m, e.x), ref = mm == -INFINITY ? 0.f : mm;
-            l = l * exp2f(m - ref) + e.y * exp2f(e.x - ref);
-            m = mm;
+    {
+        const int tx = threadIdx.x % kRows, ty = threadIdx.x / kRows;
+        const long i = (long)blockIdx.x * kRows + tx;
+        float m = -INFINITY, l = 0.f;
+        if (i < rows) {
+#pragma unroll 4
+            for (int x = ty; x < slots; x += kLanes) {
+                const float2 e = part[(long)x * rows + i];
+                const float mm = fmaxf(m, e.x), ref = mm == -INFINITY ? 0.f : mm;
+                l = l * exp2f(m - ref) + e.y * exp2f(e.x - ref);
+                m = mm;
+            }
         }
-    sm[ty][tx] = m;
-    sl[ty][tx] = l;
+        sm[tx][ty] = m;
+        sl[tx][ty] = l;
+    }
     __syncthreads();
-    // warp ty takes row ty of the block: lane tx one thread's part of it
-    const long row = (long)blockIdx.x * 32 + ty;
-    if (row >= rows) return;
-    m = sm[tx][ty];
-    l = sl[tx][ty];
-    float mm = m;
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const long row = (long)blockIdx.x * kRows + ty;
+    if (ty >= kRows || row >= rows) return;
+    float mm = -INFINITY;
+    for (int x = tx; x < kLanes; x += 32) mm = fmaxf(mm, sm[ty][x]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
     const float ref = mm == -INFINITY ? 0.f : mm;
-    l *= exp2f(m - ref);
+    float l = 0.f;
+    for (int x = tx; x < kLanes; x += 32) l += sl[ty][x] * exp2f(sm[ty][x] - ref);
 #pragma unroll
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     const float y_lse = ref + log2f(l);
@@ -476,7 +490,6 @@ long up(long a, long b) { return (a + b - 1) / b * b; }
 struct LossPlan {
     int parts, dp;          // bf16 parts of an element; operand row pitch (d rounded up to 8)
     bool copy_h, copy_w;
-    bool tma_out;           // TMA stores can address dh and dw
     int piece;              // vocabulary columns per piece
     int slots;              // forward: partial softmaxes per row over all pieces
     bool dh_slots;          // dh of several pieces adds up in slots
@@ -487,8 +500,8 @@ struct LossPlan {
     size_t col, p, ent, coef, l2, bz, ysel, part, h, ht, w, dz, dh_acc, dw_acc, dbpart, bytes;
 };
 
-// h_ok, w_ok, out_ok: 16-byte aligned bases of h, w and both of dh and dw
-LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool backward, bool h_ok, bool w_ok, bool out_ok)
+// h_ok, w_ok: 16-byte aligned bases of h and w
+LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool backward, bool h_ok, bool w_ok)
 {
     LossPlan q = {};
     size_t at = 0;
@@ -504,9 +517,7 @@ LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool back
     q.copy_h = !tma || !h_ok;
     q.copy_w = !tma || !w_ok;
     // what a vocabulary column of a piece takes; pieces start at multiples of the widest tile
-    q.tma_out = out_ok && (size_t)d * (dtype == TXL_F32 ? 4 : 2) % 16 == 0;
-    const size_t per = ((backward ? n : 0) + (q.copy_w ? (size_t)q.dp : 0)) * q.parts * 2 +
-                       (backward && !q.tma_out ? (size_t)q.dp * 4 : 0);
+    const size_t per = ((backward ? n : 0) + (q.copy_w ? (size_t)q.dp : 0)) * q.parts * 2;
     size_t most = per ? (backward ? kPieceBytes : kWeightBytes) / per / kLossPieceUnit * kLossPieceUnit : (size_t)vocab;
     if (most < (size_t)kLossPieceUnit) most = kLossPieceUnit;
     if (backward)
@@ -540,11 +551,10 @@ LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool back
         q.whole.vocab = vocab_tiling(rows, q.piece, d, q.parts);
         q.last.vocab = vocab_tiling(rows, last, d, q.parts);
         auto dw_slots = [&](const LossTiling &t, int cols) {
-            return t.splits > 1 || !q.tma_out ? (size_t)t.splits * cols * q.dp * 4 : 0;
+            return t.splits > 1 ? (size_t)t.splits * cols * q.dp * 4 : 0;
         };
         const size_t dw_whole = dw_slots(q.whole.dw, q.piece), dw_last = dw_slots(q.last.dw, last);
-        const bool dh_acc = q.dh_slots || q.whole.dh.splits > 1 || !q.tma_out;
-        q.dh_acc = take(dh_acc ? (size_t)q.whole.dh.splits * n * q.dp * 4 : 0);
+        q.dh_acc = take(q.dh_slots || q.whole.dh.splits > 1 ? (size_t)q.whole.dh.splits * n * q.dp * 4 : 0);
         q.dw_acc = take(dw_whole > dw_last ? dw_whole : dw_last);
         q.dbpart = take((size_t)up(rows, 32) / 32 * up(q.piece, 64) * 4);
     }
@@ -565,16 +575,15 @@ struct PlanEntry {
 PlanEntry g_plans[64];
 int g_plan_n = 0, g_plan_next = 0;
 
-LossPlan loss_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool backward, bool h_ok, bool w_ok, bool out_ok)
+LossPlan loss_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool backward, bool h_ok, bool w_ok)
 {
-    const PlanKey key = {rows, d, vocab, K, (int)dtype, backward * 8 + h_ok * 4 + w_ok * 2 + out_ok,
-                         device_sm_count()};
+    const PlanKey key = {rows, d, vocab, K, (int)dtype, backward * 4 + h_ok * 2 + w_ok, device_sm_count()};
     {
         std::lock_guard<std::mutex> lock(g_plan_mu);
         for (int x = 0; x < g_plan_n; ++x)
             if (!memcmp(&g_plans[x].key, &key, sizeof(key))) return g_plans[x].plan;
     }
-    const LossPlan plan = make_plan(rows, d, vocab, K, dtype, backward, h_ok, w_ok, out_ok);
+    const LossPlan plan = make_plan(rows, d, vocab, K, dtype, backward, h_ok, w_ok);
     std::lock_guard<std::mutex> lock(g_plan_mu);
     g_plans[g_plan_next].key = key;
     g_plans[g_plan_next].plan = plan;
@@ -588,8 +597,8 @@ size_t loss_bytes(int rows, int d, int vocab, int K, txl_dtype dtype, bool backw
 {
     size_t most = 0;
     for (int b = 0; b <= (backward ? 1 : 0); ++b)
-        for (int ok = 0; ok < (b ? 8 : 4); ++ok) {
-            const size_t n = loss_plan(rows, d, vocab, K, dtype, b, ok & 1, ok & 2, ok & 4).bytes;
+        for (int ok = 0; ok < 4; ++ok) {
+            const size_t n = loss_plan(rows, d, vocab, K, dtype, b, ok & 1, ok & 2).bytes;
             most = n > most ? n : most;
         }
     return most;
@@ -671,8 +680,7 @@ txl_status loss_checks(const LossArgs &a, bool backward, LossPlan *plan)
             if (&p != &o && overlap(o.p, o.bytes, p.p, p.bytes)) return TXL_ERR_INVALID;
     }
     if (a.rows == 0) return TXL_OK;
-    *plan = loss_plan(a.rows, a.d, a.vocab, a.K, a.dtype, backward, al(a.h, 16), al(a.w, 16),
-                      backward && al(a.dh, 16) && al(a.dw, 16));
+    *plan = loss_plan(a.rows, a.d, a.vocab, a.K, a.dtype, backward, al(a.h, 16), al(a.w, 16));
     return a.ws_bytes < plan->bytes ? TXL_ERR_INVALID : TXL_OK;
 }
 
@@ -698,6 +706,8 @@ int grid_of(long n, int threads)
     return (int)(want < most ? want : most);
 }
 
+int load_width(const LossArgs &a, const void *p) { return a.d % 8 == 0 && al(p, 16) ? 16 : a.d % 2 == 0 && al(p, 4) ? 4 : 1; }
+
 CopyJob copy_job(const LossArgs &a, const LossPlan &q, const void *src, size_t at, int rows, long part_stride)
 {
     CopyJob c;
@@ -706,7 +716,7 @@ CopyJob copy_job(const LossArgs &a, const LossPlan &q, const void *src, size_t a
     c.rows = rows;
     c.blocks = grid_of((long)rows * (q.dp / 8), 256);
     c.part_stride = part_stride;
-    c.vec = a.d % 8 == 0 && al(src, 16);
+    c.vec = load_width(a, src);
     return c;
 }
 
@@ -764,7 +774,7 @@ cudaError_t prepare(const LossArgs &a, const LossPlan &q, const LossRows &r, boo
     *w = w_operand(a, q, 0, a.vocab < q.piece ? a.vocab : q.piece, &p.copy[1]);
     if (ht) {
         p.h = a.h;
-        p.h_vec = a.d % 8 == 0 && al(a.h, 16);
+        p.h_vec = load_width(a, a.h);
         p.ht = (__nv_bfloat16 *)((unsigned char *)a.ws + q.ht);
         p.rp = up(a.rows, 8);
         p.ht_stride = a.d * p.rp;
@@ -808,8 +818,10 @@ cudaError_t run_fwd(const LossArgs &a, const LossPlan &q)
     }
     if (e != cudaSuccess) return e;
     const float t2 = a.temp != 0.f ? a.temp * a.temp : 1.f;
-    return loss_launch(loss_merge_kernel, (unsigned)((a.rows + 31) / 32), 1024, 0, 1, a.s, (const float2 *)part, q.slots,
-                       (const float *)(ws + q.ysel), r, t2, a.loss, a.lse_out, a.rows);
+    const int per = a.rows <= 2048 ? 8 : 32;
+    return loss_launch(per == 8 ? loss_merge_kernel<8> : loss_merge_kernel<32>, (unsigned)((a.rows + per - 1) / per), 1024,
+                       0, 1, a.s, (const float2 *)part, q.slots, (const float *)(ws + q.ysel), r, t2, a.loss, a.lse_out,
+                       a.rows);
 }
 
 LossOutput direct_out(const LossArgs &a, void *p)
@@ -820,6 +832,7 @@ LossOutput direct_out(const LossArgs &a, void *p)
     o.slot_stride = 0;
     o.f32 = a.dtype == TXL_F32;
     o.add = false;
+    o.tma = (size_t)a.d * (o.f32 ? 4 : 2) % 16 == 0 && al(p, 16);
     return o;
 }
 
@@ -843,6 +856,7 @@ LossOutput slot_out(float *p, long pitch, long stride, bool add)
     o.slot_stride = stride;
     o.f32 = true;
     o.add = add;
+    o.tma = true;
     return o;
 }
 
@@ -870,9 +884,9 @@ cudaError_t run_bwd(const LossArgs &a, const LossPlan &q)
         // both gradients of the piece in one launch, the longer items first
         LossContraction job[2];
         int n = 0;
-        const bool h_direct = !q.dh_slots && t.dh.splits == 1 && q.tma_out;
+        const bool h_direct = !q.dh_slots && t.dh.splits == 1;
         void *dw_out = a.dw ? (unsigned char *)a.dw + (size_t)v0 * a.d * esz : nullptr;
-        const bool w_direct = t.dw.splits == 1 && q.tma_out;
+        const bool w_direct = t.dw.splits == 1;
         if (a.dh) {
             LossContraction &j = job[a.dw && t.dw.first ? 1 : 0];
             ++n;
