@@ -92,7 +92,7 @@ struct LParams {
     int items;
     // vocabulary passes
     int M, N, bn, tiles_m, tiles_n, strip, ksteps;
-    const float *bz;          // [columns], biases in base-2 units; -infinity takes a column out
+    const float *bias;        // [columns]; -infinity takes a column out
     int v0;
     float alpha;
     LossRows r;
@@ -409,9 +409,22 @@ struct Cursor {
         c = in ? __ldg(col + at) : kNoColumn;
         w = in && p ? __ldg(p + at) : 0.f;
     }
-    // the first entry of a column >= from
-    __device__ __forceinline__ void seek(int from)
+    // the row's first entry of a column >= from
+    __device__ __forceinline__ void seek(const LossRows &r, long row, bool live, bool weights, int from)
     {
+        K = 0;
+        pos = 0;
+        c0 = c1 = kNoColumn;
+        p0 = 1.f;
+        if (!live) return;
+        if (r.target) {
+            const int y = target_column(r, row);
+            if (y >= from) c0 = y;
+            return;
+        }
+        K = r.K;
+        col = r.col + row * K;
+        p = weights ? r.p + row * K : nullptr;
         int lo = 0, hi = K;
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
@@ -648,9 +661,6 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
             if (lane == 0) l_arrive_leader<CG>(bar(S::AEMPTY + buf));
         };
         const uint64_t alpha2 = pair(p.alpha, p.alpha);
-        // without biases the running maximum is kept of the unscaled logits
-        const float mscale = kBias ? 1.f : p.alpha;
-
         for (int i = 0, item; ok && (item = l_next<MODE>(p, c0, G, i)) >= 0; ++i) {
             const LItem t = l_item<CG, MODE>(p, item);
             const int row0 = t.m0 + rank * 128 + 32 * q, row = row0 + lane;
@@ -660,14 +670,13 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
             Cursor cur;
             bool dead = false;
             if (MODE != MODE_CT) {
-                cur.K = live ? p.r.K : 0;
-                cur.col = p.r.col + (long)(live ? row : 0) * p.r.K;
-                cur.p = MODE == MODE_DZ ? p.r.p + (long)(live ? row : 0) * p.r.K : nullptr;
-                cur.seek(p.v0 + t.nt0 * t.bn);
+                cur.seek(p.r, row, live, MODE == MODE_DZ, p.v0 + t.n0);
                 if (MODE == MODE_DZ) {
                     if (live) {
-                        coef = p.r.coef[row];
-                        l2 = p.r.l2[row];
+                        // (a list's valid entries come first)
+                        const bool any = (p.r.target ? target_column(p.r, row) : __ldg(p.r.col + (long)row * p.r.K)) != kNoColumn;
+                        coef = row_factor(p.r, row, any);
+                        l2 = p.r.lse[row] * (1.f / kLn2);
                     }
                     dead = __any_sync(0xffffffffu, coef == 0.f);
                 }
@@ -681,18 +690,18 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                     bl[r] = __shfl_sync(0xffffffffu, l2, (lane >> 2) + 8 * r);
                 }
             }
-            auto process_dz = [&](float (&v)[32], const float2 (&bz)[4], int n0, int sub) {
+            auto process_dz = [&](float (&v)[32], const float2 (&bias)[4], int n0, int sub) {
                 if (n0 >= p.N) return;
                 const int col0 = p.v0 + n0, c2 = 2 * (lane & 3);   // columns n0 + 8 i + c2 + {0, 1}
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint64_t b2 = pair(bz[i].x, bz[i].y);
+                    const uint64_t b2 = pair(bias[i].x, bias[i].y);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         float &x = v[16 * (r >> 1) + 4 * i + 2 * (r & 1)], &y = v[16 * (r >> 1) + 4 * i + 2 * (r & 1) + 1];
                         const uint64_t off = pair(-bl[r], -bl[r]);
                         float a, b;
-                        unpair(fma2(pair(x, y), alpha2, kBias ? add2(b2, off) : off), a, b);
+                        unpair(fma2(kBias ? add2(pair(x, y), b2) : pair(x, y), alpha2, off), a, b);
                         unpair(mul2(pair(ex2(a), ex2(b)), pair(bc[r], bc[r])), x, y);
                     }
                 }
@@ -862,13 +871,19 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                 }
                 if (n0 >= p.N) return;
                 const int col0 = p.v0 + n0;
-                // y = alpha z + bz in base-2 units
+                // logits; the running maximum is kept of these, unscaled
                 if (kBias) {
+                    if (n0 + 32 <= p.N) {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float4 b4 = __ldg(reinterpret_cast<const float4 *>(p.bz + n0 + j));
-                        unpair(fma2(pair(v[j], v[j + 1]), alpha2, pair(b4.x, b4.y)), v[j], v[j + 1]);
-                        unpair(fma2(pair(v[j + 2], v[j + 3]), alpha2, pair(b4.z, b4.w)), v[j + 2], v[j + 3]);
+                        for (int j = 0; j < 32; j += 4) {
+                            const float4 b4 = __ldg(reinterpret_cast<const float4 *>(p.bias + n0 + j));
+                            unpair(add2(pair(v[j], v[j + 1]), pair(b4.x, b4.y)), v[j], v[j + 1]);
+                            unpair(add2(pair(v[j + 2], v[j + 3]), pair(b4.z, b4.w)), v[j + 2], v[j + 3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (n0 + j < p.N) v[j] += __ldg(p.bias + n0 + j);
                     }
                 }
                 if (n0 + 32 > p.N) {   // columns past the vocabulary
@@ -881,24 +896,24 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                         float y = 0.f;
 #pragma unroll
                         for (int j = 0; j < 32; ++j) y = cur.c0 == col0 + j ? v[j] : y;
-                        p.ysel[(long)row * p.r.K + cur.pos] = y * mscale;
+                        p.ysel[(long)row * p.r.K + cur.pos] = y * p.alpha;
                     }
                     cur.next();
                 }
                 __syncwarp();
-                const float cm = max32(v, m), ref = cm == -INFINITY ? 0.f : cm;
-                const uint64_t off = pair(-ref * mscale, -ref * mscale), one = pair(mscale, mscale);
+                // (no reference of -infinity, nor one that scaling makes so: the type's lowest value)
+                const float cm = max32(v, m), ref = cm * p.alpha == -INFINITY ? 0.f : cm;
+                const uint64_t off = pair(-ref * p.alpha, -ref * p.alpha);
                 uint64_t s[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     float a, b;
-                    const uint64_t x = pair(v[2 * j], v[2 * j + 1]);
-                    unpair(kBias ? add2(x, off) : fma2(x, one, off), a, b);
+                    unpair(fma2(pair(v[2 * j], v[2 * j + 1]), alpha2, off), a, b);
                     s[j & 3] = add2(s[j & 3], pair(ex2(a), ex2(b)));
                 }
                 float a, b;
                 unpair(add2(add2(s[0], s[1]), add2(s[2], s[3])), a, b);
-                l = fmaf(l, ex2((m - ref) * mscale), a + b);
+                l = fmaf(l, ex2((m - ref) * p.alpha), a + b);
                 m = cm;
             };
             auto issue = [&](uint32_t taddr, float (&v)[32]) {
@@ -908,17 +923,19 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                     l_tmem_issue(taddr, v);
             };
             // dz: the biases of a thread's columns, asked for ahead of their use
-            auto biases = [&](float2 (&bz)[4], int n0) {
+            auto biases = [&](float2 (&b)[4], int n0) {
                 if constexpr (MODE == MODE_DZ && kBias) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        bz[i] = n0 < p.N ? __ldg(reinterpret_cast<const float2 *>(p.bz + n0 + 8 * i + 2 * (lane & 3)))
-                                         : make_float2(0.f, 0.f);
+                    for (int i = 0; i < 4; ++i) {
+                        const int n = n0 + 8 * i + 2 * (lane & 3);
+                        b[i] = n + 1 < p.N ? __ldg(reinterpret_cast<const float2 *>(p.bias + n))
+                                           : make_float2(n < p.N ? __ldg(p.bias + n) : 0.f, 0.f);
+                    }
                 }
             };
-            auto work = [&](float (&v)[32], const float2 (&bz)[4], int n0, int sub) {
+            auto work = [&](float (&v)[32], const float2 (&b)[4], int n0, int sub) {
                 if (MODE == MODE_DZ)
-                    process_dz(v, bz, n0, sub);
+                    process_dz(v, b, n0, sub);
                 else
                     process(v, n0, sub);
             };
@@ -966,7 +983,7 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                     ++lt;
                     tc_fence_after();
                     if (MODE == MODE_LSE && kBias && nt + 1 < t.nt1 && 32 * lane < t.bn && (nt + 1) * t.bn + 32 * lane < t.N)   // the next tile's biases
-                        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.bz + (nt + 1) * t.bn + 32 * lane));
+                        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.bias + (nt + 1) * t.bn + 32 * lane));
                     if (half >= nch) {
                         release(buf);
                         continue;
@@ -992,7 +1009,7 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                 }
             }
             if (MODE == MODE_LSE && ok && live)
-                p.part[(long)(kSlotsPerStrip * t.strip + half) * p.M + row] = make_float2(m * mscale, l);
+                p.part[(long)(kSlotsPerStrip * t.strip + half) * p.M + row] = make_float2(m * p.alpha, l);
         }
         if (lane == 0) bulk_wait_all();
         __syncwarp();
@@ -1088,7 +1105,7 @@ cudaError_t l_launch_cg(int cg, int parts, const LMaps &maps, const LParams &p, 
 long cdiv(long a, long b) { return (a + b - 1) / b; }
 
 // the fields the two vocabulary passes share
-cudaError_t vocab_params(LParams &p, LMaps &maps, const LossMatrix &h, const LossMatrix &w, const float *bz, int v0,
+cudaError_t vocab_params(LParams &p, LMaps &maps, const LossMatrix &h, const LossMatrix &w, const float *bias, int v0,
                          float alpha, const LossRows &r, const LossTiling &t)
 {
     memset(&p, 0, sizeof(p));
@@ -1102,7 +1119,7 @@ cudaError_t vocab_params(LParams &p, LMaps &maps, const LossMatrix &h, const Los
     if (items > INT32_MAX) return cudaErrorNotSupported;
     p.items = (int)items;
     p.ksteps = (int)cdiv(h.cols, LK);
-    p.bz = bz;
+    p.bias = bias;
     p.v0 = v0;
     p.alpha = alpha;
     p.r = r;
@@ -1162,17 +1179,19 @@ LossTiling vocab_tiling(int rows, int cols, int d, int parts, double *us)
 {
     LossTiling t;
     t.cg = rows > 128 ? 2 : 1;
-    const int widest = parts == 3 ? 128 : 256;
-    t.bn = cols > widest - 64 ? widest : (cols + 63) / 64 * 64;
     t.tiles_m = (int)cdiv(rows, 128 * t.cg);
-    t.tiles_n = (int)cdiv(cols, t.bn);
     t.splits = 1;
     t.turned = t.first = false;
     t.ahead = 0;
-    // strips: few enough partial results, and the last round of CTAs full
+    // The widest tiles (narrower ones that would fill the last round of CTAs
+    // better took longer: 2816 x 512 x 131072 in 192-wide tiles 321 us, in
+    // 256-wide ones 272), in the strips that leave the last round fullest; of
+    // equal ones the longest (fewest partial results).
+    const int widest = parts == 3 ? 128 : 256;
+    t.bn = cols > widest - 64 ? widest : (int)(cdiv(cols, 64) * 64);
+    t.tiles_n = (int)cdiv(cols, t.bn);
     const long slots = device_sm_count() / t.cg;
     double best = 1e300;
-    t.strip = 1;
     for (int s = 1; s <= t.tiles_n && s <= 64; ++s) {
         const double cost = (double)cdiv(t.tiles_m * cdiv(t.tiles_n, s), slots) * (s + 0.15);
         if (cost <= best) {
@@ -1260,28 +1279,28 @@ int gradient_piece(int rows, int d, int vocab, int parts, int most)
     return best_piece;
 }
 
-cudaError_t launch_loss_lse(const LossMatrix &h, const LossMatrix &w, const float *bz, int v0, float alpha,
+cudaError_t launch_loss_lse(const LossMatrix &h, const LossMatrix &w, const float *bias, int v0, float alpha,
                             const LossRows &r, float *ysel, float2 *part, const LossTiling &t, cudaStream_t s)
 {
     LParams p;
     LMaps maps;
     memset(&maps, 0, sizeof(maps));
-    cudaError_t e = vocab_params(p, maps, h, w, bz, v0, alpha, r, t);
+    cudaError_t e = vocab_params(p, maps, h, w, bias, v0, alpha, r, t);
     if (e != cudaSuccess) return e;
     p.ysel = ysel;
     p.part = part;
-    return bz ? l_launch_cg<MODE_LSE, true>(t.cg, h.pieces, maps, p, s)
+    return bias ? l_launch_cg<MODE_LSE, true>(t.cg, h.pieces, maps, p, s)
               : l_launch_cg<MODE_LSE, false>(t.cg, h.pieces, maps, p, s);
 }
 
-cudaError_t launch_loss_dz(const LossMatrix &h, const LossMatrix &w, const float *bz, int v0, float alpha,
+cudaError_t launch_loss_dz(const LossMatrix &h, const LossMatrix &w, const float *bias, int v0, float alpha,
                            const LossRows &r, const LossMatrix &dz, float *dbpart, const LossTiling &t,
                            cudaStream_t s)
 {
     LParams p;
     LMaps maps;
     memset(&maps, 0, sizeof(maps));
-    cudaError_t e = vocab_params(p, maps, h, w, bz, v0, alpha, r, t);
+    cudaError_t e = vocab_params(p, maps, h, w, bias, v0, alpha, r, t);
     if (e != cudaSuccess) return e;
     p.dbpart = dbpart;
     p.dbpitch = dz.pitch;
@@ -1289,7 +1308,7 @@ cudaError_t launch_loss_dz(const LossMatrix &h, const LossMatrix &w, const float
     e = l_map(&maps.o[0], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dz.base, dz.cols, dz.rows, dz.pieces, dz.pitch,
               dz.piece_stride, three ? 32 : 64, 32, three ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
-    return bz ? l_launch_cg<MODE_DZ, true>(t.cg, h.pieces, maps, p, s)
+    return bias ? l_launch_cg<MODE_DZ, true>(t.cg, h.pieces, maps, p, s)
               : l_launch_cg<MODE_DZ, false>(t.cg, h.pieces, maps, p, s);
 }
 

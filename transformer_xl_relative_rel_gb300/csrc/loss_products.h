@@ -36,14 +36,26 @@ cudaError_t loss_launch(void (*kernel)(K...), unsigned grid, unsigned block, siz
 
 // One call's rows, as the kernels see them.
 struct LossRows {
-    int *col;        // [rows][K] listed columns, ascending; kNoColumn behind them
-    float *p;        // [rows][K] their weights
-    float *ent;      // [rows] sum_k p log p
-    float *coef;     // [rows] t * dloss, 0 for an empty row (backward)
-    float *l2;       // [rows] lse * log2(e) (backward)
-    int K;
+    const int64_t *target;     // cross entropy: the rows' own column, of weight 1; else NULL and
+    int *col;                  // [rows][K] listed columns, ascending; kNoColumn behind them
+    float *p;                  // [rows][K] their weights
+    float *ent;                // [rows] sum_k p log p
+    int K, vocab;
+    float t;                   // temperature
+    const float *lse, *dloss;  // [rows] (backward)
 };
 constexpr int kNoColumn = INT32_MAX;   // an invalid list entry: sorts behind every column
+constexpr float kLn2 = 0.693147180559945309f;
+__device__ __forceinline__ int target_column(const LossRows &r, long i)
+{
+    const int64_t y = r.target[i];
+    return y >= 0 && y < r.vocab ? (int)y : kNoColumn;
+}
+// t * dloss; 0 for a row without a valid entry (`any`) or a finite logit
+__device__ __forceinline__ float row_factor(const LossRows &r, long i, bool any)
+{
+    return any && r.lse[i] != -INFINITY ? r.t * r.dloss[i] : 0.f;
+}
 
 // A bf16 matrix in device memory, [pieces][rows][cols] with `pitch` elements
 // between rows (a multiple of 8, 16-byte aligned base).  One piece holds
@@ -83,14 +95,15 @@ constexpr int kLossPieceUnit = 256;
 int gradient_piece(int rows, int d, int vocab, int parts, int most);
 
 // part[2 * strip + half][row] = (maximum, sum of 2^(y - maximum)) over the
-// columns, y = alpha (h . w) + bz; ysel[row][k] = y at the listed columns
-// (vocabulary column = v0 + column of w).
-cudaError_t launch_loss_lse(const LossMatrix &h, const LossMatrix &w, const float *bz, int v0, float alpha,
+// columns, y = alpha (h . w + bias); ysel[row][k] = y at the listed columns
+// (vocabulary column = v0 + column of w).  bias: of w's columns, 16-byte
+// aligned, or NULL.
+cudaError_t launch_loss_lse(const LossMatrix &h, const LossMatrix &w, const float *bias, int v0, float alpha,
                             const LossRows &r, float *ysel, float2 *part, const LossTiling &t, cudaStream_t s);
 
 // dz = coef (2^(y - l2) - listed weights), in dz's pieces; dbpart[row / 32][column]
 // (pitch dz.pitch) the columns' sums over 32 rows each, when given.
-cudaError_t launch_loss_dz(const LossMatrix &h, const LossMatrix &w, const float *bz, int v0, float alpha,
+cudaError_t launch_loss_dz(const LossMatrix &h, const LossMatrix &w, const float *bias, int v0, float alpha,
                            const LossRows &r, const LossMatrix &dz, float *dbpart, const LossTiling &t,
                            cudaStream_t s);
 

@@ -5,12 +5,10 @@
 //   loss_i = t^2 sum_k p_ik (log p_ik - z_{i,idx_ik} / t + lse_i)
 //
 // with p the teacher's softmax over its kept entries; cross entropy is the
-// same with one entry of weight 1 and t = 1.  Both reduce to a sparse list
-// of (column, weight) per row, so one set of kernels serves both:
+// same with one entry of weight 1 (the target itself) and t = 1, so one set
+// of kernels serves both:
 //
-//   loss_prep_kernel   the row lists (for the backward also the row's factor
-//                      t * dloss and lse in base-2 units), scaled biases,
-//                      operands laid out for the products;
+//   loss_prep_kernel   the row lists, operands laid out for the products;
 //   forward            one pass over the vocabulary (loss_products.cu) leaves
 //                      a maximum and a sum per row and strip of vocabulary
 //                      tiles and the logits of the listed columns;
@@ -38,7 +36,6 @@ namespace txl {
 namespace {
 
 constexpr int kMaxTopK = 256;
-constexpr float kLn2 = 0.693147180559945309f;
 
 template <typename T>
 __device__ __forceinline__ float to_f(T x);
@@ -56,7 +53,8 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return
 
 // ------------------------------------------------------------ preparation
 // What has to be ready before the products, in one launch whose blocks take
-// different parts: the row lists, the scaled biases, operands that the TMA
+// different parts (none of them for a forward cross entropy of aligned bf16
+// operands): the teacher's row lists, unaligned biases, operands that the TMA
 // unit cannot read as they lie, and (backward) h transposed.
 struct CopyJob {
     const void *src;
@@ -69,13 +67,11 @@ struct PrepArgs {
     const int64_t *idx;
     const void *logits;   // NULL: cross entropy
     int logits_f32;
-    float t, inv_t;
-    const float *lse, *dloss;   // backward, else NULL
+    float inv_t;
     LossRows r;
     int rows, vocab, K2;
-    const float *bias;
-    float alpha;
-    float *bz;
+    const float *bias;          // copied where it is not 16-byte aligned
+    float *bias_copy;
     int d, dp;
     CopyJob copy[2];
     // h^T
@@ -97,28 +93,6 @@ __device__ __forceinline__ bool teacher_valid(const PrepArgs &p, long at)
     return e >= 0 && e < p.vocab && teacher_logit(p, at) != -INFINITY;
 }
 
-// t * dloss, 0 for a row without a valid entry or a finite logit
-__device__ __forceinline__ float row_factor(const PrepArgs &p, long i, bool valid)
-{
-    return valid && p.lse[i] != -INFINITY ? p.t * p.dloss[i] : 0.f;
-}
-
-// cross entropy: one entry of weight 1; a thread per row
-__device__ __forceinline__ void xent_rows(const PrepArgs &p)
-{
-    const long i = (long)blockIdx.x * 256 + threadIdx.x;
-    if (i >= p.rows) return;
-    const int64_t y = p.idx[i];
-    const bool valid = y >= 0 && y < p.vocab;
-    p.r.col[i] = valid ? (int)y : kNoColumn;
-    p.r.p[i] = valid ? 1.f : 0.f;
-    p.r.ent[i] = 0.f;
-    if (p.dloss) {
-        p.r.coef[i] = row_factor(p, i, valid);
-        p.r.l2[i] = p.lse[i] * (1.f / kLn2);
-    }
-}
-
 // distillation: the softmax of a row's valid entries at temperature t, then
 // the entries sorted by column (a bitonic network over the next power of
 // two).  One warp per row; K2 entries of shared memory per warp.
@@ -138,17 +112,10 @@ __device__ __forceinline__ void distill_rows(const PrepArgs &p, int *sc, float *
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     float sum = 0.f;
-    int any = 0;
     for (int k = lane; k < K2; k += 32)
-        if (sc[k] != kNoColumn) {
-            any = 1;
-            sum += expf(sp[k] - top);
-        }
+        if (sc[k] != kNoColumn) sum += expf(sp[k] - top);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        any |= __shfl_xor_sync(0xffffffffu, any, o);
-    }
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const float lt = logf(sum);
     float ent = 0.f;
     for (int k = lane; k < K2; k += 32) {
@@ -183,13 +150,7 @@ __device__ __forceinline__ void distill_rows(const PrepArgs &p, int *sc, float *
         p.r.col[base + k] = sc[k];
         p.r.p[base + k] = sp[k];
     }
-    if (lane == 0) {
-        p.r.ent[i] = ent;
-        if (p.dloss) {
-            p.r.coef[i] = row_factor(p, i, any);
-            p.r.l2[i] = p.lse[i] * (1.f / kLn2);
-        }
-    }
+    if (lane == 0) p.r.ent[i] = ent;
 }
 
 // The bf16 parts of an element: itself, or the three parts of an fp32 value,
@@ -270,11 +231,11 @@ __device__ __forceinline__ void transpose_rows(const PrepArgs &p, int block, __n
         const long i = i0 + threadIdx.x;
         bool valid = false;
         if (i < p.rows) {
-            for (int k = 0; k < p.r.K && !valid; ++k) {
-                const int64_t e = p.idx[i * p.r.K + k];
-                valid = p.logits ? teacher_valid(p, i * p.r.K + k) : e >= 0 && e < p.vocab;
-            }
-            valid = row_factor(p, i, valid) != 0.f;
+            if (p.r.target)
+                valid = target_column(p.r, i) != kNoColumn;
+            else
+                for (int k = 0; k < p.r.K && !valid; ++k) valid = teacher_valid(p, i * p.r.K + k);
+            valid = row_factor(p.r, i, valid) != 0.f;
         }
         live[threadIdx.x] = valid;
     }
@@ -314,17 +275,14 @@ __global__ void __launch_bounds__(256) loss_prep_kernel(const __grid_constant__ 
     loss_kernel_wait();
     int b = (int)blockIdx.x;
     if (b < p.row_blocks) {
-        if (p.logits)
-            distill_rows(p, reinterpret_cast<int *>(s) + (threadIdx.x >> 5) * p.K2,
-                         reinterpret_cast<float *>(s) + (8 + (threadIdx.x >> 5)) * p.K2);
-        else
-            xent_rows(p);
+        distill_rows(p, reinterpret_cast<int *>(s) + (threadIdx.x >> 5) * p.K2,
+                     reinterpret_cast<float *>(s) + (8 + (threadIdx.x >> 5)) * p.K2);
         return;
     }
     b -= p.row_blocks;
-    if (b < p.bias_blocks) {   // bz[j] = bias_j log2(e) / t
+    if (b < p.bias_blocks) {
         const long j = (long)b * 256 + threadIdx.x;
-        if (j < p.vocab) p.bz[j] = p.bias[j] * p.alpha;
+        if (j < p.vocab) p.bias_copy[j] = p.bias[j];
         return;
     }
     b -= p.bias_blocks;
@@ -452,11 +410,16 @@ loss_merge_kernel(const float2 *__restrict__ part, int slots, const float *__res
     const float y_lse = ref + log2f(l);
     float dot = 0.f;
     int any = 0;
-    for (int k = tx; k < r.K; k += 32) {
-        if (r.col[row * r.K + k] == kNoColumn) continue;
-        any = 1;
-        const float p = r.p[row * r.K + k];
-        if (p != 0.f) dot += p * (y_lse - ysel[row * r.K + k]);
+    if (r.target) {
+        any = target_column(r, row) != kNoColumn;
+        if (any && tx == 0) dot = y_lse - ysel[row];
+    } else {
+        for (int k = tx; k < r.K; k += 32) {
+            if (r.col[row * r.K + k] == kNoColumn) continue;
+            any = 1;
+            const float p = r.p[row * r.K + k];
+            if (p != 0.f) dot += p * (y_lse - ysel[row * r.K + k]);
+        }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -465,7 +428,7 @@ loss_merge_kernel(const float2 *__restrict__ part, int slots, const float *__res
     }
     if (tx == 0) {
         lse[row] = y_lse * kLn2;
-        loss[row] = any && y_lse != -INFINITY ? t2 * (r.ent[row] + kLn2 * dot) : 0.f;
+        loss[row] = any && y_lse != -INFINITY ? t2 * ((r.target ? 0.f : r.ent[row]) + kLn2 * dot) : 0.f;
     }
 }
 
@@ -479,7 +442,7 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb)
     return x < y + nb && y < x + na;
 }
 
-constexpr size_t kPieceBytes = (size_t)256 << 20;  // at most this for one piece of dz and of copied weights
+constexpr size_t kPieceBytes = (size_t)512 << 20;  // at most this for one piece of dz and of copied weights
 constexpr size_t kWeightBytes = (size_t)64 << 20;  // ... for the forward's copied weights
 constexpr int kMaxSize = 1 << 30;                  // rows and vocabulary
 
@@ -497,10 +460,11 @@ struct LossPlan {
     struct Piece {
         LossTiling vocab, dh, dw;
     } whole, last;
-    size_t col, p, ent, coef, l2, bz, ysel, part, h, ht, w, dz, dh_acc, dw_acc, dbpart, bytes;
+    size_t col, p, ent, bias, ysel, part, h, ht, w, dz, dh_acc, dw_acc, dbpart, bytes;
 };
 
 // h_ok, w_ok: 16-byte aligned bases of h and w
+// (K 0: cross entropy)
 LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool backward, bool h_ok, bool w_ok)
 {
     LossPlan q = {};
@@ -511,6 +475,7 @@ LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool back
         return o;
     };
     const size_t n = (size_t)rows;
+    const bool distill = K > 0;
     q.parts = dtype == TXL_F32 ? 3 : 1;
     q.dp = (int)up(d, 8);
     const bool tma = dtype == TXL_BF16 && d % 8 == 0;
@@ -524,10 +489,10 @@ LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool back
         q.piece = gradient_piece(rows, d, vocab, q.parts, most < (size_t)kMaxSize ? (int)most : kMaxSize);
     else
         q.piece = most < (size_t)vocab ? (int)most : vocab;
-    q.col = take(n * K * 4);
-    q.p = take(n * K * 4);
-    q.ent = take(n * 4);
-    q.bz = take((size_t)vocab * 4 + 256);   // read in fours past the last column
+    q.col = take(distill ? n * K * 4 : 0);
+    q.p = take(distill ? n * K * 4 : 0);
+    q.ent = take(distill ? n * 4 : 0);
+    q.bias = take((size_t)vocab * 4);
     q.h = take(q.copy_h ? n * q.dp * q.parts * 2 : 0);
     q.w = take(q.copy_w ? (size_t)q.piece * q.dp * q.parts * 2 : 0);
     if (!backward) {
@@ -536,11 +501,9 @@ LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool back
         q.last.vocab = vocab_tiling(rows, last, d, q.parts);
         const long more = (vocab - last) / q.piece;   // whole pieces before the last one
         q.slots = kSlotsPerStrip * (int)(more * vocab_strips(q.whole.vocab) + vocab_strips(q.last.vocab));
-        q.ysel = take(n * K * 4);
+        q.ysel = take(n * (distill ? K : 1) * 4);
         q.part = take(n * q.slots * 8);
     } else {
-        q.coef = take(n * 4);
-        q.l2 = take(n * 4);
         q.ht = take((size_t)d * up(rows, 8) * q.parts * 2);
         q.dz = take(n * up(q.piece, 64) * q.parts * 2);
         q.dh_slots = q.piece < vocab;
@@ -607,11 +570,11 @@ size_t loss_bytes(int rows, int d, int vocab, int K, txl_dtype dtype, bool backw
 struct LossArgs {
     const void *h, *w;
     const float *bias;
-    const int64_t *idx;            // [rows][K]
-    const void *t_logits;          // NULL: cross entropy
+    const int64_t *idx;            // [rows][K], or [rows] targets
+    const void *t_logits;
     txl_dtype t_dtype;
     float temp;
-    int rows, d, vocab, K;
+    int rows, d, vocab, K;         // K 0: cross entropy
     txl_dtype dtype;
     float *loss, *lse_out;         // forward
     const float *lse, *dloss;      // backward
@@ -625,7 +588,7 @@ struct LossArgs {
 txl_status loss_sizes(int rows, int d, int vocab, int K, txl_dtype dtype)
 {
     if (dtype != TXL_F32 && dtype != TXL_BF16) return TXL_ERR_UNSUPPORTED;
-    if (rows < 0 || d < 1 || vocab < 1 || K < 1) return TXL_ERR_INVALID;
+    if (rows < 0 || d < 1 || vocab < 1 || K < 0) return TXL_ERR_INVALID;
     if (K > kMaxTopK || rows > kMaxSize || vocab > kMaxSize) return TXL_ERR_UNSUPPORTED;
     return TXL_OK;
 }
@@ -644,7 +607,7 @@ txl_status loss_checks(const LossArgs &a, bool backward, LossPlan *plan)
 {
     const txl_status st = loss_sizes(a.rows, a.d, a.vocab, a.K, a.dtype);
     if (st != TXL_OK) return st;
-    const bool distill = a.temp != 0.f;
+    const bool distill = a.K > 0;
     if (distill) {
         if (a.t_dtype != TXL_F32 && a.t_dtype != TXL_BF16) return TXL_ERR_UNSUPPORTED;
         if (!(a.temp > 0.f) || isinf(a.temp)) return TXL_ERR_INVALID;
@@ -659,7 +622,7 @@ txl_status loss_checks(const LossArgs &a, bool backward, LossPlan *plan)
     const Buf ins[] = {{a.h, n * a.d * esz, esz, true},
                        {a.w, (size_t)a.vocab * a.d * esz, esz, a.rows > 0},
                        {a.bias, (size_t)a.vocab * 4, 4, false},
-                       {a.idx, n * a.K * 8, 8, true},
+                       {a.idx, n * (distill ? a.K : 1) * 8, 8, true},
                        {a.t_logits, distill ? n * a.K * tsz : 0, tsz, distill},
                        {backward ? a.lse : nullptr, n * 4, 4, backward},
                        {backward ? a.dloss : nullptr, n * 4, 4, backward}};
@@ -690,13 +653,22 @@ LossRows rows_at(const LossArgs &a, const LossPlan &q)
 {
     unsigned char *ws = (unsigned char *)a.ws;
     LossRows r;
+    r.target = a.K == 0 ? a.idx : nullptr;
     r.col = (int *)(ws + q.col);
     r.p = (float *)(ws + q.p);
     r.ent = (float *)(ws + q.ent);
-    r.coef = (float *)(ws + q.coef);
-    r.l2 = (float *)(ws + q.l2);
-    r.K = a.K;
+    r.K = a.K ? a.K : 1;
+    r.vocab = a.vocab;
+    r.t = a.temp != 0.f ? a.temp : 1.f;
+    r.lse = a.lse;
+    r.dloss = a.dloss;
     return r;
+}
+
+// the biases as the kernels read them
+const float *bias_of(const LossArgs &a, const LossPlan &q)
+{
+    return !a.bias || al(a.bias, 16) ? a.bias : (const float *)((unsigned char *)a.ws + q.bias);
 }
 
 // blocks of a pass over n threads' work that strides over its grid
@@ -724,6 +696,7 @@ cudaError_t launch_prep(const LossArgs &a, const PrepArgs &p)
 {
     const long blocks = (long)p.row_blocks + p.bias_blocks + p.t_blocks + p.copy[0].blocks + p.copy[1].blocks;
     if (blocks > INT32_MAX) return cudaErrorNotSupported;
+    if (blocks == 0) return cudaSuccess;
     return loss_launch(a.dtype == TXL_F32 ? loss_prep_kernel<float> : loss_prep_kernel<__nv_bfloat16>, (unsigned)blocks,
                        256, 0, 1, a.s, p);
 }
@@ -739,29 +712,24 @@ LossMatrix w_operand(const LossArgs &a, const LossPlan &q, long v0, int cols, Co
     return {(unsigned char *)a.ws + q.w, q.dp, stride, cols, q.dp, q.parts};
 }
 
-// The first preparation: rows, biases, h, the vocabulary's first piece and,
-// for dW, h^T.
-cudaError_t prepare(const LossArgs &a, const LossPlan &q, const LossRows &r, bool backward, LossMatrix *h, LossMatrix *w,
-                    LossMatrix *ht)
+// The first preparation: row lists, biases, h, the vocabulary's first piece
+// and, for dW, h^T.
+cudaError_t prepare(const LossArgs &a, const LossPlan &q, const LossRows &r, LossMatrix *h, LossMatrix *w, LossMatrix *ht)
 {
     PrepArgs p;
     memset(&p, 0, sizeof(p));
     p.idx = a.idx;
     p.logits = a.t_logits;
     p.logits_f32 = a.t_dtype == TXL_F32;
-    p.t = a.temp != 0.f ? a.temp : 1.f;
-    p.inv_t = 1.f / p.t;
-    p.lse = backward ? a.lse : nullptr;
-    p.dloss = backward ? a.dloss : nullptr;
+    p.inv_t = 1.f / r.t;
     p.r = r;
     p.rows = a.rows;
     p.vocab = a.vocab;
     for (p.K2 = 2; p.K2 < a.K;) p.K2 <<= 1;
-    p.row_blocks = a.t_logits ? (a.rows + 7) / 8 : (a.rows + 255) / 256;
+    p.row_blocks = a.K ? (a.rows + 7) / 8 : 0;
     p.bias = a.bias;
-    p.alpha = alpha_of(a);
-    p.bz = (float *)((unsigned char *)a.ws + q.bz);
-    p.bias_blocks = a.bias ? (a.vocab + 255) / 256 : 0;
+    p.bias_copy = (float *)((unsigned char *)a.ws + q.bias);
+    p.bias_blocks = bias_of(a, q) != a.bias ? (a.vocab + 255) / 256 : 0;
     p.d = a.d;
     p.dp = q.dp;
     if (q.copy_h) {
@@ -802,17 +770,17 @@ cudaError_t run_fwd(const LossArgs &a, const LossPlan &q)
 {
     unsigned char *ws = (unsigned char *)a.ws;
     const LossRows r = rows_at(a, q);
-    const float *bz = (const float *)(ws + q.bz);
+    const float *bias = bias_of(a, q);
     float2 *part = (float2 *)(ws + q.part);
     LossMatrix h, w;
-    cudaError_t e = prepare(a, q, r, false, &h, &w, nullptr);
+    cudaError_t e = prepare(a, q, r, &h, &w, nullptr);
     long slot = 0;
     for (long v0 = 0; e == cudaSuccess && v0 < a.vocab; v0 += q.piece) {
         const int cols = (int)(a.vocab - v0 < q.piece ? a.vocab - v0 : q.piece);
         const LossTiling t = cols == q.piece ? q.whole.vocab : q.last.vocab;
         if (v0 > 0) e = next_weights(a, q, v0, cols, &w);
         if (e == cudaSuccess)
-            e = launch_loss_lse(h, w, a.bias ? bz + v0 : nullptr, (int)v0, alpha_of(a), r, (float *)(ws + q.ysel),
+            e = launch_loss_lse(h, w, bias ? bias + v0 : nullptr, (int)v0, alpha_of(a), r, (float *)(ws + q.ysel),
                                 part + slot * a.rows, t, a.s);
         slot += kSlotsPerStrip * vocab_strips(t);
     }
@@ -864,12 +832,12 @@ cudaError_t run_bwd(const LossArgs &a, const LossPlan &q)
 {
     unsigned char *ws = (unsigned char *)a.ws;
     const LossRows r = rows_at(a, q);
-    const float *bz = (const float *)(ws + q.bz);
+    const float *bias = bias_of(a, q);
     const size_t esz = a.dtype == TXL_F32 ? 4 : 2;
     const long h_stride = (long)a.rows * q.dp;
     float *acc_h = (float *)(ws + q.dh_acc), *acc_w = (float *)(ws + q.dw_acc);
     LossMatrix h, ht, w;
-    cudaError_t e = prepare(a, q, r, true, &h, &w, a.dw ? &ht : nullptr);
+    cudaError_t e = prepare(a, q, r, &h, &w, a.dw ? &ht : nullptr);
     for (long v0 = 0; e == cudaSuccess && v0 < a.vocab; v0 += q.piece) {
         const int cols = (int)(a.vocab - v0 < q.piece ? a.vocab - v0 : q.piece);
         const bool last = v0 + cols == a.vocab;
@@ -879,7 +847,7 @@ cudaError_t run_bwd(const LossArgs &a, const LossPlan &q)
         float *dbp = a.db ? (float *)(ws + q.dbpart) : nullptr;
         if (v0 > 0) e = next_weights(a, q, v0, cols, &w);
         if (e == cudaSuccess)
-            e = launch_loss_dz(h, w, a.bias ? bz + v0 : nullptr, (int)v0, alpha_of(a), r, dz, dbp, t.vocab, a.s);
+            e = launch_loss_dz(h, w, bias ? bias + v0 : nullptr, (int)v0, alpha_of(a), r, dz, dbp, t.vocab, a.s);
         if (e != cudaSuccess) return e;
         // both gradients of the piece in one launch, the longer items first
         LossContraction job[2];
@@ -973,12 +941,13 @@ extern "C" {
 
 txl_status txl_softmax_xent_workspace(int rows, int d_model, int vocab, txl_dtype dtype, int backward, size_t *bytes)
 {
-    return loss_workspace(rows, d_model, vocab, 1, dtype, backward, bytes);
+    return loss_workspace(rows, d_model, vocab, 0, dtype, backward, bytes);
 }
 
 txl_status txl_distill_workspace(int rows, int d_model, int vocab, int top_k, txl_dtype dtype, int backward,
                                  size_t *bytes)
 {
+    if (top_k < 1) return TXL_ERR_INVALID;
     return loss_workspace(rows, d_model, vocab, top_k, dtype, backward, bytes);
 }
 
@@ -986,7 +955,7 @@ txl_status txl_softmax_xent_fwd(const void *h, const void *w, const float *bias,
                                 int d_model, int vocab, txl_dtype dtype, float *loss, float *lse, void *workspace,
                                 size_t workspace_bytes, void *stream)
 {
-    return loss_fwd({h, w, bias, target, nullptr, TXL_F32, 0.f, rows, d_model, vocab, 1, dtype, loss, lse, nullptr,
+    return loss_fwd({h, w, bias, target, nullptr, TXL_F32, 0.f, rows, d_model, vocab, 0, dtype, loss, lse, nullptr,
                      nullptr, nullptr, nullptr, nullptr, workspace, workspace_bytes, (cudaStream_t)stream});
 }
 
@@ -995,7 +964,7 @@ txl_status txl_softmax_xent_bwd(const void *h, const void *w, const float *bias,
                                 txl_dtype dtype, void *dh, void *dw, float *dbias, void *workspace,
                                 size_t workspace_bytes, void *stream)
 {
-    return loss_bwd({h, w, bias, target, nullptr, TXL_F32, 0.f, rows, d_model, vocab, 1, dtype, nullptr, nullptr, lse,
+    return loss_bwd({h, w, bias, target, nullptr, TXL_F32, 0.f, rows, d_model, vocab, 0, dtype, nullptr, nullptr, lse,
                      dloss, dh, dw, dbias, workspace, workspace_bytes, (cudaStream_t)stream});
 }
 
@@ -1004,7 +973,7 @@ txl_status txl_distill_fwd(const void *h, const void *w, const float *bias, cons
                            int d_model, int vocab, int top_k, txl_dtype dtype, float *loss, float *lse,
                            void *workspace, size_t workspace_bytes, void *stream)
 {
-    if (!(temperature > 0.f)) return TXL_ERR_INVALID;
+    if (!(temperature > 0.f) || top_k < 1) return TXL_ERR_INVALID;
     return loss_fwd({h, w, bias, teacher_idx, teacher_logits, teacher_dtype, temperature, rows, d_model, vocab, top_k,
                      dtype, loss, lse, nullptr, nullptr, nullptr, nullptr, nullptr, workspace, workspace_bytes,
                      (cudaStream_t)stream});
@@ -1015,7 +984,7 @@ txl_status txl_distill_bwd(const void *h, const void *w, const float *bias, cons
                            const float *dloss, int rows, int d_model, int vocab, int top_k, txl_dtype dtype,
                            void *dh, void *dw, float *dbias, void *workspace, size_t workspace_bytes, void *stream)
 {
-    if (!(temperature > 0.f)) return TXL_ERR_INVALID;
+    if (!(temperature > 0.f) || top_k < 1) return TXL_ERR_INVALID;
     return loss_bwd({h, w, bias, teacher_idx, teacher_logits, teacher_dtype, temperature, rows, d_model, vocab, top_k,
                      dtype, nullptr, nullptr, lse, dloss, dh, dw, dbias, workspace, workspace_bytes,
                      (cudaStream_t)stream});
