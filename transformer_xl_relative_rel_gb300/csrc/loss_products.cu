@@ -16,10 +16,10 @@
 // fp32 operands are held as three bf16 parts whose sum is exact (8 + 8 + 8
 // bits of the 24-bit significand); the product keeps the six part products
 // down to 2^-16 of the largest, dropping three of at most 2^-24, smallest
-// first.  The tensor core truncates where it accumulates (measured: a chain
-// of n additions comes out about n 2^-25 too small), so with fp32 operands an
-// accumulator takes one 64-deep step and the epilogue warps add the steps in
-// registers, rounding to nearest.
+// first.  The tensor core truncates where it accumulates (measured: a chain of
+// n additions comes out about n 2^-25 too small), so with fp32 operands an
+// accumulator takes two 64-deep steps (8 additions of the largest products)
+// and the epilogue warps add these in registers, rounding to nearest.
 //
 // Roles (12 warps): warp 0 issues the TMA loads, warp 1 the MMAs, warps 4-11
 // are two epilogue groups of four (a warp per 32 TMEM lanes), which share a
@@ -52,6 +52,7 @@ using namespace sm100;
 
 constexpr int LK = 64;                         // K elements per stage
 constexpr int LNT = 384;
+constexpr int kPartSteps = 2;                  // steps per accumulation of fp32 operands
 constexpr int LEPI = 8;                        // epilogue warps
 constexpr uint64_t LWAIT_NS = 2000000000ull;   // 2 s per wait, then give up
 
@@ -575,8 +576,8 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                 const uint64_t sa = t.a_mn ? 128 : 2, sb = t.b_mn ? 128 : 2;
                 for (int nt = t.nt0; ok && nt < t.nt1; ++nt) {
                     for (int ks = t.ks0; ok && ks < t.ks1; ++lt) {
-                        // one accumulation: the whole K range, or one step of three parts
-                        const int buf = lt & 1, k1 = kParts ? ks + 1 : t.ks1;
+                        // one accumulation: the whole K range, or some steps of three parts
+                        const int buf = lt & 1, k1 = kParts && ks + kPartSteps < t.ks1 ? ks + kPartSteps : t.ks1;
                         if (lt >= 2 && !wait(S::AEMPTY + buf, ((lt >> 1) - 1) & 1)) {
                             ok = false;
                             break;
@@ -948,7 +949,7 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                     // this half's 64 columns, summed over the steps
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v0[j] = v1[j] = 0.f;
-                    for (int ks = t.ks0; ks < t.ks1; ++ks, ++lt) {
+                    for (int ks = t.ks0; ks < t.ks1; ks += kPartSteps, ++lt) {
                         if (!wait(S::AFULL + (lt & 1), (lt >> 1) & 1)) {
                             ok = false;
                             break;
