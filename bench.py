@@ -12,6 +12,7 @@ the timed region; the per-step working set is far larger than L2.
     python bench.py [--gpus N] [--steps K] [--warmup W] [--workload NAME]
     python bench.py --impl reference ...     # the float64 CPU oracle
     python bench.py --recompute-vs-reuse     # eval cost per token, window recompute vs memory reuse
+    python bench.py --output-loss            # the output layer's losses on the workload's hidden states
 
 Prints one JSON line (rank 0).  Under torchrun each rank runs its own replica
 (weak scaling: independent sequences, no data-path collective); timing is the
@@ -1106,6 +1107,76 @@ def backward(args, local: int):
     return 0
 
 
+def output_loss(args, local: int):
+    """Time the output layer on one segment of the workload's hidden states
+    (seg_len x batch rows of d_model, bf16) and ``--vocab`` tokens: cross
+    entropy forward (evaluation) and forward plus backward (dh, dw, db), and
+    distillation from ``--top-k`` teacher logits per row, forward plus
+    backward.  Workspace and outputs allocated once, CUDA events over the
+    timed calls; the weights and the workspace are larger than L2 at the
+    default vocabulary.  FLOPs: 2 rows d_model vocab per product, one product
+    forward, three more backward (the logits again, dz W, dz^T h)."""
+    import transformer_xl_relative_rel_gb300 as txl
+    w = WORKLOADS[args.workload]
+    s = w.shape
+    L, B, d, V, K = s.seg_len, s.batch, s.d_model, args.vocab, args.top_k
+    gen = torch.Generator(device="cuda").manual_seed(13)
+    dev = torch.device("cuda", local)
+    h = torch.randn(L, B, d, generator=gen, device=dev).to(torch.bfloat16)
+    wt = (torch.randn(V, d, generator=gen, device=dev) * (2.0 / math.sqrt(d))).to(torch.bfloat16)
+    bias = torch.randn(V, generator=gen, device=dev)
+    target = torch.randint(0, V, (L, B), generator=gen, device=dev)
+    teacher = torch.randn(L, B, K, generator=gen, device=dev).sort(-1, descending=True).values
+    idx = torch.randint(0, V, (L, B, K), generator=gen, device=dev)
+    dloss = torch.full((L, B), 1.0 / (L * B), device=dev)
+    nbytes = txl.distill_workspace_bytes(L * B, d, V, K, txl.TXL_BF16, backward=True)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    loss, lse = torch.empty(L, B, device=dev), torch.empty(L, B, device=dev)
+    grads = dict(dh=torch.empty_like(h), dw=torch.empty_like(wt), db=torch.empty(V, device=dev))
+
+    def evaluate():
+        txl.softmax_xent_fwd(h, wt, target, bias=bias, loss=loss, lse=lse, workspace=ws)
+
+    def train():
+        evaluate()
+        txl.softmax_xent_bwd(h, wt, target, lse, dloss, bias=bias, grads=grads, workspace=ws)
+
+    def distil():
+        txl.distill_fwd(h, wt, idx, teacher, 2.0, bias=bias, loss=loss, lse=lse, workspace=ws)
+        txl.distill_bwd(h, wt, idx, teacher, lse, dloss, 2.0, bias=bias, grads=grads, workspace=ws)
+
+    def timed(call):
+        for _ in range(args.warmup):
+            call()
+        torch.cuda.synchronize()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        for _ in range(args.steps):
+            call()
+        e1.record()
+        torch.cuda.synchronize()
+        return e0.elapsed_time(e1) / 1e3 / args.steps
+
+    clocks = ClockSampler(local)
+    clocks.start()
+    t_eval, t_train, t_distil = timed(evaluate), timed(train), timed(distil)
+    clk = clocks.stop()
+    txl.check()
+    one = 2.0 * L * B * d * V
+    peaks, src = load_peaks()
+    peak = peaks["bf16_tflops"]
+    arm = lambda t, n: {"ms_per_call": t * 1e3, "tflops": n * one / t / 1e12, "frac_bf16_peak": n * one / t / 1e12 / peak}
+    print(json.dumps({
+        "metric": "output-layer training tokens/s and TFLOP/s (cross entropy, forward + backward), 1 GB300",
+        "value": B * L / t_train, "unit": "tokens/s", "n_gpus": 1, "steps": args.steps, "warmup": args.warmup,
+        "higher_is_better": True, "dtype": "bf16", "data": "synthetic",
+        "config": {"workload": w.name, "rows": L * B, "d_model": d, "vocab": V, "top_k": K,
+                   "workspace_bytes": nbytes},
+        "train": arm(t_train, 4), "eval": arm(t_eval, 1), "distill": arm(t_distil, 4),
+        "peak": peak, "peak_source": src, "clocks": clk}), flush=True)
+    return 0
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -1126,6 +1197,11 @@ def main(argv=None):
                     help="time the eager step only (no CUDA-graph replay of the step)")
     ap.add_argument("--backward", action="store_true",
                     help="time txl_rel_attn_bwd (gradients of one layer call) at the workload's shape")
+    ap.add_argument("--output-loss", action="store_true",
+                    help="time the output layer's losses (cross entropy, distillation) on the workload's hidden "
+                         "states")
+    ap.add_argument("--vocab", type=int, default=131072, help="vocabulary of --output-loss")
+    ap.add_argument("--top-k", type=int, default=32, help="teacher logits per row of --output-loss")
     ap.add_argument("--fused-rollover", action="store_true",
                     help="--attn-only: attention and memory update of a layer in one call "
                          "(txl_rel_attn_fwd_mem; the recurrence step does this by default); the roofline's "
@@ -1167,6 +1243,8 @@ def main(argv=None):
         return recompute_vs_reuse(args, local)
     if args.backward:
         return backward(args, local)
+    if args.output_loss:
+        return output_loss(args, local)
 
     w = WORKLOADS[args.workload]
     if args.layers or args.segments:
