@@ -719,25 +719,26 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                     for (int x = 0; x < 32; ++x)
                         if (n0 + 8 * ((x >> 2) & 3) + c2 + (x & 1) >= p.N) v[x] = 0.f;
                 }
-                // listed columns: every row's next one at a time, applied one by
-                // one by the threads that hold them
+                // listed columns: every row's next one at once; a thread asks the
+                // four lanes that follow its rows' lists
                 while (cur.c0 < col0) cur.next();
                 __syncwarp();
-                while (unsigned hit = __ballot_sync(0xffffffffu, cur.c0 < col0 + 32)) {
-                    const float mine = coef == 0.f ? 0.f : coef * cur.p0;
-                    const int mc = cur.c0 - col0;
-                    if ((hit >> lane) & 1) cur.next();
+                while (__any_sync(0xffffffffu, cur.c0 < col0 + 32)) {
+                    const bool hit = cur.c0 < col0 + 32;
+                    const int mc = hit ? cur.c0 - col0 : 64;
+                    const float mine = hit && coef != 0.f ? -coef * cur.p0 : 0.f;
+                    if (hit) cur.next();
                     __syncwarp();
-                    for (; hit; hit &= hit - 1) {
-                        const int src = __ffs(hit) - 1, c = __shfl_sync(0xffffffffu, mc, src);
-                        const float g = __shfl_sync(0xffffffffu, mine, src);
-                        const bool holds = g != 0.f && (lane >> 2) == (src & 7) && (lane & 3) == ((c >> 1) & 3);
-                        const uint64_t g2 = pair(holds && !(c & 1) ? -g : 0.f, holds && (c & 1) ? -g : 0.f);
-                        const int at = 4 * (src >> 3) + (c >> 3);
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) {
-                            const int e = 16 * (x >> 3) + 4 * (x & 3) + 2 * ((x >> 2) & 1);
-                            if (x == at) unpair(add2(pair(v[e], v[e + 1]), g2), v[e], v[e + 1]);
+                    for (int r = 0; r < 4; ++r) {
+                        const int c = __shfl_sync(0xffffffffu, mc, (lane >> 2) + 8 * r);
+                        const float g = __shfl_sync(0xffffffffu, mine, (lane >> 2) + 8 * r);
+                        const int at = ((c >> 1) & 3) == (lane & 3) ? c >> 3 : 8;
+                        const uint64_t g2 = pair(c & 1 ? 0.f : g, c & 1 ? g : 0.f);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int e = 16 * (r >> 1) + 4 * i + 2 * (r & 1);
+                            if (at == i) unpair(add2(pair(v[e], v[e + 1]), g2), v[e], v[e + 1]);
                         }
                     }
                 }
