@@ -398,7 +398,8 @@ __device__ __forceinline__ LItem l_item(const LParams &p, int item)
     return t;
 }
 
-// A row's listed columns in ascending order, the next two held in registers.
+// A row's listed columns of one parity of 64-column chunks (an epilogue group
+// works on one) in ascending order, the next two held in registers.
 struct Cursor {
     const int *col;
     const float *p;
@@ -411,7 +412,7 @@ struct Cursor {
         w = in && p ? __ldg(p + at) : 0.f;
     }
     // the row's first entry of a column >= from
-    __device__ __forceinline__ void seek(const LossRows &r, long row, bool live, bool weights, int from)
+    __device__ __forceinline__ void seek(const LossRows &r, long row, bool live, bool weights, int from, int half)
     {
         K = 0;
         pos = 0;
@@ -420,13 +421,14 @@ struct Cursor {
         if (!live) return;
         if (r.target) {
             const int y = target_column(r, row);
-            if (y >= from) c0 = y;
+            if (y >= from && ((y >> 6) & 1) == half) c0 = y;
             return;
         }
-        K = r.K;
-        col = r.col + row * K;
-        p = weights ? r.p + row * K : nullptr;
-        int lo = 0, hi = K;
+        col = r.col + row * r.K;
+        p = weights ? r.p + row * r.K : nullptr;
+        const int even = __ldg(r.even + row);
+        K = half ? r.K : even;   // the end of this parity's entries
+        int lo = half ? even : 0, hi = K;
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
             if (__ldg(col + mid) < from)
@@ -671,7 +673,7 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
             Cursor cur;
             bool dead = false;
             if (MODE != MODE_CT) {
-                cur.seek(p.r, row, live, MODE == MODE_DZ, p.v0 + t.n0);
+                cur.seek(p.r, row, live, MODE == MODE_DZ, p.v0 + t.n0, half);
                 if (MODE == MODE_DZ) {
                     if (live) {
                         // (a list's valid entries come first)
@@ -721,8 +723,6 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                 }
                 // listed columns: every row's next one at once; a thread asks the
                 // four lanes that follow its rows' lists
-                while (cur.c0 < col0) cur.next();
-                __syncwarp();
                 while (__any_sync(0xffffffffu, cur.c0 < col0 + 32)) {
                     const bool hit = cur.c0 < col0 + 32;
                     const int mc = hit ? cur.c0 - col0 : 64;
@@ -894,12 +894,10 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                         if (n0 + j >= p.N) v[j] = -INFINITY;
                 }
                 while (cur.c0 < col0 + 32) {
-                    if (cur.c0 >= col0) {
-                        float y = 0.f;
+                    float y = 0.f;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) y = cur.c0 == col0 + j ? v[j] : y;
-                        p.ysel[(long)row * p.r.K + cur.pos] = y * p.alpha;
-                    }
+                    for (int j = 0; j < 32; ++j) y = cur.c0 == col0 + j ? v[j] : y;
+                    p.ysel[(long)row * p.r.K + cur.pos] = y * p.alpha;
                     cur.next();
                 }
                 __syncwarp();

@@ -37,7 +37,9 @@ cudaError_t loss_launch(void (*kernel)(K...), unsigned grid, unsigned block, siz
 // One call's rows, as the kernels see them.
 struct LossRows {
     const int64_t *target;     // cross entropy: the rows' own column, of weight 1; else NULL and
-    int *col;                  // [rows][K] listed columns, ascending; kNoColumn behind them
+    int *col;                  // [rows][K] listed columns: those of even 64-column chunks of the vocabulary
+                               // ascending, then those of odd ones, then kNoColumn
+    int *even;                 // [rows] how many of the former
     float *p;                  // [rows][K] their weights
     float *ent;                // [rows] sum_k p log p
     int K, vocab;

@@ -94,9 +94,11 @@ __device__ __forceinline__ bool teacher_valid(const PrepArgs &p, long at)
 }
 
 // distillation: the softmax of a row's valid entries at temperature t, then
-// the entries sorted by column (a bitonic network over the next power of
-// two).  One warp per row; K2 entries of shared memory per warp.
-__device__ __forceinline__ void distill_rows(const PrepArgs &p, int *sc, float *sp)
+// the entries sorted by the parity of their column's 64-column chunk and the
+// column (a bitonic network over the next power of two).  One warp per row;
+// K2 entries of shared memory per warp.
+constexpr unsigned kNoKey = 0xffffffffu, kOdd = 1u << 31;
+__device__ __forceinline__ void distill_rows(const PrepArgs &p, unsigned *sc, float *sp)
 {
     const int lane = threadIdx.x & 31, K = p.r.K, K2 = p.K2;
     const long i = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -105,7 +107,8 @@ __device__ __forceinline__ void distill_rows(const PrepArgs &p, int *sc, float *
     float top = -INFINITY;
     for (int k = lane; k < K2; k += 32) {
         const bool valid = k < K && teacher_valid(p, base + k);
-        sc[k] = valid ? (int)p.idx[base + k] : kNoColumn;
+        const unsigned c = valid ? (unsigned)p.idx[base + k] : 0u;
+        sc[k] = valid ? c | (c & 64u ? kOdd : 0u) : kNoKey;
         sp[k] = valid ? teacher_logit(p, base + k) * p.inv_t : -INFINITY;
         top = fmaxf(top, sp[k]);
     }
@@ -113,14 +116,14 @@ __device__ __forceinline__ void distill_rows(const PrepArgs &p, int *sc, float *
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     float sum = 0.f;
     for (int k = lane; k < K2; k += 32)
-        if (sc[k] != kNoColumn) sum += expf(sp[k] - top);
+        if (sc[k] != kNoKey) sum += expf(sp[k] - top);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const float lt = logf(sum);
     float ent = 0.f;
     for (int k = lane; k < K2; k += 32) {
         float w = 0.f;
-        if (sc[k] != kNoColumn) {
+        if (sc[k] != kNoKey) {
             const float lp = sp[k] - top - lt;
             w = expf(lp);
             if (w != 0.f) ent += w * lp;   // (a NaN teacher logit stays NaN)
@@ -135,7 +138,7 @@ __device__ __forceinline__ void distill_rows(const PrepArgs &p, int *sc, float *
             for (int x = lane; x < K2 / 2; x += 32) {
                 const int a = 2 * x - (x & (step - 1)), b = a + step;
                 const bool up = (a & len) == 0;
-                const int ca = sc[a], cb = sc[b];
+                const unsigned ca = sc[a], cb = sc[b];
                 if ((ca > cb) == up && ca != cb) {
                     sc[a] = cb;
                     sc[b] = ca;
@@ -146,11 +149,19 @@ __device__ __forceinline__ void distill_rows(const PrepArgs &p, int *sc, float *
             }
             __syncwarp();
         }
+    int even = 0;
     for (int k = lane; k < K; k += 32) {
-        p.r.col[base + k] = sc[k];
+        const unsigned c = sc[k];
+        p.r.col[base + k] = c == kNoKey ? kNoColumn : (int)(c & ~kOdd);
         p.r.p[base + k] = sp[k];
+        even += !(c & kOdd);
     }
-    if (lane == 0) p.r.ent[i] = ent;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) even += __shfl_xor_sync(0xffffffffu, even, o);
+    if (lane == 0) {
+        p.r.ent[i] = ent;
+        p.r.even[i] = even;
+    }
 }
 
 // The bf16 parts of an element: itself, or the three parts of an fp32 value,
@@ -275,7 +286,7 @@ __global__ void __launch_bounds__(256) loss_prep_kernel(const __grid_constant__ 
     loss_kernel_wait();
     int b = (int)blockIdx.x;
     if (b < p.row_blocks) {
-        distill_rows(p, reinterpret_cast<int *>(s) + (threadIdx.x >> 5) * p.K2,
+        distill_rows(p, reinterpret_cast<unsigned *>(s) + (threadIdx.x >> 5) * p.K2,
                      reinterpret_cast<float *>(s) + (8 + (threadIdx.x >> 5)) * p.K2);
         return;
     }
@@ -460,7 +471,7 @@ struct LossPlan {
     struct Piece {
         LossTiling vocab, dh, dw;
     } whole, last;
-    size_t col, p, ent, bias, ysel, part, h, ht, w, dz, dh_acc, dw_acc, dbpart, bytes;
+    size_t col, even, p, ent, bias, ysel, part, h, ht, w, dz, dh_acc, dw_acc, dbpart, bytes;
 };
 
 // h_ok, w_ok: 16-byte aligned bases of h and w
@@ -491,6 +502,7 @@ LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool back
         q.piece = most < (size_t)vocab ? (int)most : vocab;
     q.col = take(distill ? n * K * 4 : 0);
     q.p = take(distill ? n * K * 4 : 0);
+    q.even = take(distill ? n * 4 : 0);
     q.ent = take(distill ? n * 4 : 0);
     q.bias = take((size_t)vocab * 4);
     q.h = take(q.copy_h ? n * q.dp * q.parts * 2 : 0);
@@ -655,6 +667,7 @@ LossRows rows_at(const LossArgs &a, const LossPlan &q)
     LossRows r;
     r.target = a.K == 0 ? a.idx : nullptr;
     r.col = (int *)(ws + q.col);
+    r.even = (int *)(ws + q.even);
     r.p = (float *)(ws + q.p);
     r.ent = (float *)(ws + q.ent);
     r.K = a.K ? a.K : 1;
