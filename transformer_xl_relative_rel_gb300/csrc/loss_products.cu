@@ -943,7 +943,10 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
             for (int nt = t.nt0; ok && nt < t.nt1; ++nt) {
                 float v0[32], v1[32];
                 float2 b0[4], b1[4];
-                biases(b0, t.n0 + (nt - t.nt0) * t.bn + 64 * half);
+                // the tile's columns, and the first of its chunks that is this group's (by its
+                // parity in the vocabulary)
+                const int first = t.n0 + (nt - t.nt0) * t.bn, mine = half ^ ((first >> 6) & 1);
+                biases(b0, first + 64 * mine);
                 if constexpr (kParts) {
                     // this half's 64 columns, summed over the steps
 #pragma unroll
@@ -954,8 +957,8 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                             break;
                         }
                         tc_fence_after();
-                        if (half < nch) {
-                            const uint32_t at = tq + (uint32_t)((lt & 1) * 256 + 64 * half);
+                        if (mine < nch) {
+                            const uint32_t at = tq + (uint32_t)((lt & 1) * 256 + 64 * mine);
                             float x[32];
                             issue(at, x);
                             l_tmem_wait(x);
@@ -969,10 +972,10 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                         release(lt & 1);
                     }
                     if (!ok) break;
-                    if (half < nch) {
-                        biases(b1, t.n0 + (nt - t.nt0) * t.bn + 64 * half + 32);
-                        work(v0, b0, t.n0 + (nt - t.nt0) * t.bn + 64 * half, 0);
-                        work(v1, b1, t.n0 + (nt - t.nt0) * t.bn + 64 * half + 32, 1);
+                    if (mine < nch) {
+                        biases(b1, first + 64 * mine + 32);
+                        work(v0, b0, first + 64 * mine, 0);
+                        work(v1, b1, first + 64 * mine + 32, 1);
                     }
                 } else {
                     const int buf = lt & 1;
@@ -984,16 +987,16 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                     tc_fence_after();
                     if (MODE == MODE_LSE && kBias && nt + 1 < t.nt1 && 32 * lane < t.bn && (nt + 1) * t.bn + 32 * lane < t.N)   // the next tile's biases
                         asm volatile("prefetch.global.L1 [%0];" ::"l"(p.bias + (nt + 1) * t.bn + 32 * lane));
-                    if (half >= nch) {
+                    if (mine >= nch) {
                         release(buf);
                         continue;
                     }
                     // each load is in flight while the columns before it are worked on
                     const uint32_t tacc = tq + (uint32_t)(buf * 256);
-                    issue(tacc + 64u * half, v0);
+                    issue(tacc + 64u * mine, v0);
                     l_tmem_wait(v0);
-                    for (int c = half; c < nch; c += 2) {
-                        const int n0 = t.n0 + (nt - t.nt0) * t.bn + 64 * c;
+                    for (int c = mine; c < nch; c += 2) {
+                        const int n0 = first + 64 * c;
                         issue(tacc + 64u * c + 32u, v1);
                         biases(b1, n0 + 32);
                         work(v0, b0, n0, 0);
@@ -1187,10 +1190,13 @@ LossTiling vocab_tiling(int rows, int cols, int d, int parts, double *us)
     // better took longer: 2816 x 512 x 131072 in 192-wide tiles 321 us, in
     // 256-wide ones 272), in the strips that leave the last round fullest; of
     // equal ones the longest (fewest partial results).
+    // Where even half as wide ones leave CTAs idle, those: every tile is then
+    // a CTA's only one.
     const int widest = parts == 3 ? 128 : 256;
-    t.bn = cols > widest - 64 ? widest : (int)(cdiv(cols, 64) * 64);
-    t.tiles_n = (int)cdiv(cols, t.bn);
     const long slots = device_sm_count() / t.cg;
+    t.bn = cols > widest - 64 ? widest : (int)(cdiv(cols, 64) * 64);
+    while (t.bn >= 128 && t.bn % 128 == 0 && t.tiles_m * cdiv(cols, t.bn / 2) <= slots) t.bn /= 2;
+    t.tiles_n = (int)cdiv(cols, t.bn);
     double best = 1e300;
     for (int s = 1; s <= t.tiles_n && s <= 64; ++s) {
         const double cost = (double)cdiv(t.tiles_m * cdiv(t.tiles_n, s), slots) * (s + 0.15);
@@ -1199,6 +1205,7 @@ LossTiling vocab_tiling(int rows, int cols, int d, int parts, double *us)
             t.strip = s;
         }
     }
+    if (t.tiles_m == 1) t.strip = 1;   // bound by reading the weights: every SM reads (2 x 768 x 90326: 36.7 -> 33.3 us)
     if (us) {
         const double main = cdiv(d, LK) * step_us(t.bn, parts), epi = kEpilogueUs * t.bn / 256;
         *us = best * (main > epi ? main : epi) + kLaunchUs;
@@ -1211,12 +1218,13 @@ double gradient_tiling(int rows, int d, int cols, int whole, int parts, bool dh_
 {
     const int cg = rows > 128 ? 2 : 1;
     // dh as the transpose of W^T dz^T unless that wastes more rows of its tiles
-    // than an MN-major B costs
+    // than an MN-major B costs, or reading the weights bounds it (few rows):
+    // as B they come in twice the bytes per stage
     LossTiling turned;
     job_tiles(turned, d, rows, cg, parts);
     job_tiles(*dh, rows, d, cg, parts);
     turned.turned = true;
-    if ((double)turned.tiles_m * cdiv(rows, 64) <= kMnB * dh->tiles_m * cdiv(d, 64)) *dh = turned;
+    if (cg == 2 && (double)turned.tiles_m * cdiv(rows, 64) <= kMnB * dh->tiles_m * cdiv(d, 64)) *dh = turned;
     job_tiles(*dw, cols, d, cg, parts);
     const long slots = device_sm_count() / cg;
     const long n0 = (long)dh->tiles_m * dh->tiles_n, n1 = (long)dw->tiles_m * dw->tiles_n;

@@ -320,7 +320,7 @@ struct SumJob {
 struct FinishArgs {
     const float *dbpart;
     float *db;
-    int parts, cols, db_blocks;
+    int parts, cols, db_blocks, db_lanes;
     long pitch;
     int d, dp;
     SumJob sum[2];
@@ -351,22 +351,21 @@ __device__ __forceinline__ void sum_slots(const SumJob &j, int d, int dp, int bl
 template <typename T>
 __global__ void __launch_bounds__(1024) loss_finish_kernel(const __grid_constant__ FinishArgs p)
 {
-    __shared__ float s[32][33];
+    __shared__ float s[1024];
     loss_kernel_begin();
     loss_kernel_wait();
     int b = (int)blockIdx.x;
-    if (b < p.db_blocks) {   // 32 columns, 32 threads per column
-        const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-        const long j = (long)b * 32 + tx;
+    if (b < p.db_blocks) {   // db_lanes threads per column, each some of the row groups
+        const int wide = 1024 / p.db_lanes, tx = threadIdx.x % wide, ty = threadIdx.x / wide;
+        const long j = (long)b * wide + tx;
         float sum = 0.f;
         if (j < p.cols)
-            for (int x = ty; x < p.parts; x += 32) sum += p.dbpart[x * p.pitch + j];
-        s[ty][tx] = sum;
+            for (int x = ty; x < p.parts; x += p.db_lanes) sum += p.dbpart[x * p.pitch + j];
+        s[threadIdx.x] = sum;
         __syncthreads();
         if (ty == 0 && j < p.cols) {
-            float all = 0.f;
-            for (int x = 0; x < 32; ++x) all += s[x][tx];
-            p.db[j] = all;
+            for (int x = 1; x < p.db_lanes; ++x) sum += s[x * wide + tx];
+            p.db[j] = sum;
         }
         return;
     }
@@ -905,7 +904,8 @@ cudaError_t run_bwd(const LossArgs &a, const LossPlan &q)
             f.parts = (int)(up(a.rows, 32) / 32);
             f.cols = cols;
             f.pitch = pitch;
-            f.db_blocks = (cols + 31) / 32;
+            for (f.db_lanes = 1; f.db_lanes < 32 && 4 * f.db_lanes < f.parts;) f.db_lanes <<= 1;
+            f.db_blocks = (int)((cols + 1024 / f.db_lanes - 1) / (1024 / f.db_lanes));
         }
         if (a.dw && !w_direct) f.sum[0] = sum_job(a, acc_w, t.dw.splits, w_stride, dw_out, cols);
         if (a.dh && !h_direct && last) f.sum[1] = sum_job(a, acc_h, t.dh.splits, h_stride, a.dh, a.rows);
