@@ -424,7 +424,8 @@ txl_status txl_rel_attn_fwd_noalloc(const void *q, const void *k, const void *v,
  * Pointers are element-aligned (h, w: 2 or 4 bytes; float32: 4; int64: 8);
  * rows of w and h that the TMA unit can address (d_model a multiple of 8,
  * 16-byte aligned bases) are read in place with TXL_BF16, others are copied
- * piece by piece into the workspace first.
+ * piece by piece into the workspace first (not for a handful of rows with
+ * d_model <= 1024 and w 16-byte aligned).
  * rows == 0: nothing to do.  d_model >= 1, vocab >= 1, else TXL_ERR_INVALID;
  * vocab <= 2^30 and rows <= 2^30, else TXL_ERR_UNSUPPORTED.  Asynchronous on
  * stream; no allocation; results do not depend on what else runs (no
@@ -454,7 +455,7 @@ txl_status txl_softmax_xent_fwd(const void *h, const void *w, const float *bias,
  * workspace : as above, for backward = 1 (which also suffices for the
  *             forward).
  * rows == 0: dw and dbias are set to 0.  Outputs must not overlap each other,
- * any input or the workspace.  bf16: dz is rounded once to bf16 for the two
+ * any input or the workspace.  bf16: dz is rounded at most once to bf16 for the two
  * products (fp32 accumulation over the whole vocabulary and all rows, one
  * rounding of the results); dbias sums the unrounded dz.
  */

@@ -102,6 +102,56 @@ def test_distill_sizes(rows, d, vocab, k, t, dtype, t_dtype):
     _check_distill(_inputs(rows, d, vocab, dtype, rows * 5 + d + k, bias=k % 2 == 1, k=k, t_dtype=t_dtype), t)
 
 
+# few rows: heights 2, 8, 16 and the first past them, rows of every alignment,
+# chunks of 16 to 64 tokens, blocks of one and of many chunks, the widest rows
+FEW = [(1, 1, 1), (2, 3, 17), (1, 1024, 9001), (2, 410, 20011), (3, 30, 65), (8, 769, 3001), (9, 64, 64),
+       (8, 1023, 5001), (15, 2, 40000), (16, 1024, 5003), (16, 410, 2433), (17, 410, 300), (7, 1025, 200), (5, 6, 9729)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,d,vocab", FEW)
+def test_few_rows(rows, d, vocab, dtype):
+    _check_xent(_inputs(rows, d, vocab, dtype, rows + d, bias=(rows + d) % 2 == 0))
+    k = min(256, 3 + vocab // 50)     # listed columns in chunks of both parities
+    _check_distill(_inputs(rows, d, vocab, dtype, rows + 2 * d, bias=d % 2 == 1, k=k), 2.0)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 41), (BF, 62), (F32, 41), (F32, 62), (F32, 64)])
+def test_few_rows_edges(dtype, d):
+    """Empty rows, infinities, absent gradients, untouched neighbours and a
+    gradient that is only element-aligned, as for many rows."""
+    import transformer_xl_relative_rel_gb300 as txl
+    p = _inputs(6, d, 1500, dtype, 5, k=9)
+    q = dict(p, h=p["h"].clone(), dloss=p["dloss"].clone(), bias=p["bias"].clone())
+    q["h"][1] = float("nan")
+    q["dloss"][1] = float("nan")
+    for fn in (_xent, lambda x: _distill(x, 2.0)):
+        a, b = fn(p), fn(q)
+        for n in ("loss", "dh", "dw", "db"):
+            assert torch.equal(a[n], b[n]), n
+        assert not b["dh"][1].any() and not b["dh"][2].any()      # an empty row, dloss 0
+        assert torch.equal(fn(dict(p, bias=None))["lse"], fn(dict(p, bias=torch.zeros_like(p["bias"])))["lse"])
+    p["bias"][10:1490] = -float("inf")
+    for n in ("target", "idx"):
+        p[n] = torch.where((p[n] >= 0) & (p[n] < 1500), p[n] % 10, p[n])
+    _check_xent(p)
+    _check_distill(p, 2.0)
+    whole = _xent(p)
+    loss, lse = txl.softmax_xent_fwd(p["h"], p["w"], p["target"], bias=p["bias"])
+    for names in (("dh",), ("dw",), ("db",), ("dh", "db")):
+        flats = {n: torch.full((whole[n].numel() + 16,), 7.0, dtype=whole[n].dtype, device="cuda") for n in names}
+        grads = {n: flats[n][1:1 + whole[n].numel()].view(whole[n].shape) for n in names}
+        txl.softmax_xent_bwd(p["h"], p["w"], p["target"], lse, p["dloss"], bias=p["bias"], grads=grads)
+        for n in names:
+            assert torch.equal(grads[n], whole[n]), (names, n)
+            assert flats[n][0] == 7 and (flats[n][1 + whole[n].numel():] == 7).all(), (names, n)
+    p["bias"][:] = -float("inf")
+    g = _xent(p)
+    assert (g["lse"] == -float("inf")).all() and not g["loss"].any()
+    assert not g["dh"].any() and not g["dw"].any() and not g["db"].any()
+    txl.check()
+
+
 def test_small_problem_matches_the_oracle():
     p = _inputs(9, 16, 70, F32, 3, k=4)
     n = lambda x: x.double().cpu().numpy()

@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libtxl.so")
 SOURCES = ["api.cu", "attn_f32.cu", "attn_bf16.cu", "rollover.cu", "noalloc.cu", "project.cu", "pack.cu", "backward.cu",
-           "output_loss.cu", "loss_products.cu"]
+           "output_loss.cu", "loss_products.cu", "loss_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -530,13 +530,14 @@ txl_status txl_check(void *stream)
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return cuda_fail(e);
-    unsigned int word = 0, gword = 0, bword = 0, lword = 0;
+    unsigned int word = 0, gword = 0, bword = 0, lword = 0, fword = 0;
     e = read_and_clear_device_error(&word, s);
     if (e == cudaSuccess) e = read_and_clear_gemm_error(&gword, s);
     if (e == cudaSuccess) e = read_and_clear_bwd_error(&bword, s);
     if (e == cudaSuccess) e = read_and_clear_loss_error(&lword, s);
+    if (e == cudaSuccess) e = read_and_clear_few_error(&fword, s);
     if (e != cudaSuccess) return cuda_fail(e);
-    return (word | gword | bword | lword) ? TXL_ERR_TIMEOUT : TXL_OK;
+    return (word | gword | bword | lword | fword) ? TXL_ERR_TIMEOUT : TXL_OK;
 }
 
 const char *txl_status_string(txl_status st)

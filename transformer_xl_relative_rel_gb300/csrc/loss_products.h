@@ -129,6 +129,31 @@ struct LossContraction {
 };
 cudaError_t launch_loss_gradients(const LossContraction *jobs, int n, int parts, cudaStream_t s);
 
+// The losses of a handful of rows on the CUDA cores (loss_few.cu), where the
+// tensor-core kernel would need a copy of the weights.
+constexpr int kFewColumns = 1024;   // widest d_model
+struct FewShape {
+    int tok, slots;    // tokens per chunk, chunks in the ring
+    int per, blocks;   // tokens per block
+};
+// false: sizes for the tensor-core kernel.  w_ok: w is 16-byte aligned.
+bool few_shape(int rows, int d, int vocab, bool f32, bool w_ok, FewShape *s);
+struct FewCall {
+    const void *h, *w;
+    const float *bias;
+    LossRows r;
+    int rows, d, vocab;
+    FewShape s;
+    bool f32, backward;
+    float alpha;
+    float *ysel;         // forward: as launch_loss_lse
+    float2 *part;        // ... [blocks][rows]
+    void *dh, *dw;       // backward; each and db may be NULL
+    float *db, *dh_part; // dh_part: [blocks][rows][d]
+};
+cudaError_t launch_loss_few(const FewCall &a, cudaStream_t s);
+cudaError_t read_and_clear_few_error(unsigned int *word, cudaStream_t s);
+
 cudaError_t read_and_clear_loss_error(unsigned int *word, cudaStream_t s);
 
 }  // namespace txl

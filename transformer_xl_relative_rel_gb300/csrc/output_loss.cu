@@ -462,6 +462,8 @@ long up(long a, long b) { return (a + b - 1) / b * b; }
 // alignment and the number of SMs alone.
 struct LossPlan {
     int parts, dp;          // bf16 parts of an element; operand row pitch (d rounded up to 8)
+    bool few;               // on the CUDA cores, ...
+    FewShape shape;
     bool copy_h, copy_w;
     int piece;              // vocabulary columns per piece
     int slots;              // forward: partial softmaxes per row over all pieces
@@ -489,6 +491,22 @@ LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool back
     q.parts = dtype == TXL_F32 ? 3 : 1;
     q.dp = (int)up(d, 8);
     const bool tma = dtype == TXL_BF16 && d % 8 == 0;
+    q.few = few_shape(rows, d, vocab, dtype == TXL_F32, w_ok, &q.shape);
+    if (q.few) {
+        q.col = take(distill ? n * K * 4 : 0);
+        q.p = take(distill ? n * K * 4 : 0);
+        q.even = take(distill ? n * 4 : 0);
+        q.ent = take(distill ? n * 4 : 0);
+        q.slots = q.shape.blocks;
+        if (backward) {
+            q.dh_acc = take(n * q.shape.blocks * d * 4);
+        } else {
+            q.ysel = take(n * (distill ? K : 1) * 4);
+            q.part = take(n * q.slots * 8);
+        }
+        q.bytes = at ? at : 256;
+        return q;
+    }
     q.copy_h = !tma || !h_ok;
     q.copy_w = !tma || !w_ok;
     // what a vocabulary column of a piece takes; pieces start at multiples of the widest tile
@@ -680,7 +698,7 @@ LossRows rows_at(const LossArgs &a, const LossPlan &q)
 // the biases as the kernels read them
 const float *bias_of(const LossArgs &a, const LossPlan &q)
 {
-    return !a.bias || al(a.bias, 16) ? a.bias : (const float *)((unsigned char *)a.ws + q.bias);
+    return q.few || !a.bias || al(a.bias, 16) ? a.bias : (const float *)((unsigned char *)a.ws + q.bias);
 }
 
 // blocks of a pass over n threads' work that strides over its grid
@@ -742,6 +760,7 @@ cudaError_t prepare(const LossArgs &a, const LossPlan &q, const LossRows &r, Los
     p.bias = a.bias;
     p.bias_copy = (float *)((unsigned char *)a.ws + q.bias);
     p.bias_blocks = bias_of(a, q) != a.bias ? (a.vocab + 255) / 256 : 0;
+    if (q.few) return launch_prep(a, p);
     p.d = a.d;
     p.dp = q.dp;
     if (q.copy_h) {
@@ -778,6 +797,30 @@ cudaError_t next_weights(const LossArgs &a, const LossPlan &q, long v0, int cols
     return q.copy_w ? launch_prep(a, p) : cudaSuccess;
 }
 
+FewCall few_call(const LossArgs &a, const LossPlan &q, const LossRows &r, bool backward)
+{
+    unsigned char *ws = (unsigned char *)a.ws;
+    FewCall f;
+    f.h = a.h;
+    f.w = a.w;
+    f.bias = a.bias;
+    f.r = r;
+    f.rows = a.rows;
+    f.d = a.d;
+    f.vocab = a.vocab;
+    f.s = q.shape;
+    f.f32 = a.dtype == TXL_F32;
+    f.backward = backward;
+    f.alpha = alpha_of(a);
+    f.ysel = (float *)(ws + q.ysel);
+    f.part = (float2 *)(ws + q.part);
+    f.dh = backward ? a.dh : nullptr;
+    f.dw = backward ? a.dw : nullptr;
+    f.db = backward ? a.db : nullptr;
+    f.dh_part = (float *)(ws + q.dh_acc);
+    return f;
+}
+
 cudaError_t run_fwd(const LossArgs &a, const LossPlan &q)
 {
     unsigned char *ws = (unsigned char *)a.ws;
@@ -786,8 +829,9 @@ cudaError_t run_fwd(const LossArgs &a, const LossPlan &q)
     float2 *part = (float2 *)(ws + q.part);
     LossMatrix h, w;
     cudaError_t e = prepare(a, q, r, &h, &w, nullptr);
+    if (e == cudaSuccess && q.few) e = launch_loss_few(few_call(a, q, r, false), a.s);
     long slot = 0;
-    for (long v0 = 0; e == cudaSuccess && v0 < a.vocab; v0 += q.piece) {
+    for (long v0 = 0; e == cudaSuccess && !q.few && v0 < a.vocab; v0 += q.piece) {
         const int cols = (int)(a.vocab - v0 < q.piece ? a.vocab - v0 : q.piece);
         const LossTiling t = cols == q.piece ? q.whole.vocab : q.last.vocab;
         if (v0 > 0) e = next_weights(a, q, v0, cols, &w);
@@ -850,6 +894,7 @@ cudaError_t run_bwd(const LossArgs &a, const LossPlan &q)
     float *acc_h = (float *)(ws + q.dh_acc), *acc_w = (float *)(ws + q.dw_acc);
     LossMatrix h, ht, w;
     cudaError_t e = prepare(a, q, r, &h, &w, a.dw ? &ht : nullptr);
+    if (q.few) return e == cudaSuccess ? launch_loss_few(few_call(a, q, r, true), a.s) : e;
     for (long v0 = 0; e == cudaSuccess && v0 < a.vocab; v0 += q.piece) {
         const int cols = (int)(a.vocab - v0 < q.piece ? a.vocab - v0 : q.piece);
         const bool last = v0 + cols == a.vocab;
