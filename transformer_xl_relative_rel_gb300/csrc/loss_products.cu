@@ -454,6 +454,7 @@ __global__ void __launch_bounds__(LNT, 1)
 loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ LParams p)
 {
     using S = LSmem<CG, MODE, kParts>;
+    constexpr int kDzParts = kParts ? 3 : CG == 1 ? 2 : 1;      // dz_parts()
     constexpr int ST = S::ST;
     loss_kernel_begin();
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -765,8 +766,8 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                         p.dbpart[(long)(row0 >> 5) * p.dbpitch + n0 + 8 * (lane >> 3) + c2 + ((lane >> 2) & 1)] = s[0];
                 }
 #pragma unroll
-                for (int part = 0; part < (kParts ? 3 : 1); ++part) {
-                    if (kParts || sub == 0) stage_wait();
+                for (int part = 0; part < kDzParts; ++part) {
+                    if (kDzParts > 1 || sub == 0) stage_wait();
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         uint32_t w4[4];
@@ -774,18 +775,18 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                         for (int i = 0; i < 4; ++i) {
                             float &a = v[16 * (r >> 1) + 4 * i + 2 * (r & 1)], &b = v[16 * (r >> 1) + 4 * i + 2 * (r & 1) + 1];
                             w4[i] = pack2(a, b);
-                            if (kParts) {
+                            if (part + 1 < kDzParts) {
                                 a -= top_part(a);
                                 b -= top_part(b);
                             }
                         }
-                        // rows of 128 bytes (64 per part of fp32) and their swizzles
+                        // rows of 128 bytes (64 per part of several) and their swizzles
                         const int y = 8 * r + (lane & 7), i = lane >> 3;
-                        st_blocks(kParts ? stg_a + y * 64 + ((i ^ ((y >> 1) & 3)) << 4)
-                                         : stg_a + y * 128 + (((4 * sub + i) ^ (y & 7)) << 4),
+                        st_blocks(kDzParts > 1 ? stg_a + y * 64 + ((i ^ ((y >> 1) & 3)) << 4)
+                                               : stg_a + y * 128 + (((4 * sub + i) ^ (y & 7)) << 4),
                                   w4[0], w4[1], w4[2], w4[3]);
                     }
-                    if (kParts) {
+                    if (kDzParts > 1) {
                         if (row0 < p.M) store(0, n0, row0, part, false);
                     } else if ((sub == 1 || n0 + 32 >= p.N) && row0 < p.M) {
                         // the second half of the chunk may lie past the last column
@@ -1264,18 +1265,19 @@ double gradient_tiling(int rows, int d, int cols, int whole, int parts, bool dh_
 int gradient_piece(int rows, int d, int vocab, int parts, int most)
 {
     if (vocab <= kLossPieceUnit) return vocab;
+    const int n = dz_rows(rows, parts);
     int best_piece = 0;
     double best = 1e300;
     const long units = cdiv(vocab, kLossPieceUnit), least = cdiv(units, most / kLossPieceUnit);
-    for (long n = least; n <= units && n < least + 12; ++n) {
-        const long piece = cdiv(units, n) * kLossPieceUnit;
+    for (long x = least; x <= units && x < least + 12; ++x) {
+        const long piece = cdiv(units, x) * kLossPieceUnit;
         const int cols = (int)(piece < vocab ? piece : vocab), last = vocab % cols;
         LossTiling a, b;
         auto cost = [&](int c) {
             double vus;
             vocab_tiling(rows, c, d, parts, &vus);
-            const double dz = (double)rows * c * 2 * parts, hbm = dz > kL2Bytes ? dz / kHbmPerUs : 0.0;
-            const double g = gradient_tiling(rows, d, c, cols, parts, cols < vocab, 0, &a, &b);
+            const double dz = (double)n * c * 2 * parts, hbm = dz > kL2Bytes ? dz / kHbmPerUs : 0.0;
+            const double g = gradient_tiling(n, d, c, cols, parts, cols < vocab || n != rows, 0, &a, &b);
             return (vus > hbm ? vus : hbm) + (g > 2 * hbm ? g : 2 * hbm);
         };
         const double us = vocab / cols * cost(cols) + (last ? cost(last) : 0.0);
@@ -1312,9 +1314,9 @@ cudaError_t launch_loss_dz(const LossMatrix &h, const LossMatrix &w, const float
     if (e != cudaSuccess) return e;
     p.dbpart = dbpart;
     p.dbpitch = dz.pitch;
-    const bool three = dz.pieces == 3;
+    const bool several = dz.pieces > 1;
     e = l_map(&maps.o[0], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dz.base, dz.cols, dz.rows, dz.pieces, dz.pitch,
-              dz.piece_stride, three ? 32 : 64, 32, three ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+              dz.piece_stride, several ? 32 : 64, 32, several ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
     return bias ? l_launch_cg<MODE_DZ, true>(t.cg, h.pieces, maps, p, s)
               : l_launch_cg<MODE_DZ, false>(t.cg, h.pieces, maps, p, s);

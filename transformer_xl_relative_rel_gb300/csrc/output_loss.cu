@@ -79,6 +79,7 @@ struct PrepArgs {
     __nv_bfloat16 *ht;
     long rp, ht_stride;
     int h_vec, t_cols;    // column blocks of the transpose
+    int twice;            // with h's rows once more behind the first (for the second part of dz)
     int row_blocks, bias_blocks, t_blocks;
 };
 
@@ -264,6 +265,11 @@ __device__ __forceinline__ void transpose_rows(const PrepArgs &p, int block, __n
     for (int x = threadIdx.x; x < 512; x += 256) {
         const int c = x >> 3, y = (x & 7) * 8;
         if (c0 + c >= p.d || i0 + y >= p.rp) continue;
+        if (p.twice) {
+            __nv_bfloat16 *to = p.ht + (c0 + c) * p.rp + i0 + y;
+            for (int j = 0; j < 8 && i0 + y + j < p.rows; ++j) to[j] = to[p.rows + j] = s[c * 65 + y + j];
+            continue;
+        }
 #pragma unroll
         for (int part = 0; part < kParts; ++part) {
             __align__(16) __nv_bfloat16 b[8];
@@ -461,6 +467,7 @@ long up(long a, long b) { return (a + b - 1) / b * b; }
 // How a call is divided and where things lie in the workspace; from sizes,
 // alignment and the number of SMs alone.
 struct LossPlan {
+    int dz_rows;            // rows of dz with its parts (dz_rows())
     int parts, dp;          // bf16 parts of an element; operand row pitch (d rounded up to 8)
     bool few;               // on the CUDA cores, ...
     FewShape shape;
@@ -510,7 +517,8 @@ LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool back
     q.copy_h = !tma || !h_ok;
     q.copy_w = !tma || !w_ok;
     // what a vocabulary column of a piece takes; pieces start at multiples of the widest tile
-    const size_t per = ((backward ? n : 0) + (q.copy_w ? (size_t)q.dp : 0)) * q.parts * 2;
+    q.dz_rows = backward ? dz_rows(rows, q.parts) : 0;
+    const size_t per = ((size_t)q.dz_rows + (q.copy_w ? (size_t)q.dp : 0)) * q.parts * 2;
     size_t most = per ? (backward ? kPieceBytes : kWeightBytes) / per / kLossPieceUnit * kLossPieceUnit : (size_t)vocab;
     if (most < (size_t)kLossPieceUnit) most = kLossPieceUnit;
     if (backward)
@@ -533,20 +541,20 @@ LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool back
         q.ysel = take(n * (distill ? K : 1) * 4);
         q.part = take(n * q.slots * 8);
     } else {
-        q.ht = take((size_t)d * up(rows, 8) * q.parts * 2);
-        q.dz = take(n * up(q.piece, 64) * q.parts * 2);
-        q.dh_slots = q.piece < vocab;
+        q.ht = take((size_t)d * up(q.dz_rows, 8) * q.parts * 2);
+        q.dz = take((size_t)q.dz_rows * up(q.piece, 64) * q.parts * 2);
+        q.dh_slots = q.piece < vocab || q.dz_rows != rows;
         // every piece splits dh alike, so that each adds to the same slots; the last, narrower one may split dW further
         const int last = vocab % q.piece ? vocab % q.piece : q.piece;
-        gradient_tiling(rows, d, q.piece, q.piece, q.parts, q.dh_slots, 0, &q.whole.dh, &q.whole.dw);
-        gradient_tiling(rows, d, last, q.piece, q.parts, q.dh_slots, q.whole.dh.splits, &q.last.dh, &q.last.dw);
+        gradient_tiling(q.dz_rows, d, q.piece, q.piece, q.parts, q.dh_slots, 0, &q.whole.dh, &q.whole.dw);
+        gradient_tiling(q.dz_rows, d, last, q.piece, q.parts, q.dh_slots, q.whole.dh.splits, &q.last.dh, &q.last.dw);
         q.whole.vocab = vocab_tiling(rows, q.piece, d, q.parts);
         q.last.vocab = vocab_tiling(rows, last, d, q.parts);
         auto dw_slots = [&](const LossTiling &t, int cols) {
             return t.splits > 1 ? (size_t)t.splits * cols * q.dp * 4 : 0;
         };
         const size_t dw_whole = dw_slots(q.whole.dw, q.piece), dw_last = dw_slots(q.last.dw, last);
-        q.dh_acc = take(q.dh_slots || q.whole.dh.splits > 1 ? (size_t)q.whole.dh.splits * n * q.dp * 4 : 0);
+        q.dh_acc = take(q.dh_slots || q.whole.dh.splits > 1 ? (size_t)q.whole.dh.splits * q.dz_rows * q.dp * 4 : 0);
         q.dw_acc = take(dw_whole > dw_last ? dw_whole : dw_last);
         q.dbpart = take((size_t)up(rows, 32) / 32 * up(q.piece, 64) * 4);
     }
@@ -775,13 +783,14 @@ cudaError_t prepare(const LossArgs &a, const LossPlan &q, const LossRows &r, Los
         p.h = a.h;
         p.h_vec = load_width(a, a.h);
         p.ht = (__nv_bfloat16 *)((unsigned char *)a.ws + q.ht);
-        p.rp = up(a.rows, 8);
+        p.rp = up(q.dz_rows, 8);
+        p.twice = q.dz_rows != a.rows;
         p.ht_stride = a.d * p.rp;
         p.t_cols = (a.d + 63) / 64;
         const long blocks = (long)((a.rows + 63) / 64) * p.t_cols;
         if (blocks > INT32_MAX) return cudaErrorNotSupported;
         p.t_blocks = (int)blocks;
-        *ht = {p.ht, p.rp, p.ht_stride, a.d, (int)p.rp, q.parts};
+        *ht = {p.ht, p.rp, p.ht_stride, a.d, q.dz_rows, q.parts};
     }
     return launch_prep(a, p);
 }
@@ -890,7 +899,7 @@ cudaError_t run_bwd(const LossArgs &a, const LossPlan &q)
     const LossRows r = rows_at(a, q);
     const float *bias = bias_of(a, q);
     const size_t esz = a.dtype == TXL_F32 ? 4 : 2;
-    const long h_stride = (long)a.rows * q.dp;
+    const long h_stride = (long)q.dz_rows * q.dp;
     float *acc_h = (float *)(ws + q.dh_acc), *acc_w = (float *)(ws + q.dw_acc);
     LossMatrix h, ht, w;
     cudaError_t e = prepare(a, q, r, &h, &w, a.dw ? &ht : nullptr);
@@ -900,11 +909,13 @@ cudaError_t run_bwd(const LossArgs &a, const LossPlan &q)
         const bool last = v0 + cols == a.vocab;
         const LossPlan::Piece &t = cols == q.piece ? q.whole : q.last;
         const long pitch = up(cols, 64), w_stride = (long)cols * q.dp;
-        const LossMatrix dz = {ws + q.dz, pitch, (long)a.rows * pitch, a.rows, cols, q.parts};
+        // its parts one behind another; to the products two of them are one matrix
+        const LossMatrix dz_out = {ws + q.dz, pitch, (long)a.rows * pitch, a.rows, cols, dz_parts(a.rows, q.parts)};
+        const LossMatrix dz = {ws + q.dz, pitch, (long)a.rows * pitch, q.dz_rows, cols, q.parts};
         float *dbp = a.db ? (float *)(ws + q.dbpart) : nullptr;
         if (v0 > 0) e = next_weights(a, q, v0, cols, &w);
         if (e == cudaSuccess)
-            e = launch_loss_dz(h, w, bias ? bias + v0 : nullptr, (int)v0, alpha_of(a), r, dz, dbp, t.vocab, a.s);
+            e = launch_loss_dz(h, w, bias ? bias + v0 : nullptr, (int)v0, alpha_of(a), r, dz_out, dbp, t.vocab, a.s);
         if (e != cudaSuccess) return e;
         // both gradients of the piece in one launch, the longer items first
         LossContraction job[2];
@@ -918,8 +929,8 @@ cudaError_t run_bwd(const LossArgs &a, const LossPlan &q)
             j.a = t.dh.turned ? w : dz;
             j.b = t.dh.turned ? dz : w;
             j.a_t = j.b_t = j.out_t = t.dh.turned;
-            j.m = t.dh.turned ? a.d : a.rows;
-            j.n = t.dh.turned ? a.rows : a.d;
+            j.m = t.dh.turned ? a.d : q.dz_rows;
+            j.n = t.dh.turned ? q.dz_rows : a.d;
             j.k = cols;
             j.out = h_direct ? direct_out(a, a.dh) : slot_out(acc_h, q.dp, h_stride, v0 > 0);
             j.t = t.dh;
@@ -933,7 +944,7 @@ cudaError_t run_bwd(const LossArgs &a, const LossPlan &q)
             j.out_t = false;
             j.m = cols;
             j.n = a.d;
-            j.k = a.rows;
+            j.k = q.dz_rows;
             j.out = w_direct ? direct_out(a, dw_out) : slot_out(acc_w, q.dp, w_stride, false);
             j.t = t.dw;
         }
@@ -953,7 +964,8 @@ cudaError_t run_bwd(const LossArgs &a, const LossPlan &q)
             f.db_blocks = (int)((cols + 1024 / f.db_lanes - 1) / (1024 / f.db_lanes));
         }
         if (a.dw && !w_direct) f.sum[0] = sum_job(a, acc_w, t.dw.splits, w_stride, dw_out, cols);
-        if (a.dh && !h_direct && last) f.sum[1] = sum_job(a, acc_h, t.dh.splits, h_stride, a.dh, a.rows);
+        if (a.dh && !h_direct && last)
+            f.sum[1] = sum_job(a, acc_h, t.dh.splits * (q.dz_rows / a.rows), (long)a.rows * q.dp, a.dh, a.rows);
         const int blocks = f.db_blocks + f.sum[0].blocks + f.sum[1].blocks;
         if (blocks)
             e = loss_launch(a.dtype == TXL_F32 ? loss_finish_kernel<float> : loss_finish_kernel<__nv_bfloat16>,
