@@ -407,7 +407,8 @@ txl_status txl_rel_attn_fwd_noalloc(const void *q, const void *k, const void *v,
  * A row whose target lies outside [0, vocab) (a negative padding label, say)
  * is empty: its loss is 0, whatever h_i holds, and its lse is still
  * computed.  A row whose every logit is -infinity has lse -infinity and
- * loss 0.  A bias entry of -infinity takes its token out of the vocabulary.
+ * loss 0.  A bias entry of -infinity takes its token out of the vocabulary
+ * (its row of w has to be finite all the same).
  *
  * h         : device, dtype [rows][d_model] (any leading shape: a T-major
  *             [positions][batch][d_model] buffer has rows = positions*batch).
@@ -427,7 +428,8 @@ txl_status txl_rel_attn_fwd_noalloc(const void *q, const void *k, const void *v,
  * piece by piece into the workspace first (not for a handful of rows with
  * d_model <= 1024 and w 16-byte aligned).
  * rows == 0: nothing to do.  d_model >= 1, vocab >= 1, else TXL_ERR_INVALID;
- * vocab <= 2^30 and rows <= 2^30, else TXL_ERR_UNSUPPORTED.  Asynchronous on
+ * vocab, rows and d_model <= 2^30 and at most 2^40 elements in h and in w,
+ * else TXL_ERR_UNSUPPORTED.  Asynchronous on
  * stream; no allocation; results do not depend on what else runs (no
  * atomics: the same call gives the same bits).  bf16: products of bf16
  * operands, accumulated and normalised in fp32.
@@ -455,9 +457,10 @@ txl_status txl_softmax_xent_fwd(const void *h, const void *w, const float *bias,
  * workspace : as above, for backward = 1 (which also suffices for the
  *             forward).
  * rows == 0: dw and dbias are set to 0.  Outputs must not overlap each other,
- * any input or the workspace.  bf16: dz is rounded at most once to bf16 for the two
- * products (fp32 accumulation over the whole vocabulary and all rows, one
- * rounding of the results); dbias sums the unrounded dz.
+ * any input or the workspace.  bf16: with more than 128 rows dz is rounded
+ * once to bf16 for the two products, else it keeps at least 16 bits (fp32
+ * accumulation over the whole vocabulary and all rows, one rounding of the
+ * results); dbias sums the unrounded dz.
  */
 txl_status txl_softmax_xent_bwd(const void *h, const void *w, const float *bias, const int64_t *target,
                                 const float *lse, const float *dloss, int rows, int d_model, int vocab,
@@ -480,7 +483,7 @@ txl_status txl_softmax_xent_bwd(const void *h, const void *w, const float *bias,
  * teacher_idx    : device, int64 [rows][top_k], in any order.
  * teacher_logits : device, teacher_dtype [rows][top_k].
  * 1 <= top_k (else TXL_ERR_INVALID), top_k <= 256 (else
- * TXL_ERR_UNSUPPORTED); temperature finite and > 0.
+ * TXL_ERR_UNSUPPORTED); temperature and its inverse finite and > 0.
  */
 txl_status txl_distill_workspace(int rows, int d_model, int vocab, int top_k, txl_dtype dtype, int backward,
                                  size_t *bytes);

@@ -24,6 +24,11 @@ def _lib():
     abi.load_library()
 
 
+def abi_library():
+    from transformer_xl_relative_rel_gb300 import abi
+    return abi.load_library()
+
+
 def _inputs(rows, d, vocab, dtype, seed, bias=True, k=None, t_dtype=F32):
     g = torch.Generator(device="cuda").manual_seed(seed)
     r = lambda *s: torch.randn(*s, device="cuda", generator=g)
@@ -149,6 +154,65 @@ def test_few_rows_edges(dtype, d):
     g = _xent(p)
     assert (g["lse"] == -float("inf")).all() and not g["loss"].any()
     assert not g["dh"].any() and not g["dw"].any() and not g["db"].any()
+    txl.check()
+
+
+@pytest.mark.parametrize("dtype,rows,d,vocab", [(BF, 70, 64, 3000), (BF, 300, 72, 5003), (F32, 90, 41, 700)])
+def test_each_gradient_alone(dtype, rows, d, vocab):
+    import transformer_xl_relative_rel_gb300 as txl
+    p = _inputs(rows, d, vocab, dtype, 6, k=7)
+    loss, lse = txl.softmax_xent_fwd(p["h"], p["w"], p["target"], bias=p["bias"])
+    t_loss, t_lse = txl.distill_fwd(p["h"], p["w"], p["idx"], p["y"], 2.0, bias=p["bias"])
+    f = abi_library()
+    code = {BF: txl.TXL_BF16, F32: txl.TXL_F32}[dtype]
+    ws = torch.empty(txl.distill_workspace_bytes(rows, d, vocab, 7, code, backward=True), dtype=torch.uint8, device="cuda")
+    at = lambda x: None if x is None else x.data_ptr()
+    for op, whole in (("xent", _xent(p)), ("distill", _distill(p, 2.0))):
+        for names in (("dh",), ("dw",), ("db",), ("dw", "db"), ("dh", "db"), ("dh", "dw")):
+            g = {n: torch.full_like(whole[n], 7.0) if n in names else None for n in ("dh", "dw", "db")}
+            out = [at(g[n]) for n in ("dh", "dw", "db")] + [at(ws), ws.numel(), torch.cuda.current_stream().cuda_stream]
+            head = [at(p["h"]), at(p["w"]), at(p["bias"])]
+            if op == "xent":
+                st = f.txl_softmax_xent_bwd(*head, at(p["target"]), at(lse), at(p["dloss"]), rows, d, vocab, code, *out)
+            else:
+                st = f.txl_distill_bwd(*head, at(p["idx"]), at(p["y"]), 0, 2.0, at(t_lse), at(p["dloss"]), rows, d, vocab,
+                                       7, code, *out)
+            assert st == 0
+            for n in names:
+                assert torch.equal(g[n], whole[n]), (op, names, n)
+    txl.check()
+
+
+def test_few_rows_unaligned_weights():
+    for dtype, d in ((BF, 64), (BF, 41), (F32, 64), (F32, 31)):
+        p = _inputs(7, d, 900, dtype, 8, k=5)
+        flat = torch.empty(p["w"].numel() + 1, dtype=dtype, device="cuda")
+        w = flat[1:].view_as(p["w"])
+        w.copy_(p["w"])
+        _check_xent(dict(p, w=w))
+        _check_distill(dict(p, w=w), 2.0)
+
+
+@pytest.mark.parametrize("dtype,rows,d,vocab", [(BF, 3, 1023, 2100003), (BF, 40, 1024, 2100003), (BF, 200, 1024, 2100003),
+                                                (F32, 2, 1024, 1050003), (F32, 20, 1024, 2100003)])
+def test_offsets_past_32_bits(dtype, rows, d, vocab):
+    """Only the last 500 tokens take part (the others' bias is -infinity): the
+    result is that of a vocabulary of 500."""
+    import transformer_xl_relative_rel_gb300 as txl
+    n = 500
+    p = _inputs(rows, d, n, dtype, 9)
+    w = torch.empty(vocab, d, dtype=dtype, device="cuda").normal_(std=2 / math.sqrt(d),
+                                                                  generator=torch.Generator(device="cuda").manual_seed(1))
+    w[-n:] = p["w"]
+    bias = torch.full((vocab,), -float("inf"), device="cuda")
+    bias[-n:] = p["bias"]
+    y = p["target"]
+    far = torch.where((y >= 0) & (y < n), y + (vocab - n), y.clamp(max=-1))
+    got = _xent(dict(p, w=w, bias=bias, target=far))
+    assert not got["db"][:-n].any()
+    for x in got["dw"][:-n].split(200000):
+        assert not x.any()
+    _check_xent(p, got=dict(got, dw=got["dw"][-n:].clone(), db=got["db"][-n:]))
     txl.check()
 
 

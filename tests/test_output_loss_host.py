@@ -58,6 +58,8 @@ def test_bad_arguments(op, backward):
     assert c(vocab=0) == INVALID
     assert c(vocab=(1 << 30) + 1, nws=1 << 60) == UNSUPPORTED
     assert c(rows=(1 << 30) + 1) == UNSUPPORTED
+    assert c(d=2 ** 31 - 1) == UNSUPPORTED
+    assert c(d=1 << 20, vocab=(1 << 20) + 1, nws=1 << 60) == UNSUPPORTED
     for name in ("h", "w", "idx", "ws") + (("lse", "dloss") if backward else ("loss", "lse_out")):
         assert c(**{name: None}) == INVALID, name
     assert c(nws=256) == INVALID
@@ -88,7 +90,7 @@ def test_bad_teacher_arguments(backward):
     assert c(ydt=5) == UNSUPPORTED
     assert c(y=None) == INVALID
     assert c(y=FAKE * 5 + 2) == INVALID
-    for t in (0.0, -1.0, float("nan"), float("inf")):
+    for t in (0.0, -1.0, float("nan"), float("inf"), 1e-40):
         assert c(t=t) == INVALID
 
 

@@ -644,7 +644,7 @@ class _LossCall:
     def gradients(self, grads, w, bias, weight_grads):
         """The dict of a backward's outputs (given tensors used, absent ones made) and their pointers."""
         import torch
-        grads = {} if grads is None else grads
+        grads = {} if grads is None else dict(grads)
         given = [self.arg("dh", grads.get("dh"), self.h.shape, self.h.dtype)]
         if weight_grads:
             given.append(self.arg("dw", grads.get("dw"), w.shape, w.dtype))

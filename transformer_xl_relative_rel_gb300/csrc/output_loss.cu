@@ -460,7 +460,8 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb)
 
 constexpr size_t kPieceBytes = (size_t)512 << 20;  // at most this for one piece of dz and of copied weights
 constexpr size_t kWeightBytes = (size_t)64 << 20;  // ... for the forward's copied weights
-constexpr int kMaxSize = 1 << 30;                  // rows and vocabulary
+constexpr int kMaxSize = 1 << 30;                  // rows, vocabulary and d_model
+constexpr int64_t kMaxElements = (int64_t)1 << 40; // of h and of w
 
 long up(long a, long b) { return (a + b - 1) / b * b; }
 
@@ -626,7 +627,8 @@ txl_status loss_sizes(int rows, int d, int vocab, int K, txl_dtype dtype)
 {
     if (dtype != TXL_F32 && dtype != TXL_BF16) return TXL_ERR_UNSUPPORTED;
     if (rows < 0 || d < 1 || vocab < 1 || K < 0) return TXL_ERR_INVALID;
-    if (K > kMaxTopK || rows > kMaxSize || vocab > kMaxSize) return TXL_ERR_UNSUPPORTED;
+    if (K > kMaxTopK || rows > kMaxSize || vocab > kMaxSize || d > kMaxSize) return TXL_ERR_UNSUPPORTED;
+    if ((int64_t)(rows > vocab ? rows : vocab) * d > kMaxElements) return TXL_ERR_UNSUPPORTED;
     return TXL_OK;
 }
 
@@ -639,6 +641,8 @@ txl_status loss_workspace(int rows, int d, int vocab, int K, txl_dtype dtype, in
     return TXL_OK;
 }
 
+float alpha_of(const LossArgs &a) { return 1.f / (kLn2 * (a.temp != 0.f ? a.temp : 1.f)); }
+
 // (fills *plan when there are rows)
 txl_status loss_checks(const LossArgs &a, bool backward, LossPlan *plan)
 {
@@ -647,7 +651,8 @@ txl_status loss_checks(const LossArgs &a, bool backward, LossPlan *plan)
     const bool distill = a.K > 0;
     if (distill) {
         if (a.t_dtype != TXL_F32 && a.t_dtype != TXL_BF16) return TXL_ERR_UNSUPPORTED;
-        if (!(a.temp > 0.f) || isinf(a.temp)) return TXL_ERR_INVALID;
+        // (1 / t has to be finite too)
+        if (!(a.temp > 0.f) || isinf(a.temp) || isinf(alpha_of(a))) return TXL_ERR_INVALID;
     }
     const size_t esz = a.dtype == TXL_F32 ? 4 : 2, tsz = a.t_dtype == TXL_F32 ? 4 : 2;
     const size_t n = (size_t)a.rows;
@@ -683,8 +688,6 @@ txl_status loss_checks(const LossArgs &a, bool backward, LossPlan *plan)
     *plan = loss_plan(a.rows, a.d, a.vocab, a.K, a.dtype, backward, al(a.h, 16), al(a.w, 16));
     return a.ws_bytes < plan->bytes ? TXL_ERR_INVALID : TXL_OK;
 }
-
-float alpha_of(const LossArgs &a) { return 1.f / (kLn2 * (a.temp != 0.f ? a.temp : 1.f)); }
 
 LossRows rows_at(const LossArgs &a, const LossPlan &q)
 {
