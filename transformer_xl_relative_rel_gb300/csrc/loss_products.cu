@@ -5,7 +5,7 @@
 //   lse       A = h, B = W: the running maximum and sum of the softmax over a
 //             strip of vocabulary tiles, the logits themselves never stored;
 //   dz        A = h, B = W: dz = coef (softmax - listed weights) of one
-//             vocabulary piece, rounded to bf16 and stored;
+//             vocabulary piece, in the bf16 parts that dz_parts() says;
 //   contract  dW = dz^T h (A = dz^T read as it is stored, MN-major tiles; B =
 //             h^T from a transposed copy of h) and dh = dz W, as its transpose
 //             W^T dz^T (A = W^T as W is stored, B = dz), turned back on the
@@ -20,6 +20,18 @@
 // n additions comes out about n 2^-25 too small), so with fp32 operands an
 // accumulator takes two 64-deep steps (8 additions of the largest products)
 // and the epilogue warps add these in registers, rounding to nearest.
+//
+// What bounds them (GB300, device time of a launch, bf16): with many rows the
+// tensor pipe.  6144 x 1024 over 131072 tokens: lse 888 us (1857 TFLOP/s), dz
+// 257 us per 32768 of them (1604; it stores 403 MB meanwhile), both products
+// of that piece in one launch 474 us (1739).  At d_model 512 a tile has half
+// the products for the same epilogue: 16384 x 512 over 65536 tokens lse 653
+// us (1683), dz 762 (1443; with 64 listed columns per row 23% more before the
+// lists were searched by several probes at once), products 1372 (1603).  A
+// bias costs lse 7% and dz 12% there (9000 x 410 x 50021).  Up to 128 rows
+// the weights' way from memory: 128 x 1024 over 65536 tokens 25 us (5.3 TB/s).
+// fp32 operands take six part products and twice as many, narrower tiles:
+// 1111 x 410 x 20011 lse 107 us (1020 TFLOP/s of part products).
 //
 // Roles (12 warps): warp 0 issues the TMA loads, warp 1 the MMAs, warps 4-11
 // are two epilogue groups of four (a warp per 32 TMEM lanes), which share a

@@ -55,7 +55,9 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return
 // What has to be ready before the products, in one launch whose blocks take
 // different parts (none of them for a forward cross entropy of aligned bf16
 // operands): the teacher's row lists, unaligned biases, operands that the TMA
-// unit cannot read as they lie, and (backward) h transposed.
+// unit cannot read as they lie, and (backward) h transposed.  Bound by memory
+// latency (each element is read and written once): h^T of 6144 x 1024 in 11
+// us, with 16384 rows of 64 listed columns and 16384 x 512 in 47 us.
 struct CopyJob {
     const void *src;
     __nv_bfloat16 *dst;
@@ -317,6 +319,8 @@ __global__ void __launch_bounds__(256) loss_prep_kernel(const __grid_constant__ 
 // ------------------------------------------------------------ finishing
 // What follows the products of a vocabulary piece, in one launch: the column
 // sums of dz from those of its row groups, and gradients that lie in slots.
+// Bound by the latency of reading them: 192 row groups of 32768 columns (25
+// MB, none of it in L2) in 24 us.
 struct SumJob {
     const float *slot;
     void *out;
@@ -385,6 +389,8 @@ __global__ void __launch_bounds__(1024) loss_finish_kernel(const __grid_constant
 // Joins the strips of a row's softmax and its listed logits: kRows rows per
 // block (coalesced over rows), 1024 / kRows threads share a row's slots, then
 // a warp its entries.  8 rows where there are few, so that more SMs read.
+// Hardly more than its launch: 6144 rows 6 us, 16384 rows with 64 entries
+// each 15 us.
 template <int kRows>
 __global__ void __launch_bounds__(1024)
 loss_merge_kernel(const float2 *__restrict__ part, int slots, const float *__restrict__ ysel, LossRows r, float t2,
