@@ -586,12 +586,12 @@ class _LossCall:
     (so that a workspace freed at return is reused only behind the call)."""
 
     def __init__(self, h, w, stream):
-        d = h.shape[-1] if h.dim() else -1
-        if w.dim() != 2 or w.shape[1] != d or w.dtype != h.dtype:
+        shape, w_shape = h.shape, w.shape
+        if len(w_shape) != 2 or not shape or w_shape[1] != shape[-1] or w.dtype != h.dtype:
             raise ValueError("w must be [vocab, d_model] with h's last dimension and dtype")
-        self.lead = h.shape[:-1]
+        self.lead = shape[:-1]
         self.rows = self.lead.numel()
-        self.vocab, self.d = w.shape
+        self.vocab, self.d = w_shape
         self.code = _dtype_code(h)
         self.dev = h.get_device()
         self.h, self.stream = h, stream
@@ -630,9 +630,9 @@ class _LossCall:
             workspace = self.make((need(),), torch.uint8)
         elif workspace.get_device() != self.dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous CUDA tensor on the other tensors' device")
-        nbytes = workspace.numel() * workspace.element_size()
+        nbytes = workspace.nbytes
         stream = self.stream.cuda_stream if self.stream is not None else torch._C._cuda_getCurrentRawStream(self.dev)
-        if torch.cuda.current_device() == self.dev:
+        if torch._C._cuda_getDevice() == self.dev:
             st = fn(*args, workspace.data_ptr(), nbytes, stream)
         else:
             with torch.cuda.device(self.dev):

@@ -1,7 +1,7 @@
-// loss_few.cu -- the output-layer losses for a handful of rows whose weights
-// the tensor-core kernel could only read through a copy (fp32 operands, which
-// it takes as three bf16 parts, and bf16 rows that the TMA unit cannot
-// address), on the CUDA cores.
+// loss_few.cu -- the output-layer losses for a handful of rows on the CUDA
+// cores: where the tensor-core kernel could only read the weights through a
+// copy (fp32 operands, which it takes as three bf16 parts, and bf16 rows that
+// the TMA unit cannot address), and small vocabularies.
 //
 // With few rows both directions are bound by moving the weights: every element
 // takes 2 * rows operations per product, below what the CUDA cores do while
@@ -113,7 +113,7 @@ struct FewParams {
     float2 *part;                   // [block][rows]
     void *dw;                       // backward
     bool dw_vec;                    // dw is aligned to kV elements
-    float *db, *dh_part;            // dh_part: [block][rows][d]
+    float *db, *dh_part;            // dh_part: [block][group][rows][d]
 };
 
 // The row lists, followed along the vocabulary by thread `row` < rows; the
@@ -354,11 +354,14 @@ __global__ void __launch_bounds__(kThreads) few_bwd_kernel(const __grid_constant
     const int rl = ((tid & 31) * 2 * kR / 32) % kR;
     const float c_mine = coef[rl], l_mine = l2[rl];
     __syncthreads();
+    // narrow rows leave room for groups of threads that take the tokens in turn
+    // (fp32 8 x 64 x 65000, both directions: one group 106 us, 16 groups 58 us)
     float hr[kR][kC], dh[kR][kC];
     int col[kC];
+    const int group = tid / (kThreads / p.s.groups), tx = tid % (kThreads / p.s.groups);
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
-        col[i] = (i / kV * kThreads + tid) * kV + i % kV;
+        col[i] = (i / kV * (kThreads / p.s.groups) + tx) * kV + i % kV;
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
             hr[r][i] = col[i] < p.d ? sm.hs[r * p.dp + col[i]] : 0.f;
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(kThreads) few_bwd_kernel(const __grid_constant
             p.db[n0 + tid] = s;
         }
 #pragma unroll 2
-        for (int j = 0; j < n1 - n0; ++j) {
+        for (int j = group; j < n1 - n0; j += p.s.groups) {
             float z[kR];
 #pragma unroll
             for (int r = 0; r < kR; r += 2) {
@@ -427,7 +430,7 @@ __global__ void __launch_bounds__(kThreads) few_bwd_kernel(const __grid_constant
 #pragma unroll
             for (int i = 0; i < kC; ++i)
                 if (r < p.rows && col[i] < p.d)
-                    p.dh_part[((long)blockIdx.x * p.rows + r) * p.d + col[i]] = dh[r][i];
+                    p.dh_part[(((long)blockIdx.x * p.s.groups + group) * p.rows + r) * p.d + col[i]] = dh[r][i];
 }
 
 // dh = the blocks' parts, added in order: 32 elements per block, 32 threads each.
@@ -498,10 +501,13 @@ bool few_shape(int rows, int d, int vocab, bool f32, bool w_ok, FewShape *s)
 {
     // Both directions, this kernel / the tensor-core kernel: fp32 16 x 768 x
     // 90326 406 / 677 us, 2 x 512 x 204 26 / 50 us; bf16 8 x 769 x 90326 351 /
-    // 475 us, 8 x 410 x 20011 69 / 75 us.  Rows that the tensor-core kernel
-    // reads in place stay with it: bf16 8 x 768 x 90326 342 us here, 172 there.
+    // 475 us, 8 x 410 x 20011 67 / 75 us.  bf16 rows that the tensor-core kernel
+    // reads in place are this one's while launches are most of the time (two
+    // less): 8 x 512 x 3000 28 / 34 us, 8 x 512 x 8000 37 / 44, but 8 x 64 x 40000
+    // 56 / 48 and 8 x 768 x 90326 342 / 172.
     // w has to be aligned for the bulk copies, h and dh stay in registers.
-    if (!w_ok || d > kFewColumns || rows > (f32 ? 16 : 8) || (!f32 && d % 8 == 0)) return false;
+    const bool in_place = !f32 && d % 8 == 0, small = vocab <= (16 << 10) && (int64_t)vocab * d <= (4 << 20);
+    if (!w_ok || d > kFewColumns || rows > (f32 ? 16 : 8) || (in_place && !small)) return false;
     // chunks as large as leave a ring of three, and a ring as deep as fits
     const uint32_t room = kFewSmem - fixed_bytes(rows, d);
     s->tok = 64;
@@ -514,6 +520,8 @@ bool few_shape(int rows, int d, int vocab, bool f32, bool w_ok, FewShape *s)
     const long chunks = ((long)vocab + s->tok - 1) / s->tok, each = (chunks + sms - 1) / sms;
     s->per = (int)each * s->tok;
     s->blocks = (int)((chunks + each - 1) / each);
+    s->groups = 1;
+    while (s->groups < 16 && 2 * s->groups * d <= kFewColumns) s->groups <<= 1;
     return true;
 }
 
@@ -553,8 +561,9 @@ cudaError_t launch_loss_few(const FewCall &a, cudaStream_t s)
     const int n = a.rows * a.d;
     const unsigned blocks = (unsigned)(n + 31) / 32;
     const float *part = a.dh_part;
-    return a.f32 ? loss_launch(few_finish_kernel<float>, blocks, 1024, 0, 1, s, part, a.s.blocks, n, (float *)a.dh)
-                 : loss_launch(few_finish_kernel<__nv_bfloat16>, blocks, 1024, 0, 1, s, part, a.s.blocks, n,
+    const int parts = a.s.blocks * a.s.groups;
+    return a.f32 ? loss_launch(few_finish_kernel<float>, blocks, 1024, 0, 1, s, part, parts, n, (float *)a.dh)
+                 : loss_launch(few_finish_kernel<__nv_bfloat16>, blocks, 1024, 0, 1, s, part, parts, n,
                                (__nv_bfloat16 *)a.dh);
 }
 

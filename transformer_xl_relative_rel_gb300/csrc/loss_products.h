@@ -144,6 +144,7 @@ constexpr int kFewColumns = 1024;   // widest d_model
 struct FewShape {
     int tok, slots;    // tokens per chunk, chunks in the ring
     int per, blocks;   // tokens per block
+    int groups;        // of threads that take a chunk's tokens in turn (backward)
 };
 // false: sizes for the tensor-core kernel.  w_ok: w is 16-byte aligned.
 bool few_shape(int rows, int d, int vocab, bool f32, bool w_ok, FewShape *s);
@@ -158,7 +159,7 @@ struct FewCall {
     float *ysel;         // forward: as launch_loss_lse
     float2 *part;        // ... [blocks][rows]
     void *dh, *dw;       // backward; each and db may be NULL
-    float *db, *dh_part; // dh_part: [blocks][rows][d]
+    float *db, *dh_part; // dh_part: [blocks * groups][rows][d]
 };
 cudaError_t launch_loss_few(const FewCall &a, cudaStream_t s);
 cudaError_t read_and_clear_few_error(unsigned int *word, cudaStream_t s);

@@ -513,7 +513,7 @@ LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool back
         q.ent = take(distill ? n * 4 : 0);
         q.slots = q.shape.blocks;
         if (backward) {
-            q.dh_acc = take(n * q.shape.blocks * d * 4);
+            q.dh_acc = take(n * q.shape.blocks * q.shape.groups * d * 4);
         } else {
             q.ysel = take(n * (distill ? K : 1) * 4);
             q.part = take(n * q.slots * 8);
@@ -584,6 +584,12 @@ int g_plan_n = 0, g_plan_next = 0;
 
 LossPlan loss_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool backward, bool h_ok, bool w_ok)
 {
+    // alignment that makes no difference is left out of the key
+    FewShape few;
+    if (few_shape(rows, d, vocab, dtype == TXL_F32, w_ok, &few))
+        h_ok = false;
+    else if (dtype != TXL_BF16 || d % 8)
+        h_ok = w_ok = false;
     const PlanKey key = {rows, d, vocab, K, (int)dtype, backward * 4 + h_ok * 2 + w_ok, device_sm_count()};
     {
         std::lock_guard<std::mutex> lock(g_plan_mu);
