@@ -464,8 +464,11 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb)
     return x < y + nb && y < x + na;
 }
 
-constexpr size_t kPieceBytes = (size_t)512 << 20;  // at most this for one piece of dz and of copied weights
-constexpr size_t kWeightBytes = (size_t)64 << 20;  // ... for the forward's copied weights
+// At most this for one piece of dz and of copied weights.  Smaller pieces would
+// stay in L2, but each costs a launch and a drain: forward of fp32 20 x 1024 x
+// 131072 with 64, 128, 256, 512 MB of weights 558, 545, 463, 410 us, bf16 128 x
+// 769 x 131072 163, 141, 130, 130 us.
+constexpr size_t kPieceBytes = (size_t)512 << 20;
 constexpr int kMaxSize = 1 << 30;                  // rows, vocabulary and d_model
 constexpr int64_t kMaxElements = (int64_t)1 << 40; // of h and of w
 
@@ -526,7 +529,7 @@ LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool back
     // what a vocabulary column of a piece takes; pieces start at multiples of the widest tile
     q.dz_rows = backward ? dz_rows(rows, q.parts) : 0;
     const size_t per = ((size_t)q.dz_rows + (q.copy_w ? (size_t)q.dp : 0)) * q.parts * 2;
-    size_t most = per ? (backward ? kPieceBytes : kWeightBytes) / per / kLossPieceUnit * kLossPieceUnit : (size_t)vocab;
+    size_t most = per ? kPieceBytes / per / kLossPieceUnit * kLossPieceUnit : (size_t)vocab;
     if (most < (size_t)kLossPieceUnit) most = kLossPieceUnit;
     if (backward)
         q.piece = gradient_piece(rows, d, vocab, q.parts, most < (size_t)kMaxSize ? (int)most : kMaxSize);
