@@ -420,6 +420,50 @@ def test_captured_and_replayed():
     txl.check()
 
 
+@pytest.mark.parametrize("dtype,rows", [(F32, 5), (BF, 40)])
+def test_few_rows_captured_and_replayed(dtype, rows):
+    p = _inputs(rows, 72, 1500, dtype, 84, k=5)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        a, b = _xent(p), _distill(p, 2.0)
+    for seed in (85, 86):
+        q = _inputs(rows, 72, 1500, dtype, seed, k=5)
+        for n in ("h", "w", "bias", "dloss", "target", "idx", "y"):
+            p[n].copy_(q[n])
+        g.replay()
+        g.replay()
+        torch.cuda.synchronize()
+        _check_xent(q, got=a)
+        _check_distill(q, 2.0, got=b)
+
+
+def test_host_threads_at_once():
+    import threading
+    shapes = [(5, 72, 900, F32), (300, 64, 2000, BF), (20, 128, 700, BF), (90, 40, 300, F32)]
+    ps = [_inputs(r, d, v, t, 95 + r, k=6) for r, d, v, t in shapes]
+    want = [(_xent(p), _distill(p, 2.0)) for p in ps]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(x):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(15):
+                got = _xent(ps[x]), _distill(ps[x], 2.0)
+            s.synchronize()
+        for a, b in zip(got, want[x]):
+            wrong.extend((x, n) for n in b if not torch.equal(a[n], b[n]))
+
+    threads = [threading.Thread(target=work, args=(x,)) for x in range(len(ps))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
+
+
 def test_gradients_match_differences_of_the_forward():
     """fp32: (L(x + e) - L(x - e)) / 2e along random directions."""
     import transformer_xl_relative_rel_gb300 as txl
