@@ -26,9 +26,9 @@
 // 257 us per 32768 of them (1604; it stores 403 MB meanwhile), both products
 // of that piece in one launch 474 us (1739).  At d_model 512 a tile has half
 // the products for the same epilogue: 16384 x 512 over 65536 tokens lse 653
-// us (1683), dz 762 (1443; with 64 listed columns per row 23% more before the
-// lists were searched by several probes at once), products 1372 (1603).  A
-// bias costs lse 7% and dz 12% there (9000 x 410 x 50021).  Up to 128 rows
+// us (1683), dz 762 (1443), products 1372 (1603); 64 listed columns per row
+// cost lse 6% and dz some 15%, half of it the search at the start of a strip.
+// A bias costs lse 7% and dz 12% there (9000 x 410 x 50021).  Up to 128 rows
 // the weights' way from memory: 128 x 1024 over 65536 tokens 25 us (5.3 TB/s).
 // fp32 operands take six part products and twice as many, narrower tiles:
 // 1111 x 410 x 20011 lse 107 us (1020 TFLOP/s of part products).
@@ -748,7 +748,7 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                 }
                 // listed columns: every row's next one at once; a thread asks the
                 // four lanes that follow its rows' lists
-                while (__any_sync(0xffffffffu, cur.c0 < col0 + 32)) {
+                while (const unsigned rows = __ballot_sync(0xffffffffu, cur.c0 < col0 + 32)) {
                     const bool hit = cur.c0 < col0 + 32;
                     const int mc = hit ? cur.c0 - col0 : 64;
                     const float mine = hit && coef != 0.f ? -coef * cur.p0 : 0.f;
@@ -756,6 +756,7 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                     __syncwarp();
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
+                        if (((rows >> (8 * r)) & 0xffu) == 0) continue;
                         const int c = __shfl_sync(0xffffffffu, mc, (lane >> 2) + 8 * r);
                         const float g = __shfl_sync(0xffffffffu, mine, (lane >> 2) + 8 * r);
                         const int at = ((c >> 1) & 3) == (lane & 3) ? c >> 3 : 8;
