@@ -110,7 +110,8 @@ def test_distill_sizes(rows, d, vocab, k, t, dtype, t_dtype):
 # few rows: heights 2, 8, 16 and the first past them, rows of every alignment,
 # chunks of 16 to 64 tokens, blocks of one and of many chunks, the widest rows
 FEW = [(1, 1, 1), (2, 3, 17), (1, 1024, 9001), (2, 410, 20011), (3, 30, 65), (8, 769, 3001), (9, 64, 64),
-       (8, 1023, 5001), (15, 2, 40000), (16, 1024, 5003), (16, 410, 2433), (17, 410, 300), (7, 1025, 200), (5, 6, 9729)]
+       (8, 1023, 5001), (15, 2, 40000), (16, 1024, 5003), (16, 410, 2433), (17, 410, 300), (7, 1025, 200), (5, 6, 9729),
+       (2, 1024, 512), (8, 100, 513), (16, 128, 512), (8, 256, 500), (1, 8, 129)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])

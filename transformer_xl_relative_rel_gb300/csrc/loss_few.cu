@@ -12,7 +12,8 @@
 //   logits    a warp takes two tokens, its lanes lie along d_model; h in shared
 //             memory, fp32 products and sums;
 //   forward   each thread keeps the maximum and sum of some of the chunk's
-//             tokens for one row;
+//             tokens for one row; loss_merge_kernel joins the blocks, or they
+//             do it themselves as a cluster;
 //   backward  dz of the chunk in shared memory (fp32, not rounded); then the
 //             threads take columns of d_model: dW = dz^T h is written once,
 //             dh += dz W stays in registers.  few_finish_kernel adds the
@@ -42,6 +43,7 @@ __device__ unsigned int g_few_err;
 
 constexpr int kThreads = 256;
 constexpr int kMaxSlots = 8;
+constexpr int kCluster = 8;                           // blocks that join their parts themselves
 constexpr int kFewSmem = 220 * 1024;                  // dynamic shared memory at most
 constexpr uint64_t kFewWaitNs = 2000000000ull;        // 2 s per wait, then give up
 
@@ -111,6 +113,7 @@ struct FewParams {
     float alpha;
     float *ysel;                    // forward
     float2 *part;                   // [block][rows]
+    float t2, *loss, *lse;          // of a joined shape
     void *dw;                       // backward
     bool dw_vec;                    // dw is aligned to kV elements
     float *db, *dh_part;            // dh_part: [block][group][rows][d]
@@ -313,14 +316,25 @@ __global__ void __launch_bounds__(kThreads) few_lse_kernel(const __grid_constant
     }
     state[tid] = make_float2(m, l);
     __syncthreads();
-    if (tid >= p.rows) return;
-    for (int x = tid + kR; x < kThreads; x += kR) {
-        const float2 e = state[x];
+    auto join = [&](float2 e) {
         const float mm = fmaxf(m, e.x), ref = mm == -INFINITY ? 0.f : mm;
         l = l * exp2f(m - ref) + e.y * exp2f(e.x - ref);
         m = mm;
+    };
+    if (tid < p.rows) {
+        for (int x = tid + kR; x < kThreads; x += kR) join(state[x]);
+        p.part[(long)blockIdx.x * p.rows + tid] = make_float2(m, l);
     }
-    p.part[(long)blockIdx.x * p.rows + tid] = make_float2(m, l);
+    if (!p.s.joined) return;
+    // the cluster's first block takes what the others have left
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+    if (blockIdx.x) return;
+    for (int row = tid >> 5; row < p.rows; row += kThreads / 32) {
+        m = -INFINITY;
+        l = 0.f;
+        for (int x = 0; x < p.s.blocks; ++x) join(__ldcg(p.part + (long)x * p.rows + row));
+        row_loss(p.r, p.ysel, m == -INFINITY ? 0.f : m, l, p.t2, row, tid & 31, p.loss, p.lse);
+    }
 }
 
 template <typename T, int kV, int kR>
@@ -475,7 +489,7 @@ cudaError_t few_start(K kern, const FewParams &p, size_t smem, std::atomic<uint6
         if (e != cudaSuccess) return e;
         done.fetch_or(bit, std::memory_order_relaxed);
     }
-    return loss_launch(kern, (unsigned)p.s.blocks, kThreads, smem, 1, s, p);
+    return loss_launch(kern, (unsigned)p.s.blocks, kThreads, smem, p.s.joined ? (unsigned)p.s.blocks : 1, s, p);
 }
 
 template <typename T, int kV, int kR>
@@ -497,7 +511,7 @@ cudaError_t few_rows_of(bool backward, const FewParams &p, size_t smem, cudaStre
 
 }  // namespace
 
-bool few_shape(int rows, int d, int vocab, bool f32, bool w_ok, FewShape *s)
+bool few_shape(int rows, int d, int vocab, bool f32, bool w_ok, bool backward, FewShape *s)
 {
     // Both directions, this kernel / the tensor-core kernel: fp32 16 x 768 x
     // 90326 406 / 677 us, 2 x 512 x 204 26 / 50 us; bf16 8 x 769 x 90326 351 /
@@ -508,9 +522,22 @@ bool few_shape(int rows, int d, int vocab, bool f32, bool w_ok, FewShape *s)
     // w has to be aligned for the bulk copies, h and dh stay in registers.
     const bool in_place = !f32 && d % 8 == 0, small = vocab <= (16 << 10) && (int64_t)vocab * d <= (4 << 20);
     if (!w_ok || d > kFewColumns || rows > (f32 ? 16 : 8) || (in_place && !small)) return false;
-    // chunks as large as leave a ring of three, and a ring as deep as fits
     const uint32_t room = kFewSmem - fixed_bytes(rows, d);
     s->tok = 64;
+    // a cluster covers a vocabulary that eight blocks are soon through: no launch to
+    // join the blocks then (from Python: bf16 1 x 512 x 256 11.4 -> 9.3 us, 8 x 512 x
+    // 256 11.0 -> 9.2; larger ones want more SMs: 8 x 1024 x 500 11.0 -> 14.8)
+    s->joined = !backward && vocab <= 64 * kCluster && (int64_t)vocab * d * few_height(rows) <= (1 << 20);
+    if (s->joined) {
+        s->per = ((vocab + kCluster - 1) / kCluster + 15) / 16 * 16;
+        while (s->per % s->tok || 2 * slot_bytes(s->tok, d, f32) > room) s->tok >>= 1;
+        s->slots = (int)(room / slot_bytes(s->tok, d, f32));
+        s->slots = s->slots < kMaxSlots ? s->slots : kMaxSlots;
+        s->blocks = (vocab + s->per - 1) / s->per;
+        s->groups = 1;
+        return true;
+    }
+    // chunks as large as leave a ring of three, and a ring as deep as fits
     while (s->tok > 16 && 3 * slot_bytes(s->tok, d, f32) > room) s->tok >>= 1;
     // ... and no larger than gives every SM some
     const long sms = device_sm_count();
@@ -541,6 +568,9 @@ cudaError_t launch_loss_few(const FewCall &a, cudaStream_t s)
     p.alpha = a.alpha;
     p.ysel = a.ysel;
     p.part = a.part;
+    p.t2 = a.t2;
+    p.loss = a.loss;
+    p.lse = a.lse_out;
     p.dw = a.dw;
     p.db = a.db;
     p.dh_part = a.dh ? a.dh_part : nullptr;

@@ -59,6 +59,36 @@ __device__ __forceinline__ float row_factor(const LossRows &r, long i, bool any)
     return any && r.lse[i] != -INFINITY ? r.t * r.dloss[i] : 0.f;
 }
 
+// A row's loss and lse by the lanes of a warp, from its sum l of 2^(y - ref)
+// over the vocabulary and y at its listed columns.
+__device__ __forceinline__ void row_loss(const LossRows &r, const float *ysel, float ref, float l, float t2, long row, int lane,
+                                         float *loss, float *lse)
+{
+    const float y_lse = ref + log2f(l);
+    float dot = 0.f;
+    int any = 0;
+    if (r.target) {
+        any = target_column(r, row) != kNoColumn;
+        if (any && lane == 0) dot = y_lse - __ldcg(ysel + row);
+    } else {
+        for (int k = lane; k < r.K; k += 32) {
+            if (r.col[row * r.K + k] == kNoColumn) continue;
+            any = 1;
+            const float p = r.p[row * r.K + k];
+            if (p != 0.f) dot += p * (y_lse - __ldcg(ysel + row * r.K + k));
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        any |= __shfl_xor_sync(0xffffffffu, any, o);
+    }
+    if (lane == 0) {
+        lse[row] = y_lse * kLn2;
+        loss[row] = any && y_lse != -INFINITY ? t2 * ((r.target ? 0.f : r.ent[row]) + kLn2 * dot) : 0.f;
+    }
+}
+
 // A bf16 matrix in device memory, [pieces][rows][cols] with `pitch` elements
 // between rows (a multiple of 8, 16-byte aligned base).  One piece holds
 // bf16 values; three hold fp32 values as the exact sum of their pieces.
@@ -145,9 +175,10 @@ struct FewShape {
     int tok, slots;    // tokens per chunk, chunks in the ring
     int per, blocks;   // tokens per block
     int groups;        // of threads that take a chunk's tokens in turn (backward)
+    bool joined;       // forward: the blocks are a cluster, which writes losses
 };
 // false: sizes for the tensor-core kernel.  w_ok: w is 16-byte aligned.
-bool few_shape(int rows, int d, int vocab, bool f32, bool w_ok, FewShape *s);
+bool few_shape(int rows, int d, int vocab, bool f32, bool w_ok, bool backward, FewShape *s);
 struct FewCall {
     const void *h, *w;
     const float *bias;
@@ -158,6 +189,7 @@ struct FewCall {
     float alpha;
     float *ysel;         // forward: as launch_loss_lse
     float2 *part;        // ... [blocks][rows]
+    float t2, *loss, *lse_out; // ... of a joined shape
     void *dh, *dw;       // backward; each and db may be NULL
     float *db, *dh_part; // dh_part: [blocks * groups][rows][d]
 };

@@ -430,29 +430,7 @@ loss_merge_kernel(const float2 *__restrict__ part, int slots, const float *__res
     for (int x = tx; x < kLanes; x += 32) l += sl[ty][x] * exp2f(sm[ty][x] - ref);
 #pragma unroll
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const float y_lse = ref + log2f(l);
-    float dot = 0.f;
-    int any = 0;
-    if (r.target) {
-        any = target_column(r, row) != kNoColumn;
-        if (any && tx == 0) dot = y_lse - ysel[row];
-    } else {
-        for (int k = tx; k < r.K; k += 32) {
-            if (r.col[row * r.K + k] == kNoColumn) continue;
-            any = 1;
-            const float p = r.p[row * r.K + k];
-            if (p != 0.f) dot += p * (y_lse - ysel[row * r.K + k]);
-        }
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        any |= __shfl_xor_sync(0xffffffffu, any, o);
-    }
-    if (tx == 0) {
-        lse[row] = y_lse * kLn2;
-        loss[row] = any && y_lse != -INFINITY ? t2 * ((r.target ? 0.f : r.ent[row]) + kLn2 * dot) : 0.f;
-    }
+    row_loss(r, ysel, ref, l, t2, row, tx, loss, lse);
 }
 
 // ---------------------------------------------------------------- host side
@@ -509,7 +487,7 @@ LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool back
     q.parts = dtype == TXL_F32 ? 3 : 1;
     q.dp = (int)up(d, 8);
     const bool tma = dtype == TXL_BF16 && d % 8 == 0;
-    q.few = few_shape(rows, d, vocab, dtype == TXL_F32, w_ok, &q.shape);
+    q.few = few_shape(rows, d, vocab, dtype == TXL_F32, w_ok, backward, &q.shape);
     if (q.few) {
         q.col = take(distill ? n * K * 4 : 0);
         q.p = take(distill ? n * K * 4 : 0);
@@ -590,7 +568,7 @@ LossPlan loss_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool back
 {
     // alignment that makes no difference is left out of the key
     FewShape few;
-    if (few_shape(rows, d, vocab, dtype == TXL_F32, w_ok, &few))
+    if (few_shape(rows, d, vocab, dtype == TXL_F32, w_ok, backward, &few))
         h_ok = false;
     else if (dtype != TXL_BF16 || d % 8)
         h_ok = w_ok = false;
@@ -827,6 +805,8 @@ cudaError_t next_weights(const LossArgs &a, const LossPlan &q, long v0, int cols
     return q.copy_w ? launch_prep(a, p) : cudaSuccess;
 }
 
+float square_of(const LossArgs &a) { return a.temp != 0.f ? a.temp * a.temp : 1.f; }
+
 FewCall few_call(const LossArgs &a, const LossPlan &q, const LossRows &r, bool backward)
 {
     unsigned char *ws = (unsigned char *)a.ws;
@@ -844,6 +824,9 @@ FewCall few_call(const LossArgs &a, const LossPlan &q, const LossRows &r, bool b
     f.alpha = alpha_of(a);
     f.ysel = (float *)(ws + q.ysel);
     f.part = (float2 *)(ws + q.part);
+    f.t2 = square_of(a);
+    f.loss = a.loss;
+    f.lse_out = a.lse_out;
     f.dh = backward ? a.dh : nullptr;
     f.dw = backward ? a.dw : nullptr;
     f.db = backward ? a.db : nullptr;
@@ -870,12 +853,11 @@ cudaError_t run_fwd(const LossArgs &a, const LossPlan &q)
                                 part + slot * a.rows, t, a.s);
         slot += kSlotsPerStrip * vocab_strips(t);
     }
-    if (e != cudaSuccess) return e;
-    const float t2 = a.temp != 0.f ? a.temp * a.temp : 1.f;
+    if (e != cudaSuccess || (q.few && q.shape.joined)) return e;
     const int per = a.rows <= 2048 ? 8 : 32;
     return loss_launch(per == 8 ? loss_merge_kernel<8> : loss_merge_kernel<32>, (unsigned)((a.rows + per - 1) / per), 1024,
-                       0, 1, a.s, (const float2 *)part, q.slots, (const float *)(ws + q.ysel), r, t2, a.loss, a.lse_out,
-                       a.rows);
+                       0, 1, a.s, (const float2 *)part, q.slots, (const float *)(ws + q.ysel), r, square_of(a), a.loss,
+                       a.lse_out, a.rows);
 }
 
 LossOutput direct_out(const LossArgs &a, void *p)
