@@ -82,9 +82,9 @@ struct LSmem {
     static constexpr int ST = (int)((224u * 1024u - LEPI * 4096u * STG) / (ASZ + BSZ));
     static constexpr uint32_t A = 0, B = A + ST * ASZ, OST = B + ST * BSZ, BARS = OST + LEPI * 4096 * STG;
     static constexpr int FULL = 0, EMPTY = ST, AFULL = 2 * ST, AEMPTY = 2 * ST + 2, DONE = 2 * ST + 4,
-                         NBAR = 2 * ST + 5;
-    static constexpr uint32_t MISC = BARS + (NBAR + (NBAR & 1)) * 8;
-    static constexpr uint32_t TOTAL = MISC + 16 + 1024;
+                         JFULL = 2 * ST + 5, JEMPTY = JFULL + 4, NBAR = JEMPTY + 4;
+    static constexpr uint32_t MISC = BARS + (NBAR + (NBAR & 1)) * 8, JOIN = MISC + 16;
+    static constexpr uint32_t TOTAL = JOIN + (MODE == MODE_LSE ? 1024 : 0) + 1024;
     static_assert(TOTAL <= 232448 && ST >= 3, "shared memory");
 };
 
@@ -112,6 +112,7 @@ struct LParams {
     LossRows r;
     float *ysel, *dbpart;
     float2 *part;
+    float *loss, *lse;        // cross entropy whose rows are an item's alone; else NULL
     long dbpitch;
     // contraction: the pairs without a last item of job 0 do `ahead` items of
     // job 1 in the meantime
@@ -151,6 +152,11 @@ __device__ __forceinline__ void l_mma(uint32_t d, uint64_t a, uint64_t b, uint32
             : "memory");
     else
         mma_bf16_ss(d, a, b, idesc, acc);
+}
+// arrives on a barrier of this CTA
+__device__ __forceinline__ void l_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // arrives on the barrier of that offset in every CTA of the tile
 template <int CG>
@@ -519,6 +525,10 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
             mbar_init(bar(S::AEMPTY + b), LEPI * CG);
         }
         mbar_init(bar(S::DONE), 1);
+        for (int x = 0; MODE == MODE_LSE && x < 4; ++x) {
+            mbar_init(bar(S::JFULL + x), 1);
+            mbar_init(bar(S::JEMPTY + x), 1);
+        }
         fence_mbar_init();
         for (int j = 0; j < (MODE == MODE_CT && p.job[1].items ? 2 : 1); ++j) {
             prefetch_tmap(&maps.a[j]);
@@ -1043,8 +1053,33 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                     }
                 }
             }
-            if (MODE == MODE_LSE && ok && live)
+            if (MODE == MODE_LSE && p.loss) {
+                // the strip is the whole vocabulary: the second group's half of each row goes to the
+                // first's warp for the same rows, which is done with the row then (no launch to join
+                // them: 16896 x 512 x 256 forward 15.5 -> 11.0 us)
+                float2 *join = reinterpret_cast<float2 *>(smem + S::JOIN) + 32 * q + lane;
+                if (half) {
+                    if (ok && i > 0) ok = wait(S::JEMPTY + q, (i - 1) & 1);
+                    if (ok) {
+                        *join = make_float2(m * p.alpha, l);
+                        __syncwarp();
+                        if (lane == 0) l_arrive(bar(S::JFULL + q));
+                    }
+                } else if (ok && (ok = wait(S::JFULL + q, i & 1))) {
+                    const float2 e = *join;
+                    __syncwarp();
+                    if (lane == 0) l_arrive(bar(S::JEMPTY + q));
+                    const float ms = m * p.alpha, top = fmaxf(ms, e.x), ref = top == -INFINITY ? 0.f : top;
+                    const float y_lse = ref + log2f(l * exp2f(ms - ref) + e.y * exp2f(e.x - ref));
+                    if (live) {
+                        const bool any = target_column(p.r, row) != kNoColumn && y_lse != -INFINITY;
+                        p.lse[row] = y_lse * kLn2;
+                        p.loss[row] = any ? kLn2 * (y_lse - __ldcg(p.ysel + row)) : 0.f;
+                    }
+                }
+            } else if (MODE == MODE_LSE && ok && live) {
                 p.part[(long)(kSlotsPerStrip * t.strip + half) * p.M + row] = make_float2(m * p.alpha, l);
+            }
         }
         if (lane == 0) bulk_wait_all();
         __syncwarp();
@@ -1061,14 +1096,15 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
 // ------------------------------------------------------------------ host side
 PFN_cuTensorMapEncodeTiled_v12000 l_encode_fn()
 {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> found{nullptr};
+    PFN_cuTensorMapEncodeTiled_v12000 fn = found.load(std::memory_order_relaxed);
     if (!fn) {
         void *ptr = nullptr;
         cudaDriverEntryPointQueryResult q;
         if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
                 cudaSuccess &&
             q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+            found.store(fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr), std::memory_order_relaxed);
     }
     return fn;
 }
@@ -1327,7 +1363,7 @@ int gradient_piece(int rows, int d, int vocab, int parts, int most)
 }
 
 cudaError_t launch_loss_lse(const LossMatrix &h, const LossMatrix &w, const float *bias, int v0, float alpha,
-                            const LossRows &r, float *ysel, float2 *part, const LossTiling &t, cudaStream_t s)
+                            const LossRows &r, float *ysel, float2 *part, float *loss, float *lse, const LossTiling &t, cudaStream_t s)
 {
     LParams p;
     LMaps maps;
@@ -1336,6 +1372,8 @@ cudaError_t launch_loss_lse(const LossMatrix &h, const LossMatrix &w, const floa
     if (e != cudaSuccess) return e;
     p.ysel = ysel;
     p.part = part;
+    p.loss = loss;
+    p.lse = lse;
     return bias ? l_launch_cg<MODE_LSE, true>(t.cg, h.pieces, maps, p, s)
               : l_launch_cg<MODE_LSE, false>(t.cg, h.pieces, maps, p, s);
 }

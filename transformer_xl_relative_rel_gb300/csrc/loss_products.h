@@ -138,9 +138,10 @@ int gradient_piece(int rows, int d, int vocab, int parts, int most);
 // part[2 * strip + half][row] = (maximum, sum of 2^(y - maximum)) over the
 // columns, y = alpha (h . w + bias); ysel[row][k] = y at the listed columns
 // (vocabulary column = v0 + column of w).  bias: of w's columns, 16-byte
-// aligned, or NULL.
+// aligned, or NULL.  With loss and lse (cross entropy whose vocabulary is one
+// strip) the rows' results are written instead of part.
 cudaError_t launch_loss_lse(const LossMatrix &h, const LossMatrix &w, const float *bias, int v0, float alpha,
-                            const LossRows &r, float *ysel, float2 *part, const LossTiling &t, cudaStream_t s);
+                            const LossRows &r, float *ysel, float2 *part, float *loss, float *lse, const LossTiling &t, cudaStream_t s);
 
 // dz = coef (2^(y - l2) - listed weights), in dz's pieces; dbpart[row / 32][column]
 // (pitch dz.pitch) the columns' sums over 32 rows each, when given.

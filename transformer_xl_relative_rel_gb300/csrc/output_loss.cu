@@ -463,6 +463,7 @@ struct LossPlan {
     bool copy_h, copy_w;
     int piece;              // vocabulary columns per piece
     int slots;              // forward: partial softmaxes per row over all pieces
+    bool joined;            // ... which the kernel that makes them joins itself
     bool dh_slots;          // dh of several pieces adds up in slots
     // backward, for a whole piece and for the last one
     struct Piece {
@@ -494,6 +495,7 @@ LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool back
         q.even = take(distill ? n * 4 : 0);
         q.ent = take(distill ? n * 4 : 0);
         q.slots = q.shape.blocks;
+        q.joined = q.shape.joined;
         if (backward) {
             q.dh_acc = take(n * q.shape.blocks * q.shape.groups * d * 4);
         } else {
@@ -527,6 +529,7 @@ LossPlan make_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool back
         q.last.vocab = vocab_tiling(rows, last, d, q.parts);
         const long more = (vocab - last) / q.piece;   // whole pieces before the last one
         q.slots = kSlotsPerStrip * (int)(more * vocab_strips(q.whole.vocab) + vocab_strips(q.last.vocab));
+        q.joined = !distill && more == 0 && q.slots == kSlotsPerStrip;
         q.ysel = take(n * (distill ? K : 1) * 4);
         q.part = take(n * q.slots * 8);
     } else {
@@ -850,10 +853,10 @@ cudaError_t run_fwd(const LossArgs &a, const LossPlan &q)
         if (v0 > 0) e = next_weights(a, q, v0, cols, &w);
         if (e == cudaSuccess)
             e = launch_loss_lse(h, w, bias ? bias + v0 : nullptr, (int)v0, alpha_of(a), r, (float *)(ws + q.ysel),
-                                part + slot * a.rows, t, a.s);
+                                part + slot * a.rows, q.joined ? a.loss : nullptr, q.joined ? a.lse_out : nullptr, t, a.s);
         slot += kSlotsPerStrip * vocab_strips(t);
     }
-    if (e != cudaSuccess || (q.few && q.shape.joined)) return e;
+    if (e != cudaSuccess || q.joined) return e;
     const int per = a.rows <= 2048 ? 8 : 32;
     return loss_launch(per == 8 ? loss_merge_kernel<8> : loss_merge_kernel<32>, (unsigned)((a.rows + per - 1) / per), 1024,
                        0, 1, a.s, (const float2 *)part, q.slots, (const float *)(ws + q.ysel), r, square_of(a), a.loss,
