@@ -1,0 +1,26 @@
+"""The output-layer losses on the GPU where calls, launches, items and pieces
+follow one another: empty batches, calls of different inputs back to back in
+one workspace, row blocks that end inside a warp's rows, vocabularies of one
+strip and of several pieces, and masks of a type's lowest value.  Bounds as in
+tests/loss_helpers.py."""
+import pytest
+import torch
+
+from tests.test_gpu_output_loss import BF, F32, _distill, _inputs, _lib, _xent  # noqa: F401 (_lib: a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("vocab", [257, 32768])
+def test_no_rows_of_larger_vocabularies(vocab, dtype):
+    import transformer_xl_relative_rel_gb300 as txl
+    p = _inputs(0, 64, vocab, dtype, 3, k=3)
+    for fn in (_xent, lambda q: _distill(q, 2.0)):
+        grads = dict(dw=torch.full_like(p["w"], 7.0), db=torch.full_like(p["bias"], 7.0))
+        g = fn(p)
+        assert g["loss"].shape == g["lse"].shape == (0,) and g["dh"].shape == (0, 64)
+        assert not g["dw"].any() and not g["db"].any()
+    g = txl.softmax_xent_bwd(p["h"], p["w"], p["target"], p["dloss"], p["dloss"], bias=p["bias"], grads=grads)
+    assert g["dw"] is grads["dw"] and not g["dw"].any() and not g["db"].any()
+    txl.check()

@@ -1354,7 +1354,7 @@ int gradient_piece(int rows, int d, int vocab, int parts, int most)
             return (vus > hbm ? vus : hbm) + (g > 2 * hbm ? g : 2 * hbm);
         };
         const double us = vocab / cols * cost(cols) + (last ? cost(last) : 0.0);
-        if (us < best) {
+        if (us < best || !best_piece) {
             best = us;
             best_piece = cols;
         }

@@ -634,7 +634,8 @@ txl_status loss_workspace(int rows, int d, int vocab, int K, txl_dtype dtype, in
     if (!bytes) return TXL_ERR_INVALID;
     const txl_status st = loss_sizes(rows, d, vocab, K, dtype);
     if (st != TXL_OK) return st;
-    *bytes = loss_bytes(rows, d, vocab, K, dtype, backward != 0);
+    // (no rows: nothing is planned or launched, and nothing is needed)
+    *bytes = rows ? loss_bytes(rows, d, vocab, K, dtype, backward != 0) : 256;
     return TXL_OK;
 }
 
