@@ -6,7 +6,7 @@ tests/loss_helpers.py."""
 import pytest
 import torch
 
-from tests.test_gpu_output_loss import BF, F32, _distill, _inputs, _lib, _xent  # noqa: F401 (_lib: a fixture)
+from tests.test_gpu_output_loss import BF, F32, _check_distill, _distill, _inputs, _lib, _xent  # noqa: F401 (_lib: a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -24,3 +24,23 @@ def test_no_rows_of_larger_vocabularies(vocab, dtype):
     g = txl.softmax_xent_bwd(p["h"], p["w"], p["target"], p["dloss"], p["dloss"], bias=p["bias"], grads=grads)
     assert g["dw"] is grads["dw"] and not g["dw"].any() and not g["db"].any()
     txl.check()
+
+
+@pytest.mark.parametrize("t", [0.25, 0.5, 1.0, 2.0])
+@pytest.mark.parametrize("t_dtype", [F32, BF])
+@pytest.mark.parametrize("dtype,rows,vocab", [(F32, 5, 300), (BF, 40, 300), (BF, 300, 200), (F32, 140, 150)])
+def test_teacher_logits_of_the_lowest_value(dtype, rows, vocab, t_dtype, t):
+    """A teacher's entries masked by the type's lowest value weigh nothing next
+    to others and are alike where there are no others, at any temperature."""
+    p = _inputs(rows, 64, vocab, dtype, 11, k=6, t_dtype=t_dtype)
+    p["y"][4] = torch.finfo(t_dtype).min          # a whole row
+    p["y"][0, 2:] = torch.finfo(t_dtype).min      # some of a row
+    got = _distill(p, t)
+    torch.cuda.synchronize()
+    # p is 1/6 throughout: the float64 reference takes the same logits divided by t
+    _check_distill(p, t, got=got)
+    one = dict(p, y=p["y"].clone())
+    one["y"][4] = 0.0
+    want = _distill(one, t)
+    for n in got:
+        assert torch.equal(got[n], want[n]), n

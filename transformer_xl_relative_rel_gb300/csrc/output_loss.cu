@@ -99,7 +99,9 @@ __device__ __forceinline__ bool teacher_valid(const PrepArgs &p, long at)
 // distillation: the softmax of a row's valid entries at temperature t, then
 // the entries sorted by the parity of their column's 64-column chunk and the
 // column (a bitonic network over the next power of two).  One warp per row;
-// K2 entries of shared memory per warp.
+// K2 entries of shared memory per warp.  Logits are scaled as differences from
+// the row's largest: scaled first, a row of the type's lowest values at t < 1
+// would be -infinity throughout, and its weights NaN instead of alike.
 constexpr unsigned kNoKey = 0xffffffffu, kOdd = 1u << 31;
 __device__ __forceinline__ void distill_rows(const PrepArgs &p, unsigned *sc, float *sp)
 {
@@ -112,14 +114,14 @@ __device__ __forceinline__ void distill_rows(const PrepArgs &p, unsigned *sc, fl
         const bool valid = k < K && teacher_valid(p, base + k);
         const unsigned c = valid ? (unsigned)p.idx[base + k] : 0u;
         sc[k] = valid ? c | (c & 64u ? kOdd : 0u) : kNoKey;
-        sp[k] = valid ? teacher_logit(p, base + k) * p.inv_t : -INFINITY;
+        sp[k] = valid ? teacher_logit(p, base + k) : -INFINITY;
         top = fmaxf(top, sp[k]);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     float sum = 0.f;
     for (int k = lane; k < K2; k += 32)
-        if (sc[k] != kNoKey) sum += expf(sp[k] - top);
+        if (sc[k] != kNoKey) sum += expf((sp[k] - top) * p.inv_t);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const float lt = logf(sum);
@@ -127,7 +129,7 @@ __device__ __forceinline__ void distill_rows(const PrepArgs &p, unsigned *sc, fl
     for (int k = lane; k < K2; k += 32) {
         float w = 0.f;
         if (sc[k] != kNoKey) {
-            const float lp = sp[k] - top - lt;
+            const float lp = (sp[k] - top) * p.inv_t - lt;
             w = expf(lp);
             if (w != 0.f) ent += w * lp;   // (a NaN teacher logit stays NaN)
         }
