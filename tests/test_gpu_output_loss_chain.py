@@ -6,7 +6,8 @@ tests/loss_helpers.py."""
 import pytest
 import torch
 
-from tests.test_gpu_output_loss import BF, F32, _check_distill, _distill, _inputs, _lib, _xent  # noqa: F401 (_lib: a fixture)
+from tests.test_gpu_output_loss import (BF, F32, _check_distill, _check_xent, _distill, _inputs,  # noqa: F401
+                                        _lib, _xent)
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +45,18 @@ def test_teacher_logits_of_the_lowest_value(dtype, rows, vocab, t_dtype, t):
     want = _distill(one, t)
     for n in got:
         assert torch.equal(got[n], want[n]), n
+
+
+@pytest.mark.parametrize("dtype,vocab", [(BF, 768), (BF, 740), (F32, 384), (F32, 361)])
+def test_row_blocks_that_end_inside_a_warps_rows(dtype, vocab):
+    """39 row blocks of 256, 10 rows in the last: of 117 tiles some pairs of
+    CTAs take a whole block's and the last one's in turn, whose other warps
+    have no rows and leave what is still being stored alone."""
+    p = _inputs(38 * 256 + 10, 64, vocab, dtype, 13, k=5)
+    for fn, ref in ((_xent, _check_xent), (lambda q: _distill(q, 2.0), lambda q, got: _check_distill(q, 2.0, got=got))):
+        got = fn(p)
+        ref(p, got=got)
+        for _ in range(10):
+            again = fn(p)
+            for n in got:
+                assert torch.equal(again[n], got[n]), n

@@ -666,7 +666,8 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
         int nst = 0;
         int lt = 0;
         bool ok = true;
-        // the next staging buffer, once the store that last used it has read it
+        // the next staging buffer, once the store that last used it has read it (every use of one
+        // is followed by a store of its own)
         auto stage_wait = [&]() {
             if (S::STG == 2) {
                 stg_a = stg0 + ((nst++ & 1) ? LEPI * 4096u : 0u);
@@ -729,7 +730,9 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                 }
             }
             auto process_dz = [&](float (&v)[32], const float2 (&bias)[4], int n0, int sub) {
-                if (n0 >= p.N) return;
+                // a warp without rows stages nothing: a staging buffer is taken again by counting
+                // the stores since, and it makes none
+                if (n0 >= p.N || row0 >= p.M) return;
                 const int col0 = p.v0 + n0, c2 = 2 * (lane & 3);   // columns n0 + 8 i + c2 + {0, 1}
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -797,8 +800,7 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                         }
                     }
                     // (columns past the last one lie in the row's padding)
-                    if (row0 < p.M)
-                        p.dbpart[(long)(row0 >> 5) * p.dbpitch + n0 + 8 * (lane >> 3) + c2 + ((lane >> 2) & 1)] = s[0];
+                    p.dbpart[(long)(row0 >> 5) * p.dbpitch + n0 + 8 * (lane >> 3) + c2 + ((lane >> 2) & 1)] = s[0];
                 }
 #pragma unroll
                 for (int part = 0; part < kDzParts; ++part) {
@@ -822,8 +824,8 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                                   w4[0], w4[1], w4[2], w4[3]);
                     }
                     if (kDzParts > 1) {
-                        if (row0 < p.M) store(0, n0, row0, part, false);
-                    } else if ((sub == 1 || n0 + 32 >= p.N) && row0 < p.M) {
+                        store(0, n0, row0, part, false);
+                    } else if (sub == 1 || n0 + 32 >= p.N) {
                         // the second half of the chunk may lie past the last column
                         store(0, n0 - 32 * sub, row0, 0, false);
                     }
