@@ -60,3 +60,79 @@ def test_row_blocks_that_end_inside_a_warps_rows(dtype, vocab):
             again = fn(p)
             for n in got:
                 assert torch.equal(again[n], got[n]), n
+
+
+# rows, d_model, vocabulary, teacher entries, type: a handful of rows (one block, a cluster, many
+# blocks), one and several row blocks, lists of one and of many entries, copied weights and biases
+BACK_TO_BACK = [(5, 72, 300, 4, F32), (3, 41, 4000, 9, BF), (8, 64, 20000, 1, F32), (40, 72, 1500, 5, BF),
+                (300, 64, 3001, 64, BF), (700, 41, 900, 200, BF), (140, 48, 700, 7, F32), (1500, 128, 250, 33, BF)]
+
+
+def _steps(ps, ws, outs):
+    """A training step under each loss for each of ps, all in the workspace ws."""
+    import transformer_xl_relative_rel_gb300 as txl
+    for p, (a, b) in zip(ps, outs):
+        kw = dict(bias=p["bias"], workspace=ws)
+        txl.softmax_xent_fwd(p["h"], p["w"], p["target"], loss=a["loss"], lse=a["lse"], **kw)
+        txl.distill_fwd(p["h"], p["w"], p["idx"], p["y"], 2.0, loss=b["loss"], lse=b["lse"], **kw)
+        txl.softmax_xent_bwd(p["h"], p["w"], p["target"], a["lse"], p["dloss"], grads=a, **kw)
+        txl.distill_bwd(p["h"], p["w"], p["idx"], p["y"], b["lse"], p["dloss"], 2.0, grads=b, **kw)
+
+
+def _unaligned(x):
+    """x, one element behind a 16-byte boundary."""
+    flat = torch.empty(x.numel() + 8, dtype=x.dtype, device=x.device)
+    y = flat[1:1 + x.numel()].view(x.shape)
+    y.copy_(x)
+    return y
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("shapes", [[s] * 6 for s in BACK_TO_BACK] + [BACK_TO_BACK + BACK_TO_BACK[::-1]])
+def test_calls_back_to_back_in_one_workspace(shapes, graph):
+    """Calls of different inputs one behind another with nothing in between:
+    each gives what it gives alone in a workspace of its own."""
+    import transformer_xl_relative_rel_gb300 as txl
+    ps, size = [], 0
+    for x, (rows, d, vocab, k, dtype) in enumerate(shapes):
+        p = _inputs(rows, d, vocab, dtype, 100 + x, k=k)
+        p["bias"] = _unaligned(p["bias"])         # a copy of it is made in the workspace
+        ps.append(p)
+        code = txl.TXL_BF16 if dtype == BF else txl.TXL_F32
+        size = max(size, txl.distill_workspace_bytes(rows, d, vocab, k, code, backward=True))
+    ws = torch.full((size // 4,), float("nan"), device="cuda")
+
+    def outputs():
+        f = lambda n: torch.full((n,), 7.0, device="cuda")
+        return [[dict(loss=f(len(p["h"])), lse=f(len(p["h"])), dh=torch.full_like(p["h"], 7.0),
+                      dw=torch.full_like(p["w"], 7.0), db=f(len(p["w"]))) for _ in range(2)] for p in ps]
+
+    want = outputs()
+    for p, pair in zip(ps, want):
+        own = torch.full_like(ws, float("nan"))
+        _steps([p], own, [pair])
+        torch.cuda.synchronize()
+    got = outputs()
+    torch.cuda.synchronize()
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            _steps(ps, ws, got)
+        g.replay()
+        torch.cuda.synchronize()
+        got_again = outputs()
+        for a, b in zip(got, got_again):
+            for x, y in zip(a, b):
+                for n in x:
+                    x[n].copy_(y[n])
+        g.replay()
+        g.replay()
+    else:
+        _steps(ps, ws, got)
+        _steps(ps, ws, got)
+    torch.cuda.synchronize()
+    txl.check()
+    for x, (a, b) in enumerate(zip(got, want)):
+        for one, other in zip(a, b):
+            for n in one:
+                assert torch.equal(one[n], other[n]), (x, n)

@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kThreads) few_bwd_kernel(const __grid_constant
 // Hardly more than its launch: 2 x 1024 of 152 blocks (1.2 MB) in 4 us.
 template <typename T>
 __global__ void __launch_bounds__(1024)
-few_finish_kernel(const float *__restrict__ part, int parts, int n, T *__restrict__ dh)
+few_finish_kernel(const float *part, int parts, int n, T *dh)
 {
     __shared__ float s[32][33];
     loss_kernel_begin();

@@ -427,8 +427,8 @@ struct Cursor {
     __device__ __forceinline__ void load(int at, int &c, float &w) const
     {
         const bool in = at < K;
-        c = in ? __ldg(col + at) : kNoColumn;
-        w = in && p ? __ldg(p + at) : 0.f;
+        c = in ? col[at] : kNoColumn;
+        w = in && p ? p[at] : 0.f;
     }
     // the row's first entry of a column >= from
     __device__ __forceinline__ void seek(const LossRows &r, long row, bool live, bool weights, int from, int half)
@@ -445,7 +445,7 @@ struct Cursor {
         }
         col = r.col + row * r.K;
         p = weights ? r.p + row * r.K : nullptr;
-        const int even = __ldg(r.even + row);
+        const int even = r.even[row];
         K = half ? r.K : even;   // the end of this parity's entries
         // seven probes at once: the search waits for memory, not for instructions
         // (16384 x 512 x 65536 with 64 listed per row, both directions 3252 -> 3107 us)
@@ -456,7 +456,7 @@ struct Cursor {
 #pragma unroll
             for (int x = 0; x < 7; ++x) {
                 const int mid = base + (x + 1) * step - 1;
-                c[x] = mid < end ? __ldg(col + mid) : kNoColumn;
+                c[x] = mid < end ? col[mid] : kNoColumn;
             }
 #pragma unroll
             for (int x = 0; x < 7; ++x) {
@@ -713,7 +713,7 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
             if (MODE != MODE_CT) {
                 if (MODE == MODE_DZ && live) {
                     // (a list's valid entries come first)
-                    const bool any = (p.r.target ? target_column(p.r, row) : __ldg(p.r.col + (long)row * p.r.K)) != kNoColumn;
+                    const bool any = (p.r.target ? target_column(p.r, row) : p.r.col[(long)row * p.r.K]) != kNoColumn;
                     coef = row_factor(p.r, row, any);
                     l2 = p.r.lse[row] * (1.f / kLn2);
                 }
@@ -916,14 +916,14 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                     if (n0 + 32 <= p.N) {
 #pragma unroll
                         for (int j = 0; j < 32; j += 4) {
-                            const float4 b4 = __ldg(reinterpret_cast<const float4 *>(p.bias + n0 + j));
+                            const float4 b4 = *reinterpret_cast<const float4 *>(p.bias + n0 + j);
                             unpair(add2(pair(v[j], v[j + 1]), pair(b4.x, b4.y)), v[j], v[j + 1]);
                             unpair(add2(pair(v[j + 2], v[j + 3]), pair(b4.z, b4.w)), v[j + 2], v[j + 3]);
                         }
                     } else {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if (n0 + j < p.N) v[j] += __ldg(p.bias + n0 + j);
+                            if (n0 + j < p.N) v[j] += p.bias[n0 + j];
                     }
                 }
                 if (n0 + 32 > p.N) {   // columns past the vocabulary
@@ -966,14 +966,14 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
                     const float2 *at = reinterpret_cast<const float2 *>(p.bias + n0 + 2 * (lane & 3));
                     if (n0 + 32 <= p.N) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) b[i] = __ldg(at + 4 * i);
+                        for (int i = 0; i < 4; ++i) b[i] = at[4 * i];
                         return;
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int n = n0 + 8 * i + 2 * (lane & 3);
-                        b[i] = n + 1 < p.N ? __ldg(reinterpret_cast<const float2 *>(p.bias + n))
-                                           : make_float2(n < p.N ? __ldg(p.bias + n) : 0.f, 0.f);
+                        b[i] = n + 1 < p.N ? *reinterpret_cast<const float2 *>(p.bias + n)
+                                           : make_float2(n < p.N ? p.bias[n] : 0.f, 0.f);
                     }
                 }
             };

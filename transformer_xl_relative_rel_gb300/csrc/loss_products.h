@@ -11,7 +11,9 @@ namespace txl {
 // The losses' kernels are launched so that a kernel's blocks may be set up
 // while the kernel before it on the stream drains: each kernel lets its
 // successor do so at once, and waits for its predecessor's memory before it
-// touches any.
+// touches any.  A kernel is thus alive while others still write what it will
+// read: no load of theirs goes the way of memory that stays as it is (__ldg,
+// const __restrict__), which might be taken from before the wait.
 __device__ __forceinline__ void loss_kernel_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void loss_kernel_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 template <typename... K, typename... A>

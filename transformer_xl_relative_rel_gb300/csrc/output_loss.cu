@@ -396,8 +396,8 @@ __global__ void __launch_bounds__(1024) loss_finish_kernel(const __grid_constant
 // each 15 us.
 template <int kRows>
 __global__ void __launch_bounds__(1024)
-loss_merge_kernel(const float2 *__restrict__ part, int slots, const float *__restrict__ ysel, LossRows r, float t2,
-                  float *__restrict__ loss, float *__restrict__ lse, int rows)
+loss_merge_kernel(const float2 *part, int slots, const float *ysel, LossRows r, float t2, float *loss, float *lse,
+                  int rows)
 {
     constexpr int kLanes = 1024 / kRows;
     __shared__ float sm[kRows][kLanes + 1], sl[kRows][kLanes + 1];
