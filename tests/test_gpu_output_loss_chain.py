@@ -136,3 +136,64 @@ def test_calls_back_to_back_in_one_workspace(shapes, graph):
         for one, other in zip(a, b):
             for n in one:
                 assert torch.equal(one[n], other[n]), (x, n)
+
+
+def _xent_forward_bytes(rows, d, vocab, dtype, slots):
+    """The forward's workspace for operands copied whole and that many partial
+    results per row: bias, h, w, the targets' logits, the partial results."""
+    parts, dp = (3 if dtype == F32 else 1), (d + 7) // 8 * 8
+    up = lambda n: (n + 255) // 256 * 256
+    return up(4 * vocab) + up(rows * dp * parts * 2) + up(vocab * dp * parts * 2) + up(4 * rows) + up(8 * rows * slots)
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("dtype,rows,d,vocab", [
+    (BF, 16896, 64, 256), (BF, 20001, 64, 200), (BF, 40000, 40, 129), (BF, "1", 64, 1000), (BF, "2", 72, 997),
+    (BF, 30000, 33, 65), (F32, 20001, 64, 128), (F32, 40000, 40, 100), (F32, "1", 24, 250), (F32, "3", 24, 250)])
+def test_vocabularies_of_one_strip(dtype, rows, d, vocab, bias):
+    """The cross entropy's product launch joins its two halves of a row itself:
+    both with tokens, one tile and several, more row blocks than pairs of CTAs
+    (a pair's second item takes over the place where halves are joined).  Rows
+    as text: so many row blocks per pair, the last one ragged."""
+    import transformer_xl_relative_rel_gb300 as txl
+    if isinstance(rows, str):
+        rows = int(rows) * (torch.cuda.get_device_properties(0).multi_processor_count // 2) * 256 - 35
+    code = txl.TXL_BF16 if dtype == BF else txl.TXL_F32
+    # two partial results per row: one strip
+    assert txl.softmax_xent_workspace_bytes(rows, d, vocab, code) == _xent_forward_bytes(rows, d, vocab, dtype, 2)
+    p = _inputs(rows, d, vocab, dtype, 17, bias=bias)
+    p["target"][::7] = -1
+    p["dloss"][5::11] = 0.0
+    p["target"][3], p["target"][4], p["target"][rows - 1] = 0, vocab - 1, vocab - 1
+    p["h"][::7] = 3.0     # (an empty row's lse is still computed)
+    got = _xent(p)
+    _check_xent(p, got=got)
+    for _ in range(4):
+        loss, lse = txl.softmax_xent_fwd(p["h"], p["w"], p["target"], bias=p["bias"])
+        assert torch.equal(loss, got["loss"]) and torch.equal(lse, got["lse"])
+
+
+@pytest.mark.parametrize("dtype,rows,d,vocab", [(F32, 20, 1024, 180003), (BF, 150, 1023, 540000), (F32, 300, 520, 380001)])
+def test_forward_of_several_vocabulary_pieces(dtype, rows, d, vocab):
+    """Weights that are copied, in pieces; targets and entries in each."""
+    import transformer_xl_relative_rel_gb300 as txl
+    code, parts = (txl.TXL_BF16, 1) if dtype == BF else (txl.TXL_F32, 3)
+    assert txl.softmax_xent_workspace_bytes(rows, d, vocab, code) < vocab * d * parts * 2
+    p = _inputs(rows, d, vocab, dtype, 19, k=16)
+    from tests.loss_helpers import check, distill_reference, xent_reference
+    loss, lse = txl.softmax_xent_fwd(p["h"], p["w"], p["target"], bias=p["bias"])
+    check(dict(loss=loss, lse=lse), *xent_reference(p["h"], p["w"], p["bias"], p["target"]))
+    loss, lse = txl.distill_fwd(p["h"], p["w"], p["idx"], p["y"], 2.0, bias=p["bias"])
+    check(dict(loss=loss, lse=lse), *distill_reference(p["h"], p["w"], p["bias"], p["idx"], p["y"], 2.0))
+    txl.check()
+
+
+@pytest.mark.parametrize("dtype,rows,d,vocab", [(BF, 9000, 64, 70001), (BF, 9000, 41, 65000), (F32, 4000, 41, 50003)])
+def test_backward_of_several_vocabulary_pieces(dtype, rows, d, vocab):
+    """dz in pieces, dh added up over them; targets and entries in each."""
+    import transformer_xl_relative_rel_gb300 as txl
+    code, parts = (txl.TXL_BF16, 1) if dtype == BF else (txl.TXL_F32, 3)
+    assert txl.distill_workspace_bytes(rows, d, vocab, 20, code, backward=True) < rows * vocab * parts * 2
+    p = _inputs(rows, d, vocab, dtype, 23, k=20)
+    _check_xent(p)
+    _check_distill(p, 2.0)
