@@ -2151,17 +2151,7 @@ cudaError_t launch_selftest_wait(uint64_t limit_ns, cudaStream_t s)
 
 cudaError_t read_and_clear_device_error(unsigned int *word, cudaStream_t s)
 {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_err_word, sizeof(unsigned int), 0,
-                                              cudaMemcpyDeviceToHost, s);
-    if (e != cudaSuccess) return e;
-    e = cudaStreamSynchronize(s);
-    if (e != cudaSuccess) return e;
-    if (*word) {
-        const unsigned int zero = 0;
-        e = cudaMemcpyToSymbolAsync(g_err_word, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    }
-    return e;
+    return read_and_clear_word(g_err_word, word, s);
 }
 
 }  // namespace txl

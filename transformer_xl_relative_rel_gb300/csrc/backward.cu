@@ -1057,16 +1057,7 @@ txl_status check_sizes(int batch, int mem_len, int seg_len, int heads, int d_hea
 
 cudaError_t read_and_clear_bwd_error(unsigned int *word, cudaStream_t s)
 {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_bwd_err, sizeof(unsigned int), 0, cudaMemcpyDeviceToHost, s);
-    if (e != cudaSuccess) return e;
-    e = cudaStreamSynchronize(s);
-    if (e != cudaSuccess) return e;
-    if (*word) {
-        const unsigned int zero = 0;
-        e = cudaMemcpyToSymbolAsync(g_bwd_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    }
-    return e;
+    return read_and_clear_word(g_bwd_err, word, s);
 }
 
 }  // namespace txl

@@ -49,6 +49,17 @@ cudaError_t launch_bwd_scores(const AttnArgs &a, const void *dout, const float *
 // one warp's bounded wait on an mbarrier nothing completes, limit_ns long;
 // records the device error word when it runs out (the failure path, tested)
 cudaError_t launch_selftest_wait(uint64_t limit_ns, cudaStream_t s);
+// reads and clears one translation unit's error word (syncs on s)
+template <typename Symbol>
+cudaError_t read_and_clear_word(const Symbol &symbol, unsigned int *word, cudaStream_t s)
+{
+    cudaError_t e = cudaMemcpyFromSymbolAsync(word, symbol, sizeof(*word), 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess || *word == 0) return e;
+    const unsigned int zero = 0;
+    e = cudaMemcpyToSymbolAsync(symbol, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
+    return e == cudaSuccess ? cudaStreamSynchronize(s) : e;
+}
 // reads and clears the device error word written by bounded waits (syncs on s)
 cudaError_t read_and_clear_device_error(unsigned int *word, cudaStream_t s);
 

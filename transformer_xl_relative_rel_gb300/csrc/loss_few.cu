@@ -39,7 +39,8 @@ using namespace sm100;
 
 namespace {
 
-__device__ unsigned int g_few_err;
+__device__ unsigned int g_few_err;      // read by txl_check once a launch was made or captured
+std::atomic<bool> g_few_ran{false};
 
 constexpr int kThreads = 256;
 constexpr int kMaxSlots = 8;
@@ -489,6 +490,7 @@ cudaError_t few_start(K kern, const FewParams &p, size_t smem, std::atomic<uint6
         if (e != cudaSuccess) return e;
         done.fetch_or(bit, std::memory_order_relaxed);
     }
+    g_few_ran.store(true, std::memory_order_relaxed);
     return loss_launch(kern, (unsigned)p.s.blocks, kThreads, smem, p.s.joined ? (unsigned)p.s.blocks : 1, s, p);
 }
 
@@ -599,16 +601,8 @@ cudaError_t launch_loss_few(const FewCall &a, cudaStream_t s)
 
 cudaError_t read_and_clear_few_error(unsigned int *word, cudaStream_t s)
 {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_few_err, sizeof(unsigned int), 0, cudaMemcpyDeviceToHost, s);
-    if (e != cudaSuccess) return e;
-    e = cudaStreamSynchronize(s);
-    if (e != cudaSuccess) return e;
-    if (*word) {
-        const unsigned int zero = 0;
-        e = cudaMemcpyToSymbolAsync(g_few_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    }
-    return e;
+    if (!g_few_ran.load(std::memory_order_relaxed)) return cudaSuccess;
+    return read_and_clear_word(g_few_err, word, s);
 }
 
 }  // namespace txl

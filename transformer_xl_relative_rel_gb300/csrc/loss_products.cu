@@ -56,8 +56,10 @@
 
 namespace txl {
 
-// bounded waits of the kernel below that gave up (read by txl_check)
+// bounded waits of the kernel below that gave up (read by txl_check, a copy of
+// some 10 us, once a launch was made or captured)
 __device__ unsigned int g_loss_err;
+static std::atomic<bool> g_loss_ran{false};
 
 namespace {
 using namespace sm100;
@@ -1164,6 +1166,7 @@ cudaError_t l_launch(const LMaps &maps, const LParams &p, cudaStream_t s)
         }
         most[dev].store(n, std::memory_order_relaxed);
     }
+    g_loss_ran.store(true, std::memory_order_relaxed);
     return loss_launch(kern, (unsigned)(CG * (p.items < n ? p.items : n)), LNT, smem, CG, s, maps, p);
 }
 
@@ -1446,16 +1449,8 @@ cudaError_t launch_loss_gradients(const LossContraction *jobs, int n, int parts,
 
 cudaError_t read_and_clear_loss_error(unsigned int *word, cudaStream_t s)
 {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_loss_err, sizeof(unsigned int), 0, cudaMemcpyDeviceToHost, s);
-    if (e != cudaSuccess) return e;
-    e = cudaStreamSynchronize(s);
-    if (e != cudaSuccess) return e;
-    if (*word) {
-        const unsigned int zero = 0;
-        e = cudaMemcpyToSymbolAsync(g_loss_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    }
-    return e;
+    if (!g_loss_ran.load(std::memory_order_relaxed)) return cudaSuccess;
+    return read_and_clear_word(g_loss_err, word, s);
 }
 
 }  // namespace txl

@@ -197,8 +197,8 @@ struct FewCall {
     float *db, *dh_part; // dh_part: [blocks * groups][rows][d]
 };
 cudaError_t launch_loss_few(const FewCall &a, cudaStream_t s);
+// error words of loss_few.cu and loss_products.cu (*word stays as it is before the first launch)
 cudaError_t read_and_clear_few_error(unsigned int *word, cudaStream_t s);
-
 cudaError_t read_and_clear_loss_error(unsigned int *word, cudaStream_t s);
 
 }  // namespace txl

@@ -848,16 +848,7 @@ bool overlap_bytes(const void *a, size_t na, const void *b, size_t nb)
 
 cudaError_t read_and_clear_gemm_error(unsigned int *word, cudaStream_t s)
 {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_gemm_err, sizeof(unsigned int), 0, cudaMemcpyDeviceToHost, s);
-    if (e != cudaSuccess) return e;
-    e = cudaStreamSynchronize(s);
-    if (e != cudaSuccess) return e;
-    if (*word) {
-        const unsigned int zero = 0;
-        e = cudaMemcpyToSymbolAsync(g_gemm_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    }
-    return e;
+    return read_and_clear_word(g_gemm_err, word, s);
 }
 
 }  // namespace txl
