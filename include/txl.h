@@ -483,7 +483,8 @@ txl_status txl_softmax_xent_bwd(const void *h, const void *w, const float *bias,
  * teacher_idx    : device, int64 [rows][top_k], in any order.
  * teacher_logits : device, teacher_dtype [rows][top_k].
  * 1 <= top_k (else TXL_ERR_INVALID), top_k <= 256 (else
- * TXL_ERR_UNSUPPORTED); temperature and its inverse finite and > 0.
+ * TXL_ERR_UNSUPPORTED); 2^-63 <= temperature <= 2^63 (its square is a normal
+ * float32 number), else TXL_ERR_INVALID.
  */
 txl_status txl_distill_workspace(int rows, int d_model, int vocab, int top_k, txl_dtype dtype, int backward,
                                  size_t *bytes);

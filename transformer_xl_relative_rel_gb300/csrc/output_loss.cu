@@ -651,8 +651,8 @@ txl_status loss_checks(const LossArgs &a, bool backward, LossPlan *plan)
     const bool distill = a.K > 0;
     if (distill) {
         if (a.t_dtype != TXL_F32 && a.t_dtype != TXL_BF16) return TXL_ERR_UNSUPPORTED;
-        // (1 / t has to be finite too)
-        if (!(a.temp > 0.f) || isinf(a.temp) || isinf(alpha_of(a))) return TXL_ERR_INVALID;
+        // (the loss is scaled by t^2: outside, an infinite or vanished factor of whatever rounding left)
+        if (!(a.temp >= 0x1p-63f && a.temp <= 0x1p63f)) return TXL_ERR_INVALID;
     }
     const size_t esz = a.dtype == TXL_F32 ? 4 : 2, tsz = a.t_dtype == TXL_F32 ? 4 : 2;
     const size_t n = (size_t)a.rows;
