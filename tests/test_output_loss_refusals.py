@@ -16,3 +16,29 @@ def test_temperatures_whose_square_is_no_float(backward):
     if not torch.cuda.is_available():           # accepted: only the launch fails
         for t in (2.0 ** 63, 2.0 ** -63, 1.0):
             assert _call("distill", backward, t=t) == CUDA, t
+
+
+def test_sizes_past_a_c_int():
+    """2^32 + 5 rows are not 5 rows: sizes that ctypes would cut to 32 bits are
+    refused, in queries and calls."""
+    far = 2 ** 32 + 5
+    bf, f32, i64 = (dict(dtype=x, device="meta") for x in (torch.bfloat16, torch.float32, torch.int64))
+    for sizes in ((far, 8, 16), (8, far, 16), (8, 8, far)):
+        for backward in (False, True):
+            with pytest.raises(txl.TxlError, match="unsupported"):
+                txl.softmax_xent_workspace_bytes(*sizes, txl.TXL_BF16, backward=backward)
+            with pytest.raises(txl.TxlError, match="unsupported"):
+                txl.distill_workspace_bytes(*sizes, 4, txl.TXL_BF16, backward=backward)
+        rows, d, vocab = sizes
+        h, w = torch.empty(rows, d, **bf), torch.empty(vocab, d, **bf)
+        y, f = torch.empty(rows, **i64), torch.empty(rows, **f32)
+        idx, t = torch.empty(rows, 4, **i64), torch.empty(rows, 4, **f32)
+        for call in (lambda: txl.softmax_xent_fwd(h, w, y), lambda: txl.softmax_xent_bwd(h, w, y, f, f),
+                     lambda: txl.distill_fwd(h, w, idx, t), lambda: txl.distill_bwd(h, w, idx, t, f, f)):
+            with pytest.raises(txl.TxlError, match="unsupported"):
+                call()
+    with pytest.raises(txl.TxlError, match="unsupported"):
+        txl.distill_workspace_bytes(8, 8, 16, far, txl.TXL_BF16)
+    h, w = torch.empty(8, 8, **bf), torch.empty(16, 8, **bf)
+    with pytest.raises(txl.TxlError, match="unsupported"):
+        txl.distill_fwd(h, w, torch.empty(8, far, **i64), torch.empty(8, far, **f32))

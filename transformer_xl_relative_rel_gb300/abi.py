@@ -558,11 +558,19 @@ def mem_update_raw(dst_ptr, src_ptr, batch, mem_len, seg_len, d_model, dtype_cod
                                          dtype_code, stream_ptr)
 
 
+def _loss_sizes(what: str, *sizes: int):
+    """Refuses sizes that a C int does not hold (ctypes would pass their low
+    32 bits); the library refuses the others that are too large."""
+    if max(sizes) > 0x7fffffff:
+        _raise(2, what)
+
+
 def softmax_xent_workspace_bytes(rows: int, d_model: int, vocab: int, dtype_code: int,
                                  backward: bool = False) -> int:
     """Workspace bytes of ``softmax_xent_fwd`` (or, with ``backward``, of
     ``softmax_xent_bwd``, which then suffices for both)."""
     n = ctypes.c_size_t(0)
+    _loss_sizes("txl_softmax_xent_workspace", rows, d_model, vocab)
     st = load_library().txl_softmax_xent_workspace(rows, d_model, vocab, dtype_code, int(bool(backward)),
                                                    ctypes.byref(n))
     _raise(st, "txl_softmax_xent_workspace")
@@ -574,6 +582,7 @@ def distill_workspace_bytes(rows: int, d_model: int, vocab: int, top_k: int, dty
     """Workspace bytes of ``distill_fwd`` (or, with ``backward``, of
     ``distill_bwd``, which then suffices for both)."""
     n = ctypes.c_size_t(0)
+    _loss_sizes("txl_distill_workspace", rows, d_model, vocab, top_k)
     st = load_library().txl_distill_workspace(rows, d_model, vocab, top_k, dtype_code, int(bool(backward)),
                                               ctypes.byref(n))
     _raise(st, "txl_distill_workspace")
@@ -592,6 +601,8 @@ class _LossCall:
         self.lead = shape[:-1]
         self.rows = self.lead.numel()
         self.vocab, self.d = w_shape
+        if (self.rows | self.vocab | self.d) >> 31:
+            _loss_sizes("output-layer loss", self.rows, self.vocab, self.d)
         self.code = _dtype_code(h)
         self.dev = h.get_device()
         self.h, self.stream = h, stream
@@ -718,6 +729,7 @@ def _teacher(c, teacher_idx, teacher_logits):
     shape = teacher_idx.shape
     if shape[:-1] != c.lead or len(shape) != len(c.lead) + 1:
         raise ValueError(f"teacher_idx must be {list(c.lead)} + [top_k]")
+    _loss_sizes("output-layer loss", shape[-1])
     if teacher_logits.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"teacher_logits must be float32 or bfloat16, got {teacher_logits.dtype}")
     e = c.arg("teacher_idx", teacher_idx, shape, torch.int64)
