@@ -428,8 +428,8 @@ txl_status txl_rel_attn_fwd_noalloc(const void *q, const void *k, const void *v,
  * piece by piece into the workspace first (not for a handful of rows with
  * d_model <= 1024 and w 16-byte aligned).
  * rows == 0: nothing to do.  d_model >= 1, vocab >= 1, else TXL_ERR_INVALID;
- * vocab, rows and d_model <= 2^30 and at most 2^40 elements in h and in w,
- * else TXL_ERR_UNSUPPORTED.  Asynchronous on
+ * vocab and rows <= 2^30, d_model <= 2^24 and at most 2^40 elements in h and
+ * in w, else TXL_ERR_UNSUPPORTED.  Asynchronous on
  * stream; no allocation; results do not depend on what else runs (no
  * atomics: the same call gives the same bits).  bf16: products of bf16
  * operands, accumulated and normalised in fp32.

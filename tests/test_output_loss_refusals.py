@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import transformer_xl_relative_rel_gb300 as txl
-from tests.test_output_loss_host import CUDA, INVALID, _call, lib  # noqa: F401 (lib: a fixture)
+from tests.test_output_loss_host import CUDA, INVALID, UNSUPPORTED, _call, lib  # noqa: F401 (lib: a fixture)
 
 
 @pytest.mark.parametrize("backward", [False, True])
@@ -42,3 +42,14 @@ def test_sizes_past_a_c_int():
     h, w = torch.empty(8, 8, **bf), torch.empty(16, 8, **bf)
     with pytest.raises(txl.TxlError, match="unsupported"):
         txl.distill_fwd(h, w, torch.empty(8, far, **i64), torch.empty(8, far, **f32))
+
+
+@pytest.mark.parametrize("op,backward", [(o, b) for o in ("xent", "distill") for b in (False, True)])
+def test_rows_wider_than_a_bounded_wait(op, backward):
+    """A tile's sum over d_model has to end well within the kernels' limit of 2 s per wait."""
+    from transformer_xl_relative_rel_gb300 import abi
+    for d in ((1 << 24) + 1, 1 << 29):
+        assert _call(op, backward, d=d, nws=1 << 60) == UNSUPPORTED
+        with pytest.raises(txl.TxlError, match="unsupported"):
+            txl.softmax_xent_workspace_bytes(10, d, 100, abi.TXL_BF16, backward=backward)
+    assert txl.softmax_xent_workspace_bytes(10, 1 << 24, 100, abi.TXL_BF16, backward=backward) > 0

@@ -450,7 +450,10 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb)
 // 131072 with 64, 128, 256, 512 MB of weights 558, 545, 463, 410 us, bf16 128 x
 // 769 x 131072 163, 141, 130, 130 us.
 constexpr size_t kPieceBytes = (size_t)512 << 20;
-constexpr int kMaxSize = 1 << 30;                  // rows, vocabulary and d_model
+constexpr int kMaxSize = 1 << 30;                  // rows and vocabulary
+// d_model: the sum of a tile's products over it has to end well within the limit of the kernels'
+// waits (2 s; one SM's share of HBM delivers 2^24 columns of a bf16 tile's 256 rows in about 0.2 s)
+constexpr int kMaxWidth = 1 << 24;
 constexpr int64_t kMaxElements = (int64_t)1 << 40; // of h and of w
 
 long up(long a, long b) { return (a + b - 1) / b * b; }
@@ -626,7 +629,7 @@ txl_status loss_sizes(int rows, int d, int vocab, int K, txl_dtype dtype)
 {
     if (dtype != TXL_F32 && dtype != TXL_BF16) return TXL_ERR_UNSUPPORTED;
     if (rows < 0 || d < 1 || vocab < 1 || K < 0) return TXL_ERR_INVALID;
-    if (K > kMaxTopK || rows > kMaxSize || vocab > kMaxSize || d > kMaxSize) return TXL_ERR_UNSUPPORTED;
+    if (K > kMaxTopK || rows > kMaxSize || vocab > kMaxSize || d > kMaxWidth) return TXL_ERR_UNSUPPORTED;
     if ((int64_t)(rows > vocab ? rows : vocab) * d > kMaxElements) return TXL_ERR_UNSUPPORTED;
     return TXL_OK;
 }
