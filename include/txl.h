@@ -408,7 +408,10 @@ txl_status txl_rel_attn_fwd_noalloc(const void *q, const void *k, const void *v,
  * is empty: its loss is 0, whatever h_i holds, and its lse is still
  * computed.  A row whose every logit is -infinity has lse -infinity and
  * loss 0.  A bias entry of -infinity takes its token out of the vocabulary
- * (its row of w has to be finite all the same).
+ * (its row of w has to be finite all the same).  Logits are scaled by log2(e)
+ * in float32: one below -2^127 counts as -infinity, so that the type's lowest
+ * value masks as -infinity does (and a row of nothing else has lse -infinity
+ * and loss 0, a target among them loss infinity).
  *
  * h         : device, dtype [rows][d_model] (any leading shape: a T-major
  *             [positions][batch][d_model] buffer has rows = positions*batch).
@@ -477,7 +480,9 @@ txl_status txl_softmax_xent_bwd(const void *h, const void *w, const float *bias,
  * t^2 keeping gradients of different temperatures alike.  An entry is valid
  * when 0 <= teacher_idx < vocab and its logit is not -infinity; a row
  * without a valid entry is empty (loss 0, as a padding row above).  An index
- * listed twice counts twice.  z, h, w, bias, loss, lse, workspace and
+ * listed twice counts twice.  A teacher's logit of its type's lowest value is
+ * a value like others: of weight 0 next to larger ones, and a row of nothing
+ * else is uniform over its entries.  z, h, w, bias, loss, lse, workspace and
  * everything unsaid as txl_softmax_xent_fwd.
  *
  * teacher_idx    : device, int64 [rows][top_k], in any order.

@@ -230,3 +230,22 @@ print("COST", before * 1e6, after * 1e6)
     before, after = map(float, r.stdout.split("COST")[1].split())
     # 3 / 5 of it, and a synchronisation that both have
     assert before < 0.8 * after, (before, after)
+
+
+@pytest.mark.parametrize("dtype,rows", [(F32, 5), (BF, 40), (F32, 140), (BF, 300)])
+def test_biases_of_the_lowest_value(dtype, rows):
+    """They mask as -infinity does, to the bit: some tokens, a target among
+    them, and the whole vocabulary."""
+    p = _inputs(rows, 64, 130, dtype, 29, k=4)
+    for masked in (torch.arange(130, device="cuda") % 3 == 1, torch.ones(130, dtype=torch.bool, device="cuda")):
+        both = [dict(p, bias=torch.where(masked, torch.full_like(p["bias"], v), p["bias"]))
+                for v in (torch.finfo(F32).min, -float("inf"))]
+        a, b = (_xent(q) for q in both)
+        for n in a:
+            assert torch.equal(a[n], b[n]), n
+        counted = (p["target"] >= 0) & (p["target"] < 130)
+        lost = counted & masked[p["target"].clamp(0, 129)] & ~masked.all()
+        assert (a["loss"][lost] == float("inf")).all() and torch.isfinite(a["loss"][~lost]).all()
+        assert ((a["lse"] == -float("inf")) == masked.all()).all()
+        if masked.all():
+            assert not a["loss"].any() and not any(a[n].any() for n in ("dh", "dw", "db"))
