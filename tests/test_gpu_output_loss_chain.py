@@ -3,6 +3,10 @@ follow one another: empty batches, calls of different inputs back to back in
 one workspace, row blocks that end inside a warp's rows, vocabularies of one
 strip and of several pieces, and masks of a type's lowest value.  Bounds as in
 tests/loss_helpers.py."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -10,6 +14,7 @@ from tests.test_gpu_output_loss import (BF, F32, _check_distill, _check_xent, _d
                                         _lib, _xent)
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -203,8 +208,6 @@ def test_check_costs_what_the_program_uses():
     """txl_check reads the losses' error words only in a program that has
     called them: one that has not pays for three copies, not five (about
     11 us each)."""
-    import subprocess
-    import sys
     code = """
 import time, torch
 import transformer_xl_relative_rel_gb300 as txl
@@ -225,7 +228,7 @@ for rows in (3, 200):
 after = cost()
 print("COST", before * 1e6, after * 1e6)
 """
-    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=ROOT)
     assert r.returncode == 0, r.stderr
     before, after = map(float, r.stdout.split("COST")[1].split())
     # 3 / 5 of it, and a synchronisation that both have
@@ -249,3 +252,28 @@ def test_biases_of_the_lowest_value(dtype, rows):
         assert ((a["lse"] == -float("inf")) == masked.all()).all()
         if masked.all():
             assert not a["loss"].any() and not any(a[n].any() for n in ("dh", "dw", "db"))
+
+
+def test_first_calls_of_a_process_captured():
+    """No call has to come before a capture: kernels of every kind are first
+    launched while a graph is recorded."""
+    code = """
+import torch
+from tests.test_gpu_output_loss import BF, F32, _distill, _inputs, _xent
+shapes = [(1, 512, 256, BF), (5, 72, 3000, F32), (40, 72, 1500, BF), (300, 64, 3001, BF), (90, 41, 700, F32),
+          (300, 41, 700, F32), (700, 64, 128, BF)]
+ps = [_inputs(r, d, v, t, 3 + r, bias=r != 40, k=4) for r, d, v, t in shapes]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = [(_xent(p), _distill(p, 2.0)) for p in ps]
+g.replay()
+torch.cuda.synchronize()
+for p, (a, b) in zip(ps, got):
+    for x, y in ((a, _xent(p)), (b, _distill(p, 2.0))):
+        for n in x:
+            assert x[n] is None and y[n] is None or torch.equal(x[n], y[n]), n
+print("FINE")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=ROOT)
+    assert r.returncode == 0 and "FINE" in r.stdout, r.stdout + r.stderr
