@@ -516,11 +516,11 @@ cudaError_t few_rows_of(bool backward, const FewParams &p, size_t smem, cudaStre
 bool few_shape(int rows, int d, int vocab, bool f32, bool w_ok, bool backward, FewShape *s)
 {
     // Both directions, this kernel / the tensor-core kernel: fp32 16 x 768 x
-    // 90326 406 / 677 us, 2 x 512 x 204 26 / 50 us; bf16 8 x 769 x 90326 351 /
+    // 90326 406 / 677 us, 2 x 512 x 204 21 / 50 us; bf16 8 x 769 x 90326 377 /
     // 475 us, 8 x 410 x 20011 67 / 75 us.  bf16 rows that the tensor-core kernel
     // reads in place are this one's while launches are most of the time (two
     // less): 8 x 512 x 3000 28 / 34 us, 8 x 512 x 8000 37 / 44, but 8 x 64 x 40000
-    // 56 / 48 and 8 x 768 x 90326 342 / 172.
+    // 56 / 48 and 8 x 768 x 90326 342 / 137.
     // w has to be aligned for the bulk copies, h and dh stay in registers.
     const bool in_place = !f32 && d % 8 == 0, small = vocab <= (16 << 10) && (int64_t)vocab * d <= (4 << 20);
     if (!w_ok || d > kFewColumns || rows > (f32 ? 16 : 8) || (in_place && !small)) return false;

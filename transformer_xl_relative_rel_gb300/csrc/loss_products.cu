@@ -27,7 +27,7 @@
 // of that piece in one launch 474 us (1739).  At d_model 512 a tile has half
 // the products for the same epilogue: 16384 x 512 over 65536 tokens lse 653
 // us (1683), dz 762 (1443), products 1372 (1603); 64 listed columns per row
-// cost lse 6% and dz some 15%, half of it the search at the start of a strip.
+// cost lse 6% and dz 18%, half of it the search at the start of a strip.
 // A bias costs lse 7% and dz 12% there (9000 x 410 x 50021).  Up to 128 rows
 // the weights' way from memory: 128 x 1024 over 65536 tokens 25 us (5.3 TB/s).
 // fp32 operands take six part products and twice as many, narrower tiles:

@@ -445,8 +445,9 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb)
     return x < y + nb && y < x + na;
 }
 
-// At most this for one piece of dz and of copied weights.  Smaller pieces would
-// stay in L2, but each costs a launch and a drain: forward of fp32 20 x 1024 x
+// At most this for one piece of dz and of copied weights, where 256 columns take
+// no more (rows are not divided: dz of 2^20 bf16 rows, a third of that in fp32).
+// Smaller pieces would stay in L2, but each costs a launch and a drain: forward of fp32 20 x 1024 x
 // 131072 with 64, 128, 256, 512 MB of weights 558, 545, 463, 410 us, bf16 128 x
 // 769 x 131072 163, 141, 130, 130 us.
 constexpr size_t kPieceBytes = (size_t)512 << 20;
@@ -595,7 +596,9 @@ LossPlan loss_plan(int rows, int d, int vocab, int K, txl_dtype dtype, bool back
     return plan;
 }
 
-// The bytes either direction may need whatever the buffers' alignment.
+// The bytes either direction may need whatever the buffers' alignment (a query
+// has no buffers; a call checks for what its own need, which is less where
+// weights of many tokens are read in place).
 size_t loss_bytes(int rows, int d, int vocab, int K, txl_dtype dtype, bool backward)
 {
     size_t most = 0;
