@@ -742,7 +742,7 @@ def distill_fwd(h, w, teacher_idx, teacher_logits, temperature: float = 1.0, bia
     """Distillation loss of the output layer against a teacher's kept logits
     (txl_distill_fwd): per row temperature^2 times the KL divergence from the
     teacher's softmax over its kept entries to the student's softmax over the
-    vocabulary, both at ``temperature``.
+    vocabulary, both at ``temperature`` (2^-63 to 2^63).
 
     teacher_idx: [*lead, top_k] int64, teacher_logits: [*lead, top_k] float32
     or bfloat16 (``torch.topk``'s outputs; entries with an index outside

@@ -447,9 +447,9 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb)
 
 // At most this for one piece of dz and of copied weights, where 256 columns take
 // no more (rows are not divided: dz of 2^20 bf16 rows, a third of that in fp32).
-// Smaller pieces would stay in L2, but each costs a launch and a drain: forward of fp32 20 x 1024 x
-// 131072 with 64, 128, 256, 512 MB of weights 558, 545, 463, 410 us, bf16 128 x
-// 769 x 131072 163, 141, 130, 130 us.
+// Smaller pieces would stay in L2, but each costs a launch and a drain: forward
+// of fp32 20 x 1024 x 131072 with 64, 128, 256, 512 MB of weights 558, 545, 463,
+// 410 us, bf16 128 x 769 x 131072 163, 141, 130, 130 us.
 constexpr size_t kPieceBytes = (size_t)512 << 20;
 constexpr int kMaxSize = 1 << 30;                  // rows and vocabulary
 // d_model: the sum of a tile's products over it has to end well within the limit of the kernels'
