@@ -433,7 +433,7 @@ def _exact_round(y, u, floor_at):
     way to the next value and u make a whole."""
     mag = y.abs()
     exponent = torch.floor(torch.log2(mag.clamp(min=2.0 ** -6))).clamp(-6, 8)
-    unit = 2.0 ** (exponent - 3)
+    unit = torch.ldexp(torch.ones_like(mag), exponent.int() - 3)
     low = torch.floor(mag / unit)
     steps = low + ((mag / unit - low) + u >= 1)
     value = torch.minimum(torch.maximum(steps * unit, floor_at), torch.full_like(mag, TOP))
