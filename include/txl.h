@@ -1,6 +1,8 @@
 /*
  * txl.h -- C ABI of libtxl: Transformer-XL segment-level relative multi-head
- * attention and the per-layer memory rollover on one GB300 GPU (sm_103a).
+ * attention and the per-layer memory rollover on one GB300 GPU (sm_103a), and
+ * what a training step needs around them (projections, the embedding, layer
+ * norm, the output layer's losses, the optimiser step).
  *
  * Every pointer argument named "device" is a CUDA device pointer owned by the
  * caller; the library never frees caller memory and keeps no pointer to it
@@ -509,6 +511,189 @@ txl_status txl_distill_bwd(const void *h, const void *w, const float *bias, cons
                            const void *teacher_logits, txl_dtype teacher_dtype, float temperature, const float *lse,
                            const float *dloss, int rows, int d_model, int vocab, int top_k, txl_dtype dtype,
                            void *dh, void *dw, float *dbias, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * txl_embed_fwd -- the token embedding: out_i = scale * table[token_i] for
+ * every row i < rows (the scale is sqrt(d_model) where the table is tied to
+ * the output layer), a row of zeros for a token outside [0, vocab) (a
+ * negative padding token, say).
+ *
+ * tokens : device, int64 [rows] (any leading shape: a T-major
+ *          [positions][batch] buffer has rows = positions*batch).
+ * table  : device, dtype [vocab][d_model].
+ * out    : device output, dtype [rows][d_model]; must not overlap an input.
+ * Element-aligned pointers; rows that are multiples of 16 bytes at 16-byte
+ * aligned bases move fastest.  rows == 0: nothing to do.  d_model >= 1, vocab
+ * >= 1, else TXL_ERR_INVALID; vocab and rows <= 2^30, d_model <= 2^24 and at
+ * most 2^40 elements in table and out, else TXL_ERR_UNSUPPORTED.
+ * Asynchronous on stream; no allocation.
+ */
+txl_status txl_embed_fwd(const int64_t *tokens, const void *table, float scale, int rows, int d_model, int vocab,
+                         txl_dtype dtype, void *out, void *stream);
+
+/*
+ * txl_embed_bwd -- the table's gradient of one txl_embed_fwd call:
+ *     dtable_t = scale * sum_{i: token_i = t} dout_i
+ * for every token t, 0 for a token that no row has; with accumulate != 0 the
+ * sum is added to what dtable holds (the gradient of an output layer tied to
+ * the table, as txl_softmax_xent_bwd wrote it) and rows of other tokens are
+ * left as they are.  Rows of tokens outside [0, vocab) add nothing, whatever
+ * dout holds there.  Sums are held in fp32, in an order that the tokens alone
+ * determine (no atomics: the same call gives the same bits), and rounded once.
+ *
+ * dout      : device, dtype [rows][d_model].
+ * dtable    : device output, dtype [vocab][d_model].
+ * workspace : device scratch of at least the bytes that
+ *             txl_embed_bwd_workspace reports, 256-byte aligned, owned by the
+ *             caller: calls that may overlap on the GPU need workspaces of
+ *             their own.  Nothing is kept in it between calls.
+ * dtable and workspace must not overlap each other or an input.  rows == 0:
+ * dtable is set to 0, or left as it is.  Sizes and everything unsaid as
+ * txl_embed_fwd.
+ */
+txl_status txl_embed_bwd_workspace(int rows, int d_model, int vocab, txl_dtype dtype, size_t *bytes);
+txl_status txl_embed_bwd(const int64_t *tokens, const void *dout, float scale, int rows, int d_model, int vocab,
+                         txl_dtype dtype, int accumulate, void *dtable, void *workspace, size_t workspace_bytes,
+                         void *stream);
+
+/*
+ * txl_layer_norm_fwd -- layer norm of a residual sum, per row of d = d_model
+ * columns:
+ *     s = x + residual,  mean = sum_d s / d,  var = sum_d (s - mean)^2 / d,
+ *     rstd = 1 / sqrt(var + eps),  y = (s - mean) rstd gamma + beta
+ * after a sub-layer (y = LN(x + f(x)), the paper's order), or before one, with
+ * the sum kept for the next residual: where `sum` is given, s is rounded to
+ * dtype, stored there, and normalised as stored.
+ *
+ * x, residual : device, dtype [rows][d_model]; residual may be NULL (s = x).
+ * gamma, beta : device, float32 [d_model]; either may be NULL (1, 0).
+ * y           : device output, dtype [rows][d_model].
+ * sum         : device output, dtype [rows][d_model], or NULL.
+ * mean, rstd  : device outputs, float32 [rows], for the backward; both or
+ *               neither NULL (not stored).
+ * Outputs must not overlap each other or any input.  Element-aligned
+ * pointers; rows that are multiples of 16 bytes at 16-byte aligned bases
+ * move fastest.  eps > 0 and finite.  rows == 0: nothing to do.  d_model >=
+ * 1, else TXL_ERR_INVALID; d_model <= 8192, rows <= 2^30, else
+ * TXL_ERR_UNSUPPORTED.  fp32 arithmetic, one rounding of y.  Asynchronous on
+ * stream; no allocation.
+ */
+txl_status txl_layer_norm_fwd(const void *x, const void *residual, const float *gamma, const float *beta, float eps,
+                              int rows, int d_model, txl_dtype dtype, void *y, void *sum, float *mean, float *rstd,
+                              void *stream);
+
+/*
+ * txl_layer_norm_bwd -- gradients of one txl_layer_norm_fwd call, from its
+ * mean and rstd.  With xh = (s - mean) rstd and g = dy gamma,
+ *     dx     = rstd (g - sum_d g / d - xh sum_d (g xh) / d) + dsum
+ *     dgamma = sum_i dy_i xh_i,  dbeta = sum_i dy_i
+ * dx is the gradient of s: of x and of the residual alike.
+ *
+ * dy       : device, dtype [rows][d_model].
+ * x        : what was normalised: the forward's x, with its residual again in
+ *            `residual`; or the sum it kept, with residual NULL.
+ * dsum     : device, dtype [rows][d_model]: the gradient that reaches the kept
+ *            sum by its other path, added to dx; or NULL.
+ * dx       : device output, dtype [rows][d_model].
+ * dgamma, dbeta : device outputs, float32 [d_model]; either may be NULL (not
+ *            computed).
+ * workspace : device scratch of at least the bytes that
+ *            txl_layer_norm_bwd_workspace reports, 256-byte aligned, owned by
+ *            the caller, as txl_embed_bwd's; unused (and may be NULL) without
+ *            dgamma and dbeta.
+ * rows == 0: dgamma and dbeta are set to 0.  fp32 arithmetic and sums over
+ * rows in an order that the sizes determine (the same call gives the same
+ * bits), one rounding of dx.  Outputs must not overlap each other, any input
+ * or the workspace.  Sizes as txl_layer_norm_fwd.
+ */
+txl_status txl_layer_norm_bwd_workspace(int rows, int d_model, txl_dtype dtype, size_t *bytes);
+txl_status txl_layer_norm_bwd(const void *dy, const void *x, const void *residual, const void *dsum, const float *gamma,
+                              const float *mean, const float *rstd, int rows, int d_model, txl_dtype dtype, void *dx,
+                              float *dgamma, float *dbeta, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One tensor of an optimiser step.  Element-aligned device pointers; tensors
+ * at 16-byte boundaries move fastest.
+ */
+typedef struct {
+    void *param;              /* param_dtype [size] */
+    float *master;            /* [size]: the float32 weights of which a TXL_BF16 param is the rounded copy; or NULL
+                                 (the step acts on param itself) */
+    const void *grad;         /* grad_dtype [size] */
+    void *exp_avg;            /* m: float32 [size], or e4m3 codes of m / scale (uint8 [size]) */
+    void *exp_avg_sq;         /* v: float32 [size], or e4m3 codes of sqrt(v) / scale */
+    float *exp_avg_scale;     /* NULL: float32 moments; else their scales, one per 256 elements, */
+    float *exp_avg_sq_scale;  /* [ceil(size / 256)] each (both or neither) */
+    int64_t size;             /* elements, 0 .. 2^40 */
+    float weight_decay;       /* finite, >= 0 */
+    txl_dtype param_dtype, grad_dtype;
+} txl_adamw_tensor;
+
+typedef struct {
+    float lr;                 /* finite, >= 0 (unused with lr_device) */
+    float eps;                /* finite, > 0 */
+    double beta1, beta2;      /* 0 <= beta < 1 */
+    int64_t step;             /* the step's number t >= 1 (unused with step_device) */
+    const float *lr_device;   /* device float32 [1], or NULL: read when the kernel runs (captured steps) */
+    const int64_t *step_device;  /* device int64 [1], or NULL */
+    const float *grad_scale;  /* device float32 [1], or NULL (1): a factor of all gradients */
+    uint64_t seed;            /* of the 8-bit moments' rounding */
+} txl_adamw_options;
+
+/*
+ * txl_grad_norm -- the norm of all the tensors' gradients taken as one
+ * vector, and the factor that clips it:
+ *     norm = sqrt(sum_k sum_i grad_ki^2),  clip = min(1, max_norm / norm)
+ * A norm that is not finite (also: squares past the float32 range) has clip
+ * NaN, which makes a txl_adamw_step that takes it as its grad_scale do
+ * nothing.
+ *
+ * t          : host array of `tensors` descriptions; grad, grad_dtype and size
+ *              are used.
+ * max_norm   : > 0.
+ * norm, clip : device outputs, float32 [1]; either may be NULL.
+ * workspace  : device scratch of at least the bytes that
+ *              txl_grad_norm_workspace reports for these sizes, 256-byte
+ *              aligned, owned by the caller, as txl_embed_bwd's.
+ * Squares are rounded to fp32; their sums keep the bits of a double's, in an
+ * order that the sizes determine.  Asynchronous on stream.
+ */
+txl_status txl_grad_norm_workspace(int tensors, const txl_adamw_tensor *t, size_t *bytes);
+txl_status txl_grad_norm(int tensors, const txl_adamw_tensor *t, float max_norm, float *norm, float *clip,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * txl_adamw_step -- one AdamW step over many tensors, in place.  With p the
+ * master weights (or param where there are none), per element:
+ *     g = grad * grad_scale
+ *     m = beta1 m + (1 - beta1) g,  v = beta2 v + ((1 - beta2) g) g
+ *     p = p - lr (weight_decay p + (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps))
+ * in fp32; param is rounded to nearest from p.  Up to 384 tensors share a
+ * launch.  A grad_scale that is not finite, or a step_device below 1, makes
+ * the call leave everything as it is.
+ *
+ * 8-bit moments: x (m, or sqrt(v)) is stored as a code c and the scale of its
+ * 256 elements (the tensor's elements 256 b .. 256 b + 255), x = c * scale,
+ * with scale = max |x| (1 / 448) (a block whose largest is below 2^-100 is
+ * stored as zeros).  y = x ((1 / max |x|) 448) is rounded to one of its two
+ * neighbours among the e4m3 values, 2^(e-3) apart with e = max(floor(log2
+ * |y|), -6): to floor(|y| / 2^(e-3) + u) such steps, at most 448, and for
+ * sqrt(v) > 0 at least one (a denominator is not lost).  u is the low 16 bits
+ * (for m; the high ones for sqrt(v)) over 2^16 of
+ *     h = mix(mix(mix(mix(mix(seed lo) + seed hi) + k) + step) + i + (i >> 32) 0x9e3779b9)
+ * in 32 bits, k the tensor's place in the call, i the element, where
+ * mix(x): x = (x ^ x >> 16) 0x7feb352d, x = (x ^ x >> 15) 0x846ca68b,
+ * x ^ x >> 16.  m, v, sqrt(v) and y are computed operation by operation as
+ * written, each rounded to fp32, so that plain fp32 arithmetic gives the same
+ * codes.  The update uses m and v before they become codes.  A block with an
+ * infinite moment is lost (IEEE arithmetic: NaN); use grad_scale.
+ *
+ * t : host array of `tensors` descriptions.  param, master, the moments and
+ * their scales must overlap neither each other, in any tensor, nor a gradient
+ * or an option's device value.  tensors == 0 or sizes of 0: nothing to do.
+ * Asynchronous on stream; no allocation on the device.
+ */
+txl_status txl_adamw_step(int tensors, const txl_adamw_tensor *t, const txl_adamw_options *options, void *stream);
 
 /*
  * txl_check -- synchronise `stream`, then report and clear the library's

@@ -305,3 +305,97 @@ def distill(h, w, teacher_idx, teacher_logits, temperature=1.0, bias=None, dloss
             u = u - np.log(np.exp(u).sum())
         entries.append(([int(c) for c in e[keep]], u))
     return _sparse_loss(h, w, bias, entries, temperature, dloss)
+
+
+def embed(tokens, table, scale=1.0, dout=None):
+    """out_i = scale table[token_i], zeros for a token outside [0, vocab).
+    tokens [n], table [vocab, d].  Returns out, with ``dout`` [n, d] also the
+    table's gradient of sum_i dout_i . out_i."""
+    table = np.asarray(table, dtype=np.float64)
+    out, grad = np.zeros((len(tokens), table.shape[1])), np.zeros_like(table)
+    for i, t in enumerate(np.asarray(tokens)):
+        if 0 <= t < len(table):
+            out[i] = scale * table[t]
+            if dout is not None:
+                grad[t] += scale * np.asarray(dout[i], dtype=np.float64)
+    return out if dout is None else (out, grad)
+
+
+def layer_norm(s, gamma=None, beta=None, eps=1e-5, dy=None, dsum=None):
+    """Rows of s normalised: y = (s - mean) rstd gamma + beta, rstd = 1 /
+    sqrt(var + eps).  s [n, d].  Returns (y, mean, rstd), with ``dy`` [n, d]
+    also the gradients of sum dy . y (+ sum dsum . s): ds, dgamma, dbeta."""
+    s = np.asarray(s, dtype=np.float64)
+    d = s.shape[1]
+    gamma = np.ones(d) if gamma is None else np.asarray(gamma, dtype=np.float64)
+    beta = np.zeros(d) if beta is None else np.asarray(beta, dtype=np.float64)
+    mean = s.sum(1) / d
+    rstd = 1.0 / np.sqrt(((s - mean[:, None]) ** 2).sum(1) / d + eps)
+    hat = (s - mean[:, None]) * rstd[:, None]
+    y = hat * gamma + beta
+    if dy is None:
+        return y, mean, rstd
+    dy = np.asarray(dy, dtype=np.float64)
+    g = dy * gamma
+    ds = rstd[:, None] * (g - g.sum(1)[:, None] / d - hat * ((g * hat).sum(1)[:, None] / d))
+    if dsum is not None:
+        ds = ds + np.asarray(dsum, dtype=np.float64)
+    return y, mean, rstd, dict(dx=ds, dgamma=(dy * hat).sum(0), dbeta=dy.sum(0))
+
+
+def grad_norm(grads, max_norm):
+    """(norm of all gradients as one vector, min(1, max_norm / norm))."""
+    norm = float(np.sqrt(sum(float((np.asarray(g, dtype=np.float64) ** 2).sum()) for g in grads)))
+    return norm, (1.0 if norm <= max_norm else max_norm / norm)
+
+
+def adamw(p, grad, m, v, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, grad_scale=1.0):
+    """One AdamW step of one tensor: the new (p, m, v)."""
+    p, g, m, v = (np.asarray(x, dtype=np.float64) for x in (p, grad, m, v))
+    g = g * grad_scale
+    m = beta1 * m + (1.0 - beta1) * g
+    v = beta2 * v + (1.0 - beta2) * g * g
+    hat_m, hat_v = m / (1.0 - beta1 ** step), v / (1.0 - beta2 ** step)
+    return p - lr * (weight_decay * p + hat_m / (np.sqrt(hat_v) + eps)), m, v
+
+
+def moment_bits(seed: int, tensor: int, step: int, n: int, first: int = 0):
+    """The random fractions of an 8-bit step's rounding for elements first ..
+    first + n - 1 of a tensor: (of m, of sqrt(v)), multiples of 2^-16 below 1."""
+    word = 0xffffffff
+
+    def mix(x):
+        x = ((x ^ (x >> 16)) * 0x7feb352d) & word
+        x = ((x ^ (x >> 15)) * 0x846ca68b) & word
+        return x ^ (x >> 16)
+
+    key = mix((mix((mix((mix(seed & word) + (seed >> 32)) & word) + tensor) & word) + step) & word)
+    h = np.zeros(n, dtype=np.int64)
+    for x in range(n):
+        i = first + x
+        h[x] = mix((key + i + (i >> 32) * 0x9e3779b9) & word)
+    return (h & 0xffff) / 65536.0, (h >> 16) / 65536.0
+
+
+def moment_codes(x, u, keep: bool):
+    """x (blocks of 256 elements) in 8 bits: (values of the codes, scales, steps
+    before they were cut to whole ones).  ``keep``: what is not zero keeps at
+    least one step."""
+    x = np.asarray(x, dtype=np.float64)
+    value, steps = np.zeros_like(x), np.zeros_like(x)
+    scale = np.zeros((len(x) + 255) // 256)
+    for b in range(len(scale)):
+        at = slice(256 * b, min(len(x), 256 * b + 256))
+        top = np.abs(x[at]).max()
+        if top < 2.0 ** -100:
+            top = 0.0
+        scale[b] = top / 448.0
+        y = x[at] * (448.0 / top) if top > 0.0 else np.zeros_like(x[at])
+        e = np.floor(np.log2(np.maximum(np.abs(y), 2.0 ** -6)))
+        unit = 2.0 ** (e - 3)
+        steps[at] = np.abs(y) / unit + u[at]
+        whole = np.floor(steps[at])
+        if keep:
+            whole = np.where((y > 0) & (whole < 1), 1.0, whole)
+        value[at] = np.sign(y) * np.minimum(whole * unit, 448.0)
+    return value, scale, steps

@@ -28,7 +28,25 @@ EXPORTS = ("txl_rel_attn_fwd", "txl_mem_update", "txl_check", "txl_status_string
            "txl_rel_attn_fwd_ring", "txl_ring_append", "txl_rel_attn_fwd_padded", "txl_project_heads",
            "txl_project_qkv", "txl_project_qkv_cells", "txl_rel_table", "txl_rel_attn_bwd", "txl_rel_attn_bwd_workspace", "txl_rel_attn_fwd_lse", "txl_rel_attn_fwd_mem", "txl_rel_attn_fwd_mem_cells", "txl_rel_attn_fwd_plan", "txl_selftest_wait",
            "txl_softmax_xent_workspace", "txl_softmax_xent_fwd", "txl_softmax_xent_bwd",
-           "txl_distill_workspace", "txl_distill_fwd", "txl_distill_bwd")
+           "txl_distill_workspace", "txl_distill_fwd", "txl_distill_bwd",
+           "txl_embed_fwd", "txl_embed_bwd_workspace", "txl_embed_bwd",
+           "txl_layer_norm_fwd", "txl_layer_norm_bwd_workspace", "txl_layer_norm_bwd",
+           "txl_grad_norm_workspace", "txl_grad_norm", "txl_adamw_step")
+
+
+class _AdamwTensor(ctypes.Structure):
+    """txl_adamw_tensor"""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("param", "master", "grad", "exp_avg", "exp_avg_sq", "exp_avg_scale",
+                                                "exp_avg_sq_scale")] +
+                [("size", ctypes.c_int64), ("weight_decay", ctypes.c_float), ("param_dtype", ctypes.c_int),
+                 ("grad_dtype", ctypes.c_int)])
+
+
+class _AdamwOptions(ctypes.Structure):
+    """txl_adamw_options"""
+    _fields_ = [("lr", ctypes.c_float), ("eps", ctypes.c_float), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("step", ctypes.c_int64), ("lr_device", ctypes.c_void_p), ("step_device", ctypes.c_void_p),
+                ("grad_scale", ctypes.c_void_p), ("seed", ctypes.c_uint64)]
 
 
 class TxlError(RuntimeError):
@@ -98,6 +116,20 @@ def load_library() -> ctypes.CDLL:
     lib.txl_distill_fwd.restype = i
     lib.txl_distill_bwd.argtypes = [vp, vp, vp, vp, vp, i, f, vp, vp, i, i, i, i, i, vp, vp, vp, vp, sz, vp]
     lib.txl_distill_bwd.restype = i
+    szp, tp = ctypes.POINTER(sz), ctypes.POINTER(_AdamwTensor)
+    lib.txl_embed_fwd.argtypes = [vp, vp, f, i, i, i, i, vp, vp]
+    lib.txl_embed_bwd_workspace.argtypes = [i, i, i, i, szp]
+    lib.txl_embed_bwd.argtypes = [vp, vp, f, i, i, i, i, i, vp, vp, sz, vp]
+    lib.txl_layer_norm_fwd.argtypes = [vp, vp, vp, vp, f, i, i, i, vp, vp, vp, vp, vp]
+    lib.txl_layer_norm_bwd_workspace.argtypes = [i, i, i, szp]
+    lib.txl_layer_norm_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, vp, vp, vp, vp, sz, vp]
+    lib.txl_grad_norm_workspace.argtypes = [i, tp, szp]
+    lib.txl_grad_norm.argtypes = [i, tp, f, vp, vp, vp, sz, vp]
+    lib.txl_adamw_step.argtypes = [i, tp, ctypes.POINTER(_AdamwOptions), vp]
+    for name in ("txl_embed_fwd", "txl_embed_bwd_workspace", "txl_embed_bwd", "txl_layer_norm_fwd",
+                 "txl_layer_norm_bwd_workspace", "txl_layer_norm_bwd", "txl_grad_norm_workspace", "txl_grad_norm",
+                 "txl_adamw_step"):
+        getattr(lib, name).restype = i
     lib.txl_mem_update.argtypes = [vp, vp, i, i, i, i, i, vp]
     lib.txl_mem_update.restype = i
     lib.txl_selftest_wait.argtypes = [ctypes.c_uint, vp]
@@ -589,24 +621,16 @@ def distill_workspace_bytes(rows: int, d_model: int, vocab: int, top_k: int, dty
     return int(n.value)
 
 
-class _LossCall:
-    """The checks the output-layer losses share, and where their own tensors
-    are made: on h's device and, with ``stream`` given, in that stream's order
-    (so that a workspace freed at return is reused only behind the call)."""
+class _Call:
+    """The checks that the calls over rows share, and where their own tensors
+    are made: on the tensors' device and, with ``stream`` given, in that
+    stream's order (so that a workspace freed at return is reused only behind
+    the call)."""
 
-    def __init__(self, h, w, stream):
-        shape, w_shape = h.shape, w.shape
-        if len(w_shape) != 2 or not shape or w_shape[1] != shape[-1] or w.dtype != h.dtype:
-            raise ValueError("w must be [vocab, d_model] with h's last dimension and dtype")
-        self.lead = shape[:-1]
-        self.rows = self.lead.numel()
-        self.vocab, self.d = w_shape
-        if (self.rows | self.vocab | self.d) >> 31:
-            _loss_sizes("output-layer loss", self.rows, self.vocab, self.d)
-        self.code = _dtype_code(h)
-        self.dev = h.get_device()
-        self.h, self.stream = h, stream
-        self.placed = h.is_contiguous() and w.is_contiguous() and w.get_device() == self.dev
+    def __init__(self, first, stream):
+        self.dev = first.get_device()
+        self.device, self.stream = first.device, stream
+        self.placed = first.is_contiguous()
 
     def arg(self, name, t, shape, dtype):
         """A tensor argument's pointer (None stays None)."""
@@ -631,8 +655,17 @@ class _LossCall:
         import torch
         if self.stream is not None:
             with torch.cuda.stream(self.stream):
-                return torch.empty(shape, dtype=dtype, device=self.h.device)
-        return torch.empty(shape, dtype=dtype, device=self.h.device)
+                return torch.empty(shape, dtype=dtype, device=self.device)
+        return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def launch(self, fn, *args):
+        """fn(*args, stream) with the tensors' device current; its status"""
+        import torch
+        stream = self.stream.cuda_stream if self.stream is not None else torch._C._cuda_getCurrentRawStream(self.dev)
+        if torch._C._cuda_getDevice() == self.dev:
+            return fn(*args, stream)
+        with torch.cuda.device(self.dev):
+            return fn(*args, stream)
 
     def run(self, fn, what, need, workspace, *args):
         """Calls fn(*args, workspace, its bytes, stream); need() is the workspace's size."""
@@ -642,15 +675,28 @@ class _LossCall:
         elif workspace.get_device() != self.dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous CUDA tensor on the other tensors' device")
         nbytes = workspace.nbytes
-        stream = self.stream.cuda_stream if self.stream is not None else torch._C._cuda_getCurrentRawStream(self.dev)
-        if torch._C._cuda_getDevice() == self.dev:
-            st = fn(*args, workspace.data_ptr(), nbytes, stream)
-        else:
-            with torch.cuda.device(self.dev):
-                st = fn(*args, workspace.data_ptr(), nbytes, stream)
+        st = self.launch(fn, *args, workspace.data_ptr(), nbytes)
         if st == 1 and nbytes < need():
             raise ValueError(f"workspace must hold {need()} bytes")
         _raise(st, what)
+
+
+class _LossCall(_Call):
+    """An output-layer loss: h's rows, and the weights."""
+
+    def __init__(self, h, w, stream):
+        shape, w_shape = h.shape, w.shape
+        if len(w_shape) != 2 or not shape or w_shape[1] != shape[-1] or w.dtype != h.dtype:
+            raise ValueError("w must be [vocab, d_model] with h's last dimension and dtype")
+        self.lead = shape[:-1]
+        self.rows = self.lead.numel()
+        self.vocab, self.d = w_shape
+        if (self.rows | self.vocab | self.d) >> 31:
+            _loss_sizes("output-layer loss", self.rows, self.vocab, self.d)
+        self.code = _dtype_code(h)
+        _Call.__init__(self, h, stream)
+        self.h = h
+        self.placed = self.placed and w.is_contiguous() and w.get_device() == self.dev
 
     def gradients(self, grads, w, bias, weight_grads):
         """The dict of a backward's outputs (given tensors used, absent ones made) and their pointers."""
@@ -779,6 +825,299 @@ def distill_bwd(h, w, teacher_idx, teacher_logits, lse, dloss, temperature: floa
           lambda: distill_workspace_bytes(c.rows, c.d, c.vocab, k, c.code, backward=True), workspace, h.data_ptr(),
           w.data_ptr(), b, e, y, t_code, temperature, s, g, c.rows, c.d, c.vocab, k, c.code, *out)
     return grads
+
+
+def embed_bwd_workspace_bytes(rows: int, d_model: int, vocab: int, dtype_code: int) -> int:
+    """Workspace bytes of ``embed_bwd``."""
+    n = ctypes.c_size_t(0)
+    _loss_sizes("txl_embed_bwd_workspace", rows, d_model, vocab)
+    _raise(load_library().txl_embed_bwd_workspace(rows, d_model, vocab, dtype_code, ctypes.byref(n)),
+           "txl_embed_bwd_workspace")
+    return int(n.value)
+
+
+def embed_fwd(tokens, table, scale: float = 1.0, out=None, stream=None):
+    """The token embedding: out[..., :] = scale * table[tokens], rows of zeros
+    for tokens outside [0, vocab) (txl_embed_fwd).
+
+    tokens: [*lead] int64; table: [vocab, d_model] float32 or bfloat16; both
+    CUDA, contiguous.  Returns out [*lead, d_model] of the table's dtype."""
+    import torch
+    if table.dim() != 2:
+        raise ValueError("table must be [vocab, d_model]")
+    vocab, d = table.shape
+    c = _Call(table, stream)
+    lead = tokens.shape
+    rows = lead.numel()
+    if (rows | vocab | d) >> 31:
+        _loss_sizes("txl_embed_fwd", rows, vocab, d)
+    code = _dtype_code(table)
+    t = c.arg("tokens", tokens, lead, torch.int64)
+    shape = lead + (d,)
+    c.arg("out", out, shape, table.dtype)
+    c.on_device()
+    out = c.make(shape, table.dtype) if out is None else out
+    _raise(c.launch(load_library().txl_embed_fwd, t, table.data_ptr(), scale, rows, d, vocab, code, out.data_ptr()),
+           "txl_embed_fwd")
+    return out
+
+
+def embed_bwd(tokens, dout, dtable=None, scale: float = 1.0, accumulate: bool = False, vocab: Optional[int] = None,
+              workspace=None, stream=None):
+    """The table's gradient of one ``embed_fwd`` call (txl_embed_bwd):
+    dtable[t] = scale * the sum of dout's rows with token t.
+
+    dout: [*lead, d_model]; dtable: [vocab, d_model] of dout's dtype (made when
+    None, with ``vocab`` given).  ``accumulate=True`` adds to dtable instead of
+    overwriting it (a table tied to the output layer: the ``dw`` of its
+    losses).  ``workspace``: a CUDA tensor of at least
+    ``embed_bwd_workspace_bytes`` bytes, not shared with a call that may run at
+    the same time (made when None).  Returns dtable."""
+    import torch
+    if not dout.dim():
+        raise ValueError("dout must be [*lead, d_model]")
+    lead, d = dout.shape[:-1], dout.shape[-1]
+    if dtable is None:
+        if vocab is None or accumulate:
+            raise ValueError("without dtable, vocab is required (and there is nothing to accumulate to)")
+    elif dtable.dim() != 2 or (vocab is not None and vocab != dtable.shape[0]):
+        raise ValueError("dtable must be [vocab, d_model]")
+    else:
+        vocab = dtable.shape[0]
+    rows = lead.numel()
+    if (rows | vocab | d) >> 31:
+        _loss_sizes("txl_embed_bwd", rows, vocab, d)
+    c = _Call(dout, stream)
+    code = _dtype_code(dout)
+    t = c.arg("tokens", tokens, lead, torch.int64)
+    c.arg("dtable", dtable, (vocab, d), dout.dtype)
+    c.on_device()
+    dtable = c.make((vocab, d), dout.dtype) if dtable is None else dtable
+    c.run(load_library().txl_embed_bwd, "txl_embed_bwd", lambda: embed_bwd_workspace_bytes(rows, d, vocab, code),
+          workspace, t, dout.data_ptr(), scale, rows, d, vocab, code, 1 if accumulate else 0, dtable.data_ptr())
+    return dtable
+
+
+def layer_norm_bwd_workspace_bytes(rows: int, d_model: int, dtype_code: int) -> int:
+    """Workspace bytes of ``layer_norm_bwd``."""
+    n = ctypes.c_size_t(0)
+    _loss_sizes("txl_layer_norm_bwd_workspace", rows, d_model)
+    _raise(load_library().txl_layer_norm_bwd_workspace(rows, d_model, dtype_code, ctypes.byref(n)),
+           "txl_layer_norm_bwd_workspace")
+    return int(n.value)
+
+
+def _norm_sizes(x, what):
+    """(lead, rows, d) of a layer norm's x"""
+    if not x.dim():
+        raise ValueError("x must be [*lead, d_model]")
+    lead, d = x.shape[:-1], x.shape[-1]
+    rows = lead.numel()
+    if (rows | d) >> 31:
+        _loss_sizes(what, rows, d)
+    return lead, rows, d
+
+
+def layer_norm_fwd(x, gamma=None, beta=None, residual=None, eps: float = 1e-5, y=None, sum=None, mean=None, rstd=None,
+                   stream=None):
+    """Layer norm of x + residual over the last dimension (txl_layer_norm_fwd).
+
+    x, residual: [*lead, d_model] float32 or bfloat16 (residual may be None);
+    gamma, beta: [d_model] float32 or None (1, 0); all CUDA, contiguous.
+    ``sum``: a tensor like x that receives x + residual (for the next
+    residual), rounded to x's dtype, and is normalised as rounded.  Returns
+    (y, mean, rstd): y like x, the others float32 [*lead], for
+    ``layer_norm_bwd``."""
+    import torch
+    lead, rows, d = _norm_sizes(x, "txl_layer_norm_fwd")
+    c = _Call(x, stream)
+    code, shape, dt, f32 = _dtype_code(x), x.shape, x.dtype, torch.float32
+    r = c.arg("residual", residual, shape, dt)
+    g = c.arg("gamma", gamma, (d,), f32)
+    b = c.arg("beta", beta, (d,), f32)
+    c.arg("y", y, shape, dt)
+    kept = c.arg("sum", sum, shape, dt)
+    c.arg("mean", mean, lead, f32)
+    c.arg("rstd", rstd, lead, f32)
+    c.on_device()
+    y = c.make(shape, dt) if y is None else y
+    mean = c.make(lead, f32) if mean is None else mean
+    rstd = c.make(lead, f32) if rstd is None else rstd
+    _raise(c.launch(load_library().txl_layer_norm_fwd, x.data_ptr(), r, g, b, eps, rows, d, code, y.data_ptr(), kept,
+                    mean.data_ptr(), rstd.data_ptr()), "txl_layer_norm_fwd")
+    return y, mean, rstd
+
+
+def layer_norm_bwd(dy, x, mean, rstd, gamma=None, residual=None, dsum=None, grads=None, weight_grads: bool = True,
+                   workspace=None, stream=None):
+    """Gradients of one ``layer_norm_fwd`` call (txl_layer_norm_bwd): a dict
+    ``dx`` (like x; the gradient of x and of the residual alike) and
+    ``dgamma``, ``dbeta`` (float32 [d_model]; None with ``weight_grads=False``).
+
+    x, residual: the forward's; or the ``sum`` it kept as x, and no residual.
+    mean, rstd: the forward's.  ``dsum``: the gradient of the kept sum by its
+    other path, added to dx, or None.  ``grads``: preallocated outputs with the
+    same keys; ``workspace``: of ``layer_norm_bwd_workspace_bytes`` bytes, as
+    ``embed_bwd``'s."""
+    import torch
+    lead, rows, d = _norm_sizes(x, "txl_layer_norm_bwd")
+    c = _Call(x, stream)
+    code, shape, dt, f32 = _dtype_code(x), x.shape, x.dtype, torch.float32
+    given = c.arg("dy", dy, shape, dt)
+    r = c.arg("residual", residual, shape, dt)
+    o = c.arg("dsum", dsum, shape, dt)
+    g = c.arg("gamma", gamma, (d,), f32)
+    m = c.arg("mean", mean, lead, f32)
+    v = c.arg("rstd", rstd, lead, f32)
+    grads = {} if grads is None else dict(grads)
+    c.arg("dx", grads.get("dx"), shape, dt)
+    if weight_grads:
+        c.arg("dgamma", grads.get("dgamma"), (d,), f32)
+        c.arg("dbeta", grads.get("dbeta"), (d,), f32)
+    c.on_device()
+    if grads.get("dx") is None:
+        grads["dx"] = c.make(shape, dt)
+    for name in ("dgamma", "dbeta"):
+        if not weight_grads:
+            grads[name] = None
+        elif grads.get(name) is None:
+            grads[name] = c.make((d,), f32)
+    dg, db = grads["dgamma"], grads["dbeta"]
+    args = (given, x.data_ptr(), r, o, g, m, v, rows, d, code, grads["dx"].data_ptr(),
+            dg.data_ptr() if weight_grads else None, db.data_ptr() if weight_grads else None)
+    if weight_grads:
+        c.run(load_library().txl_layer_norm_bwd, "txl_layer_norm_bwd",
+              lambda: layer_norm_bwd_workspace_bytes(rows, d, code), workspace, *args)
+    else:
+        _raise(c.launch(load_library().txl_layer_norm_bwd, *args, None, 0), "txl_layer_norm_bwd")
+    return grads
+
+
+class AdamwTensors:
+    """The tensors of an optimiser step, checked and laid out once: lists of
+    equal length of contiguous tensors on one CUDA device, one entry per
+    weight, for ``adamw_step`` and ``grad_norm``.
+
+    params: float32 or bfloat16; grads: float32 or bfloat16, shaped alike;
+    masters: float32 weights of which the bfloat16 params are rounded copies
+    (None, or None entries: the step acts on the param itself).
+    exp_avgs, exp_avg_sqs: the moments, float32 (zeros at first), or 8 bits:
+    ``torch.float8_e4m3fn`` with exp_avg_scales, exp_avg_sq_scales, float32
+    [ceil(elements / 256)] (all zeros at first; exp_avg_sqs then holds square
+    roots); these lists may mix both, with None for float32 moments' scales.
+    weight_decay: a number, or one per tensor.
+
+    The object keeps the tensors, and steps act on their memory: a weight or
+    gradient moved elsewhere wants a new one."""
+
+    def __init__(self, params, grads, exp_avgs, exp_avg_sqs, masters=None, exp_avg_scales=None, exp_avg_sq_scales=None,
+                 weight_decay=0.0):
+        import torch
+        n = len(params)
+        none = [None] * n
+        lists = dict(params=params, grads=grads, exp_avgs=exp_avgs, exp_avg_sqs=exp_avg_sqs, masters=masters or none,
+                     exp_avg_scales=exp_avg_scales or none, exp_avg_sq_scales=exp_avg_sq_scales or none)
+        decay = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else list(weight_decay)
+        for name, x in list(lists.items()) + [("weight_decay", decay)]:
+            if len(x) != n:
+                raise ValueError(f"{name} must have an entry per param ({n}), got {len(x)}")
+        self._array = (_AdamwTensor * max(n, 1))()
+        self._dev = params[0].get_device() if n else None
+        f32 = torch.float32
+        for k in range(n):
+            p, g, m, v, master, ms, vs = (lists[name][k] for name in ("params", "grads", "exp_avgs", "exp_avg_sqs",
+                                                                      "masters", "exp_avg_scales", "exp_avg_sq_scales"))
+            code = _dtype_code(p)
+            g_code = _dtype_code(g)
+            if g.shape != p.shape or m.shape != p.shape or v.shape != p.shape or \
+                    (master is not None and master.shape != p.shape):
+                raise ValueError(f"tensor {k}: grad, master and moments must be {list(p.shape)}")
+            if master is not None and (master.dtype != f32 or code == TXL_F32):
+                raise TypeError(f"tensor {k}: a master is float32 beside a bfloat16 param")
+            state = f32 if ms is None else torch.float8_e4m3fn
+            if (ms is None) != (vs is None) or m.dtype != state or v.dtype != state:
+                raise TypeError(f"tensor {k}: moments are float32 without scales, or float8_e4m3fn with both")
+            blocks = ((p.numel() + 255) // 256,)
+            for s in (ms, vs):
+                if s is not None and (s.shape != blocks or s.dtype != f32):
+                    raise ValueError(f"tensor {k}: scales must be float32 {list(blocks)}")
+            for x in (p, g, m, v, master, ms, vs):
+                if x is not None and (not x.is_cuda or x.get_device() != self._dev or not x.is_contiguous()):
+                    raise ValueError("all tensors must be contiguous CUDA tensors on one device")
+            a = self._array[k]
+            a.param, a.master, a.grad, a.exp_avg, a.exp_avg_sq = _ptr(p), _ptr(master), _ptr(g), _ptr(m), _ptr(v)
+            a.exp_avg_scale, a.exp_avg_sq_scale = _ptr(ms), _ptr(vs)
+            a.size, a.weight_decay, a.param_dtype, a.grad_dtype = p.numel(), decay[k], code, g_code
+        self._count = n
+        self._kept = lists
+
+    def __len__(self):
+        return self._count
+
+
+class _ListCall(_Call):
+    """A call over an ``AdamwTensors``."""
+
+    def __init__(self, tensors, stream):
+        import torch
+        if not isinstance(tensors, AdamwTensors):
+            raise TypeError("tensors must be an AdamwTensors")
+        self.dev = torch.cuda.current_device() if tensors._dev is None else tensors._dev
+        self.device, self.stream, self.placed = torch.device("cuda", self.dev), stream, True
+
+
+def grad_norm_workspace_bytes(tensors) -> int:
+    """Workspace bytes of ``grad_norm``."""
+    n = ctypes.c_size_t(0)
+    _raise(load_library().txl_grad_norm_workspace(tensors._count, tensors._array, ctypes.byref(n)),
+           "txl_grad_norm_workspace")
+    return int(n.value)
+
+
+def grad_norm(tensors, max_norm: float, norm=None, clip=None, workspace=None, stream=None):
+    """The norm of all gradients of an ``AdamwTensors`` together and the
+    factor min(1, max_norm / norm) that clips them (NaN where the norm is not
+    finite), both float32 [1] on the device (txl_grad_norm): (norm, clip).
+    ``workspace``: of ``grad_norm_workspace_bytes`` bytes, as ``embed_bwd``'s."""
+    import torch
+    c = _ListCall(tensors, stream)
+    c.arg("norm", norm, (1,), torch.float32)
+    c.arg("clip", clip, (1,), torch.float32)
+    c.on_device()
+    norm = c.make((1,), torch.float32) if norm is None else norm
+    clip = c.make((1,), torch.float32) if clip is None else clip
+    c.run(load_library().txl_grad_norm, "txl_grad_norm", lambda: grad_norm_workspace_bytes(tensors), workspace,
+          tensors._count, tensors._array, max_norm, norm.data_ptr(), clip.data_ptr())
+    return norm, clip
+
+
+def adamw_step(tensors, lr, step, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, grad_scale=None,
+               seed: int = 0, stream=None) -> None:
+    """One AdamW step over an ``AdamwTensors``, in place (txl_adamw_step).
+
+    lr: a number, or a float32 [1] CUDA tensor; step: the step's number (1 at
+    first), or an int64 [1] CUDA tensor: tensors are read when the kernel runs,
+    so a captured step can be replayed with other values.  grad_scale: a
+    float32 [1] CUDA tensor that multiplies the gradients (``grad_norm``'s
+    clip), or None; one that is not finite leaves everything as it is.  seed:
+    of the 8-bit moments' stochastic rounding."""
+    import torch
+    c = _ListCall(tensors, stream)
+    o = _AdamwOptions()
+    o.beta1, o.beta2, o.eps, o.seed = beta1, beta2, eps, seed & 0xffffffffffffffff
+    if isinstance(lr, torch.Tensor):
+        o.lr_device = c.arg("lr", lr, (1,), torch.float32)
+    else:
+        o.lr = lr
+    if isinstance(step, torch.Tensor):
+        o.step_device = c.arg("step", step, (1,), torch.int64)
+    elif not 1 <= step < 2 ** 63:
+        raise ValueError(f"step must be at least 1, got {step}")
+    else:
+        o.step = step
+    o.grad_scale = c.arg("grad_scale", grad_scale, (1,), torch.float32)
+    c.on_device()
+    _raise(c.launch(load_library().txl_adamw_step, tensors._count, tensors._array, ctypes.byref(o)), "txl_adamw_step")
 
 
 def selftest_wait(limit_us: int, stream=None) -> None:

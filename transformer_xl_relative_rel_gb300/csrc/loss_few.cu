@@ -294,8 +294,8 @@ __global__ void __launch_bounds__(kThreads) few_lse_kernel(const __grid_constant
     const int tid = threadIdx.x;
     const int b0 = blockIdx.x * p.s.per, b1 = p.vocab - b0 < p.s.per ? p.vocab : b0 + p.s.per;
     const FewRing<T> ring = {p, sm.slots, sm.bars, b0, b1, (b1 - b0 + p.s.tok - 1) / p.s.tok};
-    loss_kernel_begin();
-    loss_kernel_wait();
+    chain_begin();
+    chain_wait();
     if (tid == 0) ring.start();
     FewCursor cur;
     if (tid < p.rows) cur.seek(p.r, tid, b0);
@@ -348,8 +348,8 @@ __global__ void __launch_bounds__(kThreads) few_bwd_kernel(const __grid_constant
     const int tid = threadIdx.x;
     const int b0 = blockIdx.x * p.s.per, b1 = p.vocab - b0 < p.s.per ? p.vocab : b0 + p.s.per;
     const FewRing<T> ring = {p, sm.slots, sm.bars, b0, b1, (b1 - b0 + p.s.tok - 1) / p.s.tok};
-    loss_kernel_begin();
-    loss_kernel_wait();
+    chain_begin();
+    chain_wait();
     if (tid == 0) ring.start();
     if (tid < kR) {
         float c = 0.f, l = 0.f;
@@ -455,8 +455,8 @@ __global__ void __launch_bounds__(1024)
 few_finish_kernel(const float *part, int parts, int n, T *dh)
 {
     __shared__ float s[32][33];
-    loss_kernel_begin();
-    loss_kernel_wait();
+    chain_begin();
+    chain_wait();
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, x = blockIdx.x * 32 + tx;
     float sum = 0.f;
     if (x < n)
@@ -491,7 +491,7 @@ cudaError_t few_start(K kern, const FewParams &p, size_t smem, std::atomic<uint6
         done.fetch_or(bit, std::memory_order_relaxed);
     }
     g_few_ran.store(true, std::memory_order_relaxed);
-    return loss_launch(kern, (unsigned)p.s.blocks, kThreads, smem, p.s.joined ? (unsigned)p.s.blocks : 1, s, p);
+    return chain_launch(kern, (unsigned)p.s.blocks, kThreads, smem, p.s.joined ? (unsigned)p.s.blocks : 1, s, p);
 }
 
 template <typename T, int kV, int kR>
@@ -594,8 +594,8 @@ cudaError_t launch_loss_few(const FewCall &a, cudaStream_t s)
     const unsigned blocks = (unsigned)(n + 31) / 32;
     const float *part = a.dh_part;
     const int parts = a.s.blocks * a.s.groups;
-    return a.f32 ? loss_launch(few_finish_kernel<float>, blocks, 1024, 0, 1, s, part, parts, n, (float *)a.dh)
-                 : loss_launch(few_finish_kernel<__nv_bfloat16>, blocks, 1024, 0, 1, s, part, parts, n,
+    return a.f32 ? chain_launch(few_finish_kernel<float>, blocks, 1024, 0, 1, s, part, parts, n, (float *)a.dh)
+                 : chain_launch(few_finish_kernel<__nv_bfloat16>, blocks, 1024, 0, 1, s, part, parts, n,
                                (__nv_bfloat16 *)a.dh);
 }
 

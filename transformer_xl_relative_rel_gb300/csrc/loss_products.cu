@@ -489,7 +489,7 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
     using S = LSmem<CG, MODE, kParts>;
     constexpr int kDzParts = kParts ? 3 : CG == 1 ? 2 : 1;      // dz_parts()
     constexpr int ST = S::ST;
-    loss_kernel_begin();
+    chain_begin();
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -544,7 +544,7 @@ loss_product_kernel(const __grid_constant__ LMaps maps, const __grid_constant__ 
     l_cluster_sync<CG>();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    loss_kernel_wait();
+    chain_wait();
     const int G = (int)gridDim.x / CG, c0 = (int)blockIdx.x / CG;
 
     if (warp == 0) {
@@ -1167,7 +1167,7 @@ cudaError_t l_launch(const LMaps &maps, const LParams &p, cudaStream_t s)
         most[dev].store(n, std::memory_order_relaxed);
     }
     g_loss_ran.store(true, std::memory_order_relaxed);
-    return loss_launch(kern, (unsigned)(CG * (p.items < n ? p.items : n)), LNT, smem, CG, s, maps, p);
+    return chain_launch(kern, (unsigned)(CG * (p.items < n ? p.items : n)), LNT, smem, CG, s, maps, p);
 }
 
 template <int MODE, bool kBias>

@@ -292,8 +292,8 @@ __global__ void __launch_bounds__(256) loss_prep_kernel(const __grid_constant__ 
     constexpr int kBlock = (sizeof(T) == 4 ? 3 : 1) * 64 * 65 * 2, kLists = 8 * kMaxTopK * 8;
     __shared__ __align__(16) unsigned char s[kBlock > kLists ? kBlock : kLists];
     __shared__ int live[64];
-    loss_kernel_begin();
-    loss_kernel_wait();
+    chain_begin();
+    chain_wait();
     int b = (int)blockIdx.x;
     if (b < p.row_blocks) {
         distill_rows(p, reinterpret_cast<unsigned *>(s) + (threadIdx.x >> 5) * p.K2,
@@ -364,8 +364,8 @@ template <typename T>
 __global__ void __launch_bounds__(1024) loss_finish_kernel(const __grid_constant__ FinishArgs p)
 {
     __shared__ float s[1024];
-    loss_kernel_begin();
-    loss_kernel_wait();
+    chain_begin();
+    chain_wait();
     int b = (int)blockIdx.x;
     if (b < p.db_blocks) {   // db_lanes threads per column, each some of the row groups
         const int wide = 1024 / p.db_lanes, tx = threadIdx.x % wide, ty = threadIdx.x / wide;
@@ -401,8 +401,8 @@ loss_merge_kernel(const float2 *part, int slots, const float *ysel, LossRows r, 
 {
     constexpr int kLanes = 1024 / kRows;
     __shared__ float sm[kRows][kLanes + 1], sl[kRows][kLanes + 1];
-    loss_kernel_begin();
-    loss_kernel_wait();
+    chain_begin();
+    chain_wait();
     {
         const int tx = threadIdx.x % kRows, ty = threadIdx.x / kRows;
         const long i = (long)blockIdx.x * kRows + tx;
@@ -744,7 +744,7 @@ cudaError_t launch_prep(const LossArgs &a, const PrepArgs &p)
     const long blocks = (long)p.row_blocks + p.bias_blocks + p.t_blocks + p.copy[0].blocks + p.copy[1].blocks;
     if (blocks > INT32_MAX) return cudaErrorNotSupported;
     if (blocks == 0) return cudaSuccess;
-    return loss_launch(a.dtype == TXL_F32 ? loss_prep_kernel<float> : loss_prep_kernel<__nv_bfloat16>, (unsigned)blocks,
+    return chain_launch(a.dtype == TXL_F32 ? loss_prep_kernel<float> : loss_prep_kernel<__nv_bfloat16>, (unsigned)blocks,
                        256, 0, 1, a.s, p);
 }
 
@@ -867,7 +867,7 @@ cudaError_t run_fwd(const LossArgs &a, const LossPlan &q)
     }
     if (e != cudaSuccess || q.joined) return e;
     const int per = a.rows <= 2048 ? 8 : 32;
-    return loss_launch(per == 8 ? loss_merge_kernel<8> : loss_merge_kernel<32>, (unsigned)((a.rows + per - 1) / per), 1024,
+    return chain_launch(per == 8 ? loss_merge_kernel<8> : loss_merge_kernel<32>, (unsigned)((a.rows + per - 1) / per), 1024,
                        0, 1, a.s, (const float2 *)part, q.slots, (const float *)(ws + q.ysel), r, square_of(a), a.loss,
                        a.lse_out, a.rows);
 }
@@ -987,7 +987,7 @@ cudaError_t run_bwd(const LossArgs &a, const LossPlan &q)
             f.sum[1] = sum_job(a, acc_h, t.dh.splits * (q.dz_rows / a.rows), (long)a.rows * q.dp, a.dh, a.rows);
         const int blocks = f.db_blocks + f.sum[0].blocks + f.sum[1].blocks;
         if (blocks)
-            e = loss_launch(a.dtype == TXL_F32 ? loss_finish_kernel<float> : loss_finish_kernel<__nv_bfloat16>,
+            e = chain_launch(a.dtype == TXL_F32 ? loss_finish_kernel<float> : loss_finish_kernel<__nv_bfloat16>,
                             (unsigned)blocks, 1024, 0, 1, a.s, f);
     }
     return e;
