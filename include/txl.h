@@ -631,7 +631,7 @@ typedef struct {
 
 typedef struct {
     float lr;                 /* finite, >= 0 (unused with lr_device) */
-    float eps;                /* finite, > 0 */
+    float eps;                /* finite, >= 2^-126 */
     double beta1, beta2;      /* 0 <= beta < 1 */
     int64_t step;             /* the step's number t >= 1 (unused with step_device) */
     const float *lr_device;   /* device float32 [1], or NULL: read when the kernel runs (captured steps) */
@@ -685,8 +685,8 @@ txl_status txl_grad_norm(int tensors, const txl_adamw_tensor *t, float max_norm,
  * mix(x): x = (x ^ x >> 16) 0x7feb352d, x = (x ^ x >> 15) 0x846ca68b,
  * x ^ x >> 16.  m, v, sqrt(v) and y are computed operation by operation as
  * written, each rounded to fp32, so that plain fp32 arithmetic gives the same
- * codes.  The update uses m and v before they become codes.  A block with an
- * infinite moment is lost (IEEE arithmetic: NaN); use grad_scale.
+ * codes.  The update uses m and v before they become codes.  A block with a
+ * moment that is not finite is lost: its scale becomes NaN; use grad_scale.
  *
  * t : host array of `tensors` descriptions.  param, master, the moments and
  * their scales must overlap neither each other, in any tensor, nor a gradient

@@ -174,6 +174,64 @@ def test_from_zero_moments(kind):
     assert (model["exp_avg_sqs"][0].double()[g] > 0).all()
 
 
+def test_plain_fp32_arithmetic_gives_the_same_codes():
+    """The header's formulas, operation by operation in torch's fp32, to the bit."""
+    import transformer_xl_relative_rel_gb300 as txl
+    n, step, seed = 300_000, 12, 77
+    model = _model([n], 30, KINDS["8 bits"])
+    before = _copy(model)
+    t = txl.AdamwTensors(**model)
+    scale = torch.tensor([0.37], device="cuda")
+    txl.adamw_step(t, 1e-3, step, grad_scale=scale, seed=seed)
+    wide = lambda s: s.repeat_interleave(256)[:n]
+    g = before["grads"][0].float() * scale
+    m = before["exp_avgs"][0].float() * wide(before["exp_avg_scales"][0])
+    r = before["exp_avg_sqs"][0].float() * wide(before["exp_avg_sq_scales"][0])
+    b1, c1, b2, c2 = (torch.tensor(x, dtype=F32, device="cuda") for x in (0.9, 1 - 0.9, 0.999, 1 - 0.999))
+    m = b1 * m + c1 * g
+    root = (b2 * (r * r) + (c2 * g) * g).sqrt()
+    for x, name, u, keep in ((m, "exp_avg", 0, False), (root, "exp_avg_sq", 1, True)):
+        u = random_fractions(seed, 0, step, n, "cuda")[u].float()
+        top = torch.nn.functional.pad(x, (0, -n % 256)).view(-1, 256).abs().amax(1)
+        y = x.abs() * wide((1 / top.double()).float() * 448)
+        e = torch.frexp(y)[1].clamp(min=-5) - 1
+        unit = ((e - 3 + 127) << 23).view(F32)
+        steps = (y / unit + u).floor()
+        if keep:
+            steps = torch.where(y > 0, steps.clamp(min=1), steps)
+        want = torch.sign(x) * (steps * unit).clamp(max=448)
+        assert torch.equal(model[name + "s"][0].float(), want), name
+        inverse = torch.tensor(1 / 448, dtype=F32, device="cuda")
+        assert torch.equal(model[name + "_scales"][0], top * inverse), name
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_gradients_that_are_not_finite_stay_in_their_block(bad):
+    for kind in ("8 bits", "f32"):
+        model = _model([2000, 500], 31, KINDS[kind])
+        clean = _copy(model)
+        model["grads"][0][300] = bad
+        _step(model)
+        _step(clean)
+        lost = torch.zeros(2000, dtype=torch.bool, device="cuda")
+        lost[300] = True
+        for name in ("params", "masters"):
+            if model[name][0] is not None:
+                assert torch.equal(model[name][0][~lost], clean[name][0][~lost])
+                assert torch.equal(model[name][1], clean[name][1])
+        if kind == "f32":
+            assert torch.equal(model["exp_avgs"][0][~lost], clean["exp_avgs"][0][~lost])
+            continue
+        lost[256:512] = True
+        for name in ("exp_avg", "exp_avg_sq"):
+            assert torch.equal(model[name + "s"][0].double()[~lost], clean[name + "s"][0].double()[~lost])
+            s = model[name + "_scales"][0]
+            assert s[1].isnan() and torch.equal(s[2:], clean[name + "_scales"][0][2:]) and s[0] == clean[name + "_scales"][0][0]
+        # what the next step makes of the lost block is NaN, not a number
+        _step(model, step=8)
+        assert model["masters"][0][256:512].isnan().all() and torch.isfinite(model["masters"][0][512:]).all()
+
+
 def test_values_on_the_device():
     """lr, step and grad_scale read when the kernel runs; the same results as host values."""
     import transformer_xl_relative_rel_gb300 as txl

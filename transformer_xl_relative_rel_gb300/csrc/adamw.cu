@@ -41,6 +41,7 @@ constexpr int kPer = 8;                         // elements per thread and round
 constexpr int kRound = NT * kPer;
 constexpr int kBlockElems = 256;                // elements that share a scale: one warp's
 constexpr float kTop = 448.f;                   // the largest e4m3 value
+constexpr int kRounds = 4;                      // rounds of a block of a large call
 constexpr int kMostTensors = 384, kFewTensors = 48;   // per launch: 30 KB of arguments, 4 KB
 constexpr int64_t kMaxElements = (int64_t)1 << 40;    // of one tensor
 
@@ -53,28 +54,32 @@ struct Tensor {
     float *m_scale, *v_scale;   // NULL: float32 moments
     int64_t n;
     float decay;
-    int first;               // its first chunk in the launch
     uint32_t key;            // of its random numbers
-    uint8_t param_f32, grad_f32, wide, pad;   // wide: every buffer at a 16-byte boundary (codes: 8)
+    uint8_t param_f32, grad_f32, wide, pad[5];   // wide: every buffer at a 16-byte boundary (codes: 8)
 };
 
+// A launch's tensors, cut into rounds of kRound elements.  The rounds that
+// they begin at lie together: the search of a block whose SM has not looked at
+// them yet waits for few lines.
 template <int N>
 struct Tensors {
+    int first[N];
+    int count, rounds;
     Tensor t[N];
-    int count, chunks, rounds;   // a chunk is so many rounds of kRound elements
 };
 
 struct GradTensor {
     const void *grad;
     int64_t n;
-    int first;
-    uint8_t f32, wide, pad[2];
+    uint8_t f32, wide, pad[6];
 };
 
 template <int N>
 struct GradTensors {
+    int first[N];
+    int count, chunks;
+    float one;                   // as StepScalars'
     GradTensor t[N];
-    int count, chunks, rounds;
 };
 
 struct StepScalars {
@@ -82,6 +87,7 @@ struct StepScalars {
     const int64_t *step_at;
     float lr, b1, b2, c1, c2;        // c1 = 1 - b1, c2 = 1 - b2
     float log_b1, log_b2, eps;
+    float one;                       // 1, unknown to the compiler (pair_sum)
     int64_t step;
 };
 
@@ -92,13 +98,14 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t x)
     return x ^ (x >> 16);
 }
 
+// the tensor of a round (in the norm, of a chunk)
 template <typename List>
 __device__ __forceinline__ int tensor_of(const List &l, int chunk)
 {
     int lo = 0, hi = l.count - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (l.t[mid].first <= chunk) lo = mid;
+        if (l.first[mid] <= chunk) lo = mid;
         else hi = mid - 1;
     }
     return lo;
@@ -143,158 +150,294 @@ __device__ __forceinline__ void store8(T *p, int64_t i, int n, bool wide, const 
     }
 }
 
-__device__ __forceinline__ void load_codes(const void *p, int64_t i, int n, bool wide, float scale, float (&x)[8])
+__device__ __forceinline__ void load_codes(const void *p, int64_t i, int n, bool wide, uint32_t (&raw)[2])
 {
     const uint8_t *c = (const uint8_t *)p + i;
-    uint8_t raw[8];
     if (wide) {
-        *reinterpret_cast<uint2 *>(raw) = *reinterpret_cast<const uint2 *>(c);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) raw[j] = j < n ? c[j] : 0;
+        const uint2 r = *reinterpret_cast<const uint2 *>(c);
+        raw[0] = r.x;
+        raw[1] = r.y;
+        return;
     }
+    raw[0] = raw[1] = 0;
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(raw[j] | raw[j + 1] << 8), __NV_E4M3);
-        const float2 f = __half22float2(__half2(h));
-        x[j] = __fmul_rn(f.x, scale);
-        x[j + 1] = __fmul_rn(f.y, scale);
-    }
+    for (int j = 0; j < 8; ++j)
+        if (j < n) raw[j / 4] |= (uint32_t)c[j] << (8 * (j % 4));
 }
 
-// |y| <= 448 (1 + 2^-22), or NaN, to one of its two neighbours in e4m3: up
-// where the fraction of the way and u make a whole
-__device__ __forceinline__ float round_code(float y, float u, bool keep)
+__device__ __forceinline__ void store_codes(void *p, int64_t i, int n, bool wide, const uint32_t (&raw)[2])
 {
-    const uint32_t mag = __float_as_uint(y) & 0x7fffffffu;
-    const uint32_t e = max(mag & 0x7f800000u, (127u - 6u) << 23);
-    // neighbours are 2^(exponent - 3) apart (the product is exact)
-    float steps = floorf(fmaf(__uint_as_float(mag), __uint_as_float((257u << 23) - e), u));
-    if (keep && mag != 0 && steps == 0.f) steps = 1.f;
-    const float value = steps * __uint_as_float(e - (3u << 23));
-    return copysignf(value > kTop ? kTop : value, y);      // (NaN stays NaN)
-}
-
-// the warp's 256 elements (8 per lane) as codes times one scale; h: random bits
-template <bool ROOT>
-__device__ __forceinline__ void store_codes(void *p, float *scale, int64_t i, int n, bool wide, const float (&x)[8],
-                                            const uint32_t (&h)[8])
-{
-    float top = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (top < 0x1p-100f) top = 0.f;
-    const float inverse = top > 0.f ? __fmul_rn(__frcp_rn(top), kTop) : 0.f;
-    uint8_t raw[8];
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-        float2 f;
-        const float u0 = (ROOT ? h[j] >> 16 : h[j] & 0xffffu) * 0x1p-16f;
-        const float u1 = (ROOT ? h[j + 1] >> 16 : h[j + 1] & 0xffffu) * 0x1p-16f;
-        f.x = round_code(__fmul_rn(x[j], inverse), u0, ROOT);
-        f.y = round_code(__fmul_rn(x[j + 1], inverse), u1, ROOT);
-        const uint16_t c = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
-        raw[j] = (uint8_t)c;
-        raw[j + 1] = (uint8_t)(c >> 8);
-    }
     uint8_t *c = (uint8_t *)p + i;
     if (wide) {
-        *reinterpret_cast<uint2 *>(c) = *reinterpret_cast<const uint2 *>(raw);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < n) c[j] = raw[j];
+        *reinterpret_cast<uint2 *>(c) = make_uint2(raw[0], raw[1]);
+        return;
     }
-    if ((threadIdx.x & 31) == 0 && n > 0) *scale = __fmul_rn(top, 1.f / kTop);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (j < n) c[j] = (uint8_t)(raw[j / 4] >> (8 * (j % 4)));
 }
 
+// codes 2 k and 2 k + 1 of eight, times their scale
+__device__ __forceinline__ uint64_t decode(const uint32_t (&raw)[2], int k, uint64_t scale)
+{
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(raw[k / 2] >> (16 * (k % 2))), __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    return pair_mul(pair(f.x, f.y), scale);
+}
+
+// The warp's 256 values x (8 per lane) as codes of x times one scale, which is
+// returned.  h: random bits, of which the low halves are used, for roots
+// (which are not negative, and keep at least one step) the high ones.
+//
+// Steps are counted as floats: |y| / 2^(e-3) + u, added to 2^23 towards zero,
+// has the whole steps as its low bits.  8 (e + 6) more is the code, since a
+// code's exponent field is e + 7 and its 3 bits of mantissa are steps - 8, or,
+// below the normal numbers (e = -6), its bits are the steps; a step too many
+// runs over into the exponent, as it should.  The largest y, 448 or a few
+// 2^-22 of it more, plus u < 1 - 2^-17 stays below 15 steps: no code is past 448.
+// (A warp's integer and logic operations are issued every other cycle: there
+// are as few of them as of the others.)
+template <bool ROOT>
+__device__ __forceinline__ float encode(const uint64_t (&x)[4], const uint32_t (&h)[8], uint32_t (&raw)[2])
+{
+    uint32_t bits[8], top = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float lo, hi;
+        unpair(x[k], lo, hi);
+        bits[2 * k] = __float_as_uint(lo);
+        bits[2 * k + 1] = __float_as_uint(hi);
+        if (ROOT) top = max(max(top, bits[2 * k]), bits[2 * k + 1]);
+        else top = max(max(top, bits[2 * k] & 0x7fffffffu), bits[2 * k + 1] & 0x7fffffffu);
+    }
+    top = __reduce_max_sync(0xffffffffu, top);        // (magnitudes are ordered as their bits are)
+    const float most = __uint_as_float(top);
+    raw[0] = raw[1] = 0;
+    if (most < 0x1p-100f) return 0.f;
+    if (top >= 0x7f800000u) return __uint_as_float(0x7fffffffu);     // a block that is not finite is lost
+    const float inverse = __fmul_rn(__frcp_rn(most), kTop);
+    uint32_t code[8];     // in the low bytes
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint64_t mag = ROOT ? x[k] : pair(__uint_as_float(bits[2 * k] & 0x7fffffffu),
+                                                __uint_as_float(bits[2 * k + 1] & 0x7fffffffu));
+        const uint64_t y2 = pair_mul(mag, pair(inverse, inverse));
+        float y[2], one[2], u[2], steps[2];
+        uint32_t e[2];
+        unpair(y2, y[0], y[1]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            e[j] = max(__float_as_uint(y[j]) & 0x7f800000u, (127u - 6u) << 23);
+            one[j] = __uint_as_float((257u << 23) - e[j]);                               // 2^(3 - e)
+            u[j] = __uint_as_float(__byte_perm(h[2 * k + j], 0x4b000000u, ROOT ? 0x7432 : 0x7410));   // 2^23 + 16 bits
+        }
+        const uint64_t u2 = pair_fma(pair(u[0], u[1]), pair(0x1p-16f, 0x1p-16f), pair(-128.f, -128.f));
+        const uint64_t s2 = pair_fma(y2, pair(one[0], one[1]), u2);      // (the product is exact: one rounding)
+        // 56: -8 * (127 - 6) in the low byte
+        unpair(pair_add_rz(s2, pair(0x1p23f + 56.f, 0x1p23f + 56.f)), steps[0], steps[1]);
+        code[2 * k] = __float_as_uint(steps[0]) + (e[0] >> 20);
+        code[2 * k + 1] = __float_as_uint(steps[1]) + (e[1] >> 20);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const uint32_t *c = code + 4 * k, *b = bits + 4 * k;
+        raw[k] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+        if (!ROOT) {
+            raw[k] |= __byte_perm(__byte_perm(b[0], b[1], 0x0073), __byte_perm(b[2], b[3], 0x0073), 0x5410) & 0x80808080u;
+        } else if (((raw[k] - 0x01010101u) & ~raw[k] & 0x80808080u) != 0) {      // a code of 0
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (b[j] != 0 && (raw[k] >> (8 * j) & 0xffu) == 0) raw[k] |= 1u << (8 * j);
+        }
+    }
+    return __fmul_rn(most, 1.f / kTop);
+}
+
+// a + b of products, each rounded by itself: the assembler fuses a packed
+// product and a packed addition (not scalar ones), but not a product and a
+// fused multiply-add by a 1 that it does not know
+__device__ __forceinline__ uint64_t pair_sum(float one, uint64_t a, uint64_t b) { return pair_fma(pair(one, one), a, b); }
+
 // ---------------------------------------------------------------- the step
+struct Rates {
+    float lr, factor, r1, r2;     // r1 = 1 / (1 - b1^t), r2 = 1 / sqrt(1 - b2^t)
+    int go;
+};
+
+// 1 / x to an ulp, for normal x; 0 above 2^126
+__device__ __forceinline__ float reciprocal(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// The square roots of two numbers, 0 or at least 2^-100, to nearest: a root of
+// about 22 bits and one Newton step with its exact residual (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000", 1990).
+// 0 or NaN for what is not finite; smaller numbers may be an ulp off.
+__device__ __forceinline__ uint64_t pair_sqrt(uint64_t v)
+{
+    float a, b, ra, rb;
+    unpair(v, a, b);
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(ra) : "f"(fmaxf(a, 0x1p-126f)));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(rb) : "f"(fmaxf(b, 0x1p-126f)));
+    const uint64_t r = pair(ra, rb), s = pair_mul(v, r), half = pair_mul(r, pair(0.5f, 0.5f));
+    const uint64_t residual = pair_fma(pair_sub(0, s), s, v);
+    return pair_fma(residual, half, s);
+}
+
+// eight elements of a thread
+struct Eight {
+    float g[8], p[8];
+    float m[8], v[8];          // 32-bit moments, or
+    uint32_t cm[2], cv[2];     // codes, and
+    float ms, vs;              // their scales
+};
+
+// from i on (n of them exist)
+template <bool CODES>
+__device__ __forceinline__ void load_eight(const Tensor &t, int64_t i, int n, bool wide, Eight &x)
+{
+    if (t.grad_f32) load8((const float *)t.grad, i, n, wide, x.g);
+    else load8((const __nv_bfloat16 *)t.grad, i, n, wide, x.g);
+    if (t.master) load8((const float *)t.master, i, n, wide, x.p);
+    else if (t.param_f32) load8((const float *)t.param, i, n, wide, x.p);
+    else load8((const __nv_bfloat16 *)t.param, i, n, wide, x.p);
+    if (CODES) {
+        load_codes(t.m, i, n, wide, x.cm);
+        load_codes(t.v, i, n, wide, x.cv);
+        x.ms = x.vs = 0.f;
+        if (i / kBlockElems * kBlockElems < t.n) {       // (the same for a warp)
+            x.ms = t.m_scale[i / kBlockElems];
+            x.vs = t.v_scale[i / kBlockElems];
+        }
+    } else {
+        load8((const float *)t.m, i, n, wide, x.m);
+        load8((const float *)t.v, i, n, wide, x.v);
+    }
+}
+
+// the step of what load_eight gave
+template <bool CODES>
+__device__ __forceinline__ void step_eight(const Tensor &t, const StepScalars &s, const Rates &r, uint32_t key, int64_t i,
+                                           int n, bool wide, Eight &x)
+{
+    const auto both = [](float y) { return pair(y, y); };
+    uint64_t m2[4], root2[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint64_t g2 = pair_mul(pair(x.g[2 * k], x.g[2 * k + 1]), both(r.factor));
+        uint64_t p2 = pair(x.p[2 * k], x.p[2 * k + 1]), v2;
+        if (CODES) {
+            m2[k] = decode(x.cm, k, both(x.ms));
+            v2 = decode(x.cv, k, both(x.vs));
+            v2 = pair_mul(v2, v2);
+        } else {
+            m2[k] = pair(x.m[2 * k], x.m[2 * k + 1]);
+            v2 = pair(x.v[2 * k], x.v[2 * k + 1]);
+        }
+        m2[k] = pair_sum(s.one, pair_mul(both(s.b1), m2[k]), pair_mul(both(s.c1), g2));
+        v2 = pair_sum(s.one, pair_mul(both(s.b2), v2), pair_mul(pair_mul(both(s.c2), g2), g2));
+        float a, b;
+        if (CODES) {
+            root2[k] = pair_sqrt(v2);
+        } else {
+            unpair(v2, x.v[2 * k], x.v[2 * k + 1]);
+            root2[k] = pair(__fsqrt_rn(x.v[2 * k]), __fsqrt_rn(x.v[2 * k + 1]));
+        }
+        unpair(pair_fma(root2[k], both(r.r2), both(s.eps)), a, b);
+        const uint64_t update = pair_mul(pair_mul(m2[k], both(r.r1)), pair(reciprocal(a), reciprocal(b)));
+        // (1 - lr wd as a factor would lose the small lr wd: it is added to the update)
+        p2 = pair_fma(both(-r.lr), pair_fma(both(t.decay), p2, update), p2);
+        unpair(p2, x.p[2 * k], x.p[2 * k + 1]);
+        if (!CODES) unpair(m2[k], x.m[2 * k], x.m[2 * k + 1]);
+    }
+    if (t.master) store8(t.master, i, n, wide, x.p);
+    if (t.param_f32) store8((float *)t.param, i, n, wide, x.p);
+    else store8((__nv_bfloat16 *)t.param, i, n, wide, x.p);
+    if (!CODES) {
+        store8((float *)t.m, i, n, wide, x.m);
+        store8((float *)t.v, i, n, wide, x.v);
+        return;
+    }
+    uint32_t h[8];
+    const uint32_t base = key + (uint32_t)i + (uint32_t)(i >> 32) * 0x9e3779b9u;    // (8 elements share i >> 32)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = mix(base + j);
+    // elements behind the end are zero: codes of zeros stay zeros, gradients were read as zeros
+    const float ms = encode<false>(m2, h, x.cm), vs = encode<true>(root2, h, x.cv);
+    store_codes(t.m, i, n, wide, x.cm);
+    store_codes(t.v, i, n, wide, x.cv);
+    if ((threadIdx.x & 31) == 0 && n > 0) {
+        t.m_scale[i / kBlockElems] = ms;
+        t.v_scale[i / kBlockElems] = vs;
+    }
+}
+
+// Blocks take up to kRounds rounds, gridDim.x apart: the blocks at work are
+// then next to one another in all of a tensor's buffers.
 template <int N>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(NT, 5)
 adamw_kernel(const __grid_constant__ Tensors<N> list, const __grid_constant__ StepScalars s)
 {
     chain_begin();
-    const Tensor &t = list.t[tensor_of(list, blockIdx.x)];
+    __shared__ Rates shared;
+    __shared__ int tensor[kRounds];
+    __shared__ uint32_t keys[kRounds];
     chain_wait();
-    const float lr = s.lr_at ? *s.lr_at : s.lr;
-    const int64_t step = s.step_at ? *s.step_at : s.step;
-    const float factor = s.grad_scale ? *s.grad_scale : 1.f;
-    // gradients without a finite norm, or no step's number: nothing is done
-    if (!(fabsf(factor) <= 3.4028234e38f) || step < 1) return;
-    // 1 - b^t = -expm1(t log b)
-    const float r1 = -1.f / expm1f((float)step * s.log_b1), r2 = rsqrtf(-expm1f((float)step * s.log_b2));
-    const uint32_t key = mix(t.key + (uint32_t)step);
-    const bool codes = t.m_scale != nullptr;
-    const int64_t first = (int64_t)(blockIdx.x - t.first) * list.rounds * kRound;
-    for (int round = 0; round < list.rounds; ++round) {
-        const int64_t base = first + (int64_t)round * kRound;
-        if (base >= t.n) return;
-        const int64_t i = base + threadIdx.x * kPer;
+    if (threadIdx.x < 32) {      // (one warp's instructions, not eight's)
+        Rates r;
+        r.lr = s.lr_at ? *s.lr_at : s.lr;
+        r.factor = s.grad_scale ? *s.grad_scale : 1.f;
+        const int64_t step = s.step_at ? *s.step_at : s.step;
+        if (threadIdx.x < kRounds) {
+            const int round = blockIdx.x + threadIdx.x * gridDim.x;
+            const int at = round < list.rounds ? tensor_of(list, round) : 0;
+            tensor[threadIdx.x] = at;
+            keys[threadIdx.x] = mix(list.t[at].key + (uint32_t)step);
+        }
+        // 1 - b^t = -expm1(t log b)
+        r.r1 = -1.f / expm1f((float)step * s.log_b1);
+        r.r2 = rsqrtf(-expm1f((float)step * s.log_b2));
+        // gradients without a finite norm, or no step's number: nothing is done
+        r.go = fabsf(r.factor) <= 3.4028234e38f && step >= 1;
+        shared = r;
+    }
+    __syncthreads();
+    const Rates r = shared;
+    if (!r.go) return;
+    Eight x;
+#pragma unroll 1
+    for (int k = 0; k < kRounds; ++k) {
+        const int round = blockIdx.x + k * gridDim.x;
+        if (round >= list.rounds) return;
+        const int at = tensor[k];
+        const Tensor &t = list.t[at];
+        const int64_t i = (int64_t)(round - list.first[at]) * kRound + threadIdx.x * kPer;
         const int n = i >= t.n ? 0 : t.n - i < kPer ? (int)(t.n - i) : kPer;
         const bool wide = t.wide && n == kPer;
-        const int64_t block = i / kBlockElems;       // (the same for a warp)
-        float g[8], p[8], m[8], v[8];
-        if (t.grad_f32) load8((const float *)t.grad, i, n, wide, g);
-        else load8((const __nv_bfloat16 *)t.grad, i, n, wide, g);
-        if (t.master) load8((const float *)t.master, i, n, wide, p);
-        else if (t.param_f32) load8((const float *)t.param, i, n, wide, p);
-        else load8((const __nv_bfloat16 *)t.param, i, n, wide, p);
-        if (codes) {
-            const bool any = block * kBlockElems < t.n;
-            load_codes(t.m, i, n, wide, any ? t.m_scale[block] : 0.f, m);
-            load_codes(t.v, i, n, wide, any ? t.v_scale[block] : 0.f, v);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], v[j]);
-        } else {
-            load8((const float *)t.m, i, n, wide, m);
-            load8((const float *)t.v, i, n, wide, v);
+        if (!t.m_scale) {
+            load_eight<false>(t, i, n, wide, x);
+            step_eight<false>(t, s, r, 0, i, n, wide, x);
+            continue;
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            g[j] = __fmul_rn(g[j], factor);
-            m[j] = __fadd_rn(__fmul_rn(s.b1, m[j]), __fmul_rn(s.c1, g[j]));
-            v[j] = __fadd_rn(__fmul_rn(s.b2, v[j]), __fmul_rn(__fmul_rn(s.c2, g[j]), g[j]));
-            const float root = __fsqrt_rn(v[j]);
-            // (1 - lr wd as a factor would lose the small lr wd: it is added to the update)
-            p[j] = fmaf(-lr, fmaf(t.decay, p[j], m[j] * r1 / fmaf(root, r2, s.eps)), p[j]);
-            if (codes) v[j] = root;
-        }
-        if (t.master) store8(t.master, i, n, wide, p);
-        if (t.param_f32) store8((float *)t.param, i, n, wide, p);
-        else store8((__nv_bfloat16 *)t.param, i, n, wide, p);
-        if (codes) {
-            uint32_t h[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                h[j] = mix(key + (uint32_t)(i + j) + (uint32_t)(i >> 32) * 0x9e3779b9u);
-            store_codes<false>(t.m, t.m_scale + block, i, n, wide, m, h);
-            store_codes<true>(t.v, t.v_scale + block, i, n, wide, v, h);
-        } else {
-            store8((float *)t.m, i, n, wide, m);
-            store8((float *)t.v, i, n, wide, v);
-        }
+        load_eight<true>(t, i, n, wide, x);
+        step_eight<true>(t, s, r, keys[k], i, n, wide, x);
     }
 }
 
 // ---------------------------------------------------------------- the norm
-__device__ __forceinline__ double block_sum(double v)
+// sum + low += x (in pairs), the rounding of the addition kept in low (Knuth's
+// exact difference of a sum): a thread's fp32 sums are as exact as one in
+// double, which the chip has few units for
+__device__ __forceinline__ void add_exactly(uint64_t x, float one, uint64_t &sum, uint64_t &low)
 {
-    __shared__ double part[NT / 32];
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0.0;
-#pragma unroll
-    for (int x = 0; x < NT / 32; ++x) v += part[x];
-    return v;
+    const uint64_t s = pair_sum(one, x, sum), back = pair_sub(s, sum);
+    low = pair_add(low, pair_add(pair_sub(sum, pair_sub(s, back)), pair_sum(one, x, pair_sub(0, back))));
+    sum = s;
 }
 
-// sum + low += x, the rounding of the addition kept in low (Knuth's exact
-// difference of a sum): a thread's fp32 sum as exact as one in double, which
-// the chip has few units for
 __device__ __forceinline__ void add_exactly(float x, float &sum, float &low)
 {
     const float s = __fadd_rn(sum, x), back = __fsub_rn(s, sum);
@@ -302,43 +445,92 @@ __device__ __forceinline__ void add_exactly(float x, float &sum, float &low)
     sum = s;
 }
 
-// part[chunk]: the sum of the squares of a chunk's gradients
-template <int N>
-__global__ void __launch_bounds__(NT) square_kernel(const __grid_constant__ GradTensors<N> list, double *part)
+__device__ __forceinline__ void add_squares(const float (&g)[8], float one, uint64_t &sum, uint64_t &low)
 {
-    chain_begin();
-    const GradTensor &t = list.t[tensor_of(list, blockIdx.x)];
-    chain_wait();
-    const int64_t first = (int64_t)(blockIdx.x - t.first) * list.rounds * kRound;
-    float sum = 0.f, low = 0.f;
-    for (int round = 0; round < list.rounds; ++round) {
-        const int64_t i = first + (int64_t)round * kRound + threadIdx.x * kPer;
-        const int n = i >= t.n ? 0 : t.n - i < kPer ? (int)(t.n - i) : kPer;
-        float g[8];
-        if (t.f32) load8((const float *)t.grad, i, n, t.wide && n == kPer, g);
-        else load8((const __nv_bfloat16 *)t.grad, i, n, t.wide && n == kPer, g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) add_exactly(__fmul_rn(g[j], g[j]), sum, low);
+    for (int j = 0; j < 8; j += 2) {
+        const uint64_t x = pair(g[j], g[j + 1]);
+        add_exactly(pair_mul(x, x), one, sum, low);
     }
-    // (an infinite sum has NaN in low)
-    const double total = block_sum(sum <= 3.4028234e38f ? (double)sum + (double)low : (double)sum);
-    if (threadIdx.x == 0) part[blockIdx.x] = total;
 }
 
-__global__ void __launch_bounds__(1024) norm_kernel(const double *part, long count, float max_norm, float *norm, float *clip)
+constexpr int kNormRounds = 4;      // rounds of a chunk, all asked for at once
+constexpr int kNormResident = 6;    // blocks per SM
+
+// part[block]: the sum of the squares of a range of chunks' gradients
+template <int N>
+__global__ void __launch_bounds__(NT, kNormResident) square_kernel(const __grid_constant__ GradTensors<N> list, double *part)
 {
     chain_begin();
     chain_wait();
-    __shared__ double shared[32];
+    uint64_t sum = 0, low = 0;
+    const int end = (int)((int64_t)list.chunks * (blockIdx.x + 1) / gridDim.x);
+    int chunk = (int)((int64_t)list.chunks * blockIdx.x / gridDim.x), at = tensor_of(list, chunk);
+    for (; chunk < end; ++chunk) {
+        while (at + 1 < list.count && list.first[at + 1] <= chunk) ++at;
+        const GradTensor &t = list.t[at];
+        const int64_t i = (int64_t)(chunk - list.first[at]) * kNormRounds * kRound + threadIdx.x * kPer;
+        if (t.wide && !t.f32 && i + (kNormRounds - 1) * kRound + kPer <= t.n) {
+            raw_t<__nv_bfloat16, 8> raw[kNormRounds];
+#pragma unroll
+            for (int k = 0; k < kNormRounds; ++k)
+                raw[k] = load_raw<__nv_bfloat16, 8>((const __nv_bfloat16 *)t.grad + i + k * kRound);
+#pragma unroll
+            for (int k = 0; k < kNormRounds; ++k) {
+                float g[8];
+                unpack<__nv_bfloat16, 8>(raw[k], g);
+                add_squares(g, list.one, sum, low);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kNormRounds; ++k) {
+                const int64_t j = i + k * kRound;
+                const int n = j >= t.n ? 0 : t.n - j < kPer ? (int)(t.n - j) : kPer;
+                float g[8];
+                if (t.f32) load8((const float *)t.grad, j, n, t.wide && n == kPer, g);
+                else load8((const __nv_bfloat16 *)t.grad, j, n, t.wide && n == kPer, g);
+                add_squares(g, list.one, sum, low);
+            }
+        }
+    }
+    float s[2], l[2];
+    unpair(sum, s[0], s[1]);
+    unpair(low, l[0], l[1]);
+    float low_sum = l[0] + l[1], high = s[0];
+    add_exactly(s[1], high, low_sum);
+    // in fp32 as far as it goes: the chip adds two doubles per SM and cycle
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const float other = __shfl_xor_sync(0xffffffffu, high, o);
+        low_sum += __shfl_xor_sync(0xffffffffu, low_sum, o);
+        add_exactly(other, high, low_sum);
+    }
+    __shared__ float2 sums[NT / 32];
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = make_float2(high, low_sum);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double total = 0.0;
+#pragma unroll
+        for (int x = 0; x < NT / 32; ++x)      // (an infinite sum has NaN in its low part)
+            total += sums[x].x <= 3.4028234e38f ? (double)sums[x].x + (double)sums[x].y : (double)sums[x].x;
+        part[blockIdx.x] = total;
+    }
+}
+
+__global__ void __launch_bounds__(NT) norm_kernel(const double *part, int count, float max_norm, float *norm, float *clip)
+{
+    chain_begin();
+    chain_wait();
+    __shared__ double shared[NT / 32];
     double sum = 0.0;
-    for (long x = threadIdx.x; x < count; x += 1024) sum += part[x];
+    for (int x = threadIdx.x; x < count; x += NT) sum += part[x];
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = sum;
     __syncthreads();
     if (threadIdx.x == 0) {
         sum = 0.0;
-        for (int x = 0; x < 32; ++x) sum += shared[x];
+        for (int x = 0; x < NT / 32; ++x) sum += shared[x];
         const float total = (float)sqrt(sum);
         if (norm) *norm = total;
         // (a norm that is not finite gives NaN: a step that takes it as its factor does nothing)
@@ -359,15 +551,6 @@ txl_status finish(cudaError_t e)
 bool dtype_known(txl_dtype t) { return t == TXL_F32 || t == TXL_BF16; }
 size_t size_of(txl_dtype t) { return t == TXL_F32 ? 4 : 2; }
 
-// Rounds per chunk: one where that leaves every SM no more than some blocks,
-// up to 4 where blocks are many (fewer searches).
-int rounds_for(int64_t elements)
-{
-    const int64_t rounds = (elements + kRound - 1) / kRound;
-    return rounds <= 152 * 16 ? 1 : 4;
-}
-
-// (chunks of all launches together, which the norm's workspace holds a double for each of)
 int64_t chunks_of(int64_t n, int rounds) { return (n + (int64_t)rounds * kRound - 1) / ((int64_t)rounds * kRound); }
 
 txl_status check_ranges(std::vector<CallBuffer> &ins, std::vector<CallBuffer> &outs)
@@ -409,11 +592,11 @@ txl_status tensors_known(int tensors, const txl_adamw_tensor *t)
 }
 
 template <int N>
-cudaError_t launch_step(const txl_adamw_tensor *t, const int *order, int count, int rounds, uint32_t seed,
-                        const StepScalars &sc, cudaStream_t s)
+cudaError_t launch_step(const txl_adamw_tensor *t, const int *order, int count, uint32_t seed, const StepScalars &sc,
+                        cudaStream_t s)
 {
     Tensors<N> list;
-    int chunks = 0;
+    int rounds = 0;
     for (int k = 0; k < count; ++k) {
         const txl_adamw_tensor &x = t[order[k]];
         Tensor &y = list.t[k];
@@ -426,24 +609,25 @@ cudaError_t launch_step(const txl_adamw_tensor *t, const int *order, int count, 
         y.v_scale = x.exp_avg_sq_scale;
         y.n = x.size;
         y.decay = x.weight_decay;
-        y.first = chunks;
+        list.first[k] = rounds;
         y.key = mix(seed + (uint32_t)order[k]);
         y.param_f32 = x.param_dtype == TXL_F32;
         y.grad_f32 = x.grad_dtype == TXL_F32;
         const uintptr_t state = y.m_scale ? 8 : 16;
         y.wide = at_boundary(y.param, 16) && at_boundary(y.master, 16) && at_boundary(y.grad, 16) &&
                  at_boundary(y.m, state) && at_boundary(y.v, state);
-        y.pad = 0;
-        chunks += (int)chunks_of(x.size, rounds);
+        rounds += (int)chunks_of(x.size, 1);
     }
     list.count = count;
-    list.chunks = chunks;
     list.rounds = rounds;
-    return chain_launch(adamw_kernel<N>, (unsigned)chunks, NT, 0, 1, s, list, sc);
+    // one round per block where that is few blocks, several where they are many (fewer searches)
+    const int per = rounds <= 152 * 16 ? 1 : kRounds;
+    return chain_launch(adamw_kernel<N>, (unsigned)((rounds + per - 1) / per), NT, 0, 1, s, list, sc);
 }
 
 template <int N>
-cudaError_t launch_squares(const txl_adamw_tensor *t, const int *order, int count, int rounds, double *part, cudaStream_t s)
+cudaError_t launch_squares(const txl_adamw_tensor *t, const int *order, int count, unsigned blocks, double *part,
+                           cudaStream_t s)
 {
     GradTensors<N> list;
     int chunks = 0;
@@ -452,56 +636,57 @@ cudaError_t launch_squares(const txl_adamw_tensor *t, const int *order, int coun
         GradTensor &y = list.t[k];
         y.grad = x.grad;
         y.n = x.size;
-        y.first = chunks;
+        list.first[k] = chunks;
         y.f32 = x.grad_dtype == TXL_F32;
         y.wide = at_boundary(x.grad, 16);
-        y.pad[0] = y.pad[1] = 0;
-        chunks += (int)chunks_of(x.size, rounds);
+        chunks += (int)chunks_of(x.size, kNormRounds);
     }
     list.count = count;
     list.chunks = chunks;
-    list.rounds = rounds;
-    return chain_launch(square_kernel<N>, (unsigned)chunks, NT, 0, 1, s, list, part);
+    list.one = 1.f;
+    return chain_launch(square_kernel<N>, blocks, NT, 0, 1, s, list, part);
 }
 
-// how a call's tensors are dealt out to launches
-struct Launches {
-    std::vector<int> order;      // the tensors with elements
-    int64_t total = 0, chunks = 0;
-    int rounds = 1;
+// The launches of a call: its tensors with elements, so many per launch that
+// neither they nor their chunks are too many.
+struct Launch {
+    int at, count;               // in the order of the tensors
+    int64_t chunks;
 };
 
-void deal(int tensors, const txl_adamw_tensor *t, Launches *l)
+struct Launches {
+    std::vector<int> order;
+    std::vector<Launch> each;
+};
+
+void deal(int tensors, const txl_adamw_tensor *t, int rounds, Launches *l)
 {
+    l->order.reserve(tensors);
     for (int k = 0; k < tensors; ++k)
-        if (t[k].size > 0) {
-            l->order.push_back(k);
-            l->total += t[k].size;
+        if (t[k].size > 0) l->order.push_back(k);
+    for (int at = 0; at < (int)l->order.size();) {
+        Launch one = {at, 0, 0};
+        while (at < (int)l->order.size() && one.count < kMostTensors) {
+            const int64_t more = chunks_of(t[l->order[at]].size, rounds);
+            if (one.count && one.chunks + more > (1 << 30)) break;
+            one.chunks += more;
+            ++one.count;
+            ++at;
         }
-    l->rounds = rounds_for(l->total);
-    for (int k : l->order) l->chunks += chunks_of(t[k].size, l->rounds);
+        l->each.push_back(one);
+    }
 }
 
-// calls launch(first, count, chunks before) for groups of at most kMostTensors tensors
-template <typename F>
-cudaError_t each_launch(const Launches &l, const txl_adamw_tensor *t, F launch)
+// Blocks of a launch of the norm: what the SMs hold at once, so that the last
+// launch has few sums to add.
+constexpr int64_t kNormBlocks = 152 * kNormResident;
+unsigned norm_blocks(const Launch &l) { return (unsigned)std::min(l.chunks, kNormBlocks); }
+
+size_t norm_bytes(const Launches &l)
 {
-    int64_t before = 0;
-    for (size_t at = 0; at < l.order.size();) {
-        int count = 0;
-        int64_t chunks = 0;
-        while (at + count < l.order.size() && count < kMostTensors) {
-            const int64_t more = chunks_of(t[l.order[at + count]].size, l.rounds);
-            if (count && chunks + more > INT32_MAX) break;
-            chunks += more;
-            ++count;
-        }
-        const cudaError_t e = launch((int)at, count, before);
-        if (e != cudaSuccess) return e;
-        before += chunks;
-        at += count;
-    }
-    return cudaSuccess;
+    size_t blocks = 0;
+    for (const Launch &x : l.each) blocks += norm_blocks(x);
+    return up(blocks * sizeof(double));
 }
 
 txl_status grad_norm(int tensors, const txl_adamw_tensor *t, float max_norm, float *norm, float *clip, void *workspace,
@@ -512,9 +697,10 @@ txl_status grad_norm(int tensors, const txl_adamw_tensor *t, float max_norm, flo
     if (!(max_norm > 0.f)) return TXL_ERR_INVALID;
     if (!norm && !clip) return TXL_OK;
     Launches l;
-    deal(tensors, t, &l);
-    const size_t need = up((size_t)l.chunks * 8);
+    deal(tensors, t, kNormRounds, &l);
+    const size_t need = norm_bytes(l);
     std::vector<CallBuffer> ins, outs;
+    ins.reserve(l.order.size());
     for (int k : l.order) ins.push_back({t[k].grad, (size_t)t[k].size * size_of(t[k].grad_dtype), size_of(t[k].grad_dtype), true});
     outs.push_back({norm, 4, 4, false});
     outs.push_back({clip, 4, 4, false});
@@ -522,14 +708,16 @@ txl_status grad_norm(int tensors, const txl_adamw_tensor *t, float max_norm, flo
     st = check_ranges(ins, outs);
     if (st != TXL_OK) return st;
     if (workspace_bytes < need) return TXL_ERR_INVALID;
-    cudaError_t e = each_launch(l, t, [&](int at, int count, int64_t before) {
-        double *part = (double *)workspace + before;
-        return count <= kFewTensors ? launch_squares<kFewTensors>(t, &l.order[at], count, l.rounds, part, s)
-                                    : launch_squares<kMostTensors>(t, &l.order[at], count, l.rounds, part, s);
-    });
-    if (e == cudaSuccess)
-        e = chain_launch(norm_kernel, 1, 1024, 0, 1, s, (const double *)workspace, (long)l.chunks, max_norm, norm, clip);
-    return finish(e);
+    cudaError_t e = cudaSuccess;
+    int blocks = 0;
+    for (const Launch &x : l.each) {
+        double *part = (double *)workspace + blocks;
+        blocks += (int)norm_blocks(x);
+        e = x.count <= kFewTensors ? launch_squares<kFewTensors>(t, &l.order[x.at], x.count, norm_blocks(x), part, s)
+                                   : launch_squares<kMostTensors>(t, &l.order[x.at], x.count, norm_blocks(x), part, s);
+        if (e != cudaSuccess) return finish(e);
+    }
+    return finish(chain_launch(norm_kernel, 1, NT, 0, 1, s, (const double *)workspace, blocks, max_norm, norm, clip));
 }
 
 txl_status adamw_step(int tensors, const txl_adamw_tensor *t, const txl_adamw_options *o, cudaStream_t s)
@@ -538,12 +726,13 @@ txl_status adamw_step(int tensors, const txl_adamw_tensor *t, const txl_adamw_op
     if (st != TXL_OK) return st;
     if (!o) return TXL_ERR_INVALID;
     if (!(o->beta1 >= 0.0 && o->beta1 < 1.0 && o->beta2 >= 0.0 && o->beta2 < 1.0)) return TXL_ERR_INVALID;
-    if (!(o->eps > 0.f && o->eps <= 3.4028234e38f)) return TXL_ERR_INVALID;
+    if (!(o->eps >= 0x1p-126f && o->eps <= 3.4028234e38f)) return TXL_ERR_INVALID;
     if (!o->step_device && o->step < 1) return TXL_ERR_INVALID;
     if (!o->lr_device && !(o->lr >= 0.f && o->lr <= 3.4028234e38f)) return TXL_ERR_INVALID;
     Launches l;
-    deal(tensors, t, &l);
+    deal(tensors, t, 1, &l);
     std::vector<CallBuffer> ins, outs;
+    ins.reserve(l.order.size() + 3);
     outs.reserve(l.order.size() * 6);
     for (int k : l.order) {
         const txl_adamw_tensor &x = t[k];
@@ -579,12 +768,16 @@ txl_status adamw_step(int tensors, const txl_adamw_tensor *t, const txl_adamw_op
     sc.log_b1 = (float)log(o->beta1);
     sc.log_b2 = (float)log(o->beta2);
     sc.eps = o->eps;
+    sc.one = 1.f;
     sc.step = o->step;
     const uint32_t seed = mix(mix((uint32_t)o->seed) + (uint32_t)(o->seed >> 32));
-    return finish(each_launch(l, t, [&](int at, int count, int64_t) {
-        return count <= kFewTensors ? launch_step<kFewTensors>(t, &l.order[at], count, l.rounds, seed, sc, s)
-                                    : launch_step<kMostTensors>(t, &l.order[at], count, l.rounds, seed, sc, s);
-    }));
+    for (const Launch &x : l.each) {
+        const int *order = &l.order[x.at];
+        const cudaError_t e = x.count <= kFewTensors ? launch_step<kFewTensors>(t, order, x.count, seed, sc, s)
+                                                     : launch_step<kMostTensors>(t, order, x.count, seed, sc, s);
+        if (e != cudaSuccess) return finish(e);
+    }
+    return TXL_OK;
 }
 
 }  // namespace
@@ -601,8 +794,8 @@ txl_status txl_grad_norm_workspace(int tensors, const txl_adamw_tensor *t, size_
     if (st != TXL_OK) return st;
     try {
         Launches l;
-        deal(tensors, t, &l);
-        *bytes = up((size_t)l.chunks * 8 + 1);
+        deal(tensors, t, kNormRounds, &l);
+        *bytes = std::max(norm_bytes(l), (size_t)256);
     } catch (const std::bad_alloc &) {
         return TXL_ERR_UNSUPPORTED;
     }
