@@ -5,10 +5,14 @@
 //
 // The gradient sums rows by token in a fixed order, so that the same call
 // gives the same bits: tokens are sorted by a stable radix sort (digits of up
-// to kDigitBits bits, a counting and a placing launch per digit), the sorted
-// rows are cut into chunks of kChunk, and a warp adds up a chunk's columns,
-// writing each token's sum as its last row passes.  A token whose rows lie in
-// several chunks leaves a partial sum in each, which a last launch adds.
+// to kDigitBits bits), the sorted rows are cut into chunks of kChunk, and a
+// warp adds up a chunk's columns, writing each token's sum as its last row
+// passes.  A token whose rows lie in several chunks leaves a partial sum in
+// each, which a last launch adds.
+//
+// Up to kClusterRows rows are sorted by one cluster in its blocks' shared
+// memory, where other clusters of the launch set the table to zero meanwhile;
+// more by a counting and a placing launch per digit.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -24,7 +28,10 @@ constexpr int kMaxSize = 1 << 30;                  // rows and vocabulary
 constexpr int kMaxWidth = 1 << 24;                 // d_model
 constexpr int64_t kMaxElements = (int64_t)1 << 40; // of the table and of the rows
 constexpr int NT = 256;
-constexpr int kChunk = 32;                         // sorted rows a warp adds up
+constexpr int kChunk = 16;                         // sorted rows a warp adds up
+constexpr int kMostBlocks = 16;                    // of the sorting cluster
+constexpr int kBlockRows = 8192;                   // of one of its blocks: two lists of 64 KB beside the counters
+constexpr int kClusterRows = kMostBlocks * kBlockRows;
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kDigitBits = 9;                      // a placing block's counters: 32 warps x 512 digits, 64 KB
 
@@ -92,6 +99,18 @@ __device__ __forceinline__ int sort_digit(const SortPass &a, int key, bool in)
     return in ? (key >> a.shift) & ((1 << a.bits) - 1) : 1 << a.bits;
 }
 
+// sets the table to zero, as block `block` of `blocks` of kSortThreads threads
+__device__ __forceinline__ void zero_table(const ZeroJob &z, long block, long blocks)
+{
+    const long stride = blocks * kSortThreads, first = block * kSortThreads + threadIdx.x;
+    const size_t head = z.bytes < (-(uintptr_t)z.p & 15) ? z.bytes : (-(uintptr_t)z.p & 15);
+    const size_t n16 = (z.bytes - head) / 16, tail = z.bytes - head - 16 * n16;
+    uint4 *v = (uint4 *)(z.p + head);
+    for (long i = first; i < (long)n16; i += stride) v[i] = make_uint4(0, 0, 0, 0);
+    if (first < (long)(head / 2)) ((uint16_t *)z.p)[first] = 0;
+    if (first < (long)(tail / 2)) ((uint16_t *)(z.p + z.bytes - tail))[first] = 0;
+}
+
 // counts the tile's digits; blocks behind the tiles set the table to zero
 __global__ void __launch_bounds__(kSortThreads)
 sort_count_kernel(const __grid_constant__ SortPass a, const __grid_constant__ ZeroJob z)
@@ -102,14 +121,7 @@ sort_count_kernel(const __grid_constant__ SortPass a, const __grid_constant__ Ze
     for (int d = threadIdx.x; d < digits; d += kSortThreads) count[d] = 0;
     chain_wait();
     if ((int)blockIdx.x >= a.blocks) {
-        const long stride = (long)(gridDim.x - a.blocks) * kSortThreads;
-        const long first = (long)(blockIdx.x - a.blocks) * kSortThreads + threadIdx.x;
-        const size_t head = z.bytes < (-(uintptr_t)z.p & 15) ? z.bytes : (-(uintptr_t)z.p & 15);
-        const size_t n16 = (z.bytes - head) / 16, tail = z.bytes - head - 16 * n16;
-        uint4 *v = (uint4 *)(z.p + head);
-        for (long i = first; i < (long)n16; i += stride) v[i] = make_uint4(0, 0, 0, 0);
-        if (first < (long)(head / 2)) ((uint16_t *)z.p)[first] = 0;
-        if (first < (long)(tail / 2)) ((uint16_t *)(z.p + z.bytes - tail))[first] = 0;
+        zero_table(z, blockIdx.x - a.blocks, gridDim.x - a.blocks);
         return;
     }
     __syncthreads();
@@ -187,6 +199,130 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_c
     }
 }
 
+// ---------------------------------------------------------------- one cluster's sort
+struct ClusterSort {
+    const int64_t *tokens;
+    int *key, *row;                  // [n] sorted
+    int n, vocab, blocks, tile, bits, passes;
+};
+
+__device__ __forceinline__ uint32_t shared_address(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+// the address of another block's copy of what lies at `at` in this one's shared memory
+__device__ __forceinline__ uint32_t in_block(uint32_t at, int block)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(block));
+    return r;
+}
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// The first cluster sorts, block b holding the sorted places b tile .. of every
+// pass; the others set the table to zero.  A pass counts the digits of each
+// warp's rows, adds up over warps, exchanges the blocks' totals, and sends
+// each row to its place in its block (in the last pass, to memory).
+__global__ void __launch_bounds__(kSortThreads)
+embed_sort_kernel(const __grid_constant__ ClusterSort a, const __grid_constant__ ZeroJob z)
+{
+    chain_begin();
+    if ((int)blockIdx.x >= a.blocks) {
+        chain_wait();
+        zero_table(z, blockIdx.x - a.blocks, gridDim.x - a.blocks);
+        return;
+    }
+    extern __shared__ __align__(16) unsigned char dynamic[];
+    const int digits = 1 << a.bits, t = threadIdx.x, lane = t & 31, w = t >> 5, rank = blockIdx.x;
+    int *count = (int *)dynamic;                      // [kSortWarps][digits]
+    int *total = count + kSortWarps * digits;         // [digits] of this block
+    int *base = total + digits;                       // [digits]: the place of this block's first row of a digit
+    int *sums = base + digits;                        // [kSortWarps]
+    int2 *list[2] = {(int2 *)(sums + kSortWarps), (int2 *)(sums + kSortWarps) + a.tile};    // keys and rows
+    int *mine = count + w * digits;
+    const int first = rank * a.tile, n = max(0, min(a.tile, a.n - first));
+    const int per = (a.tile + kSortWarps - 1) / kSortWarps, from = min(w * per, n), to = min(from + per, n);
+    chain_wait();
+    for (int i = t; i < n; i += kSortThreads) {
+        const int64_t token = a.tokens[first + i];
+        list[0][i] = make_int2(token >= 0 && token < a.vocab ? (int)token : a.vocab, first + i);
+    }
+    for (int pass = 0; pass < a.passes; ++pass) {
+        const int2 *in = list[pass & 1];
+        const int shift = pass * a.bits;
+        for (int x = t; x < kSortWarps * digits / 4; x += kSortThreads) ((int4 *)count)[x] = make_int4(0, 0, 0, 0);
+        __syncthreads();
+        for (int i = from + lane; i - lane < to; i += 32) {
+            const int d = i < to ? in[i].x >> shift & (digits - 1) : digits;
+            const unsigned same = __match_any_sync(0xffffffffu, d);
+            if (i < to && (same & ((1u << lane) - 1)) == 0) mine[d] += __popc(same);
+            __syncwarp();
+        }
+        __syncthreads();
+        if (t < digits) {      // (loads before what depends on them: one wait, not 32)
+            int c[kSortWarps], run = 0;
+#pragma unroll
+            for (int x = 0; x < kSortWarps; ++x) c[x] = count[x * digits + t];
+#pragma unroll
+            for (int x = 0; x < kSortWarps; ++x) {
+                count[x * digits + t] = run;
+                run += c[x];
+            }
+            total[t] = run;
+        }
+        cluster_barrier();
+        int all = 0, before = 0;
+        if (t < digits) {
+            const uint32_t at = shared_address(total + t);
+            int c[kMostBlocks];
+#pragma unroll
+            for (int b = 0; b < kMostBlocks; ++b) {
+                c[b] = 0;
+                if (b < a.blocks) asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(c[b]) : "r"(in_block(at, b)));
+            }
+#pragma unroll
+            for (int b = 0; b < kMostBlocks; ++b) {
+                all += c[b];
+                before += b < rank ? c[b] : 0;
+            }
+        }
+        int run = all;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += v;
+        }
+        if (lane == 31) sums[w] = run;
+        __syncthreads();
+        run += __reduce_add_sync(0xffffffffu, lane < w ? sums[lane] : 0);
+        if (t < digits) base[t] = run - all + before;
+        __syncthreads();
+        const bool last = pass + 1 == a.passes;
+        const uint32_t out = shared_address(list[(pass + 1) & 1]);
+        for (int i = from + lane; i - lane < to; i += 32) {
+            const int2 one = i < to ? in[i] : make_int2(0, 0);
+            const int d = i < to ? one.x >> shift & (digits - 1) : digits;
+            const unsigned same = __match_any_sync(0xffffffffu, d), below = same & ((1u << lane) - 1);
+            if (i < to) {
+                const unsigned place = base[d] + mine[d] + __popc(below);
+                if (last) {
+                    a.key[place] = one.x;
+                    a.row[place] = one.y;
+                } else {
+                    const unsigned block = place / (unsigned)a.tile;
+                    const uint32_t at = in_block(out + (place - block * a.tile) * 8, (int)block);
+                    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(one.x), "r"(one.y) : "memory");
+                }
+            }
+            __syncwarp();
+            if (i < to && below == 0) mine[d] += __popc(same);
+            __syncwarp();
+        }
+        // (after the last pass: no block ends while another reads its totals)
+        cluster_barrier();
+    }
+}
+
 // ---------------------------------------------------------------- sums
 struct SumArgs {
     const int *key, *row;    // sorted by token
@@ -200,106 +336,183 @@ struct SumArgs {
 };
 
 template <typename T, int V>
-__device__ __forceinline__ void write_sum(const SumArgs &a, int token, int c, float (&acc)[V])
+__device__ __forceinline__ void write_sum(const SumArgs &a, int token, int c, const float (&acc)[V])
 {
     T *to = (T *)a.dtable + (size_t)token * a.d + c;
-    float old[V];
-    if (a.accumulate) unpack<T, V>(load_raw<T, V>(to), old);
+    float x[V];
+    if (a.accumulate) {
+        unpack<T, V>(load_raw<T, V>(to), x);
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = a.accumulate ? fmaf(a.scale, acc[i], old[i]) : a.scale * acc[i];
-    store_vec<T, V>(to, acc);
+        for (int i = 0; i < V; ++i) x[i] = fmaf(a.scale, acc[i], x[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = a.scale * acc[i];
+    }
+    store_vec<T, V>(to, x);
 }
 
+constexpr int kStrip = 256;      // columns of a warp: 32 K V
+
+// A warp adds kStrip columns of a chunk's rows, of which U are asked for at
+// once, as many as 64 registers hold.
 template <typename T, int V>
 __global__ void __launch_bounds__(NT) embed_sum_kernel(const __grid_constant__ SumArgs a)
 {
+    constexpr int K = kStrip / (32 * V), U = 64 / (K * (sizeof(raw_t<T, V>) >= 4 ? (int)sizeof(raw_t<T, V>) / 4 : 1));
+    static_assert(kChunk % U == 0, "a chunk is so many whole batches");
     chain_begin();
     chain_wait();
     const int lane = threadIdx.x & 31;
     const long task = (long)blockIdx.x * (NT / 32) + (threadIdx.x >> 5);
-    const int chunk = (int)(task / a.strips), c = (int)(task - (long)chunk * a.strips) * 32 * V + lane * V;
+    const int chunk = (int)(task / a.strips), c = (int)(task - (long)chunk * a.strips) * kStrip + lane * V;
     if (chunk >= a.chunks) return;
     const int first = chunk * kChunk, n = min(kChunk, a.n - first);
     const int key = lane < n ? a.key[first + lane] : a.vocab;
     const int row = lane < n ? a.row[first + lane] : 0;
     const int before = first > 0 ? a.key[first - 1] : -1, after = first + n < a.n ? a.key[first + n] : a.vocab;
-    const int live = __popc(__ballot_sync(0xffffffffu, key < a.vocab));
-    float acc[V];
+    const int live = __popc(__ballot_sync(0xffffffffu, key < a.vocab)), head = __shfl_sync(0xffffffffu, key, 0);
+    float acc[K][V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = 0.f;
-    constexpr int U = 8;     // rows asked for at once
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[k][i] = 0.f;
     for (int j = 0; j < live; j += U) {
-        raw_t<T, V> raw[U];
+        raw_t<T, V> raw[U][K];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const long r = __shfl_sync(0xffffffffu, row, (j + u) & 31);
-            if (j + u < live && c < a.d) raw[u] = load_raw<T, V>((const T *)a.dout + r * a.d + c);
+            const T *from = (const T *)a.dout + (size_t)__shfl_sync(0xffffffffu, row, (j + u) & 31) * a.d;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (j + u < live && c + 32 * k * V < a.d) raw[u][k] = load_raw<T, V>(from + c + 32 * k * V);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (j + u >= live) break;
-            const int k = __shfl_sync(0xffffffffu, key, j + u);
-            const int next = __shfl_sync(0xffffffffu, key, (j + u + 1) & 31);
-            float v[V];
-            if (c < a.d) {
-                unpack<T, V>(raw[u], v);
+            const int token = __shfl_sync(0xffffffffu, key, j + u);
+            const int next = __shfl_sync(0xffffffffu, key, (j + u + 1) & 31);     // (behind the chunk: no token)
 #pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] += v[i];
-            }
-            const bool end = j + u + 1 == n;
-            if (!end && next == k) continue;
+            for (int k = 0; k < K; ++k)
+                if (c + 32 * k * V < a.d) {
+                    float v[V];
+                    unpack<T, V>(raw[u][k], v);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) acc[k][i] += v[i];
+                }
+            if (next == token) continue;
             // the token's last row in this chunk
-            const int head = __shfl_sync(0xffffffffu, key, 0);
-            const bool from_before = k == head && before == k, goes_on = end && after == k;
-            if (c < a.d) {
-                if (from_before || goes_on)
-                    store_floats<V>(a.part + (2 * (size_t)chunk + !from_before) * a.pitch + c, acc);
-                else
-                    write_sum<T, V>(a, k, c, acc);
-            }
+            const bool from_before = token == head && before == token, goes_on = j + u + 1 == n && after == token;
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = 0.f;
+            for (int k = 0; k < K; ++k) {
+                const int at = c + 32 * k * V;
+                if (at < a.d) {
+                    if (from_before || goes_on)
+                        store_floats<V>(a.part + (2 * (size_t)chunk + !from_before) * a.pitch + at, acc[k]);
+                    else
+                        write_sum<T, V>(a, token, at, acc[k]);
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[k][i] = 0.f;
+            }
         }
     }
 }
 
-// Adds the partial sums of a token that begins in this block's chunk and goes
-// on behind it: 8 threads per column take every eighth chunk.
-constexpr int kJoinColumns = 32, kJoinLanes = NT / kJoinColumns;
+// Adds the partial sums of tokens that begin in a chunk and go on behind it.
+// Warp y looks at the y-th of a block's chunks and adds what begins there
+// where that is in few chunks; a longer token's chunks are shared out among
+// the warps, warp y taking the y-th, (y + 8)-th, ...
+constexpr int kJoinWarps = NT / 32, kJoinColumns = 128;
+constexpr int kJoinAlone = 8;      // chunks behind the first
+
+__device__ __forceinline__ void add_float4(float4 &acc, const float4 &v)
+{
+    acc.x += v.x;
+    acc.y += v.y;
+    acc.z += v.z;
+    acc.w += v.w;
+}
 
 template <typename T>
 __global__ void __launch_bounds__(NT) embed_join_kernel(const __grid_constant__ SumArgs a)
 {
     chain_begin();
+    __shared__ int token[kJoinWarps], ends[kJoinWarps];
+    __shared__ float4 sums[kJoinWarps][32];
+    const int lane = threadIdx.x & 31, y = threadIdx.x >> 5, strips = (a.d + kJoinColumns - 1) / kJoinColumns;
+    const int group = (int)(blockIdx.x / strips) * kJoinWarps, c = (int)(blockIdx.x % strips) * kJoinColumns + 4 * lane;
+    const auto part = [&](int chunk, int which) {
+        return *(const float4 *)(a.part + (2 * (size_t)chunk + which) * a.pitch + c);
+    };
     chain_wait();
-    const int strips = (a.d + kJoinColumns - 1) / kJoinColumns;
-    const int chunk = blockIdx.x / strips, last = chunk * kChunk + kChunk - 1;
-    if (last + 1 >= a.n) return;
-    const int key = a.key[last];
-    if (key >= a.vocab || a.key[last + 1] != key) return;
-    const int first = chunk * kChunk;
-    if (first > 0 && a.key[first] == key && a.key[first - 1] == key) return;   // begins before
-    int lo = last + 1, hi = a.n;              // the first sorted row behind the token's
-    while (lo < hi) {
-        const int mid = lo + (hi - lo) / 2;
-        if (a.key[mid] > key) hi = mid;
-        else lo = mid + 1;
-    }
-    const int end = (lo - 1) / kChunk;        // the last chunk with rows of it
-    const int x = threadIdx.x % kJoinColumns, y = threadIdx.x / kJoinColumns;
-    const int c = (int)(blockIdx.x % strips) * kJoinColumns + x;
-    float acc = 0.f;
-    if (c < a.d)
-        for (int k = chunk + y; k <= end; k += kJoinLanes)
-            acc += a.part[(2 * (size_t)k + (k == chunk)) * a.pitch + c];
-    __shared__ float sums[kJoinLanes][kJoinColumns];
-    sums[y][x] = acc;
-    __syncthreads();
-    if (y == 0 && c < a.d) {
-        float total[1] = {0.f};
+    {
+        const int chunk = group + y, first = chunk * kChunk, next = first + kChunk;
+        int key = -1, end = chunk;      // end: the last chunk with rows of it
+        if (next < a.n) {
+            const long at = (long)next + (long)lane * kChunk;      // (asked for at once with the others)
+            const int begin = at < a.n ? a.key[at] : -1;
+            const int before = first > 0 ? a.key[first - 1] : -1;
+            key = a.key[next - 1];
+            if (key >= a.vocab || before == key) key = -1;
+            const unsigned same = __ballot_sync(0xffffffffu, begin == key);
+            int run = same == 0xffffffffu ? 32 : __ffs(~same) - 1;
+            if (key >= 0) end += run;
+            while (key >= 0 && run == 32) {      // 32 chunks' first rows at once
+                const long more = ((long)end + 1 + lane) * kChunk;
+                const unsigned also = __ballot_sync(0xffffffffu, more < a.n && a.key[more] == key);
+                run = also == 0xffffffffu ? 32 : __ffs(~also) - 1;
+                end += run;
+            }
+            if (end == chunk) key = -1;
+        }
+        if (key >= 0 && end - chunk <= kJoinAlone) {
+            if (c < a.d) {
+                float4 v[kJoinAlone + 1];
 #pragma unroll
-        for (int k = 0; k < kJoinLanes; ++k) total[0] += sums[k][x];
-        write_sum<T, 1>(a, key, c, total);
+                for (int k = 0; k <= kJoinAlone; ++k)
+                    if (chunk + k <= end) v[k] = part(chunk + k, k == 0);
+#pragma unroll
+                for (int k = 1; k <= kJoinAlone; ++k)
+                    if (chunk + k <= end) add_float4(v[0], v[k]);
+                const float one[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (c + i < a.d) {
+                        const float x[1] = {one[i]};
+                        write_sum<T, 1>(a, key, c + i, x);
+                    }
+            }
+            key = -1;
+        }
+        if (lane == 0) {
+            token[y] = key;
+            ends[y] = end;
+        }
+    }
+    __syncthreads();
+    for (int x = 0; x < kJoinWarps; ++x) {
+        const int key = token[x], chunk = group + x, end = ends[x];
+        if (key < 0) continue;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c < a.d)
+            for (int k = chunk + y; k <= end; k += 8 * kJoinWarps) {
+                float4 v[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (k + u * kJoinWarps <= end) v[u] = part(k + u * kJoinWarps, u == 0 && k == chunk);
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (k + u * kJoinWarps <= end) add_float4(acc, v[u]);
+            }
+        sums[y][lane] = acc;
+        __syncthreads();
+        if (threadIdx.x < kJoinColumns) {
+            const int column = (int)(blockIdx.x % strips) * kJoinColumns + threadIdx.x;
+            float all[1] = {0.f};
+#pragma unroll
+            for (int k = 0; k < kJoinWarps; ++k) all[0] += ((const float *)sums[k])[threadIdx.x];
+            if (column < a.d) write_sum<T, 1>(a, key, column, all);
+        }
+        __syncthreads();
     }
 }
 
@@ -307,6 +520,7 @@ __global__ void __launch_bounds__(NT) embed_join_kernel(const __grid_constant__ 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
 struct EmbedPlan {
+    bool cluster;
     int passes, bits, tile, blocks, chunks;
     long pitch;
     size_t key[2], row[2], count, part, bytes;
@@ -319,20 +533,24 @@ EmbedPlan embed_plan(int rows, int d, int vocab)
     while (((int64_t)1 << bits) <= vocab) ++bits;      // keys 0 .. vocab
     q.passes = (bits + kDigitBits - 1) / kDigitBits;
     q.bits = (bits + q.passes - 1) / q.passes;
-    // tiles of at least a row per thread, at most about one block per SM (every block reads all counts)
-    long tile = ((long)rows + 151) / 152;
-    tile = (tile + kSortThreads - 1) / kSortThreads * kSortThreads;
-    q.tile = (int)tile;
-    q.blocks = (int)((rows + tile - 1) / tile);
+    q.cluster = rows <= kClusterRows;
+    if (q.cluster) {     // as many blocks as leave each a row per thread
+        for (q.blocks = 1; q.blocks < kMostBlocks && q.blocks * kSortThreads < rows;) q.blocks *= 2;
+        q.tile = (rows + q.blocks - 1) / q.blocks;
+    } else {             // at most about one block per SM: every block reads all counts
+        const long tile = ((long)rows + 151) / 152;
+        q.tile = (int)((tile + kSortThreads - 1) / kSortThreads * kSortThreads);
+        q.blocks = (int)(((long)rows + q.tile - 1) / q.tile);
+    }
     q.chunks = (rows + kChunk - 1) / kChunk;
     q.pitch = (d + 3) / 4 * 4;
     size_t at = 0;
     auto take = [&](size_t bytes) { const size_t p = at; at += up(bytes); return p; };
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < (q.cluster ? 1 : 2); ++x) {
         q.key[x] = take((size_t)rows * 4);
         q.row[x] = take((size_t)rows * 4);
     }
-    q.count = take((size_t)q.blocks * ((size_t)1 << q.bits) * 4);
+    q.count = take(q.cluster ? 0 : (size_t)q.blocks * ((size_t)1 << q.bits) * 4);
     q.part = take((size_t)q.chunks * 2 * q.pitch * 4);
     q.bytes = at;
     return q;
@@ -373,22 +591,44 @@ cudaError_t run_fwd(EmbedArgs a, cudaStream_t s)
 template <typename T, int V>
 cudaError_t run_sums(SumArgs a, cudaStream_t s)
 {
-    a.strips = (a.d + 32 * V - 1) / (32 * V);
+    a.strips = (a.d + kStrip - 1) / kStrip;
     const long tasks = (long)a.chunks * a.strips;
     cudaError_t e = chain_launch(embed_sum_kernel<T, V>, (unsigned)((tasks + NT / 32 - 1) / (NT / 32)), NT, 0, 1, s, a);
     if (e != cudaSuccess || a.chunks == 1) return e;
-    const long strips = (a.d + kJoinColumns - 1) / kJoinColumns;
-    return chain_launch(embed_join_kernel<T>, (unsigned)((a.chunks - 1) * strips), NT, 0, 1, s, a);
+    const long strips = (a.d + kJoinColumns - 1) / kJoinColumns, groups = (a.chunks + kJoinWarps - 2) / kJoinWarps;
+    return chain_launch(embed_join_kernel<T>, (unsigned)(groups * strips), NT, 0, 1, s, a);
 }
 
-cudaError_t run_bwd(const int64_t *tokens, const void *dout, float scale, int rows, int d, int vocab, txl_dtype dtype,
-                    bool accumulate, void *dtable, unsigned char *ws, cudaStream_t s)
+// blocks that set the table to zero: at most what fills the SMs
+unsigned zero_blocks(const ZeroJob &z)
 {
-    const EmbedPlan q = embed_plan(rows, d, vocab);
-    const size_t esz = dtype == TXL_F32 ? 4 : 2;
-    const ZeroJob none = {nullptr, 0}, whole = {(unsigned char *)dtable, (size_t)vocab * d * esz};
+    const size_t want = (z.bytes + 16 * kSortThreads * 4 - 1) / (16 * kSortThreads * 4), most = 2 * (size_t)device_sm_count();
+    return (unsigned)(want < most ? want : most);
+}
+
+cudaError_t sort_in_cluster(const EmbedPlan &q, const int64_t *tokens, int rows, int vocab, const ZeroJob &z, int *key,
+                            int *row, cudaStream_t s)
+{
+    const ClusterSort a = {tokens, key, row, rows, vocab, q.blocks, q.tile, q.bits, q.passes};
+    const size_t smem = ((size_t)(kSortWarps + 2) << q.bits) * 4 + kSortWarps * 4 + (size_t)q.tile * 16;
+    // (of all calls: the largest list and the most digits)
+    constexpr int kMost = ((kSortWarps + 2) << kDigitBits) * 4 + kSortWarps * 4 + kBlockRows * 16;
+    static_assert(kMost <= 227 << 10, "shared memory of a block");
+    cudaError_t e = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    if (e == cudaSuccess && q.blocks > 8)
+        e = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    const unsigned zero = zero_blocks(z), clusters = 1 + (zero + q.blocks - 1) / q.blocks;
+    return chain_launch(embed_sort_kernel, clusters * q.blocks, kSortThreads, smem, (unsigned)q.blocks, s, a, z);
+}
+
+cudaError_t sort_by_launches(const EmbedPlan &q, const int64_t *tokens, int rows, int vocab, const ZeroJob &z,
+                             unsigned char *ws, cudaStream_t s)
+{
     const size_t smem = (size_t)(kSortWarps << q.bits) * 4 + kSortWarps * 4;
-    cudaError_t e = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (kSortWarps << kDigitBits) * 4 + kSortWarps * 4);
+    const ZeroJob none = {nullptr, 0};
     for (int x = 0; x < q.passes && e == cudaSuccess; ++x) {
         SortPass p;
         p.tokens = x == 0 ? tokens : nullptr;
@@ -403,16 +643,27 @@ cudaError_t run_bwd(const int64_t *tokens, const void *dout, float scale, int ro
         p.blocks = q.blocks;
         p.shift = x * q.bits;
         p.bits = q.bits;
-        const bool zero = x == 0 && !accumulate;
-        const size_t rounds = whole.bytes / (16 * kSortThreads * 4) + 1, most = 2 * (size_t)device_sm_count();
-        const unsigned extra = zero ? (unsigned)(rounds < most ? rounds : most) : 0;
-        e = chain_launch(sort_count_kernel, (unsigned)q.blocks + extra, kSortThreads, 0, 1, s, p, zero ? whole : none);
+        const unsigned extra = x == 0 ? zero_blocks(z) : 0;
+        e = chain_launch(sort_count_kernel, (unsigned)q.blocks + extra, kSortThreads, 0, 1, s, p, x == 0 ? z : none);
         if (e == cudaSuccess) e = chain_launch(sort_place_kernel, (unsigned)q.blocks, kSortThreads, smem, 1, s, p);
     }
+    return e;
+}
+
+cudaError_t run_bwd(const int64_t *tokens, const void *dout, float scale, int rows, int d, int vocab, txl_dtype dtype,
+                    bool accumulate, void *dtable, unsigned char *ws, cudaStream_t s)
+{
+    const EmbedPlan q = embed_plan(rows, d, vocab);
+    const size_t esz = dtype == TXL_F32 ? 4 : 2;
+    const ZeroJob z = {(unsigned char *)dtable, accumulate ? 0 : (size_t)vocab * d * esz};
+    const int sorted = q.cluster ? 0 : (q.passes + 1) & 1;
+    int *key = (int *)(ws + q.key[sorted]), *row = (int *)(ws + q.row[sorted]);
+    const cudaError_t e = q.cluster ? sort_in_cluster(q, tokens, rows, vocab, z, key, row, s)
+                                    : sort_by_launches(q, tokens, rows, vocab, z, ws, s);
     if (e != cudaSuccess) return e;
     SumArgs a;
-    a.key = (int *)(ws + q.key[(q.passes + 1) & 1]);
-    a.row = (int *)(ws + q.row[(q.passes + 1) & 1]);
+    a.key = key;
+    a.row = row;
     a.dout = dout;
     a.dtable = dtable;
     a.part = (float *)(ws + q.part);
