@@ -5,12 +5,16 @@
 //     ds = rstd (g - mean_d(g) - xh mean_d(g xh)) + dsum,   g = dy gamma, xh = (s - mean) rstd
 //     dgamma = sum_i dy xh, dbeta = sum_i dy
 //
-// HBM-bound: a row is read once and stays in registers, as fp32, from its
-// loads to its result; G threads share it (a warp up to 1024 columns).  The
-// variance is the mean of the squared differences from the mean.  The
-// backward's groups of threads each take many rows and keep their columns'
-// sums for dgamma and dbeta in registers; a block adds its groups' up and
-// writes them, and a second launch adds the blocks' in a fixed order.
+// HBM-bound.  The variance is the mean of the squared differences from the
+// mean.  G threads share a row (a warp up to 1024 columns), which stays in
+// registers, as fp32, from its loads to its result.  The backward's warps
+// (groups of threads) take many rows each and keep their columns' sums for
+// dgamma and dbeta in registers; a block adds its warps' up and writes them,
+// and a second launch adds the blocks' in a fixed order.  Those registers
+// leave room for few warps, so up to 1024 columns a warp of the backward asks
+// for its next rows (asynchronous copies into shared memory, each lane its own
+// columns; not bf16 rows that are only 2-byte aligned, which such copies do
+// not serve) before it computes one.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -60,7 +64,7 @@ template <int G>
 constexpr int kBlock = G == 32 ? kWarpBlock : G;
 
 template <typename T, int V, int K, int G>
-__global__ void __launch_bounds__(kBlock<G>) norm_fwd_kernel(const __grid_constant__ NormArgs a)
+__global__ void __launch_bounds__(kBlock<G>, G == 32 && K * V <= 16 ? 4 : 1) norm_fwd_kernel(const __grid_constant__ NormArgs a)
 {
     chain_begin();
     __shared__ float shared[32];
@@ -78,6 +82,22 @@ __global__ void __launch_bounds__(kBlock<G>) norm_fwd_kernel(const __grid_consta
             raw[k] = load_raw<T, V>(x + c);
             if (a.residual) raw2[k] = load_raw<T, V>(res + c);
         }
+    }
+    // gamma and beta too, where the registers allow it
+    constexpr bool EARLY = K * V <= 16;
+    float gm[EARLY ? K : 1][V], bt[EARLY ? K : 1][V];
+    const auto affine = [&](int c, float (&g)[V], float (&b)[V]) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            g[i] = 1.f;
+            b[i] = 0.f;
+        }
+        if (a.gamma && c < a.d) load_floats<V>(a.gamma + c, g);
+        if (a.beta && c < a.d) load_floats<V>(a.beta + c, b);
+    };
+    if (EARLY) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) affine((k * G + t) * V, gm[EARLY ? k : 0], bt[EARLY ? k : 0]);
     }
     float sum = 0.f;
 #pragma unroll
@@ -118,15 +138,9 @@ __global__ void __launch_bounds__(kBlock<G>) norm_fwd_kernel(const __grid_consta
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int c = (k * G + t) * V;
+        float(&g)[V] = gm[EARLY ? k : 0], (&b)[V] = bt[EARLY ? k : 0];
+        if (!EARLY) affine(c, g, b);
         if (c < a.d) {
-            float g[V], b[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                g[i] = 1.f;
-                b[i] = 0.f;
-            }
-            if (a.gamma) load_floats<V>(a.gamma + c, g);
-            if (a.beta) load_floats<V>(a.beta + c, b);
 #pragma unroll
             for (int i = 0; i < V; ++i) g[i] = fmaf((s[k][i] - mean) * rstd, g[i], b[i]);
             store_vec<T, V>((T *)a.out + row * a.d + c, g);
@@ -238,6 +252,260 @@ __global__ void __launch_bounds__(kBlock<G>) norm_bwd_kernel(const __grid_consta
     }
 }
 
+// ---------------------------------------------------------------- a warp per row, read ahead
+// A lane's columns are G groups of 8: J = 8 / V vectors of V columns each,
+// vector k of all at column (k 32 + lane) V.
+constexpr int kRowWarps = kWarpBlock / 32;
+constexpr int kMostStages = 3;
+
+// shared memory of one row of one tensor; a stage: its tensors' rows, mean and rstd
+template <typename T, int G>
+constexpr int kRowBytes = 32 * 8 * G * (int)sizeof(T);
+template <typename T, int G>
+__host__ __device__ __forceinline__ int stage_bytes(int tensors) { return tensors * kRowBytes<T, G> + 16; }
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *to, const void *from)
+{
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(BYTES) : "memory");
+}
+
+// until at most n (0 .. kMostStages - 1) of the lane's groups of copies are under way
+__device__ __forceinline__ void wait_copies(int n)
+{
+    if (n == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 2;" ::: "memory");
+}
+
+// the warp's sums of a and of b: half the lanes go on with either
+__device__ __forceinline__ void two_sums(float &a, float &b)
+{
+    const bool low = (threadIdx.x & 16) == 0;
+    float v = (low ? a : b) + __shfl_xor_sync(0xffffffffu, low ? b : a, 16);
+#pragma unroll
+    for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    a = __shfl_sync(0xffffffffu, v, 0);
+    b = __shfl_sync(0xffffffffu, v, 16);
+}
+
+template <typename T, int V, int G>
+__device__ __forceinline__ void copy_row(unsigned char *to, const void *from, long row, int d, int lane)
+{
+    const T *x = (const T *)from + row * d;
+#pragma unroll
+    for (int k = 0; k < G * 8 / V; ++k) {
+        const int v = k * 32 + lane;
+        if (v * V < d) copy_async<V * (int)sizeof(T)>((T *)to + v * V, x + v * V);
+    }
+}
+
+// the lane's group g of a row in shared memory
+template <typename T, int V>
+__device__ __forceinline__ void group_of(const unsigned char *row, int g, int lane, float (&x)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8 / V; ++j) {
+        float v[V];
+        unpack<T, V>(load_raw<T, V>((const T *)row + ((g * (8 / V) + j) * 32 + lane) * V), v);
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[j * V + i] = v[i];
+    }
+}
+
+// ... and of gamma or beta
+template <int V>
+__device__ __forceinline__ void floats_of(const float *row, int g, int lane, float (&x)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8 / V; ++j) {
+        float v[V];
+        load_floats<V>(row + ((g * (8 / V) + j) * 32 + lane) * V, v);
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[j * V + i] = v[i];
+    }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_group(T *row, int g, int lane, int d, const float (&x)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8 / V; ++j) {
+        const int c = ((g * (8 / V) + j) * 32 + lane) * V;
+        float v[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = x[j * V + i];
+        if (c < d) store_vec<T, V>(row + c, v);
+    }
+}
+
+// columns past the row's end are zero in every stage: nothing copies there
+template <typename T, int V, int G>
+__device__ __forceinline__ void clear_ends(unsigned char *mine, int stages, int bytes, int tensors, int d, int lane)
+{
+    const float none[V] = {};
+    for (int x = 0; x < stages; ++x)
+        for (int y = 0; y < tensors; ++y)
+#pragma unroll
+            for (int k = 0; k < G * 8 / V; ++k) {
+                const int v = k * 32 + lane;
+                if (v * V >= d) store_vec<T, V>((T *)(mine + x * bytes + y * kRowBytes<T, G>) + v * V, none);
+            }
+}
+
+// a float vector of the columns in shared memory, zero past the row's end
+template <int G>
+__device__ __forceinline__ void load_columns(float *to, const float *from, float otherwise, int d)
+{
+    for (int c = threadIdx.x; c < 32 * 8 * G; c += kWarpBlock) to[c] = c < d ? (from ? from[c] : otherwise) : 0.f;
+}
+
+template <typename T, int V, int G>
+__global__ void __launch_bounds__(kWarpBlock, 2) norm_bwd_rows_kernel(const __grid_constant__ NormArgs a, int stages)
+{
+    chain_begin();
+    constexpr int kWide = 32 * 8 * G;
+    constexpr bool KEEP = G <= 2;
+    extern __shared__ __align__(16) unsigned char dynamic[];
+    float *gamma = (float *)dynamic;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    // tensors in a stage: dy, x, residual, dsum
+    const int at_dsum = a.residual ? 3 : 2, tensors = at_dsum + (a.dsum ? 1 : 0);
+    const int bytes = stage_bytes<T, G>(tensors);
+    unsigned char *mine = (unsigned char *)(gamma + kWide) + w * stages * bytes;
+    const long step = (long)gridDim.x * kRowWarps;
+    long row = (long)blockIdx.x * kRowWarps + w;
+    clear_ends<T, V, G>(mine, stages, bytes, tensors, a.d, lane);
+    chain_wait();
+    const auto ask = [&](long r, int stage) {
+        unsigned char *to = mine + stage * bytes;
+        if (r < a.rows) {
+            copy_row<T, V, G>(to, a.dy, r, a.d, lane);
+            copy_row<T, V, G>(to + kRowBytes<T, G>, a.x, r, a.d, lane);
+            if (a.residual) copy_row<T, V, G>(to + 2 * kRowBytes<T, G>, a.residual, r, a.d, lane);
+            if (a.dsum) copy_row<T, V, G>(to + at_dsum * kRowBytes<T, G>, a.dsum, r, a.d, lane);
+            if (lane < 2) copy_async<4>(to + tensors * kRowBytes<T, G> + 4 * lane, (lane ? a.rstd : a.mean) + r);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int x = 0; x + 1 < stages; ++x) ask(row + x * step, x);
+    load_columns<G>(gamma, a.gamma, 1.f, a.d);
+    __syncthreads();
+    uint64_t dg[G][4], db[G][4];
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dg[g][j] = db[g][j] = 0;
+    const float inverse = 1.f / (float)a.d;
+    int stage = 0, next = stages - 1;
+    for (; row < a.rows; row += step) {
+        ask(row + (stages - 1) * step, next);
+        wait_copies(stages - 1);
+        __syncwarp();           // (mean and rstd are two lanes' copies)
+        const unsigned char *x = mine + stage * bytes;
+        const float2 stats = *(const float2 *)(x + tensors * kRowBytes<T, G>);
+        const uint64_t mean2 = pair(stats.x, stats.x), rstd2 = pair(stats.y, stats.y);
+        // xh and dy gamma of a group (dy also by itself): computed for the sums and, where keeping them
+        // would take too many registers, again for dx
+        const auto load = [&](int g, uint64_t (&hat)[4], uint64_t (&dy)[4], uint64_t (&t)[4]) {
+            float v[8], u[8];
+            group_of<T, V>(x + kRowBytes<T, G>, g, lane, v);
+            if (a.residual) {
+                group_of<T, V>(x + 2 * kRowBytes<T, G>, g, lane, u);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    unpair(pair_add(pair(v[2 * j], v[2 * j + 1]), pair(u[2 * j], u[2 * j + 1])), v[2 * j], v[2 * j + 1]);
+            }
+            group_of<T, V>(x, g, lane, u);
+            float gm[8];
+            floats_of<V>(gamma, g, lane, gm);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                hat[j] = pair_mul(pair_sub(pair(v[2 * j], v[2 * j + 1]), mean2), rstd2);
+                dy[j] = pair(u[2 * j], u[2 * j + 1]);
+                t[j] = pair_mul(dy[j], pair(gm[2 * j], gm[2 * j + 1]));
+            }
+        };
+        uint64_t sums = 0, alongs = 0, hats[KEEP ? G : 1][4], ts[KEEP ? G : 1][4];
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            uint64_t(&hat)[4] = hats[KEEP ? g : 0], (&t)[4] = ts[KEEP ? g : 0], dy[4];
+            load(g, hat, dy, t);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                dg[g][j] = pair_fma(dy[j], hat[j], dg[g][j]);
+                db[g][j] = pair_add(db[g][j], dy[j]);
+                sums = pair_add(sums, t[j]);
+                alongs = pair_fma(t[j], hat[j], alongs);
+            }
+            if (!KEEP) asm volatile("" ::: "memory");      // (one group's values in registers at a time)
+        }
+        float lo, hi;
+        unpair(sums, lo, hi);
+        float sum = lo + hi;
+        unpair(alongs, lo, hi);
+        float along = lo + hi;
+        two_sums(sum, along);
+        sum *= inverse;
+        along *= inverse;
+        const uint64_t sum2 = pair(sum, sum), minus2 = pair(-along, -along);
+#pragma unroll(KEEP ? G : 1)
+        for (int g = 0; g < G; ++g) {
+            uint64_t(&hat)[4] = hats[KEEP ? g : 0], (&t)[4] = ts[KEEP ? g : 0], dy[4];
+            if (!KEEP) load(g, hat, dy, t);
+            float out[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) t[j] = pair_mul(pair_fma(hat[j], minus2, pair_sub(t[j], sum2)), rstd2);
+            if (a.dsum) {
+                float u[8];
+                group_of<T, V>(x + at_dsum * kRowBytes<T, G>, g, lane, u);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) t[j] = pair_add(t[j], pair(u[2 * j], u[2 * j + 1]));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) unpair(t[j], out[2 * j], out[2 * j + 1]);
+            store_group<T, V>((T *)a.out + row * a.d, g, lane, a.d, out);
+        }
+        __syncwarp();           // (before another row's mean and rstd arrive here)
+        stage = stage + 1 == stages ? 0 : stage + 1;
+        next = next + 1 == stages ? 0 : next + 1;
+    }
+    if (!a.weights) return;
+    // the block's sums: the stages' memory is free once every warp is through
+    wait_copies(0);
+    __syncthreads();
+    float *columns = gamma + kWide;       // [8 warps][2][kWide]
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int j = 0; j < 8 / V; ++j) {
+            const int c = ((g * (8 / V) + j) * 32 + lane) * V;
+            float x[2][V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int at = j * V + i;
+                float lo, hi;
+                unpair(dg[g][at / 2], lo, hi);
+                x[0][i] = at % 2 ? hi : lo;
+                unpair(db[g][at / 2], lo, hi);
+                x[1][i] = at % 2 ? hi : lo;
+            }
+            store_floats<V>(columns + (w * 2) * kWide + c, x[0]);
+            store_floats<V>(columns + (w * 2 + 1) * kWide + c, x[1]);
+        }
+    __syncthreads();
+    float *part = a.part + (size_t)blockIdx.x * 2 * a.pitch;
+    for (int c = threadIdx.x; c < 2 * kWide; c += kWarpBlock) {
+        float sum = 0.f;
+#pragma unroll
+        for (int x = 0; x < kRowWarps; ++x) sum += columns[x * 2 * kWide + c];
+        const int column = c % kWide;
+        if (column < a.d) part[(c / kWide) * a.pitch + column] = sum;
+    }
+}
+
 // adds the blocks' column sums: 32 threads per column
 __global__ void __launch_bounds__(1024)
 norm_columns_kernel(const float *part, int blocks, int d, int pitch, float *dgamma, float *dbeta)
@@ -282,34 +550,83 @@ txl_status norm_sizes(int rows, int d, txl_dtype dtype)
 }
 
 template <typename T, int V, int K, int G>
-cudaError_t launch_norm(const NormArgs &a, bool backward, int blocks, cudaStream_t s)
+cudaError_t launch_fwd(const NormArgs &a, cudaStream_t s)
 {
-    if (!backward) {
-        const unsigned grid = (unsigned)(G == 32 ? ((long)a.rows + kWarpBlock / 32 - 1) / (kWarpBlock / 32) : a.rows);
-        return chain_launch(norm_fwd_kernel<T, V, K, G>, grid, kBlock<G>, 0, 1, s, a);
-    }
-    const size_t smem = G == 32 ? (size_t)(kWarpBlock / 32) * 2 * 32 * V * K * 4 : 0;
-    if (smem > 48 << 10) {
-        const cudaError_t e = cudaFuncSetAttribute(norm_bwd_kernel<T, V, K, G>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    const unsigned grid = (unsigned)(G == 32 ? ((long)a.rows + kRowWarps - 1) / kRowWarps : a.rows);
+    return chain_launch(norm_fwd_kernel<T, V, K, G>, grid, kBlock<G>, 0, 1, s, a);
+}
+
+template <typename K>
+cudaError_t allow_shared(K kernel, size_t bytes)
+{
+    return bytes > 48 << 10 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)
+                            : cudaSuccess;
+}
+
+// stages that leave room for `blocks` blocks per SM (less, for a single stage of wide rows)
+int stages_for(size_t stage, size_t other, int blocks)
+{
+    const size_t most = (224 << 10) / blocks - 1024;
+    int stages = kMostStages;
+    while (stages > 1 && other + stages * kRowWarps * stage > most) --stages;
+    return stages;
+}
+
+template <typename T, int V, int G>
+cudaError_t launch_rows(const NormArgs &a, int blocks, cudaStream_t s)
+{
+    constexpr size_t kWide = 32 * 8 * G * 4;
+    const size_t stage = stage_bytes<T, G>(2 + (a.residual ? 1 : 0) + (a.dsum ? 1 : 0));
+    const int stages = stages_for(stage, kWide, 2);
+    size_t smem = stages * kRowWarps * stage;
+    if (smem < 2 * kRowWarps * kWide) smem = 2 * kRowWarps * kWide;      // (the column sums, at the end)
+    smem += kWide;
+    const cudaError_t e = allow_shared(norm_bwd_rows_kernel<T, V, G>, smem);
+    if (e != cudaSuccess) return e;
+    return chain_launch(norm_bwd_rows_kernel<T, V, G>, (unsigned)blocks, kWarpBlock, smem, 1, s, a, stages);
+}
+
+template <typename T, int V, int K, int G>
+cudaError_t launch_bwd(const NormArgs &a, int blocks, cudaStream_t s)
+{
+    const size_t smem = G == 32 ? (size_t)kRowWarps * 2 * 32 * V * K * 4 : 0;
+    const cudaError_t e = allow_shared(norm_bwd_kernel<T, V, K, G>, smem);
+    if (e != cudaSuccess) return e;
     return chain_launch(norm_bwd_kernel<T, V, K, G>, (unsigned)blocks, kBlock<G>, smem, 1, s, a);
 }
 
-// K vectors of V columns per thread for the smallest group that holds a row
+// the smallest kernels that hold a row
+template <typename T, int V>
+cudaError_t pick_fwd(const NormArgs &a, cudaStream_t s)
+{
+    if constexpr (V >= 4) {
+        if (a.d <= 256) return launch_fwd<T, V, 8 / V, 32>(a, s);
+    }
+    if (a.d <= 512) return launch_fwd<T, V, 16 / V, 32>(a, s);
+    if (a.d <= 1024) return launch_fwd<T, V, 32 / V, 32>(a, s);
+    if (a.d <= 4096) return launch_fwd<T, V, 16 / V, 256>(a, s);
+    return launch_fwd<T, V, 8 / V, 1024>(a, s);
+}
+
+template <typename T, int V>
+cudaError_t pick_bwd(const NormArgs &a, int blocks, cudaStream_t s)
+{
+    if constexpr (sizeof(T) * V >= 4) {
+        if (a.d <= 256) return launch_rows<T, V, 1>(a, blocks, s);
+        if (a.d <= 512) return launch_rows<T, V, 2>(a, blocks, s);
+        if (a.d <= 1024) return launch_rows<T, V, 4>(a, blocks, s);
+    } else {
+        if (a.d <= 512) return launch_bwd<T, V, 16 / V, 32>(a, blocks, s);
+        if (a.d <= 1024) return launch_bwd<T, V, 32 / V, 32>(a, blocks, s);
+    }
+    if (a.d <= 4096) return launch_bwd<T, V, 16 / V, 256>(a, blocks, s);
+    return launch_bwd<T, V, 8 / V, 1024>(a, blocks, s);
+}
+
 template <typename T, int V>
 cudaError_t pick_norm(const NormArgs &a, bool backward, int blocks, cudaStream_t s)
 {
-    if constexpr (V >= 4) {
-        if (a.d <= 256) return launch_norm<T, V, 8 / V, 32>(a, backward, blocks, s);
-        if (a.d <= 512) return launch_norm<T, V, 16 / V, 32>(a, backward, blocks, s);
-    } else if (a.d <= 512) {
-        return launch_norm<T, V, 16 / V, 32>(a, backward, blocks, s);
-    }
-    if (a.d <= 1024) return launch_norm<T, V, 32 / V, 32>(a, backward, blocks, s);
-    if (a.d <= 4096) return launch_norm<T, V, 16 / V, 256>(a, backward, blocks, s);
-    return launch_norm<T, V, 8 / V, 1024>(a, backward, blocks, s);
+    return backward ? pick_bwd<T, V>(a, blocks, s) : pick_fwd<T, V>(a, s);
 }
 
 // the widest vector that every row of every tensor can be read by
@@ -317,7 +634,8 @@ cudaError_t run_norm(const NormArgs &a, txl_dtype dtype, bool backward, int bloc
 {
     const size_t esz = dtype == TXL_F32 ? 4 : 2;
     int wide = (int)esz;
-    for (int n : {16, 4}) {
+    for (int n : {16, 8, 4}) {
+        if (n == 8 && esz == 2) continue;
         bool fits = (size_t)a.d * esz % n == 0;
         for (const void *p : {a.x, a.residual, a.dy, a.dsum, (const void *)a.out, (const void *)a.sum})
             fits = fits && at_boundary(p, n);
@@ -329,7 +647,8 @@ cudaError_t run_norm(const NormArgs &a, txl_dtype dtype, bool backward, int bloc
         }
     }
     if (dtype == TXL_F32)
-        return wide == 16 ? pick_norm<float, 4>(a, backward, blocks, s) : pick_norm<float, 1>(a, backward, blocks, s);
+        return wide == 16  ? pick_norm<float, 4>(a, backward, blocks, s)
+               : wide == 8 ? pick_norm<float, 2>(a, backward, blocks, s) : pick_norm<float, 1>(a, backward, blocks, s);
     return wide == 16  ? pick_norm<__nv_bfloat16, 8>(a, backward, blocks, s)
            : wide == 4 ? pick_norm<__nv_bfloat16, 2>(a, backward, blocks, s)
                        : pick_norm<__nv_bfloat16, 1>(a, backward, blocks, s);
