@@ -41,7 +41,9 @@ constexpr int kPer = 8;                         // elements per thread and round
 constexpr int kRound = NT * kPer;
 constexpr int kBlockElems = 256;                // elements that share a scale: one warp's
 constexpr float kTop = 448.f;                   // the largest e4m3 value
-constexpr int kRounds = 4;                      // rounds of a block of a large call
+constexpr int kCodesResident = 4;               // blocks per SM where moments have 8 bits
+constexpr int kResident = 4;                    // ... 32 bits
+constexpr int kRounds = 4;                      // rounds of a block, at most
 constexpr int kMostTensors = 384, kFewTensors = 48;   // per launch: 30 KB of arguments, 4 KB
 constexpr int64_t kMaxElements = (int64_t)1 << 40;    // of one tensor
 
@@ -295,10 +297,11 @@ struct Eight {
     float ms, vs;              // their scales
 };
 
-// from i on (n of them exist)
-template <bool CODES>
-__device__ __forceinline__ void load_eight(const Tensor &t, int64_t i, int n, bool wide, Eight &x)
+// from i on (n of them exist; WHOLE: the block's are all there and aligned)
+template <bool CODES, bool WHOLE>
+__device__ __forceinline__ void load_eight(const Tensor &t, int64_t i, int n, Eight &x)
 {
+    const bool wide = WHOLE || (t.wide && n == kPer);
     if (t.grad_f32) load8((const float *)t.grad, i, n, wide, x.g);
     else load8((const __nv_bfloat16 *)t.grad, i, n, wide, x.g);
     if (t.master) load8((const float *)t.master, i, n, wide, x.p);
@@ -308,7 +311,7 @@ __device__ __forceinline__ void load_eight(const Tensor &t, int64_t i, int n, bo
         load_codes(t.m, i, n, wide, x.cm);
         load_codes(t.v, i, n, wide, x.cv);
         x.ms = x.vs = 0.f;
-        if (i / kBlockElems * kBlockElems < t.n) {       // (the same for a warp)
+        if (WHOLE || i / kBlockElems * kBlockElems < t.n) {       // (the same for a warp)
             x.ms = t.m_scale[i / kBlockElems];
             x.vs = t.v_scale[i / kBlockElems];
         }
@@ -319,10 +322,11 @@ __device__ __forceinline__ void load_eight(const Tensor &t, int64_t i, int n, bo
 }
 
 // the step of what load_eight gave
-template <bool CODES>
+template <bool CODES, bool WHOLE>
 __device__ __forceinline__ void step_eight(const Tensor &t, const StepScalars &s, const Rates &r, uint32_t key, int64_t i,
-                                           int n, bool wide, Eight &x)
+                                           int n, Eight &x)
 {
+    const bool wide = WHOLE || (t.wide && n == kPer);
     const auto both = [](float y) { return pair(y, y); };
     uint64_t m2[4], root2[4];
 #pragma unroll
@@ -375,10 +379,19 @@ __device__ __forceinline__ void step_eight(const Tensor &t, const StepScalars &s
     }
 }
 
+template <bool CODES, bool WHOLE>
+__device__ __forceinline__ void eight(const Tensor &t, const StepScalars &s, const Rates &r, uint32_t key, int64_t i, int n)
+{
+    Eight x;
+    load_eight<CODES, WHOLE>(t, i, n, x);
+    step_eight<CODES, WHOLE>(t, s, r, key, i, n, x);
+}
+
 // Blocks take up to kRounds rounds, gridDim.x apart: the blocks at work are
-// then next to one another in all of a tensor's buffers.
-template <int N>
-__global__ void __launch_bounds__(NT, 5)
+// then next to one another in all of a tensor's buffers.  CODES: for lists with
+// any 8-bit moments.
+template <int N, bool CODES>
+__global__ void __launch_bounds__(NT, CODES ? kCodesResident : kResident)
 adamw_kernel(const __grid_constant__ Tensors<N> list, const __grid_constant__ StepScalars s)
 {
     chain_begin();
@@ -407,23 +420,22 @@ adamw_kernel(const __grid_constant__ Tensors<N> list, const __grid_constant__ St
     __syncthreads();
     const Rates r = shared;
     if (!r.go) return;
-    Eight x;
 #pragma unroll 1
     for (int k = 0; k < kRounds; ++k) {
         const int round = blockIdx.x + k * gridDim.x;
         if (round >= list.rounds) return;
         const int at = tensor[k];
         const Tensor &t = list.t[at];
-        const int64_t i = (int64_t)(round - list.first[at]) * kRound + threadIdx.x * kPer;
+        const int64_t base = (int64_t)(round - list.first[at]) * kRound, i = base + threadIdx.x * kPer;
         const int n = i >= t.n ? 0 : t.n - i < kPer ? (int)(t.n - i) : kPer;
-        const bool wide = t.wide && n == kPer;
-        if (!t.m_scale) {
-            load_eight<false>(t, i, n, wide, x);
-            step_eight<false>(t, s, r, 0, i, n, wide, x);
-            continue;
+        const bool whole = t.wide && base + kRound <= t.n;
+        if (CODES && t.m_scale) {
+            if (whole) eight<true, true>(t, s, r, keys[k], i, kPer);
+            else eight<true, false>(t, s, r, keys[k], i, n);
+        } else {
+            if (whole) eight<false, true>(t, s, r, 0, i, kPer);
+            else eight<false, false>(t, s, r, 0, i, n);
         }
-        load_eight<true>(t, i, n, wide, x);
-        step_eight<true>(t, s, r, keys[k], i, n, wide, x);
     }
 }
 
@@ -597,6 +609,7 @@ cudaError_t launch_step(const txl_adamw_tensor *t, const int *order, int count, 
 {
     Tensors<N> list;
     int rounds = 0;
+    bool codes = false;
     for (int k = 0; k < count; ++k) {
         const txl_adamw_tensor &x = t[order[k]];
         Tensor &y = list.t[k];
@@ -617,12 +630,16 @@ cudaError_t launch_step(const txl_adamw_tensor *t, const int *order, int count, 
         y.wide = at_boundary(y.param, 16) && at_boundary(y.master, 16) && at_boundary(y.grad, 16) &&
                  at_boundary(y.m, state) && at_boundary(y.v, state);
         rounds += (int)chunks_of(x.size, 1);
+        codes = codes || y.m_scale;
     }
     list.count = count;
     list.rounds = rounds;
-    // one round per block where that is few blocks, several where they are many (fewer searches)
-    const int per = rounds <= 152 * 16 ? 1 : kRounds;
-    return chain_launch(adamw_kernel<N>, (unsigned)((rounds + per - 1) / per), NT, 0, 1, s, list, sc);
+    // One round per block where that is few blocks.  Several where they are many, for fewer searches
+    // and rates: 2 and 4 rounds take 106 and 100 us for 34 M weights with 8-bit moments, but 1004
+    // and 1014 us for 229 M with 32-bit ones, which have less to compute.
+    const int per = rounds <= 152 * 16 ? 1 : codes ? kRounds : 2;
+    return chain_launch(codes ? adamw_kernel<N, true> : adamw_kernel<N, false>, (unsigned)((rounds + per - 1) / per), NT, 0,
+                        1, s, list, sc);
 }
 
 template <int N>
