@@ -405,8 +405,8 @@ adamw_kernel(const __grid_constant__ Tensors<N> list, const __grid_constant__ St
         r.factor = s.grad_scale ? *s.grad_scale : 1.f;
         const int64_t step = s.step_at ? *s.step_at : s.step;
         if (threadIdx.x < kRounds) {
-            const int round = blockIdx.x + threadIdx.x * gridDim.x;
-            const int at = round < list.rounds ? tensor_of(list, round) : 0;
+            const unsigned round = blockIdx.x + threadIdx.x * gridDim.x;
+            const int at = round < (unsigned)list.rounds ? tensor_of(list, (int)round) : 0;
             tensor[threadIdx.x] = at;
             keys[threadIdx.x] = mix(list.t[at].key + (uint32_t)step);
         }
@@ -422,11 +422,11 @@ adamw_kernel(const __grid_constant__ Tensors<N> list, const __grid_constant__ St
     if (!r.go) return;
 #pragma unroll 1
     for (int k = 0; k < kRounds; ++k) {
-        const int round = blockIdx.x + k * gridDim.x;
-        if (round >= list.rounds) return;
+        const unsigned round = blockIdx.x + k * gridDim.x;      // (past 2^31 for a list of 2^30)
+        if (round >= (unsigned)list.rounds) return;
         const int at = tensor[k];
         const Tensor &t = list.t[at];
-        const int64_t base = (int64_t)(round - list.first[at]) * kRound, i = base + threadIdx.x * kPer;
+        const int64_t base = (int64_t)((int)round - list.first[at]) * kRound, i = base + threadIdx.x * kPer;
         const int n = i >= t.n ? 0 : t.n - i < kPer ? (int)(t.n - i) : kPer;
         const bool whole = t.wide && base + kRound <= t.n;
         if (CODES && t.m_scale) {
