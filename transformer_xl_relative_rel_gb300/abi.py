@@ -629,7 +629,7 @@ class _Call:
 
     def __init__(self, first, stream):
         self.dev = first.get_device()
-        self.device, self.stream = first.device, stream
+        self.stream = stream
         self.placed = first.is_contiguous()
 
     def arg(self, name, t, shape, dtype):
@@ -638,7 +638,7 @@ class _Call:
             return None
         if t.shape != shape:
             raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         if t.get_device() != self.dev or not t.is_contiguous():
             self.placed = False
@@ -653,10 +653,11 @@ class _Call:
 
     def make(self, shape, dtype):
         import torch
+        device = torch.device("cuda", self.dev)
         if self.stream is not None:
             with torch.cuda.stream(self.stream):
-                return torch.empty(shape, dtype=dtype, device=self.device)
-        return torch.empty(shape, dtype=dtype, device=self.device)
+                return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
 
     def launch(self, fn, *args):
         """fn(*args, stream) with the tensors' device current; its status"""
@@ -908,14 +909,17 @@ def layer_norm_bwd_workspace_bytes(rows: int, d_model: int, dtype_code: int) -> 
 
 
 def _norm_sizes(x, what):
-    """(lead, rows, d) of a layer norm's x"""
-    if not x.dim():
+    """(shape, lead, rows, d) of a layer norm's x"""
+    shape = tuple(x.shape)
+    if not shape:
         raise ValueError("x must be [*lead, d_model]")
-    lead, d = x.shape[:-1], x.shape[-1]
-    rows = lead.numel()
+    lead, d = shape[:-1], shape[-1]
+    rows = 1
+    for n in lead:
+        rows *= n
     if (rows | d) >> 31:
         _loss_sizes(what, rows, d)
-    return lead, rows, d
+    return shape, lead, rows, d
 
 
 def layer_norm_fwd(x, gamma=None, beta=None, residual=None, eps: float = 1e-5, y=None, sum=None, mean=None, rstd=None,
@@ -929,9 +933,9 @@ def layer_norm_fwd(x, gamma=None, beta=None, residual=None, eps: float = 1e-5, y
     (y, mean, rstd): y like x, the others float32 [*lead], for
     ``layer_norm_bwd``."""
     import torch
-    lead, rows, d = _norm_sizes(x, "txl_layer_norm_fwd")
+    shape, lead, rows, d = _norm_sizes(x, "txl_layer_norm_fwd")
     c = _Call(x, stream)
-    code, shape, dt, f32 = _dtype_code(x), x.shape, x.dtype, torch.float32
+    code, dt, f32 = _dtype_code(x), x.dtype, torch.float32
     r = c.arg("residual", residual, shape, dt)
     g = c.arg("gamma", gamma, (d,), f32)
     b = c.arg("beta", beta, (d,), f32)
@@ -960,9 +964,9 @@ def layer_norm_bwd(dy, x, mean, rstd, gamma=None, residual=None, dsum=None, grad
     same keys; ``workspace``: of ``layer_norm_bwd_workspace_bytes`` bytes, as
     ``embed_bwd``'s."""
     import torch
-    lead, rows, d = _norm_sizes(x, "txl_layer_norm_bwd")
+    shape, lead, rows, d = _norm_sizes(x, "txl_layer_norm_bwd")
     c = _Call(x, stream)
-    code, shape, dt, f32 = _dtype_code(x), x.shape, x.dtype, torch.float32
+    code, dt, f32 = _dtype_code(x), x.dtype, torch.float32
     given = c.arg("dy", dy, shape, dt)
     r = c.arg("residual", residual, shape, dt)
     o = c.arg("dsum", dsum, shape, dt)
@@ -1017,39 +1021,43 @@ class AdamwTensors:
         none = [None] * n
         lists = dict(params=params, grads=grads, exp_avgs=exp_avgs, exp_avg_sqs=exp_avg_sqs, masters=masters or none,
                      exp_avg_scales=exp_avg_scales or none, exp_avg_sq_scales=exp_avg_sq_scales or none)
-        decay = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else list(weight_decay)
+        lists = {name: list(x) for name, x in lists.items()}
+        decay = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else [float(x) for x in weight_decay]
         for name, x in list(lists.items()) + [("weight_decay", decay)]:
             if len(x) != n:
                 raise ValueError(f"{name} must have an entry per param ({n}), got {len(x)}")
-        self._array = (_AdamwTensor * max(n, 1))()
-        self._dev = params[0].get_device() if n else None
-        f32 = torch.float32
-        for k in range(n):
-            p, g, m, v, master, ms, vs = (lists[name][k] for name in ("params", "grads", "exp_avgs", "exp_avg_sqs",
-                                                                      "masters", "exp_avg_scales", "exp_avg_sq_scales"))
-            code = _dtype_code(p)
-            g_code = _dtype_code(g)
-            if g.shape != p.shape or m.shape != p.shape or v.shape != p.shape or \
-                    (master is not None and master.shape != p.shape):
-                raise ValueError(f"tensor {k}: grad, master and moments must be {list(p.shape)}")
-            if master is not None and (master.dtype != f32 or code == TXL_F32):
+        array = (_AdamwTensor * max(n, 1))()
+        dev = params[0].get_device() if n else None
+        f32, e4m3 = torch.float32, torch.float8_e4m3fn
+        codes = {f32: TXL_F32, torch.bfloat16: TXL_BF16}
+        for k, (p, g, m, v, w, ms, vs, wd) in enumerate(zip(*lists.values(), decay)):
+            shape, size = p.shape, p.numel()
+            if g.shape != shape or m.shape != shape or v.shape != shape or (w is not None and w.shape != shape):
+                raise ValueError(f"tensor {k}: grad, master and moments must be {list(shape)}")
+            code, g_code = codes.get(p.dtype), codes.get(g.dtype)
+            if code is None or g_code is None:
+                raise TypeError(f"tensor {k}: unsupported dtype {p.dtype}, {g.dtype} (float32 or bfloat16)")
+            if w is not None and (w.dtype is not f32 or code == TXL_F32):
                 raise TypeError(f"tensor {k}: a master is float32 beside a bfloat16 param")
-            state = f32 if ms is None else torch.float8_e4m3fn
-            if (ms is None) != (vs is None) or m.dtype != state or v.dtype != state:
+            state = f32 if ms is None else e4m3
+            if (ms is None) != (vs is None) or m.dtype is not state or v.dtype is not state:
                 raise TypeError(f"tensor {k}: moments are float32 without scales, or float8_e4m3fn with both")
-            blocks = ((p.numel() + 255) // 256,)
-            for s in (ms, vs):
-                if s is not None and (s.shape != blocks or s.dtype != f32):
+            if ms is not None:
+                blocks = ((size + 255) // 256,)
+                if ms.shape != blocks or vs.shape != blocks or ms.dtype is not f32 or vs.dtype is not f32:
                     raise ValueError(f"tensor {k}: scales must be float32 {list(blocks)}")
-            for x in (p, g, m, v, master, ms, vs):
-                if x is not None and (not x.is_cuda or x.get_device() != self._dev or not x.is_contiguous()):
-                    raise ValueError("all tensors must be contiguous CUDA tensors on one device")
-            a = self._array[k]
-            a.param, a.master, a.grad, a.exp_avg, a.exp_avg_sq = _ptr(p), _ptr(master), _ptr(g), _ptr(m), _ptr(v)
-            a.exp_avg_scale, a.exp_avg_sq_scale = _ptr(ms), _ptr(vs)
-            a.size, a.weight_decay, a.param_dtype, a.grad_dtype = p.numel(), decay[k], code, g_code
-        self._count = n
-        self._kept = lists
+            for x in (p, g, m, v, w, ms, vs):
+                if x is not None and (x.get_device() != dev or not x.is_contiguous()):
+                    dev = -1
+            if dev < 0:
+                raise ValueError("all tensors must be contiguous CUDA tensors on one device")
+            if size:
+                array[k] = (p.data_ptr(), None if w is None else w.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(),
+                            None if ms is None else ms.data_ptr(), None if ms is None else vs.data_ptr(), size, wd, code,
+                            g_code)
+            else:
+                array[k] = (None, None, None, None, None, None, None, 0, wd, code, g_code)
+        self._array, self._dev, self._count, self._kept = array, dev, n, lists
 
     def __len__(self):
         return self._count
@@ -1063,7 +1071,7 @@ class _ListCall(_Call):
         if not isinstance(tensors, AdamwTensors):
             raise TypeError("tensors must be an AdamwTensors")
         self.dev = torch.cuda.current_device() if tensors._dev is None else tensors._dev
-        self.device, self.stream, self.placed = torch.device("cuda", self.dev), stream, True
+        self.stream, self.placed = stream, True
 
 
 def grad_norm_workspace_bytes(tensors) -> int:
