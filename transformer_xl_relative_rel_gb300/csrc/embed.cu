@@ -93,10 +93,20 @@ __device__ __forceinline__ int sort_key(const SortPass &a, int i)
     return t >= 0 && t < a.vocab ? (int)t : a.vocab;
 }
 
-// the digit of row i, one past the digits for a lane behind the end
-__device__ __forceinline__ int sort_digit(const SortPass &a, int key, bool in)
+// The lanes with the digit d, among those that have a row (in).  A ballot per
+// bit: the instruction that matches whole values takes a turn per different
+// value (131072 rows of as many tokens sorted in 51 us with it, 39 without).
+__device__ __forceinline__ unsigned same_digit(int d, int bits, bool in)
 {
-    return in ? (key >> a.shift) & ((1 << a.bits) - 1) : 1 << a.bits;
+    unsigned same = __ballot_sync(0xffffffffu, in);
+#pragma unroll
+    for (int b = 0; b < kDigitBits; ++b)
+        if (b < bits) {
+            const bool set = d >> b & 1;
+            const unsigned with = __ballot_sync(0xffffffffu, set);
+            same &= set ? with : ~with;
+        }
+    return same;
 }
 
 // sets the table to zero, as block `block` of `blocks` of kSortThreads threads
@@ -129,8 +139,8 @@ sort_count_kernel(const __grid_constant__ SortPass a, const __grid_constant__ Ze
     const int end = min(first + a.tile, a.n);
     for (int i = first + (int)threadIdx.x; i - lane < end; i += kSortThreads) {
         const bool in = i < end;
-        const int d = sort_digit(a, in ? sort_key(a, i) : 0, in);
-        const unsigned same = __match_any_sync(0xffffffffu, d);
+        const int d = (in ? sort_key(a, i) : 0) >> a.shift & (digits - 1);
+        const unsigned same = same_digit(d, a.bits, in);
         if (in && (same & ((1u << lane) - 1)) == 0) atomicAdd(&count[d], __popc(same));
     }
     __syncthreads();
@@ -152,8 +162,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_c
     const int first = blockIdx.x * a.tile + w * per, end = min(first + per, tile_end);
     for (int i = first + lane; i - lane < end; i += 32) {
         const bool in = i < end;
-        const int d = sort_digit(a, in ? sort_key(a, i) : 0, in);
-        const unsigned same = __match_any_sync(0xffffffffu, d);
+        const int d = (in ? sort_key(a, i) : 0) >> a.shift & (digits - 1);
+        const unsigned same = same_digit(d, a.bits, in);
         if (in && (same & ((1u << lane) - 1)) == 0) mine[d] += __popc(same);
         __syncwarp();
     }
@@ -186,8 +196,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_c
     for (int i = first + lane; i - lane < end; i += 32) {
         const bool in = i < end;
         const int key = in ? sort_key(a, i) : 0;
-        const int d = sort_digit(a, key, in);
-        const unsigned same = __match_any_sync(0xffffffffu, d), below = same & ((1u << lane) - 1);
+        const int d = key >> a.shift & (digits - 1);
+        const unsigned same = same_digit(d, a.bits, in), below = same & ((1u << lane) - 1);
         if (in) {
             const int to = mine[d] + __popc(below);
             a.key_out[to] = key;
@@ -253,8 +263,8 @@ embed_sort_kernel(const __grid_constant__ ClusterSort a, const __grid_constant__
         for (int x = t; x < kSortWarps * digits / 4; x += kSortThreads) ((int4 *)count)[x] = make_int4(0, 0, 0, 0);
         __syncthreads();
         for (int i = from + lane; i - lane < to; i += 32) {
-            const int d = i < to ? in[i].x >> shift & (digits - 1) : digits;
-            const unsigned same = __match_any_sync(0xffffffffu, d);
+            const int d = (i < to ? in[i].x : 0) >> shift & (digits - 1);
+            const unsigned same = same_digit(d, a.bits, i < to);
             if (i < to && (same & ((1u << lane) - 1)) == 0) mine[d] += __popc(same);
             __syncwarp();
         }
@@ -301,8 +311,8 @@ embed_sort_kernel(const __grid_constant__ ClusterSort a, const __grid_constant__
         const uint32_t out = shared_address(list[(pass + 1) & 1]);
         for (int i = from + lane; i - lane < to; i += 32) {
             const int2 one = i < to ? in[i] : make_int2(0, 0);
-            const int d = i < to ? one.x >> shift & (digits - 1) : digits;
-            const unsigned same = __match_any_sync(0xffffffffu, d), below = same & ((1u << lane) - 1);
+            const int d = one.x >> shift & (digits - 1);
+            const unsigned same = same_digit(d, a.bits, i < to), below = same & ((1u << lane) - 1);
             if (i < to) {
                 const unsigned place = base[d] + mine[d] + __popc(below);
                 if (last) {
