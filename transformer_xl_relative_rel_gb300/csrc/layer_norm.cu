@@ -514,9 +514,14 @@ norm_columns_kernel(const float *part, int blocks, int d, int pitch, float *dgam
     chain_wait();
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5, strips = (d + 31) / 32;
     const int which = blockIdx.x / strips, c = (blockIdx.x % strips) * 32 + x;
-    float sum = 0.f;
-    if (c < d)
-        for (int b = y; b < blocks; b += 32) sum += part[((size_t)b * 2 + which) * pitch + c];
+    // (all asked for at once: one wait for memory, not ten)
+    constexpr int kEach = (kMostBlocks + 31) / 32;
+    float v[kEach], sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+        v[k] = c < d && y + 32 * k < blocks ? part[((size_t)(y + 32 * k) * 2 + which) * pitch + c] : 0.f;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) sum += v[k];
     __shared__ float sums[32][33];
     sums[y][x] = sum;
     __syncthreads();
