@@ -13,6 +13,7 @@ the timed region; the per-step working set is far larger than L2.
     python bench.py --impl reference ...     # the float64 CPU oracle
     python bench.py --recompute-vs-reuse     # eval cost per token, window recompute vs memory reuse
     python bench.py --output-loss            # the output layer's losses on the workload's hidden states
+    python bench.py --train-ops              # embedding, layer norm and optimiser step at the workload's sizes
 
 Prints one JSON line (rank 0).  Under torchrun each rank runs its own replica
 (weak scaling: independent sequences, no data-path collective); timing is the
@@ -1177,6 +1178,92 @@ def output_loss(args, local: int):
     return 0
 
 
+def train_ops(args, local: int):
+    """Time what a training step needs around the attention and the output
+    layer, at the workload's sizes (bf16, ``--vocab`` tokens): the embedding
+    forward and its gradient (added to the tied output layer's), one layer norm
+    of a residual sum forward and backward, and the optimiser step over all of
+    the model's tensors (five projections, the biases and two norms per layer,
+    the tied table, the output bias; bf16 with float32 masters) with the
+    gradients' clipping, moments in 32 and in 8 bits.  CUDA events over the
+    timed calls, buffers allocated once; bytes are what each has to move."""
+    import transformer_xl_relative_rel_gb300 as txl
+    w = WORKLOADS[args.workload]
+    s = w.shape
+    n, d, V = s.seg_len * s.batch, s.d_model, args.vocab
+    dev = torch.device("cuda", local)
+    gen = torch.Generator(device=dev).manual_seed(14)
+    randn = lambda *size: torch.randn(*size, generator=gen, device=dev)
+    bf16, f32 = torch.bfloat16, torch.float32
+    tokens = (V ** torch.rand(s.seg_len, s.batch, generator=gen, device=dev).double()).long().clamp(1, V) - 1
+    table, grad = randn(V, d).to(bf16), randn(V, d).to(bf16)
+    x, res, dy, out, dx = (randn(s.seg_len, s.batch, d).to(bf16) for _ in range(5))
+    gamma, beta = 1 + 0.1 * randn(d), 0.1 * randn(d)
+    mean, rstd = torch.empty(s.seg_len, s.batch, device=dev), torch.empty(s.seg_len, s.batch, device=dev)
+    grads = dict(dx=dx, dgamma=torch.empty(d, device=dev), dbeta=torch.empty(d, device=dev))
+    ws_e = torch.empty(txl.embed_bwd_workspace_bytes(n, d, V, txl.TXL_BF16), dtype=torch.uint8, device=dev)
+    ws_n = torch.empty(txl.layer_norm_bwd_workspace_bytes(n, d, txl.TXL_BF16), dtype=torch.uint8, device=dev)
+
+    def embed():
+        txl.embed_fwd(tokens, table, math.sqrt(d), out=out)
+        txl.embed_bwd(tokens, dy, grad, math.sqrt(d), accumulate=True, workspace=ws_e)
+
+    def norm():
+        txl.layer_norm_fwd(x, gamma, beta, residual=res, y=out, mean=mean, rstd=rstd)
+        txl.layer_norm_bwd(dy, x, mean, rstd, gamma=gamma, residual=res, grads=grads, workspace=ws_n)
+
+    shapes = [(d, d)] * 5 * w.layers + [(d,)] * 6 * w.layers + [(V, d), (V,)]
+
+    def optimiser(bits):
+        masters = [0.02 * randn(*k) for k in shapes]
+        gr = [1e-3 * randn(*k).to(bf16) for k in shapes]
+        dt = torch.float8_e4m3fn if bits == 8 else f32
+        m, v = ([torch.zeros(k, dtype=f32, device=dev).to(dt) for k in shapes] for _ in range(2))
+        sc = [[torch.zeros((math.prod(k) + 255) // 256, device=dev) for k in shapes] if bits == 8 else None
+              for _ in range(2)]
+        t = txl.AdamwTensors([k.to(bf16) for k in masters], gr, m, v, masters, *sc, weight_decay=0.01)
+        ws = torch.empty(txl.grad_norm_workspace_bytes(t), dtype=torch.uint8, device=dev)
+        norm_, clip = torch.empty(1, device=dev), torch.empty(1, device=dev)
+
+        def step():
+            txl.grad_norm(t, 0.25, norm=norm_, clip=clip, workspace=ws)
+            txl.adamw_step(t, 2.5e-4, 1, grad_scale=clip, seed=1)
+        return step
+
+    def timed(call):
+        for _ in range(args.warmup):
+            call()
+        torch.cuda.synchronize()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        for _ in range(args.steps):
+            call()
+        e1.record()
+        torch.cuda.synchronize()
+        return e0.elapsed_time(e1) / 1e3 / args.steps
+
+    clocks = ClockSampler(local)
+    clocks.start()
+    params = sum(math.prod(k) for k in shapes)
+    distinct = int(tokens.unique().numel())
+    peaks, src = load_peaks()
+    cases = {"embed": (embed, 2 * n * d * 2 + 3 * distinct * d * 2 + 16 * n), "norm": (norm, 7 * n * d * 2 + 16 * n),
+             "adamw": (optimiser(32), params * 30), "adamw_8bit": (optimiser(8), params * (18 + 16 / 256))}
+    res_ = {}
+    for name, (call, nbytes) in cases.items():
+        t = timed(call)
+        res_[name] = {"us_per_call": t * 1e6, "gbs": nbytes / t / 1e9, "frac_hbm_peak": nbytes / t / 1e9 / peaks["hbm_gbs"]}
+    clk = clocks.stop()
+    txl.check()
+    print(json.dumps({
+        "metric": "optimiser step weights/s (AdamW with clipping, 32-bit moments), 1 GB300",
+        "value": params / (res_["adamw"]["us_per_call"] * 1e-6), "unit": "weights/s", "n_gpus": 1, "steps": args.steps,
+        "warmup": args.warmup, "higher_is_better": True, "dtype": "bf16", "data": "synthetic",
+        "config": {"workload": w.name, "rows": n, "d_model": d, "vocab": V, "weights": params, "tensors": len(shapes)},
+        **res_, "peak_hbm_gbs": peaks["hbm_gbs"], "peak_source": src, "clocks": clk}), flush=True)
+    return 0
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -1200,7 +1287,9 @@ def main(argv=None):
     ap.add_argument("--output-loss", action="store_true",
                     help="time the output layer's losses (cross entropy, distillation) on the workload's hidden "
                          "states")
-    ap.add_argument("--vocab", type=int, default=131072, help="vocabulary of --output-loss")
+    ap.add_argument("--train-ops", action="store_true",
+                    help="time the embedding, layer norm and optimiser step at the workload's sizes")
+    ap.add_argument("--vocab", type=int, default=131072, help="vocabulary of --output-loss and --train-ops")
     ap.add_argument("--top-k", type=int, default=32, help="teacher logits per row of --output-loss")
     ap.add_argument("--fused-rollover", action="store_true",
                     help="--attn-only: attention and memory update of a layer in one call "
@@ -1245,6 +1334,8 @@ def main(argv=None):
         return backward(args, local)
     if args.output_loss:
         return output_loss(args, local)
+    if args.train_ops:
+        return train_ops(args, local)
 
     w = WORKLOADS[args.workload]
     if args.layers or args.segments:

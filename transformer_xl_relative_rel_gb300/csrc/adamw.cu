@@ -8,8 +8,14 @@
 //
 // HBM-bound: every value is read and written once, 8 neighbouring elements
 // per thread.  All tensors of a call share a launch: their descriptions are a
-// kernel argument (up to kMostTensors of them), work is cut into chunks, and
-// a block finds its chunk's tensor by bisection.
+// kernel argument (up to kMostTensors of them), work is cut into rounds of
+// 2048 elements, and a block finds its rounds' tensors by bisection.
+//
+// Measured: 229 M weights (bf16 with masters, 32-bit moments) 905 us for 6.4 GB
+// (7.1 TB/s, a little above the measured copy rate), the norm of their
+// gradients 84 us for 458 MB; 34 M weights with 8-bit moments 100 us for 547 MB
+// (5.4 TB/s), bound by the arithmetic of the codes next to the memory (75
+// instructions an element, issued in 0.7 of the cycles).
 //
 // 8-bit moments: e4m3 codes of m and of sqrt(v) (half the exponent range of
 // v), times a scale per 256 elements that maps the largest to 448.  Rounding

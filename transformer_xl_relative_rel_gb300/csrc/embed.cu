@@ -11,8 +11,16 @@
 // each, which a last launch adds.
 //
 // Up to kClusterRows rows are sorted by one cluster in its blocks' shared
-// memory, where other clusters of the launch set the table to zero meanwhile;
-// more by a counting and a placing launch per digit.
+// memory, while other clusters of the launch set the table to zero; more by a
+// counting and a placing launch per digit.  (Counting and placing launches for
+// all took 14 us per digit for 16896 rows, the cluster 10 for the first and 5
+// for another; of 4, 8 and 16 blocks 16 are fastest: 15, 12 and 10 us.)
+//
+// What bounds it, forward and gradient of one call, under a profiler one by
+// one: 16896 x 512 rows of 256 tokens, added to the table: gather 7, sort 10,
+// sums 7, join 7 us, latencies of launches and of a handful of dependent loads
+// in each (the bytes are worth 5 us); 6144 x 1024 rows, table of 131072 set
+// to zero: 45 us for 268 MB (5.9 TB/s, the sort hidden in it), sums 8, join 4.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -345,30 +353,17 @@ struct SumArgs {
     long pitch;
 };
 
-template <typename T, int V>
-__device__ __forceinline__ void write_sum(const SumArgs &a, int token, int c, const float (&acc)[V])
-{
-    T *to = (T *)a.dtable + (size_t)token * a.d + c;
-    float x[V];
-    if (a.accumulate) {
-        unpack<T, V>(load_raw<T, V>(to), x);
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = fmaf(a.scale, acc[i], x[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = a.scale * acc[i];
-    }
-    store_vec<T, V>(to, x);
-}
-
 constexpr int kStrip = 256;      // columns of a warp: 32 K V
 
 // A warp adds kStrip columns of a chunk's rows, of which U are asked for at
-// once, as many as 64 registers hold.
-template <typename T, int V>
+// once, as many as 64 registers hold.  ACC: with each token's last row the
+// table's is asked for too (one after another they made forward and gradient
+// of 6144 x 1024 rows of 3000 tokens take 64 us where it is 26).
+template <typename T, int V, bool ACC>
 __global__ void __launch_bounds__(NT) embed_sum_kernel(const __grid_constant__ SumArgs a)
 {
-    constexpr int K = kStrip / (32 * V), U = 64 / (K * (sizeof(raw_t<T, V>) >= 4 ? (int)sizeof(raw_t<T, V>) / 4 : 1));
+    constexpr int K = kStrip / (32 * V), kRegs = K * (sizeof(raw_t<T, V>) >= 4 ? (int)sizeof(raw_t<T, V>) / 4 : 1);
+    constexpr int U = (ACC ? 32 : 64) / kRegs;
     static_assert(kChunk % U == 0, "a chunk is so many whole batches");
     chain_begin();
     chain_wait();
@@ -381,25 +376,34 @@ __global__ void __launch_bounds__(NT) embed_sum_kernel(const __grid_constant__ S
     const int row = lane < n ? a.row[first + lane] : 0;
     const int before = first > 0 ? a.key[first - 1] : -1, after = first + n < a.n ? a.key[first + n] : a.vocab;
     const int live = __popc(__ballot_sync(0xffffffffu, key < a.vocab)), head = __shfl_sync(0xffffffffu, key, 0);
+    // a token's last row here (behind the chunk: no token), and whether others of it lie before or behind
+    const int next = __shfl_down_sync(0xffffffffu, key, 1);
+    const unsigned last = __ballot_sync(0xffffffffu, lane < live && next != key);
+    const bool from_before = before == key, goes_on = lane + 1 == n && after == key;
+    const unsigned whole = __ballot_sync(0xffffffffu, lane < live && !((key == head && from_before) || goes_on));
     float acc[K][V];
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[k][i] = 0.f;
     for (int j = 0; j < live; j += U) {
-        raw_t<T, V> raw[U][K];
+        raw_t<T, V> raw[U][K], old[ACC ? U : 1][K];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const T *from = (const T *)a.dout + (size_t)__shfl_sync(0xffffffffu, row, (j + u) & 31) * a.d;
+            const T *to = (const T *)a.dtable + (size_t)__shfl_sync(0xffffffffu, key, (j + u) & 31) * a.d;
+            const bool in = j + u < live, ends = ACC && (last & whole) >> ((j + u) & 31) & 1;
 #pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (j + u < live && c + 32 * k * V < a.d) raw[u][k] = load_raw<T, V>(from + c + 32 * k * V);
+            for (int k = 0; k < K; ++k) {
+                const int at = c + 32 * k * V;
+                if (in && at < a.d) raw[u][k] = load_raw<T, V>(from + at);
+                if (ends && at < a.d) old[ACC ? u : 0][k] = load_raw<T, V>(to + at);
+            }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (j + u >= live) break;
             const int token = __shfl_sync(0xffffffffu, key, j + u);
-            const int next = __shfl_sync(0xffffffffu, key, (j + u + 1) & 31);     // (behind the chunk: no token)
 #pragma unroll
             for (int k = 0; k < K; ++k)
                 if (c + 32 * k * V < a.d) {
@@ -408,17 +412,22 @@ __global__ void __launch_bounds__(NT) embed_sum_kernel(const __grid_constant__ S
 #pragma unroll
                     for (int i = 0; i < V; ++i) acc[k][i] += v[i];
                 }
-            if (next == token) continue;
-            // the token's last row in this chunk
-            const bool from_before = token == head && before == token, goes_on = j + u + 1 == n && after == token;
+            if (!(last >> (j + u) & 1)) continue;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 const int at = c + 32 * k * V;
                 if (at < a.d) {
-                    if (from_before || goes_on)
-                        store_floats<V>(a.part + (2 * (size_t)chunk + !from_before) * a.pitch + at, acc[k]);
-                    else
-                        write_sum<T, V>(a, token, at, acc[k]);
+                    if (!(whole >> (j + u) & 1)) {
+                        // to the first place where rows of it lie in chunks before
+                        const bool begins = !(token == head && before == token);
+                        store_floats<V>(a.part + (2 * (size_t)chunk + begins) * a.pitch + at, acc[k]);
+                    } else {
+                        float x[V];
+                        if (ACC) unpack<T, V>(old[ACC ? u : 0][k], x);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) x[i] = ACC ? fmaf(a.scale, acc[k][i], x[i]) : a.scale * acc[k][i];
+                        store_vec<T, V>((T *)a.dtable + (size_t)token * a.d + at, x);
+                    }
                 }
 #pragma unroll
                 for (int i = 0; i < V; ++i) acc[k][i] = 0.f;
@@ -440,6 +449,16 @@ __device__ __forceinline__ void add_float4(float4 &acc, const float4 &v)
     acc.y += v.y;
     acc.z += v.z;
     acc.w += v.w;
+}
+
+template <typename T>
+__device__ __forceinline__ void write_sum(const SumArgs &a, int token, int c, float sum)
+{
+    T *to = (T *)a.dtable + (size_t)token * a.d + c;
+    float x[1] = {0.f};
+    if (a.accumulate) unpack<T, 1>(load_raw<T, 1>(to), x);
+    x[0] = a.accumulate ? fmaf(a.scale, sum, x[0]) : a.scale * sum;
+    store_vec<T, 1>(to, x);
 }
 
 template <typename T>
@@ -486,10 +505,7 @@ __global__ void __launch_bounds__(NT) embed_join_kernel(const __grid_constant__ 
                 const float one[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (c + i < a.d) {
-                        const float x[1] = {one[i]};
-                        write_sum<T, 1>(a, key, c + i, x);
-                    }
+                    if (c + i < a.d) write_sum<T>(a, key, c + i, one[i]);
             }
             key = -1;
         }
@@ -517,10 +533,10 @@ __global__ void __launch_bounds__(NT) embed_join_kernel(const __grid_constant__ 
         __syncthreads();
         if (threadIdx.x < kJoinColumns) {
             const int column = (int)(blockIdx.x % strips) * kJoinColumns + threadIdx.x;
-            float all[1] = {0.f};
+            float all = 0.f;
 #pragma unroll
-            for (int k = 0; k < kJoinWarps; ++k) all[0] += ((const float *)sums[k])[threadIdx.x];
-            if (column < a.d) write_sum<T, 1>(a, key, column, all);
+            for (int k = 0; k < kJoinWarps; ++k) all += ((const float *)sums[k])[threadIdx.x];
+            if (column < a.d) write_sum<T>(a, key, column, all);
         }
         __syncthreads();
     }
@@ -603,7 +619,8 @@ cudaError_t run_sums(SumArgs a, cudaStream_t s)
 {
     a.strips = (a.d + kStrip - 1) / kStrip;
     const long tasks = (long)a.chunks * a.strips;
-    cudaError_t e = chain_launch(embed_sum_kernel<T, V>, (unsigned)((tasks + NT / 32 - 1) / (NT / 32)), NT, 0, 1, s, a);
+    cudaError_t e = chain_launch(a.accumulate ? embed_sum_kernel<T, V, true> : embed_sum_kernel<T, V, false>,
+                                 (unsigned)((tasks + NT / 32 - 1) / (NT / 32)), NT, 0, 1, s, a);
     if (e != cudaSuccess || a.chunks == 1) return e;
     const long strips = (a.d + kJoinColumns - 1) / kJoinColumns, groups = (a.chunks + kJoinWarps - 2) / kJoinWarps;
     return chain_launch(embed_join_kernel<T>, (unsigned)(groups * strips), NT, 0, 1, s, a);

@@ -14,7 +14,13 @@
 // leave room for few warps, so up to 1024 columns a warp of the backward asks
 // for its next rows (asynchronous copies into shared memory, each lane its own
 // columns; not bf16 rows that are only 2-byte aligned, which such copies do
-// not serve) before it computes one.
+// not serve) before it computes one: 6144 x 1024 pre-norm rows 27.7 -> 15.0 us
+// (the forward gained nothing by it, 12 -> 14 us, and keeps a row per warp).
+//
+// Measured one by one under a profiler (about 2.5 us of each a launch): 16896 x
+// 512 bf16 with residual forward 11.8 us (52 MB), backward 15.1 us (70 MB),
+// column sums 3.6 us; 6144 x 1024 with the sum kept 11.4 us (50 MB), 15.0 us
+// (50 MB, bound by its instructions: a row's xh is computed twice) and 3.7 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
