@@ -149,6 +149,38 @@ def test_hyperparameters(kind):
         _check(before, model, hyper)
 
 
+@pytest.mark.parametrize("size", [1e-15, 1e-18, 1e-19, 1e-20, 3e-22])
+@pytest.mark.parametrize("kind", ["f32", "8 bits"])
+def test_second_moments_near_the_smallest_numbers(kind, size):
+    """From v of 2^-100 down to the denormals (whose few bits bound what a
+    root's square can be told from): the root is still the root."""
+    model = _model([3000], 33, KINDS[kind])
+    for name in ("exp_avgs", "exp_avg_sqs"):
+        model[name][0].zero_()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    model["grads"][0].copy_(size * 30 * torch.randn(3000, device="cuda", generator=g))
+    before = _copy(model)
+    hyper = dict(HYPER, step=1, eps=2.0 ** -120, lr=1e-3)
+    _step(model, hyper, decay=0.0)
+    torch.cuda.synchronize()
+    grad = before["grads"][0].double()
+    v = (1 - 0.98) * grad ** 2
+    # an update of m / sqrt(v) at the first step is the gradient's sign; v is off by half a denormal's step
+    kept = v > 2.0 ** -149 * 64
+    p = before["masters"][0] if before["masters"][0] is not None else before["params"][0]
+    got = model["masters"][0] if before["masters"][0] is not None else model["params"][0]
+    want = p.double() - 1e-3 * torch.sign(grad)
+    assert int(kept.sum()) > (100 if size > 1e-21 else 10)
+    # half of 1/64, one denormal's step in v, of an update of 1e-3, and p's own rounding
+    assert float(((got.double() - want).abs() - 2.0 ** -22 * p.abs().double())[kept].max()) <= 1e-3 * (1 / 64 + 1e-4)
+    if kind == "f32":
+        return
+    root = _dense(model["exp_avg_sqs"][0], model["exp_avg_sq_scales"][0])
+    # a code is within a step (1/8, or 2^-9 of 448 for the smallest) of what it stands for
+    off = (root - v.sqrt()).abs() - v.sqrt() / 7 - model["exp_avg_sq_scales"][0].double().repeat_interleave(256)[:3000] / 512
+    assert float(off[kept].max()) <= float(v.sqrt().max()) / 60
+
+
 @pytest.mark.parametrize("kind", ["f32", "8 bits"])
 def test_from_zero_moments(kind):
     """The first step: moments and scales are zero; elements without a gradient do not move."""
@@ -374,6 +406,53 @@ def test_captured_steps():
     for name in a:
         for x, y in zip(a[name], b[name]):
             assert x is None or torch.equal(x.view(torch.uint8), y.view(torch.uint8)), name
+
+
+def test_first_calls_of_a_process_captured():
+    """No call has to come before a capture, nor for a list of many tensors."""
+    code = """
+import torch
+import transformer_xl_relative_rel_gb300 as txl
+from tests.test_gpu_adamw import KINDS, _copy, _model
+tok = torch.randint(-1, 90, (700,), device="cuda")
+table, dout = torch.randn(90, 64, device="cuda").bfloat16(), torch.randn(700, 64, device="cuda").bfloat16()
+gamma = torch.randn(64, device="cuda")
+models = [_model([70 * k + 5 for k in range(n)], 3, KINDS[kind]) for n, kind in ((100, "mixed"), (3, "f32"))]
+twins = [_copy(m) for m in models]
+
+def calls(models):
+    x = txl.embed_fwd(tok, table, 3.0)
+    y, mean, rstd = txl.layer_norm_fwd(x, gamma, residual=dout)
+    g = txl.layer_norm_bwd(dout, x, mean, rstd, gamma=gamma, residual=dout)
+    out = [x, y, mean, rstd, g["dx"], g["dgamma"], g["dbeta"], txl.embed_bwd(tok, g["dx"], vocab=90)]
+    for m in models:
+        t = txl.AdamwTensors(**m)
+        norm, clip = txl.grad_norm(t, 0.1)
+        txl.adamw_step(t, 1e-2, 3, grad_scale=clip, seed=4)
+        out += [norm, clip]
+    return out
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = calls(models)
+graph.replay()
+torch.cuda.synchronize()
+for a, b in zip(got, calls(twins)):
+    assert torch.equal(a, b)
+for a, b in zip(models, twins):
+    for n in a:
+        for x, y in zip(a[n], b[n]):
+            assert x is None or torch.equal(x.view(torch.uint8), y.view(torch.uint8)), n
+txl.check()
+print("FINE")
+"""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=root)
+    assert r.returncode == 0 and "FINE" in r.stdout, r.stdout + r.stderr
 
 
 def test_streams_and_host_threads_at_once():

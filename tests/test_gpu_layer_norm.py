@@ -69,6 +69,15 @@ def test_every_form(dtype, d, flags):
     _check(p, *(bool(flags >> k & 1) for k in range(4)))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,d", [(3000, 1024), (77, 1022), (500, 768), (40, 1000), (30, 700), (900, 4096)])
+def test_every_tensor_of_wide_rows(dtype, rows, d):
+    """dy, x, the residual and dsum together take the most shared memory."""
+    p = _inputs(rows, d, dtype, 30)
+    _check(p, residual=True, dsum=True)
+    _check(p, residual=True, keep=True, dsum=True)
+
+
 @pytest.mark.parametrize("shift", [1, 2, 4])
 @pytest.mark.parametrize("dtype,d", [(BF, 512), (F32, 256), (BF, 3000), (BF, 8192), (F32, 8192), (BF, 410)])
 def test_unaligned(dtype, d, shift):

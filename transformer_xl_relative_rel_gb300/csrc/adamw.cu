@@ -281,14 +281,17 @@ __device__ __forceinline__ float reciprocal(float x)
     return r;
 }
 
-// The square roots of two numbers, 0 or at least 2^-100, to nearest: a root of
+// The square roots of two numbers that are not negative, to nearest: a root of
 // about 22 bits and one Newton step with its exact residual (Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000", 1990).
-// 0 or NaN for what is not finite; smaller numbers may be an ulp off.
+// "Computation of elementary functions on the IBM RISC System/6000", 1990);
+// by the function where a number is so small (below 2^-100, but not 0) that
+// the residual has no room.  NaN for infinity.
 __device__ __forceinline__ uint64_t pair_sqrt(uint64_t v)
 {
     float a, b, ra, rb;
     unpair(v, a, b);
+    // (the bits of 0, less one, are the largest)
+    if (min(__float_as_uint(a) - 1u, __float_as_uint(b) - 1u) < (27u << 23) - 1u) return pair(__fsqrt_rn(a), __fsqrt_rn(b));
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(ra) : "f"(fmaxf(a, 0x1p-126f)));
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(rb) : "f"(fmaxf(b, 0x1p-126f)));
     const uint64_t r = pair(ra, rb), s = pair_mul(v, r), half = pair_mul(r, pair(0.5f, 0.5f));
