@@ -49,8 +49,7 @@ struct EmbedArgs {
     const void *table;
     void *out;
     float scale;
-    long rows, vectors;      // vectors of V elements per row
-    int d, vocab;
+    int rows, d, vocab, shift;      // 1 << shift threads take a row
 };
 
 template <typename T, int V>
@@ -58,21 +57,29 @@ __global__ void __launch_bounds__(NT) embed_fwd_kernel(const __grid_constant__ E
 {
     chain_begin();
     chain_wait();
-    const long total = a.rows * a.vectors, stride = (long)gridDim.x * NT;
-    for (long x = (long)blockIdx.x * NT + threadIdx.x; x < total; x += stride) {
-        const long row = x / a.vectors;
-        const int c = (int)(x - row * a.vectors) * V;
-        const int64_t t = a.tokens[row];
-        float v[V];
-        if (t >= 0 && t < a.vocab) {
-            unpack<T, V>(load_raw<T, V>((const T *)a.table + t * a.d + c), v);
+    const long row = ((long)blockIdx.x * NT + threadIdx.x) >> a.shift;
+    if (row >= a.rows) return;
+    const int threads = 1 << a.shift, first = (threadIdx.x & (threads - 1)) * V, step = threads * V;
+    const int64_t t = a.tokens[row];
+    const bool in = t >= 0 && t < a.vocab;
+    const T *from = (const T *)a.table + (in ? t : 0) * a.d;
+    T *to = (T *)a.out + row * a.d;
+    constexpr int U = 4;      // vectors asked for at once
+    for (int c = first; c < a.d; c += U * step) {
+        raw_t<T, V> raw[U];
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[i] *= a.scale;
-        } else {
+        for (int u = 0; u < U; ++u)
+            if (in && c + u * step < a.d) raw[u] = load_raw<T, V>(from + c + u * step);
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = 0.f;
+        for (int u = 0; u < U; ++u) {
+            float v[V] = {};
+            if (in && c + u * step < a.d) {
+                unpack<T, V>(raw[u], v);
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[i] *= a.scale;
+            }
+            if (c + u * step < a.d) store_vec<T, V>(to + c + u * step, v);
         }
-        store_vec<T, V>((T *)a.out + row * a.d + c, v);
     }
 }
 
@@ -609,9 +616,9 @@ int load_bytes(int d, size_t esz, const void *p, const void *q)
 template <typename T, int V>
 cudaError_t run_fwd(EmbedArgs a, cudaStream_t s)
 {
-    a.vectors = a.d / V;
-    const long want = (a.rows * a.vectors + NT - 1) / NT, most = 16L * device_sm_count();
-    return chain_launch(embed_fwd_kernel<T, V>, (unsigned)(want < most ? want : most), NT, 0, 1, s, a);
+    for (a.shift = 0; a.shift < 5 && (V << a.shift) < a.d;) ++a.shift;      // a warp at most
+    const long threads = (long)a.rows << a.shift;
+    return chain_launch(embed_fwd_kernel<T, V>, (unsigned)((threads + NT - 1) / NT), NT, 0, 1, s, a);
 }
 
 template <typename T, int V>
@@ -724,7 +731,7 @@ txl_status txl_embed_fwd(const int64_t *tokens, const void *table, float scale, 
     st = check_buffers({{tokens, n * 8, 8, true}, {table, rows ? (size_t)vocab * d_model * esz : 0, esz, true}},
                        {{out, n * d_model * esz, esz, true}});
     if (st != TXL_OK || rows == 0) return st;
-    const EmbedArgs a = {tokens, table, out, scale, rows, 0, d_model, vocab};
+    const EmbedArgs a = {tokens, table, out, scale, rows, d_model, vocab, 0};
     cudaStream_t s = (cudaStream_t)stream;
     const int wide = load_bytes(d_model, esz, table, out);
     if (dtype == TXL_F32) return finish(wide == 16 ? run_fwd<float, 4>(a, s) : run_fwd<float, 1>(a, s));
