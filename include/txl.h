@@ -686,7 +686,8 @@ txl_status txl_grad_norm(int tensors, const txl_adamw_tensor *t, float max_norm,
  * x ^ x >> 16.  m, v, sqrt(v) and y are computed operation by operation as
  * written, each rounded to fp32, so that plain fp32 arithmetic gives the same
  * codes.  The update uses m and v before they become codes.  A block with a
- * moment that is not finite is lost: its scale becomes NaN; use grad_scale.
+ * moment that is not finite, or whose m or sqrt(v) is 2^126 or more, is lost:
+ * its scale becomes NaN; use grad_scale.
  *
  * t : host array of `tensors` descriptions.  param, master, the moments and
  * their scales must overlap neither each other, in any tensor, nor a gradient

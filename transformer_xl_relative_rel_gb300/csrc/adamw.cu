@@ -14,7 +14,7 @@
 // Measured: 229 M weights (bf16 with masters, 32-bit moments) 905 us for 6.4 GB
 // (7.1 TB/s, a little above the measured copy rate), the norm of their
 // gradients 84 us for 458 MB; 34 M weights with 8-bit moments 100 us for 547 MB
-// (5.4 TB/s), bound by the arithmetic of the codes next to the memory (75
+// (5.5 TB/s), bound by the arithmetic of the codes next to the memory (some 70
 // instructions an element, issued in 0.7 of the cycles).
 //
 // 8-bit moments: e4m3 codes of m and of sqrt(v) (half the exponent range of
@@ -29,6 +29,7 @@
 #include <cuda_fp8.h>
 #include <math.h>
 #include <stdint.h>
+#include <string.h>
 
 #include <algorithm>
 #include <iterator>
@@ -87,16 +88,16 @@ template <int N>
 struct GradTensors {
     int first[N];
     int count, chunks;
-    float one;                   // as StepScalars'
+    uint64_t one;                // as StepScalars'
     GradTensor t[N];
 };
 
 struct StepScalars {
     const float *lr_at, *grad_scale;
     const int64_t *step_at;
-    float lr, b1, b2, c1, c2;        // c1 = 1 - b1, c2 = 1 - b2
-    float log_b1, log_b2, eps;
-    float one;                       // 1, unknown to the compiler (pair_sum)
+    uint64_t b1, b2, c1, c2, eps;    // twice each, as pairs; c1 = 1 - b1, c2 = 1 - b2
+    uint64_t one;                    // of 1, unknown to the compiler (pair_sum)
+    float lr, log_b1, log_b2;
     int64_t step;
 };
 
@@ -194,6 +195,22 @@ __device__ __forceinline__ uint64_t decode(const uint32_t (&raw)[2], int k, uint
     return pair_mul(pair(f.x, f.y), scale);
 }
 
+// 1 / x to an ulp, for normal x; 0 above 2^126
+__device__ __forceinline__ float reciprocal(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// 1 / x to nearest, for a normal x of a normal reciprocal, by a Newton step
+// (as pair_sqrt's)
+__device__ __forceinline__ float exact_reciprocal(float x)
+{
+    const float r = reciprocal(x);
+    return fmaf(r, fmaf(-x, r, 1.f), r);
+}
+
 // The warp's 256 values x (8 per lane) as codes of x times one scale, which is
 // returned.  h: random bits, of which the low halves are used, for roots
 // (which are not negative, and keep at least one step) the high ones.
@@ -223,8 +240,9 @@ __device__ __forceinline__ float encode(const uint64_t (&x)[4], const uint32_t (
     const float most = __uint_as_float(top);
     raw[0] = raw[1] = 0;
     if (most < 0x1p-100f) return 0.f;
-    if (top >= 0x7f800000u) return __uint_as_float(0x7fffffffu);     // a block that is not finite is lost
-    const float inverse = __fmul_rn(__frcp_rn(most), kTop);
+    // a block with a value that is not finite (or of 2^126, whose reciprocal is no normal number) is lost
+    if (top >= 0x7e800000u) return __uint_as_float(0x7fffffffu);
+    const float inverse = __fmul_rn(exact_reciprocal(most), kTop);
     uint32_t code[8];     // in the low bytes
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -265,7 +283,7 @@ __device__ __forceinline__ float encode(const uint64_t (&x)[4], const uint32_t (
 // a + b of products, each rounded by itself: the assembler fuses a packed
 // product and a packed addition (not scalar ones), but not a product and a
 // fused multiply-add by a 1 that it does not know
-__device__ __forceinline__ uint64_t pair_sum(float one, uint64_t a, uint64_t b) { return pair_fma(pair(one, one), a, b); }
+__device__ __forceinline__ uint64_t pair_sum(uint64_t one, uint64_t a, uint64_t b) { return pair_fma(one, a, b); }
 
 // ---------------------------------------------------------------- the step
 struct Rates {
@@ -273,30 +291,40 @@ struct Rates {
     int go;
 };
 
-// 1 / x to an ulp, for normal x; 0 above 2^126
-__device__ __forceinline__ float reciprocal(float x)
-{
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-// The square roots of two numbers that are not negative, to nearest: a root of
+// The square roots of two numbers, 0 or at least 2^-100, to nearest: a root of
 // about 22 bits and one Newton step with its exact residual (Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000", 1990);
-// by the function where a number is so small (below 2^-100, but not 0) that
-// the residual has no room.  NaN for infinity.
+// "Computation of elementary functions on the IBM RISC System/6000", 1990).
+// NaN for infinity.  (Compared with __fsqrt_rn, and the reciprocal below with
+// __frcp_rn, at every mantissa of 14 exponents: no difference.)
 __device__ __forceinline__ uint64_t pair_sqrt(uint64_t v)
 {
     float a, b, ra, rb;
-    unpair(v, a, b);
-    // (the bits of 0, less one, are the largest)
-    if (min(__float_as_uint(a) - 1u, __float_as_uint(b) - 1u) < (27u << 23) - 1u) return pair(__fsqrt_rn(a), __fsqrt_rn(b));
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(ra) : "f"(fmaxf(a, 0x1p-126f)));
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(rb) : "f"(fmaxf(b, 0x1p-126f)));
+    unpair(pair_add(v, pair(0x1p-126f, 0x1p-126f)), a, b);      // (only 0 is changed: it has no reciprocal root)
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(ra) : "f"(a));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(rb) : "f"(b));
     const uint64_t r = pair(ra, rb), s = pair_mul(v, r), half = pair_mul(r, pair(0.5f, 0.5f));
     const uint64_t residual = pair_fma(pair_sub(0, s), s, v);
     return pair_fma(residual, half, s);
+}
+
+// eight numbers' roots; by the function where one is so small (below 2^-100,
+// but not 0) that the Newton step's residual has no room
+__device__ __forceinline__ void eight_sqrt(const uint64_t (&v)[4], uint64_t (&root)[4])
+{
+    uint32_t least = 0xffffffffu;      // (the bits of 0, less one, are the largest)
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        unpair(v[k], x[2 * k], x[2 * k + 1]);
+        least = min(min(least, __float_as_uint(x[2 * k]) - 1u), __float_as_uint(x[2 * k + 1]) - 1u);
+    }
+    if (least < (27u << 23) - 1u) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) root[k] = pair(__fsqrt_rn(x[2 * k]), __fsqrt_rn(x[2 * k + 1]));
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) root[k] = pair_sqrt(v[k]);
 }
 
 // eight elements of a thread
@@ -338,29 +366,31 @@ __device__ __forceinline__ void step_eight(const Tensor &t, const StepScalars &s
 {
     const bool wide = WHOLE || (t.wide && n == kPer);
     const auto both = [](float y) { return pair(y, y); };
-    uint64_t m2[4], root2[4];
+    uint64_t m2[4], v2[4], root2[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const uint64_t g2 = pair_mul(pair(x.g[2 * k], x.g[2 * k + 1]), both(r.factor));
-        uint64_t p2 = pair(x.p[2 * k], x.p[2 * k + 1]), v2;
         if (CODES) {
             m2[k] = decode(x.cm, k, both(x.ms));
-            v2 = decode(x.cv, k, both(x.vs));
-            v2 = pair_mul(v2, v2);
+            v2[k] = decode(x.cv, k, both(x.vs));
+            v2[k] = pair_mul(v2[k], v2[k]);
         } else {
             m2[k] = pair(x.m[2 * k], x.m[2 * k + 1]);
-            v2 = pair(x.v[2 * k], x.v[2 * k + 1]);
+            v2[k] = pair(x.v[2 * k], x.v[2 * k + 1]);
         }
-        m2[k] = pair_sum(s.one, pair_mul(both(s.b1), m2[k]), pair_mul(both(s.c1), g2));
-        v2 = pair_sum(s.one, pair_mul(both(s.b2), v2), pair_mul(pair_mul(both(s.c2), g2), g2));
-        float a, b;
-        if (CODES) {
-            root2[k] = pair_sqrt(v2);
-        } else {
-            unpair(v2, x.v[2 * k], x.v[2 * k + 1]);
+        m2[k] = pair_sum(s.one, pair_mul(s.b1, m2[k]), pair_mul(s.c1, g2));
+        v2[k] = pair_sum(s.one, pair_mul(s.b2, v2[k]), pair_mul(pair_mul(s.c2, g2), g2));
+        if (!CODES) {
+            unpair(v2[k], x.v[2 * k], x.v[2 * k + 1]);
             root2[k] = pair(__fsqrt_rn(x.v[2 * k]), __fsqrt_rn(x.v[2 * k + 1]));
         }
-        unpair(pair_fma(root2[k], both(r.r2), both(s.eps)), a, b);
+    }
+    if (CODES) eight_sqrt(v2, root2);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        uint64_t p2 = pair(x.p[2 * k], x.p[2 * k + 1]);
+        float a, b;
+        unpair(pair_fma(root2[k], both(r.r2), s.eps), a, b);
         const uint64_t update = pair_mul(pair_mul(m2[k], both(r.r1)), pair(reciprocal(a), reciprocal(b)));
         // (1 - lr wd as a factor would lose the small lr wd: it is added to the update)
         p2 = pair_fma(both(-r.lr), pair_fma(both(t.decay), p2, update), p2);
@@ -453,7 +483,7 @@ adamw_kernel(const __grid_constant__ Tensors<N> list, const __grid_constant__ St
 // sum + low += x (in pairs), the rounding of the addition kept in low (Knuth's
 // exact difference of a sum): a thread's fp32 sums are as exact as one in
 // double, which the chip has few units for
-__device__ __forceinline__ void add_exactly(uint64_t x, float one, uint64_t &sum, uint64_t &low)
+__device__ __forceinline__ void add_exactly(uint64_t x, uint64_t one, uint64_t &sum, uint64_t &low)
 {
     const uint64_t s = pair_sum(one, x, sum), back = pair_sub(s, sum);
     low = pair_add(low, pair_add(pair_sub(sum, pair_sub(s, back)), pair_sum(one, x, pair_sub(0, back))));
@@ -467,7 +497,7 @@ __device__ __forceinline__ void add_exactly(float x, float &sum, float &low)
     sum = s;
 }
 
-__device__ __forceinline__ void add_squares(const float (&g)[8], float one, uint64_t &sum, uint64_t &low)
+__device__ __forceinline__ void add_squares(const float (&g)[8], uint64_t one, uint64_t &sum, uint64_t &low)
 {
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
@@ -562,6 +592,14 @@ __global__ void __launch_bounds__(NT) norm_kernel(const double *part, int count,
 
 // ---------------------------------------------------------------- host side
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
+
+// a pair of the same number, as the kernels hold it
+uint64_t twice(float x)
+{
+    uint32_t b;
+    memcpy(&b, &x, 4);
+    return (uint64_t)b << 32 | b;
+}
 
 txl_status finish(cudaError_t e)
 {
@@ -722,7 +760,7 @@ cudaError_t launch_squares(const txl_adamw_tensor *t, const int *order, int coun
     }
     list.count = count;
     list.chunks = chunks;
-    list.one = 1.f;
+    list.one = twice(1.f);
     return chain_launch(square_kernel<N>, blocks, NT, 0, 1, s, list, part);
 }
 
@@ -831,14 +869,14 @@ txl_status adamw_step(int tensors, const txl_adamw_tensor *t, const txl_adamw_op
     sc.grad_scale = o->grad_scale;
     sc.step_at = o->step_device;
     sc.lr = o->lr;
-    sc.b1 = (float)o->beta1;
-    sc.b2 = (float)o->beta2;
-    sc.c1 = (float)(1.0 - o->beta1);
-    sc.c2 = (float)(1.0 - o->beta2);
+    sc.b1 = twice((float)o->beta1);
+    sc.b2 = twice((float)o->beta2);
+    sc.c1 = twice((float)(1.0 - o->beta1));
+    sc.c2 = twice((float)(1.0 - o->beta2));
     sc.log_b1 = (float)log(o->beta1);
     sc.log_b2 = (float)log(o->beta2);
-    sc.eps = o->eps;
-    sc.one = 1.f;
+    sc.eps = twice(o->eps);
+    sc.one = twice(1.f);
     sc.step = o->step;
     const uint32_t seed = mix(mix((uint32_t)o->seed) + (uint32_t)(o->seed >> 32));
     for (const Launch &x : l.each) {
