@@ -177,6 +177,30 @@ def test_shapes_of_more_dimensions():
     assert torch.equal(one, out[0, 0, 1])
 
 
+@pytest.mark.parametrize("rows", [5000, 131072, 131073, 300000])
+@pytest.mark.parametrize("vocab", [1 << 27, (1 << 28) + 1])
+def test_tokens_of_many_digits(rows, vocab):
+    """Vocabularies whose tokens are sorted by four digits, in one cluster and
+    by launches: tokens that differ in one digit only, each once and twice."""
+    import transformer_xl_relative_rel_gb300 as txl
+    g = _gen(12)
+    tok = torch.randint(0, vocab, (rows,), device="cuda", generator=g)
+    tok[:256] = torch.arange(256, device="cuda")
+    tok[256:512] = torch.arange(256, device="cuda") << 8
+    tok[512:768] = torch.arange(256, device="cuda") << 16
+    tok[768:776] = torch.arange(8, device="cuda") << 24
+    tok[776], tok[777], tok[778] = vocab - 1, vocab, vocab - 2
+    dout = torch.randint(-8, 9, (rows, 2), device="cuda", generator=g).to(BF)
+    grad = txl.embed_bwd(tok, dout, torch.full((vocab, 2), 3.0, dtype=BF, device="cuda"))
+    good = tok < vocab
+    names, at = torch.unique(tok[good], return_inverse=True)
+    want = torch.zeros(len(names), 2, dtype=torch.float64, device="cuda").index_add_(0, at, dout[good].double())
+    assert torch.equal(grad[names].double(), want)
+    grad[names] = 0
+    assert not grad.any()
+    txl.check()
+
+
 @pytest.mark.parametrize("rows,d,vocab", [(40, 2100, 1 << 20), (2200000, 1000, 3)])
 def test_offsets_past_32_bits(rows, d, vocab):
     """A table, and rows, of more than 2^31 elements."""

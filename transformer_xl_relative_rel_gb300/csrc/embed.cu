@@ -383,9 +383,9 @@ __global__ void __launch_bounds__(NT) embed_sum_kernel(const __grid_constant__ S
     const int row = lane < n ? a.row[first + lane] : 0;
     const int before = first > 0 ? a.key[first - 1] : -1, after = first + n < a.n ? a.key[first + n] : a.vocab;
     const int live = __popc(__ballot_sync(0xffffffffu, key < a.vocab)), head = __shfl_sync(0xffffffffu, key, 0);
-    // a token's last row here (behind the chunk: no token), and whether others of it lie before or behind
+    // a token's last row here, and whether others of it lie before or behind
     const int next = __shfl_down_sync(0xffffffffu, key, 1);
-    const unsigned last = __ballot_sync(0xffffffffu, lane < live && next != key);
+    const unsigned last = __ballot_sync(0xffffffffu, lane < live && (lane + 1 == n || next != key));
     const bool from_before = before == key, goes_on = lane + 1 == n && after == key;
     const unsigned whole = __ballot_sync(0xffffffffu, lane < live && !((key == head && from_before) || goes_on));
     float acc[K][V];
