@@ -96,11 +96,38 @@ def test_sizes(rows, d, vocab, dtype, accumulate):
 @pytest.mark.parametrize("shift", [0, 1, 2, 4])
 @pytest.mark.parametrize("kind", ["zipf", "one", "none", "two", "even"])
 @pytest.mark.parametrize("dtype,rows,d,vocab", [(BF, 2000, 64, 77), (F32, 777, 24, 1000), (BF, 300, 41, 20),
-                                                (BF, 1, 512, 256), (F32, 2, 3, 1)])
+                                                (BF, 1, 512, 256), (F32, 2, 3, 1),
+                                                (BF, 100000, 24, 77), (F32, 300001, 9, 5), (F32, 33000, 300, 40)])
 def test_tokens_and_alignments(dtype, rows, d, vocab, kind, shift):
     p = _inputs(rows, d, vocab, dtype, 5, kind, shift)
     for accumulate in (False, True):
         _check(p, -0.37, accumulate)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows", [2047 * 16 + 1, 2048 * 16, 2049 * 16 - 3, 140000])
+def test_runs_that_end_around_groups_of_chunks(rows, dtype):
+    """Sorted tokens whose rows begin and end at, just before and just behind
+    the ends of 16 rows and of 32 times 16."""
+    import transformer_xl_relative_rel_gb300 as txl
+    g = _gen(rows)
+    lengths, total = [], 0
+    near = [1, 15, 16, 17, 31, 511, 512, 513, 1023, 1024, 1025, 528, 496, 5000, 2560, 33 * 16, 3, 13, 498]
+    while total < rows:
+        lengths.append(near[len(lengths) % len(near)] + (len(lengths) // len(near)) % 5)
+        total += lengths[-1]
+    tok = torch.repeat_interleave(torch.arange(len(lengths)), torch.tensor(lengths))[:rows].cuda()
+    vocab = len(lengths)
+    dout = torch.randint(-4, 5, (rows, 140), device="cuda", generator=g).to(dtype)
+    want = torch.zeros(vocab, 140, dtype=torch.float64, device="cuda").index_add_(0, tok, dout.double())
+    order = torch.randperm(rows, device="cuda", generator=g)
+    for t, x in ((tok, dout), (tok[order], dout[order].contiguous())):
+        grad = txl.embed_bwd(t, x, vocab=vocab)
+        # whole numbers below 2^24: exact sums, one rounding
+        assert torch.equal(grad, want.to(dtype))
+        old = torch.ones(vocab, 140, dtype=dtype, device="cuda")
+        assert torch.equal(txl.embed_bwd(t, x, old, accumulate=True), (want + 1).to(dtype))
+    txl.check()
 
 
 def test_rows_of_other_tokens_stay_as_they_are():

@@ -96,9 +96,11 @@ struct SortPass {
     int n, vocab, tile, blocks, shift, bits;
 };
 
+// what the sort's first launch sets to zero besides: the table, the work list's length
 struct ZeroJob {
     unsigned char *p;
     size_t bytes;
+    int *length;
 };
 
 __device__ __forceinline__ int sort_key(const SortPass &a, int i)
@@ -145,6 +147,7 @@ sort_count_kernel(const __grid_constant__ SortPass a, const __grid_constant__ Ze
     const int digits = 1 << a.bits;
     for (int d = threadIdx.x; d < digits; d += kSortThreads) count[d] = 0;
     chain_wait();
+    if (z.length && blockIdx.x == 0 && threadIdx.x == 0) *z.length = 0;
     if ((int)blockIdx.x >= a.blocks) {
         zero_table(z, blockIdx.x - a.blocks, gridDim.x - a.blocks);
         return;
@@ -185,10 +188,15 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_c
     // a digit's rows in all blocks, and those in the blocks before this one
     int total = 0, before = 0;
     if (t < digits)
-        for (int b = 0; b < a.blocks; ++b) {
-            const int c = a.count[(size_t)b * digits + t];
-            if (b < (int)blockIdx.x) before += c;
-            total += c;
+        for (int b = 0; b < a.blocks; b += 16) {      // (16 asked for at once)
+            int c[16];
+#pragma unroll
+            for (int u = 0; u < 16; ++u) c[u] = b + u < a.blocks ? a.count[(size_t)(b + u) * digits + t] : 0;
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+                if (b + u < (int)blockIdx.x) before += c[u];
+                total += c[u];
+            }
         }
     // sums over the digits below
     int run = total;
@@ -268,6 +276,7 @@ embed_sort_kernel(const __grid_constant__ ClusterSort a, const __grid_constant__
     const int first = rank * a.tile, n = max(0, min(a.tile, a.n - first));
     const int per = (a.tile + kSortWarps - 1) / kSortWarps, from = min(w * per, n), to = min(from + per, n);
     chain_wait();
+    if (z.length && rank == 0 && t == 0) *z.length = 0;
     for (int i = t; i < n; i += kSortThreads) {
         const int64_t token = a.tokens[first + i];
         list[0][i] = make_int2(token >= 0 && token < a.vocab ? (int)token : a.vocab, first + i);
@@ -355,6 +364,7 @@ struct SumArgs {
     void *dtable;
     float *part;             // [chunks][2][pitch]: sums of a token that begins before the chunk (0), of one
                              // that begins in it and goes on behind it (1)
+    int *work;               // NULL, or the number of chunks in which a token begins that goes on, and these chunks
     float scale;
     int n, d, vocab, chunks, strips, accumulate;
     long pitch;
@@ -388,6 +398,9 @@ __global__ void __launch_bounds__(NT) embed_sum_kernel(const __grid_constant__ S
     const unsigned last = __ballot_sync(0xffffffffu, lane < live && (lane + 1 == n || next != key));
     const bool from_before = before == key, goes_on = lane + 1 == n && after == key;
     const unsigned whole = __ballot_sync(0xffffffffu, lane < live && !((key == head && from_before) || goes_on));
+    // (the list's order does not matter: its entries are summed one by one)
+    if (a.work && lane + 1 == kChunk && lane < live && goes_on && !(key == head && from_before) && c < kStrip)
+        a.work[1 + atomicAdd(a.work, 1)] = chunk;
     float acc[K][V];
 #pragma unroll
     for (int k = 0; k < K; ++k)
@@ -443,12 +456,11 @@ __global__ void __launch_bounds__(NT) embed_sum_kernel(const __grid_constant__ S
     }
 }
 
-// Adds the partial sums of tokens that begin in a chunk and go on behind it.
-// Warp y looks at the y-th of a block's chunks and adds what begins there
-// where that is in few chunks; a longer token's chunks are shared out among
-// the warps, warp y taking the y-th, (y + 8)-th, ...
+// Joining the partial sums of tokens that begin in a chunk and go on behind it.
 constexpr int kJoinWarps = NT / 32, kJoinColumns = 128;
-constexpr int kJoinAlone = 8;      // chunks behind the first
+constexpr int kJoinAlone = 8;      // chunks behind the first that a warp adds by itself
+constexpr int kGroup = 32;         // chunks whose sums are joined beforehand where one token fills them
+constexpr int kManyChunks = 2048;  // from which on there are groups and a list of work
 
 __device__ __forceinline__ void add_float4(float4 &acc, const float4 &v)
 {
@@ -456,6 +468,12 @@ __device__ __forceinline__ void add_float4(float4 &acc, const float4 &v)
     acc.y += v.y;
     acc.z += v.z;
     acc.w += v.w;
+}
+
+// the partial sums of a chunk's token from before (0) or going on (1), four columns
+__device__ __forceinline__ float4 part_of(const SumArgs &a, int chunk, int which, int c)
+{
+    return *(const float4 *)(a.part + (2 * (size_t)chunk + which) * a.pitch + c);
 }
 
 template <typename T>
@@ -468,84 +486,146 @@ __device__ __forceinline__ void write_sum(const SumArgs &a, int token, int c, fl
     store_vec<T, 1>(to, x);
 }
 
-template <typename T>
+// The sums of the warps' `acc`, of kJoinColumns columns, in the first threads.
+__device__ __forceinline__ float block_columns(const float4 &acc, float4 (&sums)[kJoinWarps][32])
+{
+    __syncthreads();             // (the places may still be read)
+    sums[threadIdx.x >> 5][threadIdx.x & 31] = acc;
+    __syncthreads();
+    float all = 0.f;
+    if (threadIdx.x < kJoinColumns)
+#pragma unroll
+        for (int k = 0; k < kJoinWarps; ++k) all += ((const float *)sums[k])[threadIdx.x];
+    return all;
+}
+
+// Joins each group of chunks that lie inside one token's: their sum takes the
+// place 1 of the first one's, which such chunks do not use.
+__global__ void __launch_bounds__(NT) embed_group_kernel(const __grid_constant__ SumArgs a)
+{
+    chain_begin();
+    __shared__ float4 sums[kJoinWarps][32];
+    const int lane = threadIdx.x & 31, y = threadIdx.x >> 5, strips = (a.d + kJoinColumns - 1) / kJoinColumns;
+    const int first = (int)(blockIdx.x / strips) * kGroup, c = (int)(blockIdx.x % strips) * kJoinColumns + 4 * lane;
+    const long row = (long)first * kChunk, after = row + kGroup * kChunk;
+    chain_wait();
+    if (row == 0 || after >= a.n) return;
+    const int key = a.key[row], before = a.key[row - 1], behind = a.key[after];
+    if (key >= a.vocab || before != key || behind != key) return;
+    constexpr int kEach = kGroup / kJoinWarps;
+    float4 v[kEach];
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) v[u] = c < a.d ? part_of(a, first + y + u * kJoinWarps, 0, c) : make_float4(0, 0, 0, 0);
+#pragma unroll
+    for (int u = 1; u < kEach; ++u) add_float4(v[0], v[u]);
+    const float all = block_columns(v[0], sums);
+    const int column = (int)(blockIdx.x % strips) * kJoinColumns + threadIdx.x;
+    if (threadIdx.x < kJoinColumns && column < a.d) a.part[(2 * (size_t)first + 1) * a.pitch + column] = all;
+}
+
+// The last chunk with rows of the token `key`, which has the first row of
+// `chunk` + 1 (a warp's search by 32 chunks' first rows at once).
+__device__ __forceinline__ int last_chunk(const SumArgs &a, int chunk, int key)
+{
+    int lo = chunk, hi = a.chunks;      // lo has rows of it, hi has not
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 32) / 33;
+        const long at = lo + (long)step * ((threadIdx.x & 31) + 1);
+        const int in = __popc(__ballot_sync(0xffffffffu, at < hi && a.key[at * kChunk] == key));
+        if ((long)lo + (long)step * (in + 1) < hi) hi = lo + step * (in + 1);
+        lo += step * in;
+    }
+    return lo;
+}
+
+// The sum of the token's chunks from `chunk` to `end` over the block's warps,
+// warp y taking the y-th, (y + 8)-th, ... of them, groups (where there are) as one.
+__device__ __forceinline__ float4 warp_share(const SumArgs &a, int chunk, int end, bool groups, int c, int y)
+{
+    // chunks before the first group inside, the groups, chunks behind them
+    int g0 = chunk / kGroup + 1, g1 = end / kGroup;
+    if (!groups || g1 < g0) g0 = g1 = end / kGroup + 1;
+    const int head = min(end + 1, g0 * kGroup) - chunk, inside = g1 - g0;
+    const int total = head + inside + (end + 1 > g1 * kGroup ? end + 1 - g1 * kGroup : 0);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < a.d)
+        for (int i = y; i < total; i += 8 * kJoinWarps) {
+            float4 v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int x = i + u * kJoinWarps;
+                if (x < head) v[u] = part_of(a, chunk + x, x == 0, c);
+                else if (x < head + inside) v[u] = part_of(a, (g0 + x - head) * kGroup, 1, c);
+                else if (x < total) v[u] = part_of(a, g1 * kGroup + x - head - inside, 0, c);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (i + u * kJoinWarps < total) add_float4(acc, v[u]);
+        }
+    return acc;
+}
+
+// Warp y looks at the y-th of eight chunks and adds what begins there where
+// that is in few chunks; a longer token's are shared out among the warps.  The
+// chunks are a block's own, or, LIST, the listed ones, blocks taking eight of
+// them and a strip in turn.
+template <typename T, bool LIST>
 __global__ void __launch_bounds__(NT) embed_join_kernel(const __grid_constant__ SumArgs a)
 {
     chain_begin();
-    __shared__ int token[kJoinWarps], ends[kJoinWarps];
+    __shared__ int token[kJoinWarps], begins[kJoinWarps], ends[kJoinWarps];
     __shared__ float4 sums[kJoinWarps][32];
     const int lane = threadIdx.x & 31, y = threadIdx.x >> 5, strips = (a.d + kJoinColumns - 1) / kJoinColumns;
-    const int group = (int)(blockIdx.x / strips) * kJoinWarps, c = (int)(blockIdx.x % strips) * kJoinColumns + 4 * lane;
-    const auto part = [&](int chunk, int which) {
-        return *(const float4 *)(a.part + (2 * (size_t)chunk + which) * a.pitch + c);
-    };
     chain_wait();
-    {
-        const int chunk = group + y, first = chunk * kChunk, next = first + kChunk;
-        int key = -1, end = chunk;      // end: the last chunk with rows of it
-        if (next < a.n) {
-            const long at = (long)next + (long)lane * kChunk;      // (asked for at once with the others)
-            const int begin = at < a.n ? a.key[at] : -1;
-            const int before = first > 0 ? a.key[first - 1] : -1;
-            key = a.key[next - 1];
-            if (key >= a.vocab || before == key) key = -1;
-            const unsigned same = __ballot_sync(0xffffffffu, begin == key);
-            int run = same == 0xffffffffu ? 32 : __ffs(~same) - 1;
-            if (key >= 0) end += run;
-            while (key >= 0 && run == 32) {      // 32 chunks' first rows at once
-                const long more = ((long)end + 1 + lane) * kChunk;
-                const unsigned also = __ballot_sync(0xffffffffu, more < a.n && a.key[more] == key);
-                run = also == 0xffffffffu ? 32 : __ffs(~also) - 1;
-                end += run;
+    const int listed = LIST ? a.work[0] : 0;
+    const long items = LIST ? ((long)listed + kJoinWarps - 1) / kJoinWarps * strips : (long)gridDim.x;
+    for (long item = blockIdx.x; item < items; item += gridDim.x) {
+        const int group = (int)(item / strips) * kJoinWarps, strip = (int)(item % strips) * kJoinColumns;
+        const int c = strip + 4 * lane;
+        {
+            const bool there = !LIST || group + y < listed;
+            const int chunk = LIST ? (there ? a.work[1 + group + y] : 0) : group + y;
+            const int first = chunk * kChunk, next = first + kChunk;
+            int key = -1, end = chunk;      // end: the last chunk with rows of it
+            if (there && next < a.n) {
+                const long at = (long)next + (long)lane * kChunk;      // (asked for at once with the others)
+                const int begin = at < a.n ? a.key[at] : -1;
+                const int before = first > 0 ? a.key[first - 1] : -1;
+                key = a.key[next - 1];
+                if (key >= a.vocab || before == key) key = -1;
+                const unsigned same = __ballot_sync(0xffffffffu, begin == key);
+                if (key >= 0) end = same == 0xffffffffu ? last_chunk(a, chunk + 32, key) : chunk + __ffs(~same) - 1;
+                if (end == chunk) key = -1;
             }
-            if (end == chunk) key = -1;
-        }
-        if (key >= 0 && end - chunk <= kJoinAlone) {
-            if (c < a.d) {
-                float4 v[kJoinAlone + 1];
+            if (key >= 0 && end - chunk <= kJoinAlone) {
+                if (c < a.d) {
+                    float4 v[kJoinAlone + 1];
 #pragma unroll
-                for (int k = 0; k <= kJoinAlone; ++k)
-                    if (chunk + k <= end) v[k] = part(chunk + k, k == 0);
+                    for (int k = 0; k <= kJoinAlone; ++k)
+                        if (chunk + k <= end) v[k] = part_of(a, chunk + k, k == 0, c);
 #pragma unroll
-                for (int k = 1; k <= kJoinAlone; ++k)
-                    if (chunk + k <= end) add_float4(v[0], v[k]);
-                const float one[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+                    for (int k = 1; k <= kJoinAlone; ++k)
+                        if (chunk + k <= end) add_float4(v[0], v[k]);
+                    const float one[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (c + i < a.d) write_sum<T>(a, key, c + i, one[i]);
+                    for (int i = 0; i < 4; ++i)
+                        if (c + i < a.d) write_sum<T>(a, key, c + i, one[i]);
+                }
+                key = -1;
             }
-            key = -1;
-        }
-        if (lane == 0) {
-            token[y] = key;
-            ends[y] = end;
-        }
-    }
-    __syncthreads();
-    for (int x = 0; x < kJoinWarps; ++x) {
-        const int key = token[x], chunk = group + x, end = ends[x];
-        if (key < 0) continue;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (c < a.d)
-            for (int k = chunk + y; k <= end; k += 8 * kJoinWarps) {
-                float4 v[8];
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    if (k + u * kJoinWarps <= end) v[u] = part(k + u * kJoinWarps, u == 0 && k == chunk);
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    if (k + u * kJoinWarps <= end) add_float4(acc, v[u]);
+            if (LIST) __syncthreads();      // (the places may still be read)
+            if (lane == 0) {
+                token[y] = key;
+                begins[y] = chunk;
+                ends[y] = end;
             }
-        sums[y][lane] = acc;
-        __syncthreads();
-        if (threadIdx.x < kJoinColumns) {
-            const int column = (int)(blockIdx.x % strips) * kJoinColumns + threadIdx.x;
-            float all = 0.f;
-#pragma unroll
-            for (int k = 0; k < kJoinWarps; ++k) all += ((const float *)sums[k])[threadIdx.x];
-            if (column < a.d) write_sum<T>(a, key, column, all);
         }
         __syncthreads();
+        for (int x = 0; x < kJoinWarps; ++x) {
+            if (token[x] < 0) continue;
+            const float all = block_columns(warp_share(a, begins[x], ends[x], LIST, c, y), sums);
+            if (threadIdx.x < kJoinColumns && strip + (int)threadIdx.x < a.d) write_sum<T>(a, token[x], strip + threadIdx.x, all);
+        }
     }
 }
 
@@ -556,7 +636,7 @@ struct EmbedPlan {
     bool cluster;
     int passes, bits, tile, blocks, chunks;
     long pitch;
-    size_t key[2], row[2], count, part, bytes;
+    size_t key[2], row[2], count, part, work, bytes;
 };
 
 EmbedPlan embed_plan(int rows, int d, int vocab)
@@ -585,6 +665,7 @@ EmbedPlan embed_plan(int rows, int d, int vocab)
     }
     q.count = take(q.cluster ? 0 : (size_t)q.blocks * ((size_t)1 << q.bits) * 4);
     q.part = take((size_t)q.chunks * 2 * q.pitch * 4);
+    q.work = take(q.chunks >= kManyChunks ? (size_t)(q.chunks + 1) * 4 : 0);
     q.bytes = at;
     return q;
 }
@@ -629,8 +710,16 @@ cudaError_t run_sums(SumArgs a, cudaStream_t s)
     cudaError_t e = chain_launch(a.accumulate ? embed_sum_kernel<T, V, true> : embed_sum_kernel<T, V, false>,
                                  (unsigned)((tasks + NT / 32 - 1) / (NT / 32)), NT, 0, 1, s, a);
     if (e != cudaSuccess || a.chunks == 1) return e;
-    const long strips = (a.d + kJoinColumns - 1) / kJoinColumns, groups = (a.chunks + kJoinWarps - 2) / kJoinWarps;
-    return chain_launch(embed_join_kernel<T>, (unsigned)(groups * strips), NT, 0, 1, s, a);
+    const long strips = (a.d + kJoinColumns - 1) / kJoinColumns;
+    if (a.work) {
+        e = chain_launch(embed_group_kernel, (unsigned)((a.chunks + kGroup - 1) / kGroup * strips), NT, 0, 1, s, a);
+        const long want = (a.chunks + kJoinWarps - 1) / kJoinWarps * strips, most = 4L * device_sm_count();
+        if (e == cudaSuccess)
+            e = chain_launch(embed_join_kernel<T, true>, (unsigned)(want < most ? want : most), NT, 0, 1, s, a);
+        return e;
+    }
+    const long groups = (a.chunks + kJoinWarps - 2) / kJoinWarps;
+    return chain_launch(embed_join_kernel<T, false>, (unsigned)(groups * strips), NT, 0, 1, s, a);
 }
 
 // blocks that set the table to zero: at most what fills the SMs
@@ -662,7 +751,7 @@ cudaError_t sort_by_launches(const EmbedPlan &q, const int64_t *tokens, int rows
     const size_t smem = (size_t)(kSortWarps << q.bits) * 4 + kSortWarps * 4;
     cudaError_t e = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (kSortWarps << kDigitBits) * 4 + kSortWarps * 4);
-    const ZeroJob none = {nullptr, 0};
+    const ZeroJob none = {nullptr, 0, nullptr};
     for (int x = 0; x < q.passes && e == cudaSuccess; ++x) {
         SortPass p;
         p.tokens = x == 0 ? tokens : nullptr;
@@ -689,7 +778,8 @@ cudaError_t run_bwd(const int64_t *tokens, const void *dout, float scale, int ro
 {
     const EmbedPlan q = embed_plan(rows, d, vocab);
     const size_t esz = dtype == TXL_F32 ? 4 : 2;
-    const ZeroJob z = {(unsigned char *)dtable, accumulate ? 0 : (size_t)vocab * d * esz};
+    int *work = q.chunks >= kManyChunks ? (int *)(ws + q.work) : nullptr;
+    const ZeroJob z = {(unsigned char *)dtable, accumulate ? 0 : (size_t)vocab * d * esz, work};
     const int sorted = q.cluster ? 0 : (q.passes + 1) & 1;
     int *key = (int *)(ws + q.key[sorted]), *row = (int *)(ws + q.row[sorted]);
     const cudaError_t e = q.cluster ? sort_in_cluster(q, tokens, rows, vocab, z, key, row, s)
@@ -701,6 +791,7 @@ cudaError_t run_bwd(const int64_t *tokens, const void *dout, float scale, int ro
     a.dout = dout;
     a.dtable = dtable;
     a.part = (float *)(ws + q.part);
+    a.work = work;
     a.scale = scale;
     a.n = rows;
     a.d = d;
