@@ -21,6 +21,9 @@
 // 512 bf16 with residual forward 11.8 us (52 MB), backward 15.1 us (70 MB),
 // column sums 3.6 us; 6144 x 1024 with the sum kept 11.4 us (50 MB), 15.0 us
 // (50 MB, bound by its instructions: a row's xh is computed twice) and 3.7 us.
+// Wider rows as 16 columns a thread (8 in the backward), so that two or more
+// blocks share an SM: 65536 x 8192 forward 1034 -> 664 us, 65536 x 2048 270 ->
+// 148 and 297 -> 198 us, against 256 and 1024 threads.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -33,8 +36,8 @@ namespace txl {
 namespace {
 
 constexpr int kMaxRows = 1 << 30;
-constexpr int kMaxNormWidth = 8192;    // 1024 threads hold 8 columns each
-constexpr int kMostBlocks = 304;       // of the backward: two per SM
+constexpr int kMaxNormWidth = 8192;    // 1024 threads of the backward hold 8 columns each
+constexpr int kMostBlocks = 608;       // of the backward: four per SM
 constexpr int kWarpBlock = 256;        // threads of a block whose warps take a row each
 
 struct NormArgs {
@@ -47,7 +50,19 @@ struct NormArgs {
     int rows, d, pitch, weights;
 };
 
-// the sum of v over the group's G threads
+// The warp's sums of a and of b: half the lanes go on with either.
+__device__ __forceinline__ void two_sums(float &a, float &b)
+{
+    const bool low = (threadIdx.x & 16) == 0;
+    float v = (low ? a : b) + __shfl_xor_sync(0xffffffffu, low ? b : a, 16);
+#pragma unroll
+    for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    a = __shfl_sync(0xffffffffu, v, 0);
+    b = __shfl_sync(0xffffffffu, v, 16);
+}
+
+// The sum of v over the group's G threads, through shared[G / 32], which the
+// sum after the next may use again (one barrier each: two places in turn).
 template <int G>
 __device__ __forceinline__ float group_sum(float v, float *shared)
 {
@@ -55,7 +70,6 @@ __device__ __forceinline__ float group_sum(float v, float *shared)
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if constexpr (G > 32) {
         const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-        __syncthreads();          // (the places may still be read)
         if (lane == 0) shared[w] = v;
         __syncthreads();
         v = lane < G / 32 ? shared[lane] : 0.f;
@@ -65,15 +79,32 @@ __device__ __forceinline__ float group_sum(float v, float *shared)
     return v;
 }
 
+// ... of a and of b
+template <int G>
+__device__ __forceinline__ void group_sums(float &a, float &b, float2 *shared)
+{
+    two_sums(a, b);
+    if constexpr (G > 32) {
+        const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+        if (lane == 0) shared[w] = make_float2(a, b);
+        __syncthreads();
+        const float2 v = lane < G / 32 ? shared[lane] : make_float2(0.f, 0.f);
+        a = v.x;
+        b = v.y;
+        two_sums(a, b);
+    }
+}
+
 // threads of a block: 8 groups of a warp, or one group
 template <int G>
 constexpr int kBlock = G == 32 ? kWarpBlock : G;
 
 template <typename T, int V, int K, int G>
-__global__ void __launch_bounds__(kBlock<G>, G == 32 && K * V <= 16 ? 4 : 1) norm_fwd_kernel(const __grid_constant__ NormArgs a)
+__global__ void __launch_bounds__(kBlock<G>, G == 32 ? (K * V <= 16 ? 4 : 1) : V * sizeof(T) == 16 ? 1024 / G : 1)
+norm_fwd_kernel(const __grid_constant__ NormArgs a)
 {
     chain_begin();
-    __shared__ float shared[32];
+    __shared__ float shared[2][32];
     const int t = G == 32 ? threadIdx.x & 31 : threadIdx.x;
     const long row = G == 32 ? (long)blockIdx.x * (kWarpBlock / 32) + (threadIdx.x >> 5) : (long)blockIdx.x;
     chain_wait();
@@ -128,7 +159,7 @@ __global__ void __launch_bounds__(kBlock<G>, G == 32 && K * V <= 16 ? 4 : 1) nor
             for (int i = 0; i < V; ++i) sum += s[k][i];
         }
     }
-    const float mean = group_sum<G>(sum, shared) / (float)a.d;
+    const float mean = group_sum<G>(sum, shared[0]) / (float)a.d;
     float square = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k)
@@ -136,7 +167,7 @@ __global__ void __launch_bounds__(kBlock<G>, G == 32 && K * V <= 16 ? 4 : 1) nor
 #pragma unroll
             for (int i = 0; i < V; ++i) square = fmaf(s[k][i] - mean, s[k][i] - mean, square);
         }
-    const float rstd = rsqrtf(group_sum<G>(square, shared) / (float)a.d + a.eps);
+    const float rstd = rsqrtf(group_sum<G>(square, shared[1]) / (float)a.d + a.eps);
     if (t == 0 && a.mean) {
         a.mean[row] = mean;
         a.rstd[row] = rstd;
@@ -158,7 +189,7 @@ template <typename T, int V, int K, int G>
 __global__ void __launch_bounds__(kBlock<G>) norm_bwd_kernel(const __grid_constant__ NormArgs a)
 {
     chain_begin();
-    __shared__ float shared[32];
+    __shared__ float2 shared[2][32];
     extern __shared__ float columns[];      // G = 32: [8 warps][2][32 V K]
     constexpr int kGroups = kBlock<G> / G;
     const int t = G == 32 ? threadIdx.x & 31 : threadIdx.x, w = G == 32 ? threadIdx.x >> 5 : 0;
@@ -169,9 +200,10 @@ __global__ void __launch_bounds__(kBlock<G>) norm_bwd_kernel(const __grid_consta
         for (int i = 0; i < V; ++i) dg[k][i] = db[k][i] = 0.f;
     chain_wait();
     const float inverse = 1.f / (float)a.d;
+    int place = 0;
     for (long row = (long)blockIdx.x * kGroups + w; row < a.rows; row += (long)gridDim.x * kGroups) {
         const size_t at = (size_t)row * a.d;
-        raw_t<T, V> rx[K], rr[K], ry[K];
+        raw_t<T, V> rx[K], rr[K], ry[K], rs[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (k * G + t) * V;
@@ -179,6 +211,7 @@ __global__ void __launch_bounds__(kBlock<G>) norm_bwd_kernel(const __grid_consta
                 rx[k] = load_raw<T, V>((const T *)a.x + at + c);
                 ry[k] = load_raw<T, V>((const T *)a.dy + at + c);
                 if (a.residual) rr[k] = load_raw<T, V>((const T *)a.residual + at + c);
+                if (a.dsum) rs[k] = load_raw<T, V>((const T *)a.dsum + at + c);
             }
         }
         const float mean = a.mean[row], rstd = a.rstd[row];
@@ -210,8 +243,10 @@ __global__ void __launch_bounds__(kBlock<G>) norm_bwd_kernel(const __grid_consta
                 }
             }
         }
-        sum = group_sum<G>(sum, shared) * inverse;
-        along = group_sum<G>(along, shared) * inverse;
+        group_sums<G>(sum, along, shared[place]);
+        place ^= 1;
+        sum *= inverse;
+        along *= inverse;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (k * G + t) * V;
@@ -220,7 +255,7 @@ __global__ void __launch_bounds__(kBlock<G>) norm_bwd_kernel(const __grid_consta
                 for (int i = 0; i < V; ++i) g[k][i] = (g[k][i] - sum - hat[k][i] * along) * rstd;
                 if (a.dsum) {
                     float r[V];
-                    unpack<T, V>(load_raw<T, V>((const T *)a.dsum + at + c), r);
+                    unpack<T, V>(rs[k], r);
 #pragma unroll
                     for (int i = 0; i < V; ++i) g[k][i] += r[i];
                 }
@@ -284,17 +319,6 @@ __device__ __forceinline__ void wait_copies(int n)
     if (n == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
     else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
     else asm volatile("cp.async.wait_group 2;" ::: "memory");
-}
-
-// the warp's sums of a and of b: half the lanes go on with either
-__device__ __forceinline__ void two_sums(float &a, float &b)
-{
-    const bool low = (threadIdx.x & 16) == 0;
-    float v = (low ? a : b) + __shfl_xor_sync(0xffffffffu, low ? b : a, 16);
-#pragma unroll
-    for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    a = __shfl_sync(0xffffffffu, v, 0);
-    b = __shfl_sync(0xffffffffu, v, 16);
 }
 
 template <typename T, int V, int G>
@@ -542,11 +566,13 @@ norm_columns_kernel(const float *part, int blocks, int d, int pitch, float *dgam
 // ---------------------------------------------------------------- host side
 int norm_pitch(int d) { return (d + 3) / 4 * 4; }
 
-// blocks of the backward: groups of 8 warps, or one row at a time
+// Blocks of the backward, as many as the SMs hold: of 8 warps that take a row
+// each, two per SM; of 8, 16 or 32 that share one, four, two and one.
 int norm_blocks(int rows, int d)
 {
     const int groups = d <= 1024 ? kWarpBlock / 32 : 1;
-    const long want = ((long)rows + groups - 1) / groups, most = d <= 4096 ? kMostBlocks : kMostBlocks / 2;
+    const long want = ((long)rows + groups - 1) / groups;
+    const long most = 152 * (d <= 1024 ? 2 : d <= 2048 ? 4 : d <= 4096 ? 2 : 1);
     return (int)(want < most ? want : most);
 }
 
@@ -615,8 +641,9 @@ cudaError_t pick_fwd(const NormArgs &a, cudaStream_t s)
     }
     if (a.d <= 512) return launch_fwd<T, V, 16 / V, 32>(a, s);
     if (a.d <= 1024) return launch_fwd<T, V, 32 / V, 32>(a, s);
+    if (a.d <= 2048) return launch_fwd<T, V, 16 / V, 128>(a, s);
     if (a.d <= 4096) return launch_fwd<T, V, 16 / V, 256>(a, s);
-    return launch_fwd<T, V, 8 / V, 1024>(a, s);
+    return launch_fwd<T, V, 16 / V, 512>(a, s);
 }
 
 template <typename T, int V>
@@ -630,7 +657,8 @@ cudaError_t pick_bwd(const NormArgs &a, int blocks, cudaStream_t s)
         if (a.d <= 512) return launch_bwd<T, V, 16 / V, 32>(a, blocks, s);
         if (a.d <= 1024) return launch_bwd<T, V, 32 / V, 32>(a, blocks, s);
     }
-    if (a.d <= 4096) return launch_bwd<T, V, 16 / V, 256>(a, blocks, s);
+    if (a.d <= 2048) return launch_bwd<T, V, 8 / V, 256>(a, blocks, s);
+    if (a.d <= 4096) return launch_bwd<T, V, 8 / V, 512>(a, blocks, s);
     return launch_bwd<T, V, 8 / V, 1024>(a, blocks, s);
 }
 
