@@ -86,6 +86,17 @@ def test_unaligned(dtype, d, shift):
     _check(p, keep=True, dsum=True)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,d,shift", [(1, 513, 0), (7, 769, 0), (3000, 771, 0), (1300, 1023, 0), (2500, 411, 0),
+                                          (1, 514, 1), (9, 770, 1), (5000, 1000, 1), (5000, 1024, 1), (3000, 256, 1)])
+def test_rows_read_by_single_elements(dtype, rows, d, shift):
+    """Odd widths, and even ones that start at an odd element; more rows than
+    the backward has groups of warps, and fewer."""
+    p = _inputs(rows, d, dtype, rows + d, shift)
+    _check(p)
+    _check(p, residual=False, affine=False, dsum=True)
+
+
 def test_one_pointer_unaligned():
     p = _inputs(45, 512, BF, 5)
     for name in p:

@@ -21,9 +21,10 @@
 // 512 bf16 with residual forward 11.8 us (52 MB), backward 15.1 us (70 MB),
 // column sums 3.6 us; 6144 x 1024 with the sum kept 11.4 us (50 MB), 15.0 us
 // (50 MB, bound by its instructions: a row's xh is computed twice) and 3.7 us.
-// Wider rows as 16 columns a thread (8 in the backward), so that two or more
-// blocks share an SM: 65536 x 8192 forward 1034 -> 664 us, 65536 x 2048 270 ->
-// 148 and 297 -> 198 us, against 256 and 1024 threads.
+// Wider rows as 16 columns a thread in the forward, 8 in the backward: 65536 x
+// 8192 forward 665 us (1024 threads of 8 columns: 1034), 65536 x 2048 forward
+// 148 (256 threads: 270), backward 198 (256 threads of up to 16 columns and
+// more barriers per row: 297).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -100,7 +101,7 @@ template <int G>
 constexpr int kBlock = G == 32 ? kWarpBlock : G;
 
 template <typename T, int V, int K, int G>
-__global__ void __launch_bounds__(kBlock<G>, G == 32 ? (K * V <= 16 ? 4 : 1) : V * sizeof(T) == 16 ? 1024 / G : 1)
+__global__ void __launch_bounds__(kBlock<G>, G == 32 ? (K * V <= 16 ? 4 : 1) : V * sizeof(T) == 16 || K * V <= 8 ? 1024 / G : 1)
 norm_fwd_kernel(const __grid_constant__ NormArgs a)
 {
     chain_begin();
@@ -567,16 +568,23 @@ norm_columns_kernel(const float *part, int blocks, int d, int pitch, float *dgam
 int norm_pitch(int d) { return (d + 3) / 4 * 4; }
 
 // Blocks of the backward, as many as the SMs hold: of 8 warps that take a row
-// each, two per SM; of 8, 16 or 32 that share one, four, two and one.
-int norm_blocks(int rows, int d)
+// each, two per SM; of 8, 16 or 32 that share one, four, two and one.  (bf16
+// rows of an odd width are read by single elements, and above 512 columns 8
+// warps share one; so are those of an even width that start at an odd element,
+// by the blocks that their width has.)
+int norm_blocks(int rows, int d, txl_dtype dtype)
 {
-    const int groups = d <= 1024 ? kWarpBlock / 32 : 1;
+    const bool warps = d <= 512 || (d <= 1024 && (d % 2 == 0 || dtype == TXL_F32));
+    const int groups = warps ? kWarpBlock / 32 : 1;
     const long want = ((long)rows + groups - 1) / groups;
-    const long most = 152 * (d <= 1024 ? 2 : d <= 2048 ? 4 : d <= 4096 ? 2 : 1);
+    const long most = 152 * (warps ? 2 : d <= 2048 ? 4 : d <= 4096 ? 2 : 1);
     return (int)(want < most ? want : most);
 }
 
-size_t norm_bytes(int rows, int d) { return (size_t)norm_blocks(rows, d) * 2 * norm_pitch(d) * 4 + 256; }
+size_t norm_bytes(int rows, int d, txl_dtype dtype)
+{
+    return (size_t)norm_blocks(rows, d, dtype) * 2 * norm_pitch(d) * 4 + 256;
+}
 
 txl_status norm_sizes(int rows, int d, txl_dtype dtype)
 {
@@ -636,11 +644,19 @@ cudaError_t launch_bwd(const NormArgs &a, int blocks, cudaStream_t s)
 template <typename T, int V>
 cudaError_t pick_fwd(const NormArgs &a, cudaStream_t s)
 {
-    if constexpr (V >= 4) {
+    if constexpr (V != 2) {
         if (a.d <= 256) return launch_fwd<T, V, 8 / V, 32>(a, s);
     }
-    if (a.d <= 512) return launch_fwd<T, V, 16 / V, 32>(a, s);
-    if (a.d <= 1024) return launch_fwd<T, V, 32 / V, 32>(a, s);
+    if constexpr (V == 1) {
+        // single elements take as many loads as columns: few of them a thread,
+        // for enough warps to wait for each other (262144 x 1023 bf16 rows 727
+        // -> 420 us, x 411 fp32 350 -> 276, against a warp per row)
+        if (a.d <= 512) return launch_fwd<T, V, 4, 128>(a, s);
+        if (a.d <= 1024) return launch_fwd<T, V, 8, 128>(a, s);
+    } else {
+        if (a.d <= 512) return launch_fwd<T, V, 16 / V, 32>(a, s);
+        if (a.d <= 1024) return launch_fwd<T, V, 32 / V, 32>(a, s);
+    }
     if (a.d <= 2048) return launch_fwd<T, V, 16 / V, 128>(a, s);
     if (a.d <= 4096) return launch_fwd<T, V, 16 / V, 256>(a, s);
     return launch_fwd<T, V, 16 / V, 512>(a, s);
@@ -654,8 +670,12 @@ cudaError_t pick_bwd(const NormArgs &a, int blocks, cudaStream_t s)
         if (a.d <= 512) return launch_rows<T, V, 2>(a, blocks, s);
         if (a.d <= 1024) return launch_rows<T, V, 4>(a, blocks, s);
     } else {
-        if (a.d <= 512) return launch_bwd<T, V, 16 / V, 32>(a, blocks, s);
-        if (a.d <= 1024) return launch_bwd<T, V, 32 / V, 32>(a, blocks, s);
+        // as many loads as columns: 262144 x 255 rows 488 -> 162 us with 8
+        // columns a lane instead of 16, x 1023 1794 -> 684 with 8 warps to a
+        // row instead of one (x 411 568 by one warp, 977 by 8)
+        if (a.d <= 256) return launch_bwd<T, V, 8, 32>(a, blocks, s);
+        if (a.d <= 512) return launch_bwd<T, V, 16, 32>(a, blocks, s);
+        if (a.d <= 1024) return launch_bwd<T, V, 4, 256>(a, blocks, s);
     }
     if (a.d <= 2048) return launch_bwd<T, V, 8 / V, 256>(a, blocks, s);
     if (a.d <= 4096) return launch_bwd<T, V, 8 / V, 512>(a, blocks, s);
@@ -727,7 +747,7 @@ txl_status txl_layer_norm_bwd_workspace(int rows, int d_model, txl_dtype dtype, 
     if (!bytes) return TXL_ERR_INVALID;
     const txl_status st = norm_sizes(rows, d_model, dtype);
     if (st != TXL_OK) return st;
-    *bytes = rows ? norm_bytes(rows, d_model) : 256;
+    *bytes = rows ? norm_bytes(rows, d_model, dtype) : 256;
     return TXL_OK;
 }
 
@@ -751,8 +771,8 @@ txl_status txl_layer_norm_bwd(const void *dy, const void *x, const void *residua
         if (dbeta && e == cudaSuccess) e = cudaMemsetAsync(dbeta, 0, w, s);
         return finish(e);
     }
-    if (scratch && (!workspace || workspace_bytes < norm_bytes(rows, d_model))) return TXL_ERR_INVALID;
-    const int blocks = norm_blocks(rows, d_model), pitch = norm_pitch(d_model);
+    if (scratch && (!workspace || workspace_bytes < norm_bytes(rows, d_model, dtype))) return TXL_ERR_INVALID;
+    const int blocks = norm_blocks(rows, d_model, dtype), pitch = norm_pitch(d_model);
     const NormArgs a = {x, residual, dy, dsum, gamma, nullptr, dx, nullptr, (float *)mean, (float *)rstd,
                         (float *)workspace, 0.f, rows, d_model, pitch, weights};
     e = run_norm(a, dtype, true, blocks, s);
