@@ -19,8 +19,8 @@
 // for another; of 4, 8 and 16 blocks 16 are fastest: 15, 12 and 10 us.)
 //
 // What bounds it, forward and gradient of one call, under a profiler one by
-// one: 16896 x 512 rows of 256 tokens, added to the table: gather 7, sort 10,
-// sums 7, join 7 us, latencies of launches and of a handful of dependent loads
+// one: 16896 x 512 rows of 256 tokens, added to the table: gather 7 to 8, sort
+// 10 to 12, sums 7, join 6 to 7 us, latencies of launches and of a handful of dependent loads
 // in each (the bytes are worth 5 us); 6144 x 1024 rows, table of 131072 set
 // to zero: 45 us for 268 MB (5.9 TB/s, the sort hidden in it), sums 8, join 4.
 #include <cuda_runtime.h>

@@ -17,10 +17,11 @@
 // not serve) before it computes one: 6144 x 1024 pre-norm rows 27.7 -> 15.0 us
 // (the forward gained nothing by it, 12 -> 14 us, and keeps a row per warp).
 //
-// Measured one by one under a profiler (about 2.5 us of each a launch): 16896 x
-// 512 bf16 with residual forward 11.8 us (52 MB), backward 15.1 us (70 MB),
-// column sums 3.6 us; 6144 x 1024 with the sum kept 11.4 us (50 MB), 15.0 us
-// (50 MB, bound by its instructions: a row's xh is computed twice) and 3.7 us.
+// Measured one by one under a profiler (about 2.5 us of each a launch; several
+// GB300s): 16896 x 512 bf16 with residual forward 11.8 to 12.7 us (52 MB),
+// backward 15.1 to 15.8 us (70 MB), column sums 3.6 to 4.2 us; 6144 x 1024 with
+// the sum kept 11.4 to 13.2 us (50 MB), 15.0 to 15.7 us (50 MB, bound by its
+// instructions: a row's xh is computed twice) and 3.7 to 4.3 us.
 // Wider rows as 16 columns a thread in the forward, 8 in the backward: 65536 x
 // 8192 forward 665 us (1024 threads of 8 columns: 1034), 65536 x 2048 forward
 // 148 (256 threads: 270), backward 198 (256 threads of up to 16 columns and
