@@ -602,6 +602,8 @@ cudaError_t launch_fwd(const NormArgs &a, cudaStream_t s)
     return chain_launch(norm_fwd_kernel<T, V, K, G>, grid, kBlock<G>, 0, 1, s, a);
 }
 
+// `bytes`: the most that any call gives this kernel.  The limit is the kernel's
+// on its device and not a call's: host threads that call at once set the same.
 template <typename K>
 cudaError_t allow_shared(K kernel, size_t bytes)
 {
@@ -618,18 +620,34 @@ int stages_for(size_t stage, size_t other, int blocks)
     return stages;
 }
 
+// stages and shared memory of norm_bwd_rows_kernel for so many tensors
+struct RowsPlan {
+    int stages;
+    size_t smem;
+};
+
+template <typename T, int G>
+RowsPlan rows_plan(int tensors)
+{
+    constexpr size_t kWide = 32 * 8 * G * 4;
+    const size_t stage = stage_bytes<T, G>(tensors);
+    const int stages = stages_for(stage, kWide, 2);
+    const size_t rows = stages * kRowWarps * stage, sums = 2 * kRowWarps * kWide;      // (the column sums, at the end)
+    return {stages, kWide + (rows > sums ? rows : sums)};
+}
+
 template <typename T, int V, int G>
 cudaError_t launch_rows(const NormArgs &a, int blocks, cudaStream_t s)
 {
-    constexpr size_t kWide = 32 * 8 * G * 4;
-    const size_t stage = stage_bytes<T, G>(2 + (a.residual ? 1 : 0) + (a.dsum ? 1 : 0));
-    const int stages = stages_for(stage, kWide, 2);
-    size_t smem = stages * kRowWarps * stage;
-    if (smem < 2 * kRowWarps * kWide) smem = 2 * kRowWarps * kWide;      // (the column sums, at the end)
-    smem += kWide;
-    const cudaError_t e = allow_shared(norm_bwd_rows_kernel<T, V, G>, smem);
+    size_t most = 0;       // (of 2 to 4 tensors, not always 4: that may leave room for fewer stages)
+    for (int n = 2; n <= 4; ++n) {
+        const size_t smem = rows_plan<T, G>(n).smem;
+        most = smem > most ? smem : most;
+    }
+    const cudaError_t e = allow_shared(norm_bwd_rows_kernel<T, V, G>, most);
     if (e != cudaSuccess) return e;
-    return chain_launch(norm_bwd_rows_kernel<T, V, G>, (unsigned)blocks, kWarpBlock, smem, 1, s, a, stages);
+    const RowsPlan q = rows_plan<T, G>(2 + (a.residual ? 1 : 0) + (a.dsum ? 1 : 0));
+    return chain_launch(norm_bwd_rows_kernel<T, V, G>, (unsigned)blocks, kWarpBlock, q.smem, 1, s, a, q.stages);
 }
 
 template <typename T, int V, int K, int G>
