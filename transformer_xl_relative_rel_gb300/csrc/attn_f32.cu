@@ -160,10 +160,12 @@ rel_attn_f32_kernel(const float *__restrict__ q, const float *__restrict__ k,
 template <int DMAX>
 cudaError_t launch(const AttnArgs &a, cudaStream_t s)
 {
-    const int DP = a.D + 1;
-    const size_t smem = sizeof(float) * ((size_t)(2 * BR + 2 * BC + RW) * DP + BR * (BC + 1));
+    constexpr auto bytes = [](int D) { return sizeof(float) * ((size_t)(2 * BR + 2 * BC + RW) * (D + 1) + BR * (BC + 1)); };
+    const size_t smem = bytes(a.D);
+    // The limit is the kernel's on its device, not a call's: that of the
+    // largest D, so that host threads that call at once set the same.
     cudaError_t e = cudaFuncSetAttribute(rel_attn_f32_kernel<DMAX>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes(DMAX));
     if (e != cudaSuccess) return e;
     dim3 grid(a.B * a.H, (a.L + BR - 1) / BR);
     rel_attn_f32_kernel<DMAX><<<grid, NT, smem, s>>>(
