@@ -431,6 +431,7 @@ __global__ void __launch_bounds__(kWarpBlock, 2) norm_bwd_rows_kernel(const __gr
 #pragma unroll
         for (int j = 0; j < 4; ++j) dg[g][j] = db[g][j] = 0;
     const float inverse = 1.f / (float)a.d;
+    const int vectors = (a.d / V - lane + 31) / 32;      // of this lane, the first ones of each row
     int stage = 0, next = stages - 1;
     for (; row < a.rows; row += step) {
         ask(row + (stages - 1) * step, next);
@@ -470,7 +471,15 @@ __global__ void __launch_bounds__(kWarpBlock, 2) norm_bwd_rows_kernel(const __gr
                 dg[g][j] = pair_fma(dy[j], hat[j], dg[g][j]);
                 db[g][j] = pair_add(db[g][j], dy[j]);
                 sums = pair_add(sums, t[j]);
-                alongs = pair_fma(t[j], hat[j], alongs);
+                // (behind the row's end t is 0, but (0 - mean) rstd may be infinite: it is left out)
+                if constexpr (V == 1) {
+                    float lo, hi;
+                    unpair(hat[j], lo, hi);
+                    const int k = g * 8 + 2 * j;
+                    alongs = pair_fma(t[j], pair(k < vectors ? lo : 0.f, k + 1 < vectors ? hi : 0.f), alongs);
+                } else {
+                    alongs = pair_fma_below(t[j], hat[j], alongs, g * (8 / V) + 2 * j / V, vectors);
+                }
             }
             if (!KEEP) asm volatile("" ::: "memory");      // (one group's values in registers at a time)
         }

@@ -149,6 +149,13 @@ __device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c)
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+// a b + c where k < n, else c
+__device__ __forceinline__ uint64_t pair_fma_below(uint64_t a, uint64_t b, uint64_t c, int k, int n)
+{
+    asm("{\n\t.reg .pred below;\n\tsetp.lt.s32 below, %3, %4;\n\t@below fma.rn.f32x2 %0, %1, %2, %0;\n\t}"
+        : "+l"(c) : "l"(a), "l"(b), "r"(k), "r"(n));
+    return c;
+}
 // a + b towards zero
 __device__ __forceinline__ uint64_t pair_add_rz(uint64_t a, uint64_t b)
 {
