@@ -685,9 +685,10 @@ txl_status txl_grad_norm(int tensors, const txl_adamw_tensor *t, float max_norm,
  * mix(x): x = (x ^ x >> 16) 0x7feb352d, x = (x ^ x >> 15) 0x846ca68b,
  * x ^ x >> 16.  m, v, sqrt(v) and y are computed operation by operation as
  * written, each rounded to fp32, so that plain fp32 arithmetic gives the same
- * codes.  The update uses m and v before they become codes.  A block with a
- * moment that is not finite, or whose m or sqrt(v) is 2^126 or more, is lost:
- * its scale becomes NaN; use grad_scale.
+ * codes.  The update uses m and v before they become codes (0 where a finite
+ * gradient's v is infinite, as with float32 moments).  A block whose m or
+ * sqrt(v) is not finite, or 2^126 or more, has lost them: its scale becomes
+ * NaN, and what the next step makes of it; use grad_scale.
  *
  * t : host array of `tensors` descriptions.  param, master, the moments and
  * their scales must overlap neither each other, in any tensor, nor a gradient

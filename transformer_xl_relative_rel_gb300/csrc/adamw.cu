@@ -308,17 +308,19 @@ __device__ __forceinline__ uint64_t pair_sqrt(uint64_t v)
 }
 
 // eight numbers' roots; by the function where one is so small (below 2^-100,
-// but not 0) that the Newton step's residual has no room
+// but not 0) that the Newton step's residual has no room, or infinite (the sum
+// then is; one that overflows of finite numbers costs time only)
 __device__ __forceinline__ void eight_sqrt(const uint64_t (&v)[4], uint64_t (&root)[4])
 {
     uint32_t least = 0xffffffffu;      // (the bits of 0, less one, are the largest)
-    float x[8];
+    float x[8], lo, hi;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         unpair(v[k], x[2 * k], x[2 * k + 1]);
         least = min(min(least, __float_as_uint(x[2 * k]) - 1u), __float_as_uint(x[2 * k + 1]) - 1u);
     }
-    if (least < (27u << 23) - 1u) {
+    unpair(pair_add(pair_add(v[0], v[1]), pair_add(v[2], v[3])), lo, hi);
+    if (least < (27u << 23) - 1u || !(lo + hi <= 3.4028234e38f)) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) root[k] = pair(__fsqrt_rn(x[2 * k]), __fsqrt_rn(x[2 * k + 1]));
         return;
