@@ -1,4 +1,4 @@
-"""The optimiser step where a value leaves fp32."""
+"""The optimiser step where a value leaves fp32, or a tensor its memory."""
 import pytest
 import torch
 
@@ -52,3 +52,25 @@ def test_a_second_moment_past_the_largest_number(kind, decay, small):
         assert int(torch.isfinite(model["exp_avg_sq_scales"][0]).sum()) == 7
     else:
         assert float(model["exp_avg_sqs"][0][300]) == float("inf")
+
+
+@pytest.mark.parametrize("kind", ["master", "8 bits"])
+def test_tensors_moved_elsewhere_leave_their_memory_to_the_step(kind):
+    """A weight whose storage is replaced after the list was made: the step
+    still acts on the memory it was given, which nobody else gets meanwhile."""
+    n = 300_000
+    model = _model([n], 42, KINDS[kind])
+    twin = _copy(model)
+    t = txl.AdamwTensors(**model)
+    moved = {name: x[0].clone() for name, x in model.items() if x[0] is not None}
+    sizes = [(x.shape, x.dtype) for x in moved.values()]
+    for name, x in moved.items():
+        model[name][0].data = x
+    # what is allocated now would get the memory, had it been given back
+    others = [torch.full(shape, 0.5, device="cuda").to(dt) for shape, dt in sizes * 3]
+    torch.cuda.synchronize()
+    txl.adamw_step(t, 1e-2, 3)
+    txl.check()
+    assert all((x.float() == 0.5).all() for x in others)
+    for name in moved:      # the new places are not the list's
+        assert torch.equal(model[name][0].view(torch.uint8), twin[name][0].view(torch.uint8)), name

@@ -1011,7 +1011,7 @@ class AdamwTensors:
     roots); these lists may mix both, with None for float32 moments' scales.
     weight_decay: a number, or one per tensor.
 
-    The object keeps the tensors, and steps act on their memory: a weight or
+    The object keeps the tensors' memory, and steps act on it: a weight or
     gradient moved elsewhere wants a new one."""
 
     def __init__(self, params, grads, exp_avgs, exp_avg_sqs, masters=None, exp_avg_scales=None, exp_avg_sq_scales=None,
@@ -1027,6 +1027,7 @@ class AdamwTensors:
             if len(x) != n:
                 raise ValueError(f"{name} must have an entry per param ({n}), got {len(x)}")
         array = (_AdamwTensor * max(n, 1))()
+        kept = []       # storages, not tensors: one whose ``data`` is replaced lets go of its storage
         dev = params[0].get_device() if n else None
         f32, e4m3 = torch.float32, torch.float8_e4m3fn
         codes = {f32: TXL_F32, torch.bfloat16: TXL_BF16}
@@ -1047,8 +1048,11 @@ class AdamwTensors:
                 if ms.shape != blocks or vs.shape != blocks or ms.dtype is not f32 or vs.dtype is not f32:
                     raise ValueError(f"tensor {k}: scales must be float32 {list(blocks)}")
             for x in (p, g, m, v, w, ms, vs):
-                if x is not None and (x.get_device() != dev or not x.is_contiguous()):
+                if x is None:
+                    continue
+                if x.get_device() != dev or not x.is_contiguous():
                     dev = -1
+                kept.append(x.untyped_storage())
             if dev < 0:
                 raise ValueError("all tensors must be contiguous CUDA tensors on one device")
             if size:
@@ -1057,7 +1061,7 @@ class AdamwTensors:
                             g_code)
             else:
                 array[k] = (None, None, None, None, None, None, None, 0, wd, code, g_code)
-        self._array, self._dev, self._count, self._kept = array, dev, n, lists
+        self._array, self._dev, self._count, self._kept = array, dev, n, kept
 
     def __len__(self):
         return self._count
