@@ -683,9 +683,10 @@ txl_status txl_grad_norm(int tensors, const txl_adamw_tensor *t, float max_norm,
  *     h = mix(mix(mix(mix(mix(seed lo) + seed hi) + k) + step) + i + (i >> 32) 0x9e3779b9)
  * in 32 bits, k the tensor's place in the call, i the element, where
  * mix(x): x = (x ^ x >> 16) 0x7feb352d, x = (x ^ x >> 15) 0x846ca68b,
- * x ^ x >> 16.  m, v, sqrt(v) and y are computed operation by operation as
- * written, each rounded to fp32, so that plain fp32 arithmetic gives the same
- * codes.  The update uses m and v before they become codes (0 where a finite
+ * x ^ x >> 16 (constants of C. Wellons, "Prospecting for Hash Functions",
+ * 2018, public domain).  m, v, sqrt(v) and y are computed operation by
+ * operation as written, each rounded to fp32, so that plain fp32 arithmetic
+ * gives the same codes.  The update uses m and v before they become codes (0 where a finite
  * gradient's v is infinite, as with float32 moments).  A block whose m or
  * sqrt(v) is not finite, or 2^126 or more, has lost them: its scale becomes
  * NaN, and what the next step makes of it; use grad_scale.

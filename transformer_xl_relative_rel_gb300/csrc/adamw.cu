@@ -101,6 +101,10 @@ struct StepScalars {
     int64_t step;
 };
 
+// A permutation of 32-bit numbers whose outputs' bits depend evenly on all of
+// the input's: two rounds of xor-shift and multiplication with the constants
+// that C. Wellons found by search and published as public domain ("Prospecting
+// for Hash Functions", 2018).
 __host__ __device__ __forceinline__ uint32_t mix(uint32_t x)
 {
     x = (x ^ (x >> 16)) * 0x7feb352du;
