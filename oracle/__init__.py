@@ -361,7 +361,9 @@ def adamw(p, grad, m, v, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, weight_deca
 
 def moment_bits(seed: int, tensor: int, step: int, n: int, first: int = 0):
     """The random fractions of an 8-bit step's rounding for elements first ..
-    first + n - 1 of a tensor: (of m, of sqrt(v)), multiples of 2^-16 below 1."""
+    first + n - 1 of a tensor: (of m, of sqrt(v)), multiples of 2^-16 below 1.
+    (The mixing constants are C. Wellons', "Prospecting for Hash Functions",
+    2018, public domain.)"""
     word = 0xffffffff
 
     def mix(x):
