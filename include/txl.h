@@ -575,8 +575,9 @@ txl_status txl_embed_bwd(const int64_t *tokens, const void *dout, float scale, i
  * pointers; rows that are multiples of 16 bytes at 16-byte aligned bases
  * move fastest.  eps > 0 and finite.  rows == 0: nothing to do.  d_model >=
  * 1, else TXL_ERR_INVALID; d_model <= 8192, rows <= 2^30, else
- * TXL_ERR_UNSUPPORTED.  fp32 arithmetic, one rounding of y.  Asynchronous on
- * stream; no allocation.
+ * TXL_ERR_UNSUPPORTED.  fp32 arithmetic, sums in an order as
+ * txl_layer_norm_bwd's, one rounding of y.  Asynchronous on stream; no
+ * allocation.
  */
 txl_status txl_layer_norm_fwd(const void *x, const void *residual, const float *gamma, const float *beta, float eps,
                               int rows, int d_model, txl_dtype dtype, void *y, void *sum, float *mean, float *rstd,
@@ -601,10 +602,12 @@ txl_status txl_layer_norm_fwd(const void *x, const void *residual, const float *
  *            txl_layer_norm_bwd_workspace reports, 256-byte aligned, owned by
  *            the caller, as txl_embed_bwd's; unused (and may be NULL) without
  *            dgamma and dbeta.
- * rows == 0: dgamma and dbeta are set to 0.  fp32 arithmetic and sums over
- * rows in an order that the sizes determine (the same call gives the same
- * bits), one rounding of dx.  Outputs must not overlap each other, any input
- * or the workspace.  Sizes as txl_layer_norm_fwd.
+ * rows == 0: dgamma and dbeta are set to 0.  fp32 arithmetic and sums, over
+ * a row and over rows, in an order that the sizes, the dtype and the buffers'
+ * alignment determine (the same call gives the same bits; at addresses of
+ * another alignment the last ones may differ), one rounding of dx.  Outputs
+ * must not overlap each other, any input or the workspace.  Sizes as
+ * txl_layer_norm_fwd.
  */
 txl_status txl_layer_norm_bwd_workspace(int rows, int d_model, txl_dtype dtype, size_t *bytes);
 txl_status txl_layer_norm_bwd(const void *dy, const void *x, const void *residual, const void *dsum, const float *gamma,
@@ -634,7 +637,8 @@ typedef struct {
     float eps;                /* finite, >= 2^-126 */
     double beta1, beta2;      /* 0 <= beta < 1 */
     int64_t step;             /* the step's number t >= 1 (unused with step_device) */
-    const float *lr_device;   /* device float32 [1], or NULL: read when the kernel runs (captured steps) */
+    const float *lr_device;   /* device float32 [1], or NULL: read when the kernel runs (captured steps), and
+                                 used as it is */
     const int64_t *step_device;  /* device int64 [1], or NULL */
     const float *grad_scale;  /* device float32 [1], or NULL (1): a factor of all gradients */
     uint64_t seed;            /* of the 8-bit moments' rounding */
@@ -644,9 +648,9 @@ typedef struct {
  * txl_grad_norm -- the norm of all the tensors' gradients taken as one
  * vector, and the factor that clips it:
  *     norm = sqrt(sum_k sum_i grad_ki^2),  clip = min(1, max_norm / norm)
- * A norm that is not finite (also: squares past the float32 range) has clip
- * NaN, which makes a txl_adamw_step that takes it as its grad_scale do
- * nothing.
+ * A norm that is not finite (also: a square, or a part's sum of squares, past
+ * the float32 range) has clip NaN, which makes a txl_adamw_step that takes it
+ * as its grad_scale do nothing.
  *
  * t          : host array of `tensors` descriptions; grad, grad_dtype and size
  *              are used.

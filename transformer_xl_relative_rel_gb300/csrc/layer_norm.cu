@@ -5,17 +5,31 @@
 //     ds = rstd (g - mean_d(g) - xh mean_d(g xh)) + dsum,   g = dy gamma, xh = (s - mean) rstd
 //     dgamma = sum_i dy xh, dbeta = sum_i dy
 //
-// HBM-bound.  The variance is the mean of the squared differences from the
-// mean.  G threads share a row (a warp up to 1024 columns), which stays in
-// registers, as fp32, from its loads to its result.  The backward's warps
-// (groups of threads) take many rows each and keep their columns' sums for
-// dgamma and dbeta in registers; a block adds its warps' up and writes them,
-// and a second launch adds the blocks' in a fixed order.  Those registers
-// leave room for few warps, so up to 1024 columns a warp of the backward asks
-// for its next rows (asynchronous copies into shared memory, each lane its own
+// HBM-bound, above some 256 columns.  The variance is the mean of the squared
+// differences from the mean.  G threads share a row, which stays in registers,
+// as fp32, from its loads to its result:
+//     forward: a warp up to 1024 columns (rows read by single elements: up to
+//     256), 128 threads up to 2048, 256 up to 4096, 512 above;
+//     backward: a warp up to 1024 columns (bf16 rows read by single elements:
+//     up to 512), 256 threads up to 2048, 512 up to 4096, 1024 above.
+// A row takes a whole warp however narrow it is: 262144 rows of 64 bf16
+// columns take 69 us forward and 79 backward where their bytes are worth 15
+// and 20, of 33 columns 80 and 88 (8 and 10).
+//
+// The backward's warps (groups of threads) take many rows each and keep their
+// columns' sums for dgamma and dbeta in registers; a block adds its warps' up
+// and writes them, and a second launch adds the blocks' in a fixed order.
+// Those registers leave room for few warps, so a warp of the backward asks for
+// its next rows (asynchronous copies into shared memory, each lane its own
 // columns; not bf16 rows that are only 2-byte aligned, which such copies do
 // not serve) before it computes one: 6144 x 1024 pre-norm rows 27.7 -> 15.0 us
 // (the forward gained nothing by it, 12 -> 14 us, and keeps a row per warp).
+// It reads two rows ahead where three stages of dy, x, the residual and dsum
+// fit beside another block's, one where two do, and none (one stage) for fp32
+// rows of more than 512 columns, and for fp32 rows of 257 to 512 and bf16 ones
+// of more than 512 with both the residual and dsum: other warps' rows are then
+// all that hides a load (fp32 262144 x 1024 with a residual 690 us, 633 at the
+// copy rate).
 //
 // Measured one by one under a profiler (about 2.5 us of each a launch; several
 // GB300s): 16896 x 512 bf16 with residual forward 11.8 to 12.7 us (52 MB),
@@ -26,6 +40,12 @@
 // 8192 forward 665 us (1024 threads of 8 columns: 1034), 65536 x 2048 forward
 // 148 (256 threads: 270), backward 198 (256 threads of up to 16 columns and
 // more barriers per row: 297).
+// Some kernels spill registers: the forward of 16 columns a thread in fp32 (76
+// bytes; 104 by pairs, 20 by bf16 pairs) and the backward's of 1024 threads (88
+// to 148).  The forward runs at the copy rate all the same (fp32 262144 x 512
+// 227 us, x 1024 446, 65536 x 2048 228, x 4096 471); the backward of 65536 x
+// 8192 fp32 takes 1.41 times its floor where x 4096, which does not spill,
+// takes 1.33.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
