@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 TXL_F32 = 0
@@ -40,6 +41,11 @@ class _AdamwTensor(ctypes.Structure):
                                                 "exp_avg_sq_scale")] +
                 [("size", ctypes.c_int64), ("weight_decay", ctypes.c_float), ("param_dtype", ctypes.c_int),
                  ("grad_dtype", ctypes.c_int)])
+
+
+# an _AdamwTensor's fields, without the padding behind them: packed at once, in
+# half the time that assigning them takes
+_ADAMW_FIELDS = struct.Struct("@7Pqfii")
 
 
 class _AdamwOptions(ctypes.Structure):
@@ -1012,7 +1018,10 @@ class AdamwTensors:
     weight_decay: a number, or one per tensor.
 
     The object keeps the tensors' memory, and steps act on it: a weight or
-    gradient moved elsewhere wants a new one."""
+    gradient moved elsewhere wants a new one (gradients stay where they are
+    when the backward calls write them by their ``grads=`` or ``dtable``).
+    Making one takes the host some 2 to 3 us per tensor, more than a step may:
+    it is made once."""
 
     def __init__(self, params, grads, exp_avgs, exp_avg_sqs, masters=None, exp_avg_scales=None, exp_avg_sq_scales=None,
                  weight_decay=0.0):
@@ -1022,11 +1031,12 @@ class AdamwTensors:
         lists = dict(params=params, grads=grads, exp_avgs=exp_avgs, exp_avg_sqs=exp_avg_sqs, masters=masters or none,
                      exp_avg_scales=exp_avg_scales or none, exp_avg_sq_scales=exp_avg_sq_scales or none)
         lists = {name: list(x) for name, x in lists.items()}
-        decay = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else [float(x) for x in weight_decay]
+        single = lambda x: ctypes.c_float(x).value       # (infinity past its range: the step refuses that)
+        decay = [single(weight_decay)] * n if isinstance(weight_decay, (int, float)) else [single(float(x)) for x in weight_decay]
         for name, x in list(lists.items()) + [("weight_decay", decay)]:
             if len(x) != n:
                 raise ValueError(f"{name} must have an entry per param ({n}), got {len(x)}")
-        array = (_AdamwTensor * max(n, 1))()
+        array, entry = (_AdamwTensor * max(n, 1))(), ctypes.sizeof(_AdamwTensor)
         kept = []       # storages, not tensors: one whose ``data`` is replaced lets go of its storage
         dev = params[0].get_device() if n else None
         f32, e4m3 = torch.float32, torch.float8_e4m3fn
@@ -1056,11 +1066,11 @@ class AdamwTensors:
             if dev < 0:
                 raise ValueError("all tensors must be contiguous CUDA tensors on one device")
             if size:
-                array[k] = (p.data_ptr(), None if w is None else w.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(),
-                            None if ms is None else ms.data_ptr(), None if ms is None else vs.data_ptr(), size, wd, code,
-                            g_code)
+                _ADAMW_FIELDS.pack_into(array, k * entry, p.data_ptr(), 0 if w is None else w.data_ptr(), g.data_ptr(),
+                                        m.data_ptr(), v.data_ptr(), 0 if ms is None else ms.data_ptr(),
+                                        0 if ms is None else vs.data_ptr(), size, wd, code, g_code)
             else:
-                array[k] = (None, None, None, None, None, None, None, 0, wd, code, g_code)
+                _ADAMW_FIELDS.pack_into(array, k * entry, 0, 0, 0, 0, 0, 0, 0, 0, wd, code, g_code)
         self._array, self._dev, self._count, self._kept = array, dev, n, kept
 
     def __len__(self):
