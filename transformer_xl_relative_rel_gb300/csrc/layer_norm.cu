@@ -33,16 +33,17 @@
 //
 // Measured one by one under a profiler (about 2.5 us of each a launch; several
 // GB300s): 16896 x 512 bf16 with residual forward 11.8 to 12.7 us (52 MB),
-// backward 15.1 to 15.8 us (70 MB), column sums 3.6 to 4.2 us; 6144 x 1024 with
-// the sum kept 11.4 to 13.2 us (50 MB), 15.0 to 15.7 us (50 MB, bound by its
+// backward 15.1 to 15.8 us (70 MB), column sums 3.6 to 4.3 us; 6144 x 1024 with
+// the sum kept 11.4 to 13.5 us (50 MB), 15.0 to 15.7 us (50 MB, bound by its
 // instructions: a row's xh is computed twice) and 3.7 to 4.3 us.
 // Wider rows as 16 columns a thread in the forward, 8 in the backward: 65536 x
 // 8192 forward 665 us (1024 threads of 8 columns: 1034), 65536 x 2048 forward
 // 148 (256 threads: 270), backward 198 (256 threads of up to 16 columns and
 // more barriers per row: 297).
 // Some kernels spill registers: the forward of 16 columns a thread in fp32 (76
-// bytes; 104 by pairs, 20 by bf16 pairs) and the backward's of 1024 threads (88
-// to 148).  The forward runs at the copy rate all the same (fp32 262144 x 512
+// bytes; 104 by pairs, 20 by bf16 pairs), the backward's of 1024 threads (88 to
+// 148) and the read-ahead one of fp32 rows above 512 columns (12; 108 by single
+// elements).  The forward runs at the copy rate all the same (fp32 262144 x 512
 // 227 us, x 1024 446, 65536 x 2048 228, x 4096 471); the backward of 65536 x
 // 8192 fp32 takes 1.41 times its floor where x 4096, which does not spill,
 // takes 1.33.
